@@ -300,6 +300,7 @@ def prepare(case, seed):
     st["case"], B = case, case["batch"]
     total = sum(fresh)
     dt = torch.bfloat16 if case["dtype"] == "bf16" else torch.float32
+    st["max_new"] = max(fresh)
     st["cu"], st["err"] = _cu(fresh), torch.zeros(1, dtype=torch.int32, device=DEV)
     if case["op"] == "append":
         # the sequences' windows (their older entries are not touched), the new rows, the RoPE table
@@ -346,8 +347,7 @@ def prepare(case, seed):
         st["scale"] = 1.0 / math.sqrt(DQK)
         st["out"] = torch.empty(total, H, LAT, dtype=torch.bfloat16, device=DEV)
         st["lse"] = torch.empty(total, H, device=DEV)
-        # the longest sequence's sizes, for the padded plain form
-        st["max_new"], st["max_ent"] = max(fresh), max(t // r for t in n)
+        st["max_ent"] = max(t // r for t in n)  # the longest sequence, for the padded plain form
     return st
 
 
@@ -385,16 +385,16 @@ def _run_own(st):
     op, err = st["case"]["op"], st["err"]
     if op == "append":
         c.n_tokens.copy_(st["n0"])  # back to the state before the call, so that the pass can be repeated
-        csa2.kv_append_ragged(c, st["cu"], st["rope"], kv=st["kv"], idx_key=st["key"], err=err)
+        csa2.kv_append_ragged(c, st["cu"], st["rope"], kv=st["kv"], idx_key=st["key"], max_new=st["max_new"], err=err)
         csa2.kv_read(c, st["cu"], start=st["n0"], out_main=st["main"], out_key=st["keys"], err=err)
-        csa2.window_read(c, st["window"], err=err)
+        csa2.window_read(c, st["window"])
         return {"main": st["main"], "key": st["keys"], "window": st["window"], "n_tokens": c.n_tokens}
     if op == "read":
         csa2.kv_read(c, st["cu"], start=st["start"], pos=st["pos"], out_main=st["main"], out_key=st["keys"], err=err)
         return {"main": st["main"], "key": st["keys"]}
     one = st["case"]["new"] == 1  # single tokens: the cache's own window ring holds all they need
-    csa2.chunk_attn(c, st["q"], st["cu"], st["out"], st["lse"], st["ws"], st["scale"], win=None if one else st["win"],
-                    sink=st["sink"], err=err)
+    csa2.chunk_attn(c, st["q"], st["cu"], st["out"], st["lse"], st["ws"], st["scale"], max_new=st["max_new"],
+                    win=None if one else st["win"], sink=st["sink"], err=err)
     return {"out": st["out"], "lse": st["lse"]}
 
 
