@@ -20,6 +20,7 @@ DEVERR_CAPACITY, DEVERR_INDEX, DEVERR_NAN, DEVERR_ROPE, DEVERR_TIMEOUT, DEVERR_I
 SWA_BF16, SWA_MXFP8 = 0, 1
 ENTRY_FP4, ENTRY_FP8 = 0, 1
 IN_F32, IN_BF16 = 0, 1
+OUT_F32, OUT_BF16 = 0, 1
 D_LATENT, D_ROPE, D_QK, D_INDEX, D_CMP, WINDOW = 512, 64, 576, 128, 704, 128
 
 EXPORTS = [
@@ -27,6 +28,8 @@ EXPORTS = [
     "csa2_score_aux_size", "csa2_index_score",
     "csa2_topk_workspace_size", "csa2_topk", "csa2_topk_noalloc", "csa2_attn_workspace_size", "csa2_sparse_attn_decode",
     "csa2_prefill_workspace_size", "csa2_prefill_chunk", "csa2_mask_to_pool", "csa2_mxf4_peak_launch",
+    "csa2_chunk_window_bytes", "csa2_kv_append_ragged", "csa2_kv_read", "csa2_window_read",
+    "csa2_chunk_attn_workspace_size", "csa2_chunk_attn",
     "csa2_bounded_wait_check", "csa2_set_phase_events",
     "csa2_phase_events_recorded", "csa2_status_string", "csa2_last_error_detail", "csa2_version",
 ]
@@ -93,6 +96,12 @@ def load() -> ctypes.CDLL:
         "csa2_prefill_chunk": (i32, [vp, i32, vp, vp, i64, i32, vp, vp, i32, vp, i32, i32, vp, f32,
                                      vp, vp, vp, vp, sz, vp, vp]),
         "csa2_mask_to_pool": (i32, [vp, i64, i32, i32, vp, vp, i32, i32, vp]),
+        "csa2_chunk_window_bytes": (sz, [i32, i32, i32, i32]),
+        "csa2_kv_append_ragged": (i32, [vp, vp, i64, vp, i64, i32, vp, vp, i32, i32, vp, i64, vp, vp, vp, vp]),
+        "csa2_kv_read": (i32, [vp, vp, i32, vp, vp, vp, i64, vp, i64, i32, vp, vp]),
+        "csa2_window_read": (i32, [vp, vp, i32, vp]),
+        "csa2_chunk_attn_workspace_size": (sz, [i32, i32, i32]),
+        "csa2_chunk_attn": (i32, [vp, vp, i32, vp, i32, i32, vp, vp, vp, f32, vp, i32, vp, vp, sz, vp, vp]),
         "csa2_mxf4_peak_launch": (i32, [i32, i32, vp, vp, vp]),
         "csa2_bounded_wait_check": (i32, [i32, i32, vp, vp]),
         "csa2_set_phase_events": (i32, [vp, i32]),
@@ -179,6 +188,51 @@ class Cache:
             self.cmp_buf.data_ptr() if self.cmp_buf is not None else None, self.n_tokens.data_ptr(),
             self.block_table.data_ptr() if self.block_table is not None else None, page_entries or 0,
             self.max_pages, self.n_pages, entry_format)
+
+    @classmethod
+    def from_planes(cls, batch, capacity, planes, ratio=1, swa_dtype=SWA_MXFP8, page_entries=None, n_pages=None,
+                    block_table=None, entry_format=ENTRY_FP4):
+        """A cache over planes the caller already holds: `planes` maps the plane names (lat_codes ..
+        idx_scales, swa_codes, swa_scales, n_tokens, and cmp_buf for ratio 2) to contiguous device
+        tensors of the sizes csa2_entry_plane_bytes() and csa2_cache_plane_bytes() give; rope_scales
+        may be missing for ENTRY_FP8, swa_scales for SWA_BF16.  Nothing is copied."""
+        L = load()
+        c = cls.__new__(cls)
+        c.batch, c.capacity, c.ratio, c.swa_dtype = batch, capacity, ratio, swa_dtype
+        c.page_entries, c.entry_format, c.block_table = page_entries, entry_format, block_table
+        if page_entries:
+            if capacity % page_entries or page_entries % 128:
+                raise ValueError(f"capacity {capacity} must be a multiple of page_entries {page_entries}, itself of 128")
+            c.max_pages = capacity // page_entries
+            c.n_pages = n_pages or batch * c.max_pages
+            _want("block_table", block_table, torch.int32, (batch, c.max_pages))
+            rows, c.idx_tiles = c.n_pages * page_entries, c.n_pages * page_entries // 128
+            tiles = c.idx_tiles
+        else:
+            c.max_pages = c.n_pages = 0
+            rows, c.idx_tiles = batch * capacity, (capacity + 127) // 128
+            tiles = batch * c.idx_tiles
+        need = [rows * L.csa2_entry_plane_bytes(entry_format, p) for p in range(4)] + [tiles * 8192, tiles * 512] + \
+            [L.csa2_cache_plane_bytes(batch, capacity, p, swa_dtype) for p in (6, 7)]
+        names = ("lat_codes", "lat_scales", "rope_codes", "rope_scales", "idx_codes", "idx_scales", "swa_codes",
+                 "swa_scales")
+        for name, n in zip(names, need):
+            t = planes.get(name)
+            if t is not None:
+                _want(name, t, torch.uint8)
+                if t.numel() < n:
+                    raise ValueError(f"{name} holds {t.numel()} of {n} bytes")
+            elif n and not (name == "swa_scales" and swa_dtype == SWA_BF16):
+                raise ValueError(f"plane {name} is missing")
+            setattr(c, name, t)
+        c.cmp_buf, c.n_tokens = planes.get("cmp_buf"), planes["n_tokens"]
+        _want("n_tokens", c.n_tokens, torch.int64, (batch,))
+        if ratio == 2:
+            _want("cmp_buf", c.cmp_buf, torch.float32, (batch, 4, 4, D_CMP))
+        p = lambda t: t.data_ptr() if t is not None else None
+        c.struct = CacheStruct(batch, capacity, ratio, swa_dtype, *[p(getattr(c, n)) for n in names], p(c.cmp_buf),
+                               p(c.n_tokens), p(block_table), page_entries or 0, c.max_pages, c.n_pages, entry_format)
+        return c
 
     def ref(self):
         return ctypes.byref(self.struct)
@@ -340,6 +394,170 @@ def mask_to_pool(scores, ratio, q_pos, pool, pool_block_size=8, stream=None):
     B, stride = scores.shape
     _check("csa2_mask_to_pool", load().csa2_mask_to_pool(_ptr(scores), stride, B, ratio, _ptr(q_pos), _ptr(pool),
                                                           pool.shape[1], pool_block_size, _stream(stream)))
+
+
+# --------------------------------------------------------------------------- ragged batches
+def _want(name, t, dtype, shape=None, like=None):
+    """Raise ValueError unless t is a contiguous device tensor of dtype (and shape; -1: any size)."""
+    if t is None or not t.is_cuda:
+        raise ValueError(f"{name}: a CUDA tensor is needed")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise ValueError(f"{name}: {t.dtype}, {dtype} is needed")
+    if shape is not None and (t.dim() != len(shape) or any(w not in (-1, n) for w, n in zip(shape, t.shape))):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, {tuple(shape)} is needed")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {like.device}")
+
+
+def _want_rows(name, t, dtype, width, like, total=None):
+    """Raise ValueError unless t holds rows of `width` elements, contiguous within a row; returns the row stride."""
+    if t is None or not t.is_cuda or t.device != like.device:
+        raise ValueError(f"{name}: a tensor on {like.device} is needed")
+    if t.dtype not in dtype:
+        raise ValueError(f"{name}: {t.dtype}, one of {dtype} is needed")
+    if t.dim() != 2 or t.shape[1] != width or (total is not None and t.shape[0] != total):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, ({'rows' if total is None else total}, {width}) is needed")
+    if t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < width):
+        raise ValueError(f"{name}: rows must be contiguous and not overlap")
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def _out_dtype(t):
+    return OUT_BF16 if t.dtype == torch.bfloat16 else OUT_F32
+
+
+class _on:
+    """The cache's device as the current one for a call, and its current stream unless one is given."""
+
+    def __init__(self, cache, stream):
+        self.dev, self.stream = cache.n_tokens.device, stream
+
+    def __enter__(self):
+        self.ctx = torch.cuda.device(self.dev)
+        self.ctx.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        return self.ctx.__exit__(*exc)
+
+
+class ChunkWindow:
+    """The window rows csa2_kv_append_ragged leaves for csa2_chunk_attn: codes and scales tensors."""
+
+    def __init__(self, codes, scales):
+        self.codes, self.scales = codes, scales
+
+
+def chunk_window(cache, total):
+    """Buffers for the window rows of a ragged append of `total` rows (csa2_chunk_window_bytes)."""
+    L, dev = load(), cache.n_tokens.device
+    n = [L.csa2_chunk_window_bytes(cache.batch, total, cache.swa_dtype, p) for p in (0, 1)]
+    rows = total + WINDOW * cache.batch
+    return ChunkWindow(torch.empty(rows, n[0] // rows, dtype=torch.uint8, device=dev),
+                       torch.empty(rows, n[1] // rows, dtype=torch.uint8, device=dev))
+
+
+def _window_ptrs(cache, win, total):
+    if win is None:
+        return None, None
+    rows = total + WINDOW * cache.batch
+    _want("win.codes", win.codes, torch.uint8, (rows, 576 if cache.swa_dtype == SWA_MXFP8 else 1152), cache.n_tokens)
+    if cache.swa_dtype == SWA_MXFP8:
+        _want("win.scales", win.scales, torch.uint8, (rows, 32), cache.n_tokens)
+    return _ptr(win.codes), _ptr(win.scales)
+
+
+def kv_append_ragged(cache: Cache, cu_new, rope_cs, kv=None, idx_key=None, cmp=None, max_new=None, win=None, err=None,
+                     stream=None):
+    """csa2_kv_append_ragged: rows cu_new[b] .. cu_new[b+1]-1 (int32 [B+1], device) are sequence b's new
+    tokens.  Ratio 1: kv [total,576], idx_key [total,128] (fp32 or bf16, rows may be strided).  Ratio 2:
+    cmp = (ca, cb, za, zb [total,704], ba, bb [2,704]) fp32.  max_new: a bound on the rows of one sequence
+    (default: all).  win: from chunk_window(cache, total), filled for chunk_attn."""
+    like = cache.n_tokens
+    _want("cu_new", cu_new, torch.int32, (cache.batch + 1,), like)
+    _want("rope_cs", rope_cs, torch.float32, (-1, 32, 2) if rope_cs is not None and rope_cs.dim() == 3 else (-1, 64), like)
+    cin, ks, is_, dt = None, 0, 0, IN_F32
+    if cache.ratio == 1:
+        if cmp is not None:
+            raise ValueError("cmp is for ratio-2 caches")
+        ks = _want_rows("kv", kv, (torch.float32, torch.bfloat16), 576, like)
+        total = kv.shape[0]
+        is_ = _want_rows("idx_key", idx_key, (kv.dtype,), 128, like, total)
+        dt = IN_BF16 if kv.dtype == torch.bfloat16 else IN_F32
+    else:
+        if cmp is None or kv is not None or idx_key is not None:
+            raise ValueError("a ratio-2 cache takes cmp rows, and no kv or idx_key")
+        total = cmp[0].shape[0]
+        for i, t in enumerate(cmp):
+            _want(f"cmp[{i}]", t, torch.float32, (total, D_CMP) if i < 4 else (2, D_CMP), like)
+        cin = CompressIn(*[t.data_ptr() for t in cmp])
+    wc, ws = _window_ptrs(cache, win, total)
+    with _on(cache, stream) as s:
+        _check("csa2_kv_append_ragged", load().csa2_kv_append_ragged(
+            cache.ref(), _ptr(kv), ks, _ptr(idx_key), is_, dt, ctypes.byref(cin) if cin is not None else None,
+            _ptr(cu_new), total, total if max_new is None else max_new, _ptr(rope_cs), rope_cs.shape[0], wc, ws,
+            _ptr(err), s))
+
+
+def kv_read(cache: Cache, cu_rows, out_main=None, out_key=None, pos=None, start=None, err=None, stream=None):
+    """csa2_kv_read: rows cu_rows[b] .. cu_rows[b+1]-1 read entries pos[r] (int32 [total], negative = zeros)
+    of sequence b, or the stretch from start[b] (int64 [B]) on, into out_main [total,576] and / or out_key
+    [total,128] (fp32 or bf16, rows may be strided)."""
+    like = cache.n_tokens
+    _want("cu_rows", cu_rows, torch.int32, (cache.batch + 1,), like)
+    first = out_main if out_main is not None else out_key
+    if first is None:
+        raise ValueError("out_main or out_key is needed")
+    total, ms, ks = first.shape[0], 0, 0
+    if out_main is not None:
+        ms = _want_rows("out_main", out_main, (torch.float32, torch.bfloat16), 576, like)
+    if out_key is not None:
+        ks = _want_rows("out_key", out_key, (first.dtype,) if out_main is not None else (torch.float32, torch.bfloat16),
+                        128, like, total)
+    if (pos is None) == (start is None):
+        raise ValueError("one of pos and start is needed")
+    if pos is not None:
+        _want("pos", pos, torch.int32, (total,), like)
+    else:
+        _want("start", start, torch.int64, (cache.batch,), like)
+    with _on(cache, stream) as s:
+        _check("csa2_kv_read", load().csa2_kv_read(cache.ref(), _ptr(cu_rows), total, _ptr(pos), _ptr(start),
+                                                   _ptr(out_main), ms, _ptr(out_key), ks, _out_dtype(first), _ptr(err), s))
+
+
+def window_read(cache: Cache, out, stream=None):
+    """csa2_window_read: out [B,128,576] (fp32 or bf16), row i = token n_tokens - 128 + i (zeros before token 0)."""
+    _want("out", out, (torch.float32, torch.bfloat16), (cache.batch, WINDOW, D_QK), cache.n_tokens)
+    with _on(cache, stream) as s:
+        _check("csa2_window_read", load().csa2_window_read(cache.ref(), _ptr(out), _out_dtype(out), s))
+
+
+def chunk_attn_workspace(total, heads, batch, device="cuda"):
+    with torch.cuda.device(device):
+        n = load().csa2_chunk_attn_workspace_size(batch, total, heads)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def chunk_attn(cache: Cache, q, cu_q, out, lse, ws, sm_scale, max_new=None, win=None, sink=None, err=None, stream=None):
+    """csa2_chunk_attn: q bf16 [total,H,576], rows cu_q[b] .. cu_q[b+1]-1 the last tokens appended to sequence
+    b -> out [total,H,512] (fp32 or bf16), lse fp32 [total,H].  win: the append's window rows (None: the ring,
+    enough for single tokens).  ws: chunk_attn_workspace()."""
+    like = cache.n_tokens
+    _want("q", q, torch.bfloat16, (-1, -1, D_QK), like)
+    total, H = q.shape[0], q.shape[1]
+    _want("cu_q", cu_q, torch.int32, (cache.batch + 1,), like)
+    _want("out", out, (torch.float32, torch.bfloat16), (total, H, D_LATENT), like)
+    _want("lse", lse, torch.float32, (total, H), like)
+    _want("ws", ws, torch.uint8, None, like)
+    if sink is not None:
+        _want("sink", sink, torch.float32, (H,), like)
+    wc, wsc = _window_ptrs(cache, win, total)
+    with _on(cache, stream) as s:
+        _check("csa2_chunk_attn", load().csa2_chunk_attn(
+            cache.ref(), _ptr(q), H, _ptr(cu_q), total, total if max_new is None else max_new, wc, wsc, _ptr(sink),
+            float(sm_scale), _ptr(out), _out_dtype(out), _ptr(lse), _ptr(ws), ws.numel(), _ptr(err), s))
 
 
 # --------------------------------------------------------------------------- measurement helpers

@@ -92,17 +92,11 @@ cudaError_t ensure_smem_limit(const void *fn, int bytes) {
 
 }  // namespace csa2
 
-namespace {
-
-using csa2::aligned16;
-using csa2::cuda_status;
-using csa2::fail;
-
 #define REQUIRE CSA2_REQUIRE
 #define REQUIRE_PTR CSA2_REQUIRE_PTR
 #define REQUIRE_OPT_PTR CSA2_REQUIRE_OPT_PTR
 
-csa2_status check_cache(const csa2_cache *c) {
+csa2_status csa2::check_cache(const csa2_cache *c) {
   REQUIRE(c != nullptr, CSA2_ERR_NULL, "cache is NULL");
   REQUIRE(c->batch >= 1 && c->batch <= 65535, CSA2_ERR_SHAPE, "cache batch %d outside 1..65535", c->batch);
   REQUIRE(c->capacity >= 1 && c->capacity <= (1 << 30), CSA2_ERR_SHAPE, "cache capacity %d outside 1..2^30",
@@ -133,6 +127,13 @@ csa2_status check_cache(const csa2_cache *c) {
   }
   return CSA2_OK;
 }
+
+namespace {
+
+using csa2::aligned16;
+using csa2::check_cache;
+using csa2::cuda_status;
+using csa2::fail;
 
 // A view of one sequence of a cache (batch 1).
 csa2_cache seq_view(const csa2_cache &c, int seq) {

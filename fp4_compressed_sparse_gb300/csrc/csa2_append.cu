@@ -26,17 +26,6 @@ __device__ __forceinline__ float load_in(const void *p, size_t i, int in_bf16) {
   return reinterpret_cast<const float *>(p)[i];
 }
 
-// Whether sequence b may take n_new more tokens (capacity in entries, RoPE table).
-__device__ __forceinline__ bool append_ok(const csa2_cache &c, int64_t t0, int n_new, int64_t rope_len) {
-  return (t0 + n_new) / c.ratio <= static_cast<int64_t>(c.capacity) && t0 + n_new <= rope_len;
-}
-
-__device__ __forceinline__ void append_fail(const csa2_cache &c, int64_t t0, int n_new, int64_t rope_len,
-                                            int32_t *err) {
-  if ((t0 + n_new) / c.ratio > static_cast<int64_t>(c.capacity)) raise_err(err, CSA2_DEVERR_CAPACITY);
-  else raise_err(err, CSA2_DEVERR_ROPE);
-}
-
 }  // namespace
 
 namespace {
@@ -118,21 +107,9 @@ __global__ void __launch_bounds__(256) k_append_r2_entries(csa2_cache c, csa2_co
   const float *b1z = has_b ? cmp_row(c, in, b, n_new, t0, 2 * i - 1, 3) : nullptr;
   float *dst_dbg = dbg ? dbg + (static_cast<size_t>(b) * (n_new / 2 + 1) + e) * kDcmp : nullptr;
   for (int j = lane; j < kDcmp; j += 32) {
-    // per-channel softmax over the 4 rows, in fp64, rounded once to fp32
-    double l0 = __dadd_rn(static_cast<double>(a0z[j]), static_cast<double>(in.ba[j]));
-    double l1 = __dadd_rn(static_cast<double>(a1z[j]), static_cast<double>(in.ba[kDcmp + j]));
-    double l2 = has_b ? __dadd_rn(static_cast<double>(b0z[j]), static_cast<double>(in.bb[j])) : -INFINITY;
-    double l3 = has_b ? __dadd_rn(static_cast<double>(b1z[j]), static_cast<double>(in.bb[kDcmp + j])) : -INFINITY;
-    double mx = fmax(fmax(l0, l1), fmax(l2, l3));
-    double e0 = exp(__dadd_rn(l0, -mx)), e1 = exp(__dadd_rn(l1, -mx));
-    double e2 = has_b ? exp(__dadd_rn(l2, -mx)) : 0.0, e3 = has_b ? exp(__dadd_rn(l3, -mx)) : 0.0;
-    double den = __dadd_rn(__dadd_rn(__dadd_rn(__dadd_rn(0.0, e0), e1), e2), e3);
-    double acc = 0.0;
-    acc = __dadd_rn(acc, __dmul_rn(__ddiv_rn(e0, den), static_cast<double>(a0c[j])));
-    acc = __dadd_rn(acc, __dmul_rn(__ddiv_rn(e1, den), static_cast<double>(a1c[j])));
-    acc = __dadd_rn(acc, __dmul_rn(__ddiv_rn(e2, den), has_b ? static_cast<double>(b0c[j]) : 0.0));
-    acc = __dadd_rn(acc, __dmul_rn(__ddiv_rn(e3, den), has_b ? static_cast<double>(b1c[j]) : 0.0));
-    const float v = __double2float_rn(acc);
+    const float v = r2_compress_channel(a0z[j], a1z[j], has_b ? b0z[j] : 0.0f, has_b ? b1z[j] : 0.0f, in.ba[j],
+                                        in.ba[kDcmp + j], in.bb[j], in.bb[kDcmp + j], a0c[j], a1c[j],
+                                        has_b ? b0c[j] : 0.0f, has_b ? b1c[j] : 0.0f, has_b);
     srow[warp][j] = v;
     if (dst_dbg) dst_dbg[j] = v;
   }

@@ -1,0 +1,56 @@
+// csa2_decode.cuh -- cached entries and window tokens back to fp32, in units of
+// eight values (exact: at most 8 significant bits times a power of two).
+#pragma once
+
+#include "csa2_device.cuh"
+
+namespace csa2 {
+
+// Eight E2M1 codes (low nibble first) times a scale.
+__device__ __forceinline__ void e2m1x8(uint32_t w, float s, float *v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h;
+    asm("{\n .reg .b8 t;\n cvt.u8.u32 t, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n" : "=r"(h) : "r"(w >> (8 * i)));
+    const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h));
+    v[2 * i] = f.x * s;
+    v[2 * i + 1] = f.y * s;
+  }
+}
+__device__ __forceinline__ void e4m3x8(uint2 w, float s, float *v) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = e4m3_value(((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0xFFu) * s;
+}
+__device__ __forceinline__ void bf16x8(uint4 w, float *v) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+// Unit u (values 8u .. 8u + 7: latent units 0..63, then RoPE) of physical entry pe.
+__device__ __forceinline__ void entry_unit8(const csa2_cache &c, int64_t pe, int u, float *v) {
+  if (c.entry_format == CSA2_ENTRY_FP8) {
+    if (u < 64)
+      e4m3x8(reinterpret_cast<const uint2 *>(c.lat_codes + pe * 512)[u], e8m0_value(c.lat_scales[pe * 16 + (u >> 2)]), v);
+    else
+      bf16x8(reinterpret_cast<const uint4 *>(c.rope_codes + pe * 128)[u - 64], v);
+  } else if (u < 64) {
+    e2m1x8(reinterpret_cast<const uint32_t *>(c.lat_codes + pe * 256)[u], e4m3_value(c.lat_scales[pe * 32 + (u >> 1)]), v);
+  } else {
+    e2m1x8(reinterpret_cast<const uint32_t *>(c.rope_codes + pe * 32)[u - 64],
+           e4m3_value(c.rope_scales[pe * 4 + ((u - 64) >> 1)]), v);
+  }
+}
+
+// Unit u of window row `row` (a ring slot or a chunk's window row).
+__device__ __forceinline__ void window_unit8(const uint8_t *codes, const uint8_t *scales, int swa_dtype, int64_t row,
+                                             int u, float *v) {
+  if (swa_dtype == CSA2_SWA_MXFP8)
+    e4m3x8(reinterpret_cast<const uint2 *>(codes + row * 576)[u], e8m0_value(scales[row * kSwaScaleStride + (u >> 2)]), v);
+  else
+    bf16x8(reinterpret_cast<const uint4 *>(codes + row * 1152)[u], v);
+}
+
+}  // namespace csa2

@@ -7,6 +7,39 @@
 
 namespace csa2 {
 
+// Whether sequence b may take n_new more tokens (capacity in entries, RoPE table).
+__device__ __forceinline__ bool append_ok(const csa2_cache &c, int64_t t0, int n_new, int64_t rope_len) {
+  return (t0 + n_new) / c.ratio <= static_cast<int64_t>(c.capacity) && t0 + n_new <= rope_len;
+}
+
+__device__ __forceinline__ void append_fail(const csa2_cache &c, int64_t t0, int n_new, int64_t rope_len,
+                                            int32_t *err) {
+  if ((t0 + n_new) / c.ratio > static_cast<int64_t>(c.capacity)) raise_err(err, CSA2_DEVERR_CAPACITY);
+  else raise_err(err, CSA2_DEVERR_ROPE);
+}
+
+// One channel of a ratio-2 entry ([P5] §2.3.1): softmax over the gate logits
+// Z + B of the 4 rows (the b rows only when the entry has a predecessor), then
+// the gated sum of the C rows, in fp64, rounded once to fp32.
+__device__ __forceinline__ float r2_compress_channel(float za0, float za1, float zb0, float zb1, float ba0, float ba1,
+                                                     float bb0, float bb1, float ca0, float ca1, float cb0, float cb1,
+                                                     bool has_b) {
+  double l0 = __dadd_rn(static_cast<double>(za0), static_cast<double>(ba0));
+  double l1 = __dadd_rn(static_cast<double>(za1), static_cast<double>(ba1));
+  double l2 = has_b ? __dadd_rn(static_cast<double>(zb0), static_cast<double>(bb0)) : -INFINITY;
+  double l3 = has_b ? __dadd_rn(static_cast<double>(zb1), static_cast<double>(bb1)) : -INFINITY;
+  double mx = fmax(fmax(l0, l1), fmax(l2, l3));
+  double e0 = exp(__dadd_rn(l0, -mx)), e1 = exp(__dadd_rn(l1, -mx));
+  double e2 = has_b ? exp(__dadd_rn(l2, -mx)) : 0.0, e3 = has_b ? exp(__dadd_rn(l3, -mx)) : 0.0;
+  double den = __dadd_rn(__dadd_rn(__dadd_rn(__dadd_rn(0.0, e0), e1), e2), e3);
+  double acc = 0.0;
+  acc = __dadd_rn(acc, __dmul_rn(__ddiv_rn(e0, den), static_cast<double>(ca0)));
+  acc = __dadd_rn(acc, __dmul_rn(__ddiv_rn(e1, den), static_cast<double>(ca1)));
+  acc = __dadd_rn(acc, __dmul_rn(__ddiv_rn(e2, den), static_cast<double>(cb0)));
+  acc = __dadd_rn(acc, __dmul_rn(__ddiv_rn(e3, den), static_cast<double>(cb1)));
+  return __double2float_rn(acc);
+}
+
 // Encode entry `e` of sequence b from an fp32 row in shared memory:
 // row[0:576] = main vector (RoPE dims 512..575 not yet rotated), row[576:704] = indexer key.
 // The cache's entry format decides the record: V4.1 FP4 (the 288 B record and

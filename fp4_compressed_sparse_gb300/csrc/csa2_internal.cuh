@@ -12,6 +12,8 @@ void set_error_detail(const char *msg);
 csa2_status fail(csa2_status st, const char *fmt, ...) __attribute__((format(printf, 2, 3)));
 // CSA2_OK for cudaSuccess, else CSA2_ERR_CUDA with "what: <CUDA error text>" as the detail
 csa2_status cuda_status(cudaError_t e, const char *what);
+// host validation of a cache descriptor
+csa2_status check_cache(const csa2_cache *c);
 // SM count of the current device (queried once per device)
 int device_sm_count();
 // Raises fn's dynamic shared-memory limit to at least `bytes` on the current
@@ -40,6 +42,29 @@ __host__ __forceinline__ bool aligned16(const void *p) { return (reinterpret_cas
 cudaError_t launch_kv_append(const csa2_cache &c, const void *kv, const void *ik, int in_dtype,
                              const csa2_compress_in *cmp, const float *rope_cs, int64_t rope_len, int n_new,
                              float *cmp_dbg, int32_t *err, cudaStream_t s);
+
+// ------------------------------------------------------------------ ragged batches
+// Sequence of packed row r: the last b with cu[b] <= r, or -1 for a row of no
+// sequence (r >= cu[batch], or before cu[0]).
+__device__ __forceinline__ int ragged_seq(const int32_t *cu, int batch, int r) {
+  if (r >= cu[batch] || r < cu[0]) return -1;
+  int lo = 0, hi = batch;  // cu[lo] <= r < cu[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (cu[mid] <= r) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+// Rows of sequence b: its first row and their number; false (count 0) when cu is
+// not a non-decreasing list within 0..total, or the count breaks max_new.
+__device__ __forceinline__ bool ragged_rows(const int32_t *cu, int b, int total, int max_new, int &first, int &n) {
+  first = cu[b];
+  const int end = cu[b + 1];
+  const bool ok = first >= 0 && end >= first && end <= total && end - first <= max_new;
+  n = ok ? end - first : 0;
+  return ok;
+}
 
 // ------------------------------------------------------------------ score sideband
 // Per score row, the index-score kernel also leaves a 13-bit histogram of the

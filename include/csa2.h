@@ -377,6 +377,107 @@ csa2_status csa2_prefill_chunk(const csa2_cache *cache, int32_t seq, const csa2_
                                size_t ws_bytes, int32_t *err_word, csa2_stream_t stream);
 
 /*
+ * Ragged calls: a batch whose sequences bring different numbers of new tokens
+ * (chunks of prompts beside single decoded tokens).  The tokens are packed one
+ * sequence after the other: sequence b has rows cu[b] .. cu[b+1]-1 of every
+ * per-token array, cu int32 [batch+1] in device memory with cu[0] = 0,
+ * non-decreasing; a sequence may have none.  total is the number of rows the
+ * arrays hold (host): rows from cu[batch] on belong to no sequence, so one call
+ * (or captured graph) may serve batches that fill it differently; outputs of
+ * those rows are left as they were.  max_new is the caller's bound on
+ * cu[b+1]-cu[b] (host; it decides launch shapes): a sequence that breaks it, or
+ * whose cu does not fit the arrays, is skipped with the INDEX bit.
+ *
+ * Window rows of a chunk.  The ring holds a sequence's last 128 tokens, but a
+ * chunk's earlier queries look further back: for them the append leaves, per
+ * sequence, the 128 tokens before the chunk followed by the chunk's own, in the
+ * window's format, rows cu[b] + 128 b .. : row cu[b] + 128 b + i is token
+ * P - 128 + i, P = n_tokens[b] before the append (zeros where that is
+ * negative).  win_codes: (total + 128 batch) rows of 576 (MXFP8) or 1,152
+ * (bf16) bytes; win_scales: as many rows of 32 bytes (MXFP8; may be NULL for
+ * bf16).  csa2_chunk_window_bytes() gives the two sizes (plane 0, 1).
+ */
+size_t csa2_chunk_window_bytes(int32_t batch, int32_t total, int32_t swa_dtype, int32_t plane);
+
+/*
+ * csa2_kv_append_ragged: csa2_kv_append for a ragged batch; the records, the
+ * ring, the compression buffer and n_tokens end up as if every sequence had
+ * been appended by itself.
+ *   ratio 1: kv rows of 576, idx_key rows of 128, element type in_dtype, row t at
+ *            kv + t * kv_stride elements (kv_stride >= 576, key_stride >= 128, both
+ *            multiples of 8: a row may be a slice of a wider projection);
+ *            cmp = NULL.
+ *   ratio 2: cmp rows [total][704] each; kv = idx_key = NULL, strides ignored.
+ *   win_codes / win_scales: the chunk's window rows (above), or NULL.
+ * The call reads the ring before it overwrites it; win_codes must not be in use
+ * by an earlier call on another stream.  total 0 is a valid call (nothing done).
+ * Device errors: CAPACITY, ROPE (nothing written for the sequence, its n_tokens
+ * stays), INDEX (a page id outside the pool, cu, max_new).
+ */
+csa2_status csa2_kv_append_ragged(const csa2_cache *cache, const void *kv, int64_t kv_stride, const void *idx_key,
+                                  int64_t key_stride, int32_t in_dtype, const csa2_compress_in *cmp,
+                                  const int32_t *cu_new, int32_t total, int32_t max_new, const float *rope_cs,
+                                  int64_t rope_len, uint8_t *win_codes, uint8_t *win_scales, int32_t *err_word,
+                                  csa2_stream_t stream);
+
+/* element types of what the reads and the chunk attention write */
+#define CSA2_OUT_F32 0
+#define CSA2_OUT_BF16 1
+
+/*
+ * csa2_kv_read: cached entries back as the values they stand for.
+ *   Rows cu_rows[b] .. cu_rows[b+1]-1 read sequence b: row r is entry
+ *   pos[r] (int32 [total]; any order, repeats allowed, negative = an empty row)
+ *   when pos != NULL, else entry start[b] + (r - cu_rows[b]) (int64 [batch]).
+ *   out_main: rows of 576 (512 latent, then the 64 rotated RoPE dims), or NULL;
+ *   out_key: rows of 128 (the indexer key), or NULL; out_dtype, row strides in
+ *   elements (>= 576 / 128, multiples of 8).  Every value is exact in fp32, and in
+ *   bf16 too for FP4 records and keys, MXFP8 latents and bf16 RoPE dims.
+ *   Empty rows are zeros.  Rows of no sequence are left as they were.
+ * Device errors: INDEX (an entry not in the cache, floor(n_tokens/ratio) or more,
+ * a negative start, or a bad page id: the row is zeros).
+ */
+csa2_status csa2_kv_read(const csa2_cache *cache, const int32_t *cu_rows, int32_t total, const int32_t *pos,
+                         const int64_t *start, void *out_main, int64_t main_stride, void *out_key, int64_t key_stride,
+                         int32_t out_dtype, int32_t *err_word, csa2_stream_t stream);
+
+/*
+ * csa2_window_read: the sliding window's tokens in order, out [batch][128][576]
+ * of out_dtype: row i is token n_tokens[b] - 128 + i (zeros where negative).
+ */
+csa2_status csa2_window_read(const csa2_cache *cache, void *out, int32_t out_dtype, csa2_stream_t stream);
+
+/*
+ * csa2_chunk_attn: dense attention of a ragged batch's new tokens (already
+ * appended) over every visible entry of the cache and the window: the layer
+ * form without a selection ([P5] §2.3.2 dense attention over compressed
+ * entries; window-only layers; contexts no longer than the top-k).  Definition
+ * and operands as csa2_sparse_attn_decode with every visible entry selected.
+ *   q: bf16 [total][n_heads][576]; query row cu_q[b] + i of a sequence with n
+ *      new tokens is at position p = n_tokens[b] - n + i; it sees entries
+ *      s < floor(p / ratio) and window tokens max(0, p-127) .. p.
+ *   win_codes / win_scales: the append's window rows for the same cu, or NULL:
+ *      the window then comes from the ring, which holds what single new tokens
+ *      need (a query whose window reaches behind the ring raises INDEX and goes
+ *      without those tokens).
+ *   sink: fp32 [n_heads] or NULL; sm_scale finite.
+ *   out: out_dtype [total][n_heads][512]; lse: fp32 [total][n_heads].
+ * n_heads: a multiple of 16, 16..128.  The work is split over the GPU by the
+ * batch's total work, so a row's last bits may change with the batch (use
+ * csa2_sparse_attn_decode where batch invariance is needed); equal calls give
+ * equal bits.
+ * ws: device workspace of csa2_chunk_attn_workspace_size() bytes (for the
+ * current device); calls that may overlap need one each.
+ * Device errors: INDEX (a page id outside the pool: those entries are skipped;
+ * cu, max_new; a window behind the ring), TIMEOUT.
+ */
+size_t csa2_chunk_attn_workspace_size(int32_t batch, int32_t total, int32_t n_heads);
+csa2_status csa2_chunk_attn(const csa2_cache *cache, const uint16_t *q, int32_t n_heads, const int32_t *cu_q,
+                            int32_t total, int32_t max_new, const uint8_t *win_codes, const uint8_t *win_scales,
+                            const float *sink, float sm_scale, void *out, int32_t out_dtype, float *lse, void *ws,
+                            size_t ws_bytes, int32_t *err_word, csa2_stream_t stream);
+
+/*
  * csa2_mxf4_peak_launch: measurement helper (not a step of the method).
  * Launches n_ctas CTAs that each issue `iters` back-to-back block-scaled FP4
  * tensor-core MMAs (tcgen05 kind::mxf4, M 128 x N 128 x K 64, the index score's
