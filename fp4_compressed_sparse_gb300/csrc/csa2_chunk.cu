@@ -7,16 +7,16 @@
 //
 // A sequence's query rows (token, head) are cut into row tiles of 64 rows; a
 // row tile's keys are the visible entries 0 .. T-1 followed by its window
-// tokens, in key tiles of 128 (an entry tile never straddles a page).  Three
+// tokens, in key tiles of 64 (an entry tile never straddles a page).  Three
 // launches: k_chunk_plan lists the row tiles and deals all key tiles out evenly
 // over the SMs (a row tile may be shared by several CTAs, at most two partial
 // results per CTA), k_chunk_attn computes, k_chunk_merge joins the row tiles
 // that were shared.
 //
 // Work and bound.  2 x 1088 flop per (row, key) against 324 B per key: with 64
-// heads 430 flop per byte, so the tensor cores bound it, not HBM.  With 64 rows
-// the operands' shared-memory reads (6 KB per 32-cycle MMA step, 128 B per
-// cycle) allow about two thirds of the tensor rate.
+// heads 430 flop per byte, so the tensor cores bound it, not HBM.  fp16 operands
+// hold the records exactly (E2M1 x E4M3 has 6 significant bits; other formats
+// with a power of two per key), accumulators are fp32.
 #include <cmath>
 #include <cuda_fp16.h>
 
@@ -27,20 +27,20 @@
 namespace csa2 {
 namespace {
 
-constexpr int kRows = 64;                        // rows of a row tile
-constexpr int kKeys = 128;                       // keys of a key tile
-constexpr int kBlk = kKeys * 128;                // one 64-dim block of a key tile: 16 KB
-constexpr int kQBlk = kRows * 128;               // one 64-dim block of the query: 8 KB
-constexpr int kBlocks = kDqk / 64;               // 9: 8 latent, 1 RoPE
-constexpr int kSmWarps = 8, kPrWarps = 8;        // softmax / producer warps
-constexpr int kMmaWarp = kSmWarps + kPrWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
-constexpr uint32_t kColS = 0, kColO = 256;       // TMEM columns: S^T 64, O^T 4 x 64
+constexpr int kRows = 64;                    // rows of a row tile
+constexpr int kKeys = 64;                    // keys of a key tile
+constexpr int kBlk = kKeys * 128;            // a 64-dim block of a key tile, or of the query: 8 KB
+constexpr int kBlocks = kDqk / 64;           // 9: 8 latent, 1 RoPE
+constexpr int kTile = kBlocks * kBlk;        // 73,728 B
+constexpr int kSmWarps = 4, kPrWarps = 8;    // softmax / producer warps
+constexpr int kMmaWarp = kSmWarps + kPrWarps, kAheadWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kAheadWarp + 1);
+constexpr int kAhead = 4;                    // key tiles requested into L2 ahead of use
+constexpr uint32_t kColS = 0, kColO = 256;   // TMEM columns: S 2 x 64, O^T 4 x 64
 constexpr uint32_t kWaitIters = 200;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kUnset = -1e30f;                 // reference maximum of a row that has seen no key
-constexpr float kTop = 8.0f, kSlack = 15.0f;     // a new reference puts the maximum at 2^8; 2^15 still fits fp16
-constexpr int64_t kPartFloats = 4 * 64 * kKeys + 2 * kRows;  // O^T [4][16][128][4], then (m, l) per row
+constexpr float kTop = 4.0f, kSlack = 15.0f;  // a new reference puts the maximum at 2^4; 2^15 still fits fp16
+constexpr int64_t kPartFloats = kLat * kRows + 2 * kRows;  // O^T [4][16][128][4], then (m, l) per row
 
 struct ChunkArgs {
   csa2_cache c;
@@ -201,24 +201,68 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
   d |= static_cast<uint64_t>(2) << 61;
   return d;
 }
-// kind::f16, fp16 x fp16 -> fp32; mn: both operands MN-major
-__host__ __device__ constexpr uint32_t idesc_f16(int m, int n, int mn) {
-  return (1u << 4) | (static_cast<uint32_t>(mn) << 15) | (static_cast<uint32_t>(mn) << 16) |
-         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
+// Issued by one elected lane of a warp whose control flow is uniform: the
+// descriptors then live in uniform registers and a step's issue takes about 33
+// cycles (61 from inside a one-lane branch), as long as the step itself.
+__device__ __forceinline__ void mma_f16(uint32_t elected, uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  if (elected)
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
+            d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
 }
-__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(
-          d_tmem),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc)
-      : "memory");
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e;
 }
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t *r) {
+// S[64 rows][64 keys] = Q K^T, K 16 per step
+__device__ __forceinline__ void mma_qk(uint32_t elected, uint32_t d, uint64_t dq, uint64_t dk) {
+  constexpr uint32_t id = (1u << 4) | ((kKeys >> 3) << 17) | ((kRows >> 4) << 24);
+#pragma unroll
+  for (int i = 0; i < 36; ++i)
+    mma_f16(elected, d, dq + (((i / 4) * kBlk + 32 * (i % 4)) >> 4), dk + (((i / 4) * kBlk + 32 * (i % 4)) >> 4), id, i ? 1u : 0u);
+}
+// 128 dims of O^T[512 dims][64 rows] += V^T P^T, 16 keys per step; V^T MN-major
+__device__ __forceinline__ void mma_pv(uint32_t elected, uint32_t d, uint64_t dv, uint64_t dp, uint32_t acc) {
+  constexpr uint32_t id = (1u << 4) | (1u << 15) | ((kRows >> 3) << 17) | ((128u >> 4) << 24);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) mma_f16(elected, d, dv + ((2048 * i) >> 4), dp + ((32 * i) >> 4), id, i ? 1u : acc);
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t *r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t *r) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+// wait for four of them, their registers tied to it
+__device__ __forceinline__ void tmem_ld_wait_x8x4(uint32_t *r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) : : "memory");
+}
+// 16 lanes x 64 columns, the lanes' rows spread over the warp: thread t gets
+// columns 8 j + 2 (t % 4) + {0, 1} of row t / 4 in r[4 j], r[4 j + 1] and of row
+// t / 4 + 8 in r[4 j + 2], r[4 j + 3].  Waits.
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t *r) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(
-          taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\ntcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -253,21 +297,18 @@ __device__ __forceinline__ uint4 ldg16(const void *p) {
 }
 
 struct __align__(1024) ChunkSmem {
-  uint8_t k[kBlocks][kBlk];   // the key tile in fp16; block 8 (RoPE) then holds P^T
-  uint8_t q[kBlocks][kQBlk];
-  __align__(16) float2 fm[kRows];      // logit factor and minus the reference maximum (log2 units) of each row
-  __align__(16) float alpha[kRows];
-  __align__(16) float fin[kRows];
-  __align__(16) float qf[kRows];
-  float lsum[4][kRows];
-  int32_t rowmax[kRows];               // ordered-int maxima of a tile (reference updates)
-  int32_t vis[kRows], w0[kRows];       // a row sees keys j < vis and w0 <= j < w0 + 128
-  float sg[2][kKeys];                  // sigma of each key (-inf: no key)
-  int plain[2];                        // every key valid with sigma 0
-  uint32_t tmem;
-  __align__(8) uint64_t full[5];       // dims 128 i .. of the tile filled (4: RoPE)
-  __align__(8) uint64_t empty[5];      // ... read by the last MMA (4: P too)
-  __align__(8) uint64_t s_full, p_full, q_ready;
+  uint8_t k[2][kBlocks][kBlk];      // two key tiles in fp16; block 8 (RoPE) then holds the tile's P
+  uint8_t q[kBlocks][kBlk];
+  __align__(16) float alpha[kRows]; // rescale of a row's O^T column in this tile (1: none)
+  __align__(16) float fin[kRows];   // output factor of the finished item's rows
+  __align__(16) float2 sg[2][kKeys]; // sigma of each key (-inf: no key) and 2^sigma
+  float f[kRows];                   // logit factor of each row
+  int32_t vis[kRows], w0[kRows];    // a row sees keys j < vis and w0 <= j < w0 + 128
+  int plain[2];                     // every key valid with sigma 0
+  uint32_t tmem, progress;          // progress: the key tile (of this CTA's) being filled
+  __align__(8) uint64_t full[2];      // tile filled
+  __align__(8) uint64_t empty[2][4];  // ... and PV over its dims 128 i .. complete (3: P read too)
+  __align__(8) uint64_t s_full[2], p_full, q_ready;
 };
 
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, int32_t *err) {
@@ -278,43 +319,33 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, int32_
   }
   return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
-__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;\n" ::: "memory"); }
+__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 128;\n" ::: "memory"); }
 __device__ __forceinline__ int bar_softmax_or(int v) {
   int r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n selp.s32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.s32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
       : "r"(v)
       : "memory");
   return r;
 }
-__device__ __forceinline__ void bar_producers() { asm volatile("bar.sync 2, 256;\n" ::: "memory"); }
-__device__ __forceinline__ int32_t order_int(float f) {
-  const int32_t i = __float_as_int(f);
-  return i >= 0 ? i : i ^ 0x7FFFFFFF;
-}
-__device__ __forceinline__ float order_float(int32_t i) { return __int_as_float(i >= 0 ? i : i ^ 0x7FFFFFFF); }
 
-// The work items of one CTA, in order: key tiles [k0, k1) of row tile t.
+// The work items of one CTA, in order: key tiles [k0, k1) of row tile t.  (Kept
+// small: what is needed once per item is read again.)
 struct Items {
-  const Plan &p;
-  CtaRange r;
-  int t;
-  int64_t c0;
-  RowTile x;
-  int k0, k1;
-  __device__ __forceinline__ Items(const Plan &plan, int g) : p(plan), r(plan.cta[g]), t(r.tile - 1), c0(0) {}
-  __device__ __forceinline__ bool next() {
+  int t, k0, k1;
+  __device__ __forceinline__ Items(const Plan &p, int g) { t = p.cta[g].tile - 1; }
+  __device__ __forceinline__ const RowTile *x(const Plan &p) const { return p.tile + t; }
+  __device__ __forceinline__ bool next(const Plan &p, int g) {
+    const int64_t lo = p.cta[g].lo, hi = p.cta[g].hi;
+    if (hi <= lo) return false;
     for (;;) {
-      ++t;
-      if (r.hi <= r.lo) return false;
-      c0 = p.cum[t];
-      if (c0 >= r.hi || t >= p.max_tiles) return false;
-      x = p.tile[t];
-      k0 = static_cast<int>(r.lo > c0 ? r.lo - c0 : 0);
-      k1 = static_cast<int>(r.hi - c0 < x.ntiles ? r.hi - c0 : x.ntiles);
+      const int64_t c0 = p.cum[++t];
+      if (c0 >= hi || t >= p.max_tiles) return false;
+      const int nt = p.tile[t].ntiles;
+      k0 = static_cast<int>(lo > c0 ? lo - c0 : 0);
+      k1 = static_cast<int>(hi - c0 < nt ? hi - c0 : nt);
       if (k0 < k1) return true;
-      if (c0 + x.ntiles + 1 >= r.hi) return false;
     }
   }
 };
@@ -326,63 +357,70 @@ __device__ __forceinline__ int sigma_of(int e) {
   return max(-24, min(120, e - 8));
 }
 
-// ------------------------------------------------------------------ producers
-// Tiles of whole entries in the common formats come through registers, half a
-// tile ahead: step s < 8 is dims 128 (s / 2) .. of keys 64 (s % 2) .., one quarter
-// (32 dims) of a key per thread; steps 8, 9 are the RoPE dims.
+// ------------------------------------------------------------------ filling a tile
+// Five steps: dims 128 s .. of the 64 keys (s < 4), then the RoPE dims; four
+// threads per key, 32 (RoPE: 16) dims each.  The records come through registers,
+// requested a whole tile ahead (and into L2 further ahead, by the ahead warp).
+template <class Raw>
+struct IsFp4 {
+  static constexpr bool v = false;
+};
 struct RawFp4 {
-  uint4 w;
-  uint32_t sc;
+  uint4 w[4];
+  uint2 r;
+  uint32_t sc[5];
+};
+template <>
+struct IsFp4<RawFp4> {
+  static constexpr bool v = true;
 };
 struct RawFp8 {
-  uint4 w[2];
-  uint32_t sc;
+  uint4 w[5][2];
+  uint4 sc;  // the key's 16 scales: word s holds those of step s
 };
-__device__ __forceinline__ void load_raw(const csa2_cache &c, int64_t base, int s, int pt, RawFp4 &r) {
-  if (s < 8) {
-    const int64_t e = base + 64 * (s & 1) + (pt >> 2);
-    r.w = ldg16(c.lat_codes + e * 256 + 64 * (s >> 1) + 16 * (pt & 3));
-    r.sc = __ldg(reinterpret_cast<const uint16_t *>(c.lat_scales + e * 32 + 8 * (s >> 1) + 2 * (pt & 3)));
-  } else if (s == 8) {
-    const int64_t e = base + (pt >> 1);
-    r.w = ldg16(c.rope_codes + e * 32 + 16 * (pt & 1));
-    r.sc = __ldg(reinterpret_cast<const uint16_t *>(c.rope_scales + e * 4 + 2 * (pt & 1)));
+__device__ __forceinline__ uint32_t ldg_u16(const uint8_t *p) { return __ldg(reinterpret_cast<const uint16_t *>(p)); }
+__device__ __forceinline__ void load_step(const csa2_cache &c, int64_t e, int qd, int s, RawFp4 &r) {
+  if (s < 4) {
+    r.w[s] = ldg16(c.lat_codes + e * 256 + 64 * s + 16 * qd);
+    r.sc[s] = ldg_u16(c.lat_scales + e * 32 + 8 * s + 2 * qd);
+  } else {
+    r.r = __ldg(reinterpret_cast<const uint2 *>(c.rope_codes + e * 32 + 8 * qd));
+    r.sc[4] = __ldg(c.rope_scales + e * 4 + qd);
   }
 }
-__device__ __forceinline__ void load_raw(const csa2_cache &c, int64_t base, int s, int pt, RawFp8 &r) {
-  const int64_t e = base + 64 * (s & 1) + (pt >> 2);
-  const uint8_t *src = s < 8 ? c.lat_codes + e * 512 + 128 * (s >> 1) + 32 * (pt & 3) : c.rope_codes + e * 128 + 32 * (pt & 3);
-  r.w[0] = ldg16(src);
-  r.w[1] = ldg16(src + 16);
-  if (s < 8) r.sc = __ldg(c.lat_scales + e * 16 + 4 * (s >> 1) + (pt & 3));
+__device__ __forceinline__ void load_step(const csa2_cache &c, int64_t e, int qd, int s, RawFp8 &r) {
+  const uint8_t *src = s < 4 ? c.lat_codes + e * 512 + 128 * s + 32 * qd : c.rope_codes + e * 128 + 32 * qd;
+  r.w[s][0] = ldg16(src);
+  r.w[s][1] = ldg16(src + 16);
+  if (s == 4) r.sc = ldg16(c.lat_scales + e * 16);  // (the last step: the old scales are done with)
 }
+
 __device__ __forceinline__ uint4 dq_e2m1(uint32_t w, uint32_t s2) {
   return make_uint4(hmul2u(e2m1x2_h2(w), s2), hmul2u(e2m1x2_h2(w >> 8), s2), hmul2u(e2m1x2_h2(w >> 16), s2),
                     hmul2u(e2m1x2_h2(w >> 24), s2));
 }
-// 16-byte chunk x (8 dims) of key `key` in a 64-dim block
+// 16-byte chunk x (8 dims) of key (or query row) `key` in a 64-dim block
 __device__ __forceinline__ uint8_t *chunk_at(uint8_t *blk, int key, int x) { return blk + key * 128 + ((x ^ (key & 7)) << 4); }
-
-__device__ __forceinline__ void store_raw(ChunkSmem &sm, int s, int pt, const RawFp4 &r, int) {
-  uint32_t w[4] = {r.w.x, r.w.y, r.w.z, r.w.w};
-  uint32_t sa = e4m3x2_h2((r.sc & 0xFF) * 0x101), sb = e4m3x2_h2((r.sc >> 8) * 0x101);
-  if (s < 8) {
-    const int key = 64 * (s & 1) + (pt >> 2), qd = pt & 3;
-    uint8_t *blk = sm.k[2 * (s >> 1) + (qd >> 1)];
-    // the second block's lanes take their chunks in the order 2 3 0 1, so that the
-    // eight lanes of a store phase (2 keys x 4 quarters) hit eight different 16 B banks
-    const int flip = qd & 2;
-    if (flip) {
+// Chunks i = 0..3 of a thread's 32 dims of step s.  Lanes of the second 64-dim
+// block (qd >= 2) take theirs in the order 2 3 0 1, so that the eight lanes of a
+// store phase (2 keys x 4 quarters) hit eight different 16 B banks.
+__device__ __forceinline__ uint8_t *quarter_at(uint8_t (*k)[kBlk], int s, int key, int qd, int i) {
+  return chunk_at(k[2 * s + (qd >> 1)], key, 4 * (qd & 1) + (i ^ (qd & 2)));
+}
+__device__ __forceinline__ void store_step(uint8_t (*k)[kBlk], int s, int key, int qd, const RawFp4 &r, int) {
+  if (s < 4) {
+    uint32_t w[4] = {r.w[s].x, r.w[s].y, r.w[s].z, r.w[s].w};
+    uint32_t sa = e4m3x2_h2((r.sc[s] & 0xFF) * 0x101), sb = e4m3x2_h2((r.sc[s] >> 8) * 0x101);
+    if (qd & 2) {
       const uint32_t t0 = w[0], t1 = w[1], ts = sa;
       w[0] = w[2], w[1] = w[3], w[2] = t0, w[3] = t1, sa = sb, sb = ts;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint4 *>(chunk_at(blk, key, 4 * (qd & 1) + (i ^ flip))) = dq_e2m1(w[i], i < 2 ? sa : sb);
-  } else if (s == 8) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint4 *>(chunk_at(sm.k[8], pt >> 1, 4 * (pt & 1) + i)) = dq_e2m1(w[i], i < 2 ? sa : sb);
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(quarter_at(k, s, key, qd, i)) = dq_e2m1(w[i], i < 2 ? sa : sb);
+  } else {
+    const uint32_t s2 = e4m3x2_h2(r.sc[4] * 0x101);
+    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, 2 * qd)) = dq_e2m1(r.r.x, s2);
+    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, 2 * qd + 1)) = dq_e2m1(r.r.y, s2);
   }
 }
 // factor 2^k as an fp16 pair (k <= 15; zero where fp16 has no such value)
@@ -390,53 +428,46 @@ __device__ __forceinline__ uint32_t pow2_h2(int k) {
   const uint32_t h = k < -24 ? 0u : k < -14 ? 1u << (k + 24) : static_cast<uint32_t>(k + 15) << 10;
   return h * 0x10001u;
 }
-__device__ __forceinline__ void store_raw(ChunkSmem &sm, int s, int pt, const RawFp8 &r, int sigma) {
-  const int key = 64 * (s & 1) + (pt >> 2), qd = pt & 3;
-  uint32_t o[16];
-  const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
-  if (s < 8) {
-    const uint32_t m2 = pow2_h2(static_cast<int>(r.sc) - 127 - sigma);
-    const int flip = qd & 2;
-    uint8_t *blk = sm.k[2 * (s >> 1) + (qd >> 1)];
+// 32 E4M3 values times 2^(sc - 127 - sigma) as a thread's dims of step s
+__device__ __forceinline__ void store_e4m3(uint8_t (*k)[kBlk], int s, int key, int qd, const uint4 *c, uint32_t sc, int sigma) {
+  const uint32_t m2 = pow2_h2(static_cast<int>(sc) - 127 - sigma);
+  const bool flip = qd & 2;
+  const uint4 a = flip ? c[1] : c[0], b = flip ? c[0] : c[1];
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      o[2 * i] = hmul2u(e4m3x2_h2(w[i]), m2);
-      o[2 * i + 1] = hmul2u(e4m3x2_h2(w[i] >> 16), m2);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = i ^ 2;
-      *reinterpret_cast<uint4 *>(chunk_at(blk, key, 4 * (qd & 1) + (i ^ flip))) =
-          flip ? make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3])
-               : make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-    }
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<uint4 *>(quarter_at(k, s, key, qd, i)) =
+        make_uint4(hmul2u(e4m3x2_h2(w[2 * i]), m2), hmul2u(e4m3x2_h2(w[2 * i] >> 16), m2),
+                   hmul2u(e4m3x2_h2(w[2 * i + 1]), m2), hmul2u(e4m3x2_h2(w[2 * i + 1] >> 16), m2));
+}
+__device__ __forceinline__ uint4 bf16x8_h(uint4 v, float inv) {
+  return make_uint4(pack_h2(__uint_as_float(v.x << 16) * inv, __uint_as_float(v.x & 0xFFFF0000u) * inv),
+                    pack_h2(__uint_as_float(v.y << 16) * inv, __uint_as_float(v.y & 0xFFFF0000u) * inv),
+                    pack_h2(__uint_as_float(v.z << 16) * inv, __uint_as_float(v.z & 0xFFFF0000u) * inv),
+                    pack_h2(__uint_as_float(v.w << 16) * inv, __uint_as_float(v.w & 0xFFFF0000u) * inv));
+}
+__device__ __forceinline__ uint32_t word_of(uint4 v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ void store_step(uint8_t (*k)[kBlk], int s, int key, int qd, const RawFp8 &r, int sigma) {
+  if (s < 4) {
+    store_e4m3(k, s, key, qd, r.w[s], (word_of(r.sc, s) >> (8 * qd)) & 0xFF, sigma);
   } else {  // 16 RoPE dims in bf16
     const float inv = pow2f(-sigma);
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      o[i] = pack_h2(__uint_as_float(w[i] << 16) * inv, __uint_as_float(w[i] & 0xFFFF0000u) * inv);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<uint4 *>(chunk_at(sm.k[8], key, 2 * qd + i)) = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, 2 * qd)) = bf16x8_h(r.w[4][0], inv);
+    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, 2 * qd + 1)) = bf16x8_h(r.w[4][1], inv);
   }
 }
-template <class Raw>
-struct IsFp4 {
-  static constexpr bool v = false;
-};
-template <>
-struct IsFp4<RawFp4> {
-  static constexpr bool v = true;
-};
-__device__ __forceinline__ int e8m0_top(uint4 s, int more) {  // largest of 16 scale bytes and `more`
+__device__ __forceinline__ int e8m0_top(uint4 s) {  // largest of 16 scale bytes
   uint32_t m = __vmaxu4(__vmaxu4(s.x, s.y), __vmaxu4(s.z, s.w));
   m = __vmaxu4(m, m >> 16);
-  m = max(m & 0xFF, (m >> 8) & 0xFF);
-  return max(static_cast<int>(m), more);
+  return max(m & 0xFF, (m >> 8) & 0xFF);
 }
 __device__ __forceinline__ uint32_t bf16_top(uint4 v, uint32_t m) {  // largest magnitude bits of 8 bf16
   const uint32_t a = __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), b = __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu);
   return __vmaxu2(m, __vmaxu2(a, b));
+}
+__device__ __forceinline__ uint32_t key_max(uint32_t bf) {  // over the four threads of a key
+  bf = __vmaxu2(bf, __shfl_xor_sync(0xffffffffu, bf, 1));
+  return __vmaxu2(bf, __shfl_xor_sync(0xffffffffu, bf, 2));
 }
 // exponent e (largest magnitude about 2^e) of a key: an E8M0 top (block maximum
 // about 2^(top - 119)) and / or the largest bf16 magnitude
@@ -445,179 +476,237 @@ __device__ __forceinline__ int key_exponent(int e8, uint32_t bf) {
   const int a = e8 > 0 ? e8 - 119 : -2000, b = mb > 0 ? (mb >> 7) - 127 : -2000;
   return max(a, b);
 }
+__device__ __forceinline__ int raw_sigma(const RawFp4 &) { return 0; }
+__device__ __forceinline__ int raw_sigma(const RawFp8 &r) {
+  return sigma_of(key_exponent(e8m0_top(r.sc), key_max(bf16_top(r.w[4][0], bf16_top(r.w[4][1], 0)))));
+}
 
 // A tile that is not made of whole entries alone: key j is entry j (j < T), a
-// window token, or nothing.  Two threads per key, straight from memory.
+// window token, or nothing.
 struct TailKey {
-  int kind;  // 0 nothing, 1 entry, 2 window row
-  int64_t at;
-  const uint8_t *codes, *scales;
-  int sigma;
+  int kind;  // 0 nothing, 1 FP4 entry, 2 V4 entry, 3 MXFP8 window row, 4 bf16 window row
+  const uint8_t *codes, *scales, *rope, *rope_scales;
 };
-__device__ __noinline__ void tail_key(const ChunkArgs &a, const RowTile &x, int64_t j, int half, TailKey &k) {
+// Physical entry of entry e (32-bit divisions: this is on the tiles' critical
+// path), or -1 for a page id outside the pool.
+__device__ __forceinline__ int64_t entry_at(const csa2_cache &c, int seq, int e) {
+  if (c.block_table == nullptr) return static_cast<int64_t>(seq) * c.capacity + e;
+  const uint32_t pg = static_cast<uint32_t>(e) / static_cast<uint32_t>(c.page_entries);
+  const int32_t page = __ldg(c.block_table + static_cast<int64_t>(seq) * c.max_pages + pg);
+  if (page < 0 || page >= c.n_pages) return -1;
+  return static_cast<int64_t>(page) * c.page_entries + (e - static_cast<int>(pg) * c.page_entries);
+}
+__device__ __forceinline__ void tail_key(const ChunkArgs &a, const RowTile &x, int64_t j, TailKey &k) {
   const csa2_cache &c = a.c;
   k.kind = 0;
-  k.sigma = 0;
   if (j < x.T) {
-    k.at = phys_entry(entry_map(c), x.seq, j);
-    if (k.at >= 0) k.kind = 1;
-    else raise_err(a.err, CSA2_DEVERR_INDEX);
+    const int64_t e = entry_at(c, x.seq, static_cast<int>(j));
+    if (e < 0) {
+      raise_err(a.err, CSA2_DEVERR_INDEX);
+      return;
+    }
+    const bool fp8 = c.entry_format == CSA2_ENTRY_FP8;
+    k.kind = fp8 ? 2 : 1;
+    k.codes = c.lat_codes + e * (fp8 ? 512 : 256);
+    k.scales = c.lat_scales + e * (fp8 ? 16 : 32);
+    k.rope = c.rope_codes + e * (fp8 ? 128 : 32);
+    k.rope_scales = fp8 ? nullptr : c.rope_scales + e * 4;
   } else if (j < x.nkeys) {
     const int64_t tok = x.pos0 - (kWin - 1) + (j - x.T);
-    if (tok >= 0) {
-      if (a.win_codes != nullptr) {
-        k.kind = 2;
-        k.codes = a.win_codes;
-        k.scales = a.win_scales;
-        k.at = x.win0 + (j - x.T);
-      } else if (tok >= c.n_tokens[x.seq] - kWin) {
-        k.kind = 2;
-        k.codes = c.swa_codes;
-        k.scales = c.swa_scales;
-        k.at = static_cast<int64_t>(x.seq) * kWin + (tok & (kWin - 1));
-      } else {
-        raise_err(a.err, CSA2_DEVERR_INDEX);
-      }
+    if (tok < 0) return;
+    const uint8_t *codes = c.swa_codes, *scales = c.swa_scales;
+    int64_t at = static_cast<int64_t>(x.seq) * kWin + (tok & (kWin - 1));
+    if (a.win_codes != nullptr) {
+      codes = a.win_codes;
+      scales = a.win_scales;
+      at = x.win0 + (j - x.T);
+    } else if (tok < c.n_tokens[x.seq] - kWin) {
+      raise_err(a.err, CSA2_DEVERR_INDEX);
+      return;
     }
+    const bool fp8 = c.swa_dtype == CSA2_SWA_MXFP8;
+    k.kind = fp8 ? 3 : 4;
+    k.codes = codes + at * (fp8 ? 576 : 1152);
+    k.scales = fp8 ? scales + at * kSwaScaleStride : nullptr;
+    k.rope = k.codes + (fp8 ? 512 : 1024);
+    k.rope_scales = fp8 ? k.scales + 16 : nullptr;
   }
+}
+__device__ __forceinline__ int tail_sigma(const TailKey &k, int qd) {
   int e8 = 0;
   uint32_t bf = 0;
-  if (k.kind == 1 && c.entry_format == CSA2_ENTRY_FP8) {
-    e8 = e8m0_top(*reinterpret_cast<const uint4 *>(c.lat_scales + k.at * 16), 0);
-    const uint4 *rc = reinterpret_cast<const uint4 *>(c.rope_codes + k.at * 128);
-    for (int i = 4 * half; i < 4 * half + 4; ++i) bf = bf16_top(rc[i], bf);
-  } else if (k.kind == 2) {
-    if (c.swa_dtype == CSA2_SWA_MXFP8) {
-      const uint8_t *s = k.scales + k.at * kSwaScaleStride;
-      e8 = e8m0_top(*reinterpret_cast<const uint4 *>(s), max(static_cast<int>(s[16]), static_cast<int>(s[17])));
+  if (k.kind == 2) {
+    e8 = e8m0_top(ldg16(k.scales));
+    bf = bf16_top(ldg16(k.rope + 32 * qd), bf16_top(ldg16(k.rope + 32 * qd + 16), 0));
+  } else if (k.kind == 3) {
+    e8 = max(e8m0_top(ldg16(k.scales)), static_cast<int>(max(k.rope_scales[0], k.rope_scales[1])));
+  } else if (k.kind == 4) {
+#pragma unroll
+    for (int i = 0; i < 18; ++i) bf = bf16_top(ldg16(k.codes + 288 * qd + 16 * i), bf);
+  }
+  bf = key_max(bf);
+  return k.kind >= 2 ? sigma_of(key_exponent(e8, bf)) : 0;
+}
+struct RawTail {
+  uint4 w[4];
+  uint32_t sc;
+};
+__device__ __forceinline__ void tail_load(const TailKey &k, int s, int qd, RawTail &r) {
+  if (k.kind == 1) {
+    if (s < 4) {
+      r.w[0] = ldg16(k.codes + 64 * s + 16 * qd);
+      r.sc = ldg_u16(k.scales + 8 * s + 2 * qd);
     } else {
-      const uint4 *rc = reinterpret_cast<const uint4 *>(k.codes + k.at * 1152);
-      for (int i = 36 * half; i < 36 * half + 36; ++i) bf = bf16_top(rc[i], bf);
+      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(k.rope + 8 * qd));
+      r.w[0].x = v.x, r.w[0].y = v.y;
+      r.sc = __ldg(k.rope_scales + qd);
+    }
+  } else if (k.kind == 2 || k.kind == 3) {
+    const bool half = k.kind == 3 && s == 4;  // 16 E4M3 RoPE dims
+    const uint8_t *src = s < 4 ? k.codes + 128 * s + 32 * qd : k.rope + (half ? 16 : 32) * qd;
+    r.w[0] = ldg16(src);
+    if (!half) r.w[1] = ldg16(src + 16);
+    if (s < 4) r.sc = __ldg(k.scales + 4 * s + qd);
+    else if (half) r.sc = __ldg(k.rope_scales + (qd >> 1));
+  } else if (k.kind == 4) {
+    const uint8_t *src = s < 4 ? k.codes + 256 * s + 64 * qd : k.rope + 32 * qd;
+    r.w[0] = ldg16(src);
+    r.w[1] = ldg16(src + 16);
+    if (s < 4) {
+      r.w[2] = ldg16(src + 32);
+      r.w[3] = ldg16(src + 48);
     }
   }
-  bf = __vmaxu2(bf, __shfl_xor_sync(0xffffffffu, bf, 1));
-  if (k.kind == 2 || (k.kind == 1 && c.entry_format == CSA2_ENTRY_FP8)) k.sigma = sigma_of(key_exponent(e8, bf));
 }
-// units u0 .. u0 + n - 1 (8 dims each) of the key into block `blk`, chunks x0 ..
-__device__ __noinline__ void tail_fill(const ChunkArgs &a, const TailKey &k, uint8_t *blk, int key, int u0, int x0, int n) {
-  const float inv = pow2f(-k.sigma);
-  for (int i = 0; i < n; ++i) {
-    float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    if (k.kind == 1) entry_unit8(a.c, k.at, u0 + i, v);
-    else if (k.kind == 2) window_unit8(k.codes, k.scales, a.c.swa_dtype, k.at, u0 + i, v);
-    *reinterpret_cast<uint4 *>(chunk_at(blk, key, x0 + i)) =
-        make_uint4(pack_h2(v[0] * inv, v[1] * inv), pack_h2(v[2] * inv, v[3] * inv), pack_h2(v[4] * inv, v[5] * inv),
-                   pack_h2(v[6] * inv, v[7] * inv));
+__device__ __forceinline__ void tail_store(uint8_t (*k)[kBlk], const TailKey &t, int s, int key, int qd, const RawTail &r, int sigma) {
+  uint4 o[4];
+  const float inv = pow2f(-sigma);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = make_uint4(0, 0, 0, 0);
+  if (t.kind == 1) {
+    const uint32_t sa = e4m3x2_h2((r.sc & 0xFF) * 0x101), sb = s < 4 ? e4m3x2_h2((r.sc >> 8) * 0x101) : sa;
+    o[0] = dq_e2m1(r.w[0].x, sa);
+    o[1] = dq_e2m1(r.w[0].y, sa);
+    o[2] = dq_e2m1(r.w[0].z, sb);
+    o[3] = dq_e2m1(r.w[0].w, sb);
+  } else if (t.kind == 4 || (t.kind == 2 && s == 4)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = bf16x8_h(r.w[i], inv);
+  } else if (t.kind) {
+    const uint32_t m2 = pow2_h2(static_cast<int>(r.sc) - 127 - sigma);
+    const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = make_uint4(hmul2u(e4m3x2_h2(w[2 * i]), m2), hmul2u(e4m3x2_h2(w[2 * i] >> 16), m2),
+                        hmul2u(e4m3x2_h2(w[2 * i + 1]), m2), hmul2u(e4m3x2_h2(w[2 * i + 1] >> 16), m2));
+  }
+  if (s < 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(chunk_at(k[2 * s + (qd >> 1)], key, 4 * (qd & 1) + i)) = o[i];
+  } else {
+    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, 2 * qd)) = o[0];
+    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, 2 * qd + 1)) = o[1];
   }
 }
 
-// Physical entry of the first key of key tile kt, or -1 when the tile is not 128
+// Physical entry of the first key of key tile kt, or -1 when the tile is not 64
 // whole entries of one valid page.
-__device__ __forceinline__ int64_t whole_tile(const csa2_cache &c, const RowTile &x, int kt) {
-  if ((kt + 1) * static_cast<int64_t>(kKeys) > x.T) return -1;
-  return phys_entry(entry_map(c), x.seq, static_cast<int64_t>(kt) * kKeys);
+__device__ __forceinline__ int64_t whole_tile(const csa2_cache &c, int seq, int T, int kt) {
+  if ((kt + 1) * static_cast<int64_t>(kKeys) > T) return -1;
+  return entry_at(c, seq, kt * kKeys);
 }
 
+__device__ __noinline__ void fill_tail(const ChunkArgs &a, uint8_t (*k)[kBlk], float2 *sg, const RowTile &x, int64_t j0, int pt) {
+  const int key = pt >> 2, qd = pt & 3;
+  TailKey t;
+  tail_key(a, x, j0 + key, t);
+  RawTail r;
+  tail_load(t, 0, qd, r);
+  const int sigma = tail_sigma(t, qd);
+  if (qd == 0) sg[key] = t.kind ? make_float2(static_cast<float>(sigma), pow2f(sigma)) : make_float2(-INFINITY, 0.0f);
+#pragma unroll 1
+  for (int s = 0; s < 5; ++s) {
+    const RawTail now = r;
+    if (s < 4) tail_load(t, s + 1, qd, r);
+    tail_store(k, t, s, key, qd, now, sigma);
+  }
+}
+
+// The producer warps: tile n into buffer n % 2 once the PV that read it last is
+// complete.
 template <class Raw>
-__device__ __forceinline__ void produce(const ChunkArgs &a, const Plan &p, ChunkSmem &sm, int pt, int lane) {
-  constexpr int kSteps = 10, kAhead = 5;
+__device__ __forceinline__ void produce(const ChunkArgs &a, const Plan &p, ChunkSmem &sm, int pt) {
   const csa2_cache &c = a.c;
-  Raw raw[kAhead];
+  const int key = pt >> 2, qd = pt & 3;
   Items it(p, blockIdx.x);
-  bool more = it.next(), dead = false;
-  int kt = more ? it.k0 : 0;
-  int64_t base = more ? whole_tile(c, it.x, kt) : -1;
+  bool more = it.next(p, blockIdx.x), dead = false;
+  int kt = 0, seq = 0, T = 0;
+  int64_t base = -1;
+  Raw raw;
+  if (more) {
+    kt = it.k0, seq = it.x(p)->seq, T = it.x(p)->T;
+    base = whole_tile(c, seq, T, kt);
+  }
   if (base >= 0) {
 #pragma unroll
-    for (int s = 0; s < kAhead; ++s) load_raw(c, base, s, pt, raw[s]);
+    for (int s = 0; s < 5; ++s) load_step(c, base + key, qd, s, raw);
   }
-  for (uint32_t n = 0; more; ++n) {  // n: tiles so far
-    const RowTile x = it.x;
-    const int cur = kt;
-    const int64_t cbase = base;
-    // the next tile of this CTA
+  for (uint32_t n = 0; more; ++n) {
+    const int t = it.t, cur = kt, b = n & 1;
+    const bool whole = base >= 0;
     if (++kt >= it.k1) {
-      more = it.next();
-      kt = more ? it.k0 : 0;
+      more = it.next(p, blockIdx.x);
+      if (more) kt = it.k0, seq = it.x(p)->seq, T = it.x(p)->T;
     }
-    base = more ? whole_tile(c, it.x, kt) : -1;
-    const uint32_t par = (n & 1) ^ 1;
-    if (cbase >= 0) {
-      int sig0 = 0, sig1 = 0;
+    base = more ? whole_tile(c, seq, T, kt) : -1;
+    const uint32_t par = ((n >> 1) & 1) ^ 1;
+    if (n >= 2 && !dead) dead = !wait_warp(&sm.empty[b][0], par, a.err);
+    if (pt == 0) {
+      *const_cast<volatile uint32_t *>(&sm.progress) = n;
+      sm.plain[b] = whole && IsFp4<Raw>::v;
+    }
+    if (whole) {
+      const int sigma = raw_sigma(raw);
+      if (qd == 0) sm.sg[b][key] = make_float2(static_cast<float>(sigma), pow2f(sigma));
 #pragma unroll
-      for (int s = 0; s < kSteps; ++s) {
-        if ((s & 1) == 0) {
-          if (n > 0 && !dead) dead = !wait_warp(&sm.empty[s >> 1], par, a.err);
-          if (s == 0) {  // the key scalings of this tile (their last readers are two tiles back)
-            if (IsFp4<Raw>::v) {
-              if (pt < kKeys) sm.sg[n & 1][pt] = 0.0f;
-              if (pt == 0) sm.plain[n & 1] = 1;
-            } else {
-              const int key = pt >> 1, half = pt & 1;
-              const int64_t e = cbase + key;
-              uint32_t bf = 0;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) bf = bf16_top(ldg16(c.rope_codes + e * 128 + 64 * half + 16 * i), bf);
-              bf = __vmaxu2(bf, __shfl_xor_sync(0xffffffffu, bf, 1));
-              const int sg = sigma_of(key_exponent(e8m0_top(ldg16(c.lat_scales + e * 16), 0), bf));
-              if (half == 0) sm.sg[n & 1][key] = static_cast<float>(sg);
-              if (pt == 0) sm.plain[n & 1] = 0;
-              bar_producers();
-              sig0 = static_cast<int>(sm.sg[n & 1][pt >> 2]);
-              sig1 = static_cast<int>(sm.sg[n & 1][64 + (pt >> 2)]);
-            }
-          }
-        }
-        store_raw(sm, s, pt, raw[s % kAhead], (s & 1) ? sig1 : sig0);
-        if (s + kAhead < kSteps) load_raw(c, cbase, s + kAhead, pt, raw[s % kAhead]);
-        else if (base >= 0) load_raw(c, base, s + kAhead - kSteps, pt, raw[s % kAhead]);
-        if (s & 1) {
-          tc::fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&sm.full[s >> 1]);
-        }
+      for (int s = 0; s < 5; ++s) {
+        // dims 128 s .. are free as soon as their part of PV is complete, RoPE with the last
+        if (n >= 2 && s >= 1 && s < 4 && !dead) dead = !wait_warp(&sm.empty[b][s], par, a.err);
+        store_step(sm.k[b], s, key, qd, raw, sigma);
+        if (base >= 0) load_step(c, base + key, qd, s, raw);
       }
     } else {
-      const int key = pt >> 1, half = pt & 1;
-      TailKey k;
-      tail_key(a, x, static_cast<int64_t>(cur) * kKeys + key, half, k);
-      for (int i = 0; i < 5; ++i) {
-        if (n > 0 && !dead) dead = !wait_warp(&sm.empty[i], par, a.err);
-        if (i == 0) {
-          if (half == 0) sm.sg[n & 1][key] = k.kind ? static_cast<float>(k.sigma) : -INFINITY;
-          if (pt == 0) sm.plain[n & 1] = 0;
-        }
-        if (i < 4) tail_fill(a, k, sm.k[2 * i + half], key, 16 * i + 8 * half, 0, 8);
-        else tail_fill(a, k, sm.k[8], key, 64 + 4 * half, 4 * half, 4);
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&sm.full[i]);
-      }
+      if (n >= 2 && !dead) dead = !wait_warp(&sm.empty[b][3], par, a.err);
+      fill_tail(a, sm.k[b], sm.sg[b], p.tile[t], static_cast<int64_t>(cur) * kKeys, pt);
+      raw = Raw{};
       if (base >= 0) {
 #pragma unroll
-        for (int s = 0; s < kAhead; ++s) load_raw(c, base, s, pt, raw[s]);
+        for (int s = 0; s < 5; ++s) load_step(c, base + key, qd, s, raw);
       }
     }
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if ((pt & 31) == 0) tc::mbar_arrive(&sm.full[b]);
   }
 }
 
-// ------------------------------------------------------------------ softmax warps
-// Query rows of the item to fp16 with a power-of-two scale per row, and each
-// row's bounds.  Eight rows per warp.
-__device__ __forceinline__ void load_query(const ChunkArgs &a, const RowTile &x, ChunkSmem &sm, int warp, int lane) {
+// ------------------------------------------------------------------ query, softmax, read-out
+// Query rows of an item to fp16 with a power-of-two scale per row, each row's
+// logit factor and bounds.  Sixteen rows per warp.
+__device__ __noinline__ void load_query(const ChunkArgs &a, const RowTile &x, ChunkSmem &sm, int warp, int lane) {
   constexpr int kPer = kDqk / 2 / 32;  // 9 words per lane
 #pragma unroll 1
-  for (int j0 = 0; j0 < kRows / kSmWarps; j0 += 4) {
-    uint32_t raw[4][kPer];
+  for (int j0 = 0; j0 < kRows / kSmWarps; j0 += 2) {
+    uint32_t raw[2][kPer];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       const int r = warp * (kRows / kSmWarps) + j0 + j;
       const uint32_t *src = reinterpret_cast<const uint32_t *>(a.q + (x.row0 + r) * kDqk);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) raw[j][i] = r < x.nrows ? __ldg(src + lane + 32 * i) : 0u;
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       const int r = warp * (kRows / kSmWarps) + j0 + j;
       uint32_t m = 0;
 #pragma unroll
@@ -634,7 +723,7 @@ __device__ __forceinline__ void load_query(const ChunkArgs &a, const RowTile &x,
             pack_h2(__uint_as_float(raw[j][i] << 16) * inv, __uint_as_float(raw[j][i] & 0xFFFF0000u) * inv);
       }
       if (lane == 0) {
-        sm.qf[r] = pow2f(ex) * a.sm_scale * kLog2e;
+        sm.f[r] = pow2f(ex) * a.sm_scale * kLog2e;
         const int dtok = (x.head0 + min(r, x.nrows - 1)) / a.heads;
         sm.vis[r] = static_cast<int>(visible(x.pos0 + dtok, a.c.ratio, a.c.capacity));
         sm.w0[r] = x.T + dtok;
@@ -646,273 +735,305 @@ __device__ __forceinline__ void load_query(const ChunkArgs &a, const RowTile &x,
   if (lane == 0) tc::mbar_arrive(&sm.q_ready);
 }
 
-// v[0..31] over the 32 lanes: lane i gets the reduction of v[i]
-template <class Op>
-__device__ __forceinline__ float warp_columns(float *v, int lane, Op op) {
+// O^T of a finished item out of tensor memory: normalised rows, or (part) this
+// CTA's part of a shared row tile.  Each warp has 32 dims of every block.
+__device__ __noinline__ void read_out(const ChunkArgs &a, const ChunkSmem &sm, float *part, int64_t row0, int nrows,
+                                      uint32_t tmem, int warp, int lane) {
+  const int dim = 32 * warp + lane;
+  const uint32_t ta = tmem + (static_cast<uint32_t>(32 * warp) << 16) + kColO;
+#pragma unroll 1
+  for (int i16 = 0; i16 < 16; ++i16) {
+    const int b = i16 >> 2, h0 = 16 * (i16 & 3);
+    uint32_t r[16];
+    tc::tmem_ld_32x32b_x16(ta + 16 * i16, r);
+    tc::tmem_ld_wait_x16(r);
+    if (part != nullptr) {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    const bool up = lane & o;
+      for (int i = 0; i < 16; i += 4)
+        *reinterpret_cast<uint4 *>(part + ((b * 16 + (h0 + i) / 4) * 128 + dim) * 4) =
+            make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
+    } else if (a.bf16) {
+      // lane pairs exchange so that each stores two neighbouring dims of one row
 #pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float keep = up ? v[i + o] : v[i], send = up ? v[i] : v[i + o];
-      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+      for (int i = 0; i < 16; i += 2) {
+        const float v0 = __uint_as_float(r[i]) * sm.fin[h0 + i], v1 = __uint_as_float(r[i + 1]) * sm.fin[h0 + i + 1];
+        const float o = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
+        const int row = h0 + i + (lane & 1);
+        const __nv_bfloat162 t2 = lane & 1 ? __floats2bfloat162_rn(o, v1) : __floats2bfloat162_rn(v0, o);
+        if (row < nrows)
+          *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + (row0 + row) * kLat + 128 * b +
+                                              (dim & ~1)) = t2;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (h0 + i < nrows)
+          static_cast<float *>(a.out)[(row0 + h0 + i) * kLat + 128 * b + dim] = __uint_as_float(r[i]) * sm.fin[h0 + i];
     }
   }
-  return v[0];
 }
 
-__device__ __forceinline__ void softmax(const ChunkArgs &a, const Plan &p, ChunkSmem &sm, uint32_t tmem, int tid) {
-  const int warp = tid >> 5, lane = tid & 31, quarter = warp & 3, half = warp >> 2;
-  const int key = 32 * quarter + lane;
-  const uint32_t lane_base = static_cast<uint32_t>(32 * quarter) << 16;
-  const int c0 = 32 * half;  // this thread's rows c0 .. c0 + 31
-  bool dead = false;
-  uint32_t n = 0;            // tiles so far
+// The softmax warps: warp w has rows 16 w .. + 15 of S (TMEM lanes 32 w ..), a
+// thread 16 keys of rows ra and rb, so row maxima and sums are two shuffles.  A
+// row's reference maximum moves only when a weight would exceed 2^15 (fp16);
+// then its O^T column is rescaled.
+__device__ __forceinline__ void softmax(const ChunkArgs &a, const Plan &p, ChunkSmem &sm, uint32_t tmem, int warp, int lane) {
+  const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
+  const int ra = 16 * warp + (lane >> 2), rb = ra + 8, col = 2 * (lane & 3);
   Items it(p, blockIdx.x);
-  bool more = it.next();
-  if (more) load_query(a, it.x, sm, warp, lane);
+  bool more = it.next(p, blockIdx.x), dead = false;
+  uint32_t n = 0;  // tiles so far
+  if (more) load_query(a, *it.x(p), sm, warp, lane);
   while (more) {
-    const RowTile x = it.x;
+    const RowTile *x = it.x(p);
     const int k0 = it.k0, k1 = it.k1;
-    float l[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) l[i] = 0.0f;
-    bar_softmax();  // qf, vis, w0 of every row written; the last item's fm, fin read
-    if (tid < kRows) {
-      sm.fm[tid] = make_float2(sm.qf[tid], -kUnset);
-      sm.rowmax[tid] = order_int(-INFINITY);
-    }
-    const int vis_all = sm.vis[0];  // the first row sees least
-    bar_softmax();
+    // this warp's rows only, written by itself
+    const float fa = sm.f[ra], fb = sm.f[rb];
+    const int va = sm.vis[ra], vb = sm.vis[rb], wa = sm.w0[ra], wb = sm.w0[rb];
+    float ma = 0.0f, mb = 0.0f, la = 0.0f, lb = 0.0f;  // reference (log2 units), sum
+    bool seen_a = false, seen_b = false;               // the reference is set
     for (int kt = k0; kt < k1; ++kt, ++n) {
-      if (!dead) dead = !wait_warp(&sm.full[4], n & 1, a.err);  // sg, plain of this tile
-      if (!dead) dead = !wait_warp(&sm.s_full, n & 1, a.err);
+      const int b = n & 1;
+      if (!dead) dead = !wait_warp(&sm.full[b], (n >> 1) & 1, a.err);  // sg, plain of this tile
+      if (!dead) dead = !wait_warp(&sm.s_full[b], (n >> 1) & 1, a.err);
       tc::tc_fence_after();
-      const float sg = sm.sg[n & 1][key];
-      const bool fast = sm.plain[n & 1] && (kt + 1) * kKeys <= vis_all;
-      const float g = sg == -INFINITY ? 0.0f : ex2(sg);
-      const int j = kt * kKeys + key;
       float s[32];
-      // exponents of the weighted weights: x = z + sigma - m (log2 units)
-      auto exponents = [&]() -> float {
-        uint32_t *u = reinterpret_cast<uint32_t *>(s);
-        tc::tmem_ld_32x32b_x16(tmem + lane_base + kColS + c0, u);
-        tc::tmem_ld_32x32b_x16(tmem + lane_base + kColS + c0 + 16, u + 16);
-        tc::tmem_ld_wait_x16(u);
-        tc::tmem_ld_wait_x16(u + 16);
-        float top = -INFINITY;
-        if (fast) {
+      tmem_ld_rows16(tmem + lane_base + kColS + 64 * b, reinterpret_cast<uint32_t *>(s));
+      // exponents of the weighted weights, x = z + sigma - m, and their row maxima
+      float ta = -INFINITY, tb = -INFINITY;
+      const bool fast = sm.plain[b] && (kt + 1) * kKeys <= va;  // (rb sees no less)
+      if (fast) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float4 f = *reinterpret_cast<const float4 *>(&sm.fm[c0 + i]);
-            s[i] = fmaf(s[i], f.x, f.y);
-            s[i + 1] = fmaf(s[i + 1], f.z, f.w);
-            top = fmaxf(top, fmaxf(s[i], s[i + 1]));
+        for (int j = 0; j < 32; j += 4) {
+          s[j] = fmaf(s[j], fa, -ma);
+          s[j + 1] = fmaf(s[j + 1], fa, -ma);
+          s[j + 2] = fmaf(s[j + 2], fb, -mb);
+          s[j + 3] = fmaf(s[j + 3], fb, -mb);
+          ta = fmaxf(ta, fmaxf(s[j], s[j + 1]));
+          tb = fmaxf(tb, fmaxf(s[j + 2], s[j + 3]));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4) {
+          const int k = 2 * j + col, key = kt * kKeys + k;
+          const float4 g = *reinterpret_cast<const float4 *>(&sm.sg[b][k]);  // (sigma, 2^sigma) of two keys
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int kk = key + i;
+            const float sg = i ? g.z : g.x, g2 = i ? g.w : g.y;
+            const bool see_a = kk < va || (kk >= wa && kk < wa + kWin), see_b = kk < vb || (kk >= wb && kk < wb + kWin);
+            s[j + i] = see_a ? fmaf(s[j + i] * g2, fa, sg - ma) : -INFINITY;
+            s[j + 2 + i] = see_b ? fmaf(s[j + 2 + i] * g2, fb, sg - mb) : -INFINITY;
+            ta = fmaxf(ta, s[j + i]);
+            tb = fmaxf(tb, s[j + 2 + i]);
           }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const float2 f = sm.fm[c0 + i];
-            const int w0 = sm.w0[c0 + i];
-            const bool see = j < sm.vis[c0 + i] || (j >= w0 && j < w0 + kWin);
-            s[i] = see ? fmaf(s[i] * g, f.x, sg + f.y) : -INFINITY;
-            top = fmaxf(top, s[i]);
-          }
         }
-        return top;
-      };
-      const float top = exponents();
-      if (bar_softmax_or(top > kSlack)) {
-        // some row has no reference yet, or outgrew it: the tile's row maxima
-        // (relative to the old reference), new references, O^T and l rescaled
-        float v[32];
-        // logits without the reference
-        {
-          uint32_t *u = reinterpret_cast<uint32_t *>(v);
-          tc::tmem_ld_32x32b_x16(tmem + lane_base + kColS + c0, u);
-          tc::tmem_ld_32x32b_x16(tmem + lane_base + kColS + c0 + 16, u + 16);
-          tc::tmem_ld_wait_x16(u);
-          tc::tmem_ld_wait_x16(u + 16);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = s[i] == -INFINITY ? -INFINITY : fmaf(v[i] * g, sm.fm[c0 + i].x, sg);
-        }
-        const float mx = warp_columns(v, lane, [](float x0, float y0) { return fmaxf(x0, y0); });
-        atomicMax(&sm.rowmax[c0 + lane], order_int(mx));
-        bar_softmax();
-        if (tid < kRows) {
-          const float m_old = -sm.fm[tid].y, t = order_float(sm.rowmax[tid]);
-          float al = 1.0f;
-          if (t > m_old + kSlack) {  // kUnset: any logit
-            const float m_new = t - kTop;
-            al = m_old == kUnset ? 0.0f : ex2(m_old - m_new);
-            sm.fm[tid].y = -m_new;
-          }
-          sm.alpha[tid] = al;
-          sm.rowmax[tid] = order_int(-INFINITY);
-        }
-        bar_softmax();
-        if (kt > k0) {  // O^T holds something: PV of the last tile has to be complete
-          if (!dead) dead = !wait_warp(&sm.empty[4], (n & 1) ^ 1, a.err);
-          tc::tc_fence_after();
-#pragma unroll 1
-          for (int b = 2 * half; b < 2 * half + 2; ++b)
-#pragma unroll 1
-            for (int h0 = 0; h0 < kRows; h0 += 16) {
-              uint32_t r[16];
-              const uint32_t ta = tmem + lane_base + kColO + 64 * b + h0;
-              tc::tmem_ld_32x32b_x16(ta, r);
-              tc::tmem_ld_wait_x16(r);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * sm.alpha[h0 + i]);
-              tmem_st_x16(ta, r);
-            }
-          asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
-        }
-#pragma unroll
-        for (int i = 0; i < 32; ++i) l[i] *= sm.alpha[c0 + i];
-        exponents();
       }
-      // weights: l in fp32 (without sigma), P^T to fp16 (with it; at most 2^15)
-      const float inv_g = fast ? 1.0f : ex2(-max(sg, -126.0f));
-      uint8_t *pb = sm.k[8];
+      ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, 1));
+      tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, 1));
+      ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, 2));
+      tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, 2));
+      const bool mva = seen_a ? ta > kSlack : ta > -INFINITY, mvb = seen_b ? tb > kSlack : tb > -INFINITY;
+      if (__any_sync(0xffffffffu, mva || mvb)) {
+        const float da = mva ? ta - kTop : 0.0f, db = mvb ? tb - kTop : 0.0f;
+        const float ala = mva ? (seen_a ? ex2(-da) : 0.0f) : 1.0f, alb = mvb ? (seen_b ? ex2(-db) : 0.0f) : 1.0f;
+        ma += da;
+        mb += db;
+        la *= ala;
+        lb *= alb;
 #pragma unroll
-      for (int i = 0; i < 32; i += 8) {
-        uint32_t w[4];
-#pragma unroll
-        for (int h = 0; h < 8; h += 2) {
-          const float p0 = ex2(s[i + h]), p1 = ex2(s[i + h + 1]);
-          l[i + h] = fast ? l[i + h] + p0 : fmaf(p0, inv_g, l[i + h]);
-          l[i + h + 1] = fast ? l[i + h + 1] + p1 : fmaf(p1, inv_g, l[i + h + 1]);
-          w[h / 2] = pack_h2(p0, p1);
+        for (int j = 0; j < 32; j += 4) {
+          s[j] -= da;
+          s[j + 1] -= da;
+          s[j + 2] -= db;
+          s[j + 3] -= db;
         }
-        *reinterpret_cast<uint4 *>(chunk_at(pb, key, (c0 + i) >> 3)) = make_uint4(w[0], w[1], w[2], w[3]);
+        seen_a |= mva;
+        seen_b |= mvb;
+        if ((lane & 3) == 0) {
+          sm.alpha[ra] = ala;
+          sm.alpha[rb] = alb;
+        }
+      } else if ((lane & 3) == 0) {
+        sm.alpha[ra] = 1.0f;
+        sm.alpha[rb] = 1.0f;
+      }
+      if (bar_softmax_or(kt > k0 && (mva || mvb))) {
+        // some row's reference moved: its O^T column follows, once the last PV is complete
+        if (!dead) dead = !wait_warp(&sm.empty[b ^ 1][3], ((n - 1) >> 1) & 1, a.err);
+        tc::tc_fence_after();
+#pragma unroll 1
+        for (int h0 = 0; h0 < kRows; h0 += 8) {
+          const float4 a0 = *reinterpret_cast<const float4 *>(&sm.alpha[h0]), a1 = *reinterpret_cast<const float4 *>(&sm.alpha[h0 + 4]);
+          const float al[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+          bool any = false;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) any |= al[i] != 1.0f;
+          if (!any) continue;
+          uint32_t r[32];  // the four blocks' columns in flight together
+          const uint32_t at = tmem + lane_base + kColO + h0;
+#pragma unroll
+          for (int blk = 0; blk < 4; ++blk) tmem_ld_x8(at + 64 * blk, r + 8 * blk);
+          tmem_ld_wait_x8x4(r);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * al[i & 7]);
+#pragma unroll
+          for (int blk = 0; blk < 4; ++blk) tmem_st_x8(at + 64 * blk, r + 8 * blk);
+        }
+        asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+      }
+      // weights: l in fp32 (without sigma), P to fp16 (with it; at most 2^15)
+      uint8_t *pa = sm.k[b][8] + ra * 128 + 2 * col, *pb = pa + 8 * 128;  // ra % 8 == rb % 8
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float p0 = ex2(s[4 * j]), p1 = ex2(s[4 * j + 1]), p2 = ex2(s[4 * j + 2]), p3 = ex2(s[4 * j + 3]);
+        if (fast) {
+          la += p0 + p1;
+          lb += p2 + p3;
+        } else {
+          const float4 g = *reinterpret_cast<const float4 *>(&sm.sg[b][8 * j + col]);
+          const float g0 = ex2(-fmaxf(g.x, -126.0f)), g1 = ex2(-fmaxf(g.z, -126.0f));
+          la = fmaf(p0, g0, fmaf(p1, g1, la));
+          lb = fmaf(p2, g0, fmaf(p3, g1, lb));
+        }
+        const int at = (j ^ (ra & 7)) << 4;
+        *reinterpret_cast<uint32_t *>(pa + at) = pack_h2(p0, p1);
+        *reinterpret_cast<uint32_t *>(pb + at) = pack_h2(p2, p3);
       }
       tc::fence_proxy_async_smem();
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sm.p_full);
     }
-    // ---- the item's last tile is on its way: sums, the next item's query, then O^T
-    const float ls = warp_columns(l, lane, [](float x0, float y0) { return x0 + y0; });
-    sm.lsum[quarter][c0 + lane] = ls;
-    more = it.next();
-    bar_softmax();
-    float m = -INFINITY, sum = 0.0f;  // row tid (tid < 64)
-    if (tid < kRows) {
-      m = -sm.fm[tid].y;
-      sum = sm.lsum[0][tid] + sm.lsum[1][tid] + sm.lsum[2][tid] + sm.lsum[3][tid];
-      if (m == kUnset) m = -INFINITY;
-    }
-    const bool direct = k0 == 0 && k1 == x.ntiles;
-    if (tid < kRows && direct) {
-      float f = 1.0f;
-      if (a.sink != nullptr) {
-        const float z = a.sink[(x.head0 + tid) % a.heads] * kLog2e;
-        const float mf = fmaxf(m, z);
-        f = m == -INFINITY ? 0.0f : ex2(m - mf);
-        sum = sum * f + ex2(z - mf);
-        m = mf;
-      }
-      sm.fin[tid] = sum > 0.0f ? f / sum : 0.0f;
-      if (tid < x.nrows) a.lse[x.row0 + tid] = sum > 0.0f ? (m + log2f(sum)) * kLn2 : -INFINITY;
-    }
-    if (more) load_query(a, it.x, sm, warp, lane);
-    bar_softmax();  // fin written
-    if (!dead) dead = !wait_warp(&sm.empty[4], (n - 1) & 1, a.err);  // PV of the last tile
-    tc::tc_fence_after();
-    const int slot = 2 * blockIdx.x + (k0 > 0 ? 0 : 1);
-    float *part = p.part + slot * kPartFloats;
-    if (!direct && tid < kRows)
-      *reinterpret_cast<float2 *>(part + 4 * 64 * kKeys + 2 * tid) = make_float2(m, sum);
-#pragma unroll 1
-    for (int b = 2 * half; b < 2 * half + 2; ++b) {
-#pragma unroll 1
-      for (int h0 = 0; h0 < kRows; h0 += 32) {
-        uint32_t r[32];
-        tc::tmem_ld_32x32b_x16(tmem + lane_base + kColO + 64 * b + h0, r);
-        tc::tmem_ld_32x32b_x16(tmem + lane_base + kColO + 64 * b + h0 + 16, r + 16);
-        tc::tmem_ld_wait_x16(r);
-        tc::tmem_ld_wait_x16(r + 16);
-        if (dead) continue;
-        if (!direct) {
-#pragma unroll
-          for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<uint4 *>(part + ((b * 16 + (h0 + i) / 4) * kKeys + key) * 4) = make_uint4(r[i], r[i + 1], r[i + 2], r[i + 3]);
-        } else if (a.bf16) {
-          // lane pairs exchange so that each stores two neighbouring dims of one row
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const float v0 = __uint_as_float(r[i]) * sm.fin[h0 + i], v1 = __uint_as_float(r[i + 1]) * sm.fin[h0 + i + 1];
-            const float o = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
-            const int row = h0 + i + (lane & 1);
-            const __nv_bfloat162 t2 = lane & 1 ? __floats2bfloat162_rn(o, v1) : __floats2bfloat162_rn(v0, o);
-            if (row < x.nrows)
-              *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(a.out) + (x.row0 + row) * kLat + 128 * b + (key & ~1)) = t2;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (h0 + i < x.nrows)
-              static_cast<float *>(a.out)[(x.row0 + h0 + i) * kLat + 128 * b + key] = __uint_as_float(r[i]) * sm.fin[h0 + i];
+    // ---- the item's last PV is on its way: sums, output factors, the next query
+    la += __shfl_xor_sync(0xffffffffu, la, 1);
+    lb += __shfl_xor_sync(0xffffffffu, lb, 1);
+    la += __shfl_xor_sync(0xffffffffu, la, 2);
+    lb += __shfl_xor_sync(0xffffffffu, lb, 2);
+    const bool direct = k0 == 0 && k1 == x->ntiles;
+    float *part = direct ? nullptr : p.part + (2 * blockIdx.x + (k0 > 0 ? 0 : 1)) * kPartFloats;
+    if ((lane & 3) < 2) {  // lane 0 of a row's four: ra, lane 1: rb
+      const bool second = lane & 1;
+      const int r = second ? rb : ra;
+      float m = second ? (seen_b ? mb : -INFINITY) : (seen_a ? ma : -INFINITY), sum = second ? lb : la;
+      if (!direct) {
+        *reinterpret_cast<float2 *>(part + kLat * kRows + 2 * r) = make_float2(m, sum);
+      } else {
+        float f = 1.0f;
+        if (a.sink != nullptr) {
+          const float z = a.sink[(x->head0 + r) % a.heads] * kLog2e;
+          const float mf = fmaxf(m, z);
+          f = m == -INFINITY ? 0.0f : ex2(m - mf);
+          sum = sum * f + ex2(z - mf);
+          m = mf;
         }
+        sm.fin[r] = sum > 0.0f ? f / sum : 0.0f;
+        if (r < x->nrows && !dead) a.lse[x->row0 + r] = sum > 0.0f ? (m + log2f(sum)) * kLn2 : -INFINITY;
       }
     }
+    more = it.next(p, blockIdx.x);
+    if (more) load_query(a, *it.x(p), sm, warp, lane);  // (S of the last tile is complete)
+    bar_softmax();                                      // fin
+    if (!dead) dead = !wait_warp(&sm.empty[(n - 1) & 1][3], ((n - 1) >> 1) & 1, a.err);
+    tc::tc_fence_after();
+    if (!dead) read_out(a, sm, part, x->row0, x->nrows, tmem, warp, lane);
     tc::tc_fence_before();
+    bar_softmax();  // fin read
   }
 }
 
 // ------------------------------------------------------------------ MMA issuer
-// Per key tile: S^T[128 keys][64 rows] = K Q^T as the tile's dims arrive, then,
-// with P^T, O^T[512 dims][64 rows] += V^T P^T in four blocks of 128 dims, each
-// handed back to the producers as it completes.
+// Per key tile: S = Q K^T once the tile is filled, PV once its P is there.  The
+// S of the next tile is issued before the PV of this one whenever that tile is
+// ready first, so that the tensor cores work while the softmax does.
 __device__ __forceinline__ void issue(const ChunkArgs &a, const Plan &p, ChunkSmem &sm, uint32_t tmem) {
-  constexpr uint32_t idS = idesc_f16(kKeys, kRows, 0), idO = idesc_f16(128, kRows, 1);
-  const uint32_t ka = tc::smem_addr(sm.k), qa = tc::smem_addr(sm.q), pa = ka + 8 * kBlk;
+  const uint32_t e = elect_one();
+  const uint32_t ka = tc::smem_addr(sm.k);
+  const uint64_t dq = desc_sw128(tc::smem_addr(sm.q), 16, 1024), dk = desc_sw128(ka, 16, 1024);
+  const uint64_t dv = desc_sw128(ka, kBlk, 1024), dp = desc_sw128(ka + 8 * kBlk, 16, 1024);
   Items it(p, blockIdx.x);
-  bool dead = false;
   uint32_t n = 0, items = 0;
-  auto wait = [&](uint64_t *bar, uint32_t par) {
-    if (!dead && !tc::mbar_wait_bounded(bar, par, kWaitIters)) {
-      dead = true;
-      raise_err(a.err, CSA2_DEVERR_TIMEOUT);
-    }
+  auto qk = [&](uint32_t t) {
+    tc::tc_fence_after();
+    mma_qk(e, tmem + kColS + 64 * (t & 1), dq, dk + (t & 1) * (kTile >> 4));
+    if (e) tc::mma_commit(&sm.s_full[t & 1]);
   };
-  while (it.next()) {
-    wait(&sm.q_ready, items & 1);
+  while (it.next(p, blockIdx.x)) {
+    const int tiles = it.k1 - it.k0;
+    if (!wait_warp(&sm.q_ready, items & 1, a.err)) return;
     ++items;
-    for (int kt = it.k0; kt < it.k1; ++kt, ++n) {
-#pragma unroll 1
-      for (int i = 0; i < 5; ++i) {
-        wait(&sm.full[i], n & 1);
-        if (dead) break;
-        tc::tc_fence_after();
-        for (int b = 2 * i; b < min(2 * i + 2, kBlocks); ++b)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16(tmem + kColS, desc_sw128(ka + b * kBlk + 32 * kk, 16, 1024), desc_sw128(qa + b * kQBlk + 32 * kk, 16, 1024),
-                    idS, (b | kk) ? 1u : 0u);
+    bool ahead = false;  // S of tile n is issued
+    for (int i = 0; i < tiles; ++i, ++n) {
+      if (!ahead) {
+        if (!wait_warp(&sm.full[n & 1], (n >> 1) & 1, a.err)) return;
+        qk(n);
       }
-      if (!dead) tc::mma_commit(&sm.s_full);
-      wait(&sm.p_full, n & 1);
-      if (dead) break;
+      ahead = false;
+      // whichever comes first: the next tile, or this one's P (bounded polls)
+      bool ready = false;
+      for (uint32_t poll = 0; !ready && poll < kWaitIters * 1000; ++poll) {
+        if (!ahead && i + 1 < tiles && tc::mbar_try_wait(&sm.full[(n + 1) & 1], ((n + 1) >> 1) & 1, 0)) {
+          ahead = true;
+          qk(n + 1);
+        }
+        ready = tc::mbar_try_wait(&sm.p_full, n & 1, ahead || i + 1 == tiles ? 1000u : 0u);
+      }
+      if (!ready) {
+        raise_err(a.err, CSA2_DEVERR_TIMEOUT);
+        return;
+      }
       tc::tc_fence_after();
+      const uint32_t buf = (n & 1) * (kTile >> 4);
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_f16(tmem + kColO + 64 * i, desc_sw128(ka + 2 * i * kBlk + 2048 * ks, kBlk, 1024),
-                  desc_sw128(pa + 2048 * ks, kBlk, 1024), idO, (kt > it.k0 || ks) ? 1u : 0u);
-        tc::mma_commit(&sm.empty[i]);
+      for (int blk = 0; blk < 4; ++blk) {
+        mma_pv(e, tmem + kColO + 64 * blk, dv + buf + ((2 * kBlk * blk) >> 4), dp + buf, i > 0 ? 1u : 0u);
+        if (e) tc::mma_commit(&sm.empty[n & 1][blk]);
       }
-      tc::mma_commit(&sm.empty[4]);
     }
-    if (dead) break;
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 1) k_chunk_attn(ChunkArgs a, Plan p) {
-  extern __shared__ uint8_t smem_raw[];
-  ChunkSmem &sm = *reinterpret_cast<ChunkSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+// One thread that asks for the records of the CTA's coming key tiles: whole
+// tiles are contiguous in every plane, so a few bulk prefetches into L2 each.
+__device__ __forceinline__ void prefetch_l2(const uint8_t *p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(p), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void ahead(const ChunkArgs &a, const Plan &p, ChunkSmem &sm) {
+  const csa2_cache &c = a.c;
+  const volatile uint32_t *progress = &sm.progress;
+  Items it(p, blockIdx.x);
+  uint32_t n = 0;
+  while (it.next(p, blockIdx.x)) {
+    const int seq = it.x(p)->seq, T = it.x(p)->T;
+    for (int kt = it.k0; kt < it.k1; ++kt, ++n) {
+      // (bounded: were the workers to stop, it would only ask too early)
+      for (int i = 0; i < 100000 && *progress + kAhead < n; ++i) __nanosleep(100);
+      const int64_t base = whole_tile(c, seq, T, kt);
+      if (base < 0) continue;
+      if (c.entry_format == CSA2_ENTRY_FP8) {
+        prefetch_l2(c.lat_codes + base * 512, kKeys * 512);
+        prefetch_l2(c.lat_scales + base * 16, kKeys * 16);
+        prefetch_l2(c.rope_codes + base * 128, kKeys * 128);
+      } else {
+        prefetch_l2(c.lat_codes + base * 256, kKeys * 256);
+        prefetch_l2(c.lat_scales + base * 32, kKeys * 32);
+        prefetch_l2(c.rope_codes + base * 32, kKeys * 32);
+        // (4 B per entry: in a dense cache the tile may start between two 16 B
+        // boundaries, and a bulk prefetch may not)
+        const uintptr_t rs = reinterpret_cast<uintptr_t>(c.rope_scales + base * 4);
+        const uintptr_t r0 = (rs + 15) & ~uintptr_t(15), r1 = (rs + kKeys * 4) & ~uintptr_t(15);
+        prefetch_l2(reinterpret_cast<const uint8_t *>(r0), static_cast<uint32_t>(r1 - r0));
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 1) k_chunk_attn(const __grid_constant__ ChunkArgs a,
+                                                             const __grid_constant__ Plan p) {
+  // aligned by its declaration, not by arithmetic on the pointer, after which every
+  // access would be a generic one with a 64-bit address
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  ChunkSmem &sm = *reinterpret_cast<ChunkSmem *>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const CtaRange r = p.cta[blockIdx.x];
   if (r.hi <= r.lo) return;  // the whole CTA
@@ -921,26 +1042,29 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunk_attn(ChunkArgs a, Plan p)
     tc::tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.full[i], kPrWarps);
-      tc::mbar_init(&sm.empty[i], 1);
+      for (int j = 0; j < 4; ++j) tc::mbar_init(&sm.empty[i][j], 1);
+      tc::mbar_init(&sm.s_full[i], 1);
     }
-    tc::mbar_init(&sm.s_full, 1);
     tc::mbar_init(&sm.p_full, kSmWarps);
     tc::mbar_init(&sm.q_ready, kSmWarps);
     tc::fence_mbar_init();
+    sm.progress = 0;
   }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = sm.tmem;
   if (warp < kSmWarps) {
-    softmax(a, p, sm, tmem, tid);
+    softmax(a, p, sm, tmem, warp, lane);
   } else if (warp < kMmaWarp) {
-    if (a.c.entry_format == CSA2_ENTRY_FP8) produce<RawFp8>(a, p, sm, tid - 32 * kSmWarps, lane);
-    else produce<RawFp4>(a, p, sm, tid - 32 * kSmWarps, lane);
-  } else if (lane == 0) {
+    if (a.c.entry_format == CSA2_ENTRY_FP8) produce<RawFp8>(a, p, sm, tid - 32 * kSmWarps);
+    else produce<RawFp4>(a, p, sm, tid - 32 * kSmWarps);
+  } else if (warp == kMmaWarp) {
     issue(a, p, sm, tmem);
+  } else if (lane == 0) {
+    ahead(a, p, sm);
   }
   tc::tc_fence_before();
   __syncthreads();
@@ -952,25 +1076,26 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunk_attn(ChunkArgs a, Plan p)
 
 // Row tiles shared by several CTAs: block (g, y) joins the one that ends in CTA
 // g, rows 4 (y % 16) .. of dims 128 (y / 16) .., its parts in CTA order.
-__global__ void __launch_bounds__(kKeys) k_chunk_merge(ChunkArgs a, Plan p) {
+__global__ void __launch_bounds__(128) k_chunk_merge(ChunkArgs a, Plan p) {
   const int g = blockIdx.x, blk = blockIdx.y / 16, i4 = blockIdx.y % 16, d = threadIdx.x;
   Items it(p, g);
-  if (!it.next() || it.k0 == 0 || it.k1 != it.x.ntiles) return;
-  const RowTile &x = it.x;
+  if (!it.next(p, g) || it.k0 == 0 || it.k1 != it.x(p)->ntiles) return;
+  const RowTile &x = *it.x(p);
+  const int64_t c0 = p.cum[it.t];
   if (4 * i4 >= x.nrows) return;
   int g0 = g;  // the CTA that holds the row tile's first key tile
-  while (g0 > 0 && p.cta[g0].lo > it.c0) --g0;
+  while (g0 > 0 && p.cta[g0].lo > c0) --g0;
   float m[4], l[4], o[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = 0.0f, o[r] = 0.0f;
   for (int k = g0; k <= g; ++k) {  // the reference of the whole row
-    const float *ml = p.part + (2 * k + (k == g0 ? 1 : 0)) * kPartFloats + 4 * 64 * kKeys + 8 * i4;
+    const float *ml = p.part + (2 * k + (k == g0 ? 1 : 0)) * kPartFloats + kLat * kRows + 8 * i4;
 #pragma unroll
     for (int r = 0; r < 4; ++r) m[r] = fmaxf(m[r], ml[2 * r]);
   }
   for (int k = g0; k <= g; ++k) {
-    const float *part = p.part + (2 * k + (k == g0 ? 1 : 0)) * kPartFloats, *ml = part + 4 * 64 * kKeys + 8 * i4;
-    const float4 v = *reinterpret_cast<const float4 *>(part + ((blk * 16 + i4) * kKeys + d) * 4);
+    const float *part = p.part + (2 * k + (k == g0 ? 1 : 0)) * kPartFloats, *ml = part + kLat * kRows + 8 * i4;
+    const float4 v = *reinterpret_cast<const float4 *>(part + ((blk * 16 + i4) * 128 + d) * 4);
     const float vv[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -1074,7 +1199,7 @@ csa2_status csa2_chunk_attn(const csa2_cache *cache, const uint16_t *q, int32_t 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   csa2::k_chunk_plan<<<1, 1024, 0, s>>>(a, p);
   csa2::k_chunk_attn<<<L.n_cta, csa2::kThreads, smem, s>>>(a, p);
-  csa2::k_chunk_merge<<<dim3(L.n_cta, 64), csa2::kKeys, 0, s>>>(a, p);
+  csa2::k_chunk_merge<<<dim3(L.n_cta, 64), 128, 0, s>>>(a, p);
   return cuda_status(cudaGetLastError(), "csa2_chunk_attn launch");
 }
 
