@@ -32,12 +32,12 @@ constexpr int kKeys = 64;                    // keys of a key tile
 constexpr int kBlk = kKeys * 128;            // a 64-dim block of a key tile, or of the query: 8 KB
 constexpr int kBlocks = kDqk / 64;           // 9: 8 latent, 1 RoPE
 constexpr int kTile = kBlocks * kBlk;        // 73,728 B
-constexpr int kSmWarps = 4, kPrWarps = 8;    // softmax / producer warps
+constexpr int kSmWarps = 8, kPrWarps = 8;    // softmax / producer warps
 constexpr int kMmaWarp = kSmWarps + kPrWarps, kAheadWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kAheadWarp + 1);
 constexpr int kAhead = 4;                    // key tiles requested into L2 ahead of use
 constexpr uint32_t kColS = 0, kColO = 256;   // TMEM columns: S 2 x 64, O^T 4 x 64
-constexpr uint32_t kWaitIters = 200;
+constexpr uint32_t kWaitIters = 200, kPolls = 1u << 20;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kTop = 4.0f, kSlack = 15.0f;  // a new reference puts the maximum at 2^4; 2^15 still fits fp16
 constexpr int64_t kPartFloats = kLat * kRows + 2 * kRows;  // O^T [4][16][128][4], then (m, l) per row
@@ -251,17 +251,15 @@ __device__ __forceinline__ void tmem_ld_wait_x8x4(uint32_t *r) {
                : "memory");
   asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) : : "memory");
 }
-// 16 lanes x 64 columns, the lanes' rows spread over the warp: thread t gets
+// 16 lanes x 32 columns, the lanes' rows spread over the warp: thread t gets
 // columns 8 j + 2 (t % 4) + {0, 1} of row t / 4 in r[4 j], r[4 j + 1] and of row
 // t / 4 + 8 in r[4 j + 2], r[4 j + 3].  Waits.
 __device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t *r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\ntcgen05.wait::ld.sync.aligned;\n"
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;\n"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 }
@@ -303,6 +301,7 @@ struct __align__(1024) ChunkSmem {
   __align__(16) float fin[kRows];   // output factor of the finished item's rows
   __align__(16) float2 sg[2][kKeys]; // sigma of each key (-inf: no key) and 2^sigma
   float f[kRows];                   // logit factor of each row
+  float tmax[2][kRows], lsum[kRows];  // row maxima of a tile's halves; sums of the second half
   int32_t vis[kRows], w0[kRows];    // a row sees keys j < vis and w0 <= j < w0 + 128
   int plain[2];                     // every key valid with sigma 0
   uint32_t tmem, progress;          // progress: the key tile (of this CTA's) being filled
@@ -311,19 +310,26 @@ struct __align__(1024) ChunkSmem {
   __align__(8) uint64_t s_full[2], p_full, q_ready;
 };
 
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, int32_t *err) {
-  int ok = 1;
-  if ((threadIdx.x & 31) == 0) {
-    ok = tc::mbar_wait_bounded(bar, parity, kWaitIters) ? 1 : 0;
-    if (!ok) raise_err(err, CSA2_DEVERR_TIMEOUT);
-  }
-  return __shfl_sync(0xffffffffu, ok, 0) != 0;
+// Whether a phase is complete, without waiting; the same answer in every lane.
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(tc::smem_addr(bar)), "r"(parity)
+      : "memory");
+  return __any_sync(0xffffffffu, ok);
 }
-__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 128;\n" ::: "memory"); }
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, int32_t *err) {
+  const bool ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(bar, parity, kWaitIters));
+  if (!ok && (threadIdx.x & 31) == 0) raise_err(err, CSA2_DEVERR_TIMEOUT);
+  return ok;
+}
+__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;\n" ::: "memory"); }
 __device__ __forceinline__ int bar_softmax_or(int v) {
   int r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.or.pred q, 1, 128, p;\n selp.s32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.s32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n selp.s32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
       : "r"(v)
       : "memory");
@@ -692,7 +698,7 @@ __device__ __forceinline__ void produce(const ChunkArgs &a, const Plan &p, Chunk
 
 // ------------------------------------------------------------------ query, softmax, read-out
 // Query rows of an item to fp16 with a power-of-two scale per row, each row's
-// logit factor and bounds.  Sixteen rows per warp.
+// logit factor and bounds.  Eight rows per warp.
 __device__ __noinline__ void load_query(const ChunkArgs &a, const RowTile &x, ChunkSmem &sm, int warp, int lane) {
   constexpr int kPer = kDqk / 2 / 32;  // 9 words per lane
 #pragma unroll 1
@@ -736,13 +742,13 @@ __device__ __noinline__ void load_query(const ChunkArgs &a, const RowTile &x, Ch
 }
 
 // O^T of a finished item out of tensor memory: normalised rows, or (part) this
-// CTA's part of a shared row tile.  Each warp has 32 dims of every block.
+// CTA's part of a shared row tile.  Each warp has 32 dims of two blocks.
 __device__ __noinline__ void read_out(const ChunkArgs &a, const ChunkSmem &sm, float *part, int64_t row0, int nrows,
                                       uint32_t tmem, int warp, int lane) {
-  const int dim = 32 * warp + lane;
-  const uint32_t ta = tmem + (static_cast<uint32_t>(32 * warp) << 16) + kColO;
+  const int dim = 32 * (warp & 3) + lane;
+  const uint32_t ta = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kColO;
 #pragma unroll 1
-  for (int i16 = 0; i16 < 16; ++i16) {
+  for (int i16 = 8 * (warp >> 2); i16 < 8 * (warp >> 2) + 8; ++i16) {
     const int b = i16 >> 2, h0 = 16 * (i16 & 3);
     uint32_t r[16];
     tc::tmem_ld_32x32b_x16(ta + 16 * i16, r);
@@ -773,38 +779,39 @@ __device__ __noinline__ void read_out(const ChunkArgs &a, const ChunkSmem &sm, f
   }
 }
 
-// The softmax warps: warp w has rows 16 w .. + 15 of S (TMEM lanes 32 w ..), a
-// thread 16 keys of rows ra and rb, so row maxima and sums are two shuffles.  A
+// The softmax warps: warps w and w + 4 have rows 16 w .. + 15 of S (TMEM lanes
+// 32 w ..) and half of the keys each, a thread eight keys of rows ra and rb.  A
 // row's reference maximum moves only when a weight would exceed 2^15 (fp16);
-// then its O^T column is rescaled.
+// the two warps then agree on it, and the row's O^T column is rescaled.
 __device__ __forceinline__ void softmax(const ChunkArgs &a, const Plan &p, ChunkSmem &sm, uint32_t tmem, int warp, int lane) {
-  const uint32_t lane_base = static_cast<uint32_t>(32 * warp) << 16;
-  const int ra = 16 * warp + (lane >> 2), rb = ra + 8, col = 2 * (lane & 3);
+  const int half = warp >> 2;
+  const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+  const int ra = 16 * (warp & 3) + (lane >> 2), rb = ra + 8, col = 32 * half + 2 * (lane & 3);
   Items it(p, blockIdx.x);
   bool more = it.next(p, blockIdx.x), dead = false;
   uint32_t n = 0;  // tiles so far
   if (more) load_query(a, *it.x(p), sm, warp, lane);
+  bar_softmax();
   while (more) {
     const RowTile *x = it.x(p);
     const int k0 = it.k0, k1 = it.k1;
-    // this warp's rows only, written by itself
     const float fa = sm.f[ra], fb = sm.f[rb];
     const int va = sm.vis[ra], vb = sm.vis[rb], wa = sm.w0[ra], wb = sm.w0[rb];
-    float ma = 0.0f, mb = 0.0f, la = 0.0f, lb = 0.0f;  // reference (log2 units), sum
+    float ma = 0.0f, mb = 0.0f, la = 0.0f, lb = 0.0f;  // reference (log2 units), this half's sum
     bool seen_a = false, seen_b = false;               // the reference is set
     for (int kt = k0; kt < k1; ++kt, ++n) {
       const int b = n & 1;
       if (!dead) dead = !wait_warp(&sm.full[b], (n >> 1) & 1, a.err);  // sg, plain of this tile
       if (!dead) dead = !wait_warp(&sm.s_full[b], (n >> 1) & 1, a.err);
       tc::tc_fence_after();
-      float s[32];
-      tmem_ld_rows16(tmem + lane_base + kColS + 64 * b, reinterpret_cast<uint32_t *>(s));
+      float s[16];
+      tmem_ld_rows16(tmem + lane_base + kColS + 64 * b + 32 * half, reinterpret_cast<uint32_t *>(s));
       // exponents of the weighted weights, x = z + sigma - m, and their row maxima
       float ta = -INFINITY, tb = -INFINITY;
       const bool fast = sm.plain[b] && (kt + 1) * kKeys <= va;  // (rb sees no less)
       if (fast) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
+        for (int j = 0; j < 16; j += 4) {
           s[j] = fmaf(s[j], fa, -ma);
           s[j + 1] = fmaf(s[j + 1], fa, -ma);
           s[j + 2] = fmaf(s[j + 2], fb, -mb);
@@ -814,7 +821,7 @@ __device__ __forceinline__ void softmax(const ChunkArgs &a, const Plan &p, Chunk
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
+        for (int j = 0; j < 16; j += 4) {
           const int k = 2 * j + col, key = kt * kKeys + k;
           const float4 g = *reinterpret_cast<const float4 *>(&sm.sg[b][k]);  // (sigma, 2^sigma) of two keys
 #pragma unroll
@@ -833,59 +840,64 @@ __device__ __forceinline__ void softmax(const ChunkArgs &a, const Plan &p, Chunk
       tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, 1));
       ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, 2));
       tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, 2));
-      const bool mva = seen_a ? ta > kSlack : ta > -INFINITY, mvb = seen_b ? tb > kSlack : tb > -INFINITY;
-      if (__any_sync(0xffffffffu, mva || mvb)) {
+      if ((lane & 3) == 0) {
+        sm.tmax[half][ra] = ta;
+        sm.tmax[half][rb] = tb;
+      }
+      if (bar_softmax_or(ta > (seen_a ? kSlack : -INFINITY) || tb > (seen_b ? kSlack : -INFINITY))) {
+        // some row's reference moves: both halves' maxima, the same decision in both
+        ta = fmaxf(ta, sm.tmax[half ^ 1][ra]);
+        tb = fmaxf(tb, sm.tmax[half ^ 1][rb]);
+        const bool mva = ta > (seen_a ? kSlack : -INFINITY), mvb = tb > (seen_b ? kSlack : -INFINITY);
         const float da = mva ? ta - kTop : 0.0f, db = mvb ? tb - kTop : 0.0f;
         const float ala = mva ? (seen_a ? ex2(-da) : 0.0f) : 1.0f, alb = mvb ? (seen_b ? ex2(-db) : 0.0f) : 1.0f;
         ma += da;
         mb += db;
         la *= ala;
         lb *= alb;
+        seen_a |= mva;
+        seen_b |= mvb;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
+        for (int j = 0; j < 16; j += 4) {
           s[j] -= da;
           s[j + 1] -= da;
           s[j + 2] -= db;
           s[j + 3] -= db;
         }
-        seen_a |= mva;
-        seen_b |= mvb;
-        if ((lane & 3) == 0) {
+        if (half == 0 && (lane & 3) == 0) {
           sm.alpha[ra] = ala;
           sm.alpha[rb] = alb;
         }
-      } else if ((lane & 3) == 0) {
-        sm.alpha[ra] = 1.0f;
-        sm.alpha[rb] = 1.0f;
-      }
-      if (bar_softmax_or(kt > k0 && (mva || mvb))) {
-        // some row's reference moved: its O^T column follows, once the last PV is complete
-        if (!dead) dead = !wait_warp(&sm.empty[b ^ 1][3], ((n - 1) >> 1) & 1, a.err);
-        tc::tc_fence_after();
+        bar_softmax();
+        if (kt > k0) {
+          // the moved rows' O^T columns follow, once the last PV is complete
+          if (!dead) dead = !wait_warp(&sm.empty[b ^ 1][3], ((n - 1) >> 1) & 1, a.err);
+          tc::tc_fence_after();
 #pragma unroll 1
-        for (int h0 = 0; h0 < kRows; h0 += 8) {
-          const float4 a0 = *reinterpret_cast<const float4 *>(&sm.alpha[h0]), a1 = *reinterpret_cast<const float4 *>(&sm.alpha[h0 + 4]);
-          const float al[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-          bool any = false;
+          for (int h0 = 32 * half; h0 < 32 * half + 32; h0 += 8) {
+            const float4 a0 = *reinterpret_cast<const float4 *>(&sm.alpha[h0]), a1 = *reinterpret_cast<const float4 *>(&sm.alpha[h0 + 4]);
+            const float al[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+            bool any = false;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) any |= al[i] != 1.0f;
-          if (!any) continue;
-          uint32_t r[32];  // the four blocks' columns in flight together
-          const uint32_t at = tmem + lane_base + kColO + h0;
+            for (int i = 0; i < 8; ++i) any |= al[i] != 1.0f;
+            if (!any) continue;
+            uint32_t r[32];  // the four blocks' columns in flight together
+            const uint32_t at = tmem + lane_base + kColO + h0;
 #pragma unroll
-          for (int blk = 0; blk < 4; ++blk) tmem_ld_x8(at + 64 * blk, r + 8 * blk);
-          tmem_ld_wait_x8x4(r);
+            for (int blk = 0; blk < 4; ++blk) tmem_ld_x8(at + 64 * blk, r + 8 * blk);
+            tmem_ld_wait_x8x4(r);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * al[i & 7]);
+            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * al[i & 7]);
 #pragma unroll
-          for (int blk = 0; blk < 4; ++blk) tmem_st_x8(at + 64 * blk, r + 8 * blk);
+            for (int blk = 0; blk < 4; ++blk) tmem_st_x8(at + 64 * blk, r + 8 * blk);
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
         }
-        asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
       }
       // weights: l in fp32 (without sigma), P to fp16 (with it; at most 2^15)
-      uint8_t *pa = sm.k[b][8] + ra * 128 + 2 * col, *pb = pa + 8 * 128;  // ra % 8 == rb % 8
+      uint8_t *pa = sm.k[b][8] + ra * 128 + 4 * (lane & 3), *pb = pa + 8 * 128;  // ra % 8 == rb % 8
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const float p0 = ex2(s[4 * j]), p1 = ex2(s[4 * j + 1]), p2 = ex2(s[4 * j + 2]), p3 = ex2(s[4 * j + 3]);
         if (fast) {
           la += p0 + p1;
@@ -896,7 +908,7 @@ __device__ __forceinline__ void softmax(const ChunkArgs &a, const Plan &p, Chunk
           la = fmaf(p0, g0, fmaf(p1, g1, la));
           lb = fmaf(p2, g0, fmaf(p3, g1, lb));
         }
-        const int at = (j ^ (ra & 7)) << 4;
+        const int at = ((4 * half + j) ^ (ra & 7)) << 4;
         *reinterpret_cast<uint32_t *>(pa + at) = pack_h2(p0, p1);
         *reinterpret_cast<uint32_t *>(pb + at) = pack_h2(p2, p3);
       }
@@ -910,12 +922,17 @@ __device__ __forceinline__ void softmax(const ChunkArgs &a, const Plan &p, Chunk
     lb += __shfl_xor_sync(0xffffffffu, lb, 1);
     la += __shfl_xor_sync(0xffffffffu, la, 2);
     lb += __shfl_xor_sync(0xffffffffu, lb, 2);
+    if (half == 1 && (lane & 3) == 0) {
+      sm.lsum[ra] = la;
+      sm.lsum[rb] = lb;
+    }
+    bar_softmax();
     const bool direct = k0 == 0 && k1 == x->ntiles;
     float *part = direct ? nullptr : p.part + (2 * blockIdx.x + (k0 > 0 ? 0 : 1)) * kPartFloats;
-    if ((lane & 3) < 2) {  // lane 0 of a row's four: ra, lane 1: rb
+    if (half == 0 && (lane & 3) < 2) {  // lane 0 of a row's four: ra, lane 1: rb
       const bool second = lane & 1;
       const int r = second ? rb : ra;
-      float m = second ? (seen_b ? mb : -INFINITY) : (seen_a ? ma : -INFINITY), sum = second ? lb : la;
+      float m = second ? (seen_b ? mb : -INFINITY) : (seen_a ? ma : -INFINITY), sum = (second ? lb : la) + sm.lsum[r];
       if (!direct) {
         *reinterpret_cast<float2 *>(part + kLat * kRows + 2 * r) = make_float2(m, sum);
       } else {
@@ -933,12 +950,12 @@ __device__ __forceinline__ void softmax(const ChunkArgs &a, const Plan &p, Chunk
     }
     more = it.next(p, blockIdx.x);
     if (more) load_query(a, *it.x(p), sm, warp, lane);  // (S of the last tile is complete)
-    bar_softmax();                                      // fin
+    bar_softmax();                                      // fin, the next rows' data
     if (!dead) dead = !wait_warp(&sm.empty[(n - 1) & 1][3], ((n - 1) >> 1) & 1, a.err);
     tc::tc_fence_after();
     if (!dead) read_out(a, sm, part, x->row0, x->nrows, tmem, warp, lane);
     tc::tc_fence_before();
-    bar_softmax();  // fin read
+    // (fin is written again only after another item's barriers)
   }
 }
 
@@ -969,19 +986,17 @@ __device__ __forceinline__ void issue(const ChunkArgs &a, const Plan &p, ChunkSm
         qk(n);
       }
       ahead = false;
-      // whichever comes first: the next tile, or this one's P (bounded polls)
+      // whichever comes first: the next tile, or this one's P (bounded polls that
+      // do not suspend while either may come)
       bool ready = false;
-      for (uint32_t poll = 0; !ready && poll < kWaitIters * 1000; ++poll) {
-        if (!ahead && i + 1 < tiles && tc::mbar_try_wait(&sm.full[(n + 1) & 1], ((n + 1) >> 1) & 1, 0)) {
+      for (uint32_t poll = 0; !ready && !ahead && i + 1 < tiles && poll < kPolls; ++poll) {
+        ready = mbar_test(&sm.p_full, n & 1);
+        if (!ready && mbar_test(&sm.full[(n + 1) & 1], ((n + 1) >> 1) & 1)) {
           ahead = true;
           qk(n + 1);
         }
-        ready = tc::mbar_try_wait(&sm.p_full, n & 1, ahead || i + 1 == tiles ? 1000u : 0u);
       }
-      if (!ready) {
-        raise_err(a.err, CSA2_DEVERR_TIMEOUT);
-        return;
-      }
+      if (!ready && !wait_warp(&sm.p_full, n & 1, a.err)) return;
       tc::tc_fence_after();
       const uint32_t buf = (n & 1) * (kTile >> 4);
 #pragma unroll 1
