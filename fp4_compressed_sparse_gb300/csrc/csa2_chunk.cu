@@ -230,26 +230,8 @@ __device__ __forceinline__ void mma_pv(uint32_t elected, uint32_t d, uint64_t dv
 #pragma unroll
   for (int i = 0; i < 4; ++i) mma_f16(elected, d, dv + ((2048 * i) >> 4), dp + ((32 * i) >> 4), id, i ? 1u : acc);
 }
-__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t *r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t *r) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr));
-}
-// wait for four of them, their registers tied to it
-__device__ __forceinline__ void tmem_ld_wait_x8x4(uint32_t *r) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28])
-               :
-               : "memory");
-  asm volatile("" : "+r"(r[29]), "+r"(r[30]), "+r"(r[31]) : : "memory");
+__device__ __forceinline__ void tmem_st_x1(uint32_t taddr, uint32_t v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\n" ::"r"(taddr), "r"(v) : "memory");
 }
 // 16 lanes x 32 columns, the lanes' rows spread over the warp: thread t gets
 // columns 8 j + 2 (t % 4) + {0, 1} of row t / 4 in r[4 j], r[4 j + 1] and of row
@@ -294,6 +276,14 @@ __device__ __forceinline__ uint4 ldg16(const void *p) {
   return v;
 }
 
+// One key tile of the CTA, as the ahead warp lists it for the producers.
+struct TileRef {
+  int64_t base;  // physical entry of its first key; -1: not 64 whole entries; kNoTile after the last one
+  int32_t t, kt;
+};
+constexpr int64_t kNoTile = -2;
+constexpr int kRing = 16;
+
 struct __align__(1024) ChunkSmem {
   uint8_t k[2][kBlocks][kBlk];      // two key tiles in fp16; block 8 (RoPE) then holds the tile's P
   uint8_t q[kBlocks][kBlk];
@@ -301,12 +291,15 @@ struct __align__(1024) ChunkSmem {
   __align__(16) float fin[kRows];   // output factor of the finished item's rows
   __align__(16) float2 sg[2][kKeys]; // sigma of each key (-inf: no key) and 2^sigma
   float f[kRows];                   // logit factor of each row
+  uint32_t moved[2];                // rows whose reference moves in this tile
   float tmax[2][kRows], lsum[kRows];  // row maxima of a tile's halves; sums of the second half
   int32_t vis[kRows], w0[kRows];    // a row sees keys j < vis and w0 <= j < w0 + 128
   int plain[2];                     // every key valid with sigma 0
   uint32_t tmem, progress;          // progress: the key tile (of this CTA's) being filled
+  uint32_t listed;                  // key tiles in the ring so far
+  __align__(16) TileRef ring[kRing];
   __align__(8) uint64_t full[2];      // tile filled
-  __align__(8) uint64_t empty[2][4];  // ... and PV over its dims 128 i .. complete (3: P read too)
+  __align__(8) uint64_t empty[2];     // ... and its PV complete
   __align__(8) uint64_t s_full[2], p_full, q_ready;
 };
 
@@ -639,60 +632,59 @@ __device__ __noinline__ void fill_tail(const ChunkArgs &a, uint8_t (*k)[kBlk], f
 }
 
 // The producer warps: tile n into buffer n % 2 once the PV that read it last is
-// complete.
+// complete.  Which tiles, and where they lie, they are told through the ring:
+// a page-table load of their own would wait behind the records' loads.
+__device__ __forceinline__ TileRef ring_get(const ChunkSmem &sm, uint32_t n, int32_t *err) {
+  const volatile uint32_t *listed = &sm.listed;
+  uint32_t i = 0;
+  while (*listed <= n && i < kPolls) ++i;
+  if (*listed <= n) {
+    raise_err(err, CSA2_DEVERR_TIMEOUT);
+    return TileRef{kNoTile, 0, 0};
+  }
+  __threadfence_block();
+  const volatile TileRef *r = &sm.ring[n % kRing];
+  return TileRef{r->base, r->t, r->kt};
+}
 template <class Raw>
 __device__ __forceinline__ void produce(const ChunkArgs &a, const Plan &p, ChunkSmem &sm, int pt) {
   const csa2_cache &c = a.c;
   const int key = pt >> 2, qd = pt & 3;
-  Items it(p, blockIdx.x);
-  bool more = it.next(p, blockIdx.x), dead = false;
-  int kt = 0, seq = 0, T = 0;
-  int64_t base = -1;
+  bool dead = false;
   Raw raw;
-  if (more) {
-    kt = it.k0, seq = it.x(p)->seq, T = it.x(p)->T;
-    base = whole_tile(c, seq, T, kt);
-  }
-  if (base >= 0) {
+  TileRef cur = ring_get(sm, 0, a.err);
+  if (cur.base >= 0) {
 #pragma unroll
-    for (int s = 0; s < 5; ++s) load_step(c, base + key, qd, s, raw);
+    for (int s = 0; s < 5; ++s) load_step(c, cur.base + key, qd, s, raw);
   }
-  for (uint32_t n = 0; more; ++n) {
-    const int t = it.t, cur = kt, b = n & 1;
-    const bool whole = base >= 0;
-    if (++kt >= it.k1) {
-      more = it.next(p, blockIdx.x);
-      if (more) kt = it.k0, seq = it.x(p)->seq, T = it.x(p)->T;
-    }
-    base = more ? whole_tile(c, seq, T, kt) : -1;
-    const uint32_t par = ((n >> 1) & 1) ^ 1;
-    if (n >= 2 && !dead) dead = !wait_warp(&sm.empty[b][0], par, a.err);
+  for (uint32_t n = 0; cur.base != kNoTile; ++n) {
+    const int b = n & 1;
+    const TileRef next = ring_get(sm, n + 1, a.err);
+    if (n >= 2 && !dead) dead = !wait_warp(&sm.empty[b], ((n >> 1) & 1) ^ 1, a.err);
     if (pt == 0) {
       *const_cast<volatile uint32_t *>(&sm.progress) = n;
-      sm.plain[b] = whole && IsFp4<Raw>::v;
+      sm.plain[b] = cur.base >= 0 && IsFp4<Raw>::v;
     }
-    if (whole) {
+    if (cur.base >= 0) {
       const int sigma = raw_sigma(raw);
       if (qd == 0) sm.sg[b][key] = make_float2(static_cast<float>(sigma), pow2f(sigma));
 #pragma unroll
       for (int s = 0; s < 5; ++s) {
-        // dims 128 s .. are free as soon as their part of PV is complete, RoPE with the last
-        if (n >= 2 && s >= 1 && s < 4 && !dead) dead = !wait_warp(&sm.empty[b][s], par, a.err);
         store_step(sm.k[b], s, key, qd, raw, sigma);
-        if (base >= 0) load_step(c, base + key, qd, s, raw);
+        if (next.base >= 0) load_step(c, next.base + key, qd, s, raw);
       }
     } else {
-      if (n >= 2 && !dead) dead = !wait_warp(&sm.empty[b][3], par, a.err);
-      fill_tail(a, sm.k[b], sm.sg[b], p.tile[t], static_cast<int64_t>(cur) * kKeys, pt);
+      fill_tail(a, sm.k[b], sm.sg[b], p.tile[cur.t], static_cast<int64_t>(cur.kt) * kKeys, pt);
       raw = Raw{};
-      if (base >= 0) {
+      if (next.base >= 0) {
 #pragma unroll
-        for (int s = 0; s < 5; ++s) load_step(c, base + key, qd, s, raw);
+        for (int s = 0; s < 5; ++s) load_step(c, next.base + key, qd, s, raw);
       }
     }
     tc::fence_proxy_async_smem();
     __syncwarp();
     if ((pt & 31) == 0) tc::mbar_arrive(&sm.full[b]);
+    cur = next;
   }
 }
 
@@ -865,34 +857,43 @@ __device__ __forceinline__ void softmax(const ChunkArgs &a, const Plan &p, Chunk
           s[j + 3] -= db;
         }
         if (half == 0 && (lane & 3) == 0) {
-          sm.alpha[ra] = ala;
-          sm.alpha[rb] = alb;
+          if (mva) {
+            sm.alpha[ra] = ala;
+            atomicOr(&sm.moved[ra >> 5], 1u << (ra & 31));
+          }
+          if (mvb) {
+            sm.alpha[rb] = alb;
+            atomicOr(&sm.moved[rb >> 5], 1u << (rb & 31));
+          }
         }
         bar_softmax();
+        uint32_t todo = sm.moved[half];  // this warp's share: rows 32 half .., its 32 dims of each block
         if (kt > k0) {
           // the moved rows' O^T columns follow, once the last PV is complete
-          if (!dead) dead = !wait_warp(&sm.empty[b ^ 1][3], ((n - 1) >> 1) & 1, a.err);
+          if (!dead) dead = !wait_warp(&sm.empty[b ^ 1], ((n - 1) >> 1) & 1, a.err);
           tc::tc_fence_after();
-#pragma unroll 1
-          for (int h0 = 32 * half; h0 < 32 * half + 32; h0 += 8) {
-            const float4 a0 = *reinterpret_cast<const float4 *>(&sm.alpha[h0]), a1 = *reinterpret_cast<const float4 *>(&sm.alpha[h0 + 4]);
-            const float al[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-            bool any = false;
+          const uint32_t at = tmem + lane_base + kColO + 32 * half;
+          while (todo) {  // four rows' columns of the four blocks in flight together
+            int row[4];
+            uint32_t r[16];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) any |= al[i] != 1.0f;
-            if (!any) continue;
-            uint32_t r[32];  // the four blocks' columns in flight together
-            const uint32_t at = tmem + lane_base + kColO + h0;
+            for (int i = 0; i < 4; ++i) {
+              row[i] = todo ? __ffs(todo) - 1 : row[0];
+              todo &= todo - 1;
+            }
 #pragma unroll
-            for (int blk = 0; blk < 4; ++blk) tmem_ld_x8(at + 64 * blk, r + 8 * blk);
-            tmem_ld_wait_x8x4(r);
+            for (int i = 0; i < 16; ++i) tc::tmem_ld_32x32b_x1(at + 64 * (i & 3) + row[i >> 2], r[i]);
+            tc::tmem_ld_wait_x16(r);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * al[i & 7]);
-#pragma unroll
-            for (int blk = 0; blk < 4; ++blk) tmem_st_x8(at + 64 * blk, r + 8 * blk);
+            for (int i = 0; i < 16; ++i) {
+              const float v = __uint_as_float(r[i]) * sm.alpha[32 * half + row[i >> 2]];
+              tmem_st_x1(at + 64 * (i & 3) + row[i >> 2], __float_as_uint(v));
+            }
           }
           asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
         }
+        bar_softmax();  // every warp has read its part of moved
+        if (warp == 0 && lane < 2) sm.moved[lane] = 0;
       }
       // weights: l in fp32 (without sigma), P to fp16 (with it; at most 2^15)
       uint8_t *pa = sm.k[b][8] + ra * 128 + 4 * (lane & 3), *pb = pa + 8 * 128;  // ra % 8 == rb % 8
@@ -951,7 +952,7 @@ __device__ __forceinline__ void softmax(const ChunkArgs &a, const Plan &p, Chunk
     more = it.next(p, blockIdx.x);
     if (more) load_query(a, *it.x(p), sm, warp, lane);  // (S of the last tile is complete)
     bar_softmax();                                      // fin, the next rows' data
-    if (!dead) dead = !wait_warp(&sm.empty[(n - 1) & 1][3], ((n - 1) >> 1) & 1, a.err);
+    if (!dead) dead = !wait_warp(&sm.empty[(n - 1) & 1], ((n - 1) >> 1) & 1, a.err);
     tc::tc_fence_after();
     if (!dead) read_out(a, sm, part, x->row0, x->nrows, tmem, warp, lane);
     tc::tc_fence_before();
@@ -1000,16 +1001,16 @@ __device__ __forceinline__ void issue(const ChunkArgs &a, const Plan &p, ChunkSm
       tc::tc_fence_after();
       const uint32_t buf = (n & 1) * (kTile >> 4);
 #pragma unroll 1
-      for (int blk = 0; blk < 4; ++blk) {
+      for (int blk = 0; blk < 4; ++blk)
         mma_pv(e, tmem + kColO + 64 * blk, dv + buf + ((2 * kBlk * blk) >> 4), dp + buf, i > 0 ? 1u : 0u);
-        if (e) tc::mma_commit(&sm.empty[n & 1][blk]);
-      }
+      if (e) tc::mma_commit(&sm.empty[n & 1]);
     }
   }
 }
 
-// One thread that asks for the records of the CTA's coming key tiles: whole
-// tiles are contiguous in every plane, so a few bulk prefetches into L2 each.
+// One thread that lists the CTA's coming key tiles for the producers and asks
+// for their records: whole tiles are contiguous in every plane, so a few bulk
+// prefetches into L2 each.
 __device__ __forceinline__ void prefetch_l2(const uint8_t *p, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(p), "r"(bytes) : "memory");
 }
@@ -1018,12 +1019,31 @@ __device__ __forceinline__ void ahead(const ChunkArgs &a, const Plan &p, ChunkSm
   const volatile uint32_t *progress = &sm.progress;
   Items it(p, blockIdx.x);
   uint32_t n = 0;
+  auto list = [&](int64_t base, int t, int kt) {
+    volatile TileRef *r = &sm.ring[n % kRing];
+    r->base = base;
+    r->t = t;
+    r->kt = kt;
+    __threadfence_block();
+    *const_cast<volatile uint32_t *>(&sm.listed) = ++n;
+  };
   while (it.next(p, blockIdx.x)) {
     const int seq = it.x(p)->seq, T = it.x(p)->T;
-    for (int kt = it.k0; kt < it.k1; ++kt, ++n) {
-      // (bounded: were the workers to stop, it would only ask too early)
-      for (int i = 0; i < 100000 && *progress + kAhead < n; ++i) __nanosleep(100);
+    for (int kt = it.k0; kt < it.k1; ++kt) {
       const int64_t base = whole_tile(c, seq, T, kt);
+      // not further ahead than the ring and the L2 should hold (bounded: a stopped
+      // producer has raised its own error)
+      uint32_t i = 0;
+      while (*progress + kAhead < n && i < kPolls) {
+        __nanosleep(100);
+        ++i;
+      }
+      if (*progress + kAhead < n) {
+        raise_err(a.err, CSA2_DEVERR_TIMEOUT);
+        list(kNoTile, 0, 0);
+        return;
+      }
+      list(base, it.t, kt);
       if (base < 0) continue;
       if (c.entry_format == CSA2_ENTRY_FP8) {
         prefetch_l2(c.lat_codes + base * 512, kKeys * 512);
@@ -1041,6 +1061,7 @@ __device__ __forceinline__ void ahead(const ChunkArgs &a, const Plan &p, ChunkSm
       }
     }
   }
+  list(kNoTile, 0, 0);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) k_chunk_attn(const __grid_constant__ ChunkArgs a,
@@ -1059,13 +1080,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunk_attn(const __grid_constan
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sm.full[i], kPrWarps);
-      for (int j = 0; j < 4; ++j) tc::mbar_init(&sm.empty[i][j], 1);
+      tc::mbar_init(&sm.empty[i], 1);
       tc::mbar_init(&sm.s_full[i], 1);
     }
     tc::mbar_init(&sm.p_full, kSmWarps);
     tc::mbar_init(&sm.q_ready, kSmWarps);
     tc::fence_mbar_init();
     sm.progress = 0;
+    sm.listed = 0;
+    sm.moved[0] = sm.moved[1] = 0;
   }
   tc::tc_fence_before();
   __syncthreads();
