@@ -32,7 +32,7 @@ constexpr int kKeys = 64;                    // keys of a key tile
 constexpr int kBlk = kKeys * 128;            // a 64-dim block of a key tile, or of the query: 8 KB
 constexpr int kBlocks = kDqk / 64;           // 9: 8 latent, 1 RoPE
 constexpr int kTile = kBlocks * kBlk;        // 73,728 B
-constexpr int kSmWarps = 8, kPrWarps = 8;    // softmax / producer warps
+constexpr int kSmWarps = 8, kPrWarps = 16;   // softmax / producer warps
 constexpr int kMmaWarp = kSmWarps + kPrWarps, kAheadWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kAheadWarp + 1);
 constexpr int kAhead = 4;                    // key tiles requested into L2 ahead of use
@@ -291,7 +291,7 @@ struct __align__(1024) ChunkSmem {
   __align__(16) float fin[kRows];   // output factor of the finished item's rows
   __align__(16) float2 sg[2][kKeys]; // sigma of each key (-inf: no key) and 2^sigma
   float f[kRows];                   // logit factor of each row
-  uint32_t moved[2];                // rows whose reference moves in this tile
+  uint32_t moved[2][2];             // rows whose reference moves in a tile (by its parity)
   float tmax[2][kRows], lsum[kRows];  // row maxima of a tile's halves; sums of the second half
   int32_t vis[kRows], w0[kRows];    // a row sees keys j < vis and w0 <= j < w0 + 128
   int plain[2];                     // every key valid with sigma 0
@@ -357,40 +357,36 @@ __device__ __forceinline__ int sigma_of(int e) {
 }
 
 // ------------------------------------------------------------------ filling a tile
-// Five steps: dims 128 s .. of the 64 keys (s < 4), then the RoPE dims; four
-// threads per key, 32 (RoPE: 16) dims each.  The records come through registers,
+// Five steps: dims 128 s .. of the 64 keys (s < 4), then the RoPE dims; eight
+// threads per key, 16 (RoPE: 8) dims each.  The records come through registers,
 // requested a whole tile ahead (and into L2 further ahead, by the ahead warp).
 template <class Raw>
 struct IsFp4 {
   static constexpr bool v = false;
 };
 struct RawFp4 {
-  uint4 w[4];
-  uint2 r;
-  uint32_t sc[5];
+  uint2 w[4];
+  uint32_t r, sc[5];
 };
 template <>
 struct IsFp4<RawFp4> {
   static constexpr bool v = true;
 };
 struct RawFp8 {
-  uint4 w[5][2];
+  uint4 w[5];
   uint4 sc;  // the key's 16 scales: word s holds those of step s
 };
-__device__ __forceinline__ uint32_t ldg_u16(const uint8_t *p) { return __ldg(reinterpret_cast<const uint16_t *>(p)); }
-__device__ __forceinline__ void load_step(const csa2_cache &c, int64_t e, int qd, int s, RawFp4 &r) {
+__device__ __forceinline__ void load_step(const csa2_cache &c, int64_t e, int o, int s, RawFp4 &r) {
   if (s < 4) {
-    r.w[s] = ldg16(c.lat_codes + e * 256 + 64 * s + 16 * qd);
-    r.sc[s] = ldg_u16(c.lat_scales + e * 32 + 8 * s + 2 * qd);
+    r.w[s] = __ldg(reinterpret_cast<const uint2 *>(c.lat_codes + e * 256 + 64 * s + 8 * o));
+    r.sc[s] = __ldg(c.lat_scales + e * 32 + 8 * s + o);
   } else {
-    r.r = __ldg(reinterpret_cast<const uint2 *>(c.rope_codes + e * 32 + 8 * qd));
-    r.sc[4] = __ldg(c.rope_scales + e * 4 + qd);
+    r.r = __ldg(reinterpret_cast<const uint32_t *>(c.rope_codes + e * 32 + 4 * o));
+    r.sc[4] = __ldg(c.rope_scales + e * 4 + (o >> 1));
   }
 }
-__device__ __forceinline__ void load_step(const csa2_cache &c, int64_t e, int qd, int s, RawFp8 &r) {
-  const uint8_t *src = s < 4 ? c.lat_codes + e * 512 + 128 * s + 32 * qd : c.rope_codes + e * 128 + 32 * qd;
-  r.w[s][0] = ldg16(src);
-  r.w[s][1] = ldg16(src + 16);
+__device__ __forceinline__ void load_step(const csa2_cache &c, int64_t e, int o, int s, RawFp8 &r) {
+  r.w[s] = ldg16(s < 4 ? c.lat_codes + e * 512 + 128 * s + 16 * o : c.rope_codes + e * 128 + 16 * o);
   if (s == 4) r.sc = ldg16(c.lat_scales + e * 16);  // (the last step: the old scales are done with)
 }
 
@@ -398,46 +394,38 @@ __device__ __forceinline__ uint4 dq_e2m1(uint32_t w, uint32_t s2) {
   return make_uint4(hmul2u(e2m1x2_h2(w), s2), hmul2u(e2m1x2_h2(w >> 8), s2), hmul2u(e2m1x2_h2(w >> 16), s2),
                     hmul2u(e2m1x2_h2(w >> 24), s2));
 }
+__device__ __forceinline__ uint4 dq_e4m3(uint32_t w0, uint32_t w1, uint32_t m2) {
+  return make_uint4(hmul2u(e4m3x2_h2(w0), m2), hmul2u(e4m3x2_h2(w0 >> 16), m2), hmul2u(e4m3x2_h2(w1), m2),
+                    hmul2u(e4m3x2_h2(w1 >> 16), m2));
+}
 // 16-byte chunk x (8 dims) of key (or query row) `key` in a 64-dim block
 __device__ __forceinline__ uint8_t *chunk_at(uint8_t *blk, int key, int x) { return blk + key * 128 + ((x ^ (key & 7)) << 4); }
-// Chunks i = 0..3 of a thread's 32 dims of step s.  Lanes of the second 64-dim
-// block (qd >= 2) take theirs in the order 2 3 0 1, so that the eight lanes of a
-// store phase (2 keys x 4 quarters) hit eight different 16 B banks.
-__device__ __forceinline__ uint8_t *quarter_at(uint8_t (*k)[kBlk], int s, int key, int qd, int i) {
-  return chunk_at(k[2 * s + (qd >> 1)], key, 4 * (qd & 1) + (i ^ (qd & 2)));
+// The two chunks of a thread's 16 dims of step s: lo = its first 8 dims.  The
+// threads of the second 64-dim block (o >= 4) store theirs in the other order, so
+// that a key's eight threads hit eight different 16 B banks at a time.
+__device__ __forceinline__ void put_step(uint8_t (*k)[kBlk], int s, int key, int o, uint4 lo, uint4 hi) {
+  const int flip = o >> 2;
+  uint8_t *blk = k[2 * s + flip];
+  const int x = 2 * (o & 3);
+  *reinterpret_cast<uint4 *>(chunk_at(blk, key, x + flip)) = flip ? hi : lo;
+  *reinterpret_cast<uint4 *>(chunk_at(blk, key, x + (flip ^ 1))) = flip ? lo : hi;
 }
-__device__ __forceinline__ void store_step(uint8_t (*k)[kBlk], int s, int key, int qd, const RawFp4 &r, int) {
-  if (s < 4) {
-    uint32_t w[4] = {r.w[s].x, r.w[s].y, r.w[s].z, r.w[s].w};
-    uint32_t sa = e4m3x2_h2((r.sc[s] & 0xFF) * 0x101), sb = e4m3x2_h2((r.sc[s] >> 8) * 0x101);
-    if (qd & 2) {
-      const uint32_t t0 = w[0], t1 = w[1], ts = sa;
-      w[0] = w[2], w[1] = w[3], w[2] = t0, w[3] = t1, sa = sb, sb = ts;
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(quarter_at(k, s, key, qd, i)) = dq_e2m1(w[i], i < 2 ? sa : sb);
+__device__ __forceinline__ void store_step(uint8_t (*k)[kBlk], int s, int key, int o, const RawFp4 &r, int) {
+  const uint32_t s2 = e4m3x2_h2(r.sc[s] * 0x101);
+  if (s < 4) {  // (the swap before the conversion: two registers instead of eight)
+    const uint32_t w0 = o >= 4 ? r.w[s].y : r.w[s].x, w1 = o >= 4 ? r.w[s].x : r.w[s].y;
+    uint8_t *blk = k[2 * s + (o >> 2)];
+    const int x = 2 * (o & 3) + (o >> 2);
+    *reinterpret_cast<uint4 *>(chunk_at(blk, key, x)) = dq_e2m1(w0, s2);
+    *reinterpret_cast<uint4 *>(chunk_at(blk, key, x ^ 1)) = dq_e2m1(w1, s2);
   } else {
-    const uint32_t s2 = e4m3x2_h2(r.sc[4] * 0x101);
-    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, 2 * qd)) = dq_e2m1(r.r.x, s2);
-    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, 2 * qd + 1)) = dq_e2m1(r.r.y, s2);
+    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, o)) = dq_e2m1(r.r, s2);
   }
 }
 // factor 2^k as an fp16 pair (k <= 15; zero where fp16 has no such value)
 __device__ __forceinline__ uint32_t pow2_h2(int k) {
   const uint32_t h = k < -24 ? 0u : k < -14 ? 1u << (k + 24) : static_cast<uint32_t>(k + 15) << 10;
   return h * 0x10001u;
-}
-// 32 E4M3 values times 2^(sc - 127 - sigma) as a thread's dims of step s
-__device__ __forceinline__ void store_e4m3(uint8_t (*k)[kBlk], int s, int key, int qd, const uint4 *c, uint32_t sc, int sigma) {
-  const uint32_t m2 = pow2_h2(static_cast<int>(sc) - 127 - sigma);
-  const bool flip = qd & 2;
-  const uint4 a = flip ? c[1] : c[0], b = flip ? c[0] : c[1];
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    *reinterpret_cast<uint4 *>(quarter_at(k, s, key, qd, i)) =
-        make_uint4(hmul2u(e4m3x2_h2(w[2 * i]), m2), hmul2u(e4m3x2_h2(w[2 * i] >> 16), m2),
-                   hmul2u(e4m3x2_h2(w[2 * i + 1]), m2), hmul2u(e4m3x2_h2(w[2 * i + 1] >> 16), m2));
 }
 __device__ __forceinline__ uint4 bf16x8_h(uint4 v, float inv) {
   return make_uint4(pack_h2(__uint_as_float(v.x << 16) * inv, __uint_as_float(v.x & 0xFFFF0000u) * inv),
@@ -446,13 +434,12 @@ __device__ __forceinline__ uint4 bf16x8_h(uint4 v, float inv) {
                     pack_h2(__uint_as_float(v.w << 16) * inv, __uint_as_float(v.w & 0xFFFF0000u) * inv));
 }
 __device__ __forceinline__ uint32_t word_of(uint4 v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-__device__ __forceinline__ void store_step(uint8_t (*k)[kBlk], int s, int key, int qd, const RawFp8 &r, int sigma) {
+__device__ __forceinline__ void store_step(uint8_t (*k)[kBlk], int s, int key, int o, const RawFp8 &r, int sigma) {
   if (s < 4) {
-    store_e4m3(k, s, key, qd, r.w[s], (word_of(r.sc, s) >> (8 * qd)) & 0xFF, sigma);
-  } else {  // 16 RoPE dims in bf16
-    const float inv = pow2f(-sigma);
-    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, 2 * qd)) = bf16x8_h(r.w[4][0], inv);
-    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, 2 * qd + 1)) = bf16x8_h(r.w[4][1], inv);
+    const uint32_t m2 = pow2_h2(static_cast<int>((word_of(r.sc, s) >> (8 * (o >> 1))) & 0xFF) - 127 - sigma);
+    put_step(k, s, key, o, dq_e4m3(r.w[s].x, r.w[s].y, m2), dq_e4m3(r.w[s].z, r.w[s].w, m2));
+  } else {  // 8 RoPE dims in bf16
+    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, o)) = bf16x8_h(r.w[4], pow2f(-sigma));
   }
 }
 __device__ __forceinline__ int e8m0_top(uint4 s) {  // largest of 16 scale bytes
@@ -464,9 +451,10 @@ __device__ __forceinline__ uint32_t bf16_top(uint4 v, uint32_t m) {  // largest 
   const uint32_t a = __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), b = __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu);
   return __vmaxu2(m, __vmaxu2(a, b));
 }
-__device__ __forceinline__ uint32_t key_max(uint32_t bf) {  // over the four threads of a key
+__device__ __forceinline__ uint32_t key_max(uint32_t bf) {  // over the eight threads of a key
   bf = __vmaxu2(bf, __shfl_xor_sync(0xffffffffu, bf, 1));
-  return __vmaxu2(bf, __shfl_xor_sync(0xffffffffu, bf, 2));
+  bf = __vmaxu2(bf, __shfl_xor_sync(0xffffffffu, bf, 2));
+  return __vmaxu2(bf, __shfl_xor_sync(0xffffffffu, bf, 4));
 }
 // exponent e (largest magnitude about 2^e) of a key: an E8M0 top (block maximum
 // about 2^(top - 119)) and / or the largest bf16 magnitude
@@ -477,7 +465,7 @@ __device__ __forceinline__ int key_exponent(int e8, uint32_t bf) {
 }
 __device__ __forceinline__ int raw_sigma(const RawFp4 &) { return 0; }
 __device__ __forceinline__ int raw_sigma(const RawFp8 &r) {
-  return sigma_of(key_exponent(e8m0_top(r.sc), key_max(bf16_top(r.w[4][0], bf16_top(r.w[4][1], 0)))));
+  return sigma_of(key_exponent(e8m0_top(r.sc), key_max(bf16_top(r.w[4], 0))));
 }
 
 // A tile that is not made of whole entries alone: key j is entry j (j < T), a
@@ -531,81 +519,65 @@ __device__ __forceinline__ void tail_key(const ChunkArgs &a, const RowTile &x, i
     k.rope_scales = fp8 ? k.scales + 16 : nullptr;
   }
 }
-__device__ __forceinline__ int tail_sigma(const TailKey &k, int qd) {
+__device__ __forceinline__ int tail_sigma(const TailKey &k, int o) {
   int e8 = 0;
   uint32_t bf = 0;
   if (k.kind == 2) {
     e8 = e8m0_top(ldg16(k.scales));
-    bf = bf16_top(ldg16(k.rope + 32 * qd), bf16_top(ldg16(k.rope + 32 * qd + 16), 0));
+    bf = bf16_top(ldg16(k.rope + 16 * o), 0);
   } else if (k.kind == 3) {
     e8 = max(e8m0_top(ldg16(k.scales)), static_cast<int>(max(k.rope_scales[0], k.rope_scales[1])));
   } else if (k.kind == 4) {
 #pragma unroll
-    for (int i = 0; i < 18; ++i) bf = bf16_top(ldg16(k.codes + 288 * qd + 16 * i), bf);
+    for (int i = 0; i < 9; ++i) bf = bf16_top(ldg16(k.codes + 144 * o + 16 * i), bf);
   }
   bf = key_max(bf);
   return k.kind >= 2 ? sigma_of(key_exponent(e8, bf)) : 0;
 }
 struct RawTail {
-  uint4 w[4];
+  uint4 w[2];
   uint32_t sc;
 };
-__device__ __forceinline__ void tail_load(const TailKey &k, int s, int qd, RawTail &r) {
+__device__ __forceinline__ void tail_load(const TailKey &k, int s, int o, RawTail &r) {
   if (k.kind == 1) {
     if (s < 4) {
-      r.w[0] = ldg16(k.codes + 64 * s + 16 * qd);
-      r.sc = ldg_u16(k.scales + 8 * s + 2 * qd);
-    } else {
-      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(k.rope + 8 * qd));
+      const uint2 v = __ldg(reinterpret_cast<const uint2 *>(k.codes + 64 * s + 8 * o));
       r.w[0].x = v.x, r.w[0].y = v.y;
-      r.sc = __ldg(k.rope_scales + qd);
+      r.sc = __ldg(k.scales + 8 * s + o);
+    } else {
+      r.w[0].x = __ldg(reinterpret_cast<const uint32_t *>(k.rope + 4 * o));
+      r.sc = __ldg(k.rope_scales + (o >> 1));
     }
+  } else if (k.kind == 3 && s == 4) {
+    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(k.rope + 8 * o));
+    r.w[0].x = v.x, r.w[0].y = v.y;
+    r.sc = __ldg(k.rope_scales + (o >> 2));
   } else if (k.kind == 2 || k.kind == 3) {
-    const bool half = k.kind == 3 && s == 4;  // 16 E4M3 RoPE dims
-    const uint8_t *src = s < 4 ? k.codes + 128 * s + 32 * qd : k.rope + (half ? 16 : 32) * qd;
-    r.w[0] = ldg16(src);
-    if (!half) r.w[1] = ldg16(src + 16);
-    if (s < 4) r.sc = __ldg(k.scales + 4 * s + qd);
-    else if (half) r.sc = __ldg(k.rope_scales + (qd >> 1));
+    r.w[0] = ldg16(s < 4 ? k.codes + 128 * s + 16 * o : k.rope + 16 * o);
+    if (s < 4) r.sc = __ldg(k.scales + 4 * s + (o >> 1));
   } else if (k.kind == 4) {
-    const uint8_t *src = s < 4 ? k.codes + 256 * s + 64 * qd : k.rope + 32 * qd;
+    const uint8_t *src = s < 4 ? k.codes + 256 * s + 32 * o : k.rope + 16 * o;
     r.w[0] = ldg16(src);
-    r.w[1] = ldg16(src + 16);
-    if (s < 4) {
-      r.w[2] = ldg16(src + 32);
-      r.w[3] = ldg16(src + 48);
-    }
+    if (s < 4) r.w[1] = ldg16(src + 16);
   }
 }
-__device__ __forceinline__ void tail_store(uint8_t (*k)[kBlk], const TailKey &t, int s, int key, int qd, const RawTail &r, int sigma) {
-  uint4 o[4];
-  const float inv = pow2f(-sigma);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = make_uint4(0, 0, 0, 0);
+__device__ __forceinline__ void tail_store(uint8_t (*k)[kBlk], const TailKey &t, int s, int key, int o, const RawTail &r, int sigma) {
+  uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
   if (t.kind == 1) {
-    const uint32_t sa = e4m3x2_h2((r.sc & 0xFF) * 0x101), sb = s < 4 ? e4m3x2_h2((r.sc >> 8) * 0x101) : sa;
-    o[0] = dq_e2m1(r.w[0].x, sa);
-    o[1] = dq_e2m1(r.w[0].y, sa);
-    o[2] = dq_e2m1(r.w[0].z, sb);
-    o[3] = dq_e2m1(r.w[0].w, sb);
+    const uint32_t s2 = e4m3x2_h2(r.sc * 0x101);
+    lo = dq_e2m1(r.w[0].x, s2);
+    hi = dq_e2m1(r.w[0].y, s2);
   } else if (t.kind == 4 || (t.kind == 2 && s == 4)) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = bf16x8_h(r.w[i], inv);
+    const float inv = pow2f(-sigma);
+    lo = bf16x8_h(r.w[0], inv);
+    hi = bf16x8_h(r.w[1], inv);
   } else if (t.kind) {
     const uint32_t m2 = pow2_h2(static_cast<int>(r.sc) - 127 - sigma);
-    const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      o[i] = make_uint4(hmul2u(e4m3x2_h2(w[2 * i]), m2), hmul2u(e4m3x2_h2(w[2 * i] >> 16), m2),
-                        hmul2u(e4m3x2_h2(w[2 * i + 1]), m2), hmul2u(e4m3x2_h2(w[2 * i + 1] >> 16), m2));
+    lo = dq_e4m3(r.w[0].x, r.w[0].y, m2);
+    hi = dq_e4m3(r.w[0].z, r.w[0].w, m2);
   }
-  if (s < 4) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(chunk_at(k[2 * s + (qd >> 1)], key, 4 * (qd & 1) + i)) = o[i];
-  } else {
-    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, 2 * qd)) = o[0];
-    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, 2 * qd + 1)) = o[1];
-  }
+  if (s < 4) put_step(k, s, key, o, lo, hi);
+  else *reinterpret_cast<uint4 *>(chunk_at(k[8], key, o)) = lo;
 }
 
 // Physical entry of the first key of key tile kt, or -1 when the tile is not 64
@@ -616,18 +588,18 @@ __device__ __forceinline__ int64_t whole_tile(const csa2_cache &c, int seq, int 
 }
 
 __device__ __noinline__ void fill_tail(const ChunkArgs &a, uint8_t (*k)[kBlk], float2 *sg, const RowTile &x, int64_t j0, int pt) {
-  const int key = pt >> 2, qd = pt & 3;
+  const int key = pt >> 3, o = pt & 7;
   TailKey t;
   tail_key(a, x, j0 + key, t);
   RawTail r;
-  tail_load(t, 0, qd, r);
-  const int sigma = tail_sigma(t, qd);
-  if (qd == 0) sg[key] = t.kind ? make_float2(static_cast<float>(sigma), pow2f(sigma)) : make_float2(-INFINITY, 0.0f);
+  tail_load(t, 0, o, r);
+  const int sigma = tail_sigma(t, o);
+  if (o == 0) sg[key] = t.kind ? make_float2(static_cast<float>(sigma), pow2f(sigma)) : make_float2(-INFINITY, 0.0f);
 #pragma unroll 1
   for (int s = 0; s < 5; ++s) {
     const RawTail now = r;
-    if (s < 4) tail_load(t, s + 1, qd, r);
-    tail_store(k, t, s, key, qd, now, sigma);
+    if (s < 4) tail_load(t, s + 1, o, r);
+    tail_store(k, t, s, key, o, now, sigma);
   }
 }
 
@@ -649,13 +621,13 @@ __device__ __forceinline__ TileRef ring_get(const ChunkSmem &sm, uint32_t n, int
 template <class Raw>
 __device__ __forceinline__ void produce(const ChunkArgs &a, const Plan &p, ChunkSmem &sm, int pt) {
   const csa2_cache &c = a.c;
-  const int key = pt >> 2, qd = pt & 3;
+  const int key = pt >> 3, o = pt & 7;
   bool dead = false;
   Raw raw;
   TileRef cur = ring_get(sm, 0, a.err);
   if (cur.base >= 0) {
 #pragma unroll
-    for (int s = 0; s < 5; ++s) load_step(c, cur.base + key, qd, s, raw);
+    for (int s = 0; s < 5; ++s) load_step(c, cur.base + key, o, s, raw);
   }
   for (uint32_t n = 0; cur.base != kNoTile; ++n) {
     const int b = n & 1;
@@ -667,18 +639,18 @@ __device__ __forceinline__ void produce(const ChunkArgs &a, const Plan &p, Chunk
     }
     if (cur.base >= 0) {
       const int sigma = raw_sigma(raw);
-      if (qd == 0) sm.sg[b][key] = make_float2(static_cast<float>(sigma), pow2f(sigma));
+      if (o == 0) sm.sg[b][key] = make_float2(static_cast<float>(sigma), pow2f(sigma));
 #pragma unroll
       for (int s = 0; s < 5; ++s) {
-        store_step(sm.k[b], s, key, qd, raw, sigma);
-        if (next.base >= 0) load_step(c, next.base + key, qd, s, raw);
+        store_step(sm.k[b], s, key, o, raw, sigma);
+        if (next.base >= 0) load_step(c, next.base + key, o, s, raw);
       }
     } else {
       fill_tail(a, sm.k[b], sm.sg[b], p.tile[cur.t], static_cast<int64_t>(cur.kt) * kKeys, pt);
       raw = Raw{};
       if (next.base >= 0) {
 #pragma unroll
-        for (int s = 0; s < 5; ++s) load_step(c, next.base + key, qd, s, raw);
+        for (int s = 0; s < 5; ++s) load_step(c, next.base + key, o, s, raw);
       }
     }
     tc::fence_proxy_async_smem();
@@ -836,7 +808,10 @@ __device__ __forceinline__ void softmax(const ChunkArgs &a, const Plan &p, Chunk
         sm.tmax[half][ra] = ta;
         sm.tmax[half][rb] = tb;
       }
-      if (bar_softmax_or(ta > (seen_a ? kSlack : -INFINITY) || tb > (seen_b ? kSlack : -INFINITY))) {
+      const bool moving = bar_softmax_or(ta > (seen_a ? kSlack : -INFINITY) || tb > (seen_b ? kSlack : -INFINITY));
+      // the next tile's list starts empty (the last tile's, in its place, has been read)
+      if (warp == 0 && lane < 2) sm.moved[b ^ 1][lane] = 0;
+      if (moving) {
         // some row's reference moves: both halves' maxima, the same decision in both
         ta = fmaxf(ta, sm.tmax[half ^ 1][ra]);
         tb = fmaxf(tb, sm.tmax[half ^ 1][rb]);
@@ -859,17 +834,38 @@ __device__ __forceinline__ void softmax(const ChunkArgs &a, const Plan &p, Chunk
         if (half == 0 && (lane & 3) == 0) {
           if (mva) {
             sm.alpha[ra] = ala;
-            atomicOr(&sm.moved[ra >> 5], 1u << (ra & 31));
+            atomicOr(&sm.moved[b][ra >> 5], 1u << (ra & 31));
           }
           if (mvb) {
             sm.alpha[rb] = alb;
-            atomicOr(&sm.moved[rb >> 5], 1u << (rb & 31));
+            atomicOr(&sm.moved[b][rb >> 5], 1u << (rb & 31));
           }
         }
+      }
+      // weights: l in fp32 (without sigma), P to fp16 (with it; at most 2^15)
+      uint8_t *pa = sm.k[b][8] + ra * 128 + 4 * (lane & 3), *pb = pa + 8 * 128;  // ra % 8 == rb % 8
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p0 = ex2(s[4 * j]), p1 = ex2(s[4 * j + 1]), p2 = ex2(s[4 * j + 2]), p3 = ex2(s[4 * j + 3]);
+        if (fast) {
+          la += p0 + p1;
+          lb += p2 + p3;
+        } else {
+          const float4 g = *reinterpret_cast<const float4 *>(&sm.sg[b][8 * j + col]);
+          const float g0 = ex2(-fmaxf(g.x, -126.0f)), g1 = ex2(-fmaxf(g.z, -126.0f));
+          la = fmaf(p0, g0, fmaf(p1, g1, la));
+          lb = fmaf(p2, g0, fmaf(p3, g1, lb));
+        }
+        const int at = ((4 * half + j) ^ (ra & 7)) << 4;
+        *reinterpret_cast<uint32_t *>(pa + at) = pack_h2(p0, p1);
+        *reinterpret_cast<uint32_t *>(pb + at) = pack_h2(p2, p3);
+      }
+      if (moving) {
+        // the moved rows' O^T columns follow, once the last PV is complete (this
+        // comes after the weights: they do not depend on it)
         bar_softmax();
-        uint32_t todo = sm.moved[half];  // this warp's share: rows 32 half .., its 32 dims of each block
+        uint32_t todo = sm.moved[b][half];  // this warp's share: rows 32 half .., its 32 dims of each block
         if (kt > k0) {
-          // the moved rows' O^T columns follow, once the last PV is complete
           if (!dead) dead = !wait_warp(&sm.empty[b ^ 1], ((n - 1) >> 1) & 1, a.err);
           tc::tc_fence_after();
           const uint32_t at = tmem + lane_base + kColO + 32 * half;
@@ -892,26 +888,6 @@ __device__ __forceinline__ void softmax(const ChunkArgs &a, const Plan &p, Chunk
           }
           asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
         }
-        bar_softmax();  // every warp has read its part of moved
-        if (warp == 0 && lane < 2) sm.moved[lane] = 0;
-      }
-      // weights: l in fp32 (without sigma), P to fp16 (with it; at most 2^15)
-      uint8_t *pa = sm.k[b][8] + ra * 128 + 4 * (lane & 3), *pb = pa + 8 * 128;  // ra % 8 == rb % 8
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float p0 = ex2(s[4 * j]), p1 = ex2(s[4 * j + 1]), p2 = ex2(s[4 * j + 2]), p3 = ex2(s[4 * j + 3]);
-        if (fast) {
-          la += p0 + p1;
-          lb += p2 + p3;
-        } else {
-          const float4 g = *reinterpret_cast<const float4 *>(&sm.sg[b][8 * j + col]);
-          const float g0 = ex2(-fmaxf(g.x, -126.0f)), g1 = ex2(-fmaxf(g.z, -126.0f));
-          la = fmaf(p0, g0, fmaf(p1, g1, la));
-          lb = fmaf(p2, g0, fmaf(p3, g1, lb));
-        }
-        const int at = ((4 * half + j) ^ (ra & 7)) << 4;
-        *reinterpret_cast<uint32_t *>(pa + at) = pack_h2(p0, p1);
-        *reinterpret_cast<uint32_t *>(pb + at) = pack_h2(p2, p3);
       }
       tc::fence_proxy_async_smem();
       tc::tc_fence_before();
@@ -1088,7 +1064,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunk_attn(const __grid_constan
     tc::fence_mbar_init();
     sm.progress = 0;
     sm.listed = 0;
-    sm.moved[0] = sm.moved[1] = 0;
+    sm.moved[0][0] = sm.moved[0][1] = sm.moved[1][0] = sm.moved[1][1] = 0;
   }
   tc::tc_fence_before();
   __syncthreads();
