@@ -73,7 +73,7 @@ struct __align__(16) RowTile {
 struct CtaRange {
   int64_t lo, hi;  // units [lo, hi) of the whole work (a row tile of n key tiles is n + 1 units)
   int32_t tile;    // the row tile that holds unit lo
-  int32_t pad;
+  int32_t first;   // the row tile ends here and began in CTA `first`: its parts are joined; -1: not so
 };
 struct Plan {
   int32_t *seq_tile;  // [batch + 1] first row tile of each sequence
@@ -85,7 +85,7 @@ struct Plan {
 };
 
 __host__ __device__ inline int64_t visible(int64_t pos, int ratio, int64_t cap) {
-  const int64_t v = pos > 0 ? pos / ratio : 0;
+  const int64_t v = pos > 0 ? pos >> (ratio - 1) : 0;  // ratio 1 or 2
   return v < cap ? v : cap;
 }
 
@@ -101,26 +101,47 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sh) {
   __syncthreads();
   if (lane == 31) sh[warp] = v;
   __syncthreads();
-  int64_t base = 0;
-  for (int w = 0; w < warp; ++w) base += sh[w];
-  return v + base;
+  int64_t w = warp > lane ? sh[lane] : 0;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+  return v + w;
+}
+// Largest i in [0, n) with list[i] <= v (list[0] <= v): a binary search.
+template <class T>
+__device__ __forceinline__ int last_at_most(const T *list, int n, T v) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (list[mid] <= v) lo = mid;
+    else hi = mid;
+  }
+  return lo;
 }
 
+// One block.  The two lists it searches (first row tile of each sequence, first
+// unit of each row tile) are kept in shared memory as far as they fit, as a
+// search in global memory is a chain of L2 round trips.
+constexpr int kListSeq = 1024, kListTile = 2048;
 __global__ void __launch_bounds__(1024) k_chunk_plan(ChunkArgs a, Plan p) {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");  // k_chunk_attn may set itself up
   __shared__ int64_t sh[32];
   __shared__ int64_t carry;
+  __shared__ int32_t l_seq[kListSeq + 1];
+  __shared__ int64_t l_cum[kListTile + 1];
   const int tid = threadIdx.x;
   const csa2_cache &c = a.c;
-  if (tid == 0) carry = 0;
-  __syncthreads();
+  int32_t *seq_tile = c.batch <= kListSeq ? l_seq : p.seq_tile;
+  if (tid == 0) {
+    carry = 0;
+    seq_tile[0] = 0;
+  }
   for (int b0 = 0; b0 < c.batch; b0 += 1024) {  // row tiles of each sequence
     const int b = b0 + tid;
     int first = 0, n = 0;
     if (b < c.batch && !ragged_rows(a.cu, b, a.total, a.max_new, first, n)) raise_err(a.err, CSA2_DEVERR_INDEX);
     const int64_t rt = (static_cast<int64_t>(n) * a.heads + kRows - 1) / kRows;
     const int64_t incl = block_scan(rt, sh) + carry;
-    if (b < c.batch) p.seq_tile[b + 1] = static_cast<int32_t>(min(incl, static_cast<int64_t>(p.max_tiles)));
-    if (b == 0) p.seq_tile[0] = 0;
+    if (b < c.batch) seq_tile[b + 1] = static_cast<int32_t>(min(incl, static_cast<int64_t>(p.max_tiles)));
     __syncthreads();
     if (tid == 1023) carry = incl;
     __syncthreads();
@@ -128,41 +149,46 @@ __global__ void __launch_bounds__(1024) k_chunk_plan(ChunkArgs a, Plan p) {
   // overlapping sequences (a broken cu) may ask for more row tiles than there are rows
   if (tid == 0 && carry > p.max_tiles) raise_err(a.err, CSA2_DEVERR_INDEX);
   const int n_tiles = static_cast<int>(min(carry, static_cast<int64_t>(p.max_tiles)));
+  const bool fits = n_tiles <= kListTile;
+  int64_t *cum = fits ? l_cum : p.cum;
   __syncthreads();
-  if (tid == 0) carry = 0;
+  if (tid == 0) {
+    carry = 0;
+    cum[0] = 0;
+    p.cum[0] = 0;
+  }
   __syncthreads();
   for (int t0 = 0; t0 < n_tiles; t0 += 1024) {
     const int t = t0 + tid;
     int64_t units = 0;
     if (t < n_tiles) {
-      int lo = 0, hi = c.batch;  // seq_tile[lo] <= t < seq_tile[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.seq_tile[mid] <= t) lo = mid;
-        else hi = mid;
-      }
+      const int b = last_at_most(seq_tile, c.batch, t);
       int first, n;
-      ragged_rows(a.cu, lo, a.total, a.max_new, first, n);
-      const int64_t r0 = static_cast<int64_t>(t - p.seq_tile[lo]) * kRows;  // within the sequence
+      ragged_rows(a.cu, b, a.total, a.max_new, first, n);
+      const int64_t P = c.n_tokens[b] - n;
+      const int64_t r0 = static_cast<int64_t>(t - seq_tile[b]) * kRows;  // within the sequence
       const int64_t left = static_cast<int64_t>(n) * a.heads - r0;
+      // (rows of a call fit 31 bits: total is at most 2^24, heads 2^7)
+      const uint32_t tok0 = static_cast<uint32_t>(r0) / static_cast<uint32_t>(a.heads);
       RowTile x{};
-      x.seq = lo;
+      x.seq = b;
       x.nrows = static_cast<int>(left < kRows ? left : kRows);
       x.row0 = static_cast<int64_t>(first) * a.heads + r0;
-      x.head0 = static_cast<int>(r0 % a.heads);
-      const int tok0 = static_cast<int>(r0 / a.heads), tok1 = static_cast<int>((r0 + x.nrows - 1) / a.heads);
-      const int64_t P = c.n_tokens[lo] - n;
+      x.head0 = static_cast<int>(r0 - static_cast<int64_t>(tok0) * a.heads);
+      const uint32_t tok1 = tok0 + static_cast<uint32_t>(x.head0 + x.nrows - 1) / static_cast<uint32_t>(a.heads);
       x.pos0 = P + tok0;
-      x.win0 = static_cast<int64_t>(first) + static_cast<int64_t>(kWin) * lo + tok0 + 1;
+      x.win0 = static_cast<int64_t>(first) + static_cast<int64_t>(kWin) * b + tok0 + 1;
       x.T = static_cast<int>(visible(P + tok1, c.ratio, c.capacity));
-      x.nkeys = x.T + kWin + (tok1 - tok0);
+      x.nkeys = x.T + kWin + static_cast<int>(tok1 - tok0);
       x.ntiles = (x.nkeys + kKeys - 1) / kKeys;
       p.tile[t] = x;
       units = x.ntiles + 1;
     }
     const int64_t incl = block_scan(units, sh) + carry;
-    if (t < n_tiles) p.cum[t + 1] = incl;
-    if (t == 0) p.cum[0] = 0;
+    if (t < n_tiles) {
+      p.cum[t + 1] = incl;
+      if (fits) cum[t + 1] = incl;
+    }
     __syncthreads();
     if (tid == 1023) carry = incl;
     __syncthreads();
@@ -172,16 +198,18 @@ __global__ void __launch_bounds__(1024) k_chunk_plan(ChunkArgs a, Plan p) {
   const int64_t g_eff = max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.n_cta), (W + 1) / 2));
   for (int g = tid; g < p.n_cta; g += 1024) {
     CtaRange r{};
-    if (g < g_eff) {
+    r.first = -1;
+    if (g < g_eff && W > 0) {
       r.lo = W * g / g_eff;
       r.hi = W * (g + 1) / g_eff;
-      int lo = 0, hi = n_tiles;  // cum[lo] <= r.lo < cum[hi]
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.cum[mid] <= r.lo) lo = mid;
-        else hi = mid;
+      r.tile = last_at_most<int64_t>(cum, n_tiles, r.lo);
+      const int64_t c0 = cum[r.tile], nt = cum[r.tile + 1] - c0 - 1;
+      if (r.lo > c0 && r.lo < c0 + nt && r.hi >= c0 + nt) {
+        int first = static_cast<int>(c0 * g_eff / W);  // the CTA of unit c0, give or take a rounding
+        while (first > 0 && W * first / g_eff > c0) --first;
+        while (W * (first + 1) / g_eff <= c0) ++first;
+        r.first = first;
       }
-      r.tile = lo;
     }
     p.cta[g] = r;
   }
@@ -519,21 +547,6 @@ __device__ __forceinline__ void tail_key(const ChunkArgs &a, const RowTile &x, i
     k.rope_scales = fp8 ? k.scales + 16 : nullptr;
   }
 }
-__device__ __forceinline__ int tail_sigma(const TailKey &k, int o) {
-  int e8 = 0;
-  uint32_t bf = 0;
-  if (k.kind == 2) {
-    e8 = e8m0_top(ldg16(k.scales));
-    bf = bf16_top(ldg16(k.rope + 16 * o), 0);
-  } else if (k.kind == 3) {
-    e8 = max(e8m0_top(ldg16(k.scales)), static_cast<int>(max(k.rope_scales[0], k.rope_scales[1])));
-  } else if (k.kind == 4) {
-#pragma unroll
-    for (int i = 0; i < 9; ++i) bf = bf16_top(ldg16(k.codes + 144 * o + 16 * i), bf);
-  }
-  bf = key_max(bf);
-  return k.kind >= 2 ? sigma_of(key_exponent(e8, bf)) : 0;
-}
 struct RawTail {
   uint4 w[2];
   uint32_t sc;
@@ -587,20 +600,37 @@ __device__ __forceinline__ int64_t whole_tile(const csa2_cache &c, int seq, int 
   return entry_at(c, seq, kt * kKeys);
 }
 
-__device__ __noinline__ void fill_tail(const ChunkArgs &a, uint8_t (*k)[kBlk], float2 *sg, const RowTile &x, int64_t j0, int pt) {
-  const int key = pt >> 3, o = pt & 7;
+// All of a thread's part is requested at once, before the wait for the buffer.
+__device__ __noinline__ bool fill_tail(const ChunkArgs &a, ChunkSmem &sm, const RowTile &x, int64_t j0, uint32_t n, int pt, bool dead) {
+  const int key = pt >> 3, o = pt & 7, b = n & 1;
   TailKey t;
   tail_key(a, x, j0 + key, t);
-  RawTail r;
-  tail_load(t, 0, o, r);
-  const int sigma = tail_sigma(t, o);
-  if (o == 0) sg[key] = t.kind ? make_float2(static_cast<float>(sigma), pow2f(sigma)) : make_float2(-INFINITY, 0.0f);
-#pragma unroll 1
-  for (int s = 0; s < 5; ++s) {
-    const RawTail now = r;
-    if (s < 4) tail_load(t, s + 1, o, r);
-    tail_store(k, t, s, key, o, now, sigma);
+  RawTail r[5];
+#pragma unroll
+  for (int s = 0; s < 5; ++s) tail_load(t, s, o, r[s]);
+  int e8 = 0;
+  uint32_t bf = 0;
+  if (t.kind == 2) {
+    e8 = e8m0_top(ldg16(t.scales));
+    bf = bf16_top(r[4].w[0], 0);
+  } else if (t.kind == 3) {
+    e8 = max(e8m0_top(ldg16(t.scales)), static_cast<int>(max(__ldg(t.rope_scales), __ldg(t.rope_scales + 1))));
+  } else if (t.kind == 4) {
+    bf = bf16_top(r[4].w[0], 0);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) bf = bf16_top(r[s].w[1], bf16_top(r[s].w[0], bf));
   }
+  bf = key_max(bf);
+  const int sigma = t.kind >= 2 ? sigma_of(key_exponent(e8, bf)) : 0;
+  if (n >= 2 && !dead) dead = !wait_warp(&sm.empty[b], ((n >> 1) & 1) ^ 1, a.err);
+  if (pt == 0) {
+    *const_cast<volatile uint32_t *>(&sm.progress) = n;
+    sm.plain[b] = 0;
+  }
+  if (o == 0) sm.sg[b][key] = t.kind ? make_float2(static_cast<float>(sigma), pow2f(sigma)) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+  for (int s = 0; s < 5; ++s) tail_store(sm.k[b], t, s, key, o, r[s], sigma);
+  return dead;
 }
 
 // The producer warps: tile n into buffer n % 2 once the PV that read it last is
@@ -632,12 +662,12 @@ __device__ __forceinline__ void produce(const ChunkArgs &a, const Plan &p, Chunk
   for (uint32_t n = 0; cur.base != kNoTile; ++n) {
     const int b = n & 1;
     const TileRef next = ring_get(sm, n + 1, a.err);
-    if (n >= 2 && !dead) dead = !wait_warp(&sm.empty[b], ((n >> 1) & 1) ^ 1, a.err);
-    if (pt == 0) {
-      *const_cast<volatile uint32_t *>(&sm.progress) = n;
-      sm.plain[b] = cur.base >= 0 && IsFp4<Raw>::v;
-    }
     if (cur.base >= 0) {
+      if (n >= 2 && !dead) dead = !wait_warp(&sm.empty[b], ((n >> 1) & 1) ^ 1, a.err);
+      if (pt == 0) {
+        *const_cast<volatile uint32_t *>(&sm.progress) = n;
+        sm.plain[b] = IsFp4<Raw>::v;
+      }
       const int sigma = raw_sigma(raw);
       if (o == 0) sm.sg[b][key] = make_float2(static_cast<float>(sigma), pow2f(sigma));
 #pragma unroll
@@ -646,7 +676,7 @@ __device__ __forceinline__ void produce(const ChunkArgs &a, const Plan &p, Chunk
         if (next.base >= 0) load_step(c, next.base + key, o, s, raw);
       }
     } else {
-      fill_tail(a, sm.k[b], sm.sg[b], p.tile[cur.t], static_cast<int64_t>(cur.kt) * kKeys, pt);
+      dead = fill_tail(a, sm, p.tile[cur.t], static_cast<int64_t>(cur.kt) * kKeys, n, pt, dead);
       raw = Raw{};
       if (next.base >= 0) {
 #pragma unroll
@@ -666,17 +696,17 @@ __device__ __forceinline__ void produce(const ChunkArgs &a, const Plan &p, Chunk
 __device__ __noinline__ void load_query(const ChunkArgs &a, const RowTile &x, ChunkSmem &sm, int warp, int lane) {
   constexpr int kPer = kDqk / 2 / 32;  // 9 words per lane
 #pragma unroll 1
-  for (int j0 = 0; j0 < kRows / kSmWarps; j0 += 2) {
-    uint32_t raw[2][kPer];
+  for (int j0 = 0; j0 < kRows / kSmWarps; j0 += 4) {
+    uint32_t raw[4][kPer];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < 4; ++j) {
       const int r = warp * (kRows / kSmWarps) + j0 + j;
       const uint32_t *src = reinterpret_cast<const uint32_t *>(a.q + (x.row0 + r) * kDqk);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) raw[j][i] = r < x.nrows ? __ldg(src + lane + 32 * i) : 0u;
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < 4; ++j) {
       const int r = warp * (kRows / kSmWarps) + j0 + j;
       uint32_t m = 0;
 #pragma unroll
@@ -1047,8 +1077,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunk_attn(const __grid_constan
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   ChunkSmem &sm = *reinterpret_cast<ChunkSmem *>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const CtaRange r = p.cta[blockIdx.x];
-  if (r.hi <= r.lo) return;  // the whole CTA
   if (warp == kMmaWarp) {
     tc::tmem_alloc(&sm.tmem, 512);
     tc::tmem_relinquish();
@@ -1070,6 +1098,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunk_attn(const __grid_constan
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = sm.tmem;
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the plan is written
   if (warp < kSmWarps) {
     softmax(a, p, sm, tmem, warp, lane);
   } else if (warp < kMmaWarp) {
@@ -1088,52 +1118,74 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunk_attn(const __grid_constan
   }
 }
 
-// Row tiles shared by several CTAs: block (g, y) joins the one that ends in CTA
-// g, rows 4 (y % 16) .. of dims 128 (y / 16) .., its parts in CTA order.
-__global__ void __launch_bounds__(128) k_chunk_merge(ChunkArgs a, Plan p) {
-  const int g = blockIdx.x, blk = blockIdx.y / 16, i4 = blockIdx.y % 16, d = threadIdx.x;
-  Items it(p, g);
-  if (!it.next(p, g) || it.k0 == 0 || it.k1 != it.x(p)->ntiles) return;
-  const RowTile &x = *it.x(p);
-  const int64_t c0 = p.cum[it.t];
-  if (4 * i4 >= x.nrows) return;
-  int g0 = g;  // the CTA that holds the row tile's first key tile
-  while (g0 > 0 && p.cta[g0].lo > c0) --g0;
-  float m[4], l[4], o[4];
+// Row tiles shared by several CTAs: block (g, y) joins rows 8 y .. + 7 of the one
+// that ends in CTA g, its parts in CTA order (part k is CTA first + k's).
+constexpr int kMaxCta = 256;
+__global__ void __launch_bounds__(256) k_chunk_merge(ChunkArgs a, Plan p) {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  __shared__ float wt[kMaxCta][8];
+  const int g = blockIdx.x, y = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const CtaRange cr = p.cta[g];
+  if (cr.first < 0) return;
+  const RowTile &x = p.tile[cr.tile];
+  const int nrows = x.nrows, n = g - cr.first + 1;
+  if (8 * y >= nrows) return;
+  const int64_t row0 = x.row0;
+  // the first part is the last item of its CTA (slot 1), the others the first of theirs (slot 0)
+  const float *part0 = p.part + (2 * cr.first + 1) * kPartFloats, *part1 = p.part + 2 * (cr.first + 1) * kPartFloats;
+  auto part = [&](int k) { return k == 0 ? part0 : part1 + 2 * static_cast<int64_t>(k - 1) * kPartFloats; };
+  {  // warp = row: the parts' weights, normalised
+    const int r = 8 * y + warp;
+    float m = -INFINITY, l = 0.0f;
+    for (int k = lane; k < n; k += 32) m = fmaxf(m, part(k)[kLat * kRows + 2 * r]);
 #pragma unroll
-  for (int r = 0; r < 4; ++r) m[r] = -INFINITY, l[r] = 0.0f, o[r] = 0.0f;
-  for (int k = g0; k <= g; ++k) {  // the reference of the whole row
-    const float *ml = p.part + (2 * k + (k == g0 ? 1 : 0)) * kPartFloats + kLat * kRows + 8 * i4;
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int k = lane; k < n; k += 32) {
+      const float2 ml = *reinterpret_cast<const float2 *>(part(k) + kLat * kRows + 2 * r);
+      const float w = ml.x == -INFINITY ? 0.0f : ex2(ml.x - m);
+      wt[k][warp] = w;
+      l = fmaf(w, ml.y, l);
+    }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) m[r] = fmaxf(m[r], ml[2 * r]);
+    for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    float f = 1.0f;
+    if (a.sink != nullptr) {
+      const float z = a.sink[(x.head0 + r) % a.heads] * kLog2e, mf = fmaxf(m, z);
+      f = m == -INFINITY ? 0.0f : ex2(m - mf);
+      l = l * f + ex2(z - mf);
+      m = mf;
+    }
+    f = l > 0.0f ? f / l : 0.0f;
+    for (int k = lane; k < n; k += 32) wt[k][warp] *= f;
+    if (lane == 0 && r < nrows) a.lse[row0 + r] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
-  for (int k = g0; k <= g; ++k) {
-    const float *part = p.part + (2 * k + (k == g0 ? 1 : 0)) * kPartFloats, *ml = part + kLat * kRows + 8 * i4;
-    const float4 v = *reinterpret_cast<const float4 *>(part + ((blk * 16 + i4) * 128 + d) * 4);
-    const float vv[4] = {v.x, v.y, v.z, v.w};
+  __syncthreads();
+  // thread = one dim of each 128-dim block, four rows
+  const int d = threadIdx.x & 127, half = threadIdx.x >> 7, i4 = 2 * y + half;
+  float o[4][4] = {};
+#pragma unroll 2
+  for (int k = 0; k < n; ++k) {
+    const float *q = part(k) + (i4 * 128 + d) * 4;
+    const float4 w = *reinterpret_cast<const float4 *>(&wt[k][4 * half]);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float w = ml[2 * r] == -INFINITY ? 0.0f : ex2(ml[2 * r] - m[r]);
-      l[r] = fmaf(w, ml[2 * r + 1], l[r]);
-      o[r] = w == 0.0f ? o[r] : fmaf(w, vv[r], o[r]);
+    for (int b = 0; b < 4; ++b) {
+      const float4 v = *reinterpret_cast<const float4 *>(q + b * 16 * 128 * 4);
+      o[b][0] = w.x == 0.0f ? o[b][0] : fmaf(w.x, v.x, o[b][0]);
+      o[b][1] = w.y == 0.0f ? o[b][1] : fmaf(w.y, v.y, o[b][1]);
+      o[b][2] = w.z == 0.0f ? o[b][2] : fmaf(w.z, v.z, o[b][2]);
+      o[b][3] = w.w == 0.0f ? o[b][3] : fmaf(w.w, v.w, o[b][3]);
     }
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int row = 4 * i4 + r;
-    if (row >= x.nrows) break;
-    float f = 1.0f;
-    if (a.sink != nullptr) {
-      const float z = a.sink[(x.head0 + row) % a.heads] * kLog2e, mf = fmaxf(m[r], z);
-      f = m[r] == -INFINITY ? 0.0f : ex2(m[r] - mf);
-      l[r] = l[r] * f + ex2(z - mf);
-      m[r] = mf;
+    if (row >= nrows) break;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int64_t at = (row0 + row) * kLat + 128 * b + d;
+      if (a.bf16) static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(o[b][r]);
+      else static_cast<float *>(a.out)[at] = o[b][r];
     }
-    const float v = l[r] > 0.0f ? o[r] * (f / l[r]) : 0.0f;
-    const int64_t at = (x.row0 + row) * kLat + 128 * blk + d;
-    if (a.bf16) static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(v);
-    else static_cast<float *>(a.out)[at] = v;
-    if (d == 0 && blk == 0) a.lse[x.row0 + row] = l[r] > 0.0f ? (m[r] + log2f(l[r])) * kLn2 : -INFINITY;
   }
 }
 
@@ -1146,7 +1198,7 @@ PlanLayout plan_layout(int batch, int total, int heads) {
   auto up = [](size_t b) { return (b + 255) & ~size_t(255); };
   const int64_t t = static_cast<int64_t>(total) * heads / kRows + (batch < total ? batch : total) + 1;
   L.max_tiles = static_cast<int>(t);
-  L.n_cta = device_sm_count();
+  L.n_cta = device_sm_count() < kMaxCta ? device_sm_count() : kMaxCta;
   size_t o = 0;
   L.seq_tile = o;
   o = up(o + (static_cast<size_t>(batch) + 1) * 4);
@@ -1212,9 +1264,28 @@ csa2_status csa2_chunk_attn(const csa2_cache *cache, const uint16_t *q, int32_t 
   if (e != cudaSuccess) return cuda_status(e, "csa2_chunk_attn shared memory");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   csa2::k_chunk_plan<<<1, 1024, 0, s>>>(a, p);
-  csa2::k_chunk_attn<<<L.n_cta, csa2::kThreads, smem, s>>>(a, p);
-  csa2::k_chunk_merge<<<dim3(L.n_cta, 64), 128, 0, s>>>(a, p);
-  return cuda_status(cudaGetLastError(), "csa2_chunk_attn launch");
+  e = cudaGetLastError();
+  // each of the next two may set itself up while the one before still runs
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (e == cudaSuccess) {
+    cfg.gridDim = dim3(L.n_cta);
+    cfg.blockDim = dim3(csa2::kThreads);
+    cfg.dynamicSmemBytes = smem;
+    e = cudaLaunchKernelEx(&cfg, csa2::k_chunk_attn, a, p);
+  }
+  if (e == cudaSuccess) {
+    cfg.gridDim = dim3(L.n_cta, csa2::kRows / 8);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    e = cudaLaunchKernelEx(&cfg, csa2::k_chunk_merge, a, p);
+  }
+  return cuda_status(e, "csa2_chunk_attn launch");
 }
 
 }  // extern "C"
