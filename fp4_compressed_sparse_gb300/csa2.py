@@ -398,49 +398,54 @@ def mask_to_pool(scores, ratio, q_pos, pool, pool_block_size=8, stream=None):
 
 # --------------------------------------------------------------------------- ragged batches
 def _want(name, t, dtype, shape=None, like=None):
-    """Raise ValueError unless t is a contiguous device tensor of dtype (and shape; -1: any size)."""
+    """Raise ValueError unless t is a contiguous device tensor of dtype (and shape; -1: any size), on like's device."""
     if t is None or not t.is_cuda:
         raise ValueError(f"{name}: a CUDA tensor is needed")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
         raise ValueError(f"{name}: {t.dtype}, {dtype} is needed")
-    if shape is not None and (t.dim() != len(shape) or any(w not in (-1, n) for w, n in zip(shape, t.shape))):
+    if shape is not None and t.shape != shape and (
+            t.dim() != len(shape) or any(w not in (-1, n) for w, n in zip(shape, t.shape))):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, {tuple(shape)} is needed")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
-    if like is not None and t.device != like.device:
+    if like is not None and t.get_device() != like.get_device():
         raise ValueError(f"{name} is on {t.device}, the cache on {like.device}")
 
 
 def _want_rows(name, t, dtype, width, like, total=None):
     """Raise ValueError unless t holds rows of `width` elements, contiguous within a row; returns the row stride."""
-    if t is None or not t.is_cuda or t.device != like.device:
+    if t is None or not t.is_cuda or t.get_device() != like.get_device():
         raise ValueError(f"{name}: a tensor on {like.device} is needed")
     if t.dtype not in dtype:
         raise ValueError(f"{name}: {t.dtype}, one of {dtype} is needed")
     if t.dim() != 2 or t.shape[1] != width or (total is not None and t.shape[0] != total):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, ({'rows' if total is None else total}, {width}) is needed")
-    if t.stride(1) != 1 or (t.shape[0] > 1 and t.stride(0) < width):
+    if t.shape[0] <= 1:
+        return width
+    row, one = t.stride()
+    if one != 1 or row < width:
         raise ValueError(f"{name}: rows must be contiguous and not overlap")
-    return t.stride(0) if t.shape[0] > 1 else width
+    return row
 
 
 def _out_dtype(t):
-    return OUT_BF16 if t.dtype == torch.bfloat16 else OUT_F32
+    return OUT_BF16 if t.dtype is torch.bfloat16 else OUT_F32
 
 
-class _on:
-    """The cache's device as the current one for a call, and its current stream unless one is given."""
+def _adr(t):
+    return None if t is None else t.data_ptr()
 
-    def __init__(self, cache, stream):
-        self.dev, self.stream = cache.n_tokens.device, stream
 
-    def __enter__(self):
-        self.ctx = torch.cuda.device(self.dev)
-        self.ctx.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *exc):
-        return self.ctx.__exit__(*exc)
+def _call(fn, cache, stream, *args):
+    """fn(cache, *args, stream) with the cache's device as the current one, on its current stream unless one is given."""
+    f, dev = getattr(_lib or load(), fn), cache.n_tokens.get_device()
+    if dev == torch.cuda.current_device():
+        s = stream if stream is not None else torch.cuda.current_stream()
+        _check(fn, f(cache.ref(), *args, s.cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            s = stream if stream is not None else torch.cuda.current_stream()
+            _check(fn, f(cache.ref(), *args, s.cuda_stream))
 
 
 class ChunkWindow:
@@ -466,7 +471,10 @@ def _window_ptrs(cache, win, total):
     _want("win.codes", win.codes, torch.uint8, (rows, 576 if cache.swa_dtype == SWA_MXFP8 else 1152), cache.n_tokens)
     if cache.swa_dtype == SWA_MXFP8:
         _want("win.scales", win.scales, torch.uint8, (rows, 32), cache.n_tokens)
-    return _ptr(win.codes), _ptr(win.scales)
+    return _adr(win.codes), _adr(win.scales)
+
+
+_FLOATS = (torch.float32, torch.bfloat16)
 
 
 def kv_append_ragged(cache: Cache, cu_new, rope_cs, kv=None, idx_key=None, cmp=None, max_new=None, win=None, err=None,
@@ -482,23 +490,20 @@ def kv_append_ragged(cache: Cache, cu_new, rope_cs, kv=None, idx_key=None, cmp=N
     if cache.ratio == 1:
         if cmp is not None:
             raise ValueError("cmp is for ratio-2 caches")
-        ks = _want_rows("kv", kv, (torch.float32, torch.bfloat16), 576, like)
+        ks = _want_rows("kv", kv, _FLOATS, 576, like)
         total = kv.shape[0]
         is_ = _want_rows("idx_key", idx_key, (kv.dtype,), 128, like, total)
-        dt = IN_BF16 if kv.dtype == torch.bfloat16 else IN_F32
+        dt = IN_BF16 if kv.dtype is torch.bfloat16 else IN_F32
     else:
         if cmp is None or kv is not None or idx_key is not None:
             raise ValueError("a ratio-2 cache takes cmp rows, and no kv or idx_key")
         total = cmp[0].shape[0]
         for i, t in enumerate(cmp):
             _want(f"cmp[{i}]", t, torch.float32, (total, D_CMP) if i < 4 else (2, D_CMP), like)
-        cin = CompressIn(*[t.data_ptr() for t in cmp])
+        cin = ctypes.byref(CompressIn(*[t.data_ptr() for t in cmp]))
     wc, ws = _window_ptrs(cache, win, total)
-    with _on(cache, stream) as s:
-        _check("csa2_kv_append_ragged", load().csa2_kv_append_ragged(
-            cache.ref(), _ptr(kv), ks, _ptr(idx_key), is_, dt, ctypes.byref(cin) if cin is not None else None,
-            _ptr(cu_new), total, total if max_new is None else max_new, _ptr(rope_cs), rope_cs.shape[0], wc, ws,
-            _ptr(err), s))
+    _call("csa2_kv_append_ragged", cache, stream, _adr(kv), ks, _adr(idx_key), is_, dt, cin, _adr(cu_new), total,
+          total if max_new is None else max_new, _adr(rope_cs), rope_cs.shape[0], wc, ws, _adr(err))
 
 
 def kv_read(cache: Cache, cu_rows, out_main=None, out_key=None, pos=None, start=None, err=None, stream=None):
@@ -512,26 +517,23 @@ def kv_read(cache: Cache, cu_rows, out_main=None, out_key=None, pos=None, start=
         raise ValueError("out_main or out_key is needed")
     total, ms, ks = first.shape[0], 0, 0
     if out_main is not None:
-        ms = _want_rows("out_main", out_main, (torch.float32, torch.bfloat16), 576, like)
+        ms = _want_rows("out_main", out_main, _FLOATS, 576, like)
     if out_key is not None:
-        ks = _want_rows("out_key", out_key, (first.dtype,) if out_main is not None else (torch.float32, torch.bfloat16),
-                        128, like, total)
+        ks = _want_rows("out_key", out_key, (first.dtype,) if out_main is not None else _FLOATS, 128, like, total)
     if (pos is None) == (start is None):
         raise ValueError("one of pos and start is needed")
     if pos is not None:
         _want("pos", pos, torch.int32, (total,), like)
     else:
         _want("start", start, torch.int64, (cache.batch,), like)
-    with _on(cache, stream) as s:
-        _check("csa2_kv_read", load().csa2_kv_read(cache.ref(), _ptr(cu_rows), total, _ptr(pos), _ptr(start),
-                                                   _ptr(out_main), ms, _ptr(out_key), ks, _out_dtype(first), _ptr(err), s))
+    _call("csa2_kv_read", cache, stream, _adr(cu_rows), total, _adr(pos), _adr(start), _adr(out_main), ms, _adr(out_key),
+          ks, _out_dtype(first), _adr(err))
 
 
 def window_read(cache: Cache, out, stream=None):
     """csa2_window_read: out [B,128,576] (fp32 or bf16), row i = token n_tokens - 128 + i (zeros before token 0)."""
-    _want("out", out, (torch.float32, torch.bfloat16), (cache.batch, WINDOW, D_QK), cache.n_tokens)
-    with _on(cache, stream) as s:
-        _check("csa2_window_read", load().csa2_window_read(cache.ref(), _ptr(out), _out_dtype(out), s))
+    _want("out", out, _FLOATS, (cache.batch, WINDOW, D_QK), cache.n_tokens)
+    _call("csa2_window_read", cache, stream, _adr(out), _out_dtype(out))
 
 
 def chunk_attn_workspace(total, heads, batch, device="cuda"):
@@ -546,18 +548,16 @@ def chunk_attn(cache: Cache, q, cu_q, out, lse, ws, sm_scale, max_new=None, win=
     enough for single tokens).  ws: chunk_attn_workspace()."""
     like = cache.n_tokens
     _want("q", q, torch.bfloat16, (-1, -1, D_QK), like)
-    total, H = q.shape[0], q.shape[1]
+    total, H, _ = q.shape
     _want("cu_q", cu_q, torch.int32, (cache.batch + 1,), like)
-    _want("out", out, (torch.float32, torch.bfloat16), (total, H, D_LATENT), like)
+    _want("out", out, _FLOATS, (total, H, D_LATENT), like)
     _want("lse", lse, torch.float32, (total, H), like)
     _want("ws", ws, torch.uint8, None, like)
     if sink is not None:
         _want("sink", sink, torch.float32, (H,), like)
     wc, wsc = _window_ptrs(cache, win, total)
-    with _on(cache, stream) as s:
-        _check("csa2_chunk_attn", load().csa2_chunk_attn(
-            cache.ref(), _ptr(q), H, _ptr(cu_q), total, total if max_new is None else max_new, wc, wsc, _ptr(sink),
-            float(sm_scale), _ptr(out), _out_dtype(out), _ptr(lse), _ptr(ws), ws.numel(), _ptr(err), s))
+    _call("csa2_chunk_attn", cache, stream, _adr(q), H, _adr(cu_q), total, total if max_new is None else max_new, wc, wsc,
+          _adr(sink), sm_scale, _adr(out), _out_dtype(out), _adr(lse), _adr(ws), ws.numel(), _adr(err))
 
 
 # --------------------------------------------------------------------------- measurement helpers

@@ -601,10 +601,10 @@ __device__ __forceinline__ int64_t whole_tile(const csa2_cache &c, int seq, int 
 }
 
 // All of a thread's part is requested at once, before the wait for the buffer.
-__device__ __noinline__ bool fill_tail(const ChunkArgs &a, ChunkSmem &sm, const RowTile &x, int64_t j0, uint32_t n, int pt, bool dead) {
+__device__ __noinline__ bool fill_tail(const ChunkArgs &a, const Plan &p, ChunkSmem &sm, uint32_t n, int pt, bool dead) {
   const int key = pt >> 3, o = pt & 7, b = n & 1;
   TailKey t;
-  tail_key(a, x, j0 + key, t);
+  tail_key(a, p.tile[sm.ring[n % kRing].t], static_cast<int64_t>(sm.ring[n % kRing].kt) * kKeys + key, t);
   RawTail r[5];
 #pragma unroll
   for (int s = 0; s < 5; ++s) tail_load(t, s, o, r[s]);
@@ -636,17 +636,16 @@ __device__ __noinline__ bool fill_tail(const ChunkArgs &a, ChunkSmem &sm, const 
 // The producer warps: tile n into buffer n % 2 once the PV that read it last is
 // complete.  Which tiles, and where they lie, they are told through the ring:
 // a page-table load of their own would wait behind the records' loads.
-__device__ __forceinline__ TileRef ring_get(const ChunkSmem &sm, uint32_t n, int32_t *err) {
+__device__ __forceinline__ int64_t ring_base(const ChunkSmem &sm, uint32_t n, int32_t *err) {
   const volatile uint32_t *listed = &sm.listed;
   uint32_t i = 0;
   while (*listed <= n && i < kPolls) ++i;
   if (*listed <= n) {
     raise_err(err, CSA2_DEVERR_TIMEOUT);
-    return TileRef{kNoTile, 0, 0};
+    return kNoTile;
   }
   __threadfence_block();
-  const volatile TileRef *r = &sm.ring[n % kRing];
-  return TileRef{r->base, r->t, r->kt};
+  return *const_cast<const volatile int64_t *>(&sm.ring[n % kRing].base);
 }
 template <class Raw>
 __device__ __forceinline__ void produce(const ChunkArgs &a, const Plan &p, ChunkSmem &sm, int pt) {
@@ -654,15 +653,16 @@ __device__ __forceinline__ void produce(const ChunkArgs &a, const Plan &p, Chunk
   const int key = pt >> 3, o = pt & 7;
   bool dead = false;
   Raw raw;
-  TileRef cur = ring_get(sm, 0, a.err);
-  if (cur.base >= 0) {
+  int64_t base = ring_base(sm, 0, a.err);
+  if (base >= 0) {
 #pragma unroll
-    for (int s = 0; s < 5; ++s) load_step(c, cur.base + key, o, s, raw);
+    for (int s = 0; s < 5; ++s) load_step(c, base + key, o, s, raw);
   }
-  for (uint32_t n = 0; cur.base != kNoTile; ++n) {
+  for (uint32_t n = 0; base != kNoTile; ++n) {
     const int b = n & 1;
-    const TileRef next = ring_get(sm, n + 1, a.err);
-    if (cur.base >= 0) {
+    const bool whole = base >= 0;
+    base = ring_base(sm, n + 1, a.err);
+    if (whole) {
       if (n >= 2 && !dead) dead = !wait_warp(&sm.empty[b], ((n >> 1) & 1) ^ 1, a.err);
       if (pt == 0) {
         *const_cast<volatile uint32_t *>(&sm.progress) = n;
@@ -673,20 +673,19 @@ __device__ __forceinline__ void produce(const ChunkArgs &a, const Plan &p, Chunk
 #pragma unroll
       for (int s = 0; s < 5; ++s) {
         store_step(sm.k[b], s, key, o, raw, sigma);
-        if (next.base >= 0) load_step(c, next.base + key, o, s, raw);
+        if (base >= 0) load_step(c, base + key, o, s, raw);
       }
     } else {
-      dead = fill_tail(a, sm, p.tile[cur.t], static_cast<int64_t>(cur.kt) * kKeys, n, pt, dead);
+      dead = fill_tail(a, p, sm, n, pt, dead);
       raw = Raw{};
-      if (next.base >= 0) {
+      if (base >= 0) {
 #pragma unroll
-        for (int s = 0; s < 5; ++s) load_step(c, next.base + key, o, s, raw);
+        for (int s = 0; s < 5; ++s) load_step(c, base + key, o, s, raw);
       }
     }
     tc::fence_proxy_async_smem();
     __syncwarp();
     if ((pt & 31) == 0) tc::mbar_arrive(&sm.full[b]);
-    cur = next;
   }
 }
 
