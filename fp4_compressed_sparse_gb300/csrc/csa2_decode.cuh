@@ -29,21 +29,6 @@ __device__ __forceinline__ void bf16x8(uint4 w, float *v) {
     v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
   }
 }
-// Unit u (values 8u .. 8u + 7: latent units 0..63, then RoPE) of physical entry pe.
-__device__ __forceinline__ void entry_unit8(const csa2_cache &c, int64_t pe, int u, float *v) {
-  if (c.entry_format == CSA2_ENTRY_FP8) {
-    if (u < 64)
-      e4m3x8(reinterpret_cast<const uint2 *>(c.lat_codes + pe * 512)[u], e8m0_value(c.lat_scales[pe * 16 + (u >> 2)]), v);
-    else
-      bf16x8(reinterpret_cast<const uint4 *>(c.rope_codes + pe * 128)[u - 64], v);
-  } else if (u < 64) {
-    e2m1x8(reinterpret_cast<const uint32_t *>(c.lat_codes + pe * 256)[u], e4m3_value(c.lat_scales[pe * 32 + (u >> 1)]), v);
-  } else {
-    e2m1x8(reinterpret_cast<const uint32_t *>(c.rope_codes + pe * 32)[u - 64],
-           e4m3_value(c.rope_scales[pe * 4 + ((u - 64) >> 1)]), v);
-  }
-}
-
 // Unit u of window row `row` (a ring slot or a chunk's window row).
 __device__ __forceinline__ void window_unit8(const uint8_t *codes, const uint8_t *scales, int swa_dtype, int64_t row,
                                              int u, float *v) {

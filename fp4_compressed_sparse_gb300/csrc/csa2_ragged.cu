@@ -20,7 +20,6 @@ struct RaggedAppend {
   csa2_cache c;
   const void *kv, *ik;
   int64_t kv_stride, key_stride;
-  int in_bf16;
   csa2_compress_in cmp;
   const int32_t *cu;
   int total, max_new;
@@ -31,11 +30,6 @@ struct RaggedAppend {
 };
 
 __device__ __forceinline__ int swa_bytes(const csa2_cache &c) { return c.swa_dtype == CSA2_SWA_MXFP8 ? 576 : 1152; }
-
-__device__ __forceinline__ float load_row(const void *p, int64_t i, int in_bf16) {
-  if (in_bf16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[i]);
-  return reinterpret_cast<const float *>(p)[i];
-}
 
 // Compression row `which` of token p of a sequence whose call rows start at
 // `first` (token t0): the call's, or the compression buffer's for older tokens.
@@ -62,33 +56,283 @@ __device__ __forceinline__ void store_cmp_rows(const RaggedAppend &a, int b, int
 
 constexpr int kCopyBlocks = 4;  // blocks that copy one sequence's older window rows
 
-// Blocks 0 .. total-1: one token each (entry, window row).  Further blocks: the
-// 128 older window rows of each sequence.  single: max_new is 1 and there are
-// no window rows to leave, so a token's block also finishes its sequence.
-__global__ void __launch_bounds__(kEncThreads) k_ragged_append(RaggedAppend a, int single) {
+// Part `part` of the window rows of the tokens before the chunk.
+__device__ __forceinline__ void copy_older(const RaggedAppend &a, int part) {
+  const csa2_cache &c = a.c;
+  const int b = part / kCopyBlocks, i0 = (part % kCopyBlocks) * (kWin / kCopyBlocks);
+  int first, n;
+  if (!ragged_rows(a.cu, b, a.total, a.max_new, first, n)) {
+    if (i0 == 0 && threadIdx.x == 0) raise_err(a.err, CSA2_DEVERR_INDEX);
+    return;
+  }
+  const int64_t t0 = c.n_tokens[b] - kWin;
+  const int row16 = swa_bytes(c) / 16;
+  for (int k = threadIdx.x; k < kWin / kCopyBlocks * (row16 + 2); k += blockDim.x) {
+    const int i = i0 + k / (row16 + 2), w = k % (row16 + 2);
+    const int64_t t = t0 + i;
+    const size_t dst = static_cast<size_t>(first) + static_cast<size_t>(kWin) * b + i;
+    const size_t src = static_cast<size_t>(b) * kWin + (t & (kWin - 1));
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    if (w < row16)
+      reinterpret_cast<uint4 *>(a.win_codes)[dst * row16 + w] =
+          t >= 0 ? reinterpret_cast<const uint4 *>(c.swa_codes)[src * row16 + w] : zero;
+    else if (c.swa_dtype == CSA2_SWA_MXFP8)
+      reinterpret_cast<uint4 *>(a.win_scales)[dst * 2 + w - row16] =
+          t >= 0 ? reinterpret_cast<const uint4 *>(c.swa_scales)[src * 2 + w - row16] : zero;
+  }
+}
+
+// ---------------------------------------------------------------- ratio 1: a warp per token
+// Lane l has latent dims 16 l .. + 15 (one NVFP4 group, half an MXFP8 block), RoPE
+// pair l, key dims 4 l .. + 3, all in registers: no shared memory and no block
+// barrier beyond the one after the address phase, in which one thread per token
+// finds where it goes (a chain of dependent loads) for the whole block.
+//
+// 16,384 + 16,384 bf16 tokens in the V4 format: see the figures in the header
+// comment of the launch below.
+
+// Sixteen E2M1 codes of x / s without the divisions: x / s, rounded to fp32, is at
+// most (below) a midpoint t of the grid exactly when x is at most (below) t s.
+// t s is exact (3 + 4 significant bits), and the next fp32 number from t s differs
+// by at least 2^-24 of it, the rounding of the quotient next to t by no more than
+// 2^-24 of t: never enough to carry it over (2^-25 below a power of two).
+__device__ __forceinline__ uint2 nvfp4_16(const float *x, uint32_t *scale) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+  const uint32_t sc = e4m3_code(__fdiv_rn(amax, 6.0f));
+  const float s = e4m3_value(sc);
+  if (s == 0.0f) {
+    *scale = 0;
+    return make_uint2(0, 0);
+  }
+  *scale = sc;
+  // |x| >= T[i] <=> code > i; ties go to the even code, so every other bound is
+  // the number after the midpoint
+  const uint32_t T0 = __float_as_uint(0.25f * s) + 1, T1 = __float_as_uint(0.75f * s), T2 = __float_as_uint(1.25f * s) + 1,
+                 T3 = __float_as_uint(1.75f * s), T4 = __float_as_uint(2.5f * s) + 1, T5 = __float_as_uint(3.5f * s),
+                 T6 = __float_as_uint(5.0f * s) + 1;
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t u = __float_as_uint(x[i]), v = u & 0x7FFFFFFFu;
+    const bool g4 = v >= T3, g2 = v >= (g4 ? T5 : T1);
+    const bool g1 = v >= (g4 ? (g2 ? T6 : T4) : (g2 ? T2 : T0));
+    const uint32_t code = (g4 ? 4u : 0u) | (g2 ? 2u : 0u) | (g1 ? 1u : 0u) | ((u >> 28) & 8u);
+    w[i / 8] |= code << (4 * (i % 8));
+  }
+  return make_uint2(w[0], w[1]);
+}
+// Four E4M3 codes (round to nearest even, saturating), as e4m3_code gives them.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  if (a != a || b != b || c != c || d != d)  // the conversion has another code for NaN
+    return e4m3_code(a) | (e4m3_code(b) << 8) | (e4m3_code(c) << 16) | (e4m3_code(d) << 24);
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(lo) : "f"(b), "f"(a));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(hi) : "f"(d), "f"(c));
+  return lo | (static_cast<uint32_t>(hi) << 16);
+}
+// Exponent and scale code of an MXFP8 block with this largest magnitude.
+__device__ __forceinline__ void mxfp8_scale(float amax, float *inv, uint32_t *sc) {
+  if (amax == 0.0f) {
+    *inv = 0.0f;
+    *sc = 0;
+    return;
+  }
+  const int e = max(-127, min(127, floor_log2f(amax) - 8));
+  *inv = pow2f(-e);
+  *sc = static_cast<uint32_t>(e + 127);
+}
+
+template <bool kBf16>
+struct TokenRow {
+  float x[16];  // latent dims 16 l ..
+  float2 r;     // RoPE dims 2 l, 2 l + 1
+  float4 k;     // key dims 4 l ..
+};
+__device__ __forceinline__ float2 bf2(uint32_t u) { return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u)); }
+template <bool kBf16>
+__device__ __forceinline__ void load_token(const RaggedAppend &a, int64_t r, int lane, TokenRow<kBf16> &t) {
+  if (kBf16) {
+    const __nv_bfloat16 *kv = static_cast<const __nv_bfloat16 *>(a.kv) + r * a.kv_stride;
+    const __nv_bfloat16 *ik = static_cast<const __nv_bfloat16 *>(a.ik) + r * a.key_stride;
+    uint4 v[2];
+    v[0] = __ldg(reinterpret_cast<const uint4 *>(kv + 16 * lane));
+    v[1] = __ldg(reinterpret_cast<const uint4 *>(kv + 16 * lane + 8));
+    const uint32_t rr = __ldg(reinterpret_cast<const uint32_t *>(kv + kLat + 2 * lane));
+    const uint2 kk = __ldg(reinterpret_cast<const uint2 *>(ik + 4 * lane));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = bf2(u[j]);
+        t.x[8 * i + 2 * j] = f.x;
+        t.x[8 * i + 2 * j + 1] = f.y;
+      }
+    }
+    t.r = bf2(rr);
+    const float2 k0 = bf2(kk.x), k1 = bf2(kk.y);
+    t.k = make_float4(k0.x, k0.y, k1.x, k1.y);
+  } else {
+    const float *kv = static_cast<const float *>(a.kv) + r * a.kv_stride;
+    const float *ik = static_cast<const float *>(a.ik) + r * a.key_stride;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = __ldg(reinterpret_cast<const float4 *>(kv + 16 * lane + 4 * i));
+      t.x[4 * i] = v.x, t.x[4 * i + 1] = v.y, t.x[4 * i + 2] = v.z, t.x[4 * i + 3] = v.w;
+    }
+    t.r = __ldg(reinterpret_cast<const float2 *>(kv + kLat + 2 * lane));
+    t.k = __ldg(reinterpret_cast<const float4 *>(ik + 4 * lane));
+  }
+}
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t *>(&t);
+}
+__device__ __forceinline__ float max_over(float v, int lanes) {  // over groups of `lanes` lanes
+  for (int o = 1; o < lanes; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Where a token goes.
+struct TokenPlace {
+  int64_t pe;   // physical entry; -1: nothing is stored (an error, or a row of no sequence)
+  int64_t pt;   // its indexer tile
+  int64_t win;  // row of wcodes / wscales; -1: none
+  int64_t t;
+};
+
+// kTok tokens per warp.  Blocks behind the tokens' copy the older window rows.
+template <bool kBf16, int kTok>
+__global__ void __launch_bounds__(256) k_ragged_append_r1(RaggedAppend a, int single, int token_blocks) {
+  if (static_cast<int>(blockIdx.x) >= token_blocks) {
+    copy_older(a, blockIdx.x - token_blocks);
+    return;
+  }
+  __shared__ TokenPlace place[8 * kTok];
+  const csa2_cache &c = a.c;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int r0 = blockIdx.x * 8 * kTok;
+  // the rows do not depend on their places: the first one is requested at once
+  TokenRow<kBf16> tok;
+  int r = r0 + warp;
+  if (r < a.total) load_token(a, r, lane, tok);
+  if (tid < 8 * kTok) {
+    TokenPlace pl{-1, -1, -1, 0};
+    const int row = r0 + tid;
+    const int b = row < a.total ? ragged_seq(a.cu, c.batch, row) : -1;
+    int first = 0, n = 0;
+    if (b >= 0 && !ragged_rows(a.cu, b, a.total, a.max_new, first, n)) raise_err(a.err, CSA2_DEVERR_INDEX);
+    if (n > 0) {
+      const int64_t t0 = c.n_tokens[b];
+      const int j = row - first;
+      if (!append_ok(c, t0, n, a.rope_len)) {
+        if (j == 0) append_fail(c, t0, n, a.rope_len, a.err);
+      } else {
+        pl.t = t0 + j;
+        pl.pe = phys_entry(entry_map(c), b, pl.t);
+        pl.pt = phys_tile(entry_map(c), b, pl.t / kIdxTile);
+        if (pl.pe < 0) raise_err(a.err, CSA2_DEVERR_INDEX);
+        if (a.win_codes != nullptr) pl.win = static_cast<int64_t>(row) + static_cast<int64_t>(kWin) * (b + 1);
+        else if (j >= n - kWin) pl.win = static_cast<int64_t>(b) * kWin + (pl.t & (kWin - 1));
+        if (single) c.n_tokens[b] = t0 + n;  // (its only token: nobody else reads it)
+      }
+    }
+    place[tid] = pl;
+  }
+  __syncthreads();
+  const bool fp8 = c.entry_format == CSA2_ENTRY_FP8, mx = c.swa_dtype == CSA2_SWA_MXFP8;
+#pragma unroll 1
+  for (int i = 0; i < kTok; ++i, r += 8) {
+    if (r >= a.total) break;
+    const TokenPlace pl = place[warp + 8 * i];
+    TokenRow<kBf16> cur = tok;
+    if (i + 1 < kTok && r + 8 < a.total) load_token(a, r + 8, lane, tok);
+    if (pl.pe < 0 && pl.win < 0) continue;
+    const float2 cs = __ldg(reinterpret_cast<const float2 *>(a.rope_cs + pl.t * 64 + 2 * lane));
+    rope_pair(cur.r.x, cur.r.y, cs.x, cs.y);
+    // E4M3 latents, shared by a V4 entry and an MXFP8 window row
+    uint4 lat8 = make_uint4(0, 0, 0, 0);
+    uint32_t lat8_sc = 0;
+    if ((fp8 && pl.pe >= 0) || (mx && pl.win >= 0)) {
+      float amax = 0.0f, inv;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(cur.x[j]));
+      amax = max_over(amax, 2);
+      mxfp8_scale(amax, &inv, &lat8_sc);
+      if (amax != 0.0f) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = e4m3x4(__fmul_rn(cur.x[4 * j], inv), __fmul_rn(cur.x[4 * j + 1], inv), __fmul_rn(cur.x[4 * j + 2], inv),
+                        __fmul_rn(cur.x[4 * j + 3], inv));
+        lat8 = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    if (pl.pe >= 0) {
+      if (fp8) {
+        *reinterpret_cast<uint4 *>(c.lat_codes + pl.pe * 512 + 16 * lane) = lat8;
+        if ((lane & 1) == 0) c.lat_scales[pl.pe * 16 + (lane >> 1)] = static_cast<uint8_t>(lat8_sc);
+        reinterpret_cast<uint32_t *>(c.rope_codes + pl.pe * 128)[lane] = bf16_pair(cur.r.x, cur.r.y);
+      } else {
+        uint32_t sc;
+        const uint2 w = nvfp4_16(cur.x, &sc);
+        *reinterpret_cast<uint2 *>(c.lat_codes + pl.pe * 256 + 8 * lane) = w;
+        c.lat_scales[pl.pe * 32 + lane] = static_cast<uint8_t>(sc);
+        const uint32_t byte = nvfp4_pair(cur.r.x, cur.r.y, &sc);
+        c.rope_codes[pl.pe * 32 + lane] = static_cast<uint8_t>(byte);
+        if ((lane & 7) == 0) c.rope_scales[pl.pe * 4 + (lane >> 3)] = static_cast<uint8_t>(sc);
+      }
+      // the indexer key, MXFP4: block lane / 8
+      const float x[4] = {cur.k.x, cur.k.y, cur.k.z, cur.k.w};
+      const float amax = max_over(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))), 8);
+      uint32_t codes = 0, sc = 0;
+      if (amax != 0.0f) {
+        const int e = max(-127, min(127, floor_log2f(amax) - 2));
+        const float inv = pow2f(-e);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) codes |= e2m1_code(__fmul_rn(x[j], inv)) << (4 * j);
+        sc = static_cast<uint32_t>(e + 127);
+      }
+      const int m = static_cast<int>(pl.t % kIdxTile), blk = lane >> 3;
+      *reinterpret_cast<uint16_t *>(c.idx_codes + idx_code_at(pl.pt, m, blk) + 2 * (lane & 7)) = static_cast<uint16_t>(codes);
+      if ((lane & 7) == 0) c.idx_scales[idx_scale_at(pl.pt, m) + blk] = static_cast<uint8_t>(sc);
+    }
+    if (pl.win >= 0) {
+      uint8_t *wc = (a.win_codes != nullptr ? a.win_codes : c.swa_codes) + pl.win * (mx ? 576 : 1152);
+      if (mx) {
+        uint8_t *ws = (a.win_codes != nullptr ? a.win_scales : c.swa_scales) + pl.win * kSwaScaleStride;
+        *reinterpret_cast<uint4 *>(wc + 16 * lane) = lat8;
+        if ((lane & 1) == 0) ws[lane >> 1] = static_cast<uint8_t>(lat8_sc);
+        const float amax = max_over(fmaxf(fabsf(cur.r.x), fabsf(cur.r.y)), 16);
+        float inv;
+        uint32_t sc, code = 0;
+        mxfp8_scale(amax, &inv, &sc);
+        if (amax != 0.0f) code = e4m3x4(__fmul_rn(cur.r.x, inv), __fmul_rn(cur.r.y, inv), 0.0f, 0.0f) & 0xFFFFu;
+        reinterpret_cast<uint16_t *>(wc + kLat)[lane] = static_cast<uint16_t>(code);
+        if ((lane & 15) == 0) ws[16 + (lane >> 4)] = static_cast<uint8_t>(sc);
+      } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = bf16_pair(cur.x[2 * j], cur.x[2 * j + 1]);
+        uint4 *d = reinterpret_cast<uint4 *>(wc + 32 * lane);
+        d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        reinterpret_cast<uint32_t *>(wc + 2 * kLat)[lane] = bf16_pair(cur.r.x, cur.r.y);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- ratio 2: a block per token
+// Blocks 0 .. total-1: one token each (its window row and, when it completes a
+// pair, the entry).  single: max_new is 1 and there are no window rows to leave,
+// so a token's block also finishes its sequence.
+__global__ void __launch_bounds__(kEncThreads) k_ragged_append_r2(RaggedAppend a, int single) {
   const csa2_cache &c = a.c;
   if (static_cast<int>(blockIdx.x) >= a.total) {
-    const int part = blockIdx.x - a.total, b = part / kCopyBlocks, i0 = (part % kCopyBlocks) * (kWin / kCopyBlocks);
-    int first, n;
-    if (!ragged_rows(a.cu, b, a.total, a.max_new, first, n)) {
-      if (i0 == 0 && threadIdx.x == 0) raise_err(a.err, CSA2_DEVERR_INDEX);
-      return;
-    }
-    const int64_t t0 = c.n_tokens[b] - kWin;
-    const int row16 = swa_bytes(c) / 16;
-    for (int k = threadIdx.x; k < kWin / kCopyBlocks * (row16 + 2); k += blockDim.x) {
-      const int i = i0 + k / (row16 + 2), w = k % (row16 + 2);
-      const int64_t t = t0 + i;
-      const size_t dst = static_cast<size_t>(first) + static_cast<size_t>(kWin) * b + i;
-      const size_t src = static_cast<size_t>(b) * kWin + (t & (kWin - 1));
-      const uint4 zero = make_uint4(0, 0, 0, 0);
-      if (w < row16)
-        reinterpret_cast<uint4 *>(a.win_codes)[dst * row16 + w] =
-            t >= 0 ? reinterpret_cast<const uint4 *>(c.swa_codes)[src * row16 + w] : zero;
-      else if (c.swa_dtype == CSA2_SWA_MXFP8)
-        reinterpret_cast<uint4 *>(a.win_scales)[dst * 2 + w - row16] =
-            t >= 0 ? reinterpret_cast<const uint4 *>(c.swa_scales)[src * 2 + w - row16] : zero;
-    }
+    copy_older(a, blockIdx.x - a.total);
     return;
   }
   __shared__ __align__(16) float row[kDcmp];
@@ -108,18 +352,11 @@ __global__ void __launch_bounds__(kEncThreads) k_ragged_append(RaggedAppend a, i
   }
   const int j = r - first;
   const int64_t t = t0 + j;
-  const bool mine = c.ratio == 1;  // the entry is the token itself
-  if (mine) {
-    for (int i = threadIdx.x; i < kDqk; i += blockDim.x) row[i] = load_row(a.kv, r * a.kv_stride + i, a.in_bf16);
-    for (int i = threadIdx.x; i < kDi; i += blockDim.x) row[kDqk + i] = load_row(a.ik, r * a.key_stride + i, a.in_bf16);
-  } else {
-    for (int i = threadIdx.x; i < kDqk; i += blockDim.x) row[i] = a.cmp.ca[static_cast<size_t>(r) * kDcmp + i];
-  }
+  for (int i = threadIdx.x; i < kDqk; i += blockDim.x) row[i] = a.cmp.ca[static_cast<size_t>(r) * kDcmp + i];
   if (threadIdx.x < 64) rot[threadIdx.x] = a.rope_cs[t * 64 + threadIdx.x];
   __syncthreads();
   block_rope_inplace(row, rot);
   __syncthreads();
-  if (mine) block_encode_entry(c, b, t, row, rot, a.err);
   uint8_t *wc = nullptr, *ws = nullptr;
   if (a.win_codes != nullptr) {
     const size_t i = static_cast<size_t>(r) + static_cast<size_t>(kWin) * (b + 1);
@@ -131,32 +368,30 @@ __global__ void __launch_bounds__(kEncThreads) k_ragged_append(RaggedAppend a, i
     ws = c.swa_scales + i * kSwaScaleStride;
   }
   if (wc != nullptr) block_encode_swa(wc, ws, c.swa_dtype, row, rot);
-  if (!mine) {
-    if (t & 1) {  // the pair is complete: entry t / 2, at position t - 1
-      const int64_t e = t >> 1;
-      const float *src[2][4];  // [Z, C][a0, a1, b0, b1]
-      const bool has_b = e > 0;
+  if (t & 1) {  // the pair is complete: entry t / 2, at position t - 1
+    const int64_t e = t >> 1;
+    const float *src[2][4];  // [Z, C][a0, a1, b0, b1]
+    const bool has_b = e > 0;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int64_t p = k < 2 ? 2 * e + k : has_b ? 2 * e - 4 + k : 2 * e;
-        src[0][k] = ragged_cmp_row(a, b, first, t0, p, k < 2 ? 2 : 3);
-        src[1][k] = ragged_cmp_row(a, b, first, t0, p, k < 2 ? 0 : 1);
-      }
-      __syncthreads();  // the window row has been read
-      for (int i = threadIdx.x; i < kDcmp; i += blockDim.x)
-        row[i] = r2_compress_channel(src[0][0][i], src[0][1][i], src[0][2][i], src[0][3][i], a.cmp.ba[i],
-                                     a.cmp.ba[kDcmp + i], a.cmp.bb[i], a.cmp.bb[kDcmp + i], src[1][0][i], src[1][1][i],
-                                     src[1][2][i], src[1][3][i], has_b);
-      if (threadIdx.x < 64) rot[threadIdx.x] = a.rope_cs[(t - 1) * 64 + threadIdx.x];
-      __syncthreads();
-      block_rope_inplace(row, rot);
-      __syncthreads();
-      block_encode_entry(c, b, e, row, rot, a.err);
+    for (int k = 0; k < 4; ++k) {
+      const int64_t p = k < 2 ? 2 * e + k : has_b ? 2 * e - 4 + k : 2 * e;
+      src[0][k] = ragged_cmp_row(a, b, first, t0, p, k < 2 ? 2 : 3);
+      src[1][k] = ragged_cmp_row(a, b, first, t0, p, k < 2 ? 0 : 1);
     }
-    // a single token's slot (t % 4) is none of those its entry was made from
-    if (single) store_cmp_rows(a, b, r, t);
+    __syncthreads();  // the window row has been read
+    for (int i = threadIdx.x; i < kDcmp; i += blockDim.x)
+      row[i] = r2_compress_channel(src[0][0][i], src[0][1][i], src[0][2][i], src[0][3][i], a.cmp.ba[i],
+                                   a.cmp.ba[kDcmp + i], a.cmp.bb[i], a.cmp.bb[kDcmp + i], src[1][0][i], src[1][1][i],
+                                   src[1][2][i], src[1][3][i], has_b);
+    if (threadIdx.x < 64) rot[threadIdx.x] = a.rope_cs[(t - 1) * 64 + threadIdx.x];
+    __syncthreads();
+    block_rope_inplace(row, rot);
+    __syncthreads();
+    block_encode_entry(c, b, e, row, rot, a.err);
   }
+  // a single token's slot (t % 4) is none of those its entry was made from
   if (single) {
+    store_cmp_rows(a, b, r, t);
     __syncthreads();  // every thread has read n_tokens
     if (threadIdx.x == 0) c.n_tokens[b] = t0 + n;
   }
@@ -217,65 +452,125 @@ struct ReadArgs {
   const int64_t *start;
   void *main, *key;
   int64_t main_stride, key_stride;
-  int bf16;
   int32_t *err;
 };
 
-// One warp per row, in units of 8 values: lane l has latent units l and l + 32,
-// lanes 0-7 the RoPE units, lanes 8-23 the key's; every store instruction of
-// the latent writes a contiguous 512 B (bf16).
+// 8 warps, kRow rows each, in units of 8 values: lane l has latent units l and
+// l + 32, lanes 0-7 the RoPE units, lanes 8-23 the key's; every store instruction
+// of the latent writes a contiguous 512 B (bf16).  One thread per row first finds
+// where it lies (a chain of dependent loads) for the whole block; then a warp
+// requests all its rows before it converts the first.
+struct RowPlace {
+  int64_t pe, pt;  // physical entry and indexer tile; pe -1: zeros, -2: no row
+  int32_t m;       // place in the indexer tile
+};
+struct RawRow {
+  uint2 c[2];       // latent units l, l + 32
+  uint4 x;          // lanes 0-7: RoPE, 8-23: key
+  uint32_t s[2], t; // their scales
+};
+template <bool kBf16, int kRow>
 __global__ void __launch_bounds__(256) k_kv_read(ReadArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (r >= a.total) return;
+  __shared__ RowPlace place[8 * kRow];
   const csa2_cache &c = a.c;
-  const int b = ragged_seq(a.cu, c.batch, r);
-  if (b < 0) return;
-  const int64_t e = a.pos ? static_cast<int64_t>(a.pos[r]) : a.start[b] + (r - a.cu[b]);
-  int64_t pe = -1, pt = -1;
-  bool bad = false;
-  if (e >= 0) {
-    const int64_t held = c.n_tokens[b] / c.ratio;
-    bad = e >= held || e >= c.capacity;
-    if (!bad) {
-      const EntryMap map = entry_map(c);
-      pe = phys_entry(map, b, e);
-      pt = phys_tile(map, b, e / kIdxTile);
-      bad = pe < 0 || pt < 0;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * 8 * kRow;
+  if (tid < 8 * kRow) {
+    RowPlace pl{-2, 0, 0};
+    const int64_t r = r0 + tid;
+    const int b = r < a.total ? ragged_seq(a.cu, c.batch, static_cast<int>(r)) : -1;
+    if (b >= 0) {
+      pl.pe = -1;
+      const int64_t e = a.pos ? static_cast<int64_t>(a.pos[r]) : a.start[b] + (r - a.cu[b]);
+      bool bad = e < 0 && a.pos == nullptr;  // a negative start
+      if (e >= 0) {
+        bad = e >= c.n_tokens[b] / c.ratio || e >= c.capacity;
+        if (!bad) {
+          const EntryMap map = entry_map(c);
+          pl.pe = phys_entry(map, b, e);
+          pl.pt = phys_tile(map, b, e / kIdxTile);
+          pl.m = static_cast<int>(e % kIdxTile);
+          bad = pl.pe < 0;
+        }
+      }
+      if (bad) {
+        raise_err(a.err, CSA2_DEVERR_INDEX);
+        pl.pe = -1;
+      }
     }
-  } else {
-    bad = a.pos == nullptr;  // a negative start
+    place[tid] = pl;
   }
-  if (bad && lane == 0) raise_err(a.err, CSA2_DEVERR_INDEX);
-  const bool some = e >= 0 && !bad;
-  float v[8];
-  auto zero = [&]() {
+  __syncthreads();
+  const bool fp8 = c.entry_format == CSA2_ENTRY_FP8;
+  const bool main = a.main != nullptr, key = a.key != nullptr;
+  constexpr int kBatch = kRow < 4 ? kRow : 4;  // rows in flight
+#pragma unroll 1
+  for (int i0 = 0; i0 < kRow; i0 += kBatch) {
+    RawRow raw[kBatch];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  };
-  if (a.main != nullptr) {
+    for (int i = 0; i < kBatch; ++i) {
+      const RowPlace pl = place[warp * kRow + i0 + i];
+      RawRow &w = raw[i];
+      if (pl.pe < 0) continue;
+      if (main) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int u = lane + 32 * k;
-      zero();
-      if (some) entry_unit8(c, pe, u, v);
-      store8(a.main, r * a.main_stride + 8 * u, a.bf16, v);
+        for (int k = 0; k < 2; ++k) {
+          const int u = lane + 32 * k;
+          if (fp8) {
+            w.c[k] = __ldg(reinterpret_cast<const uint2 *>(c.lat_codes + pl.pe * 512) + u);
+            w.s[k] = __ldg(c.lat_scales + pl.pe * 16 + (u >> 2));
+          } else {
+            w.c[k].x = __ldg(reinterpret_cast<const uint32_t *>(c.lat_codes + pl.pe * 256) + u);
+            w.s[k] = __ldg(c.lat_scales + pl.pe * 32 + (u >> 1));
+          }
+        }
+        if (lane < 8) {
+          if (fp8) {
+            w.x = __ldg(reinterpret_cast<const uint4 *>(c.rope_codes + pl.pe * 128) + lane);
+          } else {
+            w.x.x = __ldg(reinterpret_cast<const uint32_t *>(c.rope_codes + pl.pe * 32) + lane);
+            w.t = __ldg(c.rope_scales + pl.pe * 4 + (lane >> 1));
+          }
+        }
+      }
+      if (key && lane >= 8 && lane < 24) {
+        const int u = lane - 8;
+        w.x.x = __ldg(reinterpret_cast<const uint32_t *>(c.idx_codes + idx_code_at(pl.pt, pl.m, u >> 2) + 4 * (u & 3)));
+        w.t = __ldg(c.idx_scales + idx_scale_at(pl.pt, pl.m) + (u >> 2));
+      }
     }
-    if (lane < 8) {
-      zero();
-      if (some) entry_unit8(c, pe, 64 + lane, v);
-      store8(a.main, r * a.main_stride + kLat + 8 * lane, a.bf16, v);
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int at = warp * kRow + i0 + i;
+      const int64_t pe = place[at].pe, r = r0 + at;
+      if (pe == -2) continue;
+      const RawRow &w = raw[i];
+      float v[8];
+      auto zero = [&]() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+      };
+      if (main) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          if (pe < 0) zero();
+          else if (fp8) e4m3x8(w.c[k], e8m0_value(w.s[k]), v);
+          else e2m1x8(w.c[k].x, e4m3_value(w.s[k]), v);
+          store8(a.main, r * a.main_stride + 8 * (lane + 32 * k), kBf16, v);
+        }
+        if (lane < 8) {
+          if (pe < 0) zero();
+          else if (fp8) bf16x8(w.x, v);
+          else e2m1x8(w.x.x, e4m3_value(w.t), v);
+          store8(a.main, r * a.main_stride + kLat + 8 * lane, kBf16, v);
+        }
+      }
+      if (key && lane >= 8 && lane < 24) {
+        if (pe < 0) zero();
+        else e2m1x8(w.x.x, e8m0_value(w.t), v);
+        store8(a.key, r * a.key_stride + 8 * (lane - 8), kBf16, v);
+      }
     }
-  }
-  if (a.key != nullptr && lane >= 8 && lane < 24) {
-    const int u = lane - 8;
-    zero();
-    if (some) {
-      const int m = static_cast<int>(e % kIdxTile);
-      e2m1x8(*reinterpret_cast<const uint32_t *>(c.idx_codes + idx_code_at(pt, m, u >> 2) + 4 * (u & 3)),
-             e8m0_value(c.idx_scales[idx_scale_at(pt, m) + (u >> 2)]), v);
-    }
-    store8(a.key, r * a.key_stride + 8 * u, a.bf16, v);
   }
 }
 
@@ -351,7 +646,6 @@ csa2_status csa2_kv_append_ragged(const csa2_cache *cache, const void *kv, int64
   a.ik = idx_key;
   a.kv_stride = kv_stride;
   a.key_stride = key_stride;
-  a.in_bf16 = in_dtype == CSA2_IN_BF16;
   if (cmp != nullptr) a.cmp = *cmp;
   a.cu = cu_new;
   a.total = total;
@@ -363,8 +657,18 @@ csa2_status csa2_kv_append_ragged(const csa2_cache *cache, const void *kv, int64
   a.err = err_word;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int single = max_new == 1 && win_codes == nullptr;
-  const int blocks = total + (win_codes != nullptr ? csa2::kCopyBlocks * cache->batch : 0);
-  csa2::k_ragged_append<<<blocks, csa2::kEncThreads, 0, s>>>(a, single);
+  const int copies = win_codes != nullptr ? csa2::kCopyBlocks * cache->batch : 0;
+  if (cache->ratio == 2) {
+    csa2::k_ragged_append_r2<<<total + copies, csa2::kEncThreads, 0, s>>>(a, single);
+  } else {
+    // four tokens per warp once that still leaves every SM a block: one address
+    // phase for four times the rows
+    const int per = total >= 32 * csa2::device_sm_count() ? 32 : 8, blocks = (total + per - 1) / per;
+    const bool bf16 = in_dtype == CSA2_IN_BF16;
+    auto kern = bf16 ? (per == 32 ? csa2::k_ragged_append_r1<true, 4> : csa2::k_ragged_append_r1<true, 1>)
+                     : (per == 32 ? csa2::k_ragged_append_r1<false, 4> : csa2::k_ragged_append_r1<false, 1>);
+    kern<<<blocks + copies, 256, 0, s>>>(a, single, blocks);
+  }
   if (!single) csa2::k_ragged_finish<<<cache->batch, 256, 0, s>>>(a);
   return cuda_status(cudaGetLastError(), "csa2_kv_append_ragged launch");
 }
@@ -387,9 +691,13 @@ csa2_status csa2_kv_read(const csa2_cache *cache, const int32_t *cu_rows, int32_
   CSA2_REQUIRE(out_key == nullptr || (key_stride >= CSA2_D_INDEX && key_stride % 8 == 0), CSA2_ERR_SHAPE,
                "key_stride %lld must be a multiple of 8, 128 at least", static_cast<long long>(key_stride));
   if (total == 0) return CSA2_OK;
-  csa2::ReadArgs a{*cache, cu_rows, total, pos, start, out_main, out_key, main_stride, key_stride,
-                   out_dtype == CSA2_OUT_BF16, err_word};
-  csa2::k_kv_read<<<(total + 7) / 8, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  csa2::ReadArgs a{*cache, cu_rows, total, pos, start, out_main, out_key, main_stride, key_stride, err_word};
+  // eight rows per warp once that still leaves every SM a block or two
+  const int per = total >= 64 * csa2::device_sm_count() ? 64 : 8;
+  const bool bf16 = out_dtype == CSA2_OUT_BF16;
+  auto kern = bf16 ? (per == 64 ? csa2::k_kv_read<true, 8> : csa2::k_kv_read<true, 1>)
+                   : (per == 64 ? csa2::k_kv_read<false, 8> : csa2::k_kv_read<false, 1>);
+  kern<<<(total + per - 1) / per, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
   return cuda_status(cudaGetLastError(), "csa2_kv_read launch");
 }
 
