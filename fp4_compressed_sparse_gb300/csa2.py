@@ -398,18 +398,20 @@ def mask_to_pool(scores, ratio, q_pos, pool, pool_block_size=8, stream=None):
 
 # --------------------------------------------------------------------------- ragged batches
 def _want(name, t, dtype, shape=None, like=None):
-    """Raise ValueError unless t is a contiguous device tensor of dtype (and shape; -1: any size), on like's device."""
+    """Raise ValueError unless t is a contiguous device tensor of dtype (and shape), on like's device."""
+    if t is not None and t.is_cuda and (t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype)) and (
+            shape is None or t.shape == shape) and t.is_contiguous() and (
+            like is None or t.get_device() == like.get_device()):
+        return
     if t is None or not t.is_cuda:
         raise ValueError(f"{name}: a CUDA tensor is needed")
     if t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
         raise ValueError(f"{name}: {t.dtype}, {dtype} is needed")
-    if shape is not None and t.shape != shape and (
-            t.dim() != len(shape) or any(w not in (-1, n) for w, n in zip(shape, t.shape))):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, {tuple(shape)} is needed")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
-    if like is not None and t.get_device() != like.get_device():
-        raise ValueError(f"{name} is on {t.device}, the cache on {like.device}")
+    raise ValueError(f"{name} is on {t.device}, the cache on {like.device}")
 
 
 def _want_rows(name, t, dtype, width, like, total=None):
@@ -418,9 +420,10 @@ def _want_rows(name, t, dtype, width, like, total=None):
         raise ValueError(f"{name}: a tensor on {like.device} is needed")
     if t.dtype not in dtype:
         raise ValueError(f"{name}: {t.dtype}, one of {dtype} is needed")
-    if t.dim() != 2 or t.shape[1] != width or (total is not None and t.shape[0] != total):
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != width or (total is not None and shape[0] != total):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, ({'rows' if total is None else total}, {width}) is needed")
-    if t.shape[0] <= 1:
+    if shape[0] <= 1:
         return width
     row, one = t.stride()
     if one != 1 or row < width:
@@ -436,16 +439,22 @@ def _adr(t):
     return None if t is None else t.data_ptr()
 
 
+# the current stream's handle (the public current_stream() builds an object first, which takes as long as a launch)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 def _call(fn, cache, stream, *args):
     """fn(cache, *args, stream) with the cache's device as the current one, on its current stream unless one is given."""
     f, dev = getattr(_lib or load(), fn), cache.n_tokens.get_device()
+    s = stream.cuda_stream if stream is not None else _raw_stream(dev)
     if dev == torch.cuda.current_device():
-        s = stream if stream is not None else torch.cuda.current_stream()
-        _check(fn, f(cache.ref(), *args, s.cuda_stream))
+        status = f(cache.ref(), *args, s)
     else:
         with torch.cuda.device(dev):
-            s = stream if stream is not None else torch.cuda.current_stream()
-            _check(fn, f(cache.ref(), *args, s.cuda_stream))
+            status = f(cache.ref(), *args, s)
+    if status != OK:
+        _check(fn, status)
 
 
 class ChunkWindow:
@@ -485,7 +494,9 @@ def kv_append_ragged(cache: Cache, cu_new, rope_cs, kv=None, idx_key=None, cmp=N
     (default: all).  win: from chunk_window(cache, total), filled for chunk_attn."""
     like = cache.n_tokens
     _want("cu_new", cu_new, torch.int32, (cache.batch + 1,), like)
-    _want("rope_cs", rope_cs, torch.float32, (-1, 32, 2) if rope_cs is not None and rope_cs.dim() == 3 else (-1, 64), like)
+    _want("rope_cs", rope_cs, torch.float32, None, like)
+    if rope_cs.dim() < 2 or rope_cs.numel() != 64 * rope_cs.shape[0]:
+        raise ValueError(f"rope_cs: shape {tuple(rope_cs.shape)}, (positions, 32, 2) is needed")
     cin, ks, is_, dt = None, 0, 0, IN_F32
     if cache.ratio == 1:
         if cmp is not None:
@@ -547,7 +558,9 @@ def chunk_attn(cache: Cache, q, cu_q, out, lse, ws, sm_scale, max_new=None, win=
     b -> out [total,H,512] (fp32 or bf16), lse fp32 [total,H].  win: the append's window rows (None: the ring,
     enough for single tokens).  ws: chunk_attn_workspace()."""
     like = cache.n_tokens
-    _want("q", q, torch.bfloat16, (-1, -1, D_QK), like)
+    _want("q", q, torch.bfloat16, None, like)
+    if q.dim() != 3 or q.shape[2] != D_QK:
+        raise ValueError(f"q: shape {tuple(q.shape)}, (total, heads, {D_QK}) is needed")
     total, H, _ = q.shape
     _want("cu_q", cu_q, torch.int32, (cache.batch + 1,), like)
     _want("out", out, _FLOATS, (total, H, D_LATENT), like)

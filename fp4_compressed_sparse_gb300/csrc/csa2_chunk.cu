@@ -502,15 +502,6 @@ struct TailKey {
   int kind;  // 0 nothing, 1 FP4 entry, 2 V4 entry, 3 MXFP8 window row, 4 bf16 window row
   const uint8_t *codes, *scales, *rope, *rope_scales;
 };
-// Physical entry of entry e (32-bit divisions: this is on the tiles' critical
-// path), or -1 for a page id outside the pool.
-__device__ __forceinline__ int64_t entry_at(const csa2_cache &c, int seq, int e) {
-  if (c.block_table == nullptr) return static_cast<int64_t>(seq) * c.capacity + e;
-  const uint32_t pg = static_cast<uint32_t>(e) / static_cast<uint32_t>(c.page_entries);
-  const int32_t page = __ldg(c.block_table + static_cast<int64_t>(seq) * c.max_pages + pg);
-  if (page < 0 || page >= c.n_pages) return -1;
-  return static_cast<int64_t>(page) * c.page_entries + (e - static_cast<int>(pg) * c.page_entries);
-}
 __device__ __forceinline__ void tail_key(const ChunkArgs &a, const RowTile &x, int64_t j, TailKey &k) {
   const csa2_cache &c = a.c;
   k.kind = 0;

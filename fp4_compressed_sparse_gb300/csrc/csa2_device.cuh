@@ -62,6 +62,15 @@ __host__ __device__ __forceinline__ int64_t phys_entry(const EntryMap &m, int b,
   if (pg < 0 || pg >= m.n_pages) return -1;
   return static_cast<int64_t>(pg) * m.page + e % m.page;
 }
+// The same for an entry index that fits an int, with a 32-bit division and the
+// table read through the read-only path (for kernels whose critical path it is).
+__device__ __forceinline__ int64_t entry_at(const csa2_cache &c, int seq, int e) {
+  if (c.block_table == nullptr) return static_cast<int64_t>(seq) * c.capacity + e;
+  const uint32_t pg = static_cast<uint32_t>(e) / static_cast<uint32_t>(c.page_entries);
+  const int32_t page = __ldg(c.block_table + static_cast<int64_t>(seq) * c.max_pages + pg);
+  if (page < 0 || page >= c.n_pages) return -1;
+  return static_cast<int64_t>(page) * c.page_entries + (e - static_cast<int>(pg) * c.page_entries);
+}
 // physical 128-entry tile of tile t of sequence b for the indexer planes; -1 as above
 __host__ __device__ __forceinline__ int64_t phys_tile(const EntryMap &m, int b, int64_t t) {
   if (m.bt == nullptr) return static_cast<int64_t>(b) * idx_tiles(m.cap) + t;

@@ -469,8 +469,49 @@ struct RawRow {
   uint4 x;          // lanes 0-7: RoPE, 8-23: key
   uint32_t s[2], t; // their scales
 };
+// A unit from memory as half pairs and a scale to fp32, times the scale (exact),
+// to the output row.
+template <bool kBf16>
+__device__ __forceinline__ void store_unit(uint8_t *dst, const uint32_t *h, float s) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+    v[2 * i] = f.x * s;
+    v[2 * i + 1] = f.y * s;
+  }
+  if (kBf16) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t *>(&t);
+    }
+    *reinterpret_cast<uint4 *>(dst) = make_uint4(u[0], u[1], u[2], u[3]);
+  } else {
+    reinterpret_cast<float4 *>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
+__device__ __forceinline__ void e2m1x8_h(uint32_t w, uint32_t *h) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("{\n .reg .b8 t;\n cvt.u8.u32 t, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n" : "=r"(h[i]) : "r"(w >> (8 * i)));
+}
+__device__ __forceinline__ void e4m3x8_h(uint2 w, uint32_t *h) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n"
+        : "=r"(h[i])
+        : "h"(static_cast<uint16_t>((i < 2 ? w.x : w.y) >> (16 * (i & 1)))));
+}
+__device__ __forceinline__ float e4m3_scale(uint32_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
+  return __low2float(*reinterpret_cast<const __half2 *>(&h));
+}
 template <bool kBf16, int kRow>
-__global__ void __launch_bounds__(256) k_kv_read(ReadArgs a) {
+__global__ void __launch_bounds__(256, 4) k_kv_read(ReadArgs a) {
   __shared__ RowPlace place[8 * kRow];
   const csa2_cache &c = a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -484,12 +525,12 @@ __global__ void __launch_bounds__(256) k_kv_read(ReadArgs a) {
       const int64_t e = a.pos ? static_cast<int64_t>(a.pos[r]) : a.start[b] + (r - a.cu[b]);
       bool bad = e < 0 && a.pos == nullptr;  // a negative start
       if (e >= 0) {
-        bad = e >= c.n_tokens[b] / c.ratio || e >= c.capacity;
+        bad = e >= c.n_tokens[b] >> (c.ratio - 1) || e >= c.capacity;
         if (!bad) {
-          const EntryMap map = entry_map(c);
-          pl.pe = phys_entry(map, b, e);
-          pl.pt = phys_tile(map, b, e / kIdxTile);
+          pl.pe = entry_at(c, b, static_cast<int>(e));
           pl.m = static_cast<int>(e % kIdxTile);
+          // a page holds whole indexer tiles; a dense sequence's are padded
+          pl.pt = c.block_table != nullptr ? pl.pe / kIdxTile : b * idx_tiles(c.capacity) + e / kIdxTile;
           bad = pl.pe < 0;
         }
       }
@@ -503,40 +544,44 @@ __global__ void __launch_bounds__(256) k_kv_read(ReadArgs a) {
   __syncthreads();
   const bool fp8 = c.entry_format == CSA2_ENTRY_FP8;
   const bool main = a.main != nullptr, key = a.key != nullptr;
-  constexpr int kBatch = kRow < 4 ? kRow : 4;  // rows in flight
+  // lanes 0-7 have a RoPE unit, lanes 8-23 a key unit
+  const bool rope = main && lane < 8, has_key = key && lane >= 8 && lane < 24;
+  const int ku = lane - 8;
+  constexpr int kBatch = kRow < 4 ? kRow : 4, kElt = kBf16 ? 2 : 4;  // rows in flight; bytes of a value
 #pragma unroll 1
   for (int i0 = 0; i0 < kRow; i0 += kBatch) {
     RawRow raw[kBatch];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
-      const RowPlace pl = place[warp * kRow + i0 + i];
+      const RowPlace &pl = place[warp * kRow + i0 + i];
+      const int64_t pe = pl.pe;
       RawRow &w = raw[i];
-      if (pl.pe < 0) continue;
+      if (pe < 0) continue;
       if (main) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int u = lane + 32 * k;
-          if (fp8) {
-            w.c[k] = __ldg(reinterpret_cast<const uint2 *>(c.lat_codes + pl.pe * 512) + u);
-            w.s[k] = __ldg(c.lat_scales + pl.pe * 16 + (u >> 2));
-          } else {
-            w.c[k].x = __ldg(reinterpret_cast<const uint32_t *>(c.lat_codes + pl.pe * 256) + u);
-            w.s[k] = __ldg(c.lat_scales + pl.pe * 32 + (u >> 1));
-          }
-        }
-        if (lane < 8) {
-          if (fp8) {
-            w.x = __ldg(reinterpret_cast<const uint4 *>(c.rope_codes + pl.pe * 128) + lane);
-          } else {
-            w.x.x = __ldg(reinterpret_cast<const uint32_t *>(c.rope_codes + pl.pe * 32) + lane);
-            w.t = __ldg(c.rope_scales + pl.pe * 4 + (lane >> 1));
-          }
+        if (fp8) {
+          const uint2 *lc = reinterpret_cast<const uint2 *>(c.lat_codes + pe * 512) + lane;
+          const uint8_t *ls = c.lat_scales + pe * 16 + (lane >> 2);
+          w.c[0] = __ldg(lc);
+          w.c[1] = __ldg(lc + 32);
+          w.s[0] = __ldg(ls);
+          w.s[1] = __ldg(ls + 8);
+        } else {
+          const uint32_t *lc = reinterpret_cast<const uint32_t *>(c.lat_codes + pe * 256) + lane;
+          const uint8_t *ls = c.lat_scales + pe * 32 + (lane >> 1);
+          w.c[0].x = __ldg(lc);
+          w.c[1].x = __ldg(lc + 32);
+          w.s[0] = __ldg(ls);
+          w.s[1] = __ldg(ls + 16);
         }
       }
-      if (key && lane >= 8 && lane < 24) {
-        const int u = lane - 8;
-        w.x.x = __ldg(reinterpret_cast<const uint32_t *>(c.idx_codes + idx_code_at(pl.pt, pl.m, u >> 2) + 4 * (u & 3)));
-        w.t = __ldg(c.idx_scales + idx_scale_at(pl.pt, pl.m) + (u >> 2));
+      if (rope && fp8) {
+        w.x = __ldg(reinterpret_cast<const uint4 *>(c.rope_codes + pe * 128) + lane);
+      } else if (rope || has_key) {
+        const uint8_t *src = rope ? c.rope_codes + pe * 32 + 4 * lane
+                                  : c.idx_codes + idx_code_at(pl.pt, pl.m, ku >> 2) + 4 * (ku & 3);
+        const uint8_t *sc = rope ? c.rope_scales + pe * 4 + (lane >> 1) : c.idx_scales + idx_scale_at(pl.pt, pl.m) + (ku >> 2);
+        w.x.x = __ldg(reinterpret_cast<const uint32_t *>(src));
+        w.t = __ldg(sc);
       }
     }
 #pragma unroll
@@ -544,31 +589,34 @@ __global__ void __launch_bounds__(256) k_kv_read(ReadArgs a) {
       const int at = warp * kRow + i0 + i;
       const int64_t pe = place[at].pe, r = r0 + at;
       if (pe == -2) continue;
-      const RawRow &w = raw[i];
-      float v[8];
-      auto zero = [&]() {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-      };
+      RawRow &w = raw[i];
+      if (pe < 0) {
+        w = RawRow{};  // an empty row: codes of zero, and a scale of zero (1 for E8M0: 0 x 2^-127)
+        w.t = 0;
+      }
+      uint8_t *om = static_cast<uint8_t *>(a.main) + r * a.main_stride * kElt + 8 * kElt * lane;
+      uint32_t h[4];
       if (main) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          if (pe < 0) zero();
-          else if (fp8) e4m3x8(w.c[k], e8m0_value(w.s[k]), v);
-          else e2m1x8(w.c[k].x, e4m3_value(w.s[k]), v);
-          store8(a.main, r * a.main_stride + 8 * (lane + 32 * k), kBf16, v);
-        }
-        if (lane < 8) {
-          if (pe < 0) zero();
-          else if (fp8) bf16x8(w.x, v);
-          else e2m1x8(w.x.x, e4m3_value(w.t), v);
-          store8(a.main, r * a.main_stride + kLat + 8 * lane, kBf16, v);
+          if (fp8) e4m3x8_h(w.c[k], h);
+          else e2m1x8_h(w.c[k].x, h);
+          store_unit<kBf16>(om + 256 * kElt * k, h, fp8 ? e8m0_value(w.s[k]) : e4m3_scale(w.s[k]));
         }
       }
-      if (key && lane >= 8 && lane < 24) {
-        if (pe < 0) zero();
-        else e2m1x8(w.x.x, e8m0_value(w.t), v);
-        store8(a.key, r * a.key_stride + 8 * (lane - 8), kBf16, v);
+      if (rope && fp8) {
+        if (kBf16) {
+          *reinterpret_cast<uint4 *>(om + kLat * kElt) = w.x;
+        } else {
+          float v[8];
+          bf16x8(w.x, v);
+          reinterpret_cast<float4 *>(om + kLat * kElt)[0] = make_float4(v[0], v[1], v[2], v[3]);
+          reinterpret_cast<float4 *>(om + kLat * kElt)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+      } else if (rope || has_key) {
+        uint8_t *dst = rope ? om + kLat * kElt : static_cast<uint8_t *>(a.key) + r * a.key_stride * kElt + 8 * kElt * ku;
+        e2m1x8_h(w.x.x, h);
+        store_unit<kBf16>(dst, h, rope ? e4m3_scale(w.t) : e8m0_value(w.t));
       }
     }
   }
@@ -692,11 +740,11 @@ csa2_status csa2_kv_read(const csa2_cache *cache, const int32_t *cu_rows, int32_
                "key_stride %lld must be a multiple of 8, 128 at least", static_cast<long long>(key_stride));
   if (total == 0) return CSA2_OK;
   csa2::ReadArgs a{*cache, cu_rows, total, pos, start, out_main, out_key, main_stride, key_stride, err_word};
-  // eight rows per warp once that still leaves every SM a block or two
-  const int per = total >= 64 * csa2::device_sm_count() ? 64 : 8;
+  // four rows per warp once that still leaves every SM a block or two
+  const int per = total >= 64 * csa2::device_sm_count() ? 32 : 8;
   const bool bf16 = out_dtype == CSA2_OUT_BF16;
-  auto kern = bf16 ? (per == 64 ? csa2::k_kv_read<true, 8> : csa2::k_kv_read<true, 1>)
-                   : (per == 64 ? csa2::k_kv_read<false, 8> : csa2::k_kv_read<false, 1>);
+  auto kern = bf16 ? (per == 32 ? csa2::k_kv_read<true, 4> : csa2::k_kv_read<true, 1>)
+                   : (per == 32 ? csa2::k_kv_read<false, 4> : csa2::k_kv_read<false, 1>);
   kern<<<(total + per - 1) / per, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
   return cuda_status(cudaGetLastError(), "csa2_kv_read launch");
 }
