@@ -35,6 +35,7 @@ constexpr int kTile = kBlocks * kBlk;        // 73,728 B
 constexpr int kSmWarps = 8, kPrWarps = 16;   // softmax / producer warps
 constexpr int kMmaWarp = kSmWarps + kPrWarps, kAheadWarp = kMmaWarp + 1;
 constexpr int kThreads = 32 * (kAheadWarp + 1);
+static_assert(kPrWarps == 16, "plain is read as 16 bytes");
 constexpr int kAhead = 4;                    // key tiles requested into L2 ahead of use
 constexpr uint32_t kColS = 0, kColO = 256;   // TMEM columns: S 2 x 64, O^T 4 x 64
 constexpr uint32_t kWaitIters = 200, kPolls = 1u << 20;
@@ -322,7 +323,7 @@ struct __align__(1024) ChunkSmem {
   uint32_t moved[2][2];             // rows whose reference moves in a tile (by its parity)
   float tmax[2][kRows], lsum[kRows];  // row maxima of a tile's halves; sums of the second half
   int32_t vis[kRows], w0[kRows];    // a row sees keys j < vis and w0 <= j < w0 + 128
-  int plain[2];                     // every key valid with sigma 0
+  __align__(16) uint8_t plain[2][kPrWarps];  // a producer warp's keys are all valid with sigma 0
   uint32_t tmem, progress;          // progress: the key tile (of this CTA's) being filled
   uint32_t listed;                  // key tiles in the ring so far
   __align__(16) TileRef ring[kRing];
@@ -614,10 +615,8 @@ __device__ __noinline__ bool fill_tail(const ChunkArgs &a, const Plan &p, ChunkS
   bf = key_max(bf);
   const int sigma = t.kind >= 2 ? sigma_of(key_exponent(e8, bf)) : 0;
   if (n >= 2 && !dead) dead = !wait_warp(&sm.empty[b], ((n >> 1) & 1) ^ 1, a.err);
-  if (pt == 0) {
-    *const_cast<volatile uint32_t *>(&sm.progress) = n;
-    sm.plain[b] = 0;
-  }
+  if (pt == 0) *const_cast<volatile uint32_t *>(&sm.progress) = n;
+  if ((pt & 31) == 0) sm.plain[b][pt >> 5] = 0;
   if (o == 0) sm.sg[b][key] = t.kind ? make_float2(static_cast<float>(sigma), pow2f(sigma)) : make_float2(-INFINITY, 0.0f);
 #pragma unroll
   for (int s = 0; s < 5; ++s) tail_store(sm.k[b], t, s, key, o, r[s], sigma);
@@ -655,11 +654,10 @@ __device__ __forceinline__ void produce(const ChunkArgs &a, const Plan &p, Chunk
     base = ring_base(sm, n + 1, a.err);
     if (whole) {
       if (n >= 2 && !dead) dead = !wait_warp(&sm.empty[b], ((n >> 1) & 1) ^ 1, a.err);
-      if (pt == 0) {
-        *const_cast<volatile uint32_t *>(&sm.progress) = n;
-        sm.plain[b] = IsFp4<Raw>::v;
-      }
+      if (pt == 0) *const_cast<volatile uint32_t *>(&sm.progress) = n;
       const int sigma = raw_sigma(raw);
+      const bool plain = IsFp4<Raw>::v || __all_sync(0xffffffffu, sigma == 0);
+      if ((pt & 31) == 0) sm.plain[b][pt >> 5] = plain;
       if (o == 0) sm.sg[b][key] = make_float2(static_cast<float>(sigma), pow2f(sigma));
 #pragma unroll
       for (int s = 0; s < 5; ++s) {
@@ -792,7 +790,8 @@ __device__ __forceinline__ void softmax(const ChunkArgs &a, const Plan &p, Chunk
       tmem_ld_rows16(tmem + lane_base + kColS + 64 * b + 32 * half, reinterpret_cast<uint32_t *>(s));
       // exponents of the weighted weights, x = z + sigma - m, and their row maxima
       float ta = -INFINITY, tb = -INFINITY;
-      const bool fast = sm.plain[b] && (kt + 1) * kKeys <= va;  // (rb sees no less)
+      const uint4 pl = *reinterpret_cast<const uint4 *>(sm.plain[b]);
+      const bool fast = (pl.x & pl.y & pl.z & pl.w) == 0x01010101u && (kt + 1) * kKeys <= va;  // (rb sees no less)
       if (fast) {
 #pragma unroll
         for (int j = 0; j < 16; j += 4) {
