@@ -288,11 +288,6 @@ __device__ __forceinline__ uint32_t e4m3x2_h2(uint32_t two) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
   return r;
 }
-__device__ __forceinline__ uint32_t e2m1x2_h2(uint32_t byte) {
-  uint32_t r;
-  asm("{\n .reg .b8 t;\n cvt.u8.u32 t, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n" : "=r"(r) : "r"(byte));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<uint32_t *>(&h);
@@ -420,12 +415,14 @@ __device__ __forceinline__ void load_step(const csa2_cache &c, int64_t e, int o,
 }
 
 __device__ __forceinline__ uint4 dq_e2m1(uint32_t w, uint32_t s2) {
-  return make_uint4(hmul2u(e2m1x2_h2(w), s2), hmul2u(e2m1x2_h2(w >> 8), s2), hmul2u(e2m1x2_h2(w >> 16), s2),
-                    hmul2u(e2m1x2_h2(w >> 24), s2));
+  uint32_t h[4];
+  e2m1x8_h2(w, h);
+  return make_uint4(hmul2u(h[0], s2), hmul2u(h[1], s2), hmul2u(h[2], s2), hmul2u(h[3], s2));
 }
 __device__ __forceinline__ uint4 dq_e4m3(uint32_t w0, uint32_t w1, uint32_t m2) {
-  return make_uint4(hmul2u(e4m3x2_h2(w0), m2), hmul2u(e4m3x2_h2(w0 >> 16), m2), hmul2u(e4m3x2_h2(w1), m2),
-                    hmul2u(e4m3x2_h2(w1 >> 16), m2));
+  uint32_t h[4];
+  e4m3x8_h2(w0, w1, h);
+  return make_uint4(hmul2u(h[0], m2), hmul2u(h[1], m2), hmul2u(h[2], m2), hmul2u(h[3], m2));
 }
 // 16-byte chunk x (8 dims) of key (or query row) `key` in a 64-dim block
 __device__ __forceinline__ uint8_t *chunk_at(uint8_t *blk, int key, int x) { return blk + key * 128 + ((x ^ (key & 7)) << 4); }

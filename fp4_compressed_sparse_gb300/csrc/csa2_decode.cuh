@@ -6,17 +6,6 @@
 
 namespace csa2 {
 
-// Eight E2M1 codes (low nibble first) times a scale.
-__device__ __forceinline__ void e2m1x8(uint32_t w, float s, float *v) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t h;
-    asm("{\n .reg .b8 t;\n cvt.u8.u32 t, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n" : "=r"(h) : "r"(w >> (8 * i)));
-    const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h));
-    v[2 * i] = f.x * s;
-    v[2 * i + 1] = f.y * s;
-  }
-}
 __device__ __forceinline__ void e4m3x8(uint2 w, float s, float *v) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = e4m3_value(((i < 4 ? w.x : w.y) >> (8 * (i & 3))) & 0xFFu) * s;

@@ -170,6 +170,23 @@ __device__ __forceinline__ float e4m3_value(uint32_t c) {
 // E8M0 scale 2^(c-127), c in 0..254.
 __device__ __forceinline__ float e8m0_value(uint32_t c) { return pow2f(static_cast<int>(c) - 127); }
 
+// ---------------------------------------------------------------- conversions to fp16 pairs
+// Eight E2M1 codes (low nibble first) and eight E4M3 codes as fp16 pairs, exactly.
+// The word is unpacked by the moves, which the conversions take as byte or half
+// selectors: a shift in front of each costs as much as the conversion.
+__device__ __forceinline__ void e2m1x8_h2(uint32_t w, uint32_t *h) {
+  asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+      " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+}
+__device__ __forceinline__ void e4m3x8_h2(uint32_t w0, uint32_t w1, uint32_t *h) {
+  asm("{\n .reg .b16 a, b, c, d;\n mov.b32 {a, b}, %4;\n mov.b32 {c, d}, %5;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, b;\n cvt.rn.f16x2.e4m3x2 %2, c;\n cvt.rn.f16x2.e4m3x2 %3, d;\n}\n"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w0), "r"(w1));
+}
+
 // ---------------------------------------------------------------- group quantisers
 // Group of 16 with an E4M3 scale: s = E4M3(amax/6); codes E2M1(x/s) (IEEE
 // divisions); s == 0 gives all-zero codes.  Returns the 8 packed bytes.

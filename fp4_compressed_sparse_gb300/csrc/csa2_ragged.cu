@@ -493,18 +493,6 @@ __device__ __forceinline__ void store_unit(uint8_t *dst, const uint32_t *h, floa
     reinterpret_cast<float4 *>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
   }
 }
-__device__ __forceinline__ void e2m1x8_h(uint32_t w, uint32_t *h) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("{\n .reg .b8 t;\n cvt.u8.u32 t, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n" : "=r"(h[i]) : "r"(w >> (8 * i)));
-}
-__device__ __forceinline__ void e4m3x8_h(uint2 w, uint32_t *h) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n"
-        : "=r"(h[i])
-        : "h"(static_cast<uint16_t>((i < 2 ? w.x : w.y) >> (16 * (i & 1)))));
-}
 __device__ __forceinline__ float e4m3_scale(uint32_t c) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
@@ -599,8 +587,8 @@ __global__ void __launch_bounds__(256, 4) k_kv_read(ReadArgs a) {
       if (main) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          if (fp8) e4m3x8_h(w.c[k], h);
-          else e2m1x8_h(w.c[k].x, h);
+          if (fp8) e4m3x8_h2(w.c[k].x, w.c[k].y, h);
+          else e2m1x8_h2(w.c[k].x, h);
           store_unit<kBf16>(om + 256 * kElt * k, h, fp8 ? e8m0_value(w.s[k]) : e4m3_scale(w.s[k]));
         }
       }
@@ -615,7 +603,7 @@ __global__ void __launch_bounds__(256, 4) k_kv_read(ReadArgs a) {
         }
       } else if (rope || has_key) {
         uint8_t *dst = rope ? om + kLat * kElt : static_cast<uint8_t *>(a.key) + r * a.key_stride * kElt + 8 * kElt * ku;
-        e2m1x8_h(w.x.x, h);
+        e2m1x8_h2(w.x.x, h);
         store_unit<kBf16>(dst, h, rope ? e4m3_scale(w.t) : e8m0_value(w.t));
       }
     }
