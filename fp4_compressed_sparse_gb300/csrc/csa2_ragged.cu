@@ -469,6 +469,18 @@ struct RawRow {
   uint4 x;          // lanes 0-7: RoPE, 8-23: key
   uint32_t s[2], t; // their scales
 };
+// Eight fp32 values: one 32 B store where the address allows it (rows of an output
+// that starts on 16 B alone take two).
+__device__ __forceinline__ void store_f32x8(uint8_t *dst, const float *v) {
+  if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+    asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                 "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<float4 *>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<float4 *>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+  }
+}
 // A unit from memory as half pairs and a scale to fp32, times the scale (exact),
 // to the output row.
 template <bool kBf16>
@@ -489,8 +501,7 @@ __device__ __forceinline__ void store_unit(uint8_t *dst, const uint32_t *h, floa
     }
     *reinterpret_cast<uint4 *>(dst) = make_uint4(u[0], u[1], u[2], u[3]);
   } else {
-    reinterpret_cast<float4 *>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<float4 *>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+    store_f32x8(dst, v);
   }
 }
 __device__ __forceinline__ float e4m3_scale(uint32_t c) {
@@ -598,8 +609,7 @@ __global__ void __launch_bounds__(256, 4) k_kv_read(ReadArgs a) {
         } else {
           float v[8];
           bf16x8(w.x, v);
-          reinterpret_cast<float4 *>(om + kLat * kElt)[0] = make_float4(v[0], v[1], v[2], v[3]);
-          reinterpret_cast<float4 *>(om + kLat * kElt)[1] = make_float4(v[4], v[5], v[6], v[7]);
+          store_f32x8(om + kLat * kElt, v);
         }
       } else if (rope || has_key) {
         uint8_t *dst = rope ? om + kLat * kElt : static_cast<uint8_t *>(a.key) + r * a.key_stride * kElt + 8 * kElt * ku;
