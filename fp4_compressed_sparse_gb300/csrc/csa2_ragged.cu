@@ -86,10 +86,14 @@ __device__ __forceinline__ void copy_older(const RaggedAppend &a, int part) {
 // Lane l has latent dims 16 l .. + 15 (one NVFP4 group, half an MXFP8 block), RoPE
 // pair l, key dims 4 l .. + 3, all in registers: no shared memory and no block
 // barrier beyond the one after the address phase, in which one thread per token
-// finds where it goes (a chain of dependent loads) for the whole block.
+// finds where it goes (a chain of dependent loads: the sequence, its length, the
+// page) while the row is on its way.
 //
-// 16,384 + 16,384 bf16 tokens in the V4 format: see the figures in the header
-// comment of the launch below.
+// 32,768 bf16 tokens in the V4 format: FIGRAG
+// Latency is hidden by other blocks, four per SM (63 registers).  Several tokens per
+// warp, the next row requested ahead, share the address phase but need 64 to 80
+// registers: four per warp took 3 us longer.  A block per token through shared
+// memory took 261 us.
 
 // Sixteen E2M1 codes of x / s without the divisions: x / s, rounded to fp32, is at
 // most (below) a midpoint t of the grid exactly when x is at most (below) t s.
@@ -203,24 +207,23 @@ struct TokenPlace {
   int64_t t;
 };
 
-// kTok tokens per warp.  Blocks behind the tokens' copy the older window rows.
-template <bool kBf16, int kTok>
-__global__ void __launch_bounds__(256) k_ragged_append_r1(RaggedAppend a, int single, int token_blocks) {
+// Eight tokens per block.  Blocks behind the tokens' copy the older window rows.
+template <bool kBf16>
+__global__ void __launch_bounds__(256, 4) k_ragged_append_r1(RaggedAppend a, int single, int token_blocks) {
   if (static_cast<int>(blockIdx.x) >= token_blocks) {
     copy_older(a, blockIdx.x - token_blocks);
     return;
   }
-  __shared__ TokenPlace place[8 * kTok];
+  __shared__ TokenPlace place[8];
   const csa2_cache &c = a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int r0 = blockIdx.x * 8 * kTok;
-  // the rows do not depend on their places: the first one is requested at once
-  TokenRow<kBf16> tok;
-  int r = r0 + warp;
-  if (r < a.total) load_token(a, r, lane, tok);
-  if (tid < 8 * kTok) {
+  // the row does not depend on its place: it is requested at once
+  TokenRow<kBf16> cur;
+  const int r = blockIdx.x * 8 + warp;
+  if (r < a.total) load_token(a, r, lane, cur);
+  if (tid < 8) {
     TokenPlace pl{-1, -1, -1, 0};
-    const int row = r0 + tid;
+    const int row = blockIdx.x * 8 + tid;
     const int b = row < a.total ? ragged_seq(a.cu, c.batch, row) : -1;
     int first = 0, n = 0;
     if (b >= 0 && !ragged_rows(a.cu, b, a.total, a.max_new, first, n)) raise_err(a.err, CSA2_DEVERR_INDEX);
@@ -243,84 +246,79 @@ __global__ void __launch_bounds__(256) k_ragged_append_r1(RaggedAppend a, int si
   }
   __syncthreads();
   const bool fp8 = c.entry_format == CSA2_ENTRY_FP8, mx = c.swa_dtype == CSA2_SWA_MXFP8;
-#pragma unroll 1
-  for (int i = 0; i < kTok; ++i, r += 8) {
-    if (r >= a.total) break;
-    const TokenPlace pl = place[warp + 8 * i];
-    TokenRow<kBf16> cur = tok;
-    if (i + 1 < kTok && r + 8 < a.total) load_token(a, r + 8, lane, tok);
-    if (pl.pe < 0 && pl.win < 0) continue;
-    const float2 cs = __ldg(reinterpret_cast<const float2 *>(a.rope_cs + pl.t * 64 + 2 * lane));
-    rope_pair(cur.r.x, cur.r.y, cs.x, cs.y);
-    // E4M3 latents, shared by a V4 entry and an MXFP8 window row
-    uint4 lat8 = make_uint4(0, 0, 0, 0);
-    uint32_t lat8_sc = 0;
-    if ((fp8 && pl.pe >= 0) || (mx && pl.win >= 0)) {
-      float amax = 0.0f, inv;
+  if (r >= a.total) return;
+  const TokenPlace pl = place[warp];
+  if (pl.pe < 0 && pl.win < 0) return;
+  const float2 cs = __ldg(reinterpret_cast<const float2 *>(a.rope_cs + pl.t * 64 + 2 * lane));
+  rope_pair(cur.r.x, cur.r.y, cs.x, cs.y);
+  // E4M3 latents, shared by a V4 entry and an MXFP8 window row
+  uint4 lat8 = make_uint4(0, 0, 0, 0);
+  uint32_t lat8_sc = 0;
+  if ((fp8 && pl.pe >= 0) || (mx && pl.win >= 0)) {
+    float amax = 0.0f, inv;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(cur.x[j]));
-      amax = max_over(amax, 2);
-      mxfp8_scale(amax, &inv, &lat8_sc);
-      if (amax != 0.0f) {
-        uint32_t w[4];
+    for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(cur.x[j]));
+    amax = max_over(amax, 2);
+    mxfp8_scale(amax, &inv, &lat8_sc);
+    if (amax != 0.0f) {
+      uint32_t w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = e4m3x4(__fmul_rn(cur.x[4 * j], inv), __fmul_rn(cur.x[4 * j + 1], inv), __fmul_rn(cur.x[4 * j + 2], inv),
-                        __fmul_rn(cur.x[4 * j + 3], inv));
-        lat8 = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      for (int j = 0; j < 4; ++j)
+        w[j] = e4m3x4(__fmul_rn(cur.x[4 * j], inv), __fmul_rn(cur.x[4 * j + 1], inv), __fmul_rn(cur.x[4 * j + 2], inv),
+                      __fmul_rn(cur.x[4 * j + 3], inv));
+      lat8 = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    if (pl.pe >= 0) {
-      if (fp8) {
-        *reinterpret_cast<uint4 *>(c.lat_codes + pl.pe * 512 + 16 * lane) = lat8;
-        if ((lane & 1) == 0) c.lat_scales[pl.pe * 16 + (lane >> 1)] = static_cast<uint8_t>(lat8_sc);
-        reinterpret_cast<uint32_t *>(c.rope_codes + pl.pe * 128)[lane] = bf16_pair(cur.r.x, cur.r.y);
-      } else {
-        uint32_t sc;
-        const uint2 w = nvfp4_16(cur.x, &sc);
-        *reinterpret_cast<uint2 *>(c.lat_codes + pl.pe * 256 + 8 * lane) = w;
-        c.lat_scales[pl.pe * 32 + lane] = static_cast<uint8_t>(sc);
-        const uint32_t byte = nvfp4_pair(cur.r.x, cur.r.y, &sc);
-        c.rope_codes[pl.pe * 32 + lane] = static_cast<uint8_t>(byte);
-        if ((lane & 7) == 0) c.rope_scales[pl.pe * 4 + (lane >> 3)] = static_cast<uint8_t>(sc);
-      }
-      // the indexer key, MXFP4: block lane / 8
-      const float x[4] = {cur.k.x, cur.k.y, cur.k.z, cur.k.w};
-      const float amax = max_over(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))), 8);
-      uint32_t codes = 0, sc = 0;
-      if (amax != 0.0f) {
-        const int e = max(-127, min(127, floor_log2f(amax) - 2));
-        const float inv = pow2f(-e);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) codes |= e2m1_code(__fmul_rn(x[j], inv)) << (4 * j);
-        sc = static_cast<uint32_t>(e + 127);
-      }
-      const int m = static_cast<int>(pl.t % kIdxTile), blk = lane >> 3;
-      *reinterpret_cast<uint16_t *>(c.idx_codes + idx_code_at(pl.pt, m, blk) + 2 * (lane & 7)) = static_cast<uint16_t>(codes);
-      if ((lane & 7) == 0) c.idx_scales[idx_scale_at(pl.pt, m) + blk] = static_cast<uint8_t>(sc);
+  }
+  if (pl.pe >= 0) {
+    if (fp8) {
+      *reinterpret_cast<uint4 *>(c.lat_codes + pl.pe * 512 + 16 * lane) = lat8;
+      if ((lane & 1) == 0) c.lat_scales[pl.pe * 16 + (lane >> 1)] = static_cast<uint8_t>(lat8_sc);
+      reinterpret_cast<uint32_t *>(c.rope_codes + pl.pe * 128)[lane] = bf16_pair(cur.r.x, cur.r.y);
+    } else {
+      uint32_t sc;
+      const uint2 w = nvfp4_16(cur.x, &sc);
+      *reinterpret_cast<uint2 *>(c.lat_codes + pl.pe * 256 + 8 * lane) = w;
+      c.lat_scales[pl.pe * 32 + lane] = static_cast<uint8_t>(sc);
+      const uint32_t byte = nvfp4_pair(cur.r.x, cur.r.y, &sc);
+      c.rope_codes[pl.pe * 32 + lane] = static_cast<uint8_t>(byte);
+      if ((lane & 7) == 0) c.rope_scales[pl.pe * 4 + (lane >> 3)] = static_cast<uint8_t>(sc);
     }
-    if (pl.win >= 0) {
-      uint8_t *wc = (a.win_codes != nullptr ? a.win_codes : c.swa_codes) + pl.win * (mx ? 576 : 1152);
-      if (mx) {
-        uint8_t *ws = (a.win_codes != nullptr ? a.win_scales : c.swa_scales) + pl.win * kSwaScaleStride;
-        *reinterpret_cast<uint4 *>(wc + 16 * lane) = lat8;
-        if ((lane & 1) == 0) ws[lane >> 1] = static_cast<uint8_t>(lat8_sc);
-        const float amax = max_over(fmaxf(fabsf(cur.r.x), fabsf(cur.r.y)), 16);
-        float inv;
-        uint32_t sc, code = 0;
-        mxfp8_scale(amax, &inv, &sc);
-        if (amax != 0.0f) code = e4m3x4(__fmul_rn(cur.r.x, inv), __fmul_rn(cur.r.y, inv), 0.0f, 0.0f) & 0xFFFFu;
-        reinterpret_cast<uint16_t *>(wc + kLat)[lane] = static_cast<uint16_t>(code);
-        if ((lane & 15) == 0) ws[16 + (lane >> 4)] = static_cast<uint8_t>(sc);
-      } else {
-        uint32_t w[8];
+    // the indexer key, MXFP4: block lane / 8
+    const float x[4] = {cur.k.x, cur.k.y, cur.k.z, cur.k.w};
+    const float amax = max_over(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))), 8);
+    uint32_t codes = 0, sc = 0;
+    if (amax != 0.0f) {
+      const int e = max(-127, min(127, floor_log2f(amax) - 2));
+      const float inv = pow2f(-e);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = bf16_pair(cur.x[2 * j], cur.x[2 * j + 1]);
-        uint4 *d = reinterpret_cast<uint4 *>(wc + 32 * lane);
-        d[0] = make_uint4(w[0], w[1], w[2], w[3]);
-        d[1] = make_uint4(w[4], w[5], w[6], w[7]);
-        reinterpret_cast<uint32_t *>(wc + 2 * kLat)[lane] = bf16_pair(cur.r.x, cur.r.y);
-      }
+      for (int j = 0; j < 4; ++j) codes |= e2m1_code(__fmul_rn(x[j], inv)) << (4 * j);
+      sc = static_cast<uint32_t>(e + 127);
+    }
+    const int m = static_cast<int>(pl.t % kIdxTile), blk = lane >> 3;
+    *reinterpret_cast<uint16_t *>(c.idx_codes + idx_code_at(pl.pt, m, blk) + 2 * (lane & 7)) = static_cast<uint16_t>(codes);
+    if ((lane & 7) == 0) c.idx_scales[idx_scale_at(pl.pt, m) + blk] = static_cast<uint8_t>(sc);
+  }
+  if (pl.win >= 0) {
+    uint8_t *wc = (a.win_codes != nullptr ? a.win_codes : c.swa_codes) + pl.win * (mx ? 576 : 1152);
+    if (mx) {
+      uint8_t *ws = (a.win_codes != nullptr ? a.win_scales : c.swa_scales) + pl.win * kSwaScaleStride;
+      *reinterpret_cast<uint4 *>(wc + 16 * lane) = lat8;
+      if ((lane & 1) == 0) ws[lane >> 1] = static_cast<uint8_t>(lat8_sc);
+      const float amax = max_over(fmaxf(fabsf(cur.r.x), fabsf(cur.r.y)), 16);
+      float inv;
+      uint32_t sc, code = 0;
+      mxfp8_scale(amax, &inv, &sc);
+      if (amax != 0.0f) code = e4m3x4(__fmul_rn(cur.r.x, inv), __fmul_rn(cur.r.y, inv), 0.0f, 0.0f) & 0xFFFFu;
+      reinterpret_cast<uint16_t *>(wc + kLat)[lane] = static_cast<uint16_t>(code);
+      if ((lane & 15) == 0) ws[16 + (lane >> 4)] = static_cast<uint8_t>(sc);
+    } else {
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = bf16_pair(cur.x[2 * j], cur.x[2 * j + 1]);
+      uint4 *d = reinterpret_cast<uint4 *>(wc + 32 * lane);
+      d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      reinterpret_cast<uint32_t *>(wc + 2 * kLat)[lane] = bf16_pair(cur.r.x, cur.r.y);
     }
   }
 }
@@ -707,12 +705,8 @@ csa2_status csa2_kv_append_ragged(const csa2_cache *cache, const void *kv, int64
   if (cache->ratio == 2) {
     csa2::k_ragged_append_r2<<<total + copies, csa2::kEncThreads, 0, s>>>(a, single);
   } else {
-    // four tokens per warp once that still leaves every SM a block: one address
-    // phase for four times the rows
-    const int per = total >= 32 * csa2::device_sm_count() ? 32 : 8, blocks = (total + per - 1) / per;
-    const bool bf16 = in_dtype == CSA2_IN_BF16;
-    auto kern = bf16 ? (per == 32 ? csa2::k_ragged_append_r1<true, 4> : csa2::k_ragged_append_r1<true, 1>)
-                     : (per == 32 ? csa2::k_ragged_append_r1<false, 4> : csa2::k_ragged_append_r1<false, 1>);
+    const int blocks = (total + 7) / 8;
+    auto kern = in_dtype == CSA2_IN_BF16 ? csa2::k_ragged_append_r1<true> : csa2::k_ragged_append_r1<false>;
     kern<<<blocks + copies, 256, 0, s>>>(a, single, blocks);
   }
   if (!single) csa2::k_ragged_finish<<<cache->batch, 256, 0, s>>>(a);
@@ -738,7 +732,10 @@ csa2_status csa2_kv_read(const csa2_cache *cache, const int32_t *cu_rows, int32_
                "key_stride %lld must be a multiple of 8, 128 at least", static_cast<long long>(key_stride));
   if (total == 0) return CSA2_OK;
   csa2::ReadArgs a{*cache, cu_rows, total, pos, start, out_main, out_key, main_stride, key_stride, err_word};
-  // four rows per warp once that still leaves every SM a block or two
+  // four rows per warp (one address phase for them, their loads in flight together)
+  // once that still leaves every SM two blocks: 131,072 rows to bf16 take 43 us
+  // against 47 with one; up to 32,768 both take the same (18 us), and below
+  // the rule one row per warp is ahead (2,048 rows to fp32: 8.2 us against 10.2)
   const int per = total >= 64 * csa2::device_sm_count() ? 32 : 8;
   const bool bf16 = out_dtype == CSA2_OUT_BF16;
   auto kern = bf16 ? (per == 32 ? csa2::k_kv_read<true, 4> : csa2::k_kv_read<true, 1>)
