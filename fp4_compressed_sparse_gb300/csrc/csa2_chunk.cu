@@ -81,6 +81,7 @@ struct Plan {
   int64_t *cum;       // [max_tiles + 1] first unit of each row tile
   RowTile *tile;      // [max_tiles]
   CtaRange *cta;      // [n_cta]
+  int32_t *merge;     // [n_cta] the CTAs in which a shared row tile ends, then -1
   float *part;        // [2 n_cta][kPartFloats]
   int max_tiles, n_cta;
 };
@@ -195,6 +196,9 @@ __global__ void __launch_bounds__(1024) k_chunk_plan(ChunkArgs a, Plan p) {
     __syncthreads();
   }
   const int64_t W = carry;
+  __shared__ int32_t n_merge;
+  if (tid == 0) n_merge = 0;
+  __syncthreads();
   // small work on fewer CTAs: two units each at least
   const int64_t g_eff = max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.n_cta), (W + 1) / 2));
   for (int g = tid; g < p.n_cta; g += 1024) {
@@ -210,10 +214,13 @@ __global__ void __launch_bounds__(1024) k_chunk_plan(ChunkArgs a, Plan p) {
         while (first > 0 && W * first / g_eff > c0) --first;
         while (W * (first + 1) / g_eff <= c0) ++first;
         r.first = first;
+        p.merge[atomicAdd(&n_merge, 1)] = g;  // (in any order: each joins rows of its own)
       }
     }
     p.cta[g] = r;
   }
+  __syncthreads();
+  for (int i = n_merge + tid; i < p.n_cta; i += 1024) p.merge[i] = -1;
 }
 
 // ------------------------------------------------------------------ operands
@@ -1121,33 +1128,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunk_attn(const __grid_constan
   }
 }
 
-// Row tiles shared by several CTAs: block (g, y) joins rows 8 y .. + 7 of the one
-// that ends in CTA g, its parts in CTA order (part k is CTA first + k's).
+// Row tiles shared by several CTAs: block (x, y) joins 8 rows x 128 kDims dims of
+// the x-th of them, its parts in CTA order (part k is CTA first + k's).  A thread
+// has kDims dims of four rows.  The parts lie in L2, so what counts is how many
+// loads are in flight: eight per thread at once, the first of them before their
+// weights are known, and with few row tiles (many parts each) four times the
+// blocks.
 constexpr int kMaxCta = 256;
+template <int kDims>
 __global__ void __launch_bounds__(256) k_chunk_merge(ChunkArgs a, Plan p) {
+  constexpr int kSplit = 4 / kDims, kParts = 8 / kDims;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  __shared__ float wt[kMaxCta][8];
-  const int g = blockIdx.x, y = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ float wt[kMaxCta][8], ls[kMaxCta][8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int y = blockIdx.y / kSplit, b0 = blockIdx.y % kSplit * kDims;
+  const int g = p.merge[blockIdx.x];
+  if (g < 0) return;
   const CtaRange cr = p.cta[g];
-  if (cr.first < 0) return;
-  const RowTile &x = p.tile[cr.tile];
-  const int nrows = x.nrows, n = g - cr.first + 1;
-  if (8 * y >= nrows) return;
-  const int64_t row0 = x.row0;
+  const int n = g - cr.first + 1;
   // the first part is the last item of its CTA (slot 1), the others the first of theirs (slot 0)
   const float *part0 = p.part + (2 * cr.first + 1) * kPartFloats, *part1 = p.part + 2 * (cr.first + 1) * kPartFloats;
   auto part = [&](int k) { return k == 0 ? part0 : part1 + 2 * static_cast<int64_t>(k - 1) * kPartFloats; };
+  const int d = threadIdx.x & 127, half = threadIdx.x >> 7, i4 = 2 * y + half;
+  const int at4 = ((b0 * 16 + i4) * 128 + d) * 4;
+  float4 v[kParts][kDims];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int k = 0; k < kParts; ++k)
+      if (k0 + k < n) {
+#pragma unroll
+        for (int b = 0; b < kDims; ++b) v[k][b] = *reinterpret_cast<const float4 *>(part(k0 + k) + at4 + b * 16 * 128 * 4);
+      }
+  };
+  load(0);
+  const RowTile &x = p.tile[cr.tile];
+  const int nrows = x.nrows;
+  if (8 * y >= nrows) return;
+  const int64_t row0 = x.row0;
   {  // warp = row: the parts' weights, normalised
     const int r = 8 * y + warp;
     float m = -INFINITY, l = 0.0f;
-    for (int k = lane; k < n; k += 32) m = fmaxf(m, part(k)[kLat * kRows + 2 * r]);
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     for (int k = lane; k < n; k += 32) {
       const float2 ml = *reinterpret_cast<const float2 *>(part(k) + kLat * kRows + 2 * r);
-      const float w = ml.x == -INFINITY ? 0.0f : ex2(ml.x - m);
+      wt[k][warp] = ml.x;
+      ls[k][warp] = ml.y;
+      m = fmaxf(m, ml.x);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int k = lane; k < n; k += 32) {  // (what this lane stored)
+      const float mk = wt[k][warp], w = mk == -INFINITY ? 0.0f : ex2(mk - m);
       wt[k][warp] = w;
-      l = fmaf(w, ml.y, l);
+      l = fmaf(w, ls[k][warp], l);
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
@@ -1160,32 +1192,33 @@ __global__ void __launch_bounds__(256) k_chunk_merge(ChunkArgs a, Plan p) {
     }
     f = l > 0.0f ? f / l : 0.0f;
     for (int k = lane; k < n; k += 32) wt[k][warp] *= f;
-    if (lane == 0 && r < nrows) a.lse[row0 + r] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (b0 == 0 && lane == 0 && r < nrows) a.lse[row0 + r] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
   }
   __syncthreads();
-  // thread = one dim of each 128-dim block, four rows
-  const int d = threadIdx.x & 127, half = threadIdx.x >> 7, i4 = 2 * y + half;
-  float o[4][4] = {};
-#pragma unroll 2
-  for (int k = 0; k < n; ++k) {
-    const float *q = part(k) + (i4 * 128 + d) * 4;
-    const float4 w = *reinterpret_cast<const float4 *>(&wt[k][4 * half]);
+  float o[kDims][4] = {};
+  for (int k0 = 0;; k0 += kParts) {
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const float4 v = *reinterpret_cast<const float4 *>(q + b * 16 * 128 * 4);
-      o[b][0] = w.x == 0.0f ? o[b][0] : fmaf(w.x, v.x, o[b][0]);
-      o[b][1] = w.y == 0.0f ? o[b][1] : fmaf(w.y, v.y, o[b][1]);
-      o[b][2] = w.z == 0.0f ? o[b][2] : fmaf(w.z, v.z, o[b][2]);
-      o[b][3] = w.w == 0.0f ? o[b][3] : fmaf(w.w, v.w, o[b][3]);
+    for (int k = 0; k < kParts; ++k) {
+      if (k0 + k >= n) break;
+      const float4 w = *reinterpret_cast<const float4 *>(&wt[k0 + k][4 * half]);
+#pragma unroll
+      for (int b = 0; b < kDims; ++b) {  // (a part without keys of a row holds nothing for it)
+        o[b][0] = w.x == 0.0f ? o[b][0] : fmaf(w.x, v[k][b].x, o[b][0]);
+        o[b][1] = w.y == 0.0f ? o[b][1] : fmaf(w.y, v[k][b].y, o[b][1]);
+        o[b][2] = w.z == 0.0f ? o[b][2] : fmaf(w.z, v[k][b].z, o[b][2]);
+        o[b][3] = w.w == 0.0f ? o[b][3] : fmaf(w.w, v[k][b].w, o[b][3]);
+      }
     }
+    if (k0 + kParts >= n) break;
+    load(k0 + kParts);
   }
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int row = 4 * i4 + r;
     if (row >= nrows) break;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int64_t at = (row0 + row) * kLat + 128 * b + d;
+    for (int b = 0; b < kDims; ++b) {
+      const int64_t at = (row0 + row) * kLat + 128 * (b0 + b) + d;
       if (a.bf16) static_cast<__nv_bfloat16 *>(a.out)[at] = __float2bfloat16_rn(o[b][r]);
       else static_cast<float *>(a.out)[at] = o[b][r];
     }
@@ -1193,7 +1226,7 @@ __global__ void __launch_bounds__(256) k_chunk_merge(ChunkArgs a, Plan p) {
 }
 
 struct PlanLayout {
-  size_t seq_tile, cum, tile, cta, part, total;
+  size_t seq_tile, cum, tile, cta, merge, part, total;
   int max_tiles, n_cta;
 };
 PlanLayout plan_layout(int batch, int total, int heads) {
@@ -1211,6 +1244,8 @@ PlanLayout plan_layout(int batch, int total, int heads) {
   o = up(o + static_cast<size_t>(t) * sizeof(RowTile));
   L.cta = o;
   o = up(o + static_cast<size_t>(L.n_cta) * sizeof(CtaRange));
+  L.merge = o;
+  o = up(o + static_cast<size_t>(L.n_cta) * 4);
   L.part = o;
   o = up(o + static_cast<size_t>(2) * L.n_cta * kPartFloats * 4);
   L.total = o;
@@ -1260,7 +1295,7 @@ csa2_status csa2_chunk_attn(const csa2_cache *cache, const uint16_t *q, int32_t 
   uint8_t *wb = static_cast<uint8_t *>(ws);
   csa2::Plan p{reinterpret_cast<int32_t *>(wb + L.seq_tile), reinterpret_cast<int64_t *>(wb + L.cum),
                reinterpret_cast<csa2::RowTile *>(wb + L.tile), reinterpret_cast<csa2::CtaRange *>(wb + L.cta),
-               reinterpret_cast<float *>(wb + L.part), L.max_tiles, L.n_cta};
+               reinterpret_cast<int32_t *>(wb + L.merge), reinterpret_cast<float *>(wb + L.part), L.max_tiles, L.n_cta};
   const int smem = static_cast<int>(sizeof(csa2::ChunkSmem)) + 1024;
   static_assert(sizeof(csa2::ChunkSmem) + 1024 <= 232448, "shared memory of one CTA");
   cudaError_t e = csa2::ensure_smem_limit(reinterpret_cast<const void *>(&csa2::k_chunk_attn), smem);
@@ -1283,10 +1318,16 @@ csa2_status csa2_chunk_attn(const csa2_cache *cache, const uint16_t *q, int32_t 
     e = cudaLaunchKernelEx(&cfg, csa2::k_chunk_attn, a, p);
   }
   if (e == cudaSuccess) {
-    cfg.gridDim = dim3(L.n_cta, csa2::kRows / 8);
+    // up to 64 shared row tiles: a block per 128 dims (over 152 CTAs, 4 row tiles take
+    // 9.3 us against 12.5, 16 take 9.5 against 12.6, one of 40 parts 6.0 against 8.5);
+    // more of them, of fewer parts each, fill the SMs without (65: 9.2 us against
+    // 10.6; 152: 12.7 against 24.0)
+    const int shared = L.n_cta < L.max_tiles ? L.n_cta : L.max_tiles, split = shared <= 64 ? 4 : 1;
+    cfg.gridDim = dim3(shared, csa2::kRows / 8 * split);
     cfg.blockDim = dim3(256);
     cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, csa2::k_chunk_merge, a, p);
+    e = split == 4 ? cudaLaunchKernelEx(&cfg, csa2::k_chunk_merge<1>, a, p)
+                   : cudaLaunchKernelEx(&cfg, csa2::k_chunk_merge<4>, a, p);
   }
   return cuda_status(e, "csa2_chunk_attn launch");
 }
