@@ -34,7 +34,7 @@ constexpr int kBlocks = kDqk / 64;           // 9: 8 latent, 1 RoPE
 constexpr int kTile = kBlocks * kBlk;        // 73,728 B
 constexpr int kSmWarps = 8, kPrWarps = 16;   // softmax / producer warps
 constexpr int kMmaWarp = kSmWarps + kPrWarps, kAheadWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kAheadWarp + 1);
+constexpr int kThreads = 32 * (kAheadWarp + 3);  // whole warpgroups
 static_assert(kPrWarps == 16, "plain is read as 16 bytes");
 constexpr int kAhead = 4;                    // key tiles requested into L2 ahead of use
 constexpr uint32_t kColS = 0, kColO = 256;   // TMEM columns: S 2 x 64, O^T 4 x 64
@@ -1113,12 +1113,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunk_attn(const __grid_constan
   if (warp < kSmWarps) {
     softmax(a, p, sm, tmem, warp, lane);
   } else if (warp < kMmaWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 80;\n");
     if (a.c.entry_format == CSA2_ENTRY_FP8) produce<RawFp8>(a, p, sm, tid - 32 * kSmWarps);
     else produce<RawFp4>(a, p, sm, tid - 32 * kSmWarps);
-  } else if (warp == kMmaWarp) {
-    issue(a, p, sm, tmem);
-  } else if (lane == 0) {
-    ahead(a, p, sm);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
+    if (warp == kMmaWarp) issue(a, p, sm, tmem);
+    else if (warp == kAheadWarp && lane == 0) ahead(a, p, sm);
   }
   tc::tc_fence_before();
   __syncthreads();
