@@ -1111,13 +1111,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunk_attn(const __grid_constan
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the plan is written
   if (warp < kSmWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 80;\n");
     softmax(a, p, sm, tmem, warp, lane);
   } else if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 80;\n");
     if (a.c.entry_format == CSA2_ENTRY_FP8) produce<RawFp8>(a, p, sm, tid - 32 * kSmWarps);
     else produce<RawFp4>(a, p, sm, tid - 32 * kSmWarps);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 24;\n");
     if (warp == kMmaWarp) issue(a, p, sm, tmem);
     else if (warp == kAheadWarp && lane == 0) ahead(a, p, sm);
   }
