@@ -101,9 +101,9 @@ __device__ __forceinline__ void copy_older(const RaggedAppend &a, int part) {
 // by at least 2^-24 of it, the rounding of the quotient next to t by no more than
 // 2^-24 of t: never enough to carry it over (2^-25 below a power of two).
 __device__ __forceinline__ uint2 nvfp4_16(const float *x, uint32_t *scale) {
-  float amax = 0.0f;
+  float amax = fabsf(x[0]);  // (NaN only where all sixteen are)
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+  for (int i = 1; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
   const uint32_t sc = e4m3_code(__fdiv_rn(amax, 6.0f));
   const float s = e4m3_value(sc);
   if (s == 0.0f) {
@@ -255,9 +255,9 @@ __global__ void __launch_bounds__(256, 4) k_ragged_append_r1(RaggedAppend a, int
   uint4 lat8 = make_uint4(0, 0, 0, 0);
   uint32_t lat8_sc = 0;
   if ((fp8 && pl.pe >= 0) || (mx && pl.win >= 0)) {
-    float amax = 0.0f, inv;
+    float amax = fabsf(cur.x[0]), inv;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(cur.x[j]));
+    for (int j = 1; j < 16; ++j) amax = fmaxf(amax, fabsf(cur.x[j]));
     amax = max_over(amax, 2);
     mxfp8_scale(amax, &inv, &lat8_sc);
     if (amax != 0.0f) {
