@@ -513,6 +513,8 @@ def kv_append_ragged(cache: Cache, cu_new, rope_cs, kv=None, idx_key=None, cmp=N
             _want(f"cmp[{i}]", t, torch.float32, (total, D_CMP) if i < 4 else (2, D_CMP), like)
         cin = ctypes.byref(CompressIn(*[t.data_ptr() for t in cmp]))
     wc, ws = _window_ptrs(cache, win, total)
+    if total == 0:  # (empty tensors have no address)
+        return
     _call("csa2_kv_append_ragged", cache, stream, _adr(kv), ks, _adr(idx_key), is_, dt, cin, _adr(cu_new), total,
           total if max_new is None else max_new, _adr(rope_cs), rope_cs.shape[0], wc, ws, _adr(err))
 
@@ -537,6 +539,8 @@ def kv_read(cache: Cache, cu_rows, out_main=None, out_key=None, pos=None, start=
         _want("pos", pos, torch.int32, (total,), like)
     else:
         _want("start", start, torch.int64, (cache.batch,), like)
+    if total == 0:
+        return
     _call("csa2_kv_read", cache, stream, _adr(cu_rows), total, _adr(pos), _adr(start), _adr(out_main), ms, _adr(out_key),
           ks, _out_dtype(first), _adr(err))
 
@@ -569,6 +573,8 @@ def chunk_attn(cache: Cache, q, cu_q, out, lse, ws, sm_scale, max_new=None, win=
     if sink is not None:
         _want("sink", sink, torch.float32, (H,), like)
     wc, wsc = _window_ptrs(cache, win, total)
+    if total == 0:
+        return
     _call("csa2_chunk_attn", cache, stream, _adr(q), H, _adr(cu_q), total, total if max_new is None else max_new, wc, wsc,
           _adr(sink), sm_scale, _adr(out), _out_dtype(out), _adr(lse), _adr(ws), ws.numel(), _adr(err))
 

@@ -17,6 +17,7 @@
 // heads 430 flop per byte, so the tensor cores bound it, not HBM.  fp16 operands
 // hold the records exactly (E2M1 x E4M3 has 6 significant bits; other formats
 // with a power of two per key), accumulators are fp32.
+#include <atomic>
 #include <cmath>
 #include <cuda_fp16.h>
 
@@ -34,7 +35,11 @@ constexpr int kBlocks = kDqk / 64;           // 9: 8 latent, 1 RoPE
 constexpr int kTile = kBlocks * kBlk;        // 73,728 B
 constexpr int kSmWarps = 8, kPrWarps = 16;   // softmax / producer warps
 constexpr int kMmaWarp = kSmWarps + kPrWarps, kAheadWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kAheadWarp + 3);  // whole warpgroups
+constexpr int kThreads = 32 * (kAheadWarp + 3);  // whole warpgroups: 2 softmax, 4 producers, 1 that issues
+// Registers per thread: 7 x 72 at the launch, then moved from the issuing
+// warpgroup to the others (spills in their loops cost 6 to 11 % of the time).
+constexpr int kLaunchRegs = 72, kWorkRegs = 80, kIssueRegs = 24;
+static_assert(6 * kWorkRegs + kIssueRegs <= 7 * kLaunchRegs, "setmaxnreg draws on the launch's registers");
 static_assert(kPrWarps == 16, "plain is read as 16 bytes");
 constexpr int kAhead = 4;                    // key tiles requested into L2 ahead of use
 constexpr uint32_t kColS = 0, kColO = 256;   // TMEM columns: S 2 x 64, O^T 4 x 64
@@ -622,23 +627,33 @@ __device__ __noinline__ bool fill_tail(const ChunkArgs &a, const Plan &p, ChunkS
 #pragma unroll
   for (int s = 0; s < 5; ++s) tail_load(t, s, o, r[s]);
   int e8 = 0;
-  uint32_t bf = 0;
+  uint32_t bf = 0, lat = 0;  // largest magnitude bits of all bf16 values, of a bf16 window's latents
   if (t.kind == 2) {
     e8 = e8m0_top(ldg16(t.scales));
     bf = bf16_top(r[4].w[0], 0);
   } else if (t.kind == 3) {
     e8 = max(e8m0_top(ldg16(t.scales)), static_cast<int>(max(__ldg(t.rope_scales), __ldg(t.rope_scales + 1))));
   } else if (t.kind == 4) {
-    bf = bf16_top(r[4].w[0], 0);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) bf = bf16_top(r[s].w[1], bf16_top(r[s].w[0], bf));
+    for (int s = 0; s < 4; ++s) lat = bf16_top(r[s].w[1], bf16_top(r[s].w[0], lat));
+    bf = bf16_top(r[4].w[0], lat);
   }
   bf = key_max(bf);
+  lat = key_max(lat);
+  // A latent that is infinite or NaN would reach every row of the tile in PV (0 x it),
+  // also those that do not see the key.  The key's latents go in as zeros, and its
+  // logit is NaN for the rows that do.
+  const bool poison = max(lat & 0xFFFF, lat >> 16) >= 0x7F80;
+  if (poison) {
+#pragma unroll
+    for (int s = 0; s < 4; ++s) r[s].w[0] = r[s].w[1] = make_uint4(0, 0, 0, 0);
+  }
   const int sigma = t.kind >= 2 ? sigma_of(key_exponent(e8, bf)) : 0;
   if (n >= 2 && !dead) dead = !wait_warp(&sm.empty[b], ((n >> 1) & 1) ^ 1, a.err);
   if (pt == 0) *const_cast<volatile uint32_t *>(&sm.progress) = n;
   if ((pt & 31) == 0) sm.plain[b][pt >> 5] = 0;
-  if (o == 0) sm.sg[b][key] = t.kind ? make_float2(static_cast<float>(sigma), pow2f(sigma)) : make_float2(-INFINITY, 0.0f);
+  if (o == 0)
+    sm.sg[b][key] = t.kind ? make_float2(poison ? NAN : static_cast<float>(sigma), pow2f(sigma)) : make_float2(-INFINITY, 0.0f);
 #pragma unroll
   for (int s = 0; s < 5; ++s) tail_store(sm.k[b], t, s, key, o, r[s], sigma);
   return dead;
@@ -958,11 +973,12 @@ __device__ __forceinline__ void softmax(const ChunkArgs &a, const Plan &p, Chunk
           const float z = a.sink[(x->head0 + r) % a.heads] * kLog2e;
           const float mf = fmaxf(m, z);
           f = m == -INFINITY ? 0.0f : ex2(m - mf);
-          sum = sum * f + ex2(z - mf);
+          sum = sum * f + (z == mf ? 1.0f : ex2(z - mf));  // (an infinite sink too)
           m = mf;
         }
-        sm.fin[r] = sum > 0.0f ? f / sum : 0.0f;
-        if (r < x->nrows && !dead) a.lse[x->row0 + r] = sum > 0.0f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+        // (0: a row without keys; NaN stays NaN)
+        sm.fin[r] = sum == 0.0f ? 0.0f : f / sum;
+        if (r < x->nrows && !dead) a.lse[x->row0 + r] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * kLn2;
       }
     }
     more = it.next(p, blockIdx.x);
@@ -1111,14 +1127,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunk_attn(const __grid_constan
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");  // the plan is written
   if (warp < kSmWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 80;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kWorkRegs));
     softmax(a, p, sm, tmem, warp, lane);
   } else if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 80;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kWorkRegs));
     if (a.c.entry_format == CSA2_ENTRY_FP8) produce<RawFp8>(a, p, sm, tid - 32 * kSmWarps);
     else produce<RawFp4>(a, p, sm, tid - 32 * kSmWarps);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 24;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kIssueRegs));
     if (warp == kMmaWarp) issue(a, p, sm, tmem);
     else if (warp == kAheadWarp && lane == 0) ahead(a, p, sm);
   }
@@ -1189,12 +1205,12 @@ __global__ void __launch_bounds__(256) k_chunk_merge(ChunkArgs a, Plan p) {
     if (a.sink != nullptr) {
       const float z = a.sink[(x.head0 + r) % a.heads] * kLog2e, mf = fmaxf(m, z);
       f = m == -INFINITY ? 0.0f : ex2(m - mf);
-      l = l * f + ex2(z - mf);
+      l = l * f + (z == mf ? 1.0f : ex2(z - mf));
       m = mf;
     }
-    f = l > 0.0f ? f / l : 0.0f;
+    f = l == 0.0f ? 0.0f : f / l;
     for (int k = lane; k < n; k += 32) wt[k][warp] *= f;
-    if (b0 == 0 && lane == 0 && r < nrows) a.lse[row0 + r] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (b0 == 0 && lane == 0 && r < nrows) a.lse[row0 + r] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
   }
   __syncthreads();
   float o[kDims][4] = {};
@@ -1302,6 +1318,16 @@ csa2_status csa2_chunk_attn(const csa2_cache *cache, const uint16_t *q, int32_t 
   static_assert(sizeof(csa2::ChunkSmem) + 1024 <= 232448, "shared memory of one CTA");
   cudaError_t e = csa2::ensure_smem_limit(reinterpret_cast<const void *>(&csa2::k_chunk_attn), smem);
   if (e != cudaSuccess) return cuda_status(e, "csa2_chunk_attn shared memory");
+  // (built with fewer registers at the launch, it would wait for some that do not exist)
+  static std::atomic<int> regs{0};
+  if (regs.load(std::memory_order_relaxed) == 0) {
+    cudaFuncAttributes at{};
+    e = cudaFuncGetAttributes(&at, reinterpret_cast<const void *>(&csa2::k_chunk_attn));
+    if (e != cudaSuccess) return cuda_status(e, "csa2_chunk_attn attributes");
+    regs.store(at.numRegs, std::memory_order_relaxed);
+  }
+  CSA2_REQUIRE(regs.load(std::memory_order_relaxed) >= csa2::kLaunchRegs, CSA2_ERR_CUDA,
+               "csa2_chunk_attn was built with %d registers per thread", regs.load(std::memory_order_relaxed));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   csa2::k_chunk_plan<<<1, 1024, 0, s>>>(a, p);
   e = cudaGetLastError();

@@ -410,7 +410,8 @@ size_t csa2_chunk_window_bytes(int32_t batch, int32_t total, int32_t swa_dtype, 
  *   ratio 2: cmp rows [total][704] each; kv = idx_key = NULL, strides ignored.
  *   win_codes / win_scales: the chunk's window rows (above), or NULL.
  * The call reads the ring before it overwrites it; win_codes must not be in use
- * by an earlier call on another stream.  total 0 is a valid call (nothing done).
+ * by an earlier call on another stream.  total 0 and max_new 0 are valid calls
+ * (nothing done), here and in csa2_chunk_attn.
  * Device errors: CAPACITY, ROPE (nothing written for the sequence, its n_tokens
  * stays), INDEX (a page id outside the pool, cu, max_new).
  */
@@ -462,6 +463,11 @@ csa2_status csa2_window_read(const csa2_cache *cache, void *out, int32_t out_dty
  *      without those tokens).
  *   sink: fp32 [n_heads] or NULL; sm_scale finite.
  *   out: out_dtype [total][n_heads][512]; lse: fp32 [total][n_heads].
+ *   A row that sees nothing (bad pages, no sink) is zeros with lse -inf.  Values
+ *   of tokens that a row does not see never reach it: a window token with an
+ *   infinite or NaN latent (a bf16 window holds them as they are) makes the rows
+ *   that see it NaN, and only those.  Records hold no NaN codes: the appends
+ *   write none.
  * n_heads: a multiple of 16, 16..128.  The work is split over the GPU by the
  * batch's total work, so a row's last bits may change with the batch (use
  * csa2_sparse_attn_decode where batch invariance is needed); equal calls give

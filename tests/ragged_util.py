@@ -64,8 +64,10 @@ def window_values(codes, scales, swa):
 
 def chunk_attn(c, q, cu, scale, win=None, sink=None):
     """out, lse in fp64, and per output element the sum of p |c| (what a relative
-    error of the weights is multiplied by) and per row the sum of |z| terms."""
-    cu, outs, lses, mags, dots = cu.tolist(), [], [], [], []
+    error of the weights is multiplied by), per row the sum of |z| terms, and per
+    output element what the small weights' absolute error is multiplied by (see
+    attn_within): W sum |c| 2^-sigma, W = max p 2^sigma over the keys a row sees."""
+    cu, outs, lses, mags, dots, smalls = cu.tolist(), [], [], [], [], []
     dev = q.device
     for b in range(c.batch):
         n = cu[b + 1] - cu[b]
@@ -87,6 +89,11 @@ def chunk_attn(c, q, cu, scale, win=None, sink=None):
         see = torch.cat([torch.arange(T, device=dev)[None] < pos // c.ratio,
                          (tok[None] >= 0) & (tok[None] <= pos) & (tok[None] > pos - WIN)], -1)
         k = torch.where(see.any(0)[:, None], k, 0.0)
+        top = k.abs().amax(-1)
+        e = torch.frexp(top)[1].double() - 1  # 2^e <= top < 2^(e+1)
+        sigma = torch.where((top == 0) | ((e >= 0) & (e <= 15)), 0.0, (e - 8).clamp(-24, 120))
+        if c.entry_format == csa2.ENTRY_FP4:
+            sigma[:T] = 0
         qd = q[cu[b]:cu[b + 1]].double()
         z = torch.einsum("qhd,td->qht", qd, k) * scale
         z = z.masked_fill(~see[:, None], -math.inf)
@@ -101,8 +108,11 @@ def chunk_attn(c, q, cu, scale, win=None, sink=None):
         outs.append(torch.einsum("qht,td->qhd", p, k[:, :512]))
         mags.append(torch.einsum("qht,td->qhd", p, k[:, :512].abs()))
         lses.append((m + den.log())[..., 0])
+        s2 = torch.exp2(sigma)
+        W = (p * s2).amax(-1)
+        smalls.append(W[..., None] * torch.einsum("qt,td->qd", see.double(), k[:, :512].abs() / s2[:, None])[:, None])
         dots.append(torch.einsum("qhd,td->qht", qd.abs(), k.abs()).masked_fill(~see[:, None], 0.0).amax(-1) * abs(scale))
-    return torch.cat(outs), torch.cat(lses), torch.cat(mags), torch.cat(dots)
+    return torch.cat(outs), torch.cat(lses), torch.cat(mags), torch.cat(dots), torch.cat(smalls)
 
 
 def attn_within(out, lse, ref, live=None):
@@ -111,17 +121,19 @@ def attn_within(out, lse, ref, live=None):
     The operands' values are exact.  A logit is a sum of 36 blocks of 16 exact
     products accumulated in fp32: off by at most 40 * 2^-23 of the sum of its
     terms' magnitudes (each fp32 addition by one unit at most), and so is lse,
-    plus 2^-22 relative for the sum and the logarithm.  The weights are rounded
-    to fp16 (2^-11 relative; below 2^-14 of the scaled maximum 2^8 or more, so an
-    absolute 2^-33 per key, nothing here) and carry the logits' error; a bf16
-    output adds 2^-8 of its value."""
-    o, l, mag, dot = ref
+    plus 2^-22 relative for the sum and the logarithm.  The weights (times a power
+    of two 2^sigma of their key, whose values are divided by it) are rounded to
+    fp16 on a scale on which the largest is 2^4 at least: 2^-11 relative, or below
+    2^-14, where fp16's step is 2^-24, an absolute 2^-25.  That is 2^-25 / 2^4 =
+    2^-29 of the largest weighted weight W per key, times |c| 2^-sigma, summed.
+    They carry the logits' error; a bf16 output adds 2^-8 of its value."""
+    o, l, mag, dot, small = ref
     if live is not None:
         out, lse = out[live], lse[live]
     ez = 40 * 2.0 ** -23 * dot + 2.0 ** -22 * (1 + l.abs())
     assert torch.isfinite(out.float()).all()
     assert ((lse.double() - l).abs() <= ez).all(), float(((lse.double() - l).abs() / ez).max())
-    tol = (2.0 ** -11 + 2.0 ** -16 + 2 * ez[..., None]) * mag + 2.0 ** -30
+    tol = (2.0 ** -11 + 2.0 ** -16 + 2 * ez[..., None]) * mag + 2.0 ** -29 * small + 2.0 ** -30
     if out.dtype == torch.bfloat16:
         tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * o.abs()
     err = (out.double() - o).abs()

@@ -515,3 +515,179 @@ def test_python_refusals():
     with pytest.raises(csa2.Csa2Error):
         csa2.chunk_attn(c, q, cu, o, l, ws, float("nan"))
     assert c.n_tokens.tolist() == [10, 5]
+
+
+@pytest.mark.parametrize("swa", [csa2.SWA_MXFP8, csa2.SWA_BF16])
+@pytest.mark.parametrize("fmt", [csa2.ENTRY_FP4, csa2.ENTRY_FP8])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_append_special_values(swa, fmt, bf16):
+    """NaN, infinities, zeros of both signs, subnormals, wide ranges and values halfway between codes:
+    the bytes of csa2_kv_append."""
+    n = 96
+    g = torch.Generator(device=DEV).manual_seed(3)
+    kv, ik = (torch.randn(n, w, generator=g, device=DEV) for w in (576, 128))
+    for t in (kv, ik):
+        t[1] = 0.0
+        t[2] = -0.0
+        t[3, 5], t[4, 7], t[5, 9] = math.nan, math.inf, -math.inf
+        t[6] = math.nan
+        t[7] = -math.inf
+        t[8] *= 2.0 ** -140
+        t[9] *= 2.0 ** 120
+        t[10] = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0], device=DEV).repeat(t.shape[1] // 8)
+        t[11] = -t[10] * 3
+        t[12] = 0.0
+        t[12, -1] = 2.0 ** -20
+        t[13:40] *= torch.exp2(torch.randint(-30, 30, t[13:40].shape, generator=g, device=DEV).float())
+        t[40:60] = t[40:60].to(torch.float8_e4m3fn).float() * 1.0625
+    if bf16:
+        kv, ik = kv.to(torch.bfloat16), ik.to(torch.bfloat16)
+    rope = csa2.rope_table(THETA, 256)
+    a, b = (_cache(1, 256, swa=swa, fmt=fmt) for _ in range(2))
+    ea, eb = _err(), _err()
+    csa2.kv_append_ragged(a, _cu([n]), rope, kv=kv, idx_key=ik, err=ea)
+    csa2.kv_append(b, kv[None], ik[None], rope, err=eb)
+    assert int(ea) == int(eb) == 0
+    for name in ("lat_codes", "lat_scales", "rope_codes", "rope_scales", "idx_codes", "idx_scales", "swa_codes", "swa_scales"):
+        x, y = getattr(a, name), getattr(b, name)
+        if x is not None and not (name == "swa_scales" and swa == csa2.SWA_BF16):
+            assert torch.equal(x, y), name
+
+
+@pytest.mark.parametrize("fmt", [csa2.ENTRY_FP4, csa2.ENTRY_FP8])
+def test_kv_read_rows_on_16_bytes(fmt):
+    """fp32 rows that start 16 B, not 32 B, aligned."""
+    c, _ = _filled(1, [70], 128, fmt=fmt)
+    zero = torch.zeros(1, dtype=torch.int64, device=DEV)
+    want, wk = torch.empty(70, 576, device=DEV), torch.empty(70, 128, device=DEV)
+    csa2.kv_read(c, _cu([70]), out_main=want, out_key=wk, start=zero)
+    main = torch.full((70 * 576 + 8,), 9.0, device=DEV)
+    key = torch.full((70 * 128 + 8,), 9.0, device=DEV)
+    csa2.kv_read(c, _cu([70]), out_main=main[4:-4].view(70, 576), out_key=key[4:-4].view(70, 128), start=zero)
+    assert torch.equal(main[4:-4].view(70, 576), want) and torch.equal(key[4:-4].view(70, 128), wk)
+    for t in (main, key):
+        assert (t[:4] == 9).all() and (t[-4:] == 9).all()
+
+
+def test_far_pages():
+    """Pages at the end of a pool whose planes pass 2^32 bytes."""
+    n_pages, page = 18000, 1024  # 18.4 M entries: 4.7 GB of latent codes
+    table = torch.tensor([[n_pages - 1, 0], [n_pages - 3, n_pages - 2]], dtype=torch.int32)
+    c = csa2.Cache(2, 2 * page, page_entries=page, n_pages=n_pages, block_table=table)
+    lens = [1100, 1500]
+    g = torch.Generator(device=DEV).manual_seed(9)
+    rope, err = csa2.rope_table(THETA, 2 * page), _err()
+    kv, ik = (torch.randn(sum(lens), w, generator=g, device=DEV) for w in (576, 128))
+    csa2.kv_append_ragged(c, _cu(lens), rope, kv=kv, idx_key=ik, err=err)
+    near = csa2.Cache(2, 2 * page)
+    csa2.kv_append_ragged(near, _cu(lens), rope, kv=kv, idx_key=ik, err=err)
+    q, zero = _q(2, 64), torch.zeros(2, dtype=torch.int64, device=DEV)
+    outs = []
+    for x in (c, near):
+        main, key = torch.empty(sum(lens), 576, device=DEV), torch.empty(sum(lens), 128, device=DEV)
+        csa2.kv_read(x, _cu(lens), out_main=main, out_key=key, start=zero, err=err)
+        outs.append((main, key) + _attn(x, q, _cu([1, 1]), max_new=1))
+    assert int(err) == 0 and outs[0][4] == outs[1][4] == 0
+    for x, y in zip(outs[0][:4], outs[1][:4]):
+        assert torch.equal(x, y)
+
+
+def test_many_sequences():
+    """More sequences and row tiles than the plan keeps in shared memory; some sequences idle."""
+    B, H = 1500, 128
+    g = torch.Generator().manual_seed(10)
+    prior = torch.randint(0, 20, (B,), generator=g).tolist()
+    new = torch.randint(0, 3, (B,), generator=g).tolist()
+    c, rope = _filled(B, prior, 24)
+    total, cu, err = sum(new), _cu(new), _err()
+    assert total * H > 2048 * 64
+    win = csa2.chunk_window(c, total)
+    csa2.kv_append_ragged(c, cu, rope, kv=torch.randn(total, 576, device=DEV), idx_key=torch.randn(total, 128, device=DEV),
+                          max_new=2, win=win, err=err)
+    q = _q(total, H)
+    out, lse, e = _attn(c, q, cu, win, max_new=2)
+    assert e == 0 and int(err) == 0
+    ru.attn_within(out, lse, ru.chunk_attn(c, q, cu, 1 / math.sqrt(576), win))
+
+
+def test_two_calls_at_once():
+    """Two attentions with a workspace each, on two streams, over one cache, beside an append to another."""
+    c, rope = _filled(4, [3000, 2000, 2500, 10], 4096, page=128)
+    d, _ = _filled(4, [50, 60, 70, 80], 4096)
+    q1, q2 = _q(4, 64, seed=1), _q(4, 128, seed=2)
+    cu = _cu([1, 1, 1, 1])
+    want = [_attn(c, q, cu, max_new=1)[:2] for q in (q1, q2)]
+    kv, ik, cu_d = torch.randn(800, 576, device=DEV), torch.randn(800, 128, device=DEV), _cu([200, 200, 200, 200])
+    err, streams = _err(), [torch.cuda.Stream() for _ in range(3)]
+    got = [(torch.zeros_like(o), torch.zeros_like(l)) for o, l in want]
+    ws = [csa2.chunk_attn_workspace(4, H, 4) for H in (64, 128)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        csa2.kv_append_ragged(d, cu_d, rope, kv=kv, idx_key=ik, err=err, stream=streams[2])
+        for i, q in enumerate((q1, q2)):
+            csa2.chunk_attn(c, q, cu, got[i][0], got[i][1], ws[i], 1 / math.sqrt(576), max_new=1, err=err, stream=streams[i])
+    torch.cuda.synchronize()
+    assert int(err) == 0 and d.n_tokens.tolist() == [2050, 2060, 2070, 2080]
+    for (o, l), (wo, wl_) in zip(got, want):
+        assert torch.equal(o, wo) and torch.equal(l, wl_)
+
+
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_chunk_attn_masked_nonfinite(bad):
+    """A bf16 window holds infinities and NaN as they come: the rows that see such a token are NaN, the
+    others (earlier ones, later than 127 tokens, in the same row tiles) know nothing of it."""
+    c, rope = _filled(2, [90, 20], 512, swa=csa2.SWA_BF16)
+    n, at, H = [200, 3], 30, 16
+    cu, total = _cu(n), sum(n)
+    win = csa2.chunk_window(c, total)
+    g = torch.Generator(device=DEV).manual_seed(6)
+    kv, ik = torch.randn(total, 576, generator=g, device=DEV), torch.randn(total, 128, generator=g, device=DEV)
+    kv[at, 77] = bad
+    csa2.kv_append_ragged(c, cu, rope, kv=kv, idx_key=ik, max_new=200, win=win)
+    q = _q(total, H)
+    sees = torch.zeros(total, dtype=torch.bool, device=DEV)
+    sees[at:at + 128] = True
+    out, lse, e = _attn(c, q, cu, win, max_new=200)
+    assert e == 0 and out[sees].isnan().all() and lse[sees].isnan().all()
+    clean = csa2.ChunkWindow(win.codes.clone(), win.scales)
+    clean.codes[128 + at] = 0  # (the plain form would multiply it by zero)
+    ru.attn_within(out[~sees], lse[~sees], [t[~sees] for t in ru.chunk_attn(c, q, cu, 1 / math.sqrt(576), clean)])
+
+
+def test_chunk_attn_nonfinite_query_and_sink():
+    """A query that is not finite spoils its own row; a sink of +inf takes all the weight, one of -inf none."""
+    c, _ = _filled(3, [2000, 150, 1], 2048)
+    H, cu = 32, _cu([1, 1, 1])
+    q = _q(3, H)
+    plain, pl, _ = _attn(c, q, cu, max_new=1)
+    bad = q.clone()
+    bad[0, 3, 100], bad[1, 31, 570], bad[2, 0, 0] = math.nan, math.inf, -math.inf
+    out, lse, e = _attn(c, bad, cu, max_new=1)
+    hit = torch.zeros(3, H, dtype=torch.bool, device=DEV)
+    hit[0, 3] = hit[1, 31] = hit[2, 0] = True
+    assert e == 0 and torch.equal(out[~hit], plain[~hit]) and torch.equal(lse[~hit], pl[~hit])
+    assert out[0, 3].isnan().all() and lse[0, 3].isnan()
+    sink = torch.zeros(H, device=DEV)
+    sink[0], sink[1] = math.inf, -math.inf
+    out, lse, e = _attn(c, q, cu, sink=sink, max_new=1)
+    assert e == 0 and not out[:, 0].any() and (lse[:, 0] == math.inf).all()
+    ez = 2.0 ** -20  # the sums are the same up to their last bits
+    assert ((out[:, 1] - plain[:, 1]).abs() <= ez * plain[:, 1].abs()).all() and ((lse - pl)[:, 1].abs() <= ez * (1 + pl[:, 1].abs())).all()
+
+
+def test_empty_calls():
+    """No rows at all, and no sequence with any."""
+    c, rope = _filled(2, [10, 5], 128)
+    before = {n: getattr(c, n).clone() for n in ("n_tokens", "lat_codes", "swa_codes")}
+    e = lambda *s, **k: torch.empty(0, *s, device=DEV, **k)
+    cu, err = _cu([0, 0]), _err()
+    csa2.kv_append_ragged(c, cu, rope, kv=e(576), idx_key=e(128), err=err)
+    csa2.kv_read(c, cu, out_main=e(576), out_key=e(128), start=torch.zeros(2, dtype=torch.int64, device=DEV), err=err)
+    csa2.chunk_attn(c, e(64, 576, dtype=torch.bfloat16), cu, e(64, 512), e(64), csa2.chunk_attn_workspace(0, 64, 2), 0.1, err=err)
+    kv, ik = torch.randn(3, 576, device=DEV), torch.randn(3, 128, device=DEV)
+    csa2.kv_append_ragged(c, cu, rope, kv=kv, idx_key=ik, err=err)
+    csa2.kv_append_ragged(c, cu, rope, kv=kv, idx_key=ik, win=csa2.chunk_window(c, 3), err=err)
+    out, lse, bits = _attn(c, _q(3, 64), cu)
+    assert bits == 0 and int(err) == 0 and (out == 5).all() and (lse == 5).all()
+    for n, t in before.items():
+        assert torch.equal(getattr(c, n), t)
