@@ -89,7 +89,9 @@ __device__ __forceinline__ void copy_older(const RaggedAppend &a, int part) {
 // finds where it goes (a chain of dependent loads: the sequence, its length, the
 // page) while the row is on its way.
 //
-// 32,768 bf16 tokens in the V4 format: FIGRAG
+// 32,768 bf16 tokens in the V4 format take 27 us: 70 MB, 2.6 TB/s, 38 % of the
+// measured HBM rate; 12,871 fp32 tokens in FP4 21 us.  ALU
+// 43 %: the quantisers' instructions and the address phase's round trips.
 // Latency is hidden by other blocks, four per SM (63 registers).  Several tokens per
 // warp, the next row requested ahead, share the address phase but need 64 to 80
 // registers: four per warp took 3 us longer.  A block per token through shared
@@ -324,6 +326,8 @@ __global__ void __launch_bounds__(256, 4) k_ragged_append_r1(RaggedAppend a, int
 }
 
 // ---------------------------------------------------------------- ratio 2: a block per token
+// The compression (704 channels, fp64 softmax over four rows) is csa2_kv_append's,
+// and its arithmetic is what bounds it; every second token brings an entry.
 // Blocks 0 .. total-1: one token each (its window row and, when it completes a
 // pair, the entry).  single: max_new is 1 and there are no window rows to leave,
 // so a token's block also finishes its sequence.
@@ -395,7 +399,8 @@ __global__ void __launch_bounds__(kEncThreads) k_ragged_append_r2(RaggedAppend a
   }
 }
 
-// Once every token is encoded: the ring (from the window rows, when they were
+// Once every token is encoded (3 us, a launch of its own: no block of the append
+// knows when the last one has read the ring): the ring (from the window rows, when they were
 // asked for), the compression buffer, n_tokens.  One block per sequence.
 __global__ void __launch_bounds__(256) k_ragged_finish(RaggedAppend a) {
   const csa2_cache &c = a.c;
@@ -457,7 +462,9 @@ struct ReadArgs {
 // l + 32, lanes 0-7 the RoPE units, lanes 8-23 the key's; every store instruction
 // of the latent writes a contiguous 512 B (bf16).  One thread per row first finds
 // where it lies (a chain of dependent loads) for the whole block; then a warp
-// requests all its rows before it converts the first.
+// requests all its rows before it converts the first.  229,000 FP4 rows to bf16
+// take 67 us: 412 MB, 6.1 TB/s, 90 % of the measured copy rate; 30,011 V4 rows to
+// fp32 18 us (87 %); 16,384 FP4 rows at listed positions 11 us (round trips).
 struct RowPlace {
   int64_t pe, pt;  // physical entry and indexer tile; pe -1: zeros, -2: no row
   int32_t m;       // place in the indexer tile
@@ -618,7 +625,8 @@ __global__ void __launch_bounds__(256, 4) k_kv_read(ReadArgs a) {
   }
 }
 
-// One thread per 8 values of a window token.
+// One thread per 8 values of a window token: 32 windows 5 us, a launch and a round
+// trip or two.
 __global__ void __launch_bounds__(256) k_window_read(csa2_cache c, void *out, int bf16) {
   const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int u = static_cast<int>(id % (kDqk / 8));
