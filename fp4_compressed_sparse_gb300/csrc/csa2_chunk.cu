@@ -153,6 +153,8 @@ __global__ void __launch_bounds__(1024) k_chunk_plan(ChunkArgs a, Plan p) {
   const int tid = threadIdx.x;
   const csa2_cache &c = a.c;
   int32_t *seq_tile = c.batch <= kListSeq ? l_seq : p.seq_tile;
+  // (needed two barriers further on)
+  if (tid < c.batch && tid % 16 == 0) asm volatile("prefetch.global.L1 [%0];\n" ::"l"(c.n_tokens + tid));
   if (tid == 0) {
     carry = 0;
     seq_tile[0] = 0;
@@ -219,8 +221,9 @@ __global__ void __launch_bounds__(1024) k_chunk_plan(ChunkArgs a, Plan p) {
   __shared__ int32_t n_merge;
   if (tid == 0) n_merge = 0;
   __syncthreads();
-  // small work on fewer CTAs: two units each at least
-  const int64_t g_eff = max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.n_cta), (W + 1) / 2));
+  // no more CTAs than units (one token over 1,000 entries takes 25.7 us with a unit
+  // each, 26.6 with two)
+  const int64_t g_eff = max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.n_cta), W));
   for (int g = tid; g < p.n_cta; g += 1024) {
     CtaRange r{};
     r.first = -1;
