@@ -93,14 +93,14 @@ struct __align__(16) RowTile {
 struct CtaRange {
   int64_t lo, hi;  // units [lo, hi) of the whole work (a row tile of n key tiles is n + 1 units)
   int32_t tile;    // the row tile that holds unit lo
-  int32_t first;   // the row tile ends here and began in CTA `first`: its parts are joined; -1: not so
+  int32_t pad;
 };
 struct Plan {
   int32_t *seq_tile;  // [batch + 1] first row tile of each sequence
   int64_t *cum;       // [max_tiles + 1] first unit of each row tile
   RowTile *tile;      // [max_tiles]
   CtaRange *cta;      // [n_cta]
-  int32_t *merge;     // [n_cta] the CTAs in which a shared row tile ends, then -1
+  int4 *merge;        // [n_cta] the CTAs in which a shared row tile ends, with its first CTA and its index; then -1
   float *part;        // [2 n_cta][kPartFloats]
   int max_tiles, n_cta;
 };
@@ -111,7 +111,7 @@ __host__ __device__ inline int64_t visible(int64_t pos, int ratio, int64_t cap) 
 }
 
 // ------------------------------------------------------------------ plan
-// Inclusive scan over a 1024-thread block.
+// Inclusive scan over the block.
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(1024) k_chunk_plan(ChunkArgs a, Plan p) {
   __shared__ int64_t carry;
   __shared__ int32_t l_seq[kListSeq + 1];
   __shared__ int64_t l_cum[kListTile + 1];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, nthr = blockDim.x;
   const csa2_cache &c = a.c;
   int32_t *seq_tile = c.batch <= kListSeq ? l_seq : p.seq_tile;
   // (needed two barriers further on)
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(1024) k_chunk_plan(ChunkArgs a, Plan p) {
     carry = 0;
     seq_tile[0] = 0;
   }
-  for (int b0 = 0; b0 < c.batch; b0 += 1024) {  // row tiles of each sequence
+  for (int b0 = 0; b0 < c.batch; b0 += nthr) {  // row tiles of each sequence
     const int b = b0 + tid;
     int first = 0, n = 0;
     if (b < c.batch && !ragged_rows(a.cu, b, a.total, a.max_new, first, n)) raise_err(a.err, CSA2_DEVERR_INDEX);
@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(1024) k_chunk_plan(ChunkArgs a, Plan p) {
     const int64_t incl = block_scan(rt, sh) + carry;
     if (b < c.batch) seq_tile[b + 1] = static_cast<int32_t>(min(incl, static_cast<int64_t>(p.max_tiles)));
     __syncthreads();
-    if (tid == 1023) carry = incl;
+    if (tid == nthr - 1) carry = incl;
     __syncthreads();
   }
   // overlapping sequences (a broken cu) may ask for more row tiles than there are rows
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(1024) k_chunk_plan(ChunkArgs a, Plan p) {
     p.cum[0] = 0;
   }
   __syncthreads();
-  for (int t0 = 0; t0 < n_tiles; t0 += 1024) {
+  for (int t0 = 0; t0 < n_tiles; t0 += nthr) {
     const int t = t0 + tid;
     int64_t units = 0;
     if (t < n_tiles) {
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(1024) k_chunk_plan(ChunkArgs a, Plan p) {
       if (fits) cum[t + 1] = incl;
     }
     __syncthreads();
-    if (tid == 1023) carry = incl;
+    if (tid == nthr - 1) carry = incl;
     __syncthreads();
   }
   const int64_t W = carry;
@@ -224,9 +224,8 @@ __global__ void __launch_bounds__(1024) k_chunk_plan(ChunkArgs a, Plan p) {
   // no more CTAs than units (one token over 1,000 entries takes 25.7 us with a unit
   // each, 26.6 with two)
   const int64_t g_eff = max(static_cast<int64_t>(1), min(static_cast<int64_t>(p.n_cta), W));
-  for (int g = tid; g < p.n_cta; g += 1024) {
+  for (int g = tid; g < p.n_cta; g += nthr) {
     CtaRange r{};
-    r.first = -1;
     if (g < g_eff && W > 0) {
       r.lo = W * g / g_eff;
       r.hi = W * (g + 1) / g_eff;
@@ -236,14 +235,14 @@ __global__ void __launch_bounds__(1024) k_chunk_plan(ChunkArgs a, Plan p) {
         int first = static_cast<int>(c0 * g_eff / W);  // the CTA of unit c0, give or take a rounding
         while (first > 0 && W * first / g_eff > c0) --first;
         while (W * (first + 1) / g_eff <= c0) ++first;
-        r.first = first;
-        p.merge[atomicAdd(&n_merge, 1)] = g;  // (in any order: each joins rows of its own)
+        // (in any order: each joins rows of its own)
+        p.merge[atomicAdd(&n_merge, 1)] = make_int4(g, first, r.tile, 0);
       }
     }
     p.cta[g] = r;
   }
   __syncthreads();
-  for (int i = n_merge + tid; i < p.n_cta; i += 1024) p.merge[i] = -1;
+  for (int i = n_merge + tid; i < p.n_cta; i += nthr) p.merge[i] = make_int4(-1, 0, 0, 0);
 }
 
 // ------------------------------------------------------------------ operands
@@ -1181,12 +1180,11 @@ __global__ void __launch_bounds__(256) k_chunk_merge(ChunkArgs a, Plan p) {
   __shared__ float wt[kMaxCta][8], ls[kMaxCta][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int y = blockIdx.y / kSplit, b0 = blockIdx.y % kSplit * kDims;
-  const int g = p.merge[blockIdx.x];
-  if (g < 0) return;
-  const CtaRange cr = p.cta[g];
-  const int n = g - cr.first + 1;
+  const int4 mg = p.merge[blockIdx.x];
+  if (mg.x < 0) return;
+  const int first = mg.y, n = mg.x - first + 1;
   // the first part is the last item of its CTA (slot 1), the others the first of theirs (slot 0)
-  const float *part0 = p.part + (2 * cr.first + 1) * kPartFloats, *part1 = p.part + 2 * (cr.first + 1) * kPartFloats;
+  const float *part0 = p.part + (2 * first + 1) * kPartFloats, *part1 = p.part + 2 * (first + 1) * kPartFloats;
   auto part = [&](int k) { return k == 0 ? part0 : part1 + 2 * static_cast<int64_t>(k - 1) * kPartFloats; };
   const int d = threadIdx.x & 127, half = threadIdx.x >> 7, i4 = 2 * y + half;
   const int at4 = ((b0 * 16 + i4) * 128 + d) * 4;
@@ -1200,7 +1198,7 @@ __global__ void __launch_bounds__(256) k_chunk_merge(ChunkArgs a, Plan p) {
       }
   };
   load(0);
-  const RowTile &x = p.tile[cr.tile];
+  const RowTile &x = p.tile[mg.z];
   const int nrows = x.nrows;
   if (8 * y >= nrows) return;
   const int64_t row0 = x.row0;
@@ -1284,7 +1282,7 @@ PlanLayout plan_layout(int batch, int total, int heads) {
   L.cta = o;
   o = up(o + static_cast<size_t>(L.n_cta) * sizeof(CtaRange));
   L.merge = o;
-  o = up(o + static_cast<size_t>(L.n_cta) * 4);
+  o = up(o + static_cast<size_t>(L.n_cta) * sizeof(int4));
   L.part = o;
   o = up(o + static_cast<size_t>(2) * L.n_cta * kPartFloats * 4);
   L.total = o;
@@ -1334,7 +1332,7 @@ csa2_status csa2_chunk_attn(const csa2_cache *cache, const uint16_t *q, int32_t 
   uint8_t *wb = static_cast<uint8_t *>(ws);
   csa2::Plan p{reinterpret_cast<int32_t *>(wb + L.seq_tile), reinterpret_cast<int64_t *>(wb + L.cum),
                reinterpret_cast<csa2::RowTile *>(wb + L.tile), reinterpret_cast<csa2::CtaRange *>(wb + L.cta),
-               reinterpret_cast<int32_t *>(wb + L.merge), reinterpret_cast<float *>(wb + L.part), L.max_tiles, L.n_cta};
+               reinterpret_cast<int4 *>(wb + L.merge), reinterpret_cast<float *>(wb + L.part), L.max_tiles, L.n_cta};
   const int smem = static_cast<int>(sizeof(csa2::ChunkSmem)) + 1024;
   static_assert(sizeof(csa2::ChunkSmem) + 1024 <= 232448, "shared memory of one CTA");
   cudaError_t e = csa2::ensure_smem_limit(reinterpret_cast<const void *>(&csa2::k_chunk_attn), smem);
@@ -1350,7 +1348,9 @@ csa2_status csa2_chunk_attn(const csa2_cache *cache, const uint16_t *q, int32_t 
   CSA2_REQUIRE(regs.load(std::memory_order_relaxed) >= csa2::kLaunchRegs, CSA2_ERR_CUDA,
                "csa2_chunk_attn was built with %d registers per thread", regs.load(std::memory_order_relaxed));
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  csa2::k_chunk_plan<<<1, 1024, 0, s>>>(a, p);
+  // (with 256 threads the barriers cost 2 us less: one token over 1,000 entries 23.7 us
+  // against 25.7; more sequences or row tiles take passes, which 1,024 halve or better)
+  csa2::k_chunk_plan<<<1, cache->batch <= 256 && L.max_tiles <= 256 ? 256 : 1024, 0, s>>>(a, p);
   e = cudaGetLastError();
   // each of the next two may set itself up while the one before still runs
   cudaLaunchAttribute attr[1];
