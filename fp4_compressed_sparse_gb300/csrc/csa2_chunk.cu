@@ -715,19 +715,19 @@ __device__ __forceinline__ void produce(const ChunkArgs &a, const Plan &p, Chunk
 #pragma unroll
       for (int s = 0; s < Raw::kSteps; ++s) {
         store_step(sm.k[b], s, key, o, raw, sigma);
-        if (base >= 0) load_step(c, base + key, o, s, raw);
       }
     } else {
       dead = fill_tail(a, p, sm, n, pt, dead);
       raw = Raw{};
-      if (base >= 0) {
-#pragma unroll
-        for (int s = 0; s < Raw::kSteps; ++s) load_step(c, base + key, o, s, raw);
-      }
     }
     tc::fence_proxy_async_smem();
     __syncwarp();
     if ((pt & 31) == 0) tc::mbar_arrive(&sm.full[b]);
+    // (after the hand-over: the fence would wait for these loads too)
+    if (base >= 0) {
+#pragma unroll
+      for (int s = 0; s < Raw::kSteps; ++s) load_step(c, base + key, o, s, raw);
+    }
   }
 }
 
