@@ -706,10 +706,10 @@ __device__ __forceinline__ void produce(const ChunkArgs &a, const Plan &p, Chunk
     const bool whole = base >= 0;
     base = ring_base(sm, n + 1, a.err);
     if (whole) {
-      if (n >= 2 && !dead) dead = !wait_warp(&sm.empty[b], ((n >> 1) & 1) ^ 1, a.err);
-      if (pt == 0) *const_cast<volatile uint32_t *>(&sm.progress) = n;
       const int sigma = raw_sigma(raw);
       const bool plain = Raw::kFp4 || __all_sync(0xffffffffu, sigma == 0);
+      if (n >= 2 && !dead) dead = !wait_warp(&sm.empty[b], ((n >> 1) & 1) ^ 1, a.err);
+      if (pt == 0) *const_cast<volatile uint32_t *>(&sm.progress) = n;
       if ((pt & 31) == 0) sm.plain[b][pt >> 5] = plain;
       if (o == 0) sm.sg[b][key] = make_float2(static_cast<float>(sigma), pow2f(sigma));
 #pragma unroll
