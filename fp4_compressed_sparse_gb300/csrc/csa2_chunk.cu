@@ -420,21 +420,21 @@ struct RawFp4 {
   static constexpr bool kFp4 = true;
   static constexpr int kSteps = 3;
   uint4 w[2];
-  uint32_t r, sc[3];
+  uint32_t r, sc[5];  // a step's two scales; prepared: each as an fp16 pair
 };
 struct RawFp8 {
   static constexpr bool kFp4 = false;
   static constexpr int kSteps = 5;
   uint4 w[5];
-  uint4 sc;  // the key's 16 scales: word s holds those of step s
+  uint4 sc;  // the key's 16 scales: word s holds those of step s; prepared: the factor of step s
 };
 __device__ __forceinline__ void load_step(const csa2_cache &c, int64_t e, int o, int s, RawFp4 &r) {
   if (s < 2) {
     r.w[s] = ldg16(c.lat_codes + e * 256 + 128 * s + 16 * o);
-    r.sc[s] = __ldg(reinterpret_cast<const uint16_t *>(c.lat_scales + e * 32 + 16 * s + 2 * o));
+    r.sc[2 * s] = __ldg(reinterpret_cast<const uint16_t *>(c.lat_scales + e * 32 + 16 * s + 2 * o));
   } else {
     r.r = __ldg(reinterpret_cast<const uint32_t *>(c.rope_codes + e * 32 + 4 * o));
-    r.sc[2] = __ldg(c.rope_scales + e * 4 + (o >> 1));
+    r.sc[4] = __ldg(c.rope_scales + e * 4 + (o >> 1));
   }
 }
 __device__ __forceinline__ void load_step(const csa2_cache &c, int64_t e, int o, int s, RawFp8 &r) {
@@ -464,34 +464,39 @@ __device__ __forceinline__ void put_step(uint8_t (*k)[kBlk], int s, int key, int
   *reinterpret_cast<uint4 *>(chunk_at(blk, key, x + flip)) = flip ? hi : lo;
   *reinterpret_cast<uint4 *>(chunk_at(blk, key, x + (flip ^ 1))) = flip ? lo : hi;
 }
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t sc, int byte) {  // one scale byte, twice
-  return e4m3x2_h2(__byte_perm(sc, 0, byte * 0x11));
-}
 __device__ __forceinline__ void swap_if(bool p, uint32_t &a, uint32_t &b) {
   const uint32_t t = p ? b : a;
   b = p ? a : b;
   a = t;
 }
-__device__ __forceinline__ void store_step(uint8_t (*k)[kBlk], int s, int key, int o, const RawFp4 &r, int) {
+// What can be done with a key's registers before its buffer is free: the scales as
+// factors, and the order of the chunks.  Of a step's four chunks thread o stores
+// its chunk j ^ (o / 2) as the j-th, so that a key's eight threads hit eight
+// different 16 B banks at a time.
+__device__ __forceinline__ void prepare(RawFp4 &r, int o, int) {
+  const bool p1 = o & 2, p2 = o & 4;
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    swap_if(p1, r.w[s].x, r.w[s].y);
+    swap_if(p1, r.w[s].z, r.w[s].w);
+    swap_if(p2, r.w[s].x, r.w[s].z);
+    swap_if(p2, r.w[s].y, r.w[s].w);
+    const uint32_t two = r.sc[2 * s];
+    r.sc[2 * s] = e4m3x2_h2(__byte_perm(two, 0, p2 ? 0x11 : 0x00));
+    r.sc[2 * s + 1] = e4m3x2_h2(__byte_perm(two, 0, p2 ? 0x00 : 0x11));
+  }
+  r.sc[4] = e4m3x2_h2(__byte_perm(r.sc[4], 0, 0x00));
+}
+__device__ __forceinline__ void store_step(uint8_t (*k)[kBlk], int s, int key, int o, const RawFp4 &r) {
   if (s < 2) {
-    // four chunks; thread o stores its chunk j ^ (o / 2) as the j-th, so that a
-    // key's eight threads hit eight different 16 B banks at a time
-    uint32_t w0 = r.w[s].x, w1 = r.w[s].y, w2 = r.w[s].z, w3 = r.w[s].w;
-    const bool p1 = o & 2, p2 = o & 4;
-    swap_if(p1, w0, w1);
-    swap_if(p1, w2, w3);
-    swap_if(p2, w0, w2);
-    swap_if(p2, w1, w3);
-    const uint32_t s0 = e4m3x2_h2(__byte_perm(r.sc[s], 0, p2 ? 0x11 : 0x00));
-    const uint32_t s1 = e4m3x2_h2(__byte_perm(r.sc[s], 0, p2 ? 0x00 : 0x11));
     uint8_t *blk = k[4 * s + (o >> 1)];
     const int x = 4 * (o & 1) + (o >> 1);
-    *reinterpret_cast<uint4 *>(chunk_at(blk, key, x)) = dq_e2m1(w0, s0);
-    *reinterpret_cast<uint4 *>(chunk_at(blk, key, x ^ 1)) = dq_e2m1(w1, s0);
-    *reinterpret_cast<uint4 *>(chunk_at(blk, key, x ^ 2)) = dq_e2m1(w2, s1);
-    *reinterpret_cast<uint4 *>(chunk_at(blk, key, x ^ 3)) = dq_e2m1(w3, s1);
+    *reinterpret_cast<uint4 *>(chunk_at(blk, key, x)) = dq_e2m1(r.w[s].x, r.sc[2 * s]);
+    *reinterpret_cast<uint4 *>(chunk_at(blk, key, x ^ 1)) = dq_e2m1(r.w[s].y, r.sc[2 * s]);
+    *reinterpret_cast<uint4 *>(chunk_at(blk, key, x ^ 2)) = dq_e2m1(r.w[s].z, r.sc[2 * s + 1]);
+    *reinterpret_cast<uint4 *>(chunk_at(blk, key, x ^ 3)) = dq_e2m1(r.w[s].w, r.sc[2 * s + 1]);
   } else {
-    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, o)) = dq_e2m1(r.r, e4m3_pair(r.sc[2], 0));
+    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, o)) = dq_e2m1(r.r, r.sc[4]);
   }
 }
 // factor 2^k as an fp16 pair (k <= 15; zero where fp16 has no such value)
@@ -506,12 +511,20 @@ __device__ __forceinline__ uint4 bf16x8_h(uint4 v, float inv) {
                     pack_h2(__uint_as_float(v.w << 16) * inv, __uint_as_float(v.w & 0xFFFF0000u) * inv));
 }
 __device__ __forceinline__ uint32_t word_of(uint4 v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
-__device__ __forceinline__ void store_step(uint8_t (*k)[kBlk], int s, int key, int o, const RawFp8 &r, int sigma) {
+__device__ __forceinline__ void prepare(RawFp8 &r, int o, int sigma) {
+  const int shift = 8 * (o >> 1), off = 127 + sigma;
+  r.sc.x = pow2_h2(static_cast<int>((r.sc.x >> shift) & 0xFF) - off);
+  r.sc.y = pow2_h2(static_cast<int>((r.sc.y >> shift) & 0xFF) - off);
+  r.sc.z = pow2_h2(static_cast<int>((r.sc.z >> shift) & 0xFF) - off);
+  r.sc.w = pow2_h2(static_cast<int>((r.sc.w >> shift) & 0xFF) - off);
+  r.w[4] = bf16x8_h(r.w[4], pow2f(-sigma));  // 8 RoPE dims in bf16
+}
+__device__ __forceinline__ void store_step(uint8_t (*k)[kBlk], int s, int key, int o, const RawFp8 &r) {
   if (s < 4) {
-    const uint32_t m2 = pow2_h2(static_cast<int>((word_of(r.sc, s) >> (8 * (o >> 1))) & 0xFF) - 127 - sigma);
+    const uint32_t m2 = word_of(r.sc, s);
     put_step(k, s, key, o, dq_e4m3(r.w[s].x, r.w[s].y, m2), dq_e4m3(r.w[s].z, r.w[s].w, m2));
-  } else {  // 8 RoPE dims in bf16
-    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, o)) = bf16x8_h(r.w[4], pow2f(-sigma));
+  } else {
+    *reinterpret_cast<uint4 *>(chunk_at(k[8], key, o)) = r.w[4];
   }
 }
 __device__ __forceinline__ int e8m0_top(uint4 s) {  // largest of 16 scale bytes
@@ -708,13 +721,14 @@ __device__ __forceinline__ void produce(const ChunkArgs &a, const Plan &p, Chunk
     if (whole) {
       const int sigma = raw_sigma(raw);
       const bool plain = Raw::kFp4 || __all_sync(0xffffffffu, sigma == 0);
+      prepare(raw, o, sigma);
       if (n >= 2 && !dead) dead = !wait_warp(&sm.empty[b], ((n >> 1) & 1) ^ 1, a.err);
       if (pt == 0) *const_cast<volatile uint32_t *>(&sm.progress) = n;
       if ((pt & 31) == 0) sm.plain[b][pt >> 5] = plain;
       if (o == 0) sm.sg[b][key] = make_float2(static_cast<float>(sigma), pow2f(sigma));
 #pragma unroll
       for (int s = 0; s < Raw::kSteps; ++s) {
-        store_step(sm.k[b], s, key, o, raw, sigma);
+        store_step(sm.k[b], s, key, o, raw);
       }
     } else {
       dead = fill_tail(a, p, sm, n, pt, dead);
