@@ -22,15 +22,17 @@
 // would take all 512 and leave none for S.  Beside the query (72 KB) two key
 // tiles of 64 fit into shared memory (72 KB each), a third does not.
 //
-// What bounds it now: a key tile's way through its buffer, in cycles: fill 1,650,
-// hand-over 360, QK 1,570 (the MMAs alone 1,177), softmax 1,300 (2,100 when a row's
-// reference moves), hand-over 450, PV 880, hand-over 440.  Two buffers make that
-// about 3,700 per tile; the MMAs by themselves take 1,957 (shared-memory operands
-// at 128 B per cycle).  Tensor pipe 35 % active, ALU 36 %, issue slots 37 %.
-// Measured: 1,024 queries of 64 heads over 15,000 V4 entries 3.76 ms (592 TFLOP/s,
-// 31 % of the measured bf16 rate); ragged chunks over FP4 entries 1.32 ms (577);
-// 32 single tokens over 8K entries each 95 us, 16 over up to 51K 154 us (505);
-// one over 1,000 26 us, of which the three launches' round trips are nearly all.
+// What bounds it now: a key tile's way through its buffer, in cycles about: fill
+// 1,650, hand-over 360, QK 1,570 (the MMAs alone 1,177), softmax 1,300 (2,100 when a
+// row's reference moves), hand-over 450, PV 880, hand-over 440.  Two buffers make
+// that 3,500 to 3,700 per tile; the MMAs by themselves take 1,957 (operands from
+// shared memory at 128 B per cycle), the fill's stores 576 more of the same
+// bandwidth, so what overlaps also slows each other down.  Tensor pipe 35 %, ALU
+// 36 %, issue slots 37 %.
+// Measured: 1,024 queries of 64 heads over 15,000 V4 entries 3.46 ms (644 TFLOP/s,
+// 34 % of the measured bf16 rate); ragged chunks over FP4 entries 1.32 ms (577);
+// 32 single tokens over 8K entries each 93 us, 16 over up to 65K 153 us (507); one
+// over 1,000 23 us, of which the three launches' round trips are nearly all.
 #include <atomic>
 #include <cmath>
 #include <cuda_fp16.h>
@@ -139,7 +141,7 @@ __device__ __forceinline__ int last_at_most(const T *list, int n, T v) {
   return lo;
 }
 
-// One block: 6 us for decode batches, 10 us for a thousand row tiles.  The two
+// One block: 5 us for decode batches, 10 us for a thousand row tiles.  The two
 // lists it searches (first row tile of each sequence, first unit of each row tile)
 // are kept in shared memory as far as they fit, as a search in global memory is a
 // chain of L2 round trips.
