@@ -523,10 +523,12 @@ __global__ void __launch_bounds__(256, 4) k_kv_read(ReadArgs a) {
   if (tid < 8 * kRow) {
     RowPlace pl{-2, 0, 0};
     const int64_t r = r0 + tid;
+    // (requested before the search for the sequence, which does not need it)
+    const int32_t listed = a.pos != nullptr && r < a.total ? __ldg(a.pos + r) : 0;
     const int b = r < a.total ? ragged_seq(a.cu, c.batch, static_cast<int>(r)) : -1;
     if (b >= 0) {
       pl.pe = -1;
-      const int64_t e = a.pos ? static_cast<int64_t>(a.pos[r]) : a.start[b] + (r - a.cu[b]);
+      const int64_t e = a.pos ? static_cast<int64_t>(listed) : a.start[b] + (r - a.cu[b]);
       bool bad = e < 0 && a.pos == nullptr;  // a negative start
       if (e >= 0) {
         bad = e >= c.n_tokens[b] >> (c.ratio - 1) || e >= c.capacity;
