@@ -441,7 +441,7 @@ __device__ __forceinline__ void load_step(const csa2_cache &c, int64_t e, int o,
 }
 __device__ __forceinline__ void load_step(const csa2_cache &c, int64_t e, int o, int s, RawFp8 &r) {
   r.w[s] = ldg16(s < 4 ? c.lat_codes + e * 512 + 128 * s + 16 * o : c.rope_codes + e * 128 + 16 * o);
-  if (s == 4) r.sc = ldg16(c.lat_scales + e * 16);  // (the last step: the old scales are done with)
+  if (s == 4) r.sc = ldg16(c.lat_scales + e * 16);
 }
 
 __device__ __forceinline__ uint4 dq_e2m1(uint32_t w, uint32_t s2) {
