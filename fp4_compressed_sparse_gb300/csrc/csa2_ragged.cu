@@ -84,18 +84,16 @@ __device__ __forceinline__ void copy_older(const RaggedAppend &a, int part) {
 
 // ---------------------------------------------------------------- ratio 1: a warp per token
 // Lane l has latent dims 16 l .. + 15 (one NVFP4 group, half an MXFP8 block), RoPE
-// pair l, key dims 4 l .. + 3, all in registers: no shared memory and no block
-// barrier beyond the one after the address phase, in which one thread per token
-// finds where it goes (a chain of dependent loads: the sequence, its length, the
-// page) while the row is on its way.
+// pair l, key dims 4 l .. + 3, all in registers: no shared memory, no barrier.  While
+// the row is on its way the warp finds where it goes (a chain of dependent loads:
+// the sequence, its length, the page).
 //
-// 32,768 bf16 tokens in the V4 format take 27 us: 70 MB, 2.6 TB/s, 38 % of the
-// measured HBM rate; 12,871 fp32 tokens in FP4 21 us.  ALU
-// 43 %: the quantisers' instructions and the address phase's round trips.
-// Latency is hidden by other blocks, four per SM (63 registers).  Several tokens per
-// warp, the next row requested ahead, share the address phase but need 64 to 80
-// registers: four per warp took 3 us longer.  A block per token through shared
-// memory took 261 us.
+// 32,768 bf16 tokens in the V4 format take 24 us: 70 MB, 2.9 TB/s, 43 % of the
+// measured HBM rate; 12,871 fp32 tokens in FP4 19.5 us.  What is left are the
+// quantisers' instructions and the round trips.  Latency is hidden by other warps,
+// four blocks per SM (64 registers).  One thread per token finding its place for
+// the block, with a barrier, took 27 us; several tokens per warp, the next row
+// requested ahead, 30 us; a block per token through shared memory 261 us.
 
 // Sixteen E2M1 codes of x / s without the divisions: x / s, rounded to fp32, is at
 // most (below) a midpoint t of the grid exactly when x is at most (below) t s.
@@ -216,40 +214,39 @@ __global__ void __launch_bounds__(256, 4) k_ragged_append_r1(RaggedAppend a, int
     copy_older(a, blockIdx.x - token_blocks);
     return;
   }
-  __shared__ TokenPlace place[8];
   const csa2_cache &c = a.c;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the row does not depend on its place: it is requested at once
   TokenRow<kBf16> cur;
   const int r = blockIdx.x * 8 + warp;
-  if (r < a.total) load_token(a, r, lane, cur);
-  if (tid < 8) {
-    TokenPlace pl{-1, -1, -1, 0};
-    const int row = blockIdx.x * 8 + tid;
-    const int b = row < a.total ? ragged_seq(a.cu, c.batch, row) : -1;
-    int first = 0, n = 0;
-    if (b >= 0 && !ragged_rows(a.cu, b, a.total, a.max_new, first, n)) raise_err(a.err, CSA2_DEVERR_INDEX);
-    if (n > 0) {
-      const int64_t t0 = c.n_tokens[b];
-      const int j = row - first;
-      if (!append_ok(c, t0, n, a.rope_len)) {
-        if (j == 0) append_fail(c, t0, n, a.rope_len, a.err);
-      } else {
-        pl.t = t0 + j;
-        pl.pe = phys_entry(entry_map(c), b, pl.t);
-        pl.pt = phys_tile(entry_map(c), b, pl.t / kIdxTile);
-        if (pl.pe < 0) raise_err(a.err, CSA2_DEVERR_INDEX);
-        if (a.win_codes != nullptr) pl.win = static_cast<int64_t>(row) + static_cast<int64_t>(kWin) * (b + 1);
-        else if (j >= n - kWin) pl.win = static_cast<int64_t>(b) * kWin + (pl.t & (kWin - 1));
-        if (single) c.n_tokens[b] = t0 + n;  // (its only token: nobody else reads it)
-      }
-    }
-    place[tid] = pl;
-  }
-  __syncthreads();
-  const bool fp8 = c.entry_format == CSA2_ENTRY_FP8, mx = c.swa_dtype == CSA2_SWA_MXFP8;
   if (r >= a.total) return;
-  const TokenPlace pl = place[warp];
+  load_token(a, r, lane, cur);
+  TokenPlace pl{-1, -1, -1, 0};  // (the same in every lane)
+  const int b = ragged_seq(a.cu, c.batch, r);
+  if (b < 0) return;
+  int first, n;
+  if (!ragged_rows(a.cu, b, a.total, a.max_new, first, n)) {
+    if (lane == 0) raise_err(a.err, CSA2_DEVERR_INDEX);
+    return;
+  }
+  const int64_t t0 = c.n_tokens[b];
+  const int j = r - first;
+  if (!append_ok(c, t0, n, a.rope_len)) {
+    if (j == 0 && lane == 0) append_fail(c, t0, n, a.rope_len, a.err);
+    return;
+  }
+  pl.t = t0 + j;
+  pl.pe = entry_at(c, b, static_cast<int>(pl.t));
+  // a page holds whole indexer tiles; a dense sequence's are padded
+  pl.pt = c.block_table != nullptr ? pl.pe / kIdxTile : b * idx_tiles(c.capacity) + pl.t / kIdxTile;
+  if (a.win_codes != nullptr) pl.win = static_cast<int64_t>(r) + static_cast<int64_t>(kWin) * (b + 1);
+  else if (j >= n - kWin) pl.win = static_cast<int64_t>(b) * kWin + (pl.t & (kWin - 1));
+  __syncwarp();  // every lane has read n_tokens
+  if (lane == 0) {
+    if (pl.pe < 0) raise_err(a.err, CSA2_DEVERR_INDEX);
+    if (single) c.n_tokens[b] = t0 + n;  // (its only token: no other warp reads it)
+  }
+  const bool fp8 = c.entry_format == CSA2_ENTRY_FP8, mx = c.swa_dtype == CSA2_SWA_MXFP8;
   if (pl.pe < 0 && pl.win < 0) return;
   const float2 cs = __ldg(reinterpret_cast<const float2 *>(a.rope_cs + pl.t * 64 + 2 * lane));
   rope_pair(cur.r.x, cur.r.y, cs.x, cs.y);
@@ -461,8 +458,8 @@ struct ReadArgs {
 // 8 warps, kRow rows each, in units of 8 values: lane l has latent units l and
 // l + 32, lanes 0-7 the RoPE units, lanes 8-23 the key's; every store instruction
 // of the latent writes a contiguous 512 B (bf16).  One thread per row first finds
-// where it lies (a chain of dependent loads) for the whole block; then a warp
-// requests all its rows before it converts the first.  229,000 FP4 rows to bf16
+// where it lies (a chain of dependent loads) for the whole block (by warps, without
+// the barrier, took as long); then a warp requests all its rows before it converts the first.  229,000 FP4 rows to bf16
 // take 67 us: 412 MB, 6.1 TB/s, 90 % of the measured copy rate; 30,011 V4 rows to
 // fp32 18 us (87 %); 16,384 FP4 rows at listed positions 11 us (round trips).
 struct RowPlace {
