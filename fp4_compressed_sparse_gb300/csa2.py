@@ -397,12 +397,15 @@ def mask_to_pool(scores, ratio, q_pos, pool, pool_block_size=8, stream=None):
 
 
 # --------------------------------------------------------------------------- ragged batches
-def _want(name, t, dtype, shape=None, like=None):
-    """Raise ValueError unless t is a contiguous device tensor of dtype (and shape), on like's device."""
-    if t is not None and t.is_cuda and (t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype)) and (
-            shape is None or t.shape == shape) and t.is_contiguous() and (
-            like is None or t.get_device() == like.get_device()):
-        return
+# These calls are submitted between short kernels, so their checks are kept to the
+# few attribute reads a tensor needs (a CPU tensor's get_device() is -1).
+def _want(name, t, dtype, shape=None, dev=None):
+    """Raise ValueError unless t is a contiguous device tensor of dtype (and shape), on device dev."""
+    if t is not None:
+        d = t.get_device()
+        if (d == dev or (dev is None and d >= 0)) and (t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype)) \
+                and (shape is None or t.shape == shape) and t.is_contiguous():
+            return
     if t is None or not t.is_cuda:
         raise ValueError(f"{name}: a CUDA tensor is needed")
     if t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
@@ -411,19 +414,21 @@ def _want(name, t, dtype, shape=None, like=None):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, {tuple(shape)} is needed")
     if not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous")
-    raise ValueError(f"{name} is on {t.device}, the cache on {like.device}")
+    raise ValueError(f"{name} is on {t.device}, the cache on cuda:{dev}")
 
 
-def _want_rows(name, t, dtype, width, like, total=None):
+def _want_rows(name, t, dtype, width, dev, total=None):
     """Raise ValueError unless t holds rows of `width` elements, contiguous within a row; returns the row stride."""
-    if t is None or not t.is_cuda or t.get_device() != like.get_device():
-        raise ValueError(f"{name}: a tensor on {like.device} is needed")
+    if t is None or t.get_device() != dev:
+        raise ValueError(f"{name}: a tensor on cuda:{dev} is needed")
     if t.dtype not in dtype:
         raise ValueError(f"{name}: {t.dtype}, one of {dtype} is needed")
-    shape = t.shape
-    if len(shape) != 2 or shape[1] != width or (total is not None and shape[0] != total):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, ({'rows' if total is None else total}, {width}) is needed")
-    if shape[0] <= 1:
+    if t.dim() != 2:
+        raise ValueError(f"{name}: {t.dim()} dimensions, 2 are needed")
+    rows, w = t.shape
+    if w != width or (total is not None and rows != total):
+        raise ValueError(f"{name}: shape {(rows, w)}, ({'rows' if total is None else total}, {width}) is needed")
+    if rows <= 1:
         return width
     row, one = t.stride()
     if one != 1 or row < width:
@@ -442,13 +447,14 @@ def _adr(t):
 # the current stream's handle (the public current_stream() builds an object first, which takes as long as a launch)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _call(fn, cache, stream, *args):
+def _call(fn, cache, dev, stream, *args):
     """fn(cache, *args, stream) with the cache's device as the current one, on its current stream unless one is given."""
-    f, dev = getattr(_lib or load(), fn), cache.n_tokens.get_device()
+    f = getattr(_lib or load(), fn)
     s = stream.cuda_stream if stream is not None else _raw_stream(dev)
-    if dev == torch.cuda.current_device():
+    if dev == _current_device():
         status = f(cache.ref(), *args, s)
     else:
         with torch.cuda.device(dev):
@@ -473,13 +479,13 @@ def chunk_window(cache, total):
                        torch.empty(rows, n[1] // rows, dtype=torch.uint8, device=dev))
 
 
-def _window_ptrs(cache, win, total):
+def _window_ptrs(cache, win, total, dev):
     if win is None:
         return None, None
     rows = total + WINDOW * cache.batch
-    _want("win.codes", win.codes, torch.uint8, (rows, 576 if cache.swa_dtype == SWA_MXFP8 else 1152), cache.n_tokens)
+    _want("win.codes", win.codes, torch.uint8, (rows, 576 if cache.swa_dtype == SWA_MXFP8 else 1152), dev)
     if cache.swa_dtype == SWA_MXFP8:
-        _want("win.scales", win.scales, torch.uint8, (rows, 32), cache.n_tokens)
+        _want("win.scales", win.scales, torch.uint8, (rows, 32), dev)
     return _adr(win.codes), _adr(win.scales)
 
 
@@ -492,30 +498,30 @@ def kv_append_ragged(cache: Cache, cu_new, rope_cs, kv=None, idx_key=None, cmp=N
     tokens.  Ratio 1: kv [total,576], idx_key [total,128] (fp32 or bf16, rows may be strided).  Ratio 2:
     cmp = (ca, cb, za, zb [total,704], ba, bb [2,704]) fp32.  max_new: a bound on the rows of one sequence
     (default: all).  win: from chunk_window(cache, total), filled for chunk_attn."""
-    like = cache.n_tokens
-    _want("cu_new", cu_new, torch.int32, (cache.batch + 1,), like)
-    _want("rope_cs", rope_cs, torch.float32, None, like)
+    dev = cache.n_tokens.get_device()
+    _want("cu_new", cu_new, torch.int32, (cache.batch + 1,), dev)
+    _want("rope_cs", rope_cs, torch.float32, None, dev)
     if rope_cs.dim() < 2 or rope_cs.numel() != 64 * rope_cs.shape[0]:
         raise ValueError(f"rope_cs: shape {tuple(rope_cs.shape)}, (positions, 32, 2) is needed")
     cin, ks, is_, dt = None, 0, 0, IN_F32
     if cache.ratio == 1:
         if cmp is not None:
             raise ValueError("cmp is for ratio-2 caches")
-        ks = _want_rows("kv", kv, _FLOATS, 576, like)
+        ks = _want_rows("kv", kv, _FLOATS, 576, dev)
         total = kv.shape[0]
-        is_ = _want_rows("idx_key", idx_key, (kv.dtype,), 128, like, total)
+        is_ = _want_rows("idx_key", idx_key, (kv.dtype,), 128, dev, total)
         dt = IN_BF16 if kv.dtype is torch.bfloat16 else IN_F32
     else:
         if cmp is None or kv is not None or idx_key is not None:
             raise ValueError("a ratio-2 cache takes cmp rows, and no kv or idx_key")
         total = cmp[0].shape[0]
         for i, t in enumerate(cmp):
-            _want(f"cmp[{i}]", t, torch.float32, (total, D_CMP) if i < 4 else (2, D_CMP), like)
+            _want(f"cmp[{i}]", t, torch.float32, (total, D_CMP) if i < 4 else (2, D_CMP), dev)
         cin = ctypes.byref(CompressIn(*[t.data_ptr() for t in cmp]))
-    wc, ws = _window_ptrs(cache, win, total)
+    wc, ws = _window_ptrs(cache, win, total, dev)
     if total == 0:  # (empty tensors have no address)
         return
-    _call("csa2_kv_append_ragged", cache, stream, _adr(kv), ks, _adr(idx_key), is_, dt, cin, _adr(cu_new), total,
+    _call("csa2_kv_append_ragged", cache, dev, stream, _adr(kv), ks, _adr(idx_key), is_, dt, cin, _adr(cu_new), total,
           total if max_new is None else max_new, _adr(rope_cs), rope_cs.shape[0], wc, ws, _adr(err))
 
 
@@ -523,32 +529,33 @@ def kv_read(cache: Cache, cu_rows, out_main=None, out_key=None, pos=None, start=
     """csa2_kv_read: rows cu_rows[b] .. cu_rows[b+1]-1 read entries pos[r] (int32 [total], negative = zeros)
     of sequence b, or the stretch from start[b] (int64 [B]) on, into out_main [total,576] and / or out_key
     [total,128] (fp32 or bf16, rows may be strided)."""
-    like = cache.n_tokens
-    _want("cu_rows", cu_rows, torch.int32, (cache.batch + 1,), like)
+    dev = cache.n_tokens.get_device()
+    _want("cu_rows", cu_rows, torch.int32, (cache.batch + 1,), dev)
     first = out_main if out_main is not None else out_key
     if first is None:
         raise ValueError("out_main or out_key is needed")
     total, ms, ks = first.shape[0], 0, 0
     if out_main is not None:
-        ms = _want_rows("out_main", out_main, _FLOATS, 576, like)
+        ms = _want_rows("out_main", out_main, _FLOATS, 576, dev)
     if out_key is not None:
-        ks = _want_rows("out_key", out_key, (first.dtype,) if out_main is not None else _FLOATS, 128, like, total)
+        ks = _want_rows("out_key", out_key, (first.dtype,) if out_main is not None else _FLOATS, 128, dev, total)
     if (pos is None) == (start is None):
         raise ValueError("one of pos and start is needed")
     if pos is not None:
-        _want("pos", pos, torch.int32, (total,), like)
+        _want("pos", pos, torch.int32, (total,), dev)
     else:
-        _want("start", start, torch.int64, (cache.batch,), like)
+        _want("start", start, torch.int64, (cache.batch,), dev)
     if total == 0:
         return
-    _call("csa2_kv_read", cache, stream, _adr(cu_rows), total, _adr(pos), _adr(start), _adr(out_main), ms, _adr(out_key),
+    _call("csa2_kv_read", cache, dev, stream, _adr(cu_rows), total, _adr(pos), _adr(start), _adr(out_main), ms, _adr(out_key),
           ks, _out_dtype(first), _adr(err))
 
 
 def window_read(cache: Cache, out, stream=None):
     """csa2_window_read: out [B,128,576] (fp32 or bf16), row i = token n_tokens - 128 + i (zeros before token 0)."""
-    _want("out", out, _FLOATS, (cache.batch, WINDOW, D_QK), cache.n_tokens)
-    _call("csa2_window_read", cache, stream, _adr(out), _out_dtype(out))
+    dev = cache.n_tokens.get_device()
+    _want("out", out, _FLOATS, (cache.batch, WINDOW, D_QK), dev)
+    _call("csa2_window_read", cache, dev, stream, _adr(out), _out_dtype(out))
 
 
 def chunk_attn_workspace(total, heads, batch, device="cuda"):
@@ -561,21 +568,21 @@ def chunk_attn(cache: Cache, q, cu_q, out, lse, ws, sm_scale, max_new=None, win=
     """csa2_chunk_attn: q bf16 [total,H,576], rows cu_q[b] .. cu_q[b+1]-1 the last tokens appended to sequence
     b -> out [total,H,512] (fp32 or bf16), lse fp32 [total,H].  win: the append's window rows (None: the ring,
     enough for single tokens).  ws: chunk_attn_workspace()."""
-    like = cache.n_tokens
-    _want("q", q, torch.bfloat16, None, like)
+    dev = cache.n_tokens.get_device()
+    _want("q", q, torch.bfloat16, None, dev)
     if q.dim() != 3 or q.shape[2] != D_QK:
         raise ValueError(f"q: shape {tuple(q.shape)}, (total, heads, {D_QK}) is needed")
     total, H, _ = q.shape
-    _want("cu_q", cu_q, torch.int32, (cache.batch + 1,), like)
-    _want("out", out, _FLOATS, (total, H, D_LATENT), like)
-    _want("lse", lse, torch.float32, (total, H), like)
-    _want("ws", ws, torch.uint8, None, like)
+    _want("cu_q", cu_q, torch.int32, (cache.batch + 1,), dev)
+    _want("out", out, _FLOATS, (total, H, D_LATENT), dev)
+    _want("lse", lse, torch.float32, (total, H), dev)
+    _want("ws", ws, torch.uint8, None, dev)
     if sink is not None:
-        _want("sink", sink, torch.float32, (H,), like)
-    wc, wsc = _window_ptrs(cache, win, total)
+        _want("sink", sink, torch.float32, (H,), dev)
+    wc, wsc = _window_ptrs(cache, win, total, dev)
     if total == 0:
         return
-    _call("csa2_chunk_attn", cache, stream, _adr(q), H, _adr(cu_q), total, total if max_new is None else max_new, wc, wsc,
+    _call("csa2_chunk_attn", cache, dev, stream, _adr(q), H, _adr(cu_q), total, total if max_new is None else max_new, wc, wsc,
           _adr(sink), sm_scale, _adr(out), _out_dtype(out), _adr(lse), _adr(ws), ws.numel(), _adr(err))
 
 

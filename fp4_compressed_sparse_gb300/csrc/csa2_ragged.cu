@@ -459,9 +459,10 @@ struct ReadArgs {
 // l + 32, lanes 0-7 the RoPE units, lanes 8-23 the key's; every store instruction
 // of the latent writes a contiguous 512 B (bf16).  One thread per row first finds
 // where it lies (a chain of dependent loads) for the whole block (by warps, without
-// the barrier, took as long); then a warp requests all its rows before it converts the first.  229,000 FP4 rows to bf16
-// take 67 us: 412 MB, 6.1 TB/s, 90 % of the measured copy rate; 30,011 V4 rows to
-// fp32 18 us (87 %); 16,384 FP4 rows at listed positions 11 us (round trips).
+// the barrier, took as long); then a warp requests all its rows before it converts
+// the first.  229,000 FP4 rows to bf16 take 67 us: 412 MB, 6.1 TB/s, 90 % of the
+// measured copy rate; 30,011 V4 rows to fp32 18 us (87 %); 16,384 FP4 rows at
+// listed positions 11 us (round trips).
 struct RowPlace {
   int64_t pe, pt;  // physical entry and indexer tile; pe -1: zeros, -2: no row
   int32_t m;       // place in the indexer tile
@@ -627,7 +628,7 @@ __global__ void __launch_bounds__(256, 4) k_kv_read(ReadArgs a) {
 // One thread per 8 values of a window token: 32 windows 5 us, a launch and a round
 // trip or two.
 __global__ void __launch_bounds__(256) k_window_read(csa2_cache c, void *out, int bf16) {
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const uint32_t id = blockIdx.x * 256 + threadIdx.x;  // (65,535 sequences at most: below 2^30)
   const int u = static_cast<int>(id % (kDqk / 8));
   const int64_t at = id / (kDqk / 8);
   const int b = static_cast<int>(at / kWin), i = static_cast<int>(at % kWin);
