@@ -355,7 +355,11 @@ struct __align__(1024) ChunkSmem {
   __align__(16) TileRef ring[kRing];
   __align__(8) uint64_t full[2];      // tile filled
   __align__(8) uint64_t empty[2];     // ... and its PV complete
-  __align__(8) uint64_t s_full[2], p_full, q_ready;
+  // by tile parity, both: S of tile n + 1 may be issued before P of tile n has been
+  // waited for, so P of tile n + 1 may arrive before that wait, and a parity wait
+  // cannot tell a phase from the one two further on
+  __align__(8) uint64_t s_full[2], p_full[2];
+  __align__(8) uint64_t q_ready;
 };
 
 // Whether a phase is complete, without waiting; the same answer in every lane.
@@ -980,7 +984,7 @@ __device__ __forceinline__ void softmax(const ChunkArgs &a, const Plan &p, Chunk
       tc::fence_proxy_async_smem();
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&sm.p_full);
+      if (lane == 0) tc::mbar_arrive(&sm.p_full[b]);
     }
     // ---- the item's last PV is on its way: sums, output factors, the next query
     la += __shfl_xor_sync(0xffffffffu, la, 1);
@@ -1056,13 +1060,13 @@ __device__ __forceinline__ void issue(const ChunkArgs &a, const Plan &p, ChunkSm
       // do not suspend while either may come)
       bool ready = false;
       for (uint32_t poll = 0; !ready && !ahead && i + 1 < tiles && poll < kPolls; ++poll) {
-        ready = mbar_test(&sm.p_full, n & 1);
+        ready = mbar_test(&sm.p_full[n & 1], (n >> 1) & 1);
         if (!ready && mbar_test(&sm.full[(n + 1) & 1], ((n + 1) >> 1) & 1)) {
           ahead = true;
           qk(n + 1);
         }
       }
-      if (!ready && !wait_warp(&sm.p_full, n & 1, a.err)) return;
+      if (!ready && !wait_warp(&sm.p_full[n & 1], (n >> 1) & 1, a.err)) return;
       tc::tc_fence_after();
       const uint32_t buf = (n & 1) * (kTile >> 4);
 #pragma unroll 1
@@ -1148,8 +1152,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_chunk_attn(const __grid_constan
       tc::mbar_init(&sm.full[i], kPrWarps);
       tc::mbar_init(&sm.empty[i], 1);
       tc::mbar_init(&sm.s_full[i], 1);
+      tc::mbar_init(&sm.p_full[i], kSmWarps);
     }
-    tc::mbar_init(&sm.p_full, kSmWarps);
     tc::mbar_init(&sm.q_ready, kSmWarps);
     tc::fence_mbar_init();
     sm.progress = 0;
