@@ -702,8 +702,9 @@ __device__ __forceinline__ int64_t ring_base(const ChunkSmem &sm, uint32_t n, in
   const volatile uint32_t *listed = &sm.listed;
   uint32_t i = 0;
   while (*listed <= n && i < kPolls) ++i;
-  if (*listed <= n) {
-    raise_err(err, CSA2_DEVERR_TIMEOUT);
+  // (one answer for the warp: what follows has warp-wide operations)
+  if (!__all_sync(0xffffffffu, *listed > n)) {
+    if ((threadIdx.x & 31) == 0) raise_err(err, CSA2_DEVERR_TIMEOUT);
     return kNoTile;
   }
   __threadfence_block();

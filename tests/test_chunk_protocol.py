@@ -52,3 +52,21 @@ def test_every_order_of_s_and_p_ends(tiles):
 
 def test_the_walk_finds_a_barrier_short():
     assert _stuck(3, 2, 1) and not _stuck(3, 2, 2)
+
+
+def _function(name):
+    """The body of a function of the kernel's source."""
+    text = open(SRC).read()
+    m = re.search(r"\b" + name + r"\([^;{]*\)\s*\{", text)
+    depth, at = 1, m.end()
+    while depth:
+        depth += {"{": 1, "}": -1}.get(text[at], 0)
+        at += 1
+    return text[m.end():at]
+
+
+@pytest.mark.parametrize("name", ["wait_warp", "mbar_test", "ring_base"])
+def test_a_warp_agrees_how_a_bounded_wait_ended(name):
+    """What follows a wait that gave up differs, and has warp-wide operations: the lanes must not decide for
+    themselves.  (The ahead warp's wait is one lane's alone.)"""
+    assert re.search(r"__(all|any|ballot|shfl)_sync\(0xffffffffu", _function(name))
