@@ -1198,7 +1198,8 @@ template <int kDims>
 __global__ void __launch_bounds__(256) k_chunk_merge(ChunkArgs a, Plan p) {
   constexpr int kSplit = 4 / kDims, kParts = 8 / kDims;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  __shared__ float wt[kMaxCta][8], ls[kMaxCta][8];
+  __shared__ __align__(16) float wt[kMaxCta][8];  // (read four rows at a time)
+  __shared__ float ls[kMaxCta][8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int y = blockIdx.y / kSplit, b0 = blockIdx.y % kSplit * kDims;
   const int4 mg = p.merge[blockIdx.x];

@@ -70,3 +70,14 @@ def test_a_warp_agrees_how_a_bounded_wait_ended(name):
     """What follows a wait that gave up differs, and has warp-wide operations: the lanes must not decide for
     themselves.  (The ahead warp's wait is one lane's alone.)"""
     assert re.search(r"__(all|any|ballot|shfl)_sync\(0xffffffffu", _function(name))
+
+
+def test_shared_arrays_read_in_16_bytes_are_aligned_to_them():
+    """A shared array that is read through a 16-byte type is declared with that alignment."""
+    text = open(SRC).read()
+    wide = set(re.findall(r"reinterpret_cast<(?:const )?(?:float4|uint4) \*>\(&?(?:sm\.)?(\w+)\[", text))
+    declared = {n: line for line in text.splitlines() for n in wide
+                if re.match(r"\s*(__shared__ )?(__align__\(\d+\) )?(float|float2|uint8_t) .*\b" + n + r"\[\w+\](\[\w+\])*[,;]", line)}
+    assert {"wt", "sg", "plain"} <= set(declared)
+    for n, line in declared.items():
+        assert "__align__(16)" in line, line.strip()
