@@ -444,6 +444,15 @@ def _adr(t):
     return None if t is None else t.data_ptr()
 
 
+def _err_word(err, dev):
+    """The address of an error word, which the kernels write to; ValueError unless it is an int32 tensor on device dev."""
+    if err is None:
+        return None
+    if err.get_device() != dev or err.dtype is not torch.int32 or err.numel() == 0:
+        raise ValueError(f"err: {err.numel()} x {err.dtype} on {err.device}, an int32 on cuda:{dev} is needed")
+    return err.data_ptr()
+
+
 # the current stream's handle (the public current_stream() builds an object first, which takes as long as a launch)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
@@ -519,10 +528,11 @@ def kv_append_ragged(cache: Cache, cu_new, rope_cs, kv=None, idx_key=None, cmp=N
             _want(f"cmp[{i}]", t, torch.float32, (total, D_CMP) if i < 4 else (2, D_CMP), dev)
         cin = ctypes.byref(CompressIn(*[t.data_ptr() for t in cmp]))
     wc, ws = _window_ptrs(cache, win, total, dev)
+    ew = _err_word(err, dev)
     if total == 0:  # (empty tensors have no address)
         return
     _call("csa2_kv_append_ragged", cache, dev, stream, _adr(kv), ks, _adr(idx_key), is_, dt, cin, _adr(cu_new), total,
-          total if max_new is None else max_new, _adr(rope_cs), rope_cs.shape[0], wc, ws, _adr(err))
+          total if max_new is None else max_new, _adr(rope_cs), rope_cs.shape[0], wc, ws, ew)
 
 
 def kv_read(cache: Cache, cu_rows, out_main=None, out_key=None, pos=None, start=None, err=None, stream=None):
@@ -545,10 +555,11 @@ def kv_read(cache: Cache, cu_rows, out_main=None, out_key=None, pos=None, start=
         _want("pos", pos, torch.int32, (total,), dev)
     else:
         _want("start", start, torch.int64, (cache.batch,), dev)
+    ew = _err_word(err, dev)
     if total == 0:
         return
     _call("csa2_kv_read", cache, dev, stream, _adr(cu_rows), total, _adr(pos), _adr(start), _adr(out_main), ms, _adr(out_key),
-          ks, _out_dtype(first), _adr(err))
+          ks, _out_dtype(first), ew)
 
 
 def window_read(cache: Cache, out, stream=None):
@@ -580,10 +591,11 @@ def chunk_attn(cache: Cache, q, cu_q, out, lse, ws, sm_scale, max_new=None, win=
     if sink is not None:
         _want("sink", sink, torch.float32, (H,), dev)
     wc, wsc = _window_ptrs(cache, win, total, dev)
+    ew = _err_word(err, dev)
     if total == 0:
         return
     _call("csa2_chunk_attn", cache, dev, stream, _adr(q), H, _adr(cu_q), total, total if max_new is None else max_new, wc, wsc,
-          _adr(sink), sm_scale, _adr(out), _out_dtype(out), _adr(lse), _adr(ws), ws.numel(), _adr(err))
+          _adr(sink), sm_scale, _adr(out), _out_dtype(out), _adr(lse), _adr(ws), ws.numel(), ew)
 
 
 # --------------------------------------------------------------------------- measurement helpers

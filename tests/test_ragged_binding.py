@@ -1,0 +1,74 @@
+"""What the Python binding of the ragged calls refuses before anything is launched (no GPU: stand-ins for
+device tensors, and a recorder in place of the library call)."""
+import types
+
+import pytest
+import torch
+
+from fp4_compressed_sparse_gb300 import csa2
+
+
+class Fake:
+    """What the binding reads of a tensor."""
+
+    def __init__(self, *shape, dtype=torch.float32, dev=0, stride=None, ptr=1 << 20):
+        self.shape, self.dtype, self.dev, self.ptr = torch.Size(shape), dtype, dev, ptr
+        dense = [1]
+        for n in reversed(shape[1:]):
+            dense.insert(0, dense[0] * n)
+        self.dense, self.strides = tuple(dense[:len(shape)]), tuple(stride or dense[:len(shape)])
+
+    device = property(lambda self: f"cuda:{self.dev}" if self.dev >= 0 else "cpu")
+    is_cuda = property(lambda self: self.dev >= 0)
+    get_device = lambda self: self.dev
+    dim = lambda self: len(self.shape)
+    numel = lambda self: self.shape.numel()
+    stride = lambda self, d=None: self.strides if d is None else self.strides[d]
+    is_contiguous = lambda self: all(n == 1 or a == b for n, a, b in zip(self.shape, self.strides, self.dense))
+    data_ptr = lambda self: self.ptr
+
+
+I32, I64, BF16, U8 = torch.int32, torch.int64, torch.bfloat16, torch.uint8
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    got = []
+    monkeypatch.setattr(csa2, "_call", lambda fn, cache, dev, stream, *args: got.append((fn, dev, args)))
+    return got
+
+
+def _cache(dev=0, batch=2):
+    return types.SimpleNamespace(n_tokens=Fake(batch, dtype=I64, dev=dev), batch=batch, ratio=1, swa_dtype=csa2.SWA_MXFP8)
+
+
+def _append(c, dev=0, **kw):
+    a = dict(kv=Fake(3, 576, dev=dev), idx_key=Fake(3, 128, dev=dev), err=None)
+    a.update(kw)
+    csa2.kv_append_ragged(c, Fake(3, dtype=I32, dev=dev), Fake(64, 32, 2, dev=dev), **a)
+
+
+def _read(c, dev=0, **kw):
+    a = dict(out_main=Fake(3, 576, dev=dev), start=Fake(2, dtype=I64, dev=dev), err=None)
+    a.update(kw)
+    csa2.kv_read(c, Fake(3, dtype=I32, dev=dev), **a)
+
+
+def _attn(c, dev=0, **kw):
+    csa2.chunk_attn(c, Fake(3, 64, 576, dtype=BF16, dev=dev), Fake(3, dtype=I32, dev=dev), Fake(3, 64, 512, dev=dev),
+                    Fake(3, 64, dev=dev), Fake(1 << 20, dtype=U8, dev=dev), 0.1, **kw)
+
+
+CALLS = [_append, _read, _attn]
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_the_error_word_is_a_device_int32(calls, call):
+    """An error word that the device cannot write to: in host memory, on another device, of another type, empty."""
+    for bad in (Fake(1, dtype=I32, dev=-1), Fake(1, dtype=I32, dev=1), Fake(1, dtype=I64), Fake(0, dtype=I32)):
+        with pytest.raises(ValueError, match="err"):
+            call(_cache(), err=bad)
+    assert not calls
+    call(_cache(), err=Fake(1, dtype=I32, ptr=4096))
+    call(_cache())
+    assert len(calls) == 2 and 4096 in calls[0][2] and 4096 not in calls[1][2]
