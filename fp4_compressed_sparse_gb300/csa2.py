@@ -440,6 +440,14 @@ def _out_dtype(t):
     return OUT_BF16 if t.dtype is torch.bfloat16 else OUT_F32
 
 
+def _device(cache):
+    """The index of a cache's device."""
+    dev = cache.n_tokens.get_device()
+    if dev < 0:
+        raise ValueError(f"the cache is on {cache.n_tokens.device}, a CUDA device is needed")
+    return dev
+
+
 def _adr(t):
     return None if t is None else t.data_ptr()
 
@@ -507,7 +515,7 @@ def kv_append_ragged(cache: Cache, cu_new, rope_cs, kv=None, idx_key=None, cmp=N
     tokens.  Ratio 1: kv [total,576], idx_key [total,128] (fp32 or bf16, rows may be strided).  Ratio 2:
     cmp = (ca, cb, za, zb [total,704], ba, bb [2,704]) fp32.  max_new: a bound on the rows of one sequence
     (default: all).  win: from chunk_window(cache, total), filled for chunk_attn."""
-    dev = cache.n_tokens.get_device()
+    dev = _device(cache)
     _want("cu_new", cu_new, torch.int32, (cache.batch + 1,), dev)
     _want("rope_cs", rope_cs, torch.float32, None, dev)
     if rope_cs.dim() < 2 or rope_cs.numel() != 64 * rope_cs.shape[0]:
@@ -539,7 +547,7 @@ def kv_read(cache: Cache, cu_rows, out_main=None, out_key=None, pos=None, start=
     """csa2_kv_read: rows cu_rows[b] .. cu_rows[b+1]-1 read entries pos[r] (int32 [total], negative = zeros)
     of sequence b, or the stretch from start[b] (int64 [B]) on, into out_main [total,576] and / or out_key
     [total,128] (fp32 or bf16, rows may be strided)."""
-    dev = cache.n_tokens.get_device()
+    dev = _device(cache)
     _want("cu_rows", cu_rows, torch.int32, (cache.batch + 1,), dev)
     first = out_main if out_main is not None else out_key
     if first is None:
@@ -564,7 +572,7 @@ def kv_read(cache: Cache, cu_rows, out_main=None, out_key=None, pos=None, start=
 
 def window_read(cache: Cache, out, stream=None):
     """csa2_window_read: out [B,128,576] (fp32 or bf16), row i = token n_tokens - 128 + i (zeros before token 0)."""
-    dev = cache.n_tokens.get_device()
+    dev = _device(cache)
     _want("out", out, _FLOATS, (cache.batch, WINDOW, D_QK), dev)
     _call("csa2_window_read", cache, dev, stream, _adr(out), _out_dtype(out))
 
@@ -579,7 +587,7 @@ def chunk_attn(cache: Cache, q, cu_q, out, lse, ws, sm_scale, max_new=None, win=
     """csa2_chunk_attn: q bf16 [total,H,576], rows cu_q[b] .. cu_q[b+1]-1 the last tokens appended to sequence
     b -> out [total,H,512] (fp32 or bf16), lse fp32 [total,H].  win: the append's window rows (None: the ring,
     enough for single tokens).  ws: chunk_attn_workspace()."""
-    dev = cache.n_tokens.get_device()
+    dev = _device(cache)
     _want("q", q, torch.bfloat16, None, dev)
     if q.dim() != 3 or q.shape[2] != D_QK:
         raise ValueError(f"q: shape {tuple(q.shape)}, (total, heads, {D_QK}) is needed")

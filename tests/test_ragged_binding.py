@@ -72,3 +72,11 @@ def test_the_error_word_is_a_device_int32(calls, call):
     call(_cache(), err=Fake(1, dtype=I32, ptr=4096))
     call(_cache())
     assert len(calls) == 2 and 4096 in calls[0][2] and 4096 not in calls[1][2]
+
+
+@pytest.mark.parametrize("call", CALLS + [lambda c, dev: csa2.window_read(c, Fake(2, 128, 576, dev=dev))])
+def test_a_cache_in_host_memory(calls, call):
+    """Everything in host memory agrees on a device too, but not on one that the kernels can read."""
+    with pytest.raises(ValueError):
+        call(_cache(dev=-1), dev=-1)
+    assert not calls
