@@ -428,12 +428,12 @@ def _want_rows(name, t, dtype, width, dev, total=None):
     rows, w = t.shape
     if w != width or (total is not None and rows != total):
         raise ValueError(f"{name}: shape {(rows, w)}, ({'rows' if total is None else total}, {width}) is needed")
-    if rows <= 1:
+    if rows == 0:
         return width
     row, one = t.stride()
-    if one != 1 or row < width:
+    if one != 1 or (rows > 1 and row < width):
         raise ValueError(f"{name}: rows must be contiguous and not overlap")
-    return row
+    return row if rows > 1 else width
 
 
 def _out_dtype(t):

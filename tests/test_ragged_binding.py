@@ -80,3 +80,22 @@ def test_a_cache_in_host_memory(calls, call):
     with pytest.raises(ValueError):
         call(_cache(dev=-1), dev=-1)
     assert not calls
+
+
+@pytest.mark.parametrize("rows", [1, 2])
+def test_rows_are_contiguous_within(calls, rows):
+    """Every second column of a wider tensor, also for a single row; a single row of any row stride is fine."""
+    c, cu, rope = _cache(), Fake(3, dtype=I32), Fake(64, 32, 2)
+    every2 = lambda w: Fake(rows, w, stride=(2 * w, 2))
+    start = Fake(2, dtype=I64)
+    for bad in (lambda: csa2.kv_append_ragged(c, cu, rope, kv=every2(576), idx_key=Fake(rows, 128)),
+                lambda: csa2.kv_append_ragged(c, cu, rope, kv=Fake(rows, 576), idx_key=every2(128)),
+                lambda: csa2.kv_read(c, cu, out_main=every2(576), start=start),
+                lambda: csa2.kv_read(c, cu, out_key=every2(128), start=start)):
+        with pytest.raises(ValueError, match="contiguous"):
+            bad()
+    assert not calls
+    if rows == 1:
+        csa2.kv_append_ragged(c, cu, rope, kv=Fake(1, 576, stride=(1, 1)), idx_key=Fake(1, 128, stride=(7, 1)))
+        csa2.kv_read(c, cu, out_main=Fake(1, 576, stride=(0, 1)), start=start)
+        assert len(calls) == 2 and calls[0][2][1] == 576 and calls[0][2][3] == 128
