@@ -193,19 +193,22 @@ class Cache:
     def from_planes(cls, batch, capacity, planes, ratio=1, swa_dtype=SWA_MXFP8, page_entries=None, n_pages=None,
                     block_table=None, entry_format=ENTRY_FP4):
         """A cache over planes the caller already holds: `planes` maps the plane names (lat_codes ..
-        idx_scales, swa_codes, swa_scales, n_tokens, and cmp_buf for ratio 2) to contiguous device
-        tensors of the sizes csa2_entry_plane_bytes() and csa2_cache_plane_bytes() give; rope_scales
+        idx_scales, swa_codes, swa_scales, n_tokens, and cmp_buf for ratio 2) to contiguous tensors
+        on one device, of the sizes csa2_entry_plane_bytes() and csa2_cache_plane_bytes() give; rope_scales
         may be missing for ENTRY_FP8, swa_scales for SWA_BF16.  Nothing is copied."""
         L = load()
         c = cls.__new__(cls)
         c.batch, c.capacity, c.ratio, c.swa_dtype = batch, capacity, ratio, swa_dtype
         c.page_entries, c.entry_format, c.block_table = page_entries, entry_format, block_table
+        c.n_tokens = planes.get("n_tokens")
+        _want("n_tokens", c.n_tokens, torch.int64, (batch,))
+        dev = c.n_tokens.get_device()
         if page_entries:
             if capacity % page_entries or page_entries % 128:
                 raise ValueError(f"capacity {capacity} must be a multiple of page_entries {page_entries}, itself of 128")
             c.max_pages = capacity // page_entries
             c.n_pages = n_pages or batch * c.max_pages
-            _want("block_table", block_table, torch.int32, (batch, c.max_pages))
+            _want("block_table", block_table, torch.int32, (batch, c.max_pages), dev)
             rows, c.idx_tiles = c.n_pages * page_entries, c.n_pages * page_entries // 128
             tiles = c.idx_tiles
         else:
@@ -219,16 +222,15 @@ class Cache:
         for name, n in zip(names, need):
             t = planes.get(name)
             if t is not None:
-                _want(name, t, torch.uint8)
+                _want(name, t, torch.uint8, None, dev)
                 if t.numel() < n:
                     raise ValueError(f"{name} holds {t.numel()} of {n} bytes")
             elif n and not (name == "swa_scales" and swa_dtype == SWA_BF16):
                 raise ValueError(f"plane {name} is missing")
             setattr(c, name, t)
-        c.cmp_buf, c.n_tokens = planes.get("cmp_buf"), planes["n_tokens"]
-        _want("n_tokens", c.n_tokens, torch.int64, (batch,))
+        c.cmp_buf = planes.get("cmp_buf")
         if ratio == 2:
-            _want("cmp_buf", c.cmp_buf, torch.float32, (batch, 4, 4, D_CMP))
+            _want("cmp_buf", c.cmp_buf, torch.float32, (batch, 4, 4, D_CMP), dev)
         p = lambda t: t.data_ptr() if t is not None else None
         c.struct = CacheStruct(batch, capacity, ratio, swa_dtype, *[p(getattr(c, n)) for n in names], p(c.cmp_buf),
                                p(c.n_tokens), p(block_table), page_entries or 0, c.max_pages, c.n_pages, entry_format)

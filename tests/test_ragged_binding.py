@@ -99,3 +99,43 @@ def test_rows_are_contiguous_within(calls, rows):
         csa2.kv_append_ragged(c, cu, rope, kv=Fake(1, 576, stride=(1, 1)), idx_key=Fake(1, 128, stride=(7, 1)))
         csa2.kv_read(c, cu, out_main=Fake(1, 576, stride=(0, 1)), start=start)
         assert len(calls) == 2 and calls[0][2][1] == 576 and calls[0][2][3] == 128
+
+
+PLANES = dict(lat_codes=256 * 256, lat_scales=32 * 256, rope_codes=32 * 256, rope_scales=4 * 256, idx_codes=2 * 8192,
+              idx_scales=2 * 512, swa_codes=2 * 128 * 576, swa_scales=2 * 128 * 32)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from fp4_compressed_sparse_gb300 import build_lib
+    build_lib.build()
+    return csa2.load()
+
+
+def _planes(ratio=1):
+    """Planes of 2 sequences of 128 entries (dense, or two pages)."""
+    p = {k: Fake(n, dtype=U8) for k, n in PLANES.items()}
+    p["n_tokens"] = Fake(2, dtype=I64)
+    if ratio == 2:
+        p["cmp_buf"] = Fake(2, 4, 4, 704)
+    return p
+
+
+@pytest.mark.parametrize("ratio", [1, 2])
+def test_from_planes_on_one_device(lib, ratio):
+    """A plane or a block table on another device than the token counts: every plane in turn."""
+    paged = dict(page_entries=128, n_pages=2)
+    table = Fake(2, 1, dtype=I32)
+    csa2.Cache.from_planes(2, 128, _planes(ratio), ratio=ratio)
+    csa2.Cache.from_planes(2, 128, _planes(ratio), ratio=ratio, block_table=table, **paged)
+    for name in _planes(ratio):
+        p = _planes(ratio)
+        p[name].dev = 1
+        with pytest.raises(ValueError):
+            csa2.Cache.from_planes(2, 128, p, ratio=ratio)
+    with pytest.raises(ValueError, match="block_table"):
+        csa2.Cache.from_planes(2, 128, _planes(ratio), ratio=ratio, block_table=Fake(2, 1, dtype=I32, dev=1), **paged)
+    p = _planes(ratio)
+    del p["n_tokens"]
+    with pytest.raises(ValueError, match="n_tokens"):
+        csa2.Cache.from_planes(2, 128, p, ratio=ratio)
