@@ -20,7 +20,8 @@ __device__ __forceinline__ void append_fail(const csa2_cache &c, int64_t t0, int
 
 // One channel of a ratio-2 entry ([P5] §2.3.1): softmax over the gate logits
 // Z + B of the 4 rows (the b rows only when the entry has a predecessor), then
-// the gated sum of the C rows, in fp64, rounded once to fp32.
+// the gated sum of the C rows, in fp64, rounded once to fp32.  Without a predecessor
+// the b arguments may be anything (a weight of zero would not cover infinities).
 __device__ __forceinline__ float r2_compress_channel(float za0, float za1, float zb0, float zb1, float ba0, float ba1,
                                                      float bb0, float bb1, float ca0, float ca1, float cb0, float cb1,
                                                      bool has_b) {
@@ -35,8 +36,8 @@ __device__ __forceinline__ float r2_compress_channel(float za0, float za1, float
   double acc = 0.0;
   acc = __dadd_rn(acc, __dmul_rn(__ddiv_rn(e0, den), static_cast<double>(ca0)));
   acc = __dadd_rn(acc, __dmul_rn(__ddiv_rn(e1, den), static_cast<double>(ca1)));
-  acc = __dadd_rn(acc, __dmul_rn(__ddiv_rn(e2, den), static_cast<double>(cb0)));
-  acc = __dadd_rn(acc, __dmul_rn(__ddiv_rn(e3, den), static_cast<double>(cb1)));
+  acc = __dadd_rn(acc, __dmul_rn(__ddiv_rn(e2, den), has_b ? static_cast<double>(cb0) : 0.0));
+  acc = __dadd_rn(acc, __dmul_rn(__ddiv_rn(e3, den), has_b ? static_cast<double>(cb1) : 0.0));
   return __double2float_rn(acc);
 }
 

@@ -1,0 +1,65 @@
+"""Edges of the ragged calls: values that are not finite where they must not matter, NaN of either sign, lists
+of rows that are no lists, values of a key that lie far apart, planes of any shape."""
+import math
+
+import pytest
+import torch
+
+import ragged_util as ru
+from fp4_compressed_sparse_gb300 import csa2
+from test_gpu_ragged import DEV, THETA, _attn, _cache, _cu, _err, _filled, _lib, _q  # noqa: F401 (_lib: fixture)
+
+pytestmark = pytest.mark.gpu
+PLANES = ("lat_codes", "lat_scales", "rope_codes", "rope_scales", "idx_codes", "idx_scales", "swa_codes", "swa_scales")
+
+
+def _same_bytes(a, b):
+    """Every stored byte of two caches (of a bf16 window no scales are stored)."""
+    for name in PLANES + ("cmp_buf", "n_tokens"):
+        x, y = getattr(a, name), getattr(b, name)
+        if x is None or (name == "swa_scales" and a.swa_dtype == csa2.SWA_BF16):
+            continue
+        if name == "swa_scales":  # 18 of 32 are used
+            x, y = x[..., :18], y[..., :18]
+        if name == "cmp_buf":
+            x, y = x.view(torch.int32), y.view(torch.int32)
+        assert torch.equal(x, y), name
+
+
+def _r2_pair(rows, counts, swa=csa2.SWA_MXFP8, fmt=csa2.ENTRY_FP4, window=False):
+    """The same ratio-2 rows appended by the ragged call (as a batch of one) and by csa2_kv_append."""
+    a, b = (_cache(1, 64, ratio=2, swa=swa, fmt=fmt) for _ in range(2))
+    rope, err = csa2.rope_table(THETA, 128), _err()
+    bias = [torch.full((2, 704), 0.25, device=DEV), torch.full((2, 704), -0.5, device=DEV)]
+    at = 0
+    for n in counts:
+        part = [r[at:at + n].contiguous() for r in rows]
+        win = csa2.chunk_window(a, n) if window else None
+        csa2.kv_append_ragged(a, _cu([n]), rope, cmp=part + bias, max_new=n, win=win, err=err)
+        csa2.kv_append(b, rope_cs=rope, cmp=[r[None] for r in part] + bias, err=err)
+        at += n
+    assert int(err) == 0
+    return a, b
+
+
+def _rows4(n, seed=1):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    return [torch.randn(n, 704, generator=g, device=DEV) for _ in range(4)]
+
+
+@pytest.mark.parametrize("counts", [[2], [1, 1], [7]])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_r2_first_entry_has_no_predecessor(counts, bad):
+    """C^b and Z^b of the first pair belong to the next entry alone, whatever they hold."""
+    rows = _rows4(sum(counts))
+    rows[1][0, 5::7] = bad   # C^b
+    rows[3][0, 3::11] = bad  # Z^b
+    rows[1][1, 4::9] = bad
+    a, b = _r2_pair(rows, counts)
+    _same_bytes(a, b)
+    clean = [r.clone() for r in rows]
+    for i in (1, 3):
+        clean[i][:2] = 0.0
+    c, _ = _r2_pair(clean, counts)
+    zero = torch.zeros(1, dtype=torch.long, device=DEV)
+    assert torch.equal(ru.main_values(a, zero), ru.main_values(c, zero))
