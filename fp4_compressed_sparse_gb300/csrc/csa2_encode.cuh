@@ -168,7 +168,17 @@ __device__ __forceinline__ void warp_encode_swa(uint8_t *codes, uint8_t *scales,
 // The same encodings with a whole 256-thread block on one token: every thread
 // quantises 1..4 values and group maxima are lane shuffles, so the token's
 // ~1,300 values take a few dependent steps instead of one warp's long loops.
+//
+// kNanZero: a group of NaN alone becomes zeros, as with the warp encoders (their
+// maximum starts at 0); otherwise the largest codes, as csa2_kv_append writes them
+// at ratio 1.
 constexpr int kEncThreads = 256;
+
+// |x| where a group's maximum starts from
+template <bool kNanZero>
+__device__ __forceinline__ float mag(float x) {
+  return kNanZero ? fmaxf(0.0f, fabsf(x)) : fabsf(x);
+}
 
 // rot[0:64] = RoPE dims of row (row[512:576]) rotated with cs; threads 0..31.
 __device__ __forceinline__ void block_rope(const float *row, const float *cs, float *rot) {
@@ -195,8 +205,9 @@ __device__ __forceinline__ void block_rope_inplace(const float *row, float *rot)
 
 // Two values of an NVFP4 group of 16 held by 8 consecutive lanes: returns the
 // packed byte (first value in the low nibble); *sc = the group's scale code.
+template <bool kNanZero = false>
 __device__ __forceinline__ uint32_t nvfp4_pair(float x0, float x1, uint32_t *sc) {
-  float amax = fmaxf(fabsf(x0), fabsf(x1));
+  float amax = fmaxf(mag<kNanZero>(x0), fabsf(x1));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
@@ -212,6 +223,7 @@ __device__ __forceinline__ uint32_t nvfp4_pair(float x0, float x1, uint32_t *sc)
 
 // Entry e of sequence b from row[0:704] (smem: main vector, RoPE dims
 // unrotated, then the indexer key) and rot[0:64] (smem, rotated RoPE dims).
+template <bool kNanZero = false>
 __device__ __forceinline__ void block_encode_entry(const csa2_cache &c, int b, int64_t e, const float *row,
                                                    const float *rot, int32_t *err) {
   const int t = threadIdx.x, lane = t & 31;
@@ -228,7 +240,7 @@ __device__ __forceinline__ void block_encode_entry(const csa2_cache &c, int b, i
     const int warp = t >> 5;
     for (int g = warp; g < 16; g += kEncThreads / 32) {
       const float x = row[32 * g + lane];
-      float amax = fabsf(x);
+      float amax = mag<kNanZero>(x);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       uint32_t code = 0;
@@ -249,13 +261,13 @@ __device__ __forceinline__ void block_encode_entry(const csa2_cache &c, int b, i
   } else {
     {  // latent: thread t has dims 2t, 2t+1 (group t / 8)
       const float2 v = reinterpret_cast<const float2 *>(row)[t];
-      const uint32_t byte = nvfp4_pair(v.x, v.y, &sc);
+      const uint32_t byte = nvfp4_pair<kNanZero>(v.x, v.y, &sc);
       c.lat_codes[ent * 256 + t] = static_cast<uint8_t>(byte);
       if ((t & 7) == 0) c.lat_scales[ent * 32 + (t >> 3)] = static_cast<uint8_t>(sc);
     }
     if (t < 32) {  // RoPE sidecar: rotated dims 2t, 2t+1 (group t / 8)
       const float2 v = reinterpret_cast<const float2 *>(rot)[t];
-      const uint32_t byte = nvfp4_pair(v.x, v.y, &sc);
+      const uint32_t byte = nvfp4_pair<kNanZero>(v.x, v.y, &sc);
       c.rope_codes[ent * 32 + t] = static_cast<uint8_t>(byte);
       if ((t & 7) == 0) c.rope_scales[ent * 4 + (t >> 3)] = static_cast<uint8_t>(sc);
     }
@@ -263,7 +275,7 @@ __device__ __forceinline__ void block_encode_entry(const csa2_cache &c, int b, i
   if (t >= 32 && t < 64) {  // indexer key, MXFP4: lane l has dims 4l..4l+3 (block l / 8)
     const float4 v = reinterpret_cast<const float4 *>(row + kDqk)[lane];
     const float x[4] = {v.x, v.y, v.z, v.w};
-    float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+    float amax = fmaxf(fmaxf(mag<kNanZero>(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
@@ -286,6 +298,7 @@ __device__ __forceinline__ void block_encode_entry(const csa2_cache &c, int b, i
 
 // One window token from row[0:512] (smem) and rot[0:64] (smem) into codes
 // (576 B MXFP8 or 1152 B bf16) and scales (18 B, MXFP8).
+template <bool kNanZero = false>
 __device__ __forceinline__ void block_encode_swa(uint8_t *codes, uint8_t *scales, int swa_dtype, const float *row,
                                                  const float *rot) {
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -294,7 +307,7 @@ __device__ __forceinline__ void block_encode_swa(uint8_t *codes, uint8_t *scales
     for (int g = warp; g < 18; g += kEncThreads / 32) {
       const int d = 32 * g + lane;
       const float x = d < kLat ? row[d] : rot[d - kLat];
-      float amax = fabsf(x);
+      float amax = mag<kNanZero>(x);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       uint32_t code = 0, sc = 0;

@@ -324,7 +324,8 @@ __global__ void __launch_bounds__(256, 4) k_ragged_append_r1(RaggedAppend a, int
 
 // ---------------------------------------------------------------- ratio 2: a block per token
 // The compression (704 channels, fp64 softmax over four rows) is csa2_kv_append's,
-// and its arithmetic is what bounds it; every second token brings an entry.
+// and its arithmetic is what bounds it; every second token brings an entry.  Groups
+// of NaN alone become zeros, as csa2_kv_append's encoders for ratio 2 make them.
 // Blocks 0 .. total-1: one token each (its window row and, when it completes a
 // pair, the entry).  single: max_new is 1 and there are no window rows to leave,
 // so a token's block also finishes its sequence.
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(kEncThreads) k_ragged_append_r2(RaggedAppend a
     wc = c.swa_codes + i * swa_bytes(c);
     ws = c.swa_scales + i * kSwaScaleStride;
   }
-  if (wc != nullptr) block_encode_swa(wc, ws, c.swa_dtype, row, rot);
+  if (wc != nullptr) block_encode_swa<true>(wc, ws, c.swa_dtype, row, rot);
   if (t & 1) {  // the pair is complete: entry t / 2, at position t - 1
     const int64_t e = t >> 1;
     const float *src[2][4];  // [Z, C][a0, a1, b0, b1]
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(kEncThreads) k_ragged_append_r2(RaggedAppend a
     __syncthreads();
     block_rope_inplace(row, rot);
     __syncthreads();
-    block_encode_entry(c, b, e, row, rot, a.err);
+    block_encode_entry<true>(c, b, e, row, rot, a.err);
   }
   // a single token's slot (t % 4) is none of those its entry was made from
   if (single) {

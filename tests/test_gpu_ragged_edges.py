@@ -63,3 +63,21 @@ def test_r2_first_entry_has_no_predecessor(counts, bad):
     c, _ = _r2_pair(clean, counts)
     zero = torch.zeros(1, dtype=torch.long, device=DEV)
     assert torch.equal(ru.main_values(a, zero), ru.main_values(c, zero))
+
+
+@pytest.mark.parametrize("swa", [csa2.SWA_MXFP8, csa2.SWA_BF16])
+@pytest.mark.parametrize("fmt", [csa2.ENTRY_FP4, csa2.ENTRY_FP8])
+@pytest.mark.parametrize("counts,window", [([12], False), ([5, 1, 6], True), ([1] * 12, False)])
+def test_r2_special_values(swa, fmt, counts, window):
+    """NaN in single values, whole groups and whole rows, infinities, zeros: the bytes of csa2_kv_append."""
+    rows = _rows4(12, seed=2)
+    for i, t in enumerate(rows):
+        t[2 + i, 64:96] = math.nan       # a group of 32, and of 16 twice
+        t[3, 500:576] = math.nan         # the RoPE dims
+        t[7, 600:] = math.nan            # indexer keys
+        t[6, 17] = math.inf
+        t[8 + i % 2] = -0.0
+        t[10, ::3] = -math.inf
+    rows[0][11] = math.nan
+    a, b = _r2_pair(rows, counts, swa, fmt, window)
+    _same_bytes(a, b)
