@@ -111,6 +111,7 @@ __device__ __forceinline__ uint2 nvfp4_16(const float *x, uint32_t *scale) {
     return make_uint2(0, 0);
   }
   *scale = sc;
+  // (the sign bit of x s is that of x / s, which loses a NaN's)
   // |x| >= T[i] <=> code > i; ties go to the even code, so every other bound is
   // the number after the midpoint
   const uint32_t T0 = __float_as_uint(0.25f * s) + 1, T1 = __float_as_uint(0.75f * s), T2 = __float_as_uint(1.25f * s) + 1,
@@ -119,7 +120,7 @@ __device__ __forceinline__ uint2 nvfp4_16(const float *x, uint32_t *scale) {
   uint32_t w[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const uint32_t u = __float_as_uint(x[i]), v = u & 0x7FFFFFFFu;
+    const uint32_t v = __float_as_uint(x[i]) & 0x7FFFFFFFu, u = __float_as_uint(__fmul_rn(x[i], s));
     const bool g4 = v >= T3, g2 = v >= (g4 ? T5 : T1);
     const bool g1 = v >= (g4 ? (g2 ? T6 : T4) : (g2 ? T2 : T0));
     const uint32_t code = (g4 ? 4u : 0u) | (g2 ? 2u : 0u) | (g1 ? 1u : 0u) | ((u >> 28) & 8u);

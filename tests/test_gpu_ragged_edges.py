@@ -81,3 +81,32 @@ def test_r2_special_values(swa, fmt, counts, window):
     rows[0][11] = math.nan
     a, b = _r2_pair(rows, counts, swa, fmt, window)
     _same_bytes(a, b)
+
+
+@pytest.mark.parametrize("swa", [csa2.SWA_MXFP8, csa2.SWA_BF16])
+@pytest.mark.parametrize("fmt", [csa2.ENTRY_FP4, csa2.ENTRY_FP8])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_r1_nan_of_either_sign(swa, fmt, bf16):
+    """NaN with the sign bit set, beside other values and alone in its group."""
+    n = 9
+    g = torch.Generator(device=DEV).manual_seed(3)
+    kv, ik = (torch.randn(n, w, generator=g, device=DEV) for w in (576, 128))
+    for t in (kv, ik):
+        u = t.view(torch.int32)
+        u[1, 5] = -1                     # 0xFFFFFFFF
+        u[2, ::3] = -(1 << 22)           # 0xFFC00000
+        u[3] = -1
+        u[4, 32:64] = -(1 << 22)
+        u[5, -20:] = -1
+        u[6, ::2] = 0x7FC00000
+        u[6, 1::2] = -(1 << 22)
+    assert kv[1, 5].isnan() and kv[2, 3].isnan()
+    if bf16:
+        bits = [(t.view(torch.int32) >> 16).to(torch.int16) for t in (kv, ik)]
+        kv, ik = [b.view(torch.bfloat16) for b in bits]
+    rope, err = csa2.rope_table(THETA, 64), _err()
+    a, b = (_cache(1, 64, swa=swa, fmt=fmt) for _ in range(2))
+    csa2.kv_append_ragged(a, _cu([n]), rope, kv=kv, idx_key=ik, err=err)
+    csa2.kv_append(b, kv[None], ik[None], rope, err=err)
+    assert int(err) == 0
+    _same_bytes(a, b)
