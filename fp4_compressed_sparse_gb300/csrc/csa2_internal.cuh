@@ -65,6 +65,57 @@ __device__ __forceinline__ bool ragged_rows(const int32_t *cu, int b, int total,
   n = ok ? end - first : 0;
   return ok;
 }
+// The sequence of packed row r by a binary search (b -1: a row of no sequence), with
+// its rows as ragged_rows gives them.  n is 0 as well when the search met a bound on
+// its way that does not lie before or after those rows: the list decreases somewhere,
+// and the rows may be another sequence's too.  The way to b is the same for every row
+// that leads there, so a sequence's rows agree, and the rows of two sequences that
+// pass lie apart (where their ways part, one bound is behind the one's and before the
+// other's).
+struct RaggedRow {
+  int b, first, n;
+};
+__device__ __forceinline__ RaggedRow ragged_row(const int32_t *cu, int batch, int total, int max_new, int r) {
+  RaggedRow x{-1, cu[0], 0};
+  int end = cu[batch];
+  if (r >= end || r < x.first) return x;
+  int lo = 0, hi = batch, below = x.first, above = end;  // cu[lo] = x.first <= r < cu[hi] = end
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1, v = cu[mid];
+    if (v <= r) {
+      lo = mid;
+      x.first = v;
+      below = max(below, v);
+    } else {
+      hi = mid;
+      end = v;
+      above = min(above, v);
+    }
+  }
+  x.b = lo;
+  if (x.first >= 0 && end <= total && end - x.first <= max_new && below == x.first && above == end) x.n = end - x.first;
+  return x;
+}
+// Whether ragged_row would give rows first .. first + n - 1 to sequence b: bound number
+// `step` of the way there (0 and 1: the list's ends), true behind its end.
+__device__ __forceinline__ bool ragged_own_step(const int32_t *cu, int batch, int b, int first, int n, int step) {
+  if (step == 0) return cu[0] <= first;
+  if (step == 1) return cu[batch] >= first + n;
+  int lo = 0, hi = batch;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (--step == 1) return mid <= b ? cu[mid] <= first : cu[mid] >= first + n;
+    if (mid <= b) lo = mid;
+    else hi = mid;
+  }
+  return true;
+}
+constexpr int kOwnSteps = 18;  // of a batch of 65,535
+// ... all of them, by the block, a thread for each (a barrier).
+__device__ __forceinline__ bool block_ragged_own(const int32_t *cu, int batch, int b, int first, int n) {
+  const int t = threadIdx.x;
+  return __syncthreads_and(t >= kOwnSteps || ragged_own_step(cu, batch, b, first, n, t));
+}
 
 // ------------------------------------------------------------------ score sideband
 // Per score row, the index-score kernel also leaves a 13-bit histogram of the

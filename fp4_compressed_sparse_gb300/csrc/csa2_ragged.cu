@@ -65,6 +65,7 @@ __device__ __forceinline__ void copy_older(const RaggedAppend &a, int part) {
     if (i0 == 0 && threadIdx.x == 0) raise_err(a.err, CSA2_DEVERR_INDEX);
     return;
   }
+  if (!block_ragged_own(a.cu, c.batch, b, first, n)) return;  // (where the list decreases, the bit is raised)
   const int64_t t0 = c.n_tokens[b] - kWin;
   const int row16 = swa_bytes(c) / 16;
   for (int k = threadIdx.x; k < kWin / kCopyBlocks * (row16 + 2); k += blockDim.x) {
@@ -80,6 +81,14 @@ __device__ __forceinline__ void copy_older(const RaggedAppend &a, int part) {
       reinterpret_cast<uint4 *>(a.win_scales)[dst * 2 + w - row16] =
           t >= 0 ? reinterpret_cast<const uint4 *>(c.swa_scales)[src * 2 + w - row16] : zero;
   }
+}
+
+// Sequences without a row of theirs in the arrays are nobody's to report: a call
+// whose tokens' blocks are its only ones has some more for the list itself.
+__device__ __forceinline__ void check_list(const RaggedAppend &a, int part) {
+  const int b = part * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x);
+  int first, n;
+  if (b < a.c.batch && !ragged_rows(a.cu, b, a.total, a.max_new, first, n)) raise_err(a.err, CSA2_DEVERR_INDEX);
 }
 
 // ---------------------------------------------------------------- ratio 1: a warp per token
@@ -208,11 +217,13 @@ struct TokenPlace {
   int64_t t;
 };
 
-// Eight tokens per block.  Blocks behind the tokens' copy the older window rows.
+// Eight tokens per block.  Blocks behind the tokens' copy the older window rows, or
+// (single) check the list.
 template <bool kBf16>
 __global__ void __launch_bounds__(256, 4) k_ragged_append_r1(RaggedAppend a, int single, int token_blocks) {
   if (static_cast<int>(blockIdx.x) >= token_blocks) {
-    copy_older(a, blockIdx.x - token_blocks);
+    if (single) check_list(a, blockIdx.x - token_blocks);
+    else copy_older(a, blockIdx.x - token_blocks);
     return;
   }
   const csa2_cache &c = a.c;
@@ -223,10 +234,10 @@ __global__ void __launch_bounds__(256, 4) k_ragged_append_r1(RaggedAppend a, int
   if (r >= a.total) return;
   load_token(a, r, lane, cur);
   TokenPlace pl{-1, -1, -1, 0};  // (the same in every lane)
-  const int b = ragged_seq(a.cu, c.batch, r);
+  const RaggedRow rr = ragged_row(a.cu, c.batch, a.total, a.max_new, r);
+  const int b = rr.b, first = rr.first, n = rr.n;
   if (b < 0) return;
-  int first, n;
-  if (!ragged_rows(a.cu, b, a.total, a.max_new, first, n)) {
+  if (n == 0) {
     if (lane == 0) raise_err(a.err, CSA2_DEVERR_INDEX);
     return;
   }
@@ -333,16 +344,17 @@ __global__ void __launch_bounds__(256, 4) k_ragged_append_r1(RaggedAppend a, int
 __global__ void __launch_bounds__(kEncThreads) k_ragged_append_r2(RaggedAppend a, int single) {
   const csa2_cache &c = a.c;
   if (static_cast<int>(blockIdx.x) >= a.total) {
-    copy_older(a, blockIdx.x - a.total);
+    if (single) check_list(a, blockIdx.x - a.total);
+    else copy_older(a, blockIdx.x - a.total);
     return;
   }
   __shared__ __align__(16) float row[kDcmp];
   __shared__ __align__(16) float rot[kRope];
   const int r = blockIdx.x;
-  const int b = ragged_seq(a.cu, c.batch, r);
+  const RaggedRow rr = ragged_row(a.cu, c.batch, a.total, a.max_new, r);
+  const int b = rr.b, first = rr.first, n = rr.n;
   if (b < 0) return;
-  int first, n;
-  if (!ragged_rows(a.cu, b, a.total, a.max_new, first, n)) {
+  if (n == 0) {
     if (threadIdx.x == 0) raise_err(a.err, CSA2_DEVERR_INDEX);
     return;
   }
@@ -405,9 +417,13 @@ __global__ void __launch_bounds__(256) k_ragged_finish(RaggedAppend a) {
   const csa2_cache &c = a.c;
   const int b = blockIdx.x;
   int first, n;
-  if (!ragged_rows(a.cu, b, a.total, a.max_new, first, n) || n == 0) return;
+  if (!ragged_rows(a.cu, b, a.total, a.max_new, first, n)) {
+    if (threadIdx.x == 0) raise_err(a.err, CSA2_DEVERR_INDEX);
+    return;
+  }
+  if (n == 0) return;
   const int64_t t0 = c.n_tokens[b];
-  if (!append_ok(c, t0, n, a.rope_len)) return;
+  if (!block_ragged_own(a.cu, c.batch, b, first, n) || !append_ok(c, t0, n, a.rope_len)) return;
   if (a.win_codes != nullptr) {
     const int m = min(n, kWin), row16 = swa_bytes(c) / 16;
     const bool scales = c.swa_dtype == CSA2_SWA_MXFP8;
@@ -711,13 +727,15 @@ csa2_status csa2_kv_append_ragged(const csa2_cache *cache, const void *kv, int64
   a.err = err_word;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int single = max_new == 1 && win_codes == nullptr;
-  const int copies = win_codes != nullptr ? csa2::kCopyBlocks * cache->batch : 0;
+  // blocks behind the tokens'
+  const int more = single ? (cache->batch + 255) / 256 : win_codes != nullptr ? csa2::kCopyBlocks * cache->batch : 0;
+  static_assert(csa2::kEncThreads == 256, "the list's blocks");
   if (cache->ratio == 2) {
-    csa2::k_ragged_append_r2<<<total + copies, csa2::kEncThreads, 0, s>>>(a, single);
+    csa2::k_ragged_append_r2<<<total + more, csa2::kEncThreads, 0, s>>>(a, single);
   } else {
     const int blocks = (total + 7) / 8;
     auto kern = in_dtype == CSA2_IN_BF16 ? csa2::k_ragged_append_r1<true> : csa2::k_ragged_append_r1<false>;
-    kern<<<blocks + copies, 256, 0, s>>>(a, single, blocks);
+    kern<<<blocks + more, 256, 0, s>>>(a, single, blocks);
   }
   if (!single) csa2::k_ragged_finish<<<cache->batch, 256, 0, s>>>(a);
   return cuda_status(cudaGetLastError(), "csa2_kv_append_ragged launch");

@@ -386,7 +386,8 @@ csa2_status csa2_prefill_chunk(const csa2_cache *cache, int32_t seq, const csa2_
  * (or captured graph) may serve batches that fill it differently; outputs of
  * those rows are left as they were.  max_new is the caller's bound on
  * cu[b+1]-cu[b] (host; it decides launch shapes): a sequence that breaks it, or
- * whose cu does not fit the arrays, is skipped with the INDEX bit.
+ * whose cu does not fit the arrays, is skipped with the INDEX bit, and so is one
+ * whose rows a list that decreases somewhere gives to another one too.
  *
  * Window rows of a chunk.  The ring holds a sequence's last 128 tokens, but a
  * chunk's earlier queries look further back: for them the append leaves, per

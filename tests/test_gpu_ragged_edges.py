@@ -110,3 +110,58 @@ def test_r1_nan_of_either_sign(swa, fmt, bf16):
     csa2.kv_append(b, kv[None], ik[None], rope, err=err)
     assert int(err) == 0
     _same_bytes(a, b)
+
+
+def _list(*v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+# lists of row bounds over 3 sequences: rows, bound on a sequence's rows, which sequences keep their rows
+BROKEN = [
+    ((0, 4, 4, 10), 4, 6, (0, 1)),          # the last one's rows lie behind the arrays
+    ((0, 1, 2, 2), 1, 1, (0, 2)),           # the same with single tokens
+    ((0, 10, 8, 18), 30, 10, (0,)),         # decreasing: the last one's rows overlap the first one's
+    ((0, 4, 10, 14), 14, 5, (0, 2)),        # over the bound
+    ((0, 300, 10, 400), 400, 400, (0,)),    # decreasing far: the last one's older tokens would fall among the first one's
+    ((-3, 2, 4, 5), 5, 5, (1, 2)),          # a negative start
+    ((0, 0, 5, 3), 8, 8, ()),               # decreasing at the end: no list at all for the middle one
+    ((0, 1, 0, 1), 1, 1, (0,)),              # two claim the same row: the first one's
+]
+
+
+@pytest.mark.parametrize("bounds,total,mx,kept", BROKEN)
+@pytest.mark.parametrize("ratio", [1, 2])
+@pytest.mark.parametrize("window", [False, True])
+def test_append_broken_lists(bounds, total, mx, kept, ratio, window):
+    """Every broken list raises INDEX; a sequence that cannot be told its rows is left alone, the others are
+    appended as by themselves."""
+    def fresh(batch, start):
+        c = _cache(batch, 512, ratio=ratio)
+        g = torch.Generator(device=DEV).manual_seed(1)
+        c.swa_codes.copy_(torch.randint(0, 100, c.swa_codes.shape, generator=g, device=DEV, dtype=torch.uint8)[:1].expand_as(c.swa_codes))
+        c.n_tokens.fill_(start)
+        return c
+    start, rope = 6, csa2.rope_table(THETA, 1100)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    rows = [torch.randn(total, w, generator=g, device=DEV) for w in ((576, 128) if ratio == 1 else (704,) * 4)]
+    bias = [torch.zeros(2, 704, device=DEV)] * 2
+    def append(c, cu, rows, mx, win, err):
+        kw = dict(kv=rows[0], idx_key=rows[1]) if ratio == 1 else dict(cmp=rows + bias)
+        csa2.kv_append_ragged(c, cu, rope, max_new=mx, win=win, err=err, **kw)
+    c, err = fresh(3, start), _err()
+    win = csa2.chunk_window(c, total) if window else None
+    append(c, _list(*bounds), rows, mx, win, err)
+    assert int(err) == csa2.DEVERR_INDEX
+    for b in range(3):
+        lo, hi = bounds[b], bounds[b + 1]
+        one, e1 = fresh(1, start), _err()
+        n = hi - lo if b in kept else 0
+        if n > 0:
+            w1 = csa2.chunk_window(one, n) if window else None
+            append(one, _list(0, n), [r[lo:hi].contiguous() for r in rows], n, w1, e1)
+            if window:
+                r0 = lo + 128 * b
+                assert torch.equal(win.codes[r0:r0 + n + 128], w1.codes)
+        assert int(e1) == 0 and int(c.n_tokens[b]) == start + n
+        for name in ("lat_codes", "lat_scales", "rope_codes", "swa_codes") + (("cmp_buf",) if ratio == 2 else ()):
+            assert torch.equal(getattr(c, name)[b], getattr(one, name)[0]), (b, name)
