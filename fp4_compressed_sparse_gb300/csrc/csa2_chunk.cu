@@ -161,10 +161,15 @@ __global__ void __launch_bounds__(1024) k_chunk_plan(ChunkArgs a, Plan p) {
     carry = 0;
     seq_tile[0] = 0;
   }
+  // where the list decreases, sequences may have rows in common
+  int falls = 0;
+  for (int b = tid; b < c.batch; b += nthr) falls |= a.cu[b + 1] < a.cu[b];
+  falls = __syncthreads_or(falls);
   for (int b0 = 0; b0 < c.batch; b0 += nthr) {  // row tiles of each sequence
     const int b = b0 + tid;
     int first = 0, n = 0;
     if (b < c.batch && !ragged_rows(a.cu, b, a.total, a.max_new, first, n)) raise_err(a.err, CSA2_DEVERR_INDEX);
+    if (falls && n > 0 && !ragged_own(a.cu, c.batch, b, first, n)) n = 0;
     const int64_t rt = (static_cast<int64_t>(n) * a.heads + kRows - 1) / kRows;
     const int64_t incl = block_scan(rt, sh) + carry;
     if (b < c.batch) seq_tile[b + 1] = static_cast<int32_t>(min(incl, static_cast<int64_t>(p.max_tiles)));
@@ -172,8 +177,6 @@ __global__ void __launch_bounds__(1024) k_chunk_plan(ChunkArgs a, Plan p) {
     if (tid == nthr - 1) carry = incl;
     __syncthreads();
   }
-  // overlapping sequences (a broken cu) may ask for more row tiles than there are rows
-  if (tid == 0 && carry > p.max_tiles) raise_err(a.err, CSA2_DEVERR_INDEX);
   const int n_tiles = static_cast<int>(min(carry, static_cast<int64_t>(p.max_tiles)));
   const bool fits = n_tiles <= kListTile;
   int64_t *cum = fits ? l_cum : p.cum;

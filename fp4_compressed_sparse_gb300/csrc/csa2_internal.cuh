@@ -111,6 +111,12 @@ __device__ __forceinline__ bool ragged_own_step(const int32_t *cu, int batch, in
   return true;
 }
 constexpr int kOwnSteps = 18;  // of a batch of 65,535
+// ... all of them, by one thread (few loads wait for one another).
+__device__ __forceinline__ bool ragged_own(const int32_t *cu, int batch, int b, int first, int n) {
+  bool ok = true;
+  for (int step = 0; step < kOwnSteps; ++step) ok = ragged_own_step(cu, batch, b, first, n, step) && ok;
+  return ok;
+}
 // ... all of them, by the block, a thread for each (a barrier).
 __device__ __forceinline__ bool block_ragged_own(const int32_t *cu, int batch, int b, int first, int n) {
   const int t = threadIdx.x;

@@ -165,3 +165,28 @@ def test_append_broken_lists(bounds, total, mx, kept, ratio, window):
         assert int(e1) == 0 and int(c.n_tokens[b]) == start + n
         for name in ("lat_codes", "lat_scales", "rope_codes", "swa_codes") + (("cmp_buf",) if ratio == 2 else ()):
             assert torch.equal(getattr(c, name)[b], getattr(one, name)[0]), (b, name)
+
+
+@pytest.mark.parametrize("bounds,total,mx,kept", BROKEN)
+def test_attn_broken_lists(bounds, total, mx, kept):
+    """The same for the attention."""
+    c, _ = _filled(3, [450, 460, 470], 512)
+    q = _q(total, 16)
+    win = csa2.chunk_window(c, total)
+    g = torch.Generator(device=DEV).manual_seed(6)
+    win.codes.copy_(torch.randint(0x20, 0x40, win.codes.shape, generator=g, device=DEV, dtype=torch.uint8))  # 2^-3 .. 2
+    win.scales.fill_(127)
+    out, lse, bits = _attn(c, q, _list(*bounds), win, max_new=mx)
+    assert bits == csa2.DEVERR_INDEX
+    live = torch.zeros(total, dtype=torch.bool, device=DEV)
+    for b in kept:
+        lo, hi = bounds[b], bounds[b + 1]
+        if hi <= lo:
+            continue
+        live[lo:hi] = True
+        n = hi - lo
+        w1 = csa2.ChunkWindow(win.codes[lo + 128 * b:hi + 128 * (b + 1)], win.scales[lo + 128 * b:hi + 128 * (b + 1)])
+        one = csa2.Cache.from_planes(1, 512, {k: getattr(c, k)[b:b + 1] for k in PLANES + ("n_tokens",)})
+        ref = ru.chunk_attn(one, q[lo:hi], _cu([n]), 1 / math.sqrt(576), w1)
+        ru.attn_within(out[lo:hi], lse[lo:hi], ref)
+    assert (out[~live] == 5).all() and (lse[~live] == 5).all()
