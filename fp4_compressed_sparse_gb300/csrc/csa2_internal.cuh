@@ -44,18 +44,6 @@ cudaError_t launch_kv_append(const csa2_cache &c, const void *kv, const void *ik
                              float *cmp_dbg, int32_t *err, cudaStream_t s);
 
 // ------------------------------------------------------------------ ragged batches
-// Sequence of packed row r: the last b with cu[b] <= r, or -1 for a row of no
-// sequence (r >= cu[batch], or before cu[0]).
-__device__ __forceinline__ int ragged_seq(const int32_t *cu, int batch, int r) {
-  if (r >= cu[batch] || r < cu[0]) return -1;
-  int lo = 0, hi = batch;  // cu[lo] <= r < cu[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= r) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
 // Rows of sequence b: its first row and their number; false (count 0) when cu is
 // not a non-decreasing list within 0..total, or the count breaks max_new.
 __device__ __forceinline__ bool ragged_rows(const int32_t *cu, int b, int total, int max_new, int &first, int &n) {

@@ -541,10 +541,14 @@ __global__ void __launch_bounds__(256, 4) k_kv_read(ReadArgs a) {
     const int64_t r = r0 + tid;
     // (requested before the search for the sequence, which does not need it)
     const int32_t listed = a.pos != nullptr && r < a.total ? __ldg(a.pos + r) : 0;
-    const int b = r < a.total ? ragged_seq(a.cu, c.batch, static_cast<int>(r)) : -1;
-    if (b >= 0) {
+    RaggedRow rr{-1, 0, 0};
+    if (r < a.total) rr = ragged_row(a.cu, c.batch, a.total, a.total, static_cast<int>(r));
+    const int b = rr.b;
+    if (b >= 0 && rr.n == 0) {
+      raise_err(a.err, CSA2_DEVERR_INDEX);  // (no row: left as it was)
+    } else if (b >= 0) {
       pl.pe = -1;
-      const int64_t e = a.pos ? static_cast<int64_t>(listed) : a.start[b] + (r - a.cu[b]);
+      const int64_t e = a.pos ? static_cast<int64_t>(listed) : a.start[b] + (r - rr.first);
       bool bad = e < 0 && a.pos == nullptr;  // a negative start
       if (e >= 0) {
         bad = e >= c.n_tokens[b] >> (c.ratio - 1) || e >= c.capacity;
@@ -562,6 +566,11 @@ __global__ void __launch_bounds__(256, 4) k_kv_read(ReadArgs a) {
       }
     }
     place[tid] = pl;
+  }
+  // sequences that have no row in the arrays (the threads without a row first)
+  for (int b = blockIdx.x * 256 + (255 - tid); b < c.batch; b += gridDim.x * 256) {
+    int first, n;
+    if (!ragged_rows(a.cu, b, a.total, a.total, first, n)) raise_err(a.err, CSA2_DEVERR_INDEX);
   }
   __syncthreads();
   const bool fp8 = c.entry_format == CSA2_ENTRY_FP8;

@@ -435,9 +435,10 @@ csa2_status csa2_kv_append_ragged(const csa2_cache *cache, const void *kv, int64
  *   out_key: rows of 128 (the indexer key), or NULL; out_dtype, row strides in
  *   elements (>= 576 / 128, multiples of 8).  Every value is exact in fp32, and in
  *   bf16 too for FP4 records and keys, MXFP8 latents and bf16 RoPE dims.
- *   Empty rows are zeros.  Rows of no sequence are left as they were.
+ *   Empty rows are zeros.  Rows of no sequence, or of a skipped one, are left as
+ *   they were.
  * Device errors: INDEX (an entry not in the cache, floor(n_tokens/ratio) or more,
- * a negative start, or a bad page id: the row is zeros).
+ * a negative start, or a bad page id: the row is zeros; cu).
  */
 csa2_status csa2_kv_read(const csa2_cache *cache, const int32_t *cu_rows, int32_t total, const int32_t *pos,
                          const int64_t *start, void *out_main, int64_t main_stride, void *out_key, int64_t key_stride,

@@ -190,3 +190,25 @@ def test_attn_broken_lists(bounds, total, mx, kept):
         ref = ru.chunk_attn(one, q[lo:hi], _cu([n]), 1 / math.sqrt(576), w1)
         ru.attn_within(out[lo:hi], lse[lo:hi], ref)
     assert (out[~live] == 5).all() and (lse[~live] == 5).all()
+
+
+@pytest.mark.parametrize("bounds,total,mx,kept", [x for x in BROKEN if x[0] != (0, 4, 10, 14)])  # (reads have no bound)
+@pytest.mark.parametrize("listed", [False, True])
+def test_read_broken_lists(bounds, total, mx, kept, listed):
+    """The same for reads: INDEX, and the rows of a sequence that cannot be told them are left as they were."""
+    c, _ = _filled(3, [450, 460, 470], 512)
+    out, key = torch.full((total, 576), 7.0, device=DEV), torch.full((total, 128), 7.0, device=DEV)
+    want, wkey = out.clone(), key.clone()
+    pos = torch.arange(total, device=DEV).to(torch.int32)
+    start = torch.tensor([3, 1, 2], device=DEV)
+    err = _err()
+    csa2.kv_read(c, _list(*bounds), out_main=out, out_key=key, pos=pos if listed else None,
+                 start=None if listed else start, err=err)
+    assert int(err) == csa2.DEVERR_INDEX
+    for b in kept:
+        lo, hi = bounds[b], bounds[b + 1]
+        if hi > lo:
+            ent = pos[lo:hi].long() if listed else start[b] + torch.arange(hi - lo, device=DEV)
+            want[lo:hi] = ru.main_values(c, ru.phys(c, b, ent)).float()
+            wkey[lo:hi] = ru.key_values(c, b, ent).float()
+    assert torch.equal(out, want) and torch.equal(key, wkey)
