@@ -568,9 +568,9 @@ __global__ void __launch_bounds__(256, 4) k_kv_read(ReadArgs a) {
     place[tid] = pl;
   }
   // sequences that have no row in the arrays (the threads without a row first)
-  for (int b = blockIdx.x * 256 + (255 - tid); b < c.batch; b += gridDim.x * 256) {
+  for (int64_t b = static_cast<int64_t>(blockIdx.x) * 256 + (255 - tid); b < c.batch; b += static_cast<int64_t>(gridDim.x) * 256) {
     int first, n;
-    if (!ragged_rows(a.cu, b, a.total, a.total, first, n)) raise_err(a.err, CSA2_DEVERR_INDEX);
+    if (!ragged_rows(a.cu, static_cast<int>(b), a.total, a.total, first, n)) raise_err(a.err, CSA2_DEVERR_INDEX);
   }
   __syncthreads();
   const bool fp8 = c.entry_format == CSA2_ENTRY_FP8;
