@@ -7,6 +7,7 @@ There is no CPU fallback: if libcsa2.so is not built, load() raises.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -219,12 +220,16 @@ class Cache:
             [L.csa2_cache_plane_bytes(batch, capacity, p, swa_dtype) for p in (6, 7)]
         names = ("lat_codes", "lat_scales", "rope_codes", "rope_scales", "idx_codes", "idx_scales", "swa_codes",
                  "swa_scales")
-        for name, n in zip(names, need):
+        lead = [(rows,) if page_entries else (batch, capacity)] * 4 + [(tiles,) if page_entries else (batch, tiles // batch)] * 2 + \
+            [(batch, WINDOW)] * 2
+        for name, n, shape in zip(names, need, lead):
             t = planes.get(name)
             if t is not None:
                 _want(name, t, torch.uint8, None, dev)
                 if t.numel() < n:
                     raise ValueError(f"{name} holds {t.numel()} of {n} bytes")
+                if n:  # (of any shape, and longer ones: seen as __init__ lays them out)
+                    t = t.view(-1)[:n].view(*shape, n // math.prod(shape))
             elif n and not (name == "swa_scales" and swa_dtype == SWA_BF16):
                 raise ValueError(f"plane {name} is missing")
             setattr(c, name, t)

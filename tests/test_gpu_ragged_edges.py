@@ -212,3 +212,17 @@ def test_read_broken_lists(bounds, total, mx, kept, listed):
             want[lo:hi] = ru.main_values(c, ru.phys(c, b, ent)).float()
             wkey[lo:hi] = ru.key_values(c, b, ent).float()
     assert torch.equal(out, want) and torch.equal(key, wkey)
+
+
+def test_from_planes_of_any_shape():
+    """Flat planes, and longer ones than needed: the helpers that show entries see the shapes of a cache."""
+    for page in (None, 128):
+        c, _ = _filled(2, [200, 70], 256, page=page)
+        flat = {n: torch.cat([getattr(c, n).reshape(-1), torch.full((32,), 9, dtype=torch.uint8, device=DEV)]) for n in PLANES}
+        flat["n_tokens"] = c.n_tokens
+        d = csa2.Cache.from_planes(2, 256, flat, page_entries=page, n_pages=c.n_pages or None, block_table=c.block_table)
+        for n in PLANES[:4]:
+            assert torch.equal(d.plane(n), c.plane(n))
+        for x, y in zip(d.idx_entries(), c.idx_entries()):
+            assert torch.equal(x, y)
+        assert torch.equal(d.swa_codes, c.swa_codes) and torch.equal(d.swa_scales, c.swa_scales)

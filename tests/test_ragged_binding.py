@@ -26,6 +26,8 @@ class Fake:
     stride = lambda self, d=None: self.strides if d is None else self.strides[d]
     is_contiguous = lambda self: all(n == 1 or a == b for n, a, b in zip(self.shape, self.strides, self.dense))
     data_ptr = lambda self: self.ptr
+    view = lambda self, *shape: Fake(*shape, dtype=self.dtype, dev=self.dev, ptr=self.ptr) if shape != (-1,) else self
+    __getitem__ = lambda self, at: self
 
 
 I32, I64, BF16, U8 = torch.int32, torch.int64, torch.bfloat16, torch.uint8
