@@ -226,3 +226,40 @@ def test_from_planes_of_any_shape():
         for x, y in zip(d.idx_entries(), c.idx_entries()):
             assert torch.equal(x, y)
         assert torch.equal(d.swa_codes, c.swa_codes) and torch.equal(d.swa_scales, c.swa_scales)
+
+
+def _within_values(out, lse, ref, q, scale):
+    """ru.attn_within() for keys whose values the operands hold to 2^-25 (fp16's step is 2^-24; keys of a
+    largest magnitude of 1 to 2^16, which go in as they are), and 2^-34 more for a block of values whose codes
+    are rounded to E4M3's step of 2^-9 at 2^-24 first: D.  The outputs, weighted means of the values, move by D
+    at most, a logit by scale sum |q| D."""
+    o, l, mag, dot, small = ref
+    D = 2.0 ** -25 + 2.0 ** -34
+    ez = 40 * 2.0 ** -23 * dot + 2.0 ** -22 * (1 + l.abs()) + scale * q.double().abs().sum(-1) * D
+    assert ((lse.double() - l).abs() <= ez).all()
+    tol = (2.0 ** -11 + 2.0 ** -16 + 2 * ez[..., None]) * mag + 2.0 ** -29 * small + 2.0 ** -30 + D
+    err = (out.double() - o).abs()
+    assert (err <= tol).all(), float((err / tol).max())
+
+
+@pytest.mark.parametrize("fmt,swa", [(csa2.ENTRY_FP8, csa2.SWA_MXFP8), (csa2.ENTRY_FP8, csa2.SWA_BF16),
+                                     (csa2.ENTRY_FP4, csa2.SWA_MXFP8)])
+@pytest.mark.parametrize("prior,new", [(500, 3), (0, 200), (40, 1)])
+def test_attn_small_blocks_beside_large_ones(fmt, swa, prior, new):
+    """Blocks of 32 dims far below the key's largest magnitude, whose scale fp16 does not have."""
+    c, rope = _cache(1, 640, swa=swa, fmt=fmt), csa2.rope_table(THETA, 640)
+    g = torch.Generator(device=DEV).manual_seed(4)
+    kv = torch.randn(prior + new, 576, generator=g, device=DEV)
+    for blk, e in ((1, -17), (2, -19), (3, -23), (4, -27), (5, -40), (9, -16), (15, -12)):
+        # 2^e to 2^(e + 1), one sign: the mean is as large
+        kv[:, 32 * blk:32 * blk + 32] = (1 + torch.rand(prior + new, 32, generator=g, device=DEV)) * 2.0 ** e
+    kv[:, 540:570] *= 2.0 ** -18  # RoPE dims too
+    ik, err = torch.zeros(prior + new, 128, device=DEV), _err()
+    if prior:
+        csa2.kv_append_ragged(c, _cu([prior]), rope, kv=kv[:prior], idx_key=ik[:prior], err=err)
+    win, cu, scale = csa2.chunk_window(c, new), _cu([new]), 1 / math.sqrt(576)
+    csa2.kv_append_ragged(c, cu, rope, kv=kv[prior:], idx_key=ik[prior:], win=win, err=err)
+    q = _q(new, 64)
+    out, lse, bits = _attn(c, q, cu, win)
+    assert bits == 0 and int(err) == 0
+    _within_values(out, lse, ru.chunk_attn(c, q, cu, scale, win), q, scale)
