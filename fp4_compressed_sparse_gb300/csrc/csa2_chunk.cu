@@ -14,9 +14,15 @@
 // that were shared.
 //
 // Work and bound.  2 x 1088 flop per (row, key) against 324 B per key: with 64
-// heads 430 flop per byte, so the tensor cores bound it, not HBM.  fp16 operands
-// hold the records exactly (E2M1 x E4M3 has 6 significant bits; other formats
-// with a power of two per key), accumulators are fp32.
+// heads 430 flop per byte, so the tensor cores bound it, not HBM.
+//
+// Precision.  S, the sums and O^T are fp32, the operands fp16.  FP4 records are exact
+// (E2M1 x E4M3: 6 significant bits, 2^-10 to 2688).  The values of V4 entries and of
+// window tokens go in divided by a power of two s per key, 1 where the key's largest
+// magnitude is 2^0 to 2^16 (sigma_of): fp16's step there makes them off by 2^-25 s.  The
+// weights p, times s, are rounded to fp16 as well, as the MMA takes both operands in
+// one type: by 2^-11 of themselves (a bf16 output's rounding is 2^-9), and below
+// 2^-14 on a scale on which a row's largest is 2^4 at least by 2^-29 of that.
 //
 // Tiles.  O^T of 64 rows is 256 columns of tensor memory beside two S; 128 rows
 // would take all 512 and leave none for S.  Beside the query (72 KB) two key
@@ -29,10 +35,10 @@
 // shared memory at 128 B per cycle), the fill's stores 576 more of the same
 // bandwidth, so what overlaps also slows each other down.  Tensor pipe 35 %, ALU
 // 36 %, issue slots 37 %.
-// Measured: 1,024 queries of 64 heads over 15,000 V4 entries 3.46 ms (644 TFLOP/s,
-// 34 % of the measured bf16 rate); ragged chunks over FP4 entries 1.32 ms (577);
-// 32 single tokens over 8K entries each 93 us, 16 over up to 65K 153 us (507); one
-// over 1,000 23 us, of which the three launches' round trips are nearly all.
+// Measured: 1,024 queries of 64 heads over 15,000 V4 entries 3.53 ms (632 TFLOP/s,
+// 33 % of the measured bf16 rate); ragged chunks over FP4 entries 1.34 ms (570);
+// 32 single tokens over 8K entries each 94 us, 16 over up to 65K 154 us (504); one
+// over 1,000 24 us, of which the three launches' round trips are nearly all.
 #include <atomic>
 #include <cmath>
 #include <cuda_fp16.h>
@@ -141,7 +147,8 @@ __device__ __forceinline__ int last_at_most(const T *list, int n, T v) {
   return lo;
 }
 
-// One block: 5 us for decode batches, 10 us for a thousand row tiles.  The two
+// One block: 5 us for decode batches, 10 us for a thousand row tiles, 64 us for 16,384
+// (lists too long for shared memory; the attention of those then takes 26 ms).  The two
 // lists it searches (first row tile of each sequence, first unit of each row tile)
 // are kept in shared memory as far as they fit, as a search in global memory is a
 // chain of L2 round trips.

@@ -98,9 +98,9 @@ __device__ __forceinline__ void check_list(const RaggedAppend &a, int part) {
 // the sequence, its length, the page).
 //
 // 32,768 bf16 tokens in the V4 format take 24 us: 70 MB, 2.9 TB/s, 43 % of the
-// measured HBM rate; 12,871 fp32 tokens in FP4 19.5 us.  What is left are the
-// quantisers' instructions and the round trips.  Latency is hidden by other warps,
-// four blocks per SM (64 registers).  One thread per token finding its place for
+// measured HBM rate; 12,871 fp32 tokens in FP4 19.5 us.  Nothing is saturated (SM
+// 59 %, ALU 53 %, DRAM 27 %): the quantisers' instructions and the round trips share
+// the time.  Latency is hidden by other warps, four blocks per SM (64 registers).  One thread per token finding its place for
 // the block, with a barrier, took 27 us; several tokens per warp, the next row
 // requested ahead, 30 us; a block per token through shared memory 261 us.
 
@@ -336,7 +336,9 @@ __global__ void __launch_bounds__(256, 4) k_ragged_append_r1(RaggedAppend a, int
 
 // ---------------------------------------------------------------- ratio 2: a block per token
 // The compression (704 channels, fp64 softmax over four rows) is csa2_kv_append's,
-// and its arithmetic is what bounds it; every second token brings an entry.  Groups
+// and its arithmetic is what bounds it: 32,768 tokens take 2.7 ms (csa2_kv_append
+// 2.8), 370 MB at 2 % of the HBM rate with the fp64 pipe at 89 %.  Every second token
+// brings an entry; the others' blocks cost next to nothing beside it.  Groups
 // of NaN alone become zeros, as csa2_kv_append's encoders for ratio 2 make them.
 // Blocks 0 .. total-1: one token each (its window row and, when it completes a
 // pair, the entry).  single: max_new is 1 and there are no window rows to leave,
@@ -479,8 +481,8 @@ struct ReadArgs {
 // where it lies (a chain of dependent loads) for the whole block (by warps, without
 // the barrier, took as long); then a warp requests all its rows before it converts
 // the first.  229,000 FP4 rows to bf16 take 67 us: 412 MB, 6.1 TB/s, 90 % of the
-// measured copy rate; 30,011 V4 rows to fp32 18 us (87 %); 16,384 FP4 rows at
-// listed positions 11 us (round trips).
+// measured copy rate; 30,011 V4 rows to fp32 18 to 20 us (part of what they write is
+// still in L2 then); 16,384 FP4 rows at listed positions 11 us (round trips).
 struct RowPlace {
   int64_t pe, pt;  // physical entry and indexer tile; pe -1: zeros, -2: no row
   int32_t m;       // place in the indexer tile

@@ -434,7 +434,8 @@ csa2_status csa2_kv_append_ragged(const csa2_cache *cache, const void *kv, int64
  *   out_main: rows of 576 (512 latent, then the 64 rotated RoPE dims), or NULL;
  *   out_key: rows of 128 (the indexer key), or NULL; out_dtype, row strides in
  *   elements (>= 576 / 128, multiples of 8).  Every value is exact in fp32, and in
- *   bf16 too for FP4 records and keys, MXFP8 latents and bf16 RoPE dims.
+ *   bf16 too for FP4 records and keys, bf16 RoPE dims, and MXFP8 latents down to
+ *   bf16's step of 2^-133, to which smaller ones are rounded.
  *   Empty rows are zeros.  Rows of no sequence, or of a skipped one, are left as
  *   they were.
  * Device errors: INDEX (an entry not in the cache, floor(n_tokens/ratio) or more,
@@ -468,8 +469,17 @@ csa2_status csa2_window_read(const csa2_cache *cache, void *out, int32_t out_dty
  *   A row that sees nothing (bad pages, no sink) is zeros with lse -inf.  Values
  *   of tokens that a row does not see never reach it: a window token with an
  *   infinite or NaN latent (a bf16 window holds them as they are) makes the rows
- *   that see it NaN, and only those.  Records hold no NaN codes: the appends
- *   write none.
+ *   that see it NaN, and only those, as does a V4 entry with a NaN among its RoPE
+ *   dims.  Other records hold no NaN: the appends write none.
+ *   Precision: sums, softmax statistics and out before its rounding in fp32, FP4
+ *   records exact.  An element of out is off by at most about
+ *   sum_j p_j (2^-11 |c_j| + 2^-25 s_j) + 2^-29 W sum_j |c_j| / s_j with
+ *   W = max_j p_j s_j: the weights, and the values of V4 entries and of the window,
+ *   are fp16 in the products.  s_j is 1 for FP4 records and for keys whose largest
+ *   magnitude (RoPE dims included) lies in 2^0 .. 2^16, else 2^(e-8) for one of
+ *   2^e .. 2^(e+1), 2^-24 at least.  So a value below 2^-25 of its key's largest
+ *   magnitude may be lost, and so may keys with a largest magnitude below about
+ *   2^-20 beside much larger ones, or below 2^-49.
  * n_heads: a multiple of 16, 16..128.  The work is split over the GPU by the
  * batch's total work, so a row's last bits may change with the batch (use
  * csa2_sparse_attn_decode where batch invariance is needed); equal calls give

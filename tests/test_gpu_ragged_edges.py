@@ -228,13 +228,13 @@ def test_from_planes_of_any_shape():
         assert torch.equal(d.swa_codes, c.swa_codes) and torch.equal(d.swa_scales, c.swa_scales)
 
 
-def _within_values(out, lse, ref, q, scale):
-    """ru.attn_within() for keys whose values the operands hold to 2^-25 (fp16's step is 2^-24; keys of a
-    largest magnitude of 1 to 2^16, which go in as they are), and 2^-34 more for a block of values whose codes
-    are rounded to E4M3's step of 2^-9 at 2^-24 first: D.  The outputs, weighted means of the values, move by D
+def _within_values(out, lse, ref, q, scale, s=1.0):
+    """ru.attn_within() for keys whose values the operands hold to 2^-25 s (fp16's step is 2^-24; s is 1 for keys
+    of a largest magnitude of 1 to 2^16, which go in as they are), and 2^-34 s more for a block of values whose
+    codes are rounded to E4M3's step of 2^-9 at 2^-24 first: D.  The outputs, weighted means of the values, move by D
     at most, a logit by scale sum |q| D."""
     o, l, mag, dot, small = ref
-    D = 2.0 ** -25 + 2.0 ** -34
+    D = (2.0 ** -25 + 2.0 ** -34) * s
     ez = 40 * 2.0 ** -23 * dot + 2.0 ** -22 * (1 + l.abs()) + scale * q.double().abs().sum(-1) * D
     assert ((lse.double() - l).abs() <= ez).all()
     tol = (2.0 ** -11 + 2.0 ** -16 + 2 * ez[..., None]) * mag + 2.0 ** -29 * small + 2.0 ** -30 + D
@@ -263,3 +263,62 @@ def test_attn_small_blocks_beside_large_ones(fmt, swa, prior, new):
     out, lse, bits = _attn(c, q, cu, win)
     assert bits == 0 and int(err) == 0
     _within_values(out, lse, ru.chunk_attn(c, q, cu, scale, win), q, scale)
+
+
+def test_attn_v4_entry_with_nan_rope():
+    """A V4 entry's RoPE dims are bf16 and may be NaN: the rows that see the entry are NaN, the others know
+    nothing of it."""
+    n, at, H = 300, 100, 16
+    c, rope = _cache(1, 320, swa=csa2.SWA_MXFP8, fmt=csa2.ENTRY_FP8), csa2.rope_table(THETA, 320)
+    g = torch.Generator(device=DEV).manual_seed(6)
+    kv, ik = torch.randn(n, 576, generator=g, device=DEV), torch.randn(n, 128, generator=g, device=DEV)
+    kv[at, 530] = math.nan
+    cu, win = _cu([n]), csa2.chunk_window(c, n)
+    csa2.kv_append_ragged(c, cu, rope, kv=kv, idx_key=ik, win=win)
+    assert c.rope_codes[0, at].view(torch.bfloat16).isnan().any()
+    q = _q(n, H)
+    out, lse, e = _attn(c, q, cu, win)
+    assert e == 0 and out[at + 1:].isnan().all() and lse[at + 1:].isnan().all()
+    c.rope_codes[0, at] = 0  # (the plain form would multiply it by zero)
+    ref = ru.chunk_attn(c, q, cu, 1 / math.sqrt(576), win)
+    ru.attn_within(out[:at + 1], lse[:at + 1], [t[:at + 1] for t in ref])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_read_the_least_values(dtype):
+    """MXFP8 blocks down to the least scale: exact in fp32; in bf16 rounded to its step of 2^-133."""
+    c, rope = _cache(1, 64, fmt=csa2.ENTRY_FP8), csa2.rope_table(THETA, 64)
+    g = torch.Generator(device=DEV).manual_seed(6)
+    kv = torch.randn(20, 576, generator=g, device=DEV)
+    for i in range(20):
+        kv[i, :512] *= 2.0 ** (-133 + i)
+    kv[:, 512:] = 0.0
+    csa2.kv_append_ragged(c, _cu([20]), rope, kv=kv, idx_key=torch.zeros(20, 128, device=DEV))
+    main, win = torch.empty(20, 576, dtype=dtype, device=DEV), torch.empty(1, 128, 576, dtype=dtype, device=DEV)
+    csa2.kv_read(c, _cu([20]), out_main=main, start=torch.zeros(1, dtype=torch.int64, device=DEV))
+    csa2.window_read(c, win)
+    want = ru.main_values(c, torch.arange(20, device=DEV))
+    assert (want[:, :512] != 0).any() and torch.equal(want, want.float().double())
+    if dtype == torch.bfloat16:
+        want = (want * 2.0 ** 133).round() * 2.0 ** -133
+    for got in (main, win[0, -20:]):
+        assert torch.equal(got[:, :512].double(), want[:, :512])
+
+
+@pytest.mark.parametrize("fmt,swa", [(csa2.ENTRY_FP8, csa2.SWA_BF16), (csa2.ENTRY_FP8, csa2.SWA_MXFP8)])
+def test_attn_latents_beside_large_rope_dims(fmt, swa):
+    """RoPE dims of about 2^18 beside latents of about 1: s is 2^-8 of the power of two below the key's largest."""
+    n, H = 200, 16
+    c, rope = _cache(1, 320, swa=swa, fmt=fmt), csa2.rope_table(THETA, 320)
+    g = torch.Generator(device=DEV).manual_seed(8)
+    kv, ik = torch.randn(n, 576, generator=g, device=DEV), torch.zeros(n, 128, device=DEV)
+    kv[:, 512:] *= 2.0 ** 18
+    cu, win, scale = _cu([n]), csa2.chunk_window(c, n), 1 / math.sqrt(576)
+    csa2.kv_append_ragged(c, cu, rope, kv=kv, idx_key=ik, win=win)
+    q = _q(n, H)
+    q[..., 512:] *= 2.0 ** -18
+    out, lse, e = _attn(c, q, cu, win)
+    assert e == 0
+    top = max(float(t.abs().max()) for t in (ru.main_values(c, torch.arange(n, device=DEV)),
+                                             ru.window_values(win.codes[128:], win.scales[128:], swa)))
+    _within_values(out, lse, ru.chunk_attn(c, q, cu, scale, win), q, scale, 2.0 ** (math.frexp(top)[1] - 1 - 8))
