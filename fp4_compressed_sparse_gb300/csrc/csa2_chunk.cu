@@ -21,7 +21,7 @@
 // window tokens go in divided by a power of two s per key, 1 where the key's largest
 // magnitude is 2^0 to 2^16 (sigma_of): fp16's step there makes them off by 2^-25 s.  The
 // weights p, times s, are rounded to fp16 as well, as the MMA takes both operands in
-// one type: by 2^-11 of themselves (a bf16 output's rounding is 2^-9), and below
+// one type: by 2^-11 of themselves (a bf16 output's rounding is 2^-8), and below
 // 2^-14 on a scale on which a row's largest is 2^4 at least by 2^-29 of that.
 //
 // Tiles.  O^T of 64 rows is 256 columns of tensor memory beside two S; 128 rows
