@@ -22,6 +22,7 @@ SWA_BF16, SWA_MXFP8 = 0, 1
 ENTRY_FP4, ENTRY_FP8 = 0, 1
 IN_F32, IN_BF16 = 0, 1
 OUT_F32, OUT_BF16 = 0, 1
+FP4_NV, FP4_MX = 0, 1
 D_LATENT, D_ROPE, D_QK, D_INDEX, D_CMP, WINDOW = 512, 64, 576, 128, 704, 128
 
 EXPORTS = [
@@ -31,6 +32,8 @@ EXPORTS = [
     "csa2_prefill_workspace_size", "csa2_prefill_chunk", "csa2_mask_to_pool", "csa2_mxf4_peak_launch",
     "csa2_chunk_window_bytes", "csa2_kv_append_ragged", "csa2_kv_read", "csa2_window_read",
     "csa2_chunk_attn_workspace_size", "csa2_chunk_attn",
+    "csa2_pages_resize", "csa2_slot_map",
+    "csa2_fp4_plane_bytes", "csa2_fp4_quant", "csa2_fp4_read", "csa2_fp4_product",
     "csa2_bounded_wait_check", "csa2_set_phase_events",
     "csa2_phase_events_recorded", "csa2_status_string", "csa2_last_error_detail", "csa2_version",
 ]
@@ -54,6 +57,15 @@ class CacheStruct(ctypes.Structure):
         ("block_table", ctypes.c_void_p), ("page_entries", ctypes.c_int32), ("max_pages", ctypes.c_int32),
         ("n_pages", ctypes.c_int32), ("entry_format", ctypes.c_int32),
     ]
+
+
+class PoolStruct(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("free", "n_free", "held")]
+
+
+class Fp4Struct(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("format", ctypes.c_int32),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("row_scales", ctypes.c_void_p)]
 
 
 class CompressIn(ctypes.Structure):
@@ -103,6 +115,12 @@ def load() -> ctypes.CDLL:
         "csa2_window_read": (i32, [vp, vp, i32, vp]),
         "csa2_chunk_attn_workspace_size": (sz, [i32, i32, i32]),
         "csa2_chunk_attn": (i32, [vp, vp, i32, vp, i32, i32, vp, vp, vp, f32, vp, i32, vp, vp, sz, vp, vp]),
+        "csa2_pages_resize": (i32, [vp, vp, vp, vp, i32, i32, vp, vp, vp]),
+        "csa2_slot_map": (i32, [vp, vp, i32, i32, vp, vp, vp, vp]),
+        "csa2_fp4_plane_bytes": (sz, [i32, i32, i32, i32]),
+        "csa2_fp4_quant": (i32, [vp, vp, i64, i32, vp, vp]),
+        "csa2_fp4_read": (i32, [vp, vp, i64, i32, vp]),
+        "csa2_fp4_product": (i32, [vp, vp, vp, i64, i32, vp, vp]),
         "csa2_mxf4_peak_launch": (i32, [i32, i32, vp, vp, vp]),
         "csa2_bounded_wait_check": (i32, [i32, i32, vp, vp]),
         "csa2_set_phase_events": (i32, [vp, i32]),
@@ -476,13 +494,18 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 
 def _call(fn, cache, dev, stream, *args):
     """fn(cache, *args, stream) with the cache's device as the current one, on its current stream unless one is given."""
+    _call_on(fn, dev, stream, cache.ref(), *args)
+
+
+def _call_on(fn, dev, stream, *args):
+    """fn(*args, stream) with device dev as the current one, on its current stream unless one is given."""
     f = getattr(_lib or load(), fn)
     s = stream.cuda_stream if stream is not None else _raw_stream(dev)
     if dev == _current_device():
-        status = f(cache.ref(), *args, s)
+        status = f(*args, s)
     else:
         with torch.cuda.device(dev):
-            status = f(cache.ref(), *args, s)
+            status = f(*args, s)
     if status != OK:
         _check(fn, status)
 
@@ -611,6 +634,135 @@ def chunk_attn(cache: Cache, q, cu_q, out, lse, ws, sm_scale, max_new=None, win=
         return
     _call("csa2_chunk_attn", cache, dev, stream, _adr(q), H, _adr(cu_q), total, total if max_new is None else max_new, wc, wsc,
           _adr(sink), sm_scale, _adr(out), _out_dtype(out), _adr(lse), _adr(ws), ws.numel(), ew)
+
+
+# --------------------------------------------------------------------------- pages
+class PagePool:
+    """The free pages of a paged cache and what each sequence holds (csa2_page_pool): int32 device tensors
+    free [n_pages] (a stack), n_free [1] and held [batch].  By default every page is free (page 0 is taken
+    first), no sequence holds any and the cache's block table is cleared."""
+
+    def __init__(self, cache, free=None, n_free=None, held=None):
+        dev = _device(cache)
+        if cache.block_table is None:
+            raise ValueError("a dense cache has no pages")
+        given = [t is not None for t in (free, n_free, held)]
+        if not any(given):
+            where = cache.n_tokens.device
+            free = torch.arange(cache.n_pages - 1, -1, -1, dtype=torch.int32, device=where)
+            n_free = torch.full((1,), cache.n_pages, dtype=torch.int32, device=where)
+            held = torch.zeros(cache.batch, dtype=torch.int32, device=where)
+            cache.block_table.fill_(-1)
+        elif not all(given):
+            raise ValueError("free, n_free and held are given together, or none of them")
+        _want("free", free, torch.int32, (cache.n_pages,), dev)
+        _want("n_free", n_free, torch.int32, (1,), dev)
+        _want("held", held, torch.int32, (cache.batch,), dev)
+        self.free, self.n_free, self.held = free, n_free, held
+        self.struct = PoolStruct(free.data_ptr(), n_free.data_ptr(), held.data_ptr())
+
+
+def pages_resize(cache: Cache, pool: PagePool, target=None, cu_new=None, total=None, max_new=None, granted=None, err=None,
+                 stream=None):
+    """csa2_pages_resize: every sequence's pages for target[b] tokens (int64 [B]), or for its n_tokens plus
+    the rows cu_new (int32 [B+1]) gives it.  total, max_new: bounds on all rows and on one sequence's
+    (default: 2^24, no bound).  granted: int32 [B], 1 where a sequence holds what it needs."""
+    dev = _device(cache)
+    if cache.block_table is None:
+        raise ValueError("a dense cache has no pages")
+    _want("pool.free", pool.free, torch.int32, (cache.n_pages,), dev)
+    _want("pool.held", pool.held, torch.int32, (cache.batch,), dev)
+    if target is not None:
+        _want("target", target, torch.int64, (cache.batch,), dev)
+    if cu_new is not None:
+        _want("cu_new", cu_new, torch.int32, (cache.batch + 1,), dev)
+    if granted is not None:
+        _want("granted", granted, torch.int32, (cache.batch,), dev)
+    total = 1 << 24 if total is None else total
+    _call("csa2_pages_resize", cache, dev, stream, ctypes.byref(pool.struct), _adr(target), _adr(cu_new), total,
+          total if max_new is None else max_new, _adr(granted), _err_word(err, dev))
+
+
+def slot_map(cache: Cache, cu_new, slots=None, pos=None, max_new=None, err=None, stream=None):
+    """csa2_slot_map: slots and / or pos, int64 [total]: where each new token's entry will lie, and its position."""
+    dev = _device(cache)
+    _want("cu_new", cu_new, torch.int32, (cache.batch + 1,), dev)
+    first = slots if slots is not None else pos
+    if first is None:
+        raise ValueError("slots or pos is needed")
+    total = first.numel()
+    for name, t in (("slots", slots), ("pos", pos)):
+        if t is not None:
+            _want(name, t, torch.int64, (total,), dev)
+    ew = _err_word(err, dev)
+    if total == 0:
+        return
+    _call("csa2_slot_map", cache, dev, stream, _adr(cu_new), total, total if max_new is None else max_new, _adr(slots),
+          _adr(pos), ew)
+
+
+# --------------------------------------------------------------------------- 4-bit matrices
+class Fp4Matrix:
+    """Device planes of a 4-bit block-scaled matrix (csa2_fp4_matrix): fmt FP4_NV (E2M1, an E4M3 scale per
+    16 columns, a power of two per row) or FP4_MX (E2M1, an E8M0 scale per 32).  Filled by fp4_quant()."""
+
+    def __init__(self, rows, cols, fmt=FP4_NV, device="cuda"):
+        L = load()
+        if rows < 0 or rows > 1 << 24 or cols < 1 or cols > 1 << 17 or fmt not in (FP4_NV, FP4_MX):
+            raise ValueError(f"{rows} x {cols}, format {fmt}: rows 0..2^24, cols 1..2^17, FP4_NV or FP4_MX are needed")
+        self.rows, self.cols, self.fmt = rows, cols, fmt
+        nb = [L.csa2_fp4_plane_bytes(rows, cols, fmt, p) for p in range(3)]
+        self.codes = torch.empty(nb[0], dtype=torch.uint8, device=device)
+        self.scales = torch.empty(nb[1], dtype=torch.uint8, device=device)
+        self.row_scales = torch.empty(nb[2] // 4, dtype=torch.float32, device=device)
+        self.struct = Fp4Struct(rows, cols, fmt, self.codes.data_ptr(), self.scales.data_ptr(), self.row_scales.data_ptr())
+
+    def ref(self):
+        return ctypes.byref(self.struct)
+
+
+def _fp4_device(m):
+    dev = m.codes.get_device()
+    if dev < 0:
+        raise ValueError(f"the matrix is on {m.codes.device}, a CUDA device is needed")
+    return dev
+
+
+def fp4_quant(m: Fp4Matrix, x, err=None, stream=None):
+    """csa2_fp4_quant: x [rows, cols] (fp32 or bf16, rows may be strided) into m."""
+    dev = _fp4_device(m)
+    stride = _want_rows("x", x, _FLOATS, m.cols, dev, m.rows)
+    ew = _err_word(err, dev)
+    if m.rows == 0:
+        return
+    if m.rows == 1:  # (a single row: any stride that the rows could have)
+        stride = -(-m.cols // 8) * 8
+    _call_on("csa2_fp4_quant", dev, stream, m.ref(), _adr(x), stride, IN_BF16 if x.dtype is torch.bfloat16 else IN_F32, ew)
+
+
+def fp4_read(m: Fp4Matrix, out, stream=None):
+    """csa2_fp4_read: the values m stands for into out [rows, cols] (fp32 or bf16, rows may be strided)."""
+    dev = _fp4_device(m)
+    stride = _want_rows("out", out, _FLOATS, m.cols, dev, m.rows)
+    if m.rows == 0:
+        return
+    if m.rows == 1:
+        stride = -(-m.cols // 8) * 8
+    _call_on("csa2_fp4_read", dev, stream, m.ref(), _adr(out), stride, _out_dtype(out))
+
+
+def fp4_product(x: Fp4Matrix, w: Fp4Matrix, out, err=None, stream=None):
+    """csa2_fp4_product: out [x.rows, w.rows] = x w^T (fp32 or bf16, rows may be strided)."""
+    dev = _fp4_device(x)
+    if _fp4_device(w) != dev:
+        raise ValueError(f"w is on {w.codes.device}, x on cuda:{dev}")
+    stride = _want_rows("out", out, _FLOATS, w.rows, dev, x.rows)
+    ew = _err_word(err, dev)
+    if x.rows == 0 or w.rows == 0:
+        return
+    if x.rows == 1:
+        stride = -(-w.rows // 8) * 8
+    _call_on("csa2_fp4_product", dev, stream, x.ref(), w.ref(), _adr(out), stride, _out_dtype(out), ew)
 
 
 # --------------------------------------------------------------------------- measurement helpers

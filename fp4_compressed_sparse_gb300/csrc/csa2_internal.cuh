@@ -14,6 +14,8 @@ csa2_status fail(csa2_status st, const char *fmt, ...) __attribute__((format(pri
 csa2_status cuda_status(cudaError_t e, const char *what);
 // host validation of a cache descriptor
 csa2_status check_cache(const csa2_cache *c);
+// host validation of a 4-bit matrix (csa2_fp4.cu); name: its argument's
+csa2_status check_fp4(const csa2_fp4_matrix *m, const char *name);
 // SM count of the current device (queried once per device)
 int device_sm_count();
 // Raises fn's dynamic shared-memory limit to at least `bytes` on the current

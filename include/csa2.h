@@ -496,6 +496,111 @@ csa2_status csa2_chunk_attn(const csa2_cache *cache, const uint16_t *q, int32_t 
                             size_t ws_bytes, int32_t *err_word, csa2_stream_t stream);
 
 /*
+ * csa2_pages_resize: the pages of a paged cache for the lengths its sequences are
+ * to have ([P5] §3.5.1), without the host.  Sequence b is to hold
+ *   need_b = ceil(floor(n_b / ratio) / page_entries) pages,
+ *   n_b = target[b] (int64 [batch]), or, when target is NULL, n_tokens[b] plus the
+ *   new tokens cu_new gives it (cu_new NULL: none; cu_new, total, max_new as in the
+ *   ragged calls, before the append).
+ * pool: held int32 [batch], the pages each sequence holds (entries 0..held-1 of its
+ *   block_table row); free int32 [n_pages], a stack of free page ids, n_free int32
+ *   [1] of them.  All device memory that the caller owns, as is block_table, which
+ *   this call writes.
+ * Pages beyond need go back to the stack and their entries become -1 (a sequence
+ *   that ended: length 0; drafted tokens that were refused: the shorter length).
+ *   With R of them, the j-th in sequence and page order goes to
+ *   free[n_free + R - 1 - j].  Then the sequences that need more take pages from the
+ *   top, in order: the k-th page is the one at free[n_free + R - 1 - k].  A sequence
+ *   gets all it needs or nothing: from the first whose need does not fit on, no
+ *   sequence that needs more gets any.  Pages are handed out, not cleared.
+ * granted: int32 [batch] or NULL, 1 where a sequence holds what it needs, else 0.
+ * Equal calls give equal tables; taking pages and giving them back restores both.
+ * Device errors, the sequence left as it was: CAPACITY (need_b > max_pages), INDEX
+ *   (cu_new, max_new, a negative length, held outside 0..max_pages).  INDEX with
+ *   nothing done: n_free outside 0..n_pages, or more pages than the pool has.  INDEX
+ *   also for a returned id outside the pool.  A pool that runs out is no error: see
+ *   granted.
+ */
+typedef struct csa2_page_pool {
+  int32_t *free;   /* [n_pages] */
+  int32_t *n_free; /* [1] */
+  int32_t *held;   /* [batch] */
+} csa2_page_pool;
+csa2_status csa2_pages_resize(const csa2_cache *cache, const csa2_page_pool *pool, const int64_t *target,
+                              const int32_t *cu_new, int32_t total, int32_t max_new, int32_t *granted, int32_t *err_word,
+                              csa2_stream_t stream);
+
+/*
+ * csa2_slot_map: position and place of every new token of a ragged batch, before
+ * they are appended (cu_new, total, max_new as there).
+ *   pos: int64 [total] or NULL, n_tokens[b] + i for row cu_new[b] + i, as
+ *        csa2_query_latent takes it; slots: int64 [total] or NULL, the physical
+ *        entry (page * page_entries + offset, or b * capacity + entry in a dense
+ *        cache) of the token's entry, for planes of the caller's own beside the
+ *        cache's; -1 when the entry is not complete after this call (ratio 2).
+ * Rows of no sequence, or of a skipped one, get -1 in both.
+ * Device errors: INDEX (cu_new, max_new; a page id outside the pool: slot -1; a
+ * negative n_tokens), CAPACITY (an entry behind the capacity: slot -1).
+ */
+csa2_status csa2_slot_map(const csa2_cache *cache, const int32_t *cu_new, int32_t total, int32_t max_new, int64_t *slots,
+                          int64_t *pos, int32_t *err_word, csa2_stream_t stream);
+
+/*
+ * 4-bit block-scaled matrices: the formats the cache is held in, for the layer's
+ * own projections (their weights, and the activations they multiply).
+ *   CSA2_FP4_NV: E2M1 codes, one E4M3 scale per 16 columns (as the main entry) and
+ *     one power of two r per row.  r is the least one, 2^-62 at least, with
+ *     largest magnitude of the row / r <= 2688 = 448 x 6; then per group
+ *     s = E4M3(amax / (6 r)), codes E2M1(x / (r s)), zeros where s is 0.
+ *   CSA2_FP4_MX: E2M1 codes, one E8M0 scale per 32 columns (as the indexer key);
+ *     r = 1.
+ *   Value: code x scale x r.  A row that holds an infinity or NaN (NV: also one whose
+ *   largest magnitude is above 2688 x 2^62) gets r = NaN and raises the NAN bit: what
+ *   is read or computed from it is NaN.
+ * Planes (csa2_fp4_plane_bytes, plane 0..2), in tiles of 128 rows x 128 columns, row
+ *   tile by row tile, the operand layout of the block-scaled tensor-core MMA:
+ *   codes       tile * 8192 + j * 2048 + m * 16: the 16 bytes of 32-column piece j of
+ *               row m of the tile
+ *   scales      NV: tile * 1024 + (g / 4) * 512 + 16 (m % 32) + 4 (m / 32) + g % 4,
+ *               group g of 8; MX: tile * 512 + 16 (m % 32) + 4 (m / 32) + j
+ *   row_scales  float r per row
+ * Rows behind `rows` in the last tile are neither written nor looked at.
+ * rows 0..2^24, cols 1..2^17.
+ */
+#define CSA2_FP4_NV 0
+#define CSA2_FP4_MX 1
+typedef struct csa2_fp4_matrix {
+  int32_t rows, cols;
+  int32_t format;
+  uint8_t *codes, *scales;
+  float *row_scales;
+} csa2_fp4_matrix;
+size_t csa2_fp4_plane_bytes(int32_t rows, int32_t cols, int32_t format, int32_t plane);
+
+/*
+ * csa2_fp4_quant: the rows x, fp32 or bf16 (in_dtype, CSA2_IN_*), row t at
+ * x + t * x_stride elements (x_stride >= cols, a multiple of 8), into the matrix m.
+ * csa2_fp4_read: the values m stands for, out_dtype (CSA2_OUT_*), rows out_stride
+ * elements apart (>= cols, a multiple of 8); exact in fp32, and in bf16 too.
+ * Device errors (quant): NAN.
+ */
+csa2_status csa2_fp4_quant(const csa2_fp4_matrix *m, const void *x, int64_t x_stride, int32_t in_dtype, int32_t *err_word,
+                           csa2_stream_t stream);
+csa2_status csa2_fp4_read(const csa2_fp4_matrix *m, void *out, int64_t out_stride, int32_t out_dtype, csa2_stream_t stream);
+
+/*
+ * csa2_fp4_product: out[m][n] = sum_k x[m][k] w[n][k], x and w of one format and
+ * as many columns, out_dtype [x->rows] rows of w->rows values out_stride elements
+ * apart (>= w->rows, a multiple of 8).  Products and block scales are exact, sums in
+ * fp32 (in an order that the sizes decide; equal calls give equal bits), the rows'
+ * powers of two applied to the sum, then rounded to out_dtype.  A row's last bits may
+ * change with the number of rows.  out must not overlap x or w.
+ * Device errors: TIMEOUT.
+ */
+csa2_status csa2_fp4_product(const csa2_fp4_matrix *x, const csa2_fp4_matrix *w, void *out, int64_t out_stride,
+                             int32_t out_dtype, int32_t *err_word, csa2_stream_t stream);
+
+/*
  * csa2_mxf4_peak_launch: measurement helper (not a step of the method).
  * Launches n_ctas CTAs that each issue `iters` back-to-back block-scaled FP4
  * tensor-core MMAs (tcgen05 kind::mxf4, M 128 x N 128 x K 64, the index score's

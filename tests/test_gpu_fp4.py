@@ -1,0 +1,231 @@
+"""4-bit block-scaled matrices on the GPU: csa2_fp4_quant and csa2_fp4_read against
+the definition in 64 bits (equal), csa2_fp4_product against a 64-bit product of the
+stored values."""
+import math
+
+import pytest
+import torch
+
+import fp4_util as fu
+from fp4_compressed_sparse_gb300 import csa2
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+FMTS = [csa2.FP4_NV, csa2.FP4_MX]
+TYPES = [torch.bfloat16, torch.float32]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from fp4_compressed_sparse_gb300 import build_lib
+    build_lib.build()
+    csa2.load()
+
+
+def _err():
+    return torch.zeros(1, dtype=torch.int32, device=DEV)
+
+
+def _rows(rows, cols, dtype, seed=0):
+    """N(0,1) rows of several magnitudes, groups of zeros, a row of zeros, rows of grid midpoints."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g, device=DEV)
+    x = x * torch.exp2(torch.randint(-30, 30, (rows, 1), generator=g, device=DEV).float())
+    x[1::5] *= torch.exp2(torch.randint(-8, 8, (x[1::5].shape[0], cols), generator=g, device=DEV).float())
+    x[2::7, :40] = 0.0
+    x[3::11] = 0.0
+    # small multiples of 1/4 with the group's largest value among 6, 12, .. : quotients at the midpoints
+    mid = torch.randint(-24, 25, (rows, cols), generator=g, device=DEV).float() / 4
+    mid[:, ::16] = 6.0 * torch.randint(1, 8, mid[:, ::16].shape, generator=g, device=DEV).float()
+    x[4::6] = mid[4::6]
+    return x.to(dtype)
+
+
+def _packed(x, fmt, err=None):
+    m = csa2.Fp4Matrix(*x.shape, fmt)
+    csa2.fp4_quant(m, x, err=err)
+    return m
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 128), (3, 136), (17, 31), (130, 520), (129, 4104), (2000, 264), (1300, 2056)])
+def test_quant_is_the_definition(fmt, dtype, rows, cols):
+    """Codes and scales as values, equal; read back in both types; strided rows; columns behind the
+    last one of the tile are zeros."""
+    wide = torch.full((rows, -(-cols // 8) * 8 + 16), float("nan"), dtype=dtype, device=DEV)
+    wide[:, :cols] = _rows(rows, cols, dtype, rows + cols)
+    x, err = wide[:, :cols], _err()
+    m = csa2.Fp4Matrix(rows, cols, fmt)
+    for t in (m.codes, m.scales):
+        t.fill_(0x5A)
+    csa2.fp4_quant(m, x, err=err)
+    want = fu.quantised(x, fmt)
+    assert int(err) == 0
+    got = fu.values(m)
+    assert torch.equal(got, want)
+    full = fu.values(type("M", (), dict(vars(m), cols=-(-cols // 128) * 128)))
+    assert not full[:, cols:].any()
+    for out_t in TYPES:
+        out = torch.full((rows, -(-cols // 8) * 8 + 8), 7.0, dtype=out_t, device=DEV)
+        csa2.fp4_read(m, out[:, :cols])
+        assert torch.equal(out[:, :cols].double(), want) and (out[:, cols:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_nv_codes_at_every_midpoint(dtype):
+    """x at T s, and one step of its type beside it, for every scale s and midpoint T of the grid."""
+    s = torch.arange(8, 127, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    t = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    at = (s[:, None] * t).to(dtype)
+    up, down = (torch.nextafter(at, torch.full_like(at, v)) for v in (math.inf, 0.0))
+    x = torch.zeros(s.numel() + 1, 32, dtype=dtype)
+    x[:-1, :16] = torch.cat([at, -up, torch.zeros_like(at[:, :1]), (6 * s)[:, None].to(dtype)], -1)
+    x[:-1, 16:] = torch.cat([-at, down, torch.zeros_like(at[:, :1]), (6 * s)[:, None].to(dtype)], -1)
+    # one row of 2688 beside each fixes the row's power of two at 1
+    y = torch.zeros(s.numel() + 1, 48, dtype=dtype)
+    y[:, :32], y[:, 40] = x, 2688.0
+    y = y.to(DEV)
+    m = _packed(y, csa2.FP4_NV)
+    assert (m.row_scales[:y.shape[0]] == 1).all()
+    assert torch.equal(fu.values(m), fu.quantised(y, csa2.FP4_NV))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_quant_extreme_rows(fmt):
+    """The largest and least magnitudes, and rows of infinities and NaN: NaN wholly, the others untouched."""
+    x = torch.randn(1500, 96, device=DEV)
+    x[0] *= 2.0 ** 60
+    x[1] *= 2.0 ** -100
+    x[2] *= 2.0 ** -140
+    x[3, 5], x[4, 90], x[5, 33] = math.inf, -math.inf, math.nan
+    x[6] = 2688.0 * 2.0 ** 62
+    x[7] = torch.nextafter(torch.tensor(2688.0 * 2.0 ** 62), torch.tensor(math.inf)).item()
+    x[8] = torch.finfo(torch.float32).max
+    x[9] = 2.0 ** -149
+    for rows in (12, 1500):
+        err, y = _err(), x[:rows]
+        m = _packed(y, fmt, err)
+        want = fu.quantised(y, fmt)
+        got = fu.values(m)
+        assert torch.equal(torch.isnan(got), torch.isnan(want)) and torch.equal(got.nan_to_num(), want.nan_to_num())
+        nan = {3, 4, 5} | ({7, 8} if fmt == csa2.FP4_NV else set())
+        assert set(torch.isnan(got).all(-1).nonzero().flatten().tolist()) == nan and int(err) == csa2.DEVERR_NAN
+        out = torch.empty(rows, 96, device=DEV)
+        csa2.fp4_read(m, out)
+        assert torch.equal(torch.isnan(out), torch.isnan(want)) and torch.equal(out.double().nan_to_num(), want.nan_to_num())
+
+
+def test_rows_behind_the_last_are_not_written():
+    for fmt in FMTS:
+        m = csa2.Fp4Matrix(5, 256, fmt)
+        for t in (m.codes, m.scales):
+            t.fill_(0xA5)
+        m.row_scales.fill_(-3.0)
+        csa2.fp4_quant(m, torch.ones(5, 256, device=DEV))
+        codes = m.codes.view(2, 4, 128, 16)
+        assert (codes[:, :, 5:] == 0xA5).all() and not (codes[:, :, :5] == 0xA5).any()
+        sc = m.scales.view(-1, 32, 4, 4)
+        assert (sc[:, 5:] == 0xA5).all() and (sc[:, :5, 1:] == 0xA5).all() and (m.row_scales[5:] == -3).all()
+
+
+def _within(out, x, w):
+    """out against the 64-bit product of the stored values.
+
+    Products with their block scales are exact in the MMA, which adds 64 of them to the
+    sum per step: each step is off by at most one unit of fp32, 2^-23 of the magnitudes
+    added up so far, and so are the joins of up to 8 partial sums.  bf16 adds half a step."""
+    xv, wv = fu.values(x), fu.values(w)
+    want, mag = xv @ wv.t(), xv.abs() @ wv.abs().t()
+    tol = (-(-x.cols // 64) + 10) * 2.0 ** -23 * mag
+    if out.dtype == torch.bfloat16:
+        tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()
+    err = (out.double() - want).abs()
+    assert (err <= tol).all(), float((err / tol).nan_to_num().max())
+
+
+SHAPES = [(1, 8, 128), (1, 700, 4096), (5, 129, 40), (16, 256, 1000), (17, 130, 384), (33, 1000, 2048), (64, 96, 128),
+          (65, 704, 640), (128, 128, 8192), (129, 1, 256), (300, 2056, 136), (1, 1, 1), (501, 704, 4104), (2, 12288, 512),
+          (1000, 4100, 264), (2049, 2500, 520)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_product(fmt, dtype, M, N, K):
+    g = torch.Generator(device=DEV).manual_seed(M + N)
+    x, w = (torch.randn(r, K, generator=g, device=DEV) * torch.exp2(torch.randint(-9, 9, (r, 1), generator=g, device=DEV).float())
+            for r in (M, N))
+    pad = -(-K // 8) * 8
+    xs, ws = (torch.zeros(t.shape[0], pad, device=DEV) for t in (x, w))
+    xs[:, :K], ws[:, :K] = x, w
+    mx, mw, err = _packed(xs[:, :K], fmt), _packed(ws[:, :K], fmt), _err()
+    out = torch.full((M + 1, -(-N // 8) * 8 + 8), 3.0, dtype=dtype, device=DEV)
+    csa2.fp4_product(mx, mw, out[:M, :N], err=err)
+    assert int(err) == 0
+    _within(out[:M, :N], mx, mw)
+    assert (out[M] == 3).all() and (out[:, N:] == 3).all()
+    again = torch.empty_like(out)
+    csa2.fp4_product(mx, mw, again[:M, :N], err=err)
+    assert torch.equal(out[:M, :N], again[:M, :N])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N", [(3, 200), (100, 50), (400, 300), (2600, 3000)])
+def test_product_of_small_integers_is_exact(fmt, M, N):
+    """Values of the grid under scales that are powers of two: every sum fits fp32."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    t = torch.tensor(fu.GRID + [-v for v in fu.GRID], device=DEV)
+    x, w = (t[torch.randint(0, 16, (r, 1160), generator=g, device=DEV)] for r in (M, N))
+    x[:, ::16] = 6.0
+    w[:, ::16] = -6.0
+    mx, mw = _packed(x, fmt), _packed(w, fmt)
+    assert torch.equal(fu.values(mx), x.double()) and torch.equal(fu.values(mw), w.double())
+    out = torch.empty(M, -(-N // 8) * 8, device=DEV)[:, :N]  # (row strides are multiples of 8)
+    csa2.fp4_product(mx, mw, out)
+    assert torch.equal(out.double(), x.double() @ w.double().t())
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_product_of_nonfinite_rows(fmt):
+    """A row with an infinity or NaN makes its row (column) NaN and nothing else; zero rows are zeros."""
+    for M, N in ((20, 300), (2600, 3000)):
+        x, w = torch.randn(M, 192, device=DEV), torch.randn(N, 192, device=DEV)
+        x[3, 100], w[200, 0], x[7] = math.nan, math.inf, 0.0
+        out = torch.empty(M, -(-N // 8) * 8, device=DEV)[:, :N]
+        csa2.fp4_product(_packed(x, fmt), _packed(w, fmt), out)
+        nan = torch.isnan(out)
+        assert nan[3].all() and nan[:, 200].all() and int(nan.sum()) == M + N - 1
+        out[3] = 0
+        out[:, 200] = 0
+        assert not out[7].any()
+
+
+@pytest.mark.parametrize("M", [1, 40, 2600])
+def test_streams_graphs_and_two_calls_at_once(M):
+    """A captured quantisation and product replayed on new inputs, another stream than the tensors' own,
+    two products at once over one weight."""
+    N, K = 2600, 520
+    w = _packed(torch.randn(N, K, device=DEV), csa2.FP4_NV)
+    x, y = torch.randn(M, K, device=DEV), torch.randn(M, K, device=DEV)
+    m, n = csa2.Fp4Matrix(M, K), csa2.Fp4Matrix(M, K)
+    o, p = torch.empty(M, N, device=DEV), torch.empty(M, N, device=DEV)
+    want = []
+    for t in (x, y):
+        csa2.fp4_quant(m, t)
+        csa2.fp4_product(m, w, o)
+        want.append(o.clone())
+    torch.cuda.synchronize()
+    side, other, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    buf = x.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        csa2.fp4_quant(m, buf)
+        csa2.fp4_product(m, w, o)
+    for t, v in ((x, want[0]), (y, want[1])):
+        buf.copy_(t)
+        graph.replay()
+        csa2.fp4_quant(n, y, stream=other)
+        csa2.fp4_product(n, w, p, stream=other)
+        torch.cuda.synchronize()
+        assert torch.equal(o, v) and torch.equal(p, want[1])
