@@ -33,6 +33,7 @@ EXPORTS = [
     "csa2_chunk_window_bytes", "csa2_kv_append_ragged", "csa2_kv_read", "csa2_window_read",
     "csa2_chunk_attn_workspace_size", "csa2_chunk_attn",
     "csa2_pages_resize", "csa2_slot_map",
+    "csa2_query_latent", "csa2_value_project",
     "csa2_fp4_plane_bytes", "csa2_fp4_quant", "csa2_fp4_read", "csa2_fp4_product",
     "csa2_bounded_wait_check", "csa2_set_phase_events",
     "csa2_phase_events_recorded", "csa2_status_string", "csa2_last_error_detail", "csa2_version",
@@ -117,6 +118,8 @@ def load() -> ctypes.CDLL:
         "csa2_chunk_attn": (i32, [vp, vp, i32, vp, i32, i32, vp, vp, vp, f32, vp, i32, vp, vp, sz, vp, vp]),
         "csa2_pages_resize": (i32, [vp, vp, vp, vp, i32, i32, vp, vp, vp]),
         "csa2_slot_map": (i32, [vp, vp, i32, i32, vp, vp, vp, vp]),
+        "csa2_query_latent": (i32, [vp, i64, i32, i32, i32, vp, i64, vp, vp, i64, vp, vp, vp]),
+        "csa2_value_project": (i32, [vp, i64, i32, i32, i32, i32, vp, i64, vp, i64, vp, vp]),
         "csa2_fp4_plane_bytes": (sz, [i32, i32, i32, i32]),
         "csa2_fp4_quant": (i32, [vp, vp, i64, i32, vp, vp]),
         "csa2_fp4_read": (i32, [vp, vp, i64, i32, vp]),
@@ -699,6 +702,55 @@ def slot_map(cache: Cache, cu_new, slots=None, pos=None, max_new=None, err=None,
         return
     _call("csa2_slot_map", cache, dev, stream, _adr(cu_new), total, total if max_new is None else max_new, _adr(slots),
           _adr(pos), ew)
+
+
+# --------------------------------------------------------------------------- into and out of the latent space
+def _want_heads(name, w, dev):
+    """Raise ValueError unless w is bf16 [heads, dim, 512] on device dev, contiguous within a head; returns (heads, dim, stride)."""
+    if w is None or w.get_device() != dev:
+        raise ValueError(f"{name}: a tensor on cuda:{dev} is needed")
+    if w.dtype is not torch.bfloat16 or w.dim() != 3 or w.shape[2] != D_LATENT:
+        raise ValueError(f"{name}: {w.dtype} {tuple(w.shape)}, bfloat16 (heads, dim, {D_LATENT}) is needed")
+    H, dim, _ = w.shape
+    s = w.stride()
+    if s[2] != 1 or (dim > 1 and s[1] != D_LATENT) or (H > 1 and s[0] < dim * D_LATENT):
+        raise ValueError(f"{name}: a head's rows must be contiguous, and heads must not overlap")
+    return H, dim, s[0] if H > 1 else dim * D_LATENT
+
+
+def query_latent(q, w_uk, pos, rope_cs, out, err=None, stream=None):
+    """csa2_query_latent: q bf16 [total, H*(dim+64)] (rows may be strided), w_uk bf16 [H, dim, 512] (heads may
+    be strided), pos int64 [total] -> out bf16 [total, H, 576]: the absorbed queries with rotated RoPE dims.
+    Rows with a negative position are left as they were."""
+    dev = out.get_device()
+    H, dim, ws = _want_heads("w_uk", w_uk, dev)
+    total = out.shape[0]
+    _want("out", out, torch.bfloat16, (total, H, D_QK), dev if dev >= 0 else None)
+    qs = _want_rows("q", q, (torch.bfloat16,), H * (dim + D_ROPE), dev, total)
+    _want("pos", pos, torch.int64, (total,), dev)
+    _want("rope_cs", rope_cs, torch.float32, None, dev)
+    if rope_cs.dim() < 2 or rope_cs.numel() != 64 * rope_cs.shape[0]:
+        raise ValueError(f"rope_cs: shape {tuple(rope_cs.shape)}, (positions, 32, 2) is needed")
+    ew = _err_word(err, dev)
+    if total == 0:
+        return
+    _call_on("csa2_query_latent", dev, stream, _adr(q), qs, total, H, dim, _adr(w_uk), ws, _adr(pos), _adr(rope_cs),
+             rope_cs.shape[0], _adr(out), ew)
+
+
+def value_project(o, w_uv, out, err=None, stream=None):
+    """csa2_value_project: o [total, H, 512] (fp32 or bf16, contiguous), w_uv bf16 [H, dim, 512] (heads may be
+    strided) -> out bf16 [total, H*dim] (rows may be strided)."""
+    dev = out.get_device()
+    H, dim, ws = _want_heads("w_uv", w_uv, dev)
+    total = out.shape[0]
+    os_ = _want_rows("out", out, (torch.bfloat16,), H * dim, dev, total)
+    _want("o", o, _FLOATS, (total, H, D_LATENT), dev if dev >= 0 else None)
+    ew = _err_word(err, dev)
+    if total == 0:
+        return
+    _call_on("csa2_value_project", dev, stream, _adr(o), H * D_LATENT, IN_BF16 if o.dtype is torch.bfloat16 else IN_F32, total,
+             H, dim, _adr(w_uv), ws, _adr(out), os_, ew)
 
 
 # --------------------------------------------------------------------------- 4-bit matrices

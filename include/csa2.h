@@ -601,6 +601,42 @@ csa2_status csa2_fp4_product(const csa2_fp4_matrix *x, const csa2_fp4_matrix *w,
                              int32_t out_dtype, int32_t *err_word, csa2_stream_t stream);
 
 /*
+ * csa2_query_latent: a layer's queries into the latent space, the absorbed form that
+ * the attention calls take ([P2] §4: q W^UK), with the RoPE dims rotated as the
+ * appends rotate the keys'.  Per row t and head h
+ *   out[t][h][0:512]   = sum_k q[t][h][k] w_uk[h][k][0:512], k < dim
+ *   out[t][h][512:576] = q[t][h][dim:dim+64] rotated at position pos[t]
+ *   q: bf16, row t at q + t * q_stride elements, its heads dim + 64 values each one
+ *      after the other (q_stride >= n_heads (dim + 64), a multiple of 8);
+ *   w_uk: bf16, head h's dim rows of 512 at w_uk + h * w_stride (>= dim x 512, a
+ *      multiple of 8: keys' and values' rows may lie together);
+ *   pos: int64 [total], as csa2_slot_map leaves them; out: bf16 [total][n_heads][576].
+ * Rows with a negative position are left as they were.  Sums in fp32, rounded once.
+ * n_heads 1..128, dim a multiple of 16, 16..128.
+ * Device errors: ROPE (a position >= rope_len: the row is left as it was), TIMEOUT.
+ */
+csa2_status csa2_query_latent(const uint16_t *q, int64_t q_stride, int32_t total, int32_t n_heads, int32_t dim,
+                              const uint16_t *w_uk, int64_t w_stride, const int64_t *pos, const float *rope_cs,
+                              int64_t rope_len, uint16_t *out, int32_t *err_word, csa2_stream_t stream);
+
+/*
+ * csa2_value_project: attended latent rows to the heads' values ([P2] §4: the
+ * deferred W^UV).  Per row t and head h
+ *   out[t][h dim + j] = sum_c o[t][h][c] w_uv[h][j][c], c < 512, j < dim
+ *   o: fp32 or bf16 (in_dtype, CSA2_IN_*), row t at o + t * o_stride elements, its
+ *      heads 512 values each (o_stride >= n_heads x 512, a multiple of 8);
+ *   w_uv: bf16, head h's dim rows of 512 at w_uv + h * w_stride, as w_uk;
+ *   out: bf16, row t at out + t * out_stride (>= n_heads x dim, a multiple of 8).
+ * Sums in fp32, rounded once; fp32 rows enter as two bf16 parts, to 2^-16 of a value
+ * (magnitudes from bf16's largest on as infinities).
+ * n_heads 1..128, dim a multiple of 16, 16..128.  Device errors: TIMEOUT.
+ * A row's bits do not depend on the other rows, in both calls.
+ */
+csa2_status csa2_value_project(const void *o, int64_t o_stride, int32_t in_dtype, int32_t total, int32_t n_heads, int32_t dim,
+                               const uint16_t *w_uv, int64_t w_stride, uint16_t *out, int64_t out_stride, int32_t *err_word,
+                               csa2_stream_t stream);
+
+/*
  * csa2_mxf4_peak_launch: measurement helper (not a step of the method).
  * Launches n_ctas CTAs that each issue `iters` back-to-back block-scaled FP4
  * tensor-core MMAs (tcgen05 kind::mxf4, M 128 x N 128 x K 64, the index score's

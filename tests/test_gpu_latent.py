@@ -1,0 +1,198 @@
+"""csa2_query_latent and csa2_value_project on the GPU against 64-bit products."""
+import math
+
+import pytest
+import torch
+
+from fp4_compressed_sparse_gb300 import csa2
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+THETA = 10000.0
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from fp4_compressed_sparse_gb300 import build_lib
+    build_lib.build()
+    csa2.load()
+
+
+def _err():
+    return torch.zeros(1, dtype=torch.int32, device=DEV)
+
+
+def _weights(H, dim, g):
+    """W_UK and W_UV as slices of one [H, 2 dim, 512]."""
+    w = (torch.randn(H, 2 * dim, 512, generator=g, device=DEV) / math.sqrt(512)).to(torch.bfloat16)
+    return w[:, :dim], w[:, dim:]
+
+
+def _near(out, want, mag, steps, lost=0.0):
+    """bf16 out against 64 bits: the sum of `steps` MMA steps, each off by at most one unit of fp32 (2^-23
+    of the magnitudes added up), what the operands lost, and half a step of bf16."""
+    tol = (steps * 2.0 ** -23 + lost) * mag * (1 + 2.0 ** -8) + 2.0 ** -8 * want.abs()
+    err = (out.double() - want).abs()
+    assert (err <= tol).all(), float((err / tol).nan_to_num().max())
+
+
+QUERY = [(1, 64, 128), (2, 1, 16), (127, 16, 64), (128, 128, 128), (129, 5, 48), (500, 64, 128), (33, 128, 112), (1500, 32, 32), (3001, 16, 128)]
+
+
+@pytest.mark.parametrize("T,H,D", QUERY)
+def test_query_latent(T, H, D):
+    """Strided rows and heads; rows of negative positions left alone; RoPE dims bit for bit."""
+    g = torch.Generator(device=DEV).manual_seed(T)
+    w, _ = _weights(H, D, g)
+    wide = torch.randn(T + 2, H * (D + 64) + 24, generator=g, device=DEV).to(torch.bfloat16)
+    q = wide[:, :H * (D + 64)]
+    rope, err = csa2.rope_table(THETA, 5000), _err()
+    pos = torch.randint(0, 5000, (T + 2,), generator=g, device=DEV)
+    pos[0], pos[T // 2] = 4999, -1
+    pos[T:] = -7
+    out = torch.full((T + 2, H, 576), 9.0, dtype=torch.bfloat16, device=DEV)
+    csa2.query_latent(q, w, pos, rope, out, err=err)
+    assert int(err) == 0
+    live = pos >= 0
+    assert (out[~live] == 9).all()
+    x = q.view(T + 2, H, D + 64)[live].double() if q.is_contiguous() else q.reshape(T + 2, H, D + 64)[live].double()
+    wd = w.double()
+    want, mag = torch.einsum("thk,hkc->thc", x[..., :D], wd), torch.einsum("thk,hkc->thc", x[..., :D].abs(), wd.abs())
+    _near(out[live][..., :512], want, mag, D // 16 + 1)
+    c, s = rope[pos[live]][:, None, :, 0].double(), rope[pos[live]][:, None, :, 1].double()
+    a, b = x[..., D::2], x[..., D + 1::2]
+    f = lambda v: v.float().double()
+    rot = torch.stack([f(a * c - f(b * s)), f(b * c + f(a * s))], -1).flatten(-2)
+    assert torch.equal(out[live][..., 512:], rot.float().to(torch.bfloat16))
+
+
+def test_query_rope_errors():
+    rope, err = csa2.rope_table(THETA, 100), _err()
+    g = torch.Generator(device=DEV).manual_seed(0)
+    w, _ = _weights(4, 32, g)
+    q = torch.randn(3, 4 * 96, generator=g, device=DEV).to(torch.bfloat16)
+    out = torch.full((3, 4, 576), 9.0, dtype=torch.bfloat16, device=DEV)
+    csa2.query_latent(q, w, torch.tensor([99, 100, 2 ** 40], device=DEV), rope, out, err=err)
+    assert int(err) == csa2.DEVERR_ROPE and (out[1:] == 9).all() and not (out[0] == 9).all()
+
+
+def test_position_zero_and_far_rows():
+    """Position 0 leaves the RoPE dims as they are; offsets beyond 2^31 elements of q and out."""
+    T, H, D = 60000, 128, 128
+    rope = csa2.rope_table(THETA, 4)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    w, _ = _weights(H, D, g)
+    q = torch.empty(T, H * (D + 64), dtype=torch.bfloat16, device=DEV)
+    assert T * H * 576 > 2 ** 31
+    at = torch.tensor([0, 1, T // 2 - 1, T - 130, T - 2, T - 1], device=DEV)
+    q[at] = torch.randn(6, H * (D + 64), generator=g, device=DEV).to(torch.bfloat16)
+    pos = torch.full((T,), -1, dtype=torch.int64, device=DEV)
+    pos[at] = 0
+    out = torch.zeros(T, H, 576, dtype=torch.bfloat16, device=DEV)
+    csa2.query_latent(q, w, pos, rope, out)
+    x = q[at].view(6, H, D + 64)
+    assert torch.equal(out[at][..., 512:], x[..., D:])
+    wd, xd = w.double(), x[..., :D].double()
+    _near(out[at][..., :512], torch.einsum("thk,hkc->thc", xd, wd), torch.einsum("thk,hkc->thc", xd.abs(), wd.abs()), 9)
+    assert not out[2:T // 2 - 2].any()
+
+
+VALUE = [(1, 64, 128), (2, 1, 16), (127, 16, 64), (128, 128, 128), (129, 5, 48), (300, 64, 128), (33, 128, 112), (1500, 32, 32), (3001, 16, 128)]
+
+
+@pytest.mark.parametrize("T,H,D", VALUE)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_value_project(T, H, D, dtype):
+    g = torch.Generator(device=DEV).manual_seed(T)
+    _, w = _weights(H, D, g)
+    o, err = torch.randn(T, H, 512, generator=g, device=DEV).to(dtype), _err()
+    out = torch.full((T + 1, H * D + 8), 9.0, dtype=torch.bfloat16, device=DEV)
+    csa2.value_project(o, w, out[:T, :H * D], err=err)
+    assert int(err) == 0 and (out[T:] == 9).all() and (out[:, H * D:] == 9).all()
+    od, wd = o.double(), w.double()
+    want, mag = torch.einsum("thc,hjc->thj", od, wd), torch.einsum("thc,hjc->thj", od.abs(), wd.abs())
+    f32 = dtype == torch.float32
+    _near(out[:T, :H * D].reshape(T, H, D), want, mag, (64 if f32 else 32) + 1, 2.0 ** -16 if f32 else 0.0)
+
+
+def test_value_nonfinite_rows():
+    """An infinite or NaN latent reaches the values of its own token and head, and no other."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    _, w = _weights(4, 64, g)
+    for dtype in (torch.bfloat16, torch.float32):
+        o = torch.randn(140, 4, 512, generator=g, device=DEV).to(dtype)
+        clean, out = (torch.empty(140, 256, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+        csa2.value_project(o, w, clean)
+        o[3, 1, 77], o[130, 2, 500] = math.inf, math.nan
+        csa2.value_project(o, w, out)
+        want = o[3, 1, 77].float() * w[1, :, 77].float()
+        assert torch.equal(out[3, 64:128].float(), want) and torch.isnan(out[130, 128:192]).all()
+        out[3, 64:128], out[130, 128:192] = clean[3, 64:128], clean[130, 128:192]
+        assert torch.equal(out, clean)
+
+
+def test_a_row_does_not_depend_on_the_others():
+    g = torch.Generator(device=DEV).manual_seed(4)
+    k, v = _weights(16, 128, g)
+    rope = csa2.rope_table(THETA, 5000)
+    q = torch.randn(2000, 16 * 192, generator=g, device=DEV).to(torch.bfloat16)
+    o = torch.randn(2000, 16, 512, generator=g, device=DEV)
+    pos = torch.arange(2000, device=DEV)
+    full, val = torch.empty(2000, 16, 576, dtype=torch.bfloat16, device=DEV), torch.empty(2000, 16 * 128, dtype=torch.bfloat16, device=DEV)
+    csa2.query_latent(q, k, pos, rope, full)
+    csa2.value_project(o, v, val)
+    for lo, hi in ((0, 1), (777, 778), (100, 140), (1500, 2000)):
+        a, b = torch.empty_like(full[lo:hi]), torch.empty_like(val[lo:hi])
+        csa2.query_latent(q[lo:hi], k, pos[lo:hi].clone(), rope, a)
+        csa2.value_project(o[lo:hi], v, b)
+        assert torch.equal(a, full[lo:hi]) and torch.equal(b, val[lo:hi])
+
+
+def test_unaligned_to_32_bytes():
+    """Outputs on 16-byte boundaries (and row strides that are odd multiples of 16 bytes)."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    k, v = _weights(3, 32, g)
+    rope = csa2.rope_table(THETA, 300)
+    q, o = torch.randn(200, 3 * 96, generator=g, device=DEV).to(torch.bfloat16), torch.randn(200, 3, 512, generator=g, device=DEV)
+    pos = torch.arange(200, device=DEV)
+    a = torch.empty(200, 3, 576, dtype=torch.bfloat16, device=DEV)
+    b = torch.empty(200 * 3 * 576 + 8, dtype=torch.bfloat16, device=DEV)[8:].view(200, 3, 576)
+    c = torch.empty(200, 96, dtype=torch.bfloat16, device=DEV)
+    d = torch.empty(200, 104, dtype=torch.bfloat16, device=DEV)[:, 8:]
+    assert b.data_ptr() % 32 == 16
+    csa2.query_latent(q, k, pos, rope, a)
+    csa2.query_latent(q, k, pos, rope, b)
+    csa2.value_project(o, v, c)
+    csa2.value_project(o, v, d)
+    assert torch.equal(a, b) and torch.equal(c, d)
+
+
+@pytest.mark.parametrize("T", [1, 400])
+def test_streams_and_graphs(T):
+    g = torch.Generator(device=DEV).manual_seed(6)
+    k, v = _weights(64, 128, g)
+    rope = csa2.rope_table(THETA, 1000)
+    xs = [(torch.randn(T, 64 * 192, generator=g, device=DEV).to(torch.bfloat16), torch.randn(T, 64, 512, generator=g, device=DEV),
+           torch.randint(0, 1000, (T,), generator=g, device=DEV)) for _ in range(2)]
+    out = lambda: (torch.zeros(T, 64, 576, dtype=torch.bfloat16, device=DEV), torch.zeros(T, 64 * 128, dtype=torch.bfloat16, device=DEV))
+    want = []
+    for q, o, p in xs:
+        a, b = out()
+        csa2.query_latent(q, k, p, rope, a)
+        csa2.value_project(o, v, b)
+        want.append((a, b))
+    buf, res, res2 = [t.clone() for t in xs[0]], out(), out()
+    torch.cuda.synchronize()
+    side, other, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        csa2.query_latent(buf[0], k, buf[2], rope, res[0])
+        csa2.value_project(buf[1], v, res[1])
+    for x, w in zip(xs, want):
+        for t, s in zip(buf, x):
+            t.copy_(s)
+        graph.replay()
+        csa2.query_latent(x[0], k, x[2], rope, res2[0], stream=other)
+        csa2.value_project(x[1], v, res2[1], stream=other)
+        torch.cuda.synchronize()
+        for r in (res, res2):
+            assert torch.equal(r[0], w[0]) and torch.equal(r[1], w[1])
