@@ -66,7 +66,7 @@ class PoolStruct(ctypes.Structure):
 
 class Fp4Struct(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("format", ctypes.c_int32),
-                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("row_scales", ctypes.c_void_p)]
+                ("tiles", ctypes.c_void_p), ("row_scales", ctypes.c_void_p)]
 
 
 class CompressIn(ctypes.Structure):
@@ -763,20 +763,19 @@ class Fp4Matrix:
         if rows < 0 or rows > 1 << 24 or cols < 1 or cols > 1 << 17 or fmt not in (FP4_NV, FP4_MX):
             raise ValueError(f"{rows} x {cols}, format {fmt}: rows 0..2^24, cols 1..2^17, FP4_NV or FP4_MX are needed")
         self.rows, self.cols, self.fmt = rows, cols, fmt
-        nb = [L.csa2_fp4_plane_bytes(rows, cols, fmt, p) for p in range(3)]
-        self.codes = torch.empty(nb[0], dtype=torch.uint8, device=device)
-        self.scales = torch.empty(nb[1], dtype=torch.uint8, device=device)
-        self.row_scales = torch.empty(nb[2] // 4, dtype=torch.float32, device=device)
-        self.struct = Fp4Struct(rows, cols, fmt, self.codes.data_ptr(), self.scales.data_ptr(), self.row_scales.data_ptr())
+        nb = [L.csa2_fp4_plane_bytes(rows, cols, fmt, p) for p in range(2)]
+        self.tiles = torch.empty(nb[0], dtype=torch.uint8, device=device)
+        self.row_scales = torch.empty(nb[1] // 4, dtype=torch.float32, device=device)
+        self.struct = Fp4Struct(rows, cols, fmt, self.tiles.data_ptr(), self.row_scales.data_ptr())
 
     def ref(self):
         return ctypes.byref(self.struct)
 
 
 def _fp4_device(m):
-    dev = m.codes.get_device()
+    dev = m.tiles.get_device()
     if dev < 0:
-        raise ValueError(f"the matrix is on {m.codes.device}, a CUDA device is needed")
+        raise ValueError(f"the matrix is on {m.tiles.device}, a CUDA device is needed")
     return dev
 
 
@@ -807,7 +806,7 @@ def fp4_product(x: Fp4Matrix, w: Fp4Matrix, out, err=None, stream=None):
     """csa2_fp4_product: out [x.rows, w.rows] = x w^T (fp32 or bf16, rows may be strided)."""
     dev = _fp4_device(x)
     if _fp4_device(w) != dev:
-        raise ValueError(f"w is on {w.codes.device}, x on cuda:{dev}")
+        raise ValueError(f"w is on {w.tiles.device}, x on cuda:{dev}")
     stride = _want_rows("out", out, _FLOATS, w.rows, dev, x.rows)
     ew = _err_word(err, dev)
     if x.rows == 0 or w.rows == 0:

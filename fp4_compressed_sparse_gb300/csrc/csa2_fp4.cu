@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kQThreads) k_fp4_quant(F4Args a) {
     for (int p = kRows == 8 ? t >> 3 : t; p < pieces; p += kQThreads / kRows) {
       load32<kBf16>(x + row * a.stride * kElt, 32 * p, cols, v);
       uint32_t w[4];
-      uint8_t *sc = a.m.scales + (tile0 + (p >> 2)) * f4_scale_tile(kNv) + f4_scale_at(m);
+      uint8_t *rec = a.m.tiles + (tile0 + (p >> 2)) * f4_tile_bytes(kNv), *sc = rec + kF4CodeBytes + f4_scale_at(m);
       if constexpr (kNv) {
         uint32_t s0, s1;
 #pragma unroll
@@ -205,8 +205,7 @@ __global__ void __launch_bounds__(kQThreads) k_fp4_quant(F4Args a) {
         }
         sc[p & 3] = static_cast<uint8_t>(code);
       }
-      *reinterpret_cast<uint4 *>(a.m.codes + (tile0 + (p >> 2)) * kF4TileBytes + (p & 3) * 2048 + m * 16) =
-          make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4 *>(rec + (p & 3) * 2048 + m * 16) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
   if constexpr (!kNv) {
@@ -232,9 +231,8 @@ __global__ void __launch_bounds__(256) k_fp4_read(csa2_fp4_matrix mx, void *out,
   const float r = mx.row_scales[row];
   const int64_t tile0 = static_cast<int64_t>(row / kF4Rows) * ct;
   for (int p = blockIdx.y * 8 + warp; p < pieces; p += 8 * gridDim.y) {
-    const int64_t tile = tile0 + (p >> 2);
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(mx.codes + tile * kF4TileBytes + (p & 3) * 2048 + m * 16 + 4 * u);
-    const uint8_t *sc = mx.scales + tile * f4_scale_tile(kNv) + f4_scale_at(m);
+    const uint8_t *rec = mx.tiles + (tile0 + (p >> 2)) * f4_tile_bytes(kNv), *sc = rec + kF4CodeBytes + f4_scale_at(m);
+    const uint32_t w = *reinterpret_cast<const uint32_t *>(rec + (p & 3) * 2048 + m * 16 + 4 * u);
     const float s = kNv ? e4m3_value(sc[512 * ((p >> 1) & 1) + 2 * (p & 1) + (u >> 1)]) * r : e8m0_value(sc[p & 3]) * r;
     uint32_t h[4];
     e2m1x8_h2(w, h);
@@ -280,8 +278,8 @@ csa2_status check_fp4(const csa2_fp4_matrix *m, const char *name) {
   CSA2_REQUIRE(m->cols >= 1 && m->cols <= (1 << 17), CSA2_ERR_SHAPE, "%s: cols %d outside 1..2^17", name, m->cols);
   CSA2_REQUIRE(m->format == CSA2_FP4_NV || m->format == CSA2_FP4_MX, CSA2_ERR_RANGE, "%s: format %d", name, m->format);
   if (m->rows == 0) return CSA2_OK;
-  CSA2_REQUIRE(m->codes && m->scales && m->row_scales, CSA2_ERR_NULL, "%s: a plane is NULL", name);
-  CSA2_REQUIRE(aligned16(m->codes) && aligned16(m->scales) && aligned16(m->row_scales), CSA2_ERR_ALIGN,
+  CSA2_REQUIRE(m->tiles && m->row_scales, CSA2_ERR_NULL, "%s: a plane is NULL", name);
+  CSA2_REQUIRE(aligned16(m->tiles) && aligned16(m->row_scales), CSA2_ERR_ALIGN,
                "%s: a plane is not 16-byte aligned", name);
   return CSA2_OK;
 }
@@ -296,9 +294,8 @@ size_t csa2_fp4_plane_bytes(int32_t rows, int32_t cols, int32_t format, int32_t 
   if (rows < 0 || cols <= 0 || (format != CSA2_FP4_NV && format != CSA2_FP4_MX)) return 0;
   const size_t tiles = static_cast<size_t>(csa2::f4_row_tiles(rows)) * csa2::f4_col_tiles(cols);
   switch (plane) {
-    case 0: return tiles * csa2::kF4TileBytes;
-    case 1: return tiles * csa2::f4_scale_tile(format == CSA2_FP4_NV);
-    case 2: return static_cast<size_t>(csa2::f4_row_tiles(rows)) * csa2::kF4Rows * sizeof(float);
+    case 0: return tiles * csa2::f4_tile_bytes(format == CSA2_FP4_NV);
+    case 1: return static_cast<size_t>(csa2::f4_row_tiles(rows)) * csa2::kF4Rows * sizeof(float);
   }
   return 0;
 }

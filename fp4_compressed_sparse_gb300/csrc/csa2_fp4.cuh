@@ -2,12 +2,12 @@
 // instructions that read it.
 //
 // A matrix of rows x cols is cut into tiles of 128 rows x 128 columns, row tile by
-// row tile, in the operand layout of the block-scaled MMA (K-major, no swizzle), so a
-// tile is copied into shared memory as it lies:
-//   codes   tile * 8192 + j * 2048 + m * 16 + byte   (row m of the tile, 32-value piece j)
-//   scales  NV (E4M3 per 16): tile * 1024 + h * 512 + 16 (m % 32) + 4 (m / 32) + g,
-//           group 4 h + g of the 8;  MX (E8M0 per 32): tile * 512 + 16 (m % 32) + 4 (m / 32) + j
-//   row_scales  fp32 per row
+// row tile, each a record in the operand layout of the block-scaled MMA (K-major, no
+// swizzle), so that it is copied into shared memory as it lies:
+//   codes   j * 2048 + m * 16 + byte   (row m of the tile, 32-value piece j)
+//   scales  behind them; NV (E4M3 per 16): h * 512 + 16 (m % 32) + 4 (m / 32) + g, group
+//           4 h + g of the 8;  MX (E8M0 per 32): 16 (m % 32) + 4 (m / 32) + j
+// and row_scales, fp32 per row.
 #pragma once
 
 #include "csa2_internal.cuh"
@@ -16,8 +16,9 @@
 namespace csa2 {
 
 constexpr int kF4Rows = 128, kF4Cols = 128;
-constexpr int kF4TileBytes = 8192;
-__host__ __device__ constexpr int f4_scale_tile(bool nv) { return nv ? 1024 : 512; }
+constexpr int kF4CodeBytes = 8192;  // of a tile
+__host__ __device__ constexpr int f4_scale_bytes(bool nv) { return nv ? 1024 : 512; }
+__host__ __device__ constexpr int f4_tile_bytes(bool nv) { return kF4CodeBytes + f4_scale_bytes(nv); }
 __host__ __device__ __forceinline__ int64_t f4_col_tiles(int64_t cols) { return (cols + kF4Cols - 1) / kF4Cols; }
 __host__ __device__ __forceinline__ int64_t f4_row_tiles(int64_t rows) { return (rows + kF4Rows - 1) / kF4Rows; }
 // byte offset of the scale bytes of row m within a 512 B atom

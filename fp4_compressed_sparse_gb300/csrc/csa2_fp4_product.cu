@@ -11,6 +11,8 @@
 // output tile are dealt to the CTAs of a cluster, whose sums are added in rank order
 // through distributed shared memory: no workspace, equal calls give equal bits.
 // Bound: the weights' bytes for few tokens.
+#include <cuda.h>
+
 #include "csa2_fp4.cuh"
 
 namespace csa2 {
@@ -43,8 +45,8 @@ __device__ __forceinline__ void cluster_sync() {
 // Shared memory of a stage: codes of 128 weight rows, codes of NT tokens, both's scales.
 template <int NT, bool kNv>
 struct Split {
-  static constexpr int kA = kF4TileBytes, kB = NT * 64, kS = f4_scale_tile(kNv);
-  static constexpr int kStage = kA + kB + 2 * kS;
+  static constexpr int kRec = f4_tile_bytes(kNv), kB = NT * 64, kS = f4_scale_bytes(kNv);
+  static constexpr int kStage = kRec + kB + kS;
   static constexpr int kStages = NT <= 32 ? 8 : NT <= 64 ? 7 : 5;  // two CTAs per SM
   static constexpr int kAtoms = kNv ? 2 : 1;                       // 512 B of scales per operand
   static constexpr int kSfCols = 8 * kAtoms;                       // TMEM columns of a stage's scales
@@ -87,22 +89,21 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_split(ProductArgs a) {
   const uint32_t tmem = tmem_at, s0 = tc::smem_addr(smem);
 
   if (warp == 0 && lane == 0) {
-    const int64_t wt = static_cast<int64_t>(nt) * kt, xt = static_cast<int64_t>(m0 / kF4Rows) * kt;
-    for (int i = 0; i < nk; ++i) {
+    const uint8_t *wp = a.w.tiles + (static_cast<int64_t>(nt) * kt + k0) * L::kRec;
+    const uint8_t *xp = a.x.tiles + (static_cast<int64_t>(m0 / kF4Rows) * kt + k0) * L::kRec;
+    for (int i = 0; i < nk; ++i, wp += L::kRec, xp += L::kRec) {
       const int st = i % L::kStages;
       if (i >= L::kStages && !tc::mbar_wait_bounded(&empty[st], ((i / L::kStages) - 1) & 1, kWaitIters)) break;
-      const uint32_t sa = s0 + st * L::kStage, sb = sa + L::kA, ss = sb + L::kB;
+      const uint32_t sa = s0 + st * L::kStage, sb = sa + L::kRec;
       tc::mbar_expect_tx(&full[st], L::kStage);
-      tc::bulk_load(sa, a.w.codes + (wt + k0 + i) * kF4TileBytes, L::kA, &full[st]);
-      const uint8_t *xc = a.x.codes + (xt + k0 + i) * kF4TileBytes;
+      tc::bulk_load(sa, wp, L::kRec, &full[st]);
       if constexpr (NT == 128) {
-        tc::bulk_load(sb, xc, L::kB, &full[st]);
+        tc::bulk_load(sb, xp, L::kRec, &full[st]);
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) tc::bulk_load(sb + j * NT * 16, xc + j * 2048, NT * 16, &full[st]);
+        for (int j = 0; j < 4; ++j) tc::bulk_load(sb + j * NT * 16, xp + j * 2048, NT * 16, &full[st]);
+        tc::bulk_load(sb + L::kB, xp + kF4CodeBytes, L::kS, &full[st]);
       }
-      tc::bulk_load(ss, a.w.scales + (wt + k0 + i) * L::kS, L::kS, &full[st]);
-      tc::bulk_load(ss + L::kS, a.x.scales + (xt + k0 + i) * L::kS, L::kS, &full[st]);
       loaded = i + 1;
     }
   } else if (warp == 1 && lane == 0) {
@@ -112,14 +113,14 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_split(ProductArgs a) {
       ok = tc::mbar_wait_bounded(&full[st], (i / L::kStages) & 1, kWaitIters);
       if (!ok) break;
       tc::tc_fence_after();
-      const uint32_t sa = s0 + st * L::kStage, sb = sa + L::kA, ss = sb + L::kB;
+      const uint32_t sa = s0 + st * L::kStage, sb = sa + L::kRec;
       // a stage's scale columns are written again only once its MMAs, whose end
       // let the stage be refilled, are done
       const uint32_t sf = tmem + NT + st * L::kSfCols;
 #pragma unroll
       for (int h = 0; h < L::kAtoms; ++h) {
-        tc::tmem_cp_32x128b_x4(sf + 4 * h, tc::smem_desc_noswizzle(ss + 512 * h, 128, 128));
-        tc::tmem_cp_32x128b_x4(sf + 4 * (L::kAtoms + h), tc::smem_desc_noswizzle(ss + L::kS + 512 * h, 128, 128));
+        tc::tmem_cp_32x128b_x4(sf + 4 * h, tc::smem_desc_noswizzle(sa + kF4CodeBytes + 512 * h, 128, 128));
+        tc::tmem_cp_32x128b_x4(sf + 4 * (L::kAtoms + h), tc::smem_desc_noswizzle(sb + L::kB + 512 * h, 128, 128));
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -212,6 +213,335 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_split(ProductArgs a) {
   }
 }
 
+// ------------------------------------------------------------------ many tokens
+// k_fp4_pair: persistent clusters of two CTAs, whose SMs' tensor cores work on one tile
+// of 256 tokens x 256 columns (cta_group::2).  A CTA holds 128 of the tokens (and their
+// sums, 256 columns of tensor memory) and the codes of 128 of the weights' rows; the
+// scales of all 256 are needed by both.  The CTA of rank 0 issues for the two, and the
+// copies of both signal its barriers.
+//   warp 0      copies the tokens' records;  warp 2  the weights' codes;  warp 3  their scales
+//   warp 1      (rank 0) scales to tensor memory, MMAs
+//   warps 4-11  results: the sums are read into registers, which frees the tile's tensor
+//               memory for the next one, then scaled and written
+// A stage is two K tiles (256 columns): a copying thread needs about 0.22 us for a wait,
+// an arming and a copy, whatever its size.  Copies go by tensor maps over the records, so
+// that one fetches a box of several records' codes or scales; what lies behind the last
+// row or K tile arrives as zeros.
+constexpr int kPairThreads = 384, kPairN = 256;
+template <bool kNv>
+struct Pair {
+  static constexpr int kS = f4_scale_bytes(kNv), kRec = f4_tile_bytes(kNv), kAtoms = kNv ? 2 : 1;
+  static constexpr int kA = 2 * kRec, kB = 2 * kF4CodeBytes, kStage = kA + kB + 4 * kS;
+  static constexpr int kSfTile = kNv ? 24 : 16;  // TMEM columns of a K tile's scales: 8 per atom of the weights, then 4 per atom of the tokens
+  static constexpr int kStages = kNv ? 5 : 6;
+  static constexpr int kBytes = kStage * kStages + 1024;
+};
+constexpr int kPairStagesMax = 6;
+struct PairSync {
+  uint64_t full[kPairStagesMax], empty[kPairStagesMax];
+  uint64_t tfull, tempty;
+  uint32_t tmem;
+  int loaded;  // stages rank 0 has armed
+  int dead;    // a wait gave up
+};
+
+// Arrive on the barrier at the same place in CTA `rank` of the cluster.  Relaxed: what
+// it hands over is tensor memory, which the tcgen05 fences on both sides order (a
+// release at cluster scope takes a microsecond).
+__device__ __forceinline__ void arrive_at(uint64_t *bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(map_rank(tc::smem_addr(bar), rank))
+               : "memory");
+}
+__device__ __forceinline__ void commit_pair(uint64_t *bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n" ::"r"(
+                   tc::smem_addr(bar)),
+               "h"(static_cast<uint16_t>(3))
+               : "memory");
+}
+// A box of the map to shared memory of this CTA; its bytes count on the barrier at
+// (cluster) address bar, which may be the peer's.
+__device__ __forceinline__ void tensor_load(uint32_t dst, const CUtensorMap *map, int c1, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+      "[%6];\n" ::"r"(dst),
+      "l"(map), "r"(0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void cp_scales_pair(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+template <bool kNv>
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sfa, uint32_t sfb, uint32_t acc) {
+  if constexpr (kNv) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
+        : "memory");
+  }
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e;
+}
+
+template <bool kNv, bool kBf16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    k_fp4_pair(ProductArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
+               const __grid_constant__ CUtensorMap ms, int mt, int nt, int wide32) {
+  using L = Pair<kNv>;
+  extern __shared__ uint8_t raw[];
+  __shared__ __align__(128) PairSync sy;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  uint32_t rank;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int kt = static_cast<int>(f4_col_tiles(a.x.cols)), steps = (kt + 1) / 2;
+  const int gm = (mt + 1) / 2, tiles = gm * nt, pairs = gridDim.x / 2;
+  const uint32_t s0 = (tc::smem_addr(raw) + 1023) & ~1023u;  // (the same in both CTAs)
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(tc::smem_addr(&sy.tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n" ::: "memory");
+  }
+  if (t == 0) {
+    for (int i = 0; i < L::kStages; ++i) {
+      tc::mbar_init(&sy.full[i], 1);
+      tc::mbar_init(&sy.empty[i], 1);
+    }
+    tc::mbar_init(&sy.tfull, 1);
+    tc::mbar_init(&sy.tempty, 16);
+    sy.loaded = sy.dead = 0;
+    tc::fence_mbar_init();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the peer's barriers are initialised, its tensor memory allocated
+  tc::tc_fence_after();
+  const uint32_t tmem = sy.tmem;
+  auto gave_up = [&]() {
+    raise_err(a.err, CSA2_DEVERR_TIMEOUT);
+    *reinterpret_cast<volatile int *>(&sy.dead) = 1;
+  };
+  // tiles: down the tokens first, eight columns of tiles at a time
+  auto tile_of = [&](int i, int &m, int &n) {
+    constexpr int kBand = 8;
+    const int band = i / (kBand * gm), in = i - band * kBand * gm, width = min(kBand, nt - band * kBand);
+    m = 2 * (in / width) + static_cast<int>(rank);
+    n = band * kBand + in % width;
+  };
+  const int first = blockIdx.x / 2;
+
+  if (warp == 0 || warp == 2 || warp == 3) {
+    // ------------------------------------------------------------ copies
+    const uint32_t el = elect_one();
+    uint32_t st = 0, ph = 1;
+    int f = 0;
+    bool ok = true;
+    for (int i = first; i < tiles && ok; i += pairs) {
+      int m, n;
+      tile_of(i, m, n);
+      for (int k = 0; k < steps; ++k, ++f) {
+        if (f >= L::kStages) ok = tc::mbar_wait_bounded(&sy.empty[st], ph, kWaitIters);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t sa = s0 + st * L::kStage, bar = map_rank(tc::smem_addr(&sy.full[st]), 0);
+        if (el) {
+          if (warp == 0) {
+            if (rank == 0) tc::mbar_expect_tx(&sy.full[st], 2 * L::kStage);
+            tensor_load(sa, &mx, 0, 2 * k, m, bar);
+          } else if (warp == 2) {
+            tensor_load(sa + L::kA, &mw, 0, 2 * k, 2 * n + static_cast<int>(rank), bar);
+          } else {
+            tensor_load(sa + L::kA + L::kB, &ms, kNv ? 8 : 16, 2 * k, 2 * n, bar);
+          }
+        }
+        __syncwarp();
+        if (++st == L::kStages) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (t == 0 && rank == 0) sy.loaded = f;
+    if (!ok && lane == 0) gave_up();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs
+    const uint32_t el = elect_one();
+    constexpr uint32_t kM256 = (128u >> 4) << 24;  // (the descriptor's M, from 128 to 256)
+    constexpr uint32_t kId0 = tc::idesc_f4(kNv, kPairN, 0) + kM256, kId1 = tc::idesc_f4(kNv, kPairN, kNv ? 0 : 2) + kM256;
+    uint32_t st = 0, ph = 0, j = 0;
+    bool ok = true;
+    for (int i = first; i < tiles && ok && rank == 0; i += pairs, ++j) {
+      if (j > 0) ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sy.tempty, (j - 1) & 1, kWaitIters));
+      for (int k = 0; k < steps && ok; ++k) {
+        ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sy.full[st], ph, kWaitIters));
+        if (!ok) break;
+        tc::tc_fence_after();
+        if (el) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t sa = s0 + st * L::kStage + u * L::kRec, sb = s0 + st * L::kStage + L::kA + u * kF4CodeBytes;
+            const uint32_t ss = s0 + st * L::kStage + L::kA + L::kB + u * L::kS;  // columns 0-127; 128-255 two K tiles on
+            const uint32_t sf = tmem + kPairN + (2 * st + u) * L::kSfTile;
+            const uint64_t dsa = tc::smem_desc_noswizzle(sa + kF4CodeBytes, 128, 128), dsb = tc::smem_desc_noswizzle(ss, 128, 128),
+                           da = tc::smem_desc_noswizzle(sa, 2048, 128), db = tc::smem_desc_noswizzle(sb, 2048, 128);
+#pragma unroll
+            for (int h = 0; h < L::kAtoms; ++h) {
+              cp_scales_pair(sf + 8 * L::kAtoms + 4 * h, dsa + (512 * h >> 4));
+              cp_scales_pair(sf + 8 * h, dsb + (512 * h >> 4));
+              cp_scales_pair(sf + 8 * h + 4, dsb + ((2 * L::kS + 512 * h) >> 4));
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              mma_pair<kNv>(tmem, da + (4096 * h >> 4), db + (4096 * h >> 4), h ? kId1 : kId0,
+                            sf + 8 * L::kAtoms + (kNv ? 4 * h : 0), sf + (kNv ? 8 * h : 0), k + u + h > 0 ? 1u : 0u);
+          }
+          commit_pair(&sy.empty[st]);
+          if (k == steps - 1) commit_pair(&sy.tfull);
+        }
+        __syncwarp();
+        if (++st == L::kStages) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (!ok && lane == 0) gave_up();
+  } else {
+    // ------------------------------------------------------------ results
+    const int q = warp & 3, half = (warp - 4) >> 2;
+    uint32_t j = 0;
+    bool ok = true;
+    for (int i = first; i < tiles && ok; i += pairs, ++j) {
+      int m, n;
+      tile_of(i, m, n);
+      const int row = m * kF4Rows + 32 * q + lane, c0 = n * kPairN + 128 * half;
+      const bool live = row < a.x.rows;
+      const float r_m = live ? a.x.row_scales[row] : 0.0f;
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sy.tfull, j & 1, kWaitIters));
+      if (!ok) break;
+      tc::tc_fence_after();
+      uint32_t r[128];
+      const uint32_t at = tmem + 128 * half + (static_cast<uint32_t>(32 * q) << 16);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) tc::tmem_ld_32x32b_x16(at + 16 * c, r + 16 * c);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) tc::tmem_ld_wait_x16(r + 16 * c);
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_at(&sy.tempty, 0);
+      const int cols = min(128, a.w.rows - c0);  // columns there are (the row scales' plane holds whole tiles)
+      if (!live || cols <= 0) continue;
+      const int64_t o = row * a.stride + c0;
+#pragma unroll
+      for (int c = 0; c < 128; c += 16) {
+        float v[16];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const float4 s = __ldg(reinterpret_cast<const float4 *>(a.w.row_scales + c0 + min(c, (cols - 1) & ~15)) + u);
+          v[4 * u] = __uint_as_float(r[c + 4 * u]) * (r_m * s.x);
+          v[4 * u + 1] = __uint_as_float(r[c + 4 * u + 1]) * (r_m * s.y);
+          v[4 * u + 2] = __uint_as_float(r[c + 4 * u + 2]) * (r_m * s.z);
+          v[4 * u + 3] = __uint_as_float(r[c + 4 * u + 3]) * (r_m * s.w);
+        }
+        if constexpr (kBf16) {
+          uint16_t *p = static_cast<uint16_t *>(a.out) + o + c;
+          uint32_t w[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * u], v[2 * u + 1]);
+            w[u] = *reinterpret_cast<uint32_t *>(&b);
+          }
+          if (c + 16 <= cols) {
+            if (wide32) {
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                           "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                           : "memory");
+            } else {
+              reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+              if (c + u < cols) p[u] = static_cast<uint16_t>(w[u / 2] >> (16 * (u & 1)));
+          }
+        } else {
+          float *p = static_cast<float *>(a.out) + o + c;
+          if (c + 16 <= cols) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) reinterpret_cast<float4 *>(p)[u] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+          } else {
+#pragma unroll
+            for (int u = 0; u < 16; ++u)
+              if (c + u < cols) p[u] = v[u];
+          }
+        }
+      }
+    }
+    if (!ok && lane == 0) gave_up();
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (t == 0 && sy.dead)  // copies still in flight (rank 0: into either CTA)
+    for (int i = sy.loaded > L::kStages ? sy.loaded - L::kStages : 0; i < sy.loaded; ++i)
+      tc::mbar_wait_bounded(&sy.full[i % L::kStages], (i / L::kStages) & 1, kWaitIters);
+  cluster_sync();  // neither leaves while the other's MMAs and arrivals may come
+  if (warp == 1) {
+    tc::tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;\n" ::"r"(tmem) : "memory");
+  }
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {
+  static const EncodeTiled fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r);
+    return e == cudaSuccess && r == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeTiled>(p) : nullptr;
+  }();
+  return fn;
+}
+// A map over a matrix's records, seen as [row tile][K tile][pieces][piece bytes], whose box
+// is `pieces` pieces of two K tiles of `row_tiles` row tiles.
+bool record_map(CUtensorMap *map, const csa2_fp4_matrix &m, bool nv, int pieces, int row_tiles) {
+  const EncodeTiled encode = encode_tiled();
+  if (encode == nullptr) return false;
+  const cuuint64_t piece = nv ? 1024 : 512, rec = f4_tile_bytes(nv), kt = f4_col_tiles(m.cols);
+  const cuuint64_t dim[4] = {piece / 8, rec / piece, kt, static_cast<cuuint64_t>(f4_row_tiles(m.rows))};
+  const cuuint64_t stride[3] = {piece, rec, rec * kt};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(piece / 8), static_cast<cuuint32_t>(pieces), 2, static_cast<cuuint32_t>(row_tiles)};
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 4, m.tiles, dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool kNv, bool kBf16>
+cudaError_t launch_pair(const ProductArgs &a, cudaStream_t s) {
+  using L = Pair<kNv>;
+  const auto kern = k_fp4_pair<kNv, kBf16>;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), L::kBytes);
+  if (e != cudaSuccess) return e;
+  CUtensorMap mx, mw, ms;
+  constexpr int kCodes = kNv ? 8 : 16;  // pieces of a record that are codes; one more is the scales
+  if (!record_map(&mx, a.x, kNv, kCodes + 1, 1) || !record_map(&mw, a.w, kNv, kCodes, 1) || !record_map(&ms, a.w, kNv, 1, 2))
+    return cudaErrorNotSupported;
+  const int mt = static_cast<int>(f4_row_tiles(a.x.rows)), nt = (a.w.rows + kPairN - 1) / kPairN;
+  const int64_t tiles = static_cast<int64_t>((mt + 1) / 2) * nt, most = device_sm_count() / 2;
+  const int wide32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && a.stride % 16 == 0;
+  kern<<<static_cast<unsigned>(2 * (tiles < most ? tiles : most)), kPairThreads, L::kBytes, s>>>(a, mx, mw, ms, mt, nt, wide32);
+  return cudaGetLastError();
+}
+
 template <int NT, bool kNv, bool kBf16>
 cudaError_t launch_split(const ProductArgs &a, int ranks, cudaStream_t s) {
   using L = Split<NT, kNv>;
@@ -234,6 +564,8 @@ cudaError_t launch_split(const ProductArgs &a, int ranks, cudaStream_t s) {
 template <bool kNv, bool kBf16>
 cudaError_t launch_product(const ProductArgs &a, cudaStream_t s) {
   const int m = a.x.rows;
+  const int64_t big = (f4_row_tiles(m) + 1) / 2 * ((a.w.rows + kPairN - 1) / kPairN);
+  if (4 * 2 * big >= 3 * device_sm_count()) return launch_pair<kNv, kBf16>(a, s);
   const int nt = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
   const int64_t tiles = f4_row_tiles(a.w.rows) * ((m + nt - 1) / nt);
   const int64_t kt = f4_col_tiles(a.x.cols), sms = device_sm_count();

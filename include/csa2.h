@@ -557,12 +557,12 @@ csa2_status csa2_slot_map(const csa2_cache *cache, const int32_t *cu_new, int32_
  *   Value: code x scale x r.  A row that holds an infinity or NaN (NV: also one whose
  *   largest magnitude is above 2688 x 2^62) gets r = NaN and raises the NAN bit: what
  *   is read or computed from it is NaN.
- * Planes (csa2_fp4_plane_bytes, plane 0..2), in tiles of 128 rows x 128 columns, row
- *   tile by row tile, the operand layout of the block-scaled tensor-core MMA:
- *   codes       tile * 8192 + j * 2048 + m * 16: the 16 bytes of 32-column piece j of
- *               row m of the tile
- *   scales      NV: tile * 1024 + (g / 4) * 512 + 16 (m % 32) + 4 (m / 32) + g % 4,
- *               group g of 8; MX: tile * 512 + 16 (m % 32) + 4 (m / 32) + j
+ * Planes (csa2_fp4_plane_bytes, plane 0 and 1):
+ *   tiles       records of 128 rows x 128 columns, row tile by row tile, in the operand
+ *               layout of the block-scaled tensor-core MMA: 8,192 B of codes, the 16
+ *               bytes of 32-column piece j of row m at j * 2048 + m * 16, then the scales,
+ *               NV (1,024 B): (g / 4) * 512 + 16 (m % 32) + 4 (m / 32) + g % 4, group g of
+ *               8; MX (512 B): 16 (m % 32) + 4 (m / 32) + j
  *   row_scales  float r per row
  * Rows behind `rows` in the last tile are neither written nor looked at.
  * rows 0..2^24, cols 1..2^17.
@@ -572,7 +572,7 @@ csa2_status csa2_slot_map(const csa2_cache *cache, const int32_t *cu_new, int32_
 typedef struct csa2_fp4_matrix {
   int32_t rows, cols;
   int32_t format;
-  uint8_t *codes, *scales;
+  uint8_t *tiles;
   float *row_scales;
 } csa2_fp4_matrix;
 size_t csa2_fp4_plane_bytes(int32_t rows, int32_t cols, int32_t format, int32_t plane);

@@ -48,12 +48,13 @@ def values(m):
     """[rows, cols] fp64 from the planes of an Fp4Matrix."""
     nv = m.fmt == csa2.FP4_NV
     rt, ct = -(-m.rows // 128), -(-m.cols // 128)
-    dev = m.codes.device
+    dev = m.tiles.device
     t = torch.tensor(GRID + [-v for v in GRID], dtype=torch.float64, device=dev)
-    b = m.codes.view(rt, ct, 4, 128, 16).permute(0, 3, 1, 2, 4).reshape(rt * 128, ct * 64).int()
+    rec = m.tiles.view(rt, ct, 9216 if nv else 8704)
+    b = rec[..., :8192].reshape(rt, ct, 4, 128, 16).permute(0, 3, 1, 2, 4).reshape(rt * 128, ct * 64).int()
     v = torch.stack([t[b & 15], t[b >> 4]], -1).flatten(1)
     n = 2 if nv else 1
-    sc = m.scales.view(rt, ct, n, 32, 4, 4).permute(0, 4, 3, 1, 2, 5).reshape(rt * 128, ct * n * 4)  # row 32 i + l
+    sc = rec[..., 8192:].reshape(rt, ct, n, 32, 4, 4).permute(0, 4, 3, 1, 2, 5).reshape(rt * 128, ct * n * 4)  # row 32 i + l
     if nv:
         s = torch.arange(256, dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn).double()[sc.int()]
     else:

@@ -57,8 +57,7 @@ def test_quant_is_the_definition(fmt, dtype, rows, cols):
     wide[:, :cols] = _rows(rows, cols, dtype, rows + cols)
     x, err = wide[:, :cols], _err()
     m = csa2.Fp4Matrix(rows, cols, fmt)
-    for t in (m.codes, m.scales):
-        t.fill_(0x5A)
+    m.tiles.fill_(0x5A)
     csa2.fp4_quant(m, x, err=err)
     want = fu.quantised(x, fmt)
     assert int(err) == 0
@@ -119,13 +118,13 @@ def test_quant_extreme_rows(fmt):
 def test_rows_behind_the_last_are_not_written():
     for fmt in FMTS:
         m = csa2.Fp4Matrix(5, 256, fmt)
-        for t in (m.codes, m.scales):
-            t.fill_(0xA5)
+        m.tiles.fill_(0xA5)
         m.row_scales.fill_(-3.0)
         csa2.fp4_quant(m, torch.ones(5, 256, device=DEV))
-        codes = m.codes.view(2, 4, 128, 16)
+        rec = m.tiles.view(2, -1)
+        codes = rec[:, :8192].reshape(2, 4, 128, 16)
         assert (codes[:, :, 5:] == 0xA5).all() and not (codes[:, :, :5] == 0xA5).any()
-        sc = m.scales.view(-1, 32, 4, 4)
+        sc = rec[:, 8192:].reshape(-1, 32, 4, 4)
         assert (sc[:, 5:] == 0xA5).all() and (sc[:, :5, 1:] == 0xA5).all() and (m.row_scales[5:] == -3).all()
 
 
