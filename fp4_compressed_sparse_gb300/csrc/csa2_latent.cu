@@ -11,18 +11,15 @@
 // third of what the tensor cores need to be the bound.  HBM bounds long batches, the
 // chain of loads short ones.
 //
-// One persistent CTA per SM.  A unit is (head, column part, tile of 128 tokens), units
-// of a head and part follow one another and a CTA takes a run of them, so that its part
-// of W stays in shared memory.  Tokens are the MMA's 128 rows (a lane holds one token
-// and writes runs of its row), W's columns its N.
-//   warps 0-7    load W (once per head) and the tokens' rows into shared memory, in
-//                core matrices of 8 rows x 16 bytes; rotate the query's RoPE dims
-//   warps 8-15   read the sums out of tensor memory and write them: two groups of four,
-//                one per accumulator
-//   warp 16      issues the MMAs
-// fp32 latents (value) are split into bf16 parts hi + lo, each multiplied: what is lost
-// is 2^-16 of a value, against 2^-8 that the bf16 result's rounding takes.
-#include "csa2_internal.cuh"
+// Three forms, by the number of tokens and the latents' type (the launch rules have both
+// sides' times):
+//   k_query_few, k_value_few   a block per head and column part, W from global memory
+//                              straight into the fragments of mma.sync: one round of loads
+//   k_latent                   persistent, tcgen05, operands by tensor maps
+//   k_value_f32                the same for fp32 latents, which warps split into bf16 parts
+//                              hi + lo, each multiplied: what is lost is 2^-16 of a value,
+//                              against 2^-8 that the bf16 result's rounding takes
+#include "csa2_latent.cuh"
 #include "csa2_tc.cuh"
 
 namespace csa2 {
@@ -35,24 +32,6 @@ constexpr int kIssueWarp = kLoadWarps + kOutWarps;
 constexpr uint32_t kWaitIters = 200;
 constexpr int kWBytesMax = 128 * kLat * 2;      // 128 KB
 constexpr int kMaxStages = 5;
-
-struct LatentArgs {
-  const void *x;        // query: bf16 rows of heads x (dim + 64); value: [total][heads][512]
-  int64_t x_stride;     // elements per token
-  const uint16_t *w;    // head h: rows of 512 at w + h * w_stride
-  int64_t w_stride;
-  int heads, dim, total;
-  const int64_t *pos;   // query
-  const float *rope;
-  int64_t rope_len;
-  uint16_t *out;
-  int64_t out_stride;   // elements per token
-  int parts;            // column parts of a head
-  int np;               // columns of a part
-  int tiles;            // token tiles
-  int wide;             // 32-byte stores are aligned
-  int32_t *err;
-};
 
 struct Sync {
   uint64_t full[kMaxStages], empty[kMaxStages];
@@ -91,16 +70,6 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t *>(&v);
-}
-// x = hi + lo in bf16, to 2^-16 of x; infinities and NaN in hi alone
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-  hi = pack_bf16(a, b);
-  const float ha = __uint_as_float(hi << 16), hb = __uint_as_float(hi & 0xFFFF0000u);
-  lo = pack_bf16(isfinite(ha) ? a - ha : 0.0f, isfinite(hb) ? b - hb : 0.0f);
 }
 
 // kQuery: K = dim in one stage, W [dim][np] read MN-major.  Value: K = 512 in stages of
@@ -245,20 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent(LatentArgs a) {
               if (h == 0 && d8 == 0) raise_err(a.err, CSA2_DEVERR_ROPE);
               continue;
             }
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(qr + tok * a.x_stride) + d8);
-            const float4 *cs = reinterpret_cast<const float4 *>(a.rope + p * kRope + 8 * d8);
-            const float4 c0 = __ldg(cs), c1 = __ldg(cs + 1);
-            const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-            const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-            uint32_t o[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float x = __uint_as_float(in[j] << 16), y = __uint_as_float(in[j] & 0xFFFF0000u);
-              rope_pair(x, y, cc[2 * j], cc[2 * j + 1]);
-              o[j] = pack_bf16(x, y);
-            }
-            *reinterpret_cast<uint4 *>(a.out + tok * a.out_stride + static_cast<int64_t>(h) * kDqk + kLat + 8 * d8) =
-                make_uint4(o[0], o[1], o[2], o[3]);
+            rotate8(a, qr + tok * a.x_stride + 8 * d8, p, d8, a.out + tok * a.out_stride + static_cast<int64_t>(h) * kDqk + kLat + 8 * d8);
           }
         }
         cp_wait<0>();
@@ -421,6 +377,8 @@ csa2_status csa2_query_latent(const uint16_t *q, int64_t q_stride, int32_t total
   a.np = CSA2_D_LATENT / a.parts;
   a.wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
   a.err = err_word;
+  if (total <= csa2::kFewTokens)
+    return cuda_status(csa2::launch_query_few(a, reinterpret_cast<cudaStream_t>(stream)), "csa2_query_latent launch");
   return cuda_status(csa2::launch<true, false>(a, reinterpret_cast<cudaStream_t>(stream)), "csa2_query_latent launch");
 }
 
@@ -459,6 +417,8 @@ csa2_status csa2_value_project(const void *o, int64_t o_stride, int32_t in_dtype
   a.wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && out_stride % 16 == 0;
   a.err = err_word;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (total <= csa2::kFewTokens)
+    return cuda_status(csa2::launch_value_few(a, in_dtype == CSA2_IN_F32, s), "csa2_value_project launch");
   return cuda_status(in_dtype == CSA2_IN_F32 ? csa2::launch<false, true>(a, s) : csa2::launch<false, false>(a, s),
                      "csa2_value_project launch");
 }

@@ -1,0 +1,65 @@
+// csa2_latent.cuh -- what the kernels of csa2_query_latent and csa2_value_project share.
+#pragma once
+
+#include "csa2_internal.cuh"
+
+namespace csa2 {
+
+struct LatentArgs {
+  const void *x;        // query: bf16 rows of heads x (dim + 64); value: [total][heads][512]
+  int64_t x_stride;     // elements per token
+  const uint16_t *w;    // head h: rows of 512 at w + h * w_stride
+  int64_t w_stride;
+  int heads, dim, total;
+  const int64_t *pos;   // query
+  const float *rope;
+  int64_t rope_len;
+  uint16_t *out;
+  int64_t out_stride;   // elements per token
+  int parts;            // column parts of a head
+  int np;               // columns of a part
+  int tiles;            // token tiles
+  int wide;             // 32-byte stores are aligned
+  int32_t *err;
+};
+
+
+// Up to here the forms for few tokens are taken (both sides' times stand at them).
+constexpr int kFewTokens = 64;
+cudaError_t launch_query_few(const LatentArgs &a, cudaStream_t s);
+cudaError_t launch_value_few(const LatentArgs &a, bool f32, cudaStream_t s);
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t *>(&v);
+}
+// x = hi + lo in bf16, to 2^-16 of x; infinities and NaN in hi alone
+__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
+  hi = pack_bf16(a, b);
+  const float ha = __uint_as_float(hi << 16), hb = __uint_as_float(hi & 0xFFFF0000u);
+  lo = pack_bf16(isfinite(ha) ? a - ha : 0.0f, isfinite(hb) ? b - hb : 0.0f);
+}
+// Whether a query row is written; one behind the RoPE table raises the bit.
+__device__ __forceinline__ bool row_position(const LatentArgs &a, int64_t tok, bool report, int64_t &p) {
+  p = a.pos[tok];
+  if (p >= a.rope_len && report) raise_err(a.err, CSA2_DEVERR_ROPE);
+  return p >= 0 && p < a.rope_len;
+}
+// RoPE dims 8 d8 .. of a head from src to dst, rotated at position p.
+__device__ __forceinline__ void rotate8(const LatentArgs &a, const uint16_t *src, int64_t p, int d8, uint16_t *dst) {
+  const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src));
+  const float4 *cs = reinterpret_cast<const float4 *>(a.rope + p * kRope + 8 * d8);
+  const float4 c0 = __ldg(cs), c1 = __ldg(cs + 1);
+  const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+  const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float x = __uint_as_float(in[j] << 16), y = __uint_as_float(in[j] & 0xFFFF0000u);
+    rope_pair(x, y, cc[2 * j], cc[2 * j + 1]);
+    o[j] = pack_bf16(x, y);
+  }
+  *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+}  // namespace csa2

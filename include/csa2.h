@@ -630,7 +630,8 @@ csa2_status csa2_query_latent(const uint16_t *q, int64_t q_stride, int32_t total
  * Sums in fp32, rounded once; fp32 rows enter as two bf16 parts, to 2^-16 of a value
  * (magnitudes from bf16's largest on as infinities).
  * n_heads 1..128, dim a multiple of 16, 16..128.  Device errors: TIMEOUT.
- * A row's bits do not depend on the other rows, in both calls.
+ * In both calls a row's last bits may change with the number of rows; equal calls
+ * give equal bits.
  */
 csa2_status csa2_value_project(const void *o, int64_t o_stride, int32_t in_dtype, int32_t total, int32_t n_heads, int32_t dim,
                                const uint16_t *w_uv, int64_t w_stride, uint16_t *out, int64_t out_stride, int32_t *err_word,

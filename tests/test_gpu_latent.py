@@ -115,37 +115,45 @@ def test_value_project(T, H, D, dtype):
     _near(out[:T, :H * D].reshape(T, H, D), want, mag, (64 if f32 else 32) + 1, 2.0 ** -16 if f32 else 0.0)
 
 
-def test_value_nonfinite_rows():
+@pytest.mark.parametrize("T", [20, 140])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_value_nonfinite_rows(T, dtype):
     """An infinite or NaN latent reaches the values of its own token and head, and no other."""
     g = torch.Generator(device=DEV).manual_seed(3)
     _, w = _weights(4, 64, g)
-    for dtype in (torch.bfloat16, torch.float32):
-        o = torch.randn(140, 4, 512, generator=g, device=DEV).to(dtype)
-        clean, out = (torch.empty(140, 256, dtype=torch.bfloat16, device=DEV) for _ in range(2))
-        csa2.value_project(o, w, clean)
-        o[3, 1, 77], o[130, 2, 500] = math.inf, math.nan
-        csa2.value_project(o, w, out)
-        want = o[3, 1, 77].float() * w[1, :, 77].float()
-        assert torch.equal(out[3, 64:128].float(), want) and torch.isnan(out[130, 128:192]).all()
-        out[3, 64:128], out[130, 128:192] = clean[3, 64:128], clean[130, 128:192]
-        assert torch.equal(out, clean)
+    o = torch.randn(T, 4, 512, generator=g, device=DEV).to(dtype)
+    clean, out = (torch.empty(T, 256, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    csa2.value_project(o, w, clean)
+    o[3, 1, 77], o[T - 10, 2, 500] = math.inf, math.nan
+    csa2.value_project(o, w, out)
+    want = o[3, 1, 77].float() * w[1, :, 77].float()
+    assert torch.equal(out[3, 64:128].float(), want) and torch.isnan(out[T - 10, 128:192]).all()
+    out[3, 64:128], out[T - 10, 128:192] = clean[3, 64:128], clean[T - 10, 128:192]
+    assert torch.equal(out, clean)
 
 
-def test_a_row_does_not_depend_on_the_others():
+def test_rows_in_other_batches():
+    """A row of a smaller batch: the same bits where the form is the same, else within both roundings."""
     g = torch.Generator(device=DEV).manual_seed(4)
     k, v = _weights(16, 128, g)
     rope = csa2.rope_table(THETA, 5000)
     q = torch.randn(2000, 16 * 192, generator=g, device=DEV).to(torch.bfloat16)
     o = torch.randn(2000, 16, 512, generator=g, device=DEV)
     pos = torch.arange(2000, device=DEV)
-    full, val = torch.empty(2000, 16, 576, dtype=torch.bfloat16, device=DEV), torch.empty(2000, 16 * 128, dtype=torch.bfloat16, device=DEV)
-    csa2.query_latent(q, k, pos, rope, full)
-    csa2.value_project(o, v, val)
-    for lo, hi in ((0, 1), (777, 778), (100, 140), (1500, 2000)):
-        a, b = torch.empty_like(full[lo:hi]), torch.empty_like(val[lo:hi])
+
+    def run(lo, hi):
+        a = torch.empty(hi - lo, 16, 576, dtype=torch.bfloat16, device=DEV)
+        b = torch.empty(hi - lo, 16 * 128, dtype=torch.bfloat16, device=DEV)
         csa2.query_latent(q[lo:hi], k, pos[lo:hi].clone(), rope, a)
         csa2.value_project(o[lo:hi], v, b)
-        assert torch.equal(a, full[lo:hi]) and torch.equal(b, val[lo:hi])
+        return a, b
+    full, few = run(0, 2000), run(0, 40)
+    for (lo, hi), ref in (((0, 1), few), ((17, 18), few), ((1, 30), few), ((300, 2000), full), ((100, 300), full)):
+        for x, y in zip(run(lo, hi), ref):
+            assert torch.equal(x, y[lo:hi])
+    for x, y in zip(few, full):
+        y = y[:40].double()
+        assert ((x.double() - y).abs() <= 2.0 ** -7 * y.abs() + 2.0 ** -12).all()
 
 
 def test_unaligned_to_32_bytes():
