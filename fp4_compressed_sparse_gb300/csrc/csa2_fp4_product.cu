@@ -11,9 +11,8 @@
 // output tile are dealt to the CTAs of a cluster, whose sums are added in rank order
 // through distributed shared memory: no workspace, equal calls give equal bits.
 // Bound: the weights' bytes for few tokens.
-#include <cuda.h>
-
 #include "csa2_fp4.cuh"
+#include "csa2_tma.cuh"
 
 namespace csa2 {
 namespace {
@@ -499,30 +498,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   }
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
-                                 const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiled encode_tiled() {
-  static const EncodeTiled fn = [] {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult r;
-    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r);
-    return e == cudaSuccess && r == cudaDriverEntryPointSuccess ? reinterpret_cast<EncodeTiled>(p) : nullptr;
-  }();
-  return fn;
-}
 // A map over a matrix's records, seen as [row tile][K tile][pieces][piece bytes], whose box
 // is `pieces` pieces of two K tiles of `row_tiles` row tiles.
 bool record_map(CUtensorMap *map, const csa2_fp4_matrix &m, bool nv, int pieces, int row_tiles) {
-  const EncodeTiled encode = encode_tiled();
-  if (encode == nullptr) return false;
-  const cuuint64_t piece = nv ? 1024 : 512, rec = f4_tile_bytes(nv), kt = f4_col_tiles(m.cols);
-  const cuuint64_t dim[4] = {piece / 8, rec / piece, kt, static_cast<cuuint64_t>(f4_row_tiles(m.rows))};
-  const cuuint64_t stride[3] = {piece, rec, rec * kt};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(piece / 8), static_cast<cuuint32_t>(pieces), 2, static_cast<cuuint32_t>(row_tiles)};
-  const cuuint32_t one[4] = {1, 1, 1, 1};
-  return encode(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 4, m.tiles, dim, stride, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const uint64_t piece = nv ? 1024 : 512, rec = f4_tile_bytes(nv), kt = f4_col_tiles(m.cols);
+  const uint64_t dim[4] = {piece / 8, rec / piece, kt, static_cast<uint64_t>(f4_row_tiles(m.rows))};
+  const uint64_t stride[3] = {piece, rec, rec * kt};
+  const uint32_t box[4] = {static_cast<uint32_t>(piece / 8), static_cast<uint32_t>(pieces), 2, static_cast<uint32_t>(row_tiles)};
+  return tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 4, m.tiles, dim, stride, box, false);
 }
 
 template <bool kNv, bool kBf16>

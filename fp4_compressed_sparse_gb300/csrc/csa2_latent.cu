@@ -11,54 +11,64 @@
 // third of what the tensor cores need to be the bound.  HBM bounds long batches, the
 // chain of loads short ones.
 //
-// Three forms, by the number of tokens and the latents' type (the launch rules have both
-// sides' times):
-//   k_query_few, k_value_few   a block per head and column part, W from global memory
-//                              straight into the fragments of mma.sync: one round of loads
-//   k_latent                   persistent, tcgen05, operands by tensor maps
-//   k_value_f32                the same for fp32 latents, which warps split into bf16 parts
-//                              hi + lo, each multiplied: what is lost is 2^-16 of a value,
-//                              against 2^-8 that the bf16 result's rounding takes
+// Two forms, by the number of tokens (both sides' times stand at kFewQuery): a block per
+// head and column part with everything in flight at once (csa2_latent_few.cu), and the
+// persistent kernel of this file.  fp32 latents are split into bf16 parts hi + lo, each
+// multiplied: what is lost is 2^-16 of a value, against 2^-8 that the bf16 result's
+// rounding takes.
 #include "csa2_latent.cuh"
 #include "csa2_tc.cuh"
+#include "csa2_tma.cuh"
 
 namespace csa2 {
 namespace {
 
-constexpr int kTok = 128;                       // tokens of a tile
-constexpr int kLoadWarps = 8, kOutWarps = 8;
-constexpr int kThreads = 32 * (kLoadWarps + kOutWarps + 1);
-constexpr int kIssueWarp = kLoadWarps + kOutWarps;
-constexpr uint32_t kWaitIters = 200;
-constexpr int kWBytesMax = 128 * kLat * 2;      // 128 KB
-constexpr int kMaxStages = 5;
+constexpr int kTok = 128;                   // tokens of a tile
+constexpr uint32_t kWaitIters = 200;        // suspended polls of <= 1 ms each
+constexpr int kWBytes = 128 * kLat * 2;     // 128 KB: a head's W, or a part of it
+constexpr int kBox = kTok * 128;            // 128 rows of 128 bytes, 128-byte swizzle
+enum Mode { kQuery, kValue, kValueF32 };
 
+// Beside W: stages of the tokens' rows, for fp32 latents the bf16 parts that are made of
+// them, for queries what is on its way out.  A stage is what one wait and arming of the copying thread (0.2 us) is
+// worth: 32 KB, two boxes of 64 columns (query: all of a tile's; value: a quarter), fp32:
+// one of 32.
+template <Mode kM>
+struct Shape {
+  static constexpr int kStage = kM == kValueF32 ? kBox : 2 * kBox;
+  static constexpr int kStages = kM == kValueF32 ? 4 : kM == kQuery ? 2 : 3;
+  static constexpr int kParts = kM == kValue ? 0 : 2;  // fp32: buffers of 16 KB, hi then lo; query: 4 KB per writing warp
+  static constexpr int kBytes = kWBytes + kStages * kStage + kParts * 16384 + 1024;
+  static constexpr int kMoreWarps = kM == kValue ? 0 : 8;  // that rotate, or split
+  static constexpr int kThreads = 32 * (12 + kMoreWarps);
+};
 struct Sync {
-  uint64_t full[kMaxStages], empty[kMaxStages];
-  uint64_t wfull;
+  uint64_t full[4], empty[4];
+  uint64_t wfull, wdone;         // W has landed; the last MMAs that read it are done
+  uint64_t pfull[2], pempty[2];  // fp32: the bf16 parts
   uint64_t tfull[2], tempty[2];
   uint32_t tmem;
+  uint32_t loaded;               // stages armed
+  int dead;                      // a wait gave up
 };
 
-__device__ __forceinline__ bool wait1(uint64_t *bar, uint32_t phase, int32_t *err) {
-  if (tc::mbar_wait_bounded(bar, phase, kWaitIters)) return true;
-  raise_err(err, CSA2_DEVERR_TIMEOUT);
-  return false;
+__device__ __forceinline__ bool wait_all(uint64_t *bar, uint32_t phase) {
+  return __all_sync(0xffffffffu, tc::mbar_wait_bounded(bar, phase, kWaitIters));
 }
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t phase, int32_t *err) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = wait1(bar, phase, err) ? 1 : 0;
-  if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
-  tc::mbar_wait_bounded(bar, phase, kWaitIters);  // (each lane observes the phase itself)
-  return true;
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e;
 }
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ void load2(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint64_t *bar) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(dst),
+               "l"(map), "r"(c0), "r"(c1), "r"(tc::smem_addr(bar))
+               : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int kN>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;\n" ::"n"(kN) : "memory");
+__device__ __forceinline__ void load3(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar) {
+  asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(dst),
+               "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(tc::smem_addr(bar))
+               : "memory");
 }
 // kind::f16, bf16 x bf16 -> fp32, M 128
 __device__ __forceinline__ uint32_t idesc_bf16(int n, int b_mn) {
@@ -71,206 +81,175 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+// 128-byte swizzle.  K-major: sbo between 8-row groups.  MN-major (64 values of N per
+// row, a row per k): lbo between 64-value blocks along N, sbo between groups of 8 k.
+__device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((saddr & 0x3FFFF) >> 4) | static_cast<uint64_t>((lbo >> 4) & 0x3FFF) << 16 |
+         static_cast<uint64_t>((sbo >> 4) & 0x3FFF) << 32 | static_cast<uint64_t>(1) << 46 | static_cast<uint64_t>(2) << 61;
+}
+__device__ __forceinline__ float4 lds4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ void sts4(uint32_t at, const uint32_t *v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
 
-// kQuery: K = dim in one stage, W [dim][np] read MN-major.  Value: K = 512 in stages of
-// kKc columns (fp32: hi and lo), W [np][512] K-major.
-template <bool kQuery, bool kF32>
-struct Shape {
-  static constexpr int kStageBytes = kQuery ? kTok * 128 * 2 : kTok * 64 * 2;
-  static constexpr int kStages = kQuery ? 2 : 5;
-  static constexpr int kKc = kQuery ? 128 : kF32 ? 32 : 64;
-  static constexpr int kBytes = kWBytesMax + kStages * kStageBytes + 1024;
-};
-
-template <bool kQuery, bool kF32>
-__global__ void __launch_bounds__(kThreads, 1) k_latent(LatentArgs a) {
-  using S = Shape<kQuery, kF32>;
+// One persistent CTA per SM.  A unit is (head, column part, tile of 128 tokens), units of
+// a head and part follow one another and a CTA takes a run of them, so that its part of
+// W stays in shared memory.  Tokens are the MMA's 128 rows (a lane holds one token and
+// writes runs of its row), W's columns its N.
+//   warp 0       copies W (once per head and part) and the tokens' rows, by tensor maps
+//   warp 1       issues the MMAs
+//   warps 4-11   read the sums out of tensor memory and write them: two groups of four,
+//                one per accumulator
+//   warps 12-    query: rotate the RoPE dims, from global memory to global memory;
+//                fp32 latents: split a stage into bf16 parts hi and lo (no swizzle: core
+//                matrices of 8 rows x 16 bytes)
+template <Mode kM>
+__global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
+    k_latent(LatentArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
+             const __grid_constant__ CUtensorMap mo) {
+  using S = Shape<kM>;
+  constexpr bool kQ = kM == kQuery, kF = kM == kValueF32;
   extern __shared__ uint8_t raw[];
-  __shared__ __align__(8) Sync sy;
+  __shared__ __align__(128) Sync sy;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  const uint32_t s_w = (tc::smem_addr(raw) + 1023) & ~1023u, s_x = s_w + kWBytesMax;
-  const int jobs = kQuery && a.np > 256 ? 2 : 1, cols = a.np / jobs;  // accumulators of a unit, their columns
-  const int chunks = kQuery ? 1 : kLat / S::kKc;
-  const int w_rows = kQuery ? a.dim : a.np;                          // rows of W in shared memory
+  const uint32_t s_w = (tc::smem_addr(raw) + 1023) & ~1023u, s_x = s_w + kWBytes, s_p = s_x + S::kStages * S::kStage;
+  const int jobs = kQ && a.np > 256 ? 2 : 1, cols = a.np / jobs;  // accumulators of a unit, their columns
+  const int chunks = kQ ? 1 : kF ? kLat / 32 : kLat / 128;       // stages of a unit
   const int64_t units = static_cast<int64_t>(a.heads) * a.parts * a.tiles;
   const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
-  if (warp == kIssueWarp) {
+  if (warp == 1) {
     tc::tmem_alloc(&sy.tmem, 512);
     tc::tmem_relinquish();
   }
   if (t == 0) {
-    for (int i = 0; i < S::kStages; ++i) {
-      tc::mbar_init(&sy.full[i], kLoadWarps);
-      tc::mbar_init(&sy.empty[i], 1);
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(&sy.full[i], 1);
+      tc::mbar_init(&sy.empty[i], kF ? 8 : 1);
     }
-    tc::mbar_init(&sy.wfull, kLoadWarps);
+    tc::mbar_init(&sy.wfull, 1);
+    tc::mbar_init(&sy.wdone, 1);
     for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&sy.pfull[i], 8);
+      tc::mbar_init(&sy.pempty[i], 1);
       tc::mbar_init(&sy.tfull[i], 1);
       tc::mbar_init(&sy.tempty[i], 4);
     }
+    sy.loaded = 0;
+    sy.dead = 0;
     tc::fence_mbar_init();
   }
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = sy.tmem;
+  auto gave_up = [&]() {
+    raise_err(a.err, CSA2_DEVERR_TIMEOUT);
+    *reinterpret_cast<volatile int *>(&sy.dead) = 1;
+  };
 
-  if (warp < kLoadWarps) {
-    // ------------------------------------------------------------ loads
-    const int r8 = lane & 7, uo = lane >> 3;  // row in a group of 8, 16-byte unit of four
+  if (warp == 0) {
+    // ------------------------------------------------------------ copies
+    const uint32_t el = elect_one();
+    const int boxes = kQ ? (a.dim + 63) / 64 : kF ? 1 : 2, wide = kF ? 32 : 64;
+    const int w_boxes = kQ ? a.np / 64 : kLat / 64, w_box = (kQ ? a.dim : a.np) * 128;
     int64_t held = -1;
-    uint32_t n = 0;        // stages filled so far
-    uint32_t pending = 0;  // ... whose hand-over is still to come
+    uint32_t n = 0, st = 0, ph = 1, wn = 0;
     bool ok = true;
-    auto hand_over = [&](uint64_t *bar) {
-      tc::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(bar);
-    };
     for (int64_t u = u0; u < u1 && ok; ++u) {
       const int64_t hp = u / a.tiles;
       const int tile = static_cast<int>(u - hp * a.tiles), h = static_cast<int>(hp / a.parts), part = static_cast<int>(hp % a.parts);
-      const int t0 = tile * kTok, rows = min(kTok, a.total - t0);
       if (hp != held) {
-        for (; pending > 0; --pending) {
-          cp_wait<0>();
-          hand_over(&sy.full[(n - pending) % S::kStages]);
-        }
-        // W is free once the last stage's MMAs are done
-        if (n > 0) ok = wait_warp(&sy.empty[(n - 1) % S::kStages], ((n - 1) / S::kStages) & 1, a.err);
+        if (held >= 0) ok = wait_all(&sy.wdone, wn++ & 1);
         if (!ok) break;
-        const uint16_t *src = a.w + h * a.w_stride + (kQuery ? part * a.np : static_cast<int64_t>(part) * a.np * kLat);
-        const int w_units = (kQuery ? a.np : kLat) / 8;
-        for (int i = warp; i < (w_rows / 8) * (w_units / 4); i += kLoadWarps) {
-          const int rg = i % (w_rows / 8), un = 4 * (i / (w_rows / 8)) + uo;
-          cp16(s_w + un * (w_rows * 16) + rg * 128 + r8 * 16, src + static_cast<int64_t>(8 * rg + r8) * kLat + 8 * un);
+        if (el) {
+          tc::mbar_expect_tx(&sy.wfull, w_boxes * w_box);
+          for (int i = 0; i < w_boxes; ++i)
+            load3(s_w + i * w_box, &mw, (kQ ? part * a.np : 0) + 64 * i, kQ ? 0 : part * a.np, h, &sy.wfull);
         }
-        cp_commit();
-        cp_wait<0>();
-        hand_over(&sy.wfull);
+        __syncwarp();
         held = hp;
       }
-      for (int c = 0; c < chunks && ok; ++c, ++n) {
-        const int st = n % S::kStages;
-        if (n >= S::kStages) ok = wait_warp(&sy.empty[st], ((n / S::kStages) - 1) & 1, a.err);
+      for (int c = 0; c < chunks; ++c, ++n) {
+        if (n >= S::kStages) ok = wait_all(&sy.empty[st], ph);
         if (!ok) break;
-        const uint32_t dst = s_x + st * S::kStageBytes;
-        if constexpr (!kF32) {
-          const uint16_t *src = static_cast<const uint16_t *>(a.x) + t0 * a.x_stride +
-                                (kQuery ? static_cast<int64_t>(h) * (a.dim + kRope) : static_cast<int64_t>(h) * kLat + c * S::kKc);
-          const int n_un = kQuery ? a.dim / 8 : S::kKc / 8, quads = (n_un + 3) / 4;
-          for (int i = warp; i < 16 * quads; i += kLoadWarps) {
-            const int r = 8 * (i % 16) + r8, un = 4 * (i / 16) + uo;
-            if (r < rows && un < n_un) cp16(dst + un * (kTok * 16) + r * 16, src + r * a.x_stride + 8 * un);
-          }
-          cp_commit();
-          ++pending;
-          if constexpr (!kQuery) {  // three stages in flight
-            if (pending == 3) {
-              cp_wait<2>();
-              hand_over(&sy.full[(n - 2) % S::kStages]);
-              --pending;
-            }
-          }
-        } else {
-          const float *src = static_cast<const float *>(a.x) + t0 * a.x_stride + static_cast<int64_t>(h) * kLat + c * S::kKc;
-          float4 v[2][2];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r = 8 * (warp + 8 * i) + r8;
-            v[i][0] = v[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (r < rows) {
-              const float4 *p = reinterpret_cast<const float4 *>(src + r * a.x_stride + 8 * uo);
-              v[i][0] = __ldg(p);
-              v[i][1] = __ldg(p + 1);
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int r = 8 * (warp + 8 * i) + r8;
-            uint32_t hi[4], lo[4];
-            split2(v[i][0].x, v[i][0].y, hi[0], lo[0]);
-            split2(v[i][0].z, v[i][0].w, hi[1], lo[1]);
-            split2(v[i][1].x, v[i][1].y, hi[2], lo[2]);
-            split2(v[i][1].z, v[i][1].w, hi[3], lo[3]);
-            const uint32_t at = dst + uo * (kTok * 16) + r * 16;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at + 8192), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
-          }
-          hand_over(&sy.full[st]);
+        if (el) {
+          tc::mbar_expect_tx(&sy.full[st], boxes * kBox);
+          for (int i = 0; i < boxes; ++i)
+            load2(s_x + st * S::kStage + i * kBox, &mx, (kQ ? h * (a.dim + kRope) : h * kLat + c * (kF ? 32 : 128)) + wide * i, tile * kTok, &sy.full[st]);
         }
-      }
-      if constexpr (kQuery) {
-        if (!ok) break;
-        // RoPE while the rows arrive: a thread takes 8 dims of a token
-        if (part == 0) {
-          const uint16_t *qr = static_cast<const uint16_t *>(a.x) + static_cast<int64_t>(h) * (a.dim + kRope) + a.dim;
-          for (int i = warp; i < kTok / 4; i += kLoadWarps) {
-            const int r = 4 * i + uo, d8 = r8;
-            if (r >= rows) continue;
-            const int64_t tok = t0 + r, p = a.pos[tok];
-            if (p < 0) continue;
-            if (p >= a.rope_len) {
-              if (h == 0 && d8 == 0) raise_err(a.err, CSA2_DEVERR_ROPE);
-              continue;
-            }
-            rotate8(a, qr + tok * a.x_stride + 8 * d8, p, d8, a.out + tok * a.out_stride + static_cast<int64_t>(h) * kDqk + kLat + 8 * d8);
-          }
+        __syncwarp();
+        if (++st == S::kStages) {
+          st = 0;
+          ph ^= 1;
         }
-        cp_wait<0>();
-        hand_over(&sy.full[(n - 1) % S::kStages]);
-        pending = 0;
       }
     }
-    cp_wait<0>();
-    if (ok)
-      for (; pending > 0; --pending) hand_over(&sy.full[(n - pending) % S::kStages]);
-  } else if (warp == kIssueWarp) {
-    // ------------------------------------------------------------ MMAs
     if (lane == 0) {
-      const uint32_t id = idesc_bf16(cols, kQuery ? 1 : 0);
-      const uint32_t wu = w_rows * 16;  // bytes from one 8-column unit of W to the next
-      int64_t held = -1;
-      uint32_t n = 0, j = 0, wn = 0;
-      bool ok = true;
-      for (int64_t u = u0; u < u1 && ok; ++u) {
-        const int64_t hp = u / a.tiles;
-        if (hp != held) {
-          ok = wait1(&sy.wfull, wn++ & 1, a.err);
-          held = hp;
+      sy.loaded = n;
+      if (!ok) gave_up();
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMAs
+    const uint32_t el = elect_one(), id = idesc_bf16(cols, kQ ? 1 : 0);
+    int64_t held = -1;
+    uint32_t st = 0, ph = 0, j = 0, wn = 0;
+    bool ok = true;
+    for (int64_t u = u0; u < u1 && ok; ++u) {
+      const int64_t hp = u / a.tiles;
+      if (hp != held) {
+        ok = wait_all(&sy.wfull, wn++ & 1);
+        held = hp;
+      }
+      for (int b = 0; b < jobs && ok; ++b, ++j) {
+        const uint32_t acc = j & 1, d = tmem + 256 * acc;
+        if (j >= 2) ok = wait_all(&sy.tempty[acc], ((j >> 1) - 1) & 1);
+        for (int c = 0; c < chunks && ok; ++c) {
+          if (b == 0) ok = kF ? wait_all(&sy.pfull[st], ph) : wait_all(&sy.full[st], ph);
           if (!ok) break;
-        }
-        for (int b = 0; b < jobs && ok; ++b, ++j) {
-          const uint32_t acc = j & 1, d = tmem + 256 * acc;
-          if (j >= 2) ok = wait1(&sy.tempty[acc], ((j >> 1) - 1) & 1, a.err);
-          for (int c = 0; c < chunks && ok; ++c) {
-            const uint32_t k = kQuery ? n : n + c, st = k % S::kStages;
-            if (b == 0) ok = wait1(&sy.full[st], (k / S::kStages) & 1, a.err);
-            if (!ok) break;
-            tc::tc_fence_after();
-            const uint32_t xa = s_x + st * S::kStageBytes;
-            if constexpr (kQuery) {
+          tc::tc_fence_after();
+          if (el) {
+            if constexpr (kQ) {
+              const uint64_t dx = desc_sw128(s_x + st * S::kStage, 16, 1024);
+              const uint64_t dw = desc_sw128(s_w + b * (cols / 64) * a.dim * 128, a.dim * 128, 1024);
               for (int s = 0; s < a.dim / 16; ++s)
-                mma_bf16(d, tc::smem_desc_noswizzle(xa + 4096 * s, 2048, 128),
-                         tc::smem_desc_noswizzle(s_w + b * (cols / 8) * wu + 256 * s, 128, wu), id, s > 0 ? 1u : 0u);
-            } else {
+                mma_bf16(d, dx + (((s >> 2) * kBox + 32 * (s & 3)) >> 4), dw + (2048 * s >> 4), id, s > 0 ? 1u : 0u);
+            } else if constexpr (kF) {
+              const uint64_t dw = desc_sw128(s_w + (c >> 1) * a.np * 128, 16, 1024) + (64 * (c & 1) >> 4);
+              const uint64_t dx = tc::smem_desc_noswizzle(s_p + st * 16384, 2048, 128);
 #pragma unroll
-              for (int s = 0; s < S::kKc / 16; ++s) {
-                const uint64_t wd = tc::smem_desc_noswizzle(s_w + (c * (S::kKc / 8) + 2 * s) * wu, wu, 128);
-                mma_bf16(d, tc::smem_desc_noswizzle(xa + 4096 * s, 2048, 128), wd, id, c + s > 0 ? 1u : 0u);
-                if constexpr (kF32) mma_bf16(d, tc::smem_desc_noswizzle(xa + 8192 + 4096 * s, 2048, 128), wd, id, 1u);
+              for (int s = 0; s < 2; ++s) {
+                mma_bf16(d, dx + (4096 * s >> 4), dw + (32 * s >> 4), id, c + s > 0 ? 1u : 0u);
+                mma_bf16(d, dx + ((8192 + 4096 * s) >> 4), dw + (32 * s >> 4), id, 1u);
               }
+            } else {
+              const uint64_t dx = desc_sw128(s_x + st * S::kStage, 16, 1024);
+#pragma unroll
+              for (int s = 0; s < 8; ++s)
+                mma_bf16(d, dx + (((s >> 2) * kBox + 32 * (s & 3)) >> 4),
+                         desc_sw128(s_w + (2 * c + (s >> 2)) * a.np * 128, 16, 1024) + (32 * (s & 3) >> 4), id, c + s > 0 ? 1u : 0u);
             }
-            if (b == jobs - 1) tc::mma_commit(&sy.empty[st]);
+            if (b == jobs - 1) tc::mma_commit(kF ? &sy.pempty[st] : &sy.empty[st]);
+            if (c == chunks - 1) {
+              tc::mma_commit(&sy.tfull[acc]);
+              if (b == jobs - 1 && u + 1 < u1 && (u + 1) / a.tiles != hp) tc::mma_commit(&sy.wdone);
+            }
           }
-          if (ok) tc::mma_commit(&sy.tfull[acc]);
+          __syncwarp();
+          if (b == jobs - 1 && ++st == (kF ? 2 : S::kStages)) {
+            st = 0;
+            ph ^= 1;
+          }
         }
-        n += chunks;
       }
     }
-  } else {
+    if (!ok && lane == 0) gave_up();
+  } else if (warp >= 4 && warp < 12) {
     // ------------------------------------------------------------ results
-    const int q = warp & 3, g = (warp - kLoadWarps) >> 2;
+    const int q = warp & 3, g = (warp - 4) >> 2;
     uint32_t j = 0;
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok; ++u) {
@@ -280,33 +259,56 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent(LatentArgs a) {
       for (int b = 0; b < jobs && ok; ++b, ++j) {
         if ((j & 1) != g) continue;
         bool live = tok < a.total;
-        if constexpr (kQuery) {
-          if (live) {
-            const int64_t p = a.pos[tok];
-            live = p >= 0 && p < a.rope_len;
-          }
-        }
-        uint16_t *dst = a.out + tok * a.out_stride + (kQuery ? static_cast<int64_t>(h) * kDqk : static_cast<int64_t>(h) * a.dim) +
+        int64_t p;
+        if (kQ && live) live = row_position(a, tok, false, p);
+        uint16_t *dst = a.out + tok * a.out_stride + (kQ ? static_cast<int64_t>(h) * kDqk : static_cast<int64_t>(h) * a.dim) +
                         part * a.np + b * cols;
-        ok = wait_warp(&sy.tfull[g], (j >> 1) & 1, a.err);
+        ok = wait_all(&sy.tfull[g], (j >> 1) & 1);
         if (!ok) break;
         tc::tc_fence_after();
         const uint32_t at = tmem + 256 * g + (static_cast<uint32_t>(32 * q) << 16);
-        for (int c = 0; c < cols; c += 16) {
-          uint32_t r[16];
-          tc::tmem_ld_32x32b_x16(at + c, r);
-          tc::tmem_ld_wait_x16(r);
-          uint32_t o[8];
+        // Whole rows of queries go out as boxes of 32 tokens x 64 columns through shared
+        // memory (a lane's own 32-byte stores of 1,152-byte rows take 1.3 times as long).
+        if (kQ && __all_sync(0xffffffffu, live || tok >= a.total)) {
+          const uint32_t buf = s_p + (warp - 4) * 4096;
+          for (int c = 0; c < cols; c += 64) {
+            if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+            __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-          if (live) {
-            if (a.wide) {
-              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + c), "r"(o[0]), "r"(o[1]),
-                           "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+            for (int i = 0; i < 4; ++i) {
+              uint32_t r[16], o[8];
+              tc::tmem_ld_32x32b_x16(at + c + 16 * i, r);
+              tc::tmem_ld_wait_x16(r);
+#pragma unroll
+              for (int v = 0; v < 8; ++v) o[v] = pack_bf16(__uint_as_float(r[2 * v]), __uint_as_float(r[2 * v + 1]));
+              sts4(buf + lane * 128 + (((2 * i) ^ (lane & 7)) << 4), o);
+              sts4(buf + lane * 128 + (((2 * i + 1) ^ (lane & 7)) << 4), o + 4);
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(&mo),
+                           "r"(h * kDqk + part * a.np + b * cols + c), "r"(tile * kTok + 32 * q), "r"(buf)
                            : "memory");
-            } else {
-              reinterpret_cast<uint4 *>(dst + c)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-              reinterpret_cast<uint4 *>(dst + c)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+              asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+            }
+          }
+        } else {
+          for (int c = 0; c < cols; c += 16) {
+            uint32_t r[16], o[8];
+            tc::tmem_ld_32x32b_x16(at + c, r);
+            tc::tmem_ld_wait_x16(r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+            if (live) {
+              if (a.wide) {
+                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + c), "r"(o[0]), "r"(o[1]),
+                             "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                             : "memory");
+              } else {
+                reinterpret_cast<uint4 *>(dst + c)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                reinterpret_cast<uint4 *>(dst + c)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+              }
             }
           }
         }
@@ -315,22 +317,108 @@ __global__ void __launch_bounds__(kThreads, 1) k_latent(LatentArgs a) {
         if (lane == 0) tc::mbar_arrive(&sy.tempty[g]);
       }
     }
+    if (!ok && lane == 0) gave_up();
+  } else if (kQ && warp >= 12) {
+    // ------------------------------------------------------------ RoPE: a lane takes 8 dims of four tokens
+    // (all of a unit's loads at once, the positions a unit ahead: a chain of two loads
+    // per unit took longer than its bytes)
+    const int d8 = lane & 7, r0 = 4 * (warp - 12) + (lane >> 3);
+    int64_t p[4];
+    auto positions = [&](int64_t u) {
+      const int64_t hp = u / a.tiles, t0 = (u - hp * a.tiles) * kTok;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t tok = t0 + r0 + 32 * i;
+        if (u >= u1 || tok >= a.total || !row_position(a, tok, hp == 0 && d8 == 0, p[i])) p[i] = -1;
+      }
+    };
+    positions(u0);
+    for (int64_t u = u0; u < u1; ++u) {
+      const int64_t hp = u / a.tiles, t0 = (u - hp * a.tiles) * kTok, h = hp / a.parts;
+      const bool mine = hp % a.parts == 0;
+      const uint16_t *src = static_cast<const uint16_t *>(a.x) + (t0 + r0) * a.x_stride + h * (a.dim + kRope) + a.dim + 8 * d8;
+      Rope8 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (mine && p[i] >= 0) x[i] = load_rope8(a, src + 32 * i * a.x_stride, p[i], d8);
+      bool there[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) there[i] = mine && p[i] >= 0;
+      positions(u + 1);
+      uint16_t *dst = a.out + (t0 + r0) * a.out_stride + h * kDqk + kLat + 8 * d8;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (there[i]) store_rope8(x[i], dst + 32 * i * a.out_stride);
+    }
+  } else if (kF && warp >= 12) {
+    // ------------------------------------------------------------ fp32 stages to bf16 parts
+    const int r8 = lane & 7, uo = lane >> 3, cw = warp - 12;
+    const uint32_t n_all = static_cast<uint32_t>(u1 - u0) * chunks;
+    bool ok = true;
+    for (uint32_t n = 0; n < n_all; ++n) {
+      const uint32_t st = n % S::kStages, pb = n & 1;
+      ok = wait_all(&sy.full[st], (n / S::kStages) & 1) && (n < 2 || wait_all(&sy.pempty[pb], ((n >> 1) - 1) & 1));
+      if (!ok) break;
+      const uint32_t src = s_x + st * S::kStage, dst = s_p + pb * 16384;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 8 * (cw + 8 * i) + r8;
+        const float4 v0 = lds4(src + r * 128 + (((2 * uo) ^ r8) << 4)), v1 = lds4(src + r * 128 + (((2 * uo + 1) ^ r8) << 4));
+        uint32_t hi[4], lo[4];
+        split2(v0.x, v0.y, hi[0], lo[0]);
+        split2(v0.z, v0.w, hi[1], lo[1]);
+        split2(v1.x, v1.y, hi[2], lo[2]);
+        split2(v1.z, v1.w, hi[3], lo[3]);
+        const uint32_t at = dst + uo * (kTok * 16) + r * 16;
+        sts4(at, hi);
+        sts4(at + 8192, lo);
+      }
+      tc::fence_proxy_async_smem();  // read by the tensor cores
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&sy.pfull[pb]);
+        tc::mbar_arrive(&sy.empty[st]);
+      }
+    }
+    if (!ok && lane == 0) gave_up();
   }
+  if (kQ && warp >= 4 && warp < 12 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
   tc::tc_fence_before();
   __syncthreads();
-  if (warp == kIssueWarp) {
+  if (t == 0 && sy.dead)  // copies still in flight
+    for (uint32_t i = sy.loaded > S::kStages ? sy.loaded - S::kStages : 0; i < sy.loaded; ++i)
+      tc::mbar_wait_bounded(&sy.full[i % S::kStages], (i / S::kStages) & 1, kWaitIters);
+  __syncthreads();
+  if (warp == 1) {
     tc::tc_fence_after();
     tc::tmem_dealloc(tmem, 512);
   }
 }
 
-template <bool kQuery, bool kF32>
+template <Mode kM>
 cudaError_t launch(const LatentArgs &a, cudaStream_t s) {
-  const auto kern = k_latent<kQuery, kF32>;
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), Shape<kQuery, kF32>::kBytes);
+  const auto kern = k_latent<kM>;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), Shape<kM>::kBytes);
   if (e != cudaSuccess) return e;
+  constexpr bool kQ = kM == kQuery, kF = kM == kValueF32;
+  CUtensorMap mx, mw, mo{};
+  const uint64_t elt = kF ? 4 : 2;
+  const uint64_t x_dim[2] = {static_cast<uint64_t>(a.heads) * (kQ ? a.dim + kRope : kLat), static_cast<uint64_t>(a.total)};
+  const uint64_t x_stride[1] = {static_cast<uint64_t>(a.x_stride) * elt};
+  const uint32_t x_box[2] = {kF ? 32u : 64u, kTok};
+  const uint64_t w_dim[3] = {kLat, static_cast<uint64_t>(a.dim), static_cast<uint64_t>(a.heads)};
+  const uint64_t w_stride[2] = {kLat * 2, static_cast<uint64_t>(a.w_stride) * 2};
+  const uint32_t w_box[3] = {64, static_cast<uint32_t>(kQ ? a.dim : a.np), 1};
+  if (!tensor_map(&mx, kF ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.x, x_dim, x_stride, x_box, true) ||
+      !tensor_map(&mw, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, a.w, w_dim, w_stride, w_box, true))
+    return cudaErrorNotSupported;
+  if constexpr (kQ) {
+    const uint64_t o_dim[2] = {static_cast<uint64_t>(a.out_stride), static_cast<uint64_t>(a.total)}, o_stride[1] = {a.out_stride * 2ull};
+    const uint32_t o_box[2] = {64, 32};
+    if (!tensor_map(&mo, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, o_dim, o_stride, o_box, true)) return cudaErrorNotSupported;
+  }
   const int64_t units = static_cast<int64_t>(a.heads) * a.parts * a.tiles, sms = device_sm_count();
-  kern<<<static_cast<unsigned>(units < sms ? units : sms), kThreads, Shape<kQuery, kF32>::kBytes, s>>>(a);
+  kern<<<static_cast<unsigned>(units < sms ? units : sms), Shape<kM>::kThreads, Shape<kM>::kBytes, s>>>(a, mx, mw, mo);
   return cudaGetLastError();
 }
 
@@ -377,9 +465,9 @@ csa2_status csa2_query_latent(const uint16_t *q, int64_t q_stride, int32_t total
   a.np = CSA2_D_LATENT / a.parts;
   a.wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
   a.err = err_word;
-  if (total <= csa2::kFewTokens)
+  if (csa2::few_tokens(total, n_heads, csa2::kFewQuery))
     return cuda_status(csa2::launch_query_few(a, reinterpret_cast<cudaStream_t>(stream)), "csa2_query_latent launch");
-  return cuda_status(csa2::launch<true, false>(a, reinterpret_cast<cudaStream_t>(stream)), "csa2_query_latent launch");
+  return cuda_status(csa2::launch<csa2::kQuery>(a, reinterpret_cast<cudaStream_t>(stream)), "csa2_query_latent launch");
 }
 
 csa2_status csa2_value_project(const void *o, int64_t o_stride, int32_t in_dtype, int32_t total, int32_t n_heads, int32_t dim,
@@ -417,9 +505,9 @@ csa2_status csa2_value_project(const void *o, int64_t o_stride, int32_t in_dtype
   a.wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && out_stride % 16 == 0;
   a.err = err_word;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (total <= csa2::kFewTokens)
+  if (csa2::few_tokens(total, n_heads, csa2::kFewValue))
     return cuda_status(csa2::launch_value_few(a, in_dtype == CSA2_IN_F32, s), "csa2_value_project launch");
-  return cuda_status(in_dtype == CSA2_IN_F32 ? csa2::launch<false, true>(a, s) : csa2::launch<false, false>(a, s),
+  return cuda_status(in_dtype == CSA2_IN_F32 ? csa2::launch<csa2::kValueF32>(a, s) : csa2::launch<csa2::kValue>(a, s),
                      "csa2_value_project launch");
 }
 

@@ -24,8 +24,13 @@ struct LatentArgs {
 };
 
 
-// Up to here the forms for few tokens are taken (both sides' times stand at them).
-constexpr int kFewTokens = 64;
+// Groups of 16 tokens times heads up to which the forms for few tokens are taken.  One
+// GB300, us, few / persistent: queries of 64 heads, 32 tokens 5.3 / 6.2, 33 tokens 7.9 /
+// 6.2; of 128 heads, 16 tokens 7.3 / 6.9, 17 tokens 9.3 / 7.0.  Values of 64 heads, bf16,
+// 32 tokens 3.4 / 5.2, 64 tokens 5.6 / 5.2; fp32 64 tokens 9.0 / 11.3; of 128 heads, 32
+// tokens bf16 5.7 / 6.1, fp32 9.0 / 12.0, 64 tokens 8.5 / 6.1 and 15.6 / 12.0.
+constexpr int kFewQuery = 128, kFewValue = 256;
+inline bool few_tokens(int total, int heads, int most) { return static_cast<int64_t>((total + 15) / 16) * heads <= most; }
 cudaError_t launch_query_few(const LatentArgs &a, cudaStream_t s);
 cudaError_t launch_value_few(const LatentArgs &a, bool f32, cudaStream_t s);
 
@@ -45,13 +50,18 @@ __device__ __forceinline__ bool row_position(const LatentArgs &a, int64_t tok, b
   if (p >= a.rope_len && report) raise_err(a.err, CSA2_DEVERR_ROPE);
   return p >= 0 && p < a.rope_len;
 }
-// RoPE dims 8 d8 .. of a head from src to dst, rotated at position p.
-__device__ __forceinline__ void rotate8(const LatentArgs &a, const uint16_t *src, int64_t p, int d8, uint16_t *dst) {
-  const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src));
+// RoPE dims 8 d8 .. of a head at src, and the table's row of position p.
+struct Rope8 {
+  uint4 v;
+  float4 c0, c1;
+};
+__device__ __forceinline__ Rope8 load_rope8(const LatentArgs &a, const uint16_t *src, int64_t p, int d8) {
   const float4 *cs = reinterpret_cast<const float4 *>(a.rope + p * kRope + 8 * d8);
-  const float4 c0 = __ldg(cs), c1 = __ldg(cs + 1);
-  const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-  const float cc[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+  return Rope8{__ldg(reinterpret_cast<const uint4 *>(src)), __ldg(cs), __ldg(cs + 1)};
+}
+__device__ __forceinline__ void store_rope8(const Rope8 &r, uint16_t *dst) {
+  const uint32_t in[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+  const float cc[8] = {r.c0.x, r.c0.y, r.c0.z, r.c0.w, r.c1.x, r.c1.y, r.c1.z, r.c1.w};
   uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {

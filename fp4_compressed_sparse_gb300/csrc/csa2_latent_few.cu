@@ -38,8 +38,8 @@ __global__ void __launch_bounds__(kFewThreads) k_query_few(LatentArgs a) {
       const int64_t tok = tok0 + i / 8;
       int64_t p;
       if (tok < a.total && row_position(a, tok, h == 0 && i % 8 == 0, p))
-        rotate8(a, xh + tok * a.x_stride + a.dim + 8 * (i % 8), p, i % 8,
-                a.out + tok * a.out_stride + static_cast<int64_t>(h) * kDqk + kLat + 8 * (i % 8));
+        store_rope8(load_rope8(a, xh + tok * a.x_stride + a.dim + 8 * (i % 8), p, i % 8),
+                    a.out + tok * a.out_stride + static_cast<int64_t>(h) * kDqk + kLat + 8 * (i % 8));
     }
     return;
   }
