@@ -40,7 +40,7 @@ __device__ __forceinline__ void load32(const void *row, int c0, int cols, float 
     for (int q = 0; q < 4; ++q) {
       uint4 w = make_uint4(0, 0, 0, 0);
       if (c0 + 8 * q + 8 <= cols) {
-        w = __ldg(reinterpret_cast<const uint4 *>(p) + q);
+        w = reinterpret_cast<const uint4 *>(p)[q];
       } else {
         uint32_t t[8];
 #pragma unroll
@@ -60,7 +60,7 @@ __device__ __forceinline__ void load32(const void *row, int c0, int cols, float 
     for (int q = 0; q < 8; ++q) {
       float4 w = make_float4(0, 0, 0, 0);
       if (c0 + 4 * q + 4 <= cols) {
-        w = __ldg(reinterpret_cast<const float4 *>(p) + q);
+        w = reinterpret_cast<const float4 *>(p)[q];
       } else {
         if (c0 + 4 * q < cols) w.x = p[4 * q];
         if (c0 + 4 * q + 1 < cols) w.y = p[4 * q + 1];
@@ -120,157 +120,287 @@ __device__ __forceinline__ void nv16(const float *y, uint32_t *w, uint32_t *sc) 
   }
 }
 
-// One block: kRows consecutive rows (8, so that a piece's 16 bytes of theirs are whole
-// 128 B lines; or 1, for few rows).  A thread takes 32 values of a row at a time.
-template <bool kNv, bool kBf16, int kRows>
-__global__ void __launch_bounds__(kQThreads) k_fp4_quant(F4Args a) {
+// A row's power of two from its largest magnitude's bits: the exponent, and whether the
+// row is beyond the format.
+__device__ __forceinline__ int row_exponent(uint32_t m, uint32_t &bad) {
+  // amax = f 2^E: 2688 = 1.3125 x 2^11
+  int e = m ? floor_log2f(__uint_as_float(m)) : 0;
+  if (m >= 0x00800000u) e += (m & 0x7FFFFFu) > 0x280000u ? -10 : -11;
+  e = m ? max(e, -62) : 0;
+  bad = e > 62 || m >= 0x7F800000u;
+  return e;
+}
+constexpr uint32_t kNan = 0x7FC00000u;
+
+// 32 values to 16 bytes of codes and, returned, their scale bytes (NV 2, MX 1).
+template <bool kNv, bool kBf16>
+__device__ __forceinline__ uint32_t quant32(float *v, float back, uint32_t &bad, uint32_t *w) {
+  if constexpr (kNv) {
+    uint32_t s0, s1;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = bad ? 0.0f : __fmul_rn(v[i], back);
+    nv16<kBf16>(v, w, &s0);
+    nv16<kBf16>(v + 16, w + 2, &s1);
+    return s0 | s1 << 8;
+  } else {
+    const uint32_t top32 = top_bits<32>(v);
+    w[0] = w[1] = w[2] = w[3] = 0;
+    if (top32 >= 0x7F800000u) bad = 1;
+    if (top32 == 0 || top32 >= 0x7F800000u) return 0;
+    const int e = max(floor_log2f(__uint_as_float(top32)) - 2, -127);
+    const float inv = pow2f(-e);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(v[i], inv);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = e2m1x8(v + 8 * i);
+    return static_cast<uint32_t>(e + 127);
+  }
+}
+
+// Few rows: a block per row, a thread takes 32 values at a time.
+template <bool kNv, bool kBf16>
+__global__ void __launch_bounds__(kQThreads) k_fp4_quant_row(F4Args a) {
   constexpr int kElt = kBf16 ? 2 : 4;
-  __shared__ uint32_t top[8], part[8];
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  const int rows = a.m.rows, cols = a.m.cols;
-  const int row0 = blockIdx.x * kRows;
-  const int row = row0 + (kRows == 8 ? t & 7 : 0);  // this thread's, once it writes
-  const uint8_t *x = static_cast<const uint8_t *>(a.x);
+  __shared__ uint32_t part[8], top;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, row = blockIdx.x, cols = a.m.cols;
+  const uint8_t *x = static_cast<const uint8_t *>(a.x) + row * a.stride * kElt;
   float v[32];
   uint32_t bad = 0;
   float back = 1.0f;  // 2^-(row exponent)
   if constexpr (kNv) {
-    if constexpr (kRows == 8) {  // a warp per row
-      uint32_t m = 0;
-      if (row0 + warp < rows) {
-        const uint8_t *src = x + (row0 + warp) * a.stride * kElt;
-        for (int c = 32 * lane; c < cols; c += 1024) {
-          load32<kBf16>(src, c, cols, v);
-          m = max(m, top_bits<32>(v));
-        }
-      }
-      m = __reduce_max_sync(0xffffffffu, m);
-      if (lane == 0) top[warp] = m;
-    } else {
-      uint32_t m = 0;
-      for (int c = 32 * t; c < cols; c += 32 * kQThreads) {
-        load32<kBf16>(x + row * a.stride * kElt, c, cols, v);
-        m = max(m, top_bits<32>(v));
-      }
-      m = __reduce_max_sync(0xffffffffu, m);
-      if (lane == 0) part[warp] = m;
-      __syncthreads();
-      if (t < 8) {
-        m = __reduce_max_sync(0xffu, part[t]);
-        if (t == 0) top[0] = m;
-      }
+    uint32_t m = 0;
+    for (int c = 32 * t; c < cols; c += 32 * kQThreads) {
+      load32<kBf16>(x, c, cols, v);
+      m = max(m, top_bits<32>(v));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) part[warp] = m;
+    __syncthreads();
+    if (t < 8) {
+      m = __reduce_max_sync(0xffu, part[t]);
+      if (t == 0) top = m;
     }
     __syncthreads();
-    const uint32_t m = top[kRows == 8 ? t & 7 : 0];
-    // amax = f 2^E: 2688 = 1.3125 x 2^11
-    int e = m ? floor_log2f(__uint_as_float(m)) : 0;
-    if (m >= 0x00800000u) e += (m & 0x7FFFFFu) > 0x280000u ? -10 : -11;
-    e = m ? max(e, -62) : 0;
-    bad = e > 62 || m >= 0x7F800000u;
+    const int e = row_exponent(top, bad);
     back = bad ? 0.0f : pow2f(-e);
-    if (row < rows && t < kRows) {
-      a.m.row_scales[row] = bad ? __uint_as_float(0x7FC00000u) : pow2f(e);
+    if (t == 0) {
+      a.m.row_scales[row] = bad ? __uint_as_float(kNan) : pow2f(e);
       if (bad) raise_err(a.err, CSA2_DEVERR_NAN);
     }
   }
+  const int ct = static_cast<int>(f4_col_tiles(cols)), m = row % kF4Rows;
+  uint8_t *tiles = a.m.tiles + static_cast<int64_t>(row / kF4Rows) * ct * f4_tile_bytes(kNv);
+  for (int p = t; p < 4 * ct; p += kQThreads) {
+    uint32_t w[4];
+    load32<kBf16>(x, 32 * p, cols, v);
+    const uint32_t code = quant32<kNv, kBf16>(v, back, bad, w);
+    uint8_t *rec = tiles + static_cast<int64_t>(p >> 2) * f4_tile_bytes(kNv), *sc = rec + kF4CodeBytes + f4_scale_at(m);
+    if constexpr (kNv) *reinterpret_cast<uint16_t *>(sc + 512 * ((p >> 1) & 1) + 2 * (p & 1)) = static_cast<uint16_t>(code);
+    else sc[p & 3] = static_cast<uint8_t>(code);
+    *reinterpret_cast<uint4 *>(rec + (p & 3) * 2048 + m * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  if constexpr (!kNv) {
+    bad = __syncthreads_or(bad);
+    if (t == 0) {
+      a.m.row_scales[row] = bad ? __uint_as_float(kNan) : 1.0f;
+      if (bad) raise_err(a.err, CSA2_DEVERR_NAN);
+    }
+  }
+}
+
+// Many rows: a block per 8 rows (their 16 bytes of a piece are a whole 128 B line).
+// kStaged: the rows are read once, coalesced, a warp per row, into shared memory (row
+// pitch an odd number of 16 bytes, so that 8 rows' loads meet no bank twice); else, when
+// they do not fit there, a second time through the caches.
+template <bool kNv, bool kBf16, bool kStaged>
+__global__ void __launch_bounds__(kQThreads) k_fp4_quant_rows(F4Args a, int pitch) {
+  constexpr int kElt = kBf16 ? 2 : 4;
+  extern __shared__ __align__(16) uint8_t stage[];
+  __shared__ uint32_t top[8];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, rows = a.m.rows, cols = a.m.cols;
+  const int row0 = blockIdx.x * 8, r8 = t & 7, row = row0 + r8;  // row: this thread's, once it writes
+  const uint8_t *x = static_cast<const uint8_t *>(a.x);
   const int ct = static_cast<int>(f4_col_tiles(cols)), pieces = 4 * ct;
-  const int m = row % kF4Rows;
-  const int64_t tile0 = static_cast<int64_t>(row / kF4Rows) * ct;
-  if (row < rows) {
-    for (int p = kRows == 8 ? t >> 3 : t; p < pieces; p += kQThreads / kRows) {
-      load32<kBf16>(x + row * a.stride * kElt, 32 * p, cols, v);
-      uint32_t w[4];
-      uint8_t *rec = a.m.tiles + (tile0 + (p >> 2)) * f4_tile_bytes(kNv), *sc = rec + kF4CodeBytes + f4_scale_at(m);
+  float v[32];
+  uint32_t bad = 0, m = 0;
+  float back = 1.0f;
+  if (kStaged && row0 + warp < rows) {
+    const uint8_t *src = x + (row0 + warp) * a.stride * kElt;
+    const int bytes = cols * kElt, whole = bytes & ~15;
+#pragma unroll 8
+    for (int c = 16 * lane; c < whole; c += 512) {
+      const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src + c));
+      *reinterpret_cast<uint4 *>(stage + warp * pitch + c) = u;
       if constexpr (kNv) {
-        uint32_t s0, s1;
+        const uint32_t q[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = bad ? 0.0f : __fmul_rn(v[i], back);
-        nv16<kBf16>(v, w, &s0);
-        nv16<kBf16>(v + 16, w + 2, &s1);
-        *reinterpret_cast<uint16_t *>(sc + 512 * ((p >> 1) & 1) + 2 * (p & 1)) = static_cast<uint16_t>(s0 | s1 << 8);
-      } else {
-        const uint32_t top32 = top_bits<32>(v);
-        uint32_t code = 0;
-        w[0] = w[1] = w[2] = w[3] = 0;
-        if (top32 >= 0x7F800000u) {
-          bad = 1;
-        } else if (top32 != 0) {
-          const int e = max(floor_log2f(__uint_as_float(top32)) - 2, -127);
-          const float inv = pow2f(-e);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(v[i], inv);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = e2m1x8(v + 8 * i);
-          code = static_cast<uint32_t>(e + 127);
-        }
-        sc[p & 3] = static_cast<uint8_t>(code);
+        for (int i = 0; i < 4; ++i)
+          m = kBf16 ? max(m, max(q[i] << 16 & 0x7FFF0000u, q[i] & 0x7FFF0000u)) : max(m, q[i] & 0x7FFFFFFFu);
       }
-      *reinterpret_cast<uint4 *>(rec + (p & 3) * 2048 + m * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // the last values, and zeros to the end of the last tile
+    for (int c = whole / kElt + lane; c < 32 * pieces; c += 32) {
+      if constexpr (kBf16) {
+        const uint16_t u = c < cols ? reinterpret_cast<const uint16_t *>(src)[c] : 0;
+        reinterpret_cast<uint16_t *>(stage + warp * pitch)[c] = u;
+        m = max(m, static_cast<uint32_t>(u & 0x7FFF) << 16);
+      } else {
+        const uint32_t u = c < cols ? reinterpret_cast<const uint32_t *>(src)[c] : 0;
+        reinterpret_cast<uint32_t *>(stage + warp * pitch)[c] = u;
+        m = max(m, u & 0x7FFFFFFFu);
+      }
+    }
+  } else if (kNv && !kStaged && row0 + warp < rows) {
+    const uint8_t *src = x + (row0 + warp) * a.stride * kElt;
+    for (int c = 32 * lane; c < cols; c += 1024) {
+      load32<kBf16>(src, c, cols, v);
+      m = max(m, top_bits<32>(v));
+    }
+  }
+  if constexpr (kNv) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) top[warp] = m;
+  }
+  if constexpr (kNv || kStaged) __syncthreads();
+  if constexpr (kNv) {
+    const int e = row_exponent(top[r8], bad);
+    back = bad ? 0.0f : pow2f(-e);
+    if (row < rows && t < 8) {
+      a.m.row_scales[row] = bad ? __uint_as_float(kNan) : pow2f(e);
+      if (bad) raise_err(a.err, CSA2_DEVERR_NAN);
+    }
+  }
+  const int mr = row % kF4Rows;
+  uint8_t *tiles = a.m.tiles + static_cast<int64_t>(row / kF4Rows) * ct * f4_tile_bytes(kNv);
+  if (row < rows) {
+    // two pieces a time: their scales (NV) are one word
+    for (int p = 2 * (t >> 3); p < pieces; p += 64) {
+      uint8_t *rec = tiles + static_cast<int64_t>(p >> 2) * f4_tile_bytes(kNv), *sc = rec + kF4CodeBytes + f4_scale_at(mr);
+      uint32_t code[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t w[4];
+        if constexpr (kStaged) load32<kBf16>(stage + r8 * pitch, 32 * (p + i), 32 * pieces, v);
+        else load32<kBf16>(x + row * a.stride * kElt, 32 * (p + i), cols, v);
+        code[i] = quant32<kNv, kBf16>(v, back, bad, w);
+        *reinterpret_cast<uint4 *>(rec + ((p + i) & 3) * 2048 + mr * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if constexpr (kNv) *reinterpret_cast<uint32_t *>(sc + 512 * ((p >> 1) & 1)) = code[0] | code[1] << 16;
+      else *reinterpret_cast<uint16_t *>(sc + (p & 3)) = static_cast<uint16_t>(code[0] | code[1] << 8);
     }
   }
   if constexpr (!kNv) {
+    __syncthreads();
     if (t < 8) top[t] = 0;
     __syncthreads();
-    if (bad) atomicOr(&top[kRows == 8 ? t & 7 : 0], 1u);
+    if (bad) atomicOr(&top[r8], 1u);
     __syncthreads();
-    if (row < rows && t < kRows) {
-      a.m.row_scales[row] = top[t] ? __uint_as_float(0x7FC00000u) : 1.0f;
+    if (row < rows && t < 8) {
+      a.m.row_scales[row] = top[t] ? __uint_as_float(kNan) : 1.0f;
       if (top[t]) raise_err(a.err, CSA2_DEVERR_NAN);
     }
   }
 }
 
-// A warp: 8 rows x 32 columns at a time (128 B of codes in, 64 B per row out).
+// A warp: 8 rows of a tile at a time (16 B of codes a lane, whole lines of 8 rows; 32
+// values a lane out).
 template <bool kNv, bool kBf16>
-__global__ void __launch_bounds__(256) k_fp4_read(csa2_fp4_matrix mx, void *out, int64_t stride) {
+__global__ void __launch_bounds__(256) k_fp4_read(csa2_fp4_matrix mx, void *out, int64_t stride, int wide) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int ct = static_cast<int>(f4_col_tiles(mx.cols)), pieces = (mx.cols + 31) / 32;
-  const int row = blockIdx.x * 8 + (lane >> 2), u = lane & 3;
+  const int ct = static_cast<int>(f4_col_tiles(mx.cols));
+  const int row = blockIdx.x * 8 + (lane & 7), j = lane >> 3;
   if (row >= mx.rows) return;
   const int m = row % kF4Rows;
   const float r = mx.row_scales[row];
-  const int64_t tile0 = static_cast<int64_t>(row / kF4Rows) * ct;
-  for (int p = blockIdx.y * 8 + warp; p < pieces; p += 8 * gridDim.y) {
-    const uint8_t *rec = mx.tiles + (tile0 + (p >> 2)) * f4_tile_bytes(kNv), *sc = rec + kF4CodeBytes + f4_scale_at(m);
-    const uint32_t w = *reinterpret_cast<const uint32_t *>(rec + (p & 3) * 2048 + m * 16 + 4 * u);
-    const float s = kNv ? e4m3_value(sc[512 * ((p >> 1) & 1) + 2 * (p & 1) + (u >> 1)]) * r : e8m0_value(sc[p & 3]) * r;
-    uint32_t h[4];
-    e2m1x8_h2(w, h);
-    float v[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h[i]));
-      v[2 * i] = f.x * s;
-      v[2 * i + 1] = f.y * s;
-    }
-    const int c = 32 * p + 8 * u;
-    const int64_t at = row * stride + c;
-    if (c + 8 <= mx.cols) {
-      if constexpr (kBf16) {
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-          o[i] = *reinterpret_cast<uint32_t *>(&b);
-        }
-        *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + at) = make_uint4(o[0], o[1], o[2], o[3]);
-      } else {
-        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(out) + at);
-        o[0] = make_float4(v[0], v[1], v[2], v[3]);
-        o[1] = make_float4(v[4], v[5], v[6], v[7]);
-      }
+  const uint8_t *tiles = mx.tiles + static_cast<int64_t>(row / kF4Rows) * ct * f4_tile_bytes(kNv);
+#pragma unroll 2
+  for (int k = blockIdx.y * 8 + warp; k < ct; k += 8 * gridDim.y) {
+    const uint8_t *rec = tiles + static_cast<int64_t>(k) * f4_tile_bytes(kNv), *sc = rec + kF4CodeBytes + f4_scale_at(m);
+    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(rec + j * 2048 + m * 16));
+    float s[2];
+    if constexpr (kNv) {
+      const uint32_t c = *reinterpret_cast<const uint16_t *>(sc + 512 * (j >> 1) + 2 * (j & 1));
+      s[0] = e4m3_value(c & 0xFF) * r;
+      s[1] = e4m3_value(c >> 8) * r;
     } else {
+      s[0] = s[1] = e8m0_value(sc[j]) * r;
+    }
+    const int c0 = kF4Cols * k + 32 * j;
+    const int64_t at = row * stride + c0;
+    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c + i < mx.cols) {
-          if constexpr (kBf16) static_cast<__nv_bfloat16 *>(out)[at + i] = __float2bfloat16_rn(v[i]);
-          else static_cast<float *>(out)[at + i] = v[i];
+    for (int half = 0; half < 2; ++half) {  // 16 values
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t h[4];
+        e2m1x8_h2(in[2 * half + i], h);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h[q]));
+          v[8 * i + 2 * q] = f.x * s[half];
+          v[8 * i + 2 * q + 1] = f.y * s[half];
         }
+      }
+      const int c = c0 + 16 * half;
+      if (c + 16 <= mx.cols) {
+        uint32_t o[16];
+        if constexpr (kBf16) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            o[i] = *reinterpret_cast<uint32_t *>(&b);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(v[i]);
+        }
+        uint32_t *dst = kBf16 ? reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(out) + at + 16 * half)
+                              : reinterpret_cast<uint32_t *>(static_cast<float *>(out) + at + 16 * half);
+#pragma unroll
+        for (int i = 0; i < (kBf16 ? 1 : 2); ++i) {
+          if (wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + 8 * i), "r"(o[8 * i]), "r"(o[8 * i + 1]),
+                         "r"(o[8 * i + 2]), "r"(o[8 * i + 3]), "r"(o[8 * i + 4]), "r"(o[8 * i + 5]), "r"(o[8 * i + 6]), "r"(o[8 * i + 7])
+                         : "memory");
+          } else {
+            reinterpret_cast<uint4 *>(dst + 8 * i)[0] = make_uint4(o[8 * i], o[8 * i + 1], o[8 * i + 2], o[8 * i + 3]);
+            reinterpret_cast<uint4 *>(dst + 8 * i)[1] = make_uint4(o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (c + i < mx.cols) {
+            if constexpr (kBf16) static_cast<__nv_bfloat16 *>(out)[at + 16 * half + i] = __float2bfloat16_rn(v[i]);
+            else static_cast<float *>(out)[at + 16 * half + i] = v[i];
+          }
+      }
     }
   }
 }
 
 }  // namespace
+
+// A block per row up to eight rows per SM (a block per 8 rows would leave SMs idle);
+// above, 8 rows a block, staged while two blocks fit an SM.
+template <bool kNv, bool kBf16>
+static cudaError_t launch_quant(const F4Args &a, cudaStream_t s) {
+  if (a.m.rows < 8 * device_sm_count()) {
+    k_fp4_quant_row<kNv, kBf16><<<a.m.rows, kQThreads, 0, s>>>(a);
+    return cudaGetLastError();
+  }
+  const int pitch = static_cast<int>(f4_col_tiles(a.m.cols)) * kF4Cols * (kBf16 ? 2 : 4) + 16, blocks = (a.m.rows + 7) / 8;
+  if (8 * pitch > 112 * 1024) {
+    k_fp4_quant_rows<kNv, kBf16, false><<<blocks, kQThreads, 0, s>>>(a, 0);
+    return cudaGetLastError();
+  }
+  const auto kern = k_fp4_quant_rows<kNv, kBf16, true>;
+  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), 8 * pitch);
+  if (e != cudaSuccess) return e;
+  kern<<<blocks, kQThreads, 8 * pitch, s>>>(a, pitch);
+  return cudaGetLastError();
+}
 
 csa2_status check_fp4(const csa2_fp4_matrix *m, const char *name) {
   CSA2_REQUIRE(m != nullptr, CSA2_ERR_NULL, "%s is NULL", name);
@@ -310,16 +440,11 @@ csa2_status csa2_fp4_quant(const csa2_fp4_matrix *m, const void *x, int64_t x_st
   if (m->rows == 0) return CSA2_OK;
   CSA2_REQUIRE_PTR(x);
   const csa2::F4Args a{*m, x, x_stride, err_word};
-  const bool nv = m->format == CSA2_FP4_NV, bf = in_dtype == CSA2_IN_BF16;
-  const bool many = m->rows >= 8 * csa2::device_sm_count();
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-#define CSA2_Q(NV, BF)                                                                               \
-  (many ? csa2::k_fp4_quant<NV, BF, 8><<<(m->rows + 7) / 8, csa2::kQThreads, 0, s>>>(a)              \
-        : csa2::k_fp4_quant<NV, BF, 1><<<m->rows, csa2::kQThreads, 0, s>>>(a))
-  if (nv) bf ? CSA2_Q(true, true) : CSA2_Q(true, false);
-  else bf ? CSA2_Q(false, true) : CSA2_Q(false, false);
-#undef CSA2_Q
-  return cuda_status(cudaGetLastError(), "csa2_fp4_quant launch");
+  const bool bf = in_dtype == CSA2_IN_BF16;
+  const cudaError_t e = m->format == CSA2_FP4_NV ? (bf ? csa2::launch_quant<true, true>(a, s) : csa2::launch_quant<true, false>(a, s))
+                                                 : (bf ? csa2::launch_quant<false, true>(a, s) : csa2::launch_quant<false, false>(a, s));
+  return cuda_status(e, "csa2_fp4_quant launch");
 }
 
 csa2_status csa2_fp4_read(const csa2_fp4_matrix *m, void *out, int64_t out_stride, int32_t out_dtype, csa2_stream_t stream) {
@@ -330,18 +455,19 @@ csa2_status csa2_fp4_read(const csa2_fp4_matrix *m, void *out, int64_t out_strid
                "out_stride %lld must be a multiple of 8, %d at least", static_cast<long long>(out_stride), m->cols);
   if (m->rows == 0) return CSA2_OK;
   CSA2_REQUIRE_PTR(out);
-  const int pieces = (m->cols + 31) / 32, row_blocks = (m->rows + 7) / 8;
-  int split = (4 * csa2::device_sm_count() + row_blocks - 1) / row_blocks;  // few rows: their pieces over more blocks
-  split = split < 1 ? 1 : split > (pieces + 7) / 8 ? (pieces + 7) / 8 : split;
+  const int ct = static_cast<int>(csa2::f4_col_tiles(m->cols)), row_blocks = (m->rows + 7) / 8;
+  int split = (4 * csa2::device_sm_count() + row_blocks - 1) / row_blocks;  // few rows: their tiles over more blocks
+  split = split < 1 ? 1 : split > (ct + 7) / 8 ? (ct + 7) / 8 : split;
+  const int wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && out_stride % (out_dtype == CSA2_OUT_BF16 ? 16 : 8) == 0;
   const dim3 grid(row_blocks, split);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = out_dtype == CSA2_OUT_BF16;
   if (m->format == CSA2_FP4_NV) {
-    if (bf) csa2::k_fp4_read<true, true><<<grid, 256, 0, s>>>(*m, out, out_stride);
-    else csa2::k_fp4_read<true, false><<<grid, 256, 0, s>>>(*m, out, out_stride);
+    if (bf) csa2::k_fp4_read<true, true><<<grid, 256, 0, s>>>(*m, out, out_stride, wide);
+    else csa2::k_fp4_read<true, false><<<grid, 256, 0, s>>>(*m, out, out_stride, wide);
   } else {
-    if (bf) csa2::k_fp4_read<false, true><<<grid, 256, 0, s>>>(*m, out, out_stride);
-    else csa2::k_fp4_read<false, false><<<grid, 256, 0, s>>>(*m, out, out_stride);
+    if (bf) csa2::k_fp4_read<false, true><<<grid, 256, 0, s>>>(*m, out, out_stride, wide);
+    else csa2::k_fp4_read<false, false><<<grid, 256, 0, s>>>(*m, out, out_stride, wide);
   }
   return cuda_status(cudaGetLastError(), "csa2_fp4_read launch");
 }

@@ -49,7 +49,7 @@ def _packed(x, fmt, err=None):
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 128), (3, 136), (17, 31), (130, 520), (129, 4104), (2000, 264), (1300, 2056)])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 128), (3, 136), (17, 31), (130, 520), (129, 4104), (2000, 264), (1300, 2056), (1217, 130), (1400, 6000), (1290, 17000)])
 def test_quant_is_the_definition(fmt, dtype, rows, cols):
     """Codes and scales as values, equal; read back in both types; strided rows; columns behind the
     last one of the tile are zeros."""
