@@ -41,34 +41,72 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
 }
 
-// Shared memory of a stage: codes of 128 weight rows, codes of NT tokens, both's scales.
+// A map over a matrix's records, seen as [row tile][K tile][pieces][piece bytes], whose box
+// is `pieces` pieces of k_tiles K tiles of row_tiles row tiles.
+bool record_map(CUtensorMap *map, const csa2_fp4_matrix &m, bool nv, int pieces, int k_tiles, int row_tiles) {
+  const uint64_t piece = nv ? 1024 : 512, rec = f4_tile_bytes(nv), kt = f4_col_tiles(m.cols);
+  const uint64_t dim[4] = {piece / 8, rec / piece, kt, static_cast<uint64_t>(f4_row_tiles(m.rows))};
+  const uint64_t stride[3] = {piece, rec, rec * kt};
+  const uint32_t box[4] = {static_cast<uint32_t>(piece / 8), static_cast<uint32_t>(pieces), static_cast<uint32_t>(k_tiles),
+                           static_cast<uint32_t>(row_tiles)};
+  return tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 4, m.tiles, dim, stride, box, false);
+}
+// A map over its codes, [row tile][K tile][32-column piece][row], whose box is the first nt
+// rows of a tile in k_tiles K tiles.
+bool token_map(CUtensorMap *map, const csa2_fp4_matrix &m, bool nv, int nt, int k_tiles) {
+  const uint64_t rec = f4_tile_bytes(nv), kt = f4_col_tiles(m.cols);
+  const uint64_t dim[4] = {2048 / 8, 4, kt, static_cast<uint64_t>(f4_row_tiles(m.rows))};
+  const uint64_t stride[3] = {2048, rec, rec * kt};
+  const uint32_t box[4] = {static_cast<uint32_t>(2 * nt), 4, static_cast<uint32_t>(k_tiles), 1};
+  return tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 4, m.tiles, dim, stride, box, false);
+}
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap *map, int c0, int c1, int c2, int c3, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(tc::smem_addr(bar))
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+  return e;
+}
+
+// Shared memory of a stage, kTiles K tiles: the weights' records (128 rows), the tokens'
+// codes and scales.  A copying thread takes about 0.2 us for a wait, an arming and a copy
+// of any size, so a stage is as large as two CTAs per SM allow.
 template <int NT, bool kNv>
 struct Split {
-  static constexpr int kRec = f4_tile_bytes(kNv), kB = NT * 64, kS = f4_scale_bytes(kNv);
-  static constexpr int kStage = kRec + kB + kS;
-  static constexpr int kStages = NT <= 32 ? 8 : NT <= 64 ? 7 : 5;  // two CTAs per SM
-  static constexpr int kAtoms = kNv ? 2 : 1;                       // 512 B of scales per operand
-  static constexpr int kSfCols = 8 * kAtoms;                       // TMEM columns of a stage's scales
-  static constexpr int kCols = NT + kSfCols * kStages <= 128 ? 128 : 256;
-  static constexpr int kPitch = 128 + 4;                           // floats per token of the partial sums
-  static constexpr int kBytes = kStage * kStages > NT * kPitch * 4 ? kStage * kStages : NT * kPitch * 4;
+  static constexpr int kTiles = NT <= 32 ? 4 : 2, kStages = NT <= 32 ? 2 : 3;
+  static constexpr int kRec = f4_tile_bytes(kNv), kS = f4_scale_bytes(kNv);
+  static constexpr int kA = kTiles * kRec, kB = kTiles * NT * 64;
+  static constexpr int kStage = kA + kB + kTiles * kS;
+  static constexpr int kAtoms = kNv ? 2 : 1;    // 512 B of scales per operand and K tile
+  static constexpr int kSfCols = 8 * kAtoms;    // TMEM columns of a K tile's scales
+  static constexpr int kCols = NT + kSfCols * kTiles * kStages <= 128 ? 128 : 256;
+  static constexpr int kPitch = 128 + 4;        // floats per token of the partial sums
+  static constexpr int kBytes = (kStage * kStages > NT * kPitch * 4 ? kStage * kStages : NT * kPitch * 4) + 1024;
 };
 
 template <int NT, bool kNv, bool kBf16>
-__global__ void __launch_bounds__(kSplitThreads) k_fp4_split(ProductArgs a) {
+__global__ void __launch_bounds__(kSplitThreads)
+    k_fp4_split(ProductArgs a, const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
+                const __grid_constant__ CUtensorMap ms) {
   using L = Split<NT, kNv>;
-  extern __shared__ __align__(1024) uint8_t smem[];
+  extern __shared__ uint8_t raw[];
   __shared__ __align__(8) uint64_t full[L::kStages], empty[L::kStages], done;
   __shared__ uint32_t tmem_at;
-  __shared__ int loaded;  // K tiles whose copies were started
+  __shared__ int loaded;  // stages whose copies were started
+  const uint32_t s0 = (tc::smem_addr(raw) + 1023) & ~1023u;
+  uint8_t *smem = raw + (s0 - tc::smem_addr(raw));
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   uint32_t rank, ranks;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
   asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(ranks));
   const int nt = blockIdx.x / ranks, m0 = blockIdx.y * NT;
-  const int kt = static_cast<int>(f4_col_tiles(a.x.cols));
-  const int k0 = kt * static_cast<int>(rank) / static_cast<int>(ranks), k1 = kt * static_cast<int>(rank + 1) / static_cast<int>(ranks);
-  const int nk = k1 - k0;
+  const int kt = static_cast<int>(f4_col_tiles(a.x.cols)), steps = (kt + L::kTiles - 1) / L::kTiles;
+  const int k0 = steps * static_cast<int>(rank) / static_cast<int>(ranks);
+  const int nk = steps * static_cast<int>(rank + 1) / static_cast<int>(ranks) - k0;
   if (warp == 1) {
     tc::tmem_alloc(&tmem_at, L::kCols);
     tc::tmem_relinquish();
@@ -85,52 +123,52 @@ __global__ void __launch_bounds__(kSplitThreads) k_fp4_split(ProductArgs a) {
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
-  const uint32_t tmem = tmem_at, s0 = tc::smem_addr(smem);
+  const uint32_t tmem = tmem_at;
 
   if (warp == 0 && lane == 0) {
-    const uint8_t *wp = a.w.tiles + (static_cast<int64_t>(nt) * kt + k0) * L::kRec;
-    const uint8_t *xp = a.x.tiles + (static_cast<int64_t>(m0 / kF4Rows) * kt + k0) * L::kRec;
-    for (int i = 0; i < nk; ++i, wp += L::kRec, xp += L::kRec) {
+    for (int i = 0; i < nk; ++i) {
       const int st = i % L::kStages;
       if (i >= L::kStages && !tc::mbar_wait_bounded(&empty[st], ((i / L::kStages) - 1) & 1, kWaitIters)) break;
-      const uint32_t sa = s0 + st * L::kStage, sb = sa + L::kRec;
+      const uint32_t sa = s0 + st * L::kStage;
+      const int k = (k0 + i) * L::kTiles;
       tc::mbar_expect_tx(&full[st], L::kStage);
-      tc::bulk_load(sa, wp, L::kRec, &full[st]);
-      if constexpr (NT == 128) {
-        tc::bulk_load(sb, xp, L::kRec, &full[st]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) tc::bulk_load(sb + j * NT * 16, xp + j * 2048, NT * 16, &full[st]);
-        tc::bulk_load(sb + L::kB, xp + kF4CodeBytes, L::kS, &full[st]);
-      }
+      box_load(sa, &mw, 0, 0, k, nt, &full[st]);
+      box_load(sa + L::kA, &mx, 0, 0, k, m0 / kF4Rows, &full[st]);
+      box_load(sa + L::kA + L::kB, &ms, 0, kNv ? 8 : 16, k, m0 / kF4Rows, &full[st]);
       loaded = i + 1;
     }
-  } else if (warp == 1 && lane == 0) {
+  } else if (warp == 1) {
+    const uint32_t el = elect_one();
     bool ok = true;
     for (int i = 0; i < nk && ok; ++i) {
       const int st = i % L::kStages;
-      ok = tc::mbar_wait_bounded(&full[st], (i / L::kStages) & 1, kWaitIters);
+      ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&full[st], (i / L::kStages) & 1, kWaitIters));
       if (!ok) break;
       tc::tc_fence_after();
-      const uint32_t sa = s0 + st * L::kStage, sb = sa + L::kRec;
-      // a stage's scale columns are written again only once its MMAs, whose end
-      // let the stage be refilled, are done
-      const uint32_t sf = tmem + NT + st * L::kSfCols;
+      if (el) {
 #pragma unroll
-      for (int h = 0; h < L::kAtoms; ++h) {
-        tc::tmem_cp_32x128b_x4(sf + 4 * h, tc::smem_desc_noswizzle(sa + kF4CodeBytes + 512 * h, 128, 128));
-        tc::tmem_cp_32x128b_x4(sf + 4 * (L::kAtoms + h), tc::smem_desc_noswizzle(sb + L::kB + 512 * h, 128, 128));
-      }
+        for (int u = 0; u < L::kTiles; ++u) {
+          const uint32_t sa = s0 + st * L::kStage + u * L::kRec, sb = s0 + st * L::kStage + L::kA + u * NT * 64;
+          const uint32_t ss = s0 + st * L::kStage + L::kA + L::kB + u * L::kS;
+          // a stage's scale columns are written again only once its MMAs, whose end
+          // let the stage be refilled, are done
+          const uint32_t sf = tmem + NT + (st * L::kTiles + u) * L::kSfCols;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t sfa = sf + (kNv ? 4 * h : 0), sfb = sf + (kNv ? 8 + 4 * h : 4);
-        tc::mma_f4<kNv>(tmem, tc::smem_desc_noswizzle(sa + 4096 * h, 2048, 128),
-                        tc::smem_desc_noswizzle(sb + 2 * NT * 16 * h, NT * 16, 128), tc::idesc_f4(kNv, NT, kNv ? 0 : 2 * h), sfa,
-                        sfb, i + h > 0 ? 1u : 0u);
+          for (int h = 0; h < L::kAtoms; ++h) {
+            tc::tmem_cp_32x128b_x4(sf + 4 * h, tc::smem_desc_noswizzle(sa + kF4CodeBytes + 512 * h, 128, 128));
+            tc::tmem_cp_32x128b_x4(sf + 4 * (L::kAtoms + h), tc::smem_desc_noswizzle(ss + 512 * h, 128, 128));
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            tc::mma_f4<kNv>(tmem, tc::smem_desc_noswizzle(sa + 4096 * h, 2048, 128),
+                            tc::smem_desc_noswizzle(sb + 2 * NT * 16 * h, NT * 16, 128), tc::idesc_f4(kNv, NT, kNv ? 0 : 2 * h),
+                            sf + (kNv ? 4 * h : 0), sf + (kNv ? 8 + 4 * h : 4), i + u + h > 0 ? 1u : 0u);
+        }
+        tc::mma_commit(&empty[st]);
+        if (i == nk - 1) tc::mma_commit(&done);
       }
-      tc::mma_commit(&empty[st]);
+      __syncwarp();
     }
-    if (ok) tc::mma_commit(&done);
   }
   __syncwarp();
   // every warp waits for the sums (each observes the phase itself)
@@ -284,11 +322,6 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
         "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(acc)
         : "memory");
   }
-}
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t e;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
-  return e;
 }
 
 template <bool kNv, bool kBf16>
@@ -498,16 +531,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   }
 }
 
-// A map over a matrix's records, seen as [row tile][K tile][pieces][piece bytes], whose box
-// is `pieces` pieces of two K tiles of `row_tiles` row tiles.
-bool record_map(CUtensorMap *map, const csa2_fp4_matrix &m, bool nv, int pieces, int row_tiles) {
-  const uint64_t piece = nv ? 1024 : 512, rec = f4_tile_bytes(nv), kt = f4_col_tiles(m.cols);
-  const uint64_t dim[4] = {piece / 8, rec / piece, kt, static_cast<uint64_t>(f4_row_tiles(m.rows))};
-  const uint64_t stride[3] = {piece, rec, rec * kt};
-  const uint32_t box[4] = {static_cast<uint32_t>(piece / 8), static_cast<uint32_t>(pieces), 2, static_cast<uint32_t>(row_tiles)};
-  return tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 4, m.tiles, dim, stride, box, false);
-}
-
 template <bool kNv, bool kBf16>
 cudaError_t launch_pair(const ProductArgs &a, cudaStream_t s) {
   using L = Pair<kNv>;
@@ -516,7 +539,7 @@ cudaError_t launch_pair(const ProductArgs &a, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   CUtensorMap mx, mw, ms;
   constexpr int kCodes = kNv ? 8 : 16;  // pieces of a record that are codes; one more is the scales
-  if (!record_map(&mx, a.x, kNv, kCodes + 1, 1) || !record_map(&mw, a.w, kNv, kCodes, 1) || !record_map(&ms, a.w, kNv, 1, 2))
+  if (!record_map(&mx, a.x, kNv, kCodes + 1, 2, 1) || !record_map(&mw, a.w, kNv, kCodes, 2, 1) || !record_map(&ms, a.w, kNv, 1, 2, 2))
     return cudaErrorNotSupported;
   const int mt = static_cast<int>(f4_row_tiles(a.x.rows)), nt = (a.w.rows + kPairN - 1) / kPairN;
   const int64_t tiles = static_cast<int64_t>((mt + 1) / 2) * nt, most = device_sm_count() / 2;
@@ -528,9 +551,14 @@ cudaError_t launch_pair(const ProductArgs &a, cudaStream_t s) {
 template <int NT, bool kNv, bool kBf16>
 cudaError_t launch_split(const ProductArgs &a, int ranks, cudaStream_t s) {
   using L = Split<NT, kNv>;
-  const void *fn = reinterpret_cast<const void *>(k_fp4_split<NT, kNv, kBf16>);
-  cudaError_t e = ensure_smem_limit(fn, L::kBytes);
+  const auto kern = k_fp4_split<NT, kNv, kBf16>;
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), L::kBytes);
   if (e != cudaSuccess) return e;
+  CUtensorMap mw, mx, ms;
+  constexpr int kCodes = kNv ? 8 : 16;
+  if (!record_map(&mw, a.w, kNv, kCodes + 1, L::kTiles, 1) || !token_map(&mx, a.x, kNv, NT, L::kTiles) ||
+      !record_map(&ms, a.x, kNv, 1, L::kTiles, 1))
+    return cudaErrorNotSupported;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(f4_row_tiles(a.w.rows) * ranks), static_cast<unsigned>((a.x.rows + NT - 1) / NT));
   cfg.blockDim = dim3(kSplitThreads);
@@ -542,7 +570,7 @@ cudaError_t launch_split(const ProductArgs &a, int ranks, cudaStream_t s) {
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_fp4_split<NT, kNv, kBf16>, a);
+  return cudaLaunchKernelEx(&cfg, kern, a, mw, mx, ms);
 }
 template <bool kNv, bool kBf16>
 cudaError_t launch_product(const ProductArgs &a, cudaStream_t s) {
@@ -551,9 +579,9 @@ cudaError_t launch_product(const ProductArgs &a, cudaStream_t s) {
   if (4 * 2 * big >= 3 * device_sm_count()) return launch_pair<kNv, kBf16>(a, s);
   const int nt = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
   const int64_t tiles = f4_row_tiles(a.w.rows) * ((m + nt - 1) / nt);
-  const int64_t kt = f4_col_tiles(a.x.cols), sms = device_sm_count();
+  const int64_t steps = (f4_col_tiles(a.x.cols) + (nt <= 32 ? 3 : 1)) / (nt <= 32 ? 4 : 2), sms = device_sm_count();
   int ranks = 1;
-  while (ranks < 8 && tiles * ranks * 2 <= 2 * sms && kt >= 4 * ranks) ranks *= 2;
+  while (ranks < 8 && tiles * ranks * 2 <= 2 * sms && steps >= 2 * ranks) ranks *= 2;
   switch (nt) {
     case 16: return launch_split<16, kNv, kBf16>(a, ranks, s);
     case 32: return launch_split<32, kNv, kBf16>(a, ranks, s);
