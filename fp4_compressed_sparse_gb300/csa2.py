@@ -265,6 +265,9 @@ class Cache:
     def ref(self):
         return ctypes.byref(self.struct)
 
+    def address(self):
+        return ctypes.addressof(self.struct)
+
     def _rows(self):
         """Physical entry row of every (sequence, entry) of a paged cache: [B, cap] int64."""
         pe = self.page_entries
@@ -497,20 +500,56 @@ _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.curre
 
 def _call(fn, cache, dev, stream, *args):
     """fn(cache, *args, stream) with the cache's device as the current one, on its current stream unless one is given."""
-    _call_on(fn, dev, stream, cache.ref(), *args)
-
-
-def _call_on(fn, dev, stream, *args):
-    """fn(*args, stream) with device dev as the current one, on its current stream unless one is given."""
     f = getattr(_lib or load(), fn)
     s = stream.cuda_stream if stream is not None else _raw_stream(dev)
+    if dev == _current_device():
+        status = f(cache.ref(), *args, s)
+    else:
+        with torch.cuda.device(dev):
+            status = f(cache.ref(), *args, s)
+    if status != OK:
+        _check(fn, status)
+
+
+# The same with fewer reads per call, for the calls that take microseconds themselves: a
+# tensor is read once, and looked at again (for the reason) only when something is off.
+def _submit(fn, dev, stream, *args):
+    """fn(*args, stream) with device dev as the current one, on its current stream unless one is given."""
+    f = getattr(_lib or load(), fn)
+    s = _raw_stream(dev) if stream is None else stream.cuda_stream
     if dev == _current_device():
         status = f(*args, s)
     else:
         with torch.cuda.device(dev):
             status = f(*args, s)
-    if status != OK:
+    if status:
         _check(fn, status)
+
+
+def _err_at(err, dev):
+    if err is None:
+        return None
+    if err.get_device() == dev and err.dtype is torch.int32 and err.numel():
+        return err.data_ptr()
+    return _err_word(err, dev)
+
+
+def _list_at(name, t, n, dev, dtype=torch.int32):
+    """The address of a list of n numbers (None: none); ValueError unless it is one on device dev."""
+    if t is None:
+        return None
+    if t.get_device() != dev or t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+        _want(name, t, dtype, (n,), dev)
+    return t.data_ptr()
+
+
+def _rows_at(name, t, dtypes, rows, width, dev):
+    """The row stride of rows of `width` elements, as _want_rows; a single row gets the least one."""
+    shape, stride = t.shape, t.stride()
+    if t.get_device() == dev and t.dtype in dtypes and shape == (rows, width) and stride[1] == 1 and stride[0] >= width:
+        return stride[0] if rows > 1 else -(-width // 8) * 8
+    stride = _want_rows(name, t, dtypes, width, dev, rows)
+    return stride if rows > 1 else -(-width // 8) * 8
 
 
 class ChunkWindow:
@@ -662,7 +701,9 @@ class PagePool:
         _want("n_free", n_free, torch.int32, (1,), dev)
         _want("held", held, torch.int32, (cache.batch,), dev)
         self.free, self.n_free, self.held = free, n_free, held
+        self.sizes = (dev, cache.n_pages, cache.batch)
         self.struct = PoolStruct(free.data_ptr(), n_free.data_ptr(), held.data_ptr())
+        self.address = ctypes.addressof(self.struct)
 
 
 def pages_resize(cache: Cache, pool: PagePool, target=None, cu_new=None, total=None, max_new=None, granted=None, err=None,
@@ -670,52 +711,51 @@ def pages_resize(cache: Cache, pool: PagePool, target=None, cu_new=None, total=N
     """csa2_pages_resize: every sequence's pages for target[b] tokens (int64 [B]), or for its n_tokens plus
     the rows cu_new (int32 [B+1]) gives it.  total, max_new: bounds on all rows and on one sequence's
     (default: 2^24, no bound).  granted: int32 [B], 1 where a sequence holds what it needs."""
-    dev = _device(cache)
+    dev, B = _device(cache), cache.batch
     if cache.block_table is None:
         raise ValueError("a dense cache has no pages")
-    _want("pool.free", pool.free, torch.int32, (cache.n_pages,), dev)
-    _want("pool.held", pool.held, torch.int32, (cache.batch,), dev)
+    if pool.sizes != (dev, cache.n_pages, B):
+        raise ValueError(f"the pool is of (device, pages, sequences) {pool.sizes}, the cache of {(dev, cache.n_pages, B)}")
     if target is not None:
-        _want("target", target, torch.int64, (cache.batch,), dev)
-    if cu_new is not None:
-        _want("cu_new", cu_new, torch.int32, (cache.batch + 1,), dev)
-    if granted is not None:
-        _want("granted", granted, torch.int32, (cache.batch,), dev)
+        _want("target", target, torch.int64, (B,), dev)
     total = 1 << 24 if total is None else total
-    _call("csa2_pages_resize", cache, dev, stream, ctypes.byref(pool.struct), _adr(target), _adr(cu_new), total,
-          total if max_new is None else max_new, _adr(granted), _err_word(err, dev))
+    _submit("csa2_pages_resize", dev, stream, cache.address(), pool.address, target.data_ptr() if target is not None else None,
+            _list_at("cu_new", cu_new, B + 1, dev), total, total if max_new is None else max_new, _list_at("granted", granted, B, dev),
+            _err_at(err, dev))
 
 
 def slot_map(cache: Cache, cu_new, slots=None, pos=None, max_new=None, err=None, stream=None):
     """csa2_slot_map: slots and / or pos, int64 [total]: where each new token's entry will lie, and its position."""
     dev = _device(cache)
-    _want("cu_new", cu_new, torch.int32, (cache.batch + 1,), dev)
+    if cu_new is None:
+        raise ValueError("cu_new is needed")
     first = slots if slots is not None else pos
     if first is None:
         raise ValueError("slots or pos is needed")
     total = first.numel()
-    for name, t in (("slots", slots), ("pos", pos)):
-        if t is not None:
-            _want(name, t, torch.int64, (total,), dev)
-    ew = _err_word(err, dev)
+    at = _list_at("slots", slots, total, dev, torch.int64), _list_at("pos", pos, total, dev, torch.int64)
+    cu, ew = _list_at("cu_new", cu_new, cache.batch + 1, dev), _err_at(err, dev)
     if total == 0:
         return
-    _call("csa2_slot_map", cache, dev, stream, _adr(cu_new), total, total if max_new is None else max_new, _adr(slots),
-          _adr(pos), ew)
+    _submit("csa2_slot_map", dev, stream, cache.address(), cu, total, total if max_new is None else max_new, *at, ew)
 
 
 # --------------------------------------------------------------------------- into and out of the latent space
-def _want_heads(name, w, dev):
-    """Raise ValueError unless w is bf16 [heads, dim, 512] on device dev, contiguous within a head; returns (heads, dim, stride)."""
-    if w is None or w.get_device() != dev:
-        raise ValueError(f"{name}: a tensor on cuda:{dev} is needed")
-    if w.dtype is not torch.bfloat16 or w.dim() != 3 or w.shape[2] != D_LATENT:
-        raise ValueError(f"{name}: {w.dtype} {tuple(w.shape)}, bfloat16 (heads, dim, {D_LATENT}) is needed")
-    H, dim, _ = w.shape
-    s = w.stride()
-    if s[2] != 1 or (dim > 1 and s[1] != D_LATENT) or (H > 1 and s[0] < dim * D_LATENT):
+_BF16 = (torch.bfloat16,)
+
+
+def _heads_at(name, w, dev):
+    """(heads, dim, elements between heads) of bf16 weights [heads, dim, 512] on device dev, contiguous within a head."""
+    shape = w.shape
+    if w.get_device() != dev or dev < 0:
+        raise ValueError(f"{name}: on {w.device}, a tensor on the output's device is needed")
+    if w.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != D_LATENT:
+        raise ValueError(f"{name}: {w.dtype} {tuple(shape)}, bfloat16 (heads, dim, {D_LATENT}) is needed")
+    H, dim, _ = shape
+    head, row, one = w.stride()
+    if one != 1 or (dim > 1 and row != D_LATENT) or (H > 1 and head < dim * D_LATENT):
         raise ValueError(f"{name}: a head's rows must be contiguous, and heads must not overlap")
-    return H, dim, s[0] if H > 1 else dim * D_LATENT
+    return H, dim, head if H > 1 else dim * D_LATENT
 
 
 def query_latent(q, w_uk, pos, rope_cs, out, err=None, stream=None):
@@ -723,34 +763,34 @@ def query_latent(q, w_uk, pos, rope_cs, out, err=None, stream=None):
     be strided), pos int64 [total] -> out bf16 [total, H, 576]: the absorbed queries with rotated RoPE dims.
     Rows with a negative position are left as they were."""
     dev = out.get_device()
-    H, dim, ws = _want_heads("w_uk", w_uk, dev)
+    H, dim, ws = _heads_at("w_uk", w_uk, dev)
     total = out.shape[0]
-    _want("out", out, torch.bfloat16, (total, H, D_QK), dev if dev >= 0 else None)
-    qs = _want_rows("q", q, (torch.bfloat16,), H * (dim + D_ROPE), dev, total)
-    _want("pos", pos, torch.int64, (total,), dev)
-    _want("rope_cs", rope_cs, torch.float32, None, dev)
-    if rope_cs.dim() < 2 or rope_cs.numel() != 64 * rope_cs.shape[0]:
-        raise ValueError(f"rope_cs: shape {tuple(rope_cs.shape)}, (positions, 32, 2) is needed")
-    ew = _err_word(err, dev)
-    if total == 0:
-        return
-    _call_on("csa2_query_latent", dev, stream, _adr(q), qs, total, H, dim, _adr(w_uk), ws, _adr(pos), _adr(rope_cs),
-             rope_cs.shape[0], _adr(out), ew)
+    if out.dtype is not torch.bfloat16 or out.shape != (total, H, D_QK) or not out.is_contiguous():
+        _want("out", out, torch.bfloat16, (total, H, D_QK), dev)
+    qs = _rows_at("q", q, _BF16, total, H * (dim + D_ROPE), dev)
+    at = _list_at("pos", pos, total, dev, torch.int64)
+    n = rope_cs.shape[0]
+    if rope_cs.get_device() != dev or rope_cs.dtype is not torch.float32 or rope_cs.numel() != 64 * n or rope_cs.dim() < 2 or not rope_cs.is_contiguous():
+        _want("rope_cs", rope_cs, torch.float32, (n, D_ROPE // 2, 2), dev)
+    ew = _err_at(err, dev)
+    if total:
+        _submit("csa2_query_latent", dev, stream, q.data_ptr(), qs, total, H, dim, w_uk.data_ptr(), ws, at, rope_cs.data_ptr(), n,
+                out.data_ptr(), ew)
 
 
 def value_project(o, w_uv, out, err=None, stream=None):
     """csa2_value_project: o [total, H, 512] (fp32 or bf16, contiguous), w_uv bf16 [H, dim, 512] (heads may be
     strided) -> out bf16 [total, H*dim] (rows may be strided)."""
     dev = out.get_device()
-    H, dim, ws = _want_heads("w_uv", w_uv, dev)
-    total = out.shape[0]
-    os_ = _want_rows("out", out, (torch.bfloat16,), H * dim, dev, total)
-    _want("o", o, _FLOATS, (total, H, D_LATENT), dev if dev >= 0 else None)
-    ew = _err_word(err, dev)
-    if total == 0:
-        return
-    _call_on("csa2_value_project", dev, stream, _adr(o), H * D_LATENT, IN_BF16 if o.dtype is torch.bfloat16 else IN_F32, total,
-             H, dim, _adr(w_uv), ws, _adr(out), os_, ew)
+    H, dim, ws = _heads_at("w_uv", w_uv, dev)
+    total, dt = out.shape[0], o.dtype
+    os_ = _rows_at("out", out, _BF16, total, H * dim, dev)
+    if o.get_device() != dev or dt not in _FLOATS or o.shape != (total, H, D_LATENT) or not o.is_contiguous():
+        _want("o", o, _FLOATS, (total, H, D_LATENT), dev)
+    ew = _err_at(err, dev)
+    if total:
+        _submit("csa2_value_project", dev, stream, o.data_ptr(), H * D_LATENT, IN_BF16 if dt is torch.bfloat16 else IN_F32, total,
+                H, dim, w_uv.data_ptr(), ws, out.data_ptr(), os_, ew)
 
 
 # --------------------------------------------------------------------------- 4-bit matrices
@@ -767,9 +807,7 @@ class Fp4Matrix:
         self.tiles = torch.empty(nb[0], dtype=torch.uint8, device=device)
         self.row_scales = torch.empty(nb[1] // 4, dtype=torch.float32, device=device)
         self.struct = Fp4Struct(rows, cols, fmt, self.tiles.data_ptr(), self.row_scales.data_ptr())
-
-    def ref(self):
-        return ctypes.byref(self.struct)
+        self.address = ctypes.addressof(self.struct)
 
 
 def _fp4_device(m):
@@ -782,38 +820,27 @@ def _fp4_device(m):
 def fp4_quant(m: Fp4Matrix, x, err=None, stream=None):
     """csa2_fp4_quant: x [rows, cols] (fp32 or bf16, rows may be strided) into m."""
     dev = _fp4_device(m)
-    stride = _want_rows("x", x, _FLOATS, m.cols, dev, m.rows)
-    ew = _err_word(err, dev)
-    if m.rows == 0:
-        return
-    if m.rows == 1:  # (a single row: any stride that the rows could have)
-        stride = -(-m.cols // 8) * 8
-    _call_on("csa2_fp4_quant", dev, stream, m.ref(), _adr(x), stride, IN_BF16 if x.dtype is torch.bfloat16 else IN_F32, ew)
+    stride, ew = _rows_at("x", x, _FLOATS, m.rows, m.cols, dev), _err_at(err, dev)
+    if m.rows:
+        _submit("csa2_fp4_quant", dev, stream, m.address, x.data_ptr(), stride, IN_BF16 if x.dtype is torch.bfloat16 else IN_F32, ew)
 
 
 def fp4_read(m: Fp4Matrix, out, stream=None):
     """csa2_fp4_read: the values m stands for into out [rows, cols] (fp32 or bf16, rows may be strided)."""
     dev = _fp4_device(m)
-    stride = _want_rows("out", out, _FLOATS, m.cols, dev, m.rows)
-    if m.rows == 0:
-        return
-    if m.rows == 1:
-        stride = -(-m.cols // 8) * 8
-    _call_on("csa2_fp4_read", dev, stream, m.ref(), _adr(out), stride, _out_dtype(out))
+    stride = _rows_at("out", out, _FLOATS, m.rows, m.cols, dev)
+    if m.rows:
+        _submit("csa2_fp4_read", dev, stream, m.address, out.data_ptr(), stride, _out_dtype(out))
 
 
 def fp4_product(x: Fp4Matrix, w: Fp4Matrix, out, err=None, stream=None):
     """csa2_fp4_product: out [x.rows, w.rows] = x w^T (fp32 or bf16, rows may be strided)."""
     dev = _fp4_device(x)
-    if _fp4_device(w) != dev:
+    if w.tiles.get_device() != dev:
         raise ValueError(f"w is on {w.tiles.device}, x on cuda:{dev}")
-    stride = _want_rows("out", out, _FLOATS, w.rows, dev, x.rows)
-    ew = _err_word(err, dev)
-    if x.rows == 0 or w.rows == 0:
-        return
-    if x.rows == 1:
-        stride = -(-w.rows // 8) * 8
-    _call_on("csa2_fp4_product", dev, stream, x.ref(), w.ref(), _adr(out), stride, _out_dtype(out), ew)
+    stride, ew = _rows_at("out", out, _FLOATS, x.rows, w.rows, dev), _err_at(err, dev)
+    if x.rows and w.rows:
+        _submit("csa2_fp4_product", dev, stream, x.address, w.address, out.data_ptr(), stride, _out_dtype(out), ew)
 
 
 # --------------------------------------------------------------------------- measurement helpers

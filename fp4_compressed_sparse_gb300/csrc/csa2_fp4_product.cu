@@ -210,14 +210,18 @@ __global__ void __launch_bounds__(kSplitThreads)
   for (int i = t; i < (c_hi - c_lo) * 32; i += kSplitThreads) {
     const int c = c_lo + i / 32, n = 4 * (i % 32), m = m0 + c, gn = nt * kF4Rows + n;
     if (m >= a.x.rows || gn >= n_out) continue;
-    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (uint32_t k = 0; k < ranks; ++k) {
-      const float4 v = ld_cluster4(map_rank(tc::smem_addr(part + c * L::kPitch + n), k));
-      s.x += v.x;
-      s.y += v.y;
-      s.z += v.z;
-      s.w += v.w;
-    }
+    float4 v[8], s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k)
+      if (k < ranks) v[k] = ld_cluster4(map_rank(tc::smem_addr(part + c * L::kPitch + n), k));
+#pragma unroll
+    for (uint32_t k = 0; k < 8; ++k)
+      if (k < ranks) {
+        s.x += v[k].x;
+        s.y += v[k].y;
+        s.z += v[k].z;
+        s.w += v[k].w;
+      }
     const float rm = a.x.row_scales[m];
     const float4 rn = *reinterpret_cast<const float4 *>(a.w.row_scales + gn);  // (the plane holds whole tiles of rows)
     s.x *= rm * rn.x;
