@@ -82,7 +82,9 @@ __device__ __forceinline__ uint32_t top_bits(const float *v) {
   return t;
 }
 // Eight values to eight E2M1 codes (low nibble first), RNE, saturating: the conversion
-// instruction takes two values, the first argument into the high nibble.
+// instruction takes two values, the first argument into the high nibble.  Called outside
+// of branches and its result chosen afterwards: with a call inside a branch the compiler
+// (CUDA 13.0) gave all four conversions the same values.
 __device__ __forceinline__ uint32_t e2m1x8(const float *y) {
   uint32_t r;
   asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
@@ -92,6 +94,30 @@ __device__ __forceinline__ uint32_t e2m1x8(const float *y) {
   return r;
 }
 
+// Eight values y of a group with scale s to eight codes (see the file's head); zeros if s is 0.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t nv8(const float *y, float s) {
+  if constexpr (kBf16) {
+    const float inv = __frcp_rn(s);
+    float q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = __uint_as_float((__float_as_uint(__fmul_rn(y[i], inv)) + 0x400u) & ~0x7FFu);
+    const uint32_t w = e2m1x8(q);
+    return s != 0.0f ? w : 0u;
+  } else {
+    const float t0 = 0.25f * s, t1 = 0.75f * s, t2 = 1.25f * s, t3 = 1.75f * s, t4 = 2.5f * s, t5 = 3.5f * s, t6 = 5.0f * s;
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float a = fabsf(y[i]);
+      uint32_t c = (a > t0) + (a >= t1) + (a > t2) + (a >= t3) + (a > t4) + (a >= t5) + (a > t6);
+      c |= (__float_as_uint(y[i]) >> 28) & 8u;
+      w |= c << (4 * i);
+    }
+    return s != 0.0f ? w : 0u;
+  }
+}
+
 // 16 values y (already divided by the row's power of two) into two words and an E4M3 scale.
 template <bool kBf16>
 __device__ __forceinline__ void nv16(const float *y, uint32_t *w, uint32_t *sc) {
@@ -99,25 +125,8 @@ __device__ __forceinline__ void nv16(const float *y, uint32_t *w, uint32_t *sc) 
   const uint32_t code = e4m3_code(__fdiv_rn(amax, 6.0f));
   const float s = e4m3_value(code);
   *sc = code;
-  w[0] = w[1] = 0;
-  if (code == 0) return;
-  if constexpr (kBf16) {
-    const float inv = __frcp_rn(s);
-    float q[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = __uint_as_float((__float_as_uint(__fmul_rn(y[i], inv)) + 0x400u) & ~0x7FFu);
-    w[0] = e2m1x8(q);
-    w[1] = e2m1x8(q + 8);
-  } else {
-    const float t0 = 0.25f * s, t1 = 0.75f * s, t2 = 1.25f * s, t3 = 1.75f * s, t4 = 2.5f * s, t5 = 3.5f * s, t6 = 5.0f * s;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float a = fabsf(y[i]);
-      uint32_t c = (a > t0) + (a >= t1) + (a > t2) + (a >= t3) + (a > t4) + (a >= t5) + (a > t6);
-      c |= (__float_as_uint(y[i]) >> 28) & 8u;
-      w[i >> 3] |= c << (4 * (i & 7));
-    }
-  }
+  w[0] = nv8<kBf16>(y, s);
+  w[1] = nv8<kBf16>(y + 8, s);
 }
 
 // A row's power of two from its largest magnitude's bits: the exponent, and whether the
@@ -143,61 +152,129 @@ __device__ __forceinline__ uint32_t quant32(float *v, float back, uint32_t &bad,
     nv16<kBf16>(v + 16, w + 2, &s1);
     return s0 | s1 << 8;
   } else {
-    const uint32_t top32 = top_bits<32>(v);
-    w[0] = w[1] = w[2] = w[3] = 0;
-    if (top32 >= 0x7F800000u) bad = 1;
-    if (top32 == 0 || top32 >= 0x7F800000u) return 0;
-    const int e = max(floor_log2f(__uint_as_float(top32)) - 2, -127);
+    const uint32_t g = top_bits<32>(v);
+    bad |= g >= 0x7F800000u;
+    const bool some = g != 0 && g < 0x7F800000u;
+    const int e = some ? max(floor_log2f(__uint_as_float(g)) - 2, -127) : 0;
     const float inv = pow2f(-e);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __fmul_rn(v[i], inv);
+    for (int i = 0; i < 32; ++i) v[i] = some ? __fmul_rn(v[i], inv) : 0.0f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = e2m1x8(v + 8 * i);
-    return static_cast<uint32_t>(e + 127);
+    return some ? static_cast<uint32_t>(e + 127) : 0u;
   }
 }
 
-// Few rows: a block per row, a thread takes 32 values at a time.
-template <bool kNv, bool kBf16>
-__global__ void __launch_bounds__(kQThreads) k_fp4_quant_row(F4Args a) {
-  constexpr int kElt = kBf16 ? 2 : 4;
-  __shared__ uint32_t part[8], top;
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, row = blockIdx.x, cols = a.m.cols;
-  const uint8_t *x = static_cast<const uint8_t *>(a.x) + row * a.stride * kElt;
-  float v[32];
-  uint32_t bad = 0;
-  float back = 1.0f;  // 2^-(row exponent)
-  if constexpr (kNv) {
-    uint32_t m = 0;
-    for (int c = 32 * t; c < cols; c += 32 * kQThreads) {
-      load32<kBf16>(x, c, cols, v);
-      m = max(m, top_bits<32>(v));
+// Eight values of a row from column c0 (bf16 or fp32; zeros behind `cols`).
+template <bool kBf16>
+__device__ __forceinline__ void load8(const uint8_t *row, int c0, int cols, float *v) {
+  if constexpr (kBf16) {
+    uint4 w = make_uint4(0, 0, 0, 0);
+    const uint16_t *p = reinterpret_cast<const uint16_t *>(row) + c0;
+    if (c0 + 8 <= cols) {
+      w = *reinterpret_cast<const uint4 *>(p);
+    } else {
+      uint32_t t[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) t[i] = c0 + i < cols ? p[i] : 0u;
+      w = make_uint4(t[0] | t[1] << 16, t[2] | t[3] << 16, t[4] | t[5] << 16, t[6] | t[7] << 16);
     }
-    m = __reduce_max_sync(0xffffffffu, m);
-    if (lane == 0) part[warp] = m;
-    __syncthreads();
-    if (t < 8) {
-      m = __reduce_max_sync(0xffu, part[t]);
-      if (t == 0) top = m;
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
     }
-    __syncthreads();
-    const int e = row_exponent(top, bad);
-    back = bad ? 0.0f : pow2f(-e);
-    if (t == 0) {
-      a.m.row_scales[row] = bad ? __uint_as_float(kNan) : pow2f(e);
-      if (bad) raise_err(a.err, CSA2_DEVERR_NAN);
+  } else {
+    const float *p = reinterpret_cast<const float *>(row) + c0;
+    if (c0 + 8 <= cols) {
+      const float4 x = reinterpret_cast<const float4 *>(p)[0], y = reinterpret_cast<const float4 *>(p)[1];
+      v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w, v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = c0 + i < cols ? p[i] : 0.0f;
     }
   }
-  const int ct = static_cast<int>(f4_col_tiles(cols)), m = row % kF4Rows;
+}
+// Few rows: a block per row.  A lane takes 8 values, two lanes a group of 16 (NV), four
+// one of 32 (MX), so a warp's loads are one run; a row of up to kIter x 2048 values stays
+// in registers between the maximum and the codes, longer ones than 4 x 2048 are read twice.
+template <bool kNv, bool kBf16, int kIter>
+__global__ void __launch_bounds__(kQThreads) k_fp4_quant_row(F4Args a) {
+  constexpr int kHeld = kIter * 8 * kQThreads;
+  constexpr int kElt = kBf16 ? 2 : 4;
+  __shared__ uint32_t part[8];
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, row = blockIdx.x, cols = a.m.cols;
+  const uint8_t *x = static_cast<const uint8_t *>(a.x) + row * a.stride * kElt;
+  const int ct = static_cast<int>(f4_col_tiles(cols)), all = ct * kF4Cols, m = row % kF4Rows;
   uint8_t *tiles = a.m.tiles + static_cast<int64_t>(row / kF4Rows) * ct * f4_tile_bytes(kNv);
-  for (int p = t; p < 4 * ct; p += kQThreads) {
-    uint32_t w[4];
-    load32<kBf16>(x, 32 * p, cols, v);
-    const uint32_t code = quant32<kNv, kBf16>(v, back, bad, w);
-    uint8_t *rec = tiles + static_cast<int64_t>(p >> 2) * f4_tile_bytes(kNv), *sc = rec + kF4CodeBytes + f4_scale_at(m);
-    if constexpr (kNv) *reinterpret_cast<uint16_t *>(sc + 512 * ((p >> 1) & 1) + 2 * (p & 1)) = static_cast<uint16_t>(code);
-    else sc[p & 3] = static_cast<uint8_t>(code);
-    *reinterpret_cast<uint4 *>(rec + (p & 3) * 2048 + m * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  float v[kIter][8];
+  uint32_t bad = 0;
+  float back = 1.0f;  // 2^-(row exponent)
+  const bool held = all <= kHeld;
+  if (kNv || held) {
+    uint32_t top = 0;
+    for (int c0 = 0; c0 < all; c0 += kHeld) {
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) load8<kBf16>(x, c0 + 8 * (t + kQThreads * i), cols, v[i]);
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) top = max(top, top_bits<8>(v[i]));
+    }
+    if constexpr (kNv) {
+      top = __reduce_max_sync(0xffffffffu, top);
+      if (lane == 0) part[warp] = top;
+      __syncthreads();
+      top = part[lane & 7];
+      top = __reduce_max_sync(0xffffffffu, top);
+      const int e = row_exponent(top, bad);
+      back = bad ? 0.0f : pow2f(-e);
+      if (t == 0) {
+        a.m.row_scales[row] = bad ? __uint_as_float(kNan) : pow2f(e);
+        if (bad) raise_err(a.err, CSA2_DEVERR_NAN);
+      }
+    }
+  }
+  for (int c0 = 0; c0 < all; c0 += kHeld) {
+    if (!held) {
+#pragma unroll
+      for (int i = 0; i < kIter; ++i) load8<kBf16>(x, c0 + 8 * (t + kQThreads * i), cols, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kIter; ++i) {
+      const int c = c0 + 8 * (t + kQThreads * i);  // (tiles are whole groups of 16 lanes)
+      uint32_t code = 0, w = 0;
+      if constexpr (kNv) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = bad ? 0.0f : __fmul_rn(v[i][j], back);
+        uint32_t g = top_bits<8>(v[i]);
+        g = max(g, __shfl_xor_sync(0xffffffffu, g, 1));
+        code = e4m3_code(__fdiv_rn(__uint_as_float(g), 6.0f));
+        w = nv8<kBf16>(v[i], e4m3_value(code));
+      } else {
+        uint32_t g = top_bits<8>(v[i]);
+        g = max(g, __shfl_xor_sync(0xffffffffu, g, 1));
+        g = max(g, __shfl_xor_sync(0xffffffffu, g, 2));
+        bad |= g >= 0x7F800000u;
+        const bool some = g != 0 && g < 0x7F800000u;
+        const int e = some ? max(floor_log2f(__uint_as_float(g)) - 2, -127) : 0;
+        const float inv = pow2f(-e);
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = some ? __fmul_rn(v[i][j], inv) : 0.0f;
+        w = e2m1x8(y);
+        code = some ? static_cast<uint32_t>(e + 127) : 0u;
+      }
+      if (c < all) {
+        const int p = c / 32;  // the piece; its scales
+        uint8_t *rec = tiles + static_cast<int64_t>(p >> 2) * f4_tile_bytes(kNv), *sc = rec + kF4CodeBytes + f4_scale_at(m);
+        if constexpr (kNv) {
+          if ((lane & 1) == 0) sc[512 * ((p >> 1) & 1) + 2 * (p & 1) + ((lane >> 1) & 1)] = static_cast<uint8_t>(code);
+        } else {
+          if ((lane & 3) == 0) sc[p & 3] = static_cast<uint8_t>(code);
+        }
+        *reinterpret_cast<uint32_t *>(rec + (p & 3) * 2048 + m * 16 + 4 * (lane & 3)) = w;
+      }
+    }
   }
   if constexpr (!kNv) {
     bad = __syncthreads_or(bad);
@@ -387,7 +464,10 @@ __global__ void __launch_bounds__(256) k_fp4_read(csa2_fp4_matrix mx, void *out,
 template <bool kNv, bool kBf16>
 static cudaError_t launch_quant(const F4Args &a, cudaStream_t s) {
   if (a.m.rows < 8 * device_sm_count()) {
-    k_fp4_quant_row<kNv, kBf16><<<a.m.rows, kQThreads, 0, s>>>(a);
+    const int64_t iter = (f4_col_tiles(a.m.cols) * kF4Cols + 8 * kQThreads - 1) / (8 * kQThreads);
+    const auto kern = iter <= 1 ? k_fp4_quant_row<kNv, kBf16, 1> : iter == 2 ? k_fp4_quant_row<kNv, kBf16, 2>
+                    : iter == 3 ? k_fp4_quant_row<kNv, kBf16, 3> : k_fp4_quant_row<kNv, kBf16, 4>;
+    kern<<<a.m.rows, kQThreads, 0, s>>>(a);
     return cudaGetLastError();
   }
   const int pitch = static_cast<int>(f4_col_tiles(a.m.cols)) * kF4Cols * (kBf16 ? 2 : 4) + 16, blocks = (a.m.rows + 7) / 8;

@@ -7,7 +7,7 @@
 // by bulk copies and nothing is rearranged.
 //
 // k_fp4_split: the weights are the MMA's 128 rows (lane = output column, so a warp's
-// stores are runs of one output row), the tokens its NT columns.  The K tiles of an
+// stores are runs of one output row), the tokens its NT columns (all of them, or 128).  The K tiles of an
 // output tile are dealt to the CTAs of a cluster, whose sums are added in rank order
 // through distributed shared memory: no workspace, equal calls give equal bits.
 // Bound: the weights' bytes for few tokens.
@@ -576,16 +576,26 @@ cudaError_t launch_split(const ProductArgs &a, int ranks, cudaStream_t s) {
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, a, mw, mx, ms);
 }
+// Which kernel, and how the split one cuts the work.  One GB300, us, NV to bf16, in a graph.
+//   Pairs once 64 CTAs have a tile and more than 64 tokens share it: 501 x 4096 x 8192
+//   (64 CTAs) 15.3 against 16.0 split, 256 x 12288 x 4096 (96) 11.2 against 17.8; below,
+//   256 x 4096 x 8192 (32) 15.1 against 11.6, 64 tokens x 12288 x 4096 10.7 against 8.9.
+//   Split: the narrowest token tile that holds all tokens (a scale column is of 32 rows
+//   from the record's first on, so several tiles only of 128), then as many ranks as fit
+//   two CTAs per SM: 64 x 12288 x 4096 8.9 with 3 against 11.2 with 1, 1 x 4096 x 8192 5.8
+//   with 8 against 6.0 with 4.  128 tokens: 4 at most, their sums' way through shared
+//   memory costs more: 501 x 704 x 4104 7.7 with 4, 8.1 with 6, 9.5 with 8.
 template <bool kNv, bool kBf16>
 cudaError_t launch_product(const ProductArgs &a, cudaStream_t s) {
   const int m = a.x.rows;
   const int64_t big = (f4_row_tiles(m) + 1) / 2 * ((a.w.rows + kPairN - 1) / kPairN);
-  if (4 * 2 * big >= 3 * device_sm_count()) return launch_pair<kNv, kBf16>(a, s);
+  if (m > 64 && 2 * big >= 64) return launch_pair<kNv, kBf16>(a, s);
   const int nt = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
-  const int64_t tiles = f4_row_tiles(a.w.rows) * ((m + nt - 1) / nt);
-  const int64_t steps = (f4_col_tiles(a.x.cols) + (nt <= 32 ? 3 : 1)) / (nt <= 32 ? 4 : 2), sms = device_sm_count();
+  const int64_t tiles = f4_row_tiles(a.w.rows) * ((m + nt - 1) / nt), per = nt <= 32 ? 4 : 2;
+  const int64_t steps = (f4_col_tiles(a.x.cols) + per - 1) / per, most = 2 * device_sm_count();
   int ranks = 1;
-  while (ranks < 8 && tiles * ranks * 2 <= 2 * sms && steps >= 2 * ranks) ranks *= 2;
+  for (const int r : {2, 3, 4, 6, 8})
+    if (tiles * r <= most && r <= steps && (nt < 128 || r <= 4)) ranks = r;
   switch (nt) {
     case 16: return launch_split<16, kNv, kBf16>(a, ranks, s);
     case 32: return launch_split<32, kNv, kBf16>(a, ranks, s);

@@ -49,7 +49,8 @@ def _packed(x, fmt, err=None):
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dtype", TYPES)
-@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 128), (3, 136), (17, 31), (130, 520), (129, 4104), (2000, 264), (1300, 2056), (1217, 130), (1400, 6000), (1290, 17000)])
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 128), (3, 136), (17, 31), (130, 520), (129, 4104), (2000, 264), (1300, 2056), (1217, 130), (1400, 6000), (1290, 17000),
+                                       (7, 8192), (9, 8200), (2, 20000), (5, 2049), (3, 6144)])
 def test_quant_is_the_definition(fmt, dtype, rows, cols):
     """Codes and scales as values, equal; read back in both types; strided rows; columns behind the
     last one of the tile are zeros."""
@@ -145,7 +146,8 @@ def _within(out, x, w):
 
 SHAPES = [(1, 8, 128), (1, 700, 4096), (5, 129, 40), (16, 256, 1000), (17, 130, 384), (33, 1000, 2048), (64, 96, 128),
           (65, 704, 640), (128, 128, 8192), (129, 1, 256), (300, 2056, 136), (1, 1, 1), (501, 704, 4104), (2, 12288, 512),
-          (1000, 4100, 264), (2049, 2500, 520)]
+          (1000, 4100, 264), (2049, 2500, 520), (70, 900, 3000), (250, 700, 1100), (96, 6200, 300), (1, 300, 20000),
+          (65, 8200, 128), (200, 96, 5000)]
 
 
 @pytest.mark.parametrize("fmt", FMTS)
