@@ -31,48 +31,6 @@ struct F4Args {
   int32_t *err;
 };
 
-// |bits| of up to 32 values, and the values, from column c0 of a row; zeros behind `cols`.
-template <bool kBf16>
-__device__ __forceinline__ void load32(const void *row, int c0, int cols, float *v) {
-  if constexpr (kBf16) {
-    const uint16_t *p = static_cast<const uint16_t *>(row) + c0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (c0 + 8 * q + 8 <= cols) {
-        w = reinterpret_cast<const uint4 *>(p)[q];
-      } else {
-        uint32_t t[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t[i] = c0 + 8 * q + i < cols ? p[8 * q + i] : 0u;
-        w = make_uint4(t[0] | t[1] << 16, t[2] | t[3] << 16, t[4] | t[5] << 16, t[6] | t[7] << 16);
-      }
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[8 * q + 2 * i] = __uint_as_float(u[i] << 16);
-        v[8 * q + 2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-      }
-    }
-  } else {
-    const float *p = static_cast<const float *>(row) + c0;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      float4 w = make_float4(0, 0, 0, 0);
-      if (c0 + 4 * q + 4 <= cols) {
-        w = reinterpret_cast<const float4 *>(p)[q];
-      } else {
-        if (c0 + 4 * q < cols) w.x = p[4 * q];
-        if (c0 + 4 * q + 1 < cols) w.y = p[4 * q + 1];
-        if (c0 + 4 * q + 2 < cols) w.z = p[4 * q + 2];
-      }
-      v[4 * q] = w.x;
-      v[4 * q + 1] = w.y;
-      v[4 * q + 2] = w.z;
-      v[4 * q + 3] = w.w;
-    }
-  }
-}
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 template <int kN>
 __device__ __forceinline__ uint32_t top_bits(const float *v) {
@@ -94,39 +52,42 @@ __device__ __forceinline__ uint32_t e2m1x8(const float *y) {
   return r;
 }
 
-// Eight values y of a group with scale s to eight codes (see the file's head); zeros if s is 0.
+// Eight values of a group with scale s of a row with power of two 2^e to eight codes (see
+// the file's head), zeros if s is 0; back = 2^-e, fore = 2^e.  Both only shift exponents,
+// so they go with 1 / s, or with T s, instead of with every value.
 template <bool kBf16>
-__device__ __forceinline__ uint32_t nv8(const float *y, float s) {
+__device__ __forceinline__ uint32_t nv8(const float *x, float s, float back, float fore) {
   if constexpr (kBf16) {
-    const float inv = __frcp_rn(s);
+    const float inv = __fmul_rn(__frcp_rn(s), back);
     float q[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __uint_as_float((__float_as_uint(__fmul_rn(y[i], inv)) + 0x400u) & ~0x7FFu);
+    for (int i = 0; i < 8; ++i) q[i] = __uint_as_float((__float_as_uint(__fmul_rn(x[i], inv)) + 0x400u) & ~0x7FFu);
     const uint32_t w = e2m1x8(q);
     return s != 0.0f ? w : 0u;
   } else {
-    const float t0 = 0.25f * s, t1 = 0.75f * s, t2 = 1.25f * s, t3 = 1.75f * s, t4 = 2.5f * s, t5 = 3.5f * s, t6 = 5.0f * s;
+    const float u = __fmul_rn(s, fore);
+    const float t0 = 0.25f * u, t1 = 0.75f * u, t2 = 1.25f * u, t3 = 1.75f * u, t4 = 2.5f * u, t5 = 3.5f * u, t6 = 5.0f * u;
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float a = fabsf(y[i]);
+      const float a = fabsf(x[i]);
       uint32_t c = (a > t0) + (a >= t1) + (a > t2) + (a >= t3) + (a > t4) + (a >= t5) + (a > t6);
-      c |= (__float_as_uint(y[i]) >> 28) & 8u;
+      c |= (__float_as_uint(x[i]) >> 28) & 8u;
       w |= c << (4 * i);
     }
     return s != 0.0f ? w : 0u;
   }
 }
-
-// 16 values y (already divided by the row's power of two) into two words and an E4M3 scale.
-template <bool kBf16>
-__device__ __forceinline__ void nv16(const float *y, uint32_t *w, uint32_t *sc) {
-  const float amax = __uint_as_float(top_bits<16>(y));
-  const uint32_t code = e4m3_code(__fdiv_rn(amax, 6.0f));
-  const float s = e4m3_value(code);
-  *sc = code;
-  w[0] = nv8<kBf16>(y, s);
-  w[1] = nv8<kBf16>(y + 8, s);
+// The scale byte of a group with largest magnitude amax.
+__device__ __forceinline__ uint32_t nv_scale(float amax, float back) {
+  return e4m3_code(__fdiv_rn(__fmul_rn(amax, back), 6.0f));
+}
+template <int kN>
+__device__ __forceinline__ float top_abs(const float *v) {
+  float t = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) t = fmaxf(t, fabsf(v[i]));
+  return t;
 }
 
 // A row's power of two from its largest magnitude's bits: the exponent, and whether the
@@ -141,28 +102,18 @@ __device__ __forceinline__ int row_exponent(uint32_t m, uint32_t &bad) {
 }
 constexpr uint32_t kNan = 0x7FC00000u;
 
-// 32 values to 16 bytes of codes and, returned, their scale bytes (NV 2, MX 1).
-template <bool kNv, bool kBf16>
-__device__ __forceinline__ uint32_t quant32(float *v, float back, uint32_t &bad, uint32_t *w) {
-  if constexpr (kNv) {
-    uint32_t s0, s1;
+// 32 values of a group to 16 bytes of codes and, returned, their E8M0 scale.
+__device__ __forceinline__ uint32_t mx32(float *v, uint32_t &bad, uint32_t *w) {
+  const uint32_t g = top_bits<32>(v);
+  bad |= g >= 0x7F800000u;
+  const bool some = g != 0 && g < 0x7F800000u;
+  const int e = some ? max(floor_log2f(__uint_as_float(g)) - 2, -127) : 0;
+  const float inv = pow2f(-e);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = bad ? 0.0f : __fmul_rn(v[i], back);
-    nv16<kBf16>(v, w, &s0);
-    nv16<kBf16>(v + 16, w + 2, &s1);
-    return s0 | s1 << 8;
-  } else {
-    const uint32_t g = top_bits<32>(v);
-    bad |= g >= 0x7F800000u;
-    const bool some = g != 0 && g < 0x7F800000u;
-    const int e = some ? max(floor_log2f(__uint_as_float(g)) - 2, -127) : 0;
-    const float inv = pow2f(-e);
+  for (int i = 0; i < 32; ++i) v[i] = some ? __fmul_rn(v[i], inv) : 0.0f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = some ? __fmul_rn(v[i], inv) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = e2m1x8(v + 8 * i);
-    return some ? static_cast<uint32_t>(e + 127) : 0u;
-  }
+  for (int i = 0; i < 4; ++i) w[i] = e2m1x8(v + 8 * i);
+  return some ? static_cast<uint32_t>(e + 127) : 0u;
 }
 
 // Eight values of a row from column c0 (bf16 or fp32; zeros behind `cols`).
@@ -210,7 +161,7 @@ __global__ void __launch_bounds__(kQThreads) k_fp4_quant_row(F4Args a) {
   uint8_t *tiles = a.m.tiles + static_cast<int64_t>(row / kF4Rows) * ct * f4_tile_bytes(kNv);
   float v[kIter][8];
   uint32_t bad = 0;
-  float back = 1.0f;  // 2^-(row exponent)
+  float back = 1.0f, fore = 1.0f;  // 2^-e and 2^e, e the row's exponent
   const bool held = all <= kHeld;
   if (kNv || held) {
     uint32_t top = 0;
@@ -227,7 +178,8 @@ __global__ void __launch_bounds__(kQThreads) k_fp4_quant_row(F4Args a) {
       top = part[lane & 7];
       top = __reduce_max_sync(0xffffffffu, top);
       const int e = row_exponent(top, bad);
-      back = bad ? 0.0f : pow2f(-e);
+      back = pow2f(bad ? 0 : -e);
+      fore = pow2f(bad ? 0 : e);
       if (t == 0) {
         a.m.row_scales[row] = bad ? __uint_as_float(kNan) : pow2f(e);
         if (bad) raise_err(a.err, CSA2_DEVERR_NAN);
@@ -244,12 +196,10 @@ __global__ void __launch_bounds__(kQThreads) k_fp4_quant_row(F4Args a) {
       const int c = c0 + 8 * (t + kQThreads * i);  // (tiles are whole groups of 16 lanes)
       uint32_t code = 0, w = 0;
       if constexpr (kNv) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[i][j] = bad ? 0.0f : __fmul_rn(v[i][j], back);
-        uint32_t g = top_bits<8>(v[i]);
-        g = max(g, __shfl_xor_sync(0xffffffffu, g, 1));
-        code = e4m3_code(__fdiv_rn(__uint_as_float(g), 6.0f));
-        w = nv8<kBf16>(v[i], e4m3_value(code));
+        float g = top_abs<8>(v[i]);
+        g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
+        code = nv_scale(g, back);
+        w = nv8<kBf16>(v[i], e4m3_value(code), back, fore);
       } else {
         uint32_t g = top_bits<8>(v[i]);
         g = max(g, __shfl_xor_sync(0xffffffffu, g, 1));
@@ -285,12 +235,30 @@ __global__ void __launch_bounds__(kQThreads) k_fp4_quant_row(F4Args a) {
   }
 }
 
+// Sixteen values of a row in shared (or, with `cols` checked, global) memory.
+template <bool kBf16>
+__device__ __forceinline__ void load16(const uint8_t *row, int c0, int cols, float *v) {
+  load8<kBf16>(row, c0, cols, v);
+  load8<kBf16>(row, c0 + 8, cols, v + 8);
+}
+// Largest magnitude's bits (or a NaN's) of the values in a word: two bf16 or one fp32.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t word_top(uint32_t m, uint32_t w) {
+  if constexpr (kBf16) {  // m: two maxima
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(m), "r"(w & 0x7FFF7FFFu));
+    return r;
+  } else {
+    return max(m, w & 0x7FFFFFFFu);
+  }
+}
+
 // Many rows: a block per 8 rows (their 16 bytes of a piece are a whole 128 B line).
 // kStaged: the rows are read once, coalesced, a warp per row, into shared memory (row
 // pitch an odd number of 16 bytes, so that 8 rows' loads meet no bank twice); else, when
 // they do not fit there, a second time through the caches.
 template <bool kNv, bool kBf16, bool kStaged>
-__global__ void __launch_bounds__(kQThreads) k_fp4_quant_rows(F4Args a, int pitch) {
+__global__ void __launch_bounds__(kQThreads, kNv ? 4 : 3) k_fp4_quant_rows(F4Args a, int pitch) {
   constexpr int kElt = kBf16 ? 2 : 4;
   extern __shared__ __align__(16) uint8_t stage[];
   __shared__ uint32_t top[8];
@@ -298,75 +266,79 @@ __global__ void __launch_bounds__(kQThreads) k_fp4_quant_rows(F4Args a, int pitc
   const int row0 = blockIdx.x * 8, r8 = t & 7, row = row0 + r8;  // row: this thread's, once it writes
   const uint8_t *x = static_cast<const uint8_t *>(a.x);
   const int ct = static_cast<int>(f4_col_tiles(cols)), pieces = 4 * ct;
-  float v[32];
   uint32_t bad = 0, m = 0;
-  float back = 1.0f;
-  if (kStaged && row0 + warp < rows) {
+  if ((kNv || kStaged) && row0 + warp < rows) {
     const uint8_t *src = x + (row0 + warp) * a.stride * kElt;
-    const int bytes = cols * kElt, whole = bytes & ~15;
+    const int whole = cols * kElt & ~15;
 #pragma unroll 8
     for (int c = 16 * lane; c < whole; c += 512) {
       const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src + c));
-      *reinterpret_cast<uint4 *>(stage + warp * pitch + c) = u;
-      if constexpr (kNv) {
-        const uint32_t q[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          m = kBf16 ? max(m, max(q[i] << 16 & 0x7FFF0000u, q[i] & 0x7FFF0000u)) : max(m, q[i] & 0x7FFFFFFFu);
-      }
+      if constexpr (kStaged) *reinterpret_cast<uint4 *>(stage + warp * pitch + c) = u;
+      if constexpr (kNv) m = word_top<kBf16>(word_top<kBf16>(word_top<kBf16>(word_top<kBf16>(m, u.x), u.y), u.z), u.w);
     }
     // the last values, and zeros to the end of the last tile
     for (int c = whole / kElt + lane; c < 32 * pieces; c += 32) {
-      if constexpr (kBf16) {
-        const uint16_t u = c < cols ? reinterpret_cast<const uint16_t *>(src)[c] : 0;
-        reinterpret_cast<uint16_t *>(stage + warp * pitch)[c] = u;
-        m = max(m, static_cast<uint32_t>(u & 0x7FFF) << 16);
-      } else {
-        const uint32_t u = c < cols ? reinterpret_cast<const uint32_t *>(src)[c] : 0;
-        reinterpret_cast<uint32_t *>(stage + warp * pitch)[c] = u;
-        m = max(m, u & 0x7FFFFFFFu);
+      const uint32_t u = c >= cols ? 0u : kBf16 ? reinterpret_cast<const uint16_t *>(src)[c] : reinterpret_cast<const uint32_t *>(src)[c];
+      if constexpr (kNv) m = word_top<kBf16>(m, u);
+      if constexpr (kStaged) {
+        if constexpr (kBf16) reinterpret_cast<uint16_t *>(stage + warp * pitch)[c] = static_cast<uint16_t>(u);
+        else reinterpret_cast<uint32_t *>(stage + warp * pitch)[c] = u;
       }
-    }
-  } else if (kNv && !kStaged && row0 + warp < rows) {
-    const uint8_t *src = x + (row0 + warp) * a.stride * kElt;
-    for (int c = 32 * lane; c < cols; c += 1024) {
-      load32<kBf16>(src, c, cols, v);
-      m = max(m, top_bits<32>(v));
     }
   }
   if constexpr (kNv) {
+    if constexpr (kBf16) m = max(m << 16, m & 0x7FFF0000u);
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) top[warp] = m;
   }
   if constexpr (kNv || kStaged) __syncthreads();
-  if constexpr (kNv) {
-    const int e = row_exponent(top[r8], bad);
-    back = bad ? 0.0f : pow2f(-e);
-    if (row < rows && t < 8) {
-      a.m.row_scales[row] = bad ? __uint_as_float(kNan) : pow2f(e);
-      if (bad) raise_err(a.err, CSA2_DEVERR_NAN);
-    }
-  }
   const int mr = row % kF4Rows;
   uint8_t *tiles = a.m.tiles + static_cast<int64_t>(row / kF4Rows) * ct * f4_tile_bytes(kNv);
-  if (row < rows) {
-    // two pieces a time: their scales (NV) are one word
-    for (int p = 2 * (t >> 3); p < pieces; p += 64) {
-      uint8_t *rec = tiles + static_cast<int64_t>(p >> 2) * f4_tile_bytes(kNv), *sc = rec + kF4CodeBytes + f4_scale_at(mr);
-      uint32_t code[2];
+  const uint8_t *src = kStaged ? stage + r8 * pitch : x + row * a.stride * kElt;
+  const int have = kStaged ? 32 * pieces : cols;
+  if constexpr (kNv) {
+    const int e = row_exponent(top[r8], bad);
+    const float back = pow2f(bad ? 0 : -e), fore = pow2f(bad ? 0 : e);
+    if (row < rows && t < 8) {
+      a.m.row_scales[row] = bad ? __uint_as_float(kNan) : fore;
+      if (bad) raise_err(a.err, CSA2_DEVERR_NAN);
+    }
+    // two pieces at a time, whose four scales are one word
+    for (int p = 2 * (t >> 3); p < pieces && row < rows; p += 64) {
+      uint8_t *rec = tiles + static_cast<int64_t>(p >> 2) * f4_tile_bytes(true);
+      uint32_t code = 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         uint32_t w[4];
-        if constexpr (kStaged) load32<kBf16>(stage + r8 * pitch, 32 * (p + i), 32 * pieces, v);
-        else load32<kBf16>(x + row * a.stride * kElt, 32 * (p + i), cols, v);
-        code[i] = quant32<kNv, kBf16>(v, back, bad, w);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float v[16];
+          load16<kBf16>(src, 32 * (p + i) + 16 * g, have, v);
+          const uint32_t sc = nv_scale(top_abs<16>(v), back);
+          const float s = e4m3_value(sc);
+          w[2 * g] = nv8<kBf16>(v, s, back, fore);
+          w[2 * g + 1] = nv8<kBf16>(v + 8, s, back, fore);
+          code |= sc << (16 * i + 8 * g);
+        }
         *reinterpret_cast<uint4 *>(rec + ((p + i) & 3) * 2048 + mr * 16) = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      if constexpr (kNv) *reinterpret_cast<uint32_t *>(sc + 512 * ((p >> 1) & 1)) = code[0] | code[1] << 16;
-      else *reinterpret_cast<uint16_t *>(sc + (p & 3)) = static_cast<uint16_t>(code[0] | code[1] << 8);
+      *reinterpret_cast<uint32_t *>(rec + kF4CodeBytes + f4_scale_at(mr) + 512 * ((p >> 1) & 1)) = code;
     }
-  }
-  if constexpr (!kNv) {
+  } else {
+    for (int p = 2 * (t >> 3); p < pieces && row < rows; p += 64) {
+      uint8_t *rec = tiles + static_cast<int64_t>(p >> 2) * f4_tile_bytes(false);
+      uint32_t code = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t w[4];
+        float v[32];
+        load16<kBf16>(src, 32 * (p + i), have, v);
+        load16<kBf16>(src, 32 * (p + i) + 16, have, v + 16);
+        code |= mx32(v, bad, w) << (8 * i);
+        *reinterpret_cast<uint4 *>(rec + ((p + i) & 3) * 2048 + mr * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      *reinterpret_cast<uint16_t *>(rec + kF4CodeBytes + f4_scale_at(mr) + (p & 3)) = static_cast<uint16_t>(code);
+    }
     __syncthreads();
     if (t < 8) top[t] = 0;
     __syncthreads();
@@ -390,7 +362,7 @@ __global__ void __launch_bounds__(256) k_fp4_read(csa2_fp4_matrix mx, void *out,
   const int m = row % kF4Rows;
   const float r = mx.row_scales[row];
   const uint8_t *tiles = mx.tiles + static_cast<int64_t>(row / kF4Rows) * ct * f4_tile_bytes(kNv);
-#pragma unroll 2
+#pragma unroll 4
   for (int k = blockIdx.y * 8 + warp; k < ct; k += 8 * gridDim.y) {
     const uint8_t *rec = tiles + static_cast<int64_t>(k) * f4_tile_bytes(kNv), *sc = rec + kF4CodeBytes + f4_scale_at(m);
     const uint4 u = __ldg(reinterpret_cast<const uint4 *>(rec + j * 2048 + m * 16));
