@@ -564,7 +564,7 @@ csa2_status csa2_slot_map(const csa2_cache *cache, const int32_t *cu_new, int32_
  *               NV (1,024 B): (g / 4) * 512 + 16 (m % 32) + 4 (m / 32) + g % 4, group g of
  *               8; MX (512 B): 16 (m % 32) + 4 (m / 32) + j
  *   row_scales  float r per row
- * Rows behind `rows` in the last tile are neither written nor looked at.
+ * Rows behind `rows` in the last tile are not written, and what they hold does not matter.
  * rows 0..2^24, cols 1..2^17.
  */
 #define CSA2_FP4_NV 0
