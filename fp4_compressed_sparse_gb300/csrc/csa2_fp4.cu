@@ -155,6 +155,8 @@ __global__ void __launch_bounds__(kQThreads) k_fp4_quant_row(F4Args a) {
   constexpr int kHeld = kIter * 8 * kQThreads;
   constexpr int kElt = kBf16 ? 2 : 4;
   __shared__ uint32_t part[8];
+  next_may_start();
+  wait_for_previous();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, row = blockIdx.x, cols = a.m.cols;
   const uint8_t *x = static_cast<const uint8_t *>(a.x) + row * a.stride * kElt;
   const int ct = static_cast<int>(f4_col_tiles(cols)), all = ct * kF4Cols, m = row % kF4Rows;
@@ -262,6 +264,8 @@ __global__ void __launch_bounds__(kQThreads, kNv ? 4 : 3) k_fp4_quant_rows(F4Arg
   constexpr int kElt = kBf16 ? 2 : 4;
   extern __shared__ __align__(16) uint8_t stage[];
   __shared__ uint32_t top[8];
+  next_may_start();
+  wait_for_previous();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, rows = a.m.rows, cols = a.m.cols;
   const int row0 = blockIdx.x * 8, r8 = t & 7, row = row0 + r8;  // row: this thread's, once it writes
   const uint8_t *x = static_cast<const uint8_t *>(a.x);
@@ -355,6 +359,8 @@ __global__ void __launch_bounds__(kQThreads, kNv ? 4 : 3) k_fp4_quant_rows(F4Arg
 // values a lane out).
 template <bool kNv, bool kBf16>
 __global__ void __launch_bounds__(256) k_fp4_read(csa2_fp4_matrix mx, void *out, int64_t stride, int wide) {
+  next_may_start();
+  wait_for_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int ct = static_cast<int>(f4_col_tiles(mx.cols));
   const int row = blockIdx.x * 8 + (lane & 7), j = lane >> 3;
@@ -439,19 +445,16 @@ static cudaError_t launch_quant(const F4Args &a, cudaStream_t s) {
     const int64_t iter = (f4_col_tiles(a.m.cols) * kF4Cols + 8 * kQThreads - 1) / (8 * kQThreads);
     const auto kern = iter <= 1 ? k_fp4_quant_row<kNv, kBf16, 1> : iter == 2 ? k_fp4_quant_row<kNv, kBf16, 2>
                     : iter == 3 ? k_fp4_quant_row<kNv, kBf16, 3> : k_fp4_quant_row<kNv, kBf16, 4>;
-    kern<<<a.m.rows, kQThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_after(kern, dim3(a.m.rows), kQThreads, 0, 0, s, a);
   }
   const int pitch = static_cast<int>(f4_col_tiles(a.m.cols)) * kF4Cols * (kBf16 ? 2 : 4) + 16, blocks = (a.m.rows + 7) / 8;
   if (8 * pitch > 112 * 1024) {
-    k_fp4_quant_rows<kNv, kBf16, false><<<blocks, kQThreads, 0, s>>>(a, 0);
-    return cudaGetLastError();
+    return launch_after(k_fp4_quant_rows<kNv, kBf16, false>, dim3(blocks), kQThreads, 0, 0, s, a, 0);
   }
   const auto kern = k_fp4_quant_rows<kNv, kBf16, true>;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), 8 * pitch);
   if (e != cudaSuccess) return e;
-  kern<<<blocks, kQThreads, 8 * pitch, s>>>(a, pitch);
-  return cudaGetLastError();
+  return launch_after(kern, dim3(blocks), kQThreads, 8 * pitch, 0, s, a, pitch);
 }
 
 csa2_status check_fp4(const csa2_fp4_matrix *m, const char *name) {
@@ -514,14 +517,9 @@ csa2_status csa2_fp4_read(const csa2_fp4_matrix *m, void *out, int64_t out_strid
   const dim3 grid(row_blocks, split);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = out_dtype == CSA2_OUT_BF16;
-  if (m->format == CSA2_FP4_NV) {
-    if (bf) csa2::k_fp4_read<true, true><<<grid, 256, 0, s>>>(*m, out, out_stride, wide);
-    else csa2::k_fp4_read<true, false><<<grid, 256, 0, s>>>(*m, out, out_stride, wide);
-  } else {
-    if (bf) csa2::k_fp4_read<false, true><<<grid, 256, 0, s>>>(*m, out, out_stride, wide);
-    else csa2::k_fp4_read<false, false><<<grid, 256, 0, s>>>(*m, out, out_stride, wide);
-  }
-  return cuda_status(cudaGetLastError(), "csa2_fp4_read launch");
+  const auto kern = m->format == CSA2_FP4_NV ? (bf ? csa2::k_fp4_read<true, true> : csa2::k_fp4_read<true, false>)
+                                             : (bf ? csa2::k_fp4_read<false, true> : csa2::k_fp4_read<false, false>);
+  return cuda_status(csa2::launch_after(kern, grid, 256, 0, 0, s, *m, out, out_stride, wide), "csa2_fp4_read launch");
 }
 
 }  // extern "C"

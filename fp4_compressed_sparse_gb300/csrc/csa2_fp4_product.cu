@@ -123,6 +123,8 @@ __global__ void __launch_bounds__(kSplitThreads)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  next_may_start();
+  wait_for_previous();
   const uint32_t tmem = tmem_at;
 
   if (warp == 0 && lane == 0) {
@@ -329,7 +331,7 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
 }
 
 template <bool kNv, bool kBf16>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 1)
     k_fp4_pair(ProductArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
                const __grid_constant__ CUtensorMap ms, int mt, int nt, int wide32) {
   using L = Pair<kNv>;
@@ -359,6 +361,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   __syncthreads();
   cluster_sync();  // the peer's barriers are initialised, its tensor memory allocated
   tc::tc_fence_after();
+  next_may_start();
+  wait_for_previous();
   const uint32_t tmem = sy.tmem;
   auto gave_up = [&]() {
     raise_err(a.err, CSA2_DEVERR_TIMEOUT);
@@ -548,8 +552,8 @@ cudaError_t launch_pair(const ProductArgs &a, cudaStream_t s) {
   const int mt = static_cast<int>(f4_row_tiles(a.x.rows)), nt = (a.w.rows + kPairN - 1) / kPairN;
   const int64_t tiles = static_cast<int64_t>((mt + 1) / 2) * nt, most = device_sm_count() / 2;
   const int wide32 = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0 && a.stride % 16 == 0;
-  kern<<<static_cast<unsigned>(2 * (tiles < most ? tiles : most)), kPairThreads, L::kBytes, s>>>(a, mx, mw, ms, mt, nt, wide32);
-  return cudaGetLastError();
+  return launch_after(kern, dim3(static_cast<unsigned>(2 * (tiles < most ? tiles : most))), kPairThreads, L::kBytes, 2, s, a, mx, mw, ms,
+                      mt, nt, wide32);
 }
 
 template <int NT, bool kNv, bool kBf16>
@@ -563,18 +567,8 @@ cudaError_t launch_split(const ProductArgs &a, int ranks, cudaStream_t s) {
   if (!record_map(&mw, a.w, kNv, kCodes + 1, L::kTiles, 1) || !token_map(&mx, a.x, kNv, NT, L::kTiles) ||
       !record_map(&ms, a.x, kNv, 1, L::kTiles, 1))
     return cudaErrorNotSupported;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(f4_row_tiles(a.w.rows) * ranks), static_cast<unsigned>((a.x.rows + NT - 1) / NT));
-  cfg.blockDim = dim3(kSplitThreads);
-  cfg.dynamicSmemBytes = L::kBytes;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = ranks;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, mw, mx, ms);
+  const dim3 grid(static_cast<unsigned>(f4_row_tiles(a.w.rows) * ranks), static_cast<unsigned>((a.x.rows + NT - 1) / NT));
+  return launch_after(kern, grid, kSplitThreads, L::kBytes, ranks, s, a, mw, mx, ms);
 }
 // Which kernel, and how the split one cuts the work.  One GB300, us, NV to bf16, in a graph.
 //   Pairs once 64 CTAs have a tile and more than 64 tokens share it: 501 x 4096 x 8192

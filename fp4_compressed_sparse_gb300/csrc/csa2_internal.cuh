@@ -41,6 +41,31 @@ __host__ __forceinline__ bool aligned16(const void *p) { return (reinterpret_cas
       return ::csa2::fail(CSA2_ERR_ALIGN, "%s is not 16-byte aligned", #p);                 \
   } while (0)
 
+// ------------------------------------------------------------------ overlapped launches
+// A kernel launched by launch_after() may be resident and set itself up while the kernel
+// before it in the stream drains (or, once all blocks of that one have called
+// next_may_start(), while it runs).  It calls wait_for_previous() in every thread before it
+// reads or writes anything in memory.
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+template <class... P, class... A>
+cudaError_t launch_after(void (*kern)(P...), dim3 grid, int block, size_t smem, int cluster, cudaStream_t s, A &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 cudaError_t launch_kv_append(const csa2_cache &c, const void *kv, const void *ik, int in_dtype,
                              const csa2_compress_in *cmp, const float *rope_cs, int64_t rope_len, int n_new,
                              float *cmp_dbg, int32_t *err, cudaStream_t s);

@@ -145,6 +145,8 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
   tc::tc_fence_before();
   __syncthreads();
   tc::tc_fence_after();
+  next_may_start();
+  wait_for_previous();
   const uint32_t tmem = sy.tmem;
   auto gave_up = [&]() {
     raise_err(a.err, CSA2_DEVERR_TIMEOUT);
@@ -418,8 +420,7 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t s) {
     if (!tensor_map(&mo, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, o_dim, o_stride, o_box, true)) return cudaErrorNotSupported;
   }
   const int64_t units = static_cast<int64_t>(a.heads) * a.parts * a.tiles, sms = device_sm_count();
-  kern<<<static_cast<unsigned>(units < sms ? units : sms), Shape<kM>::kThreads, Shape<kM>::kBytes, s>>>(a, mx, mw, mo);
-  return cudaGetLastError();
+  return launch_after(kern, dim3(static_cast<unsigned>(units < sms ? units : sms)), Shape<kM>::kThreads, Shape<kM>::kBytes, 0, s, a, mx, mw, mo);
 }
 
 }  // namespace

@@ -30,6 +30,8 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 
 template <int kTiles>
 __global__ void __launch_bounds__(kFewThreads) k_query_few(LatentArgs a) {
   __shared__ float4 red[3][2][kTiles * 8][32];
+  next_may_start();
+  wait_for_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int h = blockIdx.x, part = blockIdx.y, tok0 = blockIdx.z * 16 * kTiles;
   const uint16_t *xh = static_cast<const uint16_t *>(a.x) + static_cast<int64_t>(h) * (a.dim + kRope);
@@ -122,6 +124,8 @@ __global__ void __launch_bounds__(kFewThreads) k_query_few(LatentArgs a) {
 template <int kTiles, bool kF32>
 __global__ void __launch_bounds__(kFewThreads) k_value_few(LatentArgs a) {
   __shared__ float2 red[8][kTiles][2][4][32];
+  next_may_start();
+  wait_for_previous();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int h = blockIdx.x, j0 = blockIdx.y * 32, tok0 = blockIdx.z * 16 * kTiles;
   const int c0 = 64 * warp + 8 * t;
@@ -204,16 +208,13 @@ __global__ void __launch_bounds__(kFewThreads) k_value_few(LatentArgs a) {
 
 cudaError_t launch_query_few(const LatentArgs &a, cudaStream_t s) {
   const dim3 grid(a.heads, kLat / 128 + 1, (a.total + 31) / 32);
-  if (a.total <= 16) k_query_few<1><<<grid, kFewThreads, 0, s>>>(a);
-  else k_query_few<2><<<grid, kFewThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  return launch_after(a.total <= 16 ? k_query_few<1> : k_query_few<2>, grid, kFewThreads, 0, 0, s, a);
 }
 
 cudaError_t launch_value_few(const LatentArgs &a, bool f32, cudaStream_t s) {
   const dim3 grid(a.heads, (a.dim + 31) / 32, (a.total + 31) / 32);
-  if (a.total <= 16) f32 ? k_value_few<1, true><<<grid, kFewThreads, 0, s>>>(a) : k_value_few<1, false><<<grid, kFewThreads, 0, s>>>(a);
-  else f32 ? k_value_few<2, true><<<grid, kFewThreads, 0, s>>>(a) : k_value_few<2, false><<<grid, kFewThreads, 0, s>>>(a);
-  return cudaGetLastError();
+  const auto kern = a.total <= 16 ? (f32 ? k_value_few<1, true> : k_value_few<1, false>) : (f32 ? k_value_few<2, true> : k_value_few<2, false>);
+  return launch_after(kern, grid, kFewThreads, 0, 0, s, a);
 }
 
 }  // namespace csa2
