@@ -7,14 +7,17 @@
 // beyond 2688 x 2^62 in NV, has the row scale NaN: whatever is computed from it is NaN.
 //
 // x / s in E2M1 without a division.  A quotient rounds to a code by its place among the
-// grid's midpoints T (1, 3, 5 or 7 times a power of two); s has 4 significant bits.
+// grid's midpoints T (1, 3, 5 or 7 times a power of two, 1/4 at least); s has 4 significant
+// bits.
 //   bf16 x (8 bits): x and T s are integers up to 255 and 105 times powers of two, so x / s
-//   is T or differs from it by 2^-8 of it at least.  x * RN(1 / s), off by 2^-23, is
-//   rounded to 12 fraction bits: T where the quotient is T, on its side of T where not;
-//   then the conversion instruction decides.
+//   is T or differs from it by 2^-8 of it, 2^-10, at least.  x * (1 / s), off by 2^-21 at
+//   most, is rounded to a multiple of 2^-12 (by adding 1.5 x 2^11 and taking it away): T
+//   where the quotient is T, on its side of T where not; then the conversion instruction
+//   decides.  In the same way the scale, amax / 6 in E4M3 (midpoints of 5 bits), comes from
+//   a product with 1 / 6 rounded to 12 fraction bits.
 //   fp32 x: |x| is compared with T s, which is exact.  (The correctly rounded quotient, by
 //   which the formula decides, is T only if x = T s: the next fp32 values beside T s are
-//   2^-24 of it away at least, and more than half a step of T.)
+//   2^-24 of it away at least, and more than half a step of T.)  The scale is divided.
 //
 // Bound: HBM for large matrices, a chain of loads, reductions and stores for a few rows.
 #include "csa2_fp4.cuh"
@@ -58,10 +61,11 @@ __device__ __forceinline__ uint32_t e2m1x8(const float *y) {
 template <bool kBf16>
 __device__ __forceinline__ uint32_t nv8(const float *x, float s, float back, float fore) {
   if constexpr (kBf16) {
-    const float inv = __fmul_rn(__frcp_rn(s), back);
-    float q[8];
+    float inv, q[8];
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(inv) : "f"(s));
+    inv = __fmul_rn(inv, back);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __uint_as_float((__float_as_uint(__fmul_rn(x[i], inv)) + 0x400u) & ~0x7FFu);
+    for (int i = 0; i < 8; ++i) q[i] = __fadd_rn(__fmaf_rn(x[i], inv, 3072.0f), -3072.0f);
     const uint32_t w = e2m1x8(q);
     return s != 0.0f ? w : 0u;
   } else {
@@ -78,9 +82,19 @@ __device__ __forceinline__ uint32_t nv8(const float *x, float s, float back, flo
     return s != 0.0f ? w : 0u;
   }
 }
-// The scale byte of a group with largest magnitude amax.
-__device__ __forceinline__ uint32_t nv_scale(float amax, float back) {
-  return e4m3_code(__fdiv_rn(__fmul_rn(amax, back), 6.0f));
+// The scale byte of a group with largest magnitude amax, and its value.
+template <bool kBf16>
+__device__ __forceinline__ uint32_t nv_scale(float amax, float back, float &s) {
+  const float a = __fmul_rn(amax, back);
+  float y;
+  if constexpr (kBf16) y = __uint_as_float((__float_as_uint(__fmul_rn(a, 1.0f / 6.0f)) + 0x400u) & ~0x7FFu);
+  else y = __fdiv_rn(a, 6.0f);
+  uint16_t c;
+  uint32_t h;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(c) : "f"(0.0f), "f"(y));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;\n" : "=r"(h) : "h"(c));
+  s = __half2float(__ushort_as_half(static_cast<uint16_t>(h)));
+  return c;
 }
 template <int kN>
 __device__ __forceinline__ float top_abs(const float *v) {
@@ -200,8 +214,9 @@ __global__ void __launch_bounds__(kQThreads) k_fp4_quant_row(F4Args a) {
       if constexpr (kNv) {
         float g = top_abs<8>(v[i]);
         g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
-        code = nv_scale(g, back);
-        w = nv8<kBf16>(v[i], e4m3_value(code), back, fore);
+        float sv;
+        code = nv_scale<kBf16>(g, back, sv);
+        w = nv8<kBf16>(v[i], sv, back, fore);
       } else {
         uint32_t g = top_bits<8>(v[i]);
         g = max(g, __shfl_xor_sync(0xffffffffu, g, 1));
@@ -246,9 +261,9 @@ __device__ __forceinline__ void load16(const uint8_t *row, int c0, int cols, flo
 // Largest magnitude's bits (or a NaN's) of the values in a word: two bf16 or one fp32.
 template <bool kBf16>
 __device__ __forceinline__ uint32_t word_top(uint32_t m, uint32_t w) {
-  if constexpr (kBf16) {  // m: two maxima
+  if constexpr (kBf16) {  // m: two maxima, of any sign
     uint32_t r;
-    asm("max.NaN.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(m), "r"(w & 0x7FFF7FFFu));
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(m), "r"(w));
     return r;
   } else {
     return max(m, w & 0x7FFFFFFFu);
@@ -291,7 +306,7 @@ __global__ void __launch_bounds__(kQThreads, kNv ? 4 : 3) k_fp4_quant_rows(F4Arg
     }
   }
   if constexpr (kNv) {
-    if constexpr (kBf16) m = max(m << 16, m & 0x7FFF0000u);
+    if constexpr (kBf16) m = max(m << 16 & 0x7FFF0000u, m & 0x7FFF0000u);
     m = __reduce_max_sync(0xffffffffu, m);
     if (lane == 0) top[warp] = m;
   }
@@ -316,10 +331,9 @@ __global__ void __launch_bounds__(kQThreads, kNv ? 4 : 3) k_fp4_quant_rows(F4Arg
         uint32_t w[4];
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-          float v[16];
+          float v[16], s;
           load16<kBf16>(src, 32 * (p + i) + 16 * g, have, v);
-          const uint32_t sc = nv_scale(top_abs<16>(v), back);
-          const float s = e4m3_value(sc);
+          const uint32_t sc = nv_scale<kBf16>(top_abs<16>(v), back, s);
           w[2 * g] = nv8<kBf16>(v, s, back, fore);
           w[2 * g + 1] = nv8<kBf16>(v + 8, s, back, fore);
           code |= sc << (16 * i + 8 * g);
@@ -355,80 +369,80 @@ __global__ void __launch_bounds__(kQThreads, kNv ? 4 : 3) k_fp4_quant_rows(F4Arg
   }
 }
 
-// A warp: 8 rows of a tile at a time (16 B of codes a lane, whole lines of 8 rows; 32
-// values a lane out).
+// A warp: 4 rows of a tile at a time, a lane 16 values (8 B of codes), so that a store of
+// the warp is 4 runs of 256 bytes (bf16); two groups of rows a time.
 template <bool kNv, bool kBf16>
 __global__ void __launch_bounds__(256) k_fp4_read(csa2_fp4_matrix mx, void *out, int64_t stride, int wide) {
   next_may_start();
   wait_for_previous();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, u = lane & 7;
   const int ct = static_cast<int>(f4_col_tiles(mx.cols));
-  const int row = blockIdx.x * 8 + (lane & 7), j = lane >> 3;
-  if (row >= mx.rows) return;
-  const int m = row % kF4Rows;
-  const float r = mx.row_scales[row];
-  const uint8_t *tiles = mx.tiles + static_cast<int64_t>(row / kF4Rows) * ct * f4_tile_bytes(kNv);
-#pragma unroll 4
-  for (int k = blockIdx.y * 8 + warp; k < ct; k += 8 * gridDim.y) {
-    const uint8_t *rec = tiles + static_cast<int64_t>(k) * f4_tile_bytes(kNv), *sc = rec + kF4CodeBytes + f4_scale_at(m);
-    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(rec + j * 2048 + m * 16));
-    float s[2];
-    if constexpr (kNv) {
-      const uint32_t c = *reinterpret_cast<const uint16_t *>(sc + 512 * (j >> 1) + 2 * (j & 1));
-      s[0] = e4m3_value(c & 0xFF) * r;
-      s[1] = e4m3_value(c >> 8) * r;
-    } else {
-      s[0] = s[1] = e8m0_value(sc[j]) * r;
-    }
-    const int c0 = kF4Cols * k + 32 * j;
-    const int64_t at = row * stride + c0;
-    const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+  const int row0 = blockIdx.x * 8 + (lane >> 3), m0 = row0 % kF4Rows;  // and row0 + 4, in the same tile
+  const uint8_t *tiles = mx.tiles + static_cast<int64_t>(row0 / kF4Rows) * ct * f4_tile_bytes(kNv);
+  bool there[2];
+  float r[2];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {  // 16 values
+  for (int i = 0; i < 2; ++i) {
+    there[i] = row0 + 4 * i < mx.rows;
+    r[i] = there[i] ? mx.row_scales[row0 + 4 * i] : 0.0f;
+  }
+  for (int k = blockIdx.y * 8 + warp; k < ct; k += 8 * gridDim.y) {
+    const uint8_t *rec = tiles + static_cast<int64_t>(k) * f4_tile_bytes(kNv), *sc = rec + kF4CodeBytes;
+    uint2 w[2];
+    uint32_t c[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int m = m0 + 4 * i;
+      w[i] = there[i] ? __ldg(reinterpret_cast<const uint2 *>(rec + (u >> 1) * 2048 + m * 16 + 8 * (u & 1))) : make_uint2(0, 0);
+      c[i] = there[i] ? (kNv ? sc[512 * (u >> 2) + f4_scale_at(m) + (u & 3)] : sc[f4_scale_at(m) + (u >> 1)]) : 0u;
+    }
+    const int col = kF4Cols * k + 16 * u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (!there[i]) continue;
+      const float s = (kNv ? e4m3_value(c[i]) : e8m0_value(c[i])) * r[i];
+      uint32_t h[8];
+      e2m1x8_h2(w[i].x, h);
+      e2m1x8_h2(w[i].y, h + 4);
       float v[16];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t h[4];
-        e2m1x8_h2(in[2 * half + i], h);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h[q]));
-          v[8 * i + 2 * q] = f.x * s[half];
-          v[8 * i + 2 * q + 1] = f.y * s[half];
-        }
+      for (int q = 0; q < 8; ++q) {
+        const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h[q]));
+        v[2 * q] = f.x * s;
+        v[2 * q + 1] = f.y * s;
       }
-      const int c = c0 + 16 * half;
-      if (c + 16 <= mx.cols) {
+      const int64_t at = (row0 + 4 * i) * stride + col;
+      if (col + 16 <= mx.cols) {
         uint32_t o[16];
         if constexpr (kBf16) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            o[i] = *reinterpret_cast<uint32_t *>(&b);
+          for (int q = 0; q < 8; ++q) {
+            __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
+            o[q] = *reinterpret_cast<uint32_t *>(&b);
           }
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(v[i]);
+          for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(v[q]);
         }
-        uint32_t *dst = kBf16 ? reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(out) + at + 16 * half)
-                              : reinterpret_cast<uint32_t *>(static_cast<float *>(out) + at + 16 * half);
+        uint32_t *dst = kBf16 ? reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(out) + at)
+                              : reinterpret_cast<uint32_t *>(static_cast<float *>(out) + at);
 #pragma unroll
-        for (int i = 0; i < (kBf16 ? 1 : 2); ++i) {
+        for (int q = 0; q < (kBf16 ? 8 : 16); q += 8) {
           if (wide) {
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + 8 * i), "r"(o[8 * i]), "r"(o[8 * i + 1]),
-                         "r"(o[8 * i + 2]), "r"(o[8 * i + 3]), "r"(o[8 * i + 4]), "r"(o[8 * i + 5]), "r"(o[8 * i + 6]), "r"(o[8 * i + 7])
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + q), "r"(o[q]), "r"(o[q + 1]),
+                         "r"(o[q + 2]), "r"(o[q + 3]), "r"(o[q + 4]), "r"(o[q + 5]), "r"(o[q + 6]), "r"(o[q + 7])
                          : "memory");
           } else {
-            reinterpret_cast<uint4 *>(dst + 8 * i)[0] = make_uint4(o[8 * i], o[8 * i + 1], o[8 * i + 2], o[8 * i + 3]);
-            reinterpret_cast<uint4 *>(dst + 8 * i)[1] = make_uint4(o[8 * i + 4], o[8 * i + 5], o[8 * i + 6], o[8 * i + 7]);
+            reinterpret_cast<uint4 *>(dst + q)[0] = make_uint4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+            reinterpret_cast<uint4 *>(dst + q)[1] = make_uint4(o[q + 4], o[q + 5], o[q + 6], o[q + 7]);
           }
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (c + i < mx.cols) {
-            if constexpr (kBf16) static_cast<__nv_bfloat16 *>(out)[at + 16 * half + i] = __float2bfloat16_rn(v[i]);
-            else static_cast<float *>(out)[at + 16 * half + i] = v[i];
+        for (int q = 0; q < 16; ++q)
+          if (col + q < mx.cols) {
+            if constexpr (kBf16) static_cast<__nv_bfloat16 *>(out)[at + q] = __float2bfloat16_rn(v[q]);
+            else static_cast<float *>(out)[at + q] = v[q];
           }
       }
     }
