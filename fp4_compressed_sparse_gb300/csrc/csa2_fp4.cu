@@ -15,9 +15,10 @@
 //   where the quotient is T, on its side of T where not; then the conversion instruction
 //   decides.  In the same way the scale, amax / 6 in E4M3 (midpoints of 5 bits), comes from
 //   a product with 1 / 6 rounded to 12 fraction bits.
-//   fp32 x: |x| is compared with T s, which is exact.  (The correctly rounded quotient, by
-//   which the formula decides, is T only if x = T s: the next fp32 values beside T s are
-//   2^-24 of it away at least, and more than half a step of T.)  The scale is divided.
+//   fp32 x: y = x (1 / s), then y + (x - y s) (1 / s), the remainder exact: off by less than
+//   2^-40 of the quotient before its rounding.  If x = T s that is T.  Else the quotient is
+//   2^-24 of T away from it at least (the next fp32 values beside T s), more than half a
+//   step of T: the rounded one lies on the same side.  The scale is divided.
 //
 // Bound: HBM for large matrices, a chain of loads, reductions and stores for a few rows.
 #include "csa2_fp4.cuh"
@@ -69,16 +70,14 @@ __device__ __forceinline__ uint32_t nv8(const float *x, float s, float back, flo
     const uint32_t w = e2m1x8(q);
     return s != 0.0f ? w : 0u;
   } else {
-    const float u = __fmul_rn(s, fore);
-    const float t0 = 0.25f * u, t1 = 0.75f * u, t2 = 1.25f * u, t3 = 1.75f * u, t4 = 2.5f * u, t5 = 3.5f * u, t6 = 5.0f * u;
-    uint32_t w = 0;
+    const float inv = __fmul_rn(__frcp_rn(s), back), u = __fmul_rn(s, fore);
+    float q[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float a = fabsf(x[i]);
-      uint32_t c = (a > t0) + (a >= t1) + (a > t2) + (a >= t3) + (a > t4) + (a >= t5) + (a > t6);
-      c |= (__float_as_uint(x[i]) >> 28) & 8u;
-      w |= c << (4 * i);
+      const float y = __fmul_rn(x[i], inv);
+      q[i] = __fmaf_rn(__fmaf_rn(-y, u, x[i]), inv, y);
     }
+    const uint32_t w = e2m1x8(q);
     return s != 0.0f ? w : 0u;
   }
 }
@@ -270,38 +269,39 @@ __device__ __forceinline__ uint32_t word_top(uint32_t m, uint32_t w) {
   }
 }
 
-// Many rows: a block per 8 rows (their 16 bytes of a piece are a whole 128 B line).
-// kStaged: the rows are read once, coalesced, a warp per row, into shared memory (row
-// pitch an odd number of 16 bytes, so that 8 rows' loads meet no bank twice); else, when
-// they do not fit there, a second time through the caches.
-template <bool kNv, bool kBf16, bool kStaged>
+// Many rows: a block per kRows rows (8, whose 16 bytes of a piece are a whole 128 B line, 4
+// or 2).  kStaged: the rows are read once, coalesced, 8 / kRows warps per row, into shared
+// memory (row pitch an odd number of 16 bytes, so that 8 rows' loads meet no bank twice);
+// else, when they do not fit there, a second time through the caches.
+template <bool kNv, bool kBf16, bool kStaged, int kRows>
 __global__ void __launch_bounds__(kQThreads, kNv ? 4 : 3) k_fp4_quant_rows(F4Args a, int pitch) {
-  constexpr int kElt = kBf16 ? 2 : 4;
+  constexpr int kElt = kBf16 ? 2 : 4, kParts = 8 / kRows;
   extern __shared__ __align__(16) uint8_t stage[];
   __shared__ uint32_t top[8];
   next_may_start();
   wait_for_previous();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, rows = a.m.rows, cols = a.m.cols;
-  const int row0 = blockIdx.x * 8, r8 = t & 7, row = row0 + r8;  // row: this thread's, once it writes
+  const int row0 = blockIdx.x * kRows, r8 = t % kRows, row = row0 + r8;  // row: this thread's, once it writes
   const uint8_t *x = static_cast<const uint8_t *>(a.x);
   const int ct = static_cast<int>(f4_col_tiles(cols)), pieces = 4 * ct;
   uint32_t bad = 0, m = 0;
-  if ((kNv || kStaged) && row0 + warp < rows) {
-    const uint8_t *src = x + (row0 + warp) * a.stride * kElt;
+  const int own = warp % kRows, part = warp / kRows;  // the row this warp reads (a part of)
+  if ((kNv || kStaged) && row0 + own < rows) {
+    const uint8_t *src = x + (row0 + own) * a.stride * kElt;
     const int whole = cols * kElt & ~15;
 #pragma unroll 8
-    for (int c = 16 * lane; c < whole; c += 512) {
+    for (int c = 16 * (lane + 32 * part); c < whole; c += 512 * kParts) {
       const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src + c));
-      if constexpr (kStaged) *reinterpret_cast<uint4 *>(stage + warp * pitch + c) = u;
+      if constexpr (kStaged) *reinterpret_cast<uint4 *>(stage + own * pitch + c) = u;
       if constexpr (kNv) m = word_top<kBf16>(word_top<kBf16>(word_top<kBf16>(word_top<kBf16>(m, u.x), u.y), u.z), u.w);
     }
     // the last values, and zeros to the end of the last tile
-    for (int c = whole / kElt + lane; c < 32 * pieces; c += 32) {
+    for (int c = whole / kElt + lane + 32 * part; c < 32 * pieces; c += 32 * kParts) {
       const uint32_t u = c >= cols ? 0u : kBf16 ? reinterpret_cast<const uint16_t *>(src)[c] : reinterpret_cast<const uint32_t *>(src)[c];
       if constexpr (kNv) m = word_top<kBf16>(m, u);
       if constexpr (kStaged) {
-        if constexpr (kBf16) reinterpret_cast<uint16_t *>(stage + warp * pitch)[c] = static_cast<uint16_t>(u);
-        else reinterpret_cast<uint32_t *>(stage + warp * pitch)[c] = u;
+        if constexpr (kBf16) reinterpret_cast<uint16_t *>(stage + own * pitch)[c] = static_cast<uint16_t>(u);
+        else reinterpret_cast<uint32_t *>(stage + own * pitch)[c] = u;
       }
     }
   }
@@ -316,14 +316,17 @@ __global__ void __launch_bounds__(kQThreads, kNv ? 4 : 3) k_fp4_quant_rows(F4Arg
   const uint8_t *src = kStaged ? stage + r8 * pitch : x + row * a.stride * kElt;
   const int have = kStaged ? 32 * pieces : cols;
   if constexpr (kNv) {
-    const int e = row_exponent(top[r8], bad);
+    m = top[r8];
+#pragma unroll
+    for (int i = 1; i < kParts; ++i) m = max(m, top[r8 + kRows * i]);
+    const int e = row_exponent(m, bad);
     const float back = pow2f(bad ? 0 : -e), fore = pow2f(bad ? 0 : e);
-    if (row < rows && t < 8) {
+    if (row < rows && t < kRows) {
       a.m.row_scales[row] = bad ? __uint_as_float(kNan) : fore;
       if (bad) raise_err(a.err, CSA2_DEVERR_NAN);
     }
     // two pieces at a time, whose four scales are one word
-    for (int p = 2 * (t >> 3); p < pieces && row < rows; p += 64) {
+    for (int p = 2 * (t / kRows); p < pieces && row < rows; p += 2 * (kQThreads / kRows)) {
       uint8_t *rec = tiles + static_cast<int64_t>(p >> 2) * f4_tile_bytes(true);
       uint32_t code = 0;
 #pragma unroll
@@ -343,7 +346,7 @@ __global__ void __launch_bounds__(kQThreads, kNv ? 4 : 3) k_fp4_quant_rows(F4Arg
       *reinterpret_cast<uint32_t *>(rec + kF4CodeBytes + f4_scale_at(mr) + 512 * ((p >> 1) & 1)) = code;
     }
   } else {
-    for (int p = 2 * (t >> 3); p < pieces && row < rows; p += 64) {
+    for (int p = 2 * (t / kRows); p < pieces && row < rows; p += 2 * (kQThreads / kRows)) {
       uint8_t *rec = tiles + static_cast<int64_t>(p >> 2) * f4_tile_bytes(false);
       uint32_t code = 0;
 #pragma unroll
@@ -362,7 +365,7 @@ __global__ void __launch_bounds__(kQThreads, kNv ? 4 : 3) k_fp4_quant_rows(F4Arg
     __syncthreads();
     if (bad) atomicOr(&top[r8], 1u);
     __syncthreads();
-    if (row < rows && t < 8) {
+    if (row < rows && t < kRows) {
       a.m.row_scales[row] = top[t] ? __uint_as_float(kNan) : 1.0f;
       if (top[t]) raise_err(a.err, CSA2_DEVERR_NAN);
     }
@@ -451,8 +454,16 @@ __global__ void __launch_bounds__(256) k_fp4_read(csa2_fp4_matrix mx, void *out,
 
 }  // namespace
 
+template <bool kNv, bool kBf16, bool kStaged, int kRows>
+static cudaError_t launch_rows(const F4Args &a, int pitch, cudaStream_t s) {
+  const auto kern = k_fp4_quant_rows<kNv, kBf16, kStaged, kRows>;
+  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), kRows * pitch);
+  if (e != cudaSuccess) return e;
+  return launch_after(kern, dim3((a.m.rows + kRows - 1) / kRows), kQThreads, kRows * pitch, 0, s, a, pitch);
+}
 // A block per row up to eight rows per SM (a block per 8 rows would leave SMs idle);
-// above, 8 rows a block, staged while two blocks fit an SM.
+// above, 8 rows a block, or 4 or 2 of longer rows, staged while two blocks fit an SM: 8,192
+// x 8,192 bf16 32 us with 4 against 57 read twice, fp32 with 2 against 111.
 template <bool kNv, bool kBf16>
 static cudaError_t launch_quant(const F4Args &a, cudaStream_t s) {
   if (a.m.rows < 8 * device_sm_count()) {
@@ -461,14 +472,14 @@ static cudaError_t launch_quant(const F4Args &a, cudaStream_t s) {
                     : iter == 3 ? k_fp4_quant_row<kNv, kBf16, 3> : k_fp4_quant_row<kNv, kBf16, 4>;
     return launch_after(kern, dim3(a.m.rows), kQThreads, 0, 0, s, a);
   }
-  const int pitch = static_cast<int>(f4_col_tiles(a.m.cols)) * kF4Cols * (kBf16 ? 2 : 4) + 16, blocks = (a.m.rows + 7) / 8;
-  if (8 * pitch > 112 * 1024) {
-    return launch_after(k_fp4_quant_rows<kNv, kBf16, false>, dim3(blocks), kQThreads, 0, 0, s, a, 0);
+  const int pitch = static_cast<int>(f4_col_tiles(a.m.cols)) * kF4Cols * (kBf16 ? 2 : 4) + 16;
+  constexpr int kMost = 80 * 1024;
+  if (8 * pitch <= kMost) return launch_rows<kNv, kBf16, true, 8>(a, pitch, s);
+  if constexpr (kNv) {  // (MX reads its rows once anyway: 8,192 x 5,120 fp32 43 us against 48 with 4 rows staged)
+    if (4 * pitch <= kMost) return launch_rows<kNv, kBf16, true, 4>(a, pitch, s);
+    if (2 * pitch <= kMost) return launch_rows<kNv, kBf16, true, 2>(a, pitch, s);
   }
-  const auto kern = k_fp4_quant_rows<kNv, kBf16, true>;
-  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), 8 * pitch);
-  if (e != cudaSuccess) return e;
-  return launch_after(kern, dim3(blocks), kQThreads, 8 * pitch, 0, s, a, pitch);
+  return launch_rows<kNv, kBf16, false, 8>(a, 0, s);
 }
 
 csa2_status check_fp4(const csa2_fp4_matrix *m, const char *name) {
