@@ -21,6 +21,11 @@
 //   step of T: the rounded one lies on the same side.  The scale is divided.
 //
 // Bound: HBM for large matrices, a chain of loads, reductions and stores for a few rows.
+// Measured (in a graph): 12,288 x 4,096 bf16 to NV 24 us (5.4 TB/s; issue slots 50 %, DRAM
+// 54 % of peak), read back 24 us (5.4 TB/s); 8,192 x 4,096 bf16 14 us (6.3 TB/s), fp32 28 us
+// (5.5), read 12 us (7.1, L2 holds a part); 32 rows 1.7 us.  At 11.6 instructions per value
+// the same took 31 us, at 14 compares per fp32 value 42: the conversions above are what
+// brought it near the copy rate.
 #include "csa2_fp4.cuh"
 
 namespace csa2 {

@@ -6,11 +6,18 @@
 // the sum.  Operands lie in memory as the MMA reads them, so tiles go to shared memory
 // by bulk copies and nothing is rearranged.
 //
-// k_fp4_split: the weights are the MMA's 128 rows (lane = output column, so a warp's
-// stores are runs of one output row), the tokens its NT columns (all of them, or 128).  The K tiles of an
-// output tile are dealt to the CTAs of a cluster, whose sums are added in rank order
-// through distributed shared memory: no workspace, equal calls give equal bits.
-// Bound: the weights' bytes for few tokens.
+// k_fp4_split, up to 64 tokens or few tiles: the weights are the MMA's 128 rows (lane =
+// output column, so a warp's stores are runs of one output row), the tokens its NT columns
+// (all of them, or 128 at a time).  The K tiles of an output tile are dealt to the CTAs of a
+// cluster, whose sums are added in rank order through distributed shared memory: no
+// workspace, equal calls give equal bits.  Bound: the weights' bytes.  One token by 12,288 x
+// 4,096 5.6 us with the weights in L2 (12.3 cold, 28 MB: a third of the copy rate; launch,
+// tensor memory, first box and the join are 4.5 us of either), 501 tokens x 704 x 4,104 7.7.
+//
+// k_fp4_pair, more: 8,192 x 12,288 x 4,096 NV 121 us (6.8 PFLOP/s, 71 % of the 9.5 PFLOP/s
+// that csa2_mxf4_peak_launch reaches), MX 113; 8,192^3 151 us (7.3).  Without its copies it
+// takes 108 us, without its MMAs 105 (39 KB a stage and SM, 19 TB/s out of L2): two bounds
+// that meet.  Tensor memory that never had to be drained would save 4 us.
 #include "csa2_fp4.cuh"
 #include "csa2_tma.cuh"
 
@@ -266,6 +273,7 @@ __global__ void __launch_bounds__(kSplitThreads)
 //   warp 1      (rank 0) scales to tensor memory, MMAs
 //   warps 4-11  results: the sums are read into registers, which frees the tile's tensor
 //               memory for the next one, then scaled and written
+// (One CTA per tile of 128 x 256, its copies 2 KB pieces: 445 us for 8,192 x 12,288 x 4,096.)
 // A stage is two K tiles (256 columns): a copying thread needs about 0.22 us for a wait,
 // an arming and a copy, whatever its size.  Copies go by tensor maps over the records, so
 // that one fetches a box of several records' codes or scales; what lies behind the last

@@ -6,6 +6,11 @@
 // mma.sync m16n8k16 (tokens are its 16 rows), 16 bytes a lane, whose values are dealt to
 // fragment places by renaming columns (query) or summation indices (value).  The warps of
 // a block share out K and join their sums in shared memory, in order.
+//
+// Measured (in a graph, W in L2): queries of 64 heads of 128, one token 3.8 us, 32 tokens 5.3;
+// values, one token 2.7 (bf16) and 3.0 us (fp32), 32 tokens 3.4 and 4.8.  A launch alone takes
+// 1.4.  With cold caches 7.3 us (one token) and 10.8 us (32 fp32 tokens): four round trips to
+// HBM in a row (position or bounds, operands, sums, stores).
 #include "csa2_latent.cuh"
 
 namespace csa2 {
