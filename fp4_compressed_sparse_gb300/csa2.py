@@ -779,17 +779,20 @@ def query_latent(q, w_uk, pos, rope_cs, out, err=None, stream=None):
 
 
 def value_project(o, w_uv, out, err=None, stream=None):
-    """csa2_value_project: o [total, H, 512] (fp32 or bf16, contiguous), w_uv bf16 [H, dim, 512] (heads may be
+    """csa2_value_project: o [total, H, 512] (fp32 or bf16, rows may be strided), w_uv bf16 [H, dim, 512] (heads may be
     strided) -> out bf16 [total, H*dim] (rows may be strided)."""
     dev = out.get_device()
     H, dim, ws = _heads_at("w_uv", w_uv, dev)
     total, dt = out.shape[0], o.dtype
     os_ = _rows_at("out", out, _BF16, total, H * dim, dev)
-    if o.get_device() != dev or dt not in _FLOATS or o.shape != (total, H, D_LATENT) or not o.is_contiguous():
+    token, head, one = o.stride()
+    if o.get_device() != dev or dt not in _FLOATS or o.shape != (total, H, D_LATENT) or one != 1 or (H > 1 and head != D_LATENT) \
+            or (total > 1 and token < H * D_LATENT):
         _want("o", o, _FLOATS, (total, H, D_LATENT), dev)
+        raise ValueError("o: a token's rows must be contiguous, and tokens must not overlap")
     ew = _err_at(err, dev)
     if total:
-        _submit("csa2_value_project", dev, stream, o.data_ptr(), H * D_LATENT, IN_BF16 if dt is torch.bfloat16 else IN_F32, total,
+        _submit("csa2_value_project", dev, stream, o.data_ptr(), token if total > 1 else H * D_LATENT, IN_BF16 if dt is torch.bfloat16 else IN_F32, total,
                 H, dim, w_uv.data_ptr(), ws, out.data_ptr(), os_, ew)
 
 

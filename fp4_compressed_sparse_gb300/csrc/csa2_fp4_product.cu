@@ -201,14 +201,19 @@ __global__ void __launch_bounds__(kSplitThreads)
   if (warp >= 2) {
     const int q = warp & 3, n = 32 * q + lane;
 #pragma unroll
-    for (int c = 0; c < NT; c += 16) {
-      uint32_t r[16];
+    for (int c = 0; c < NT; c += 32) {
+      uint32_t r[2][16];
       if (nk > 0) {
-        tc::tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * q) << 16) + c, r);
-        tc::tmem_ld_wait_x16(r);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (c + 16 * h < NT) tc::tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * q) << 16) + c + 16 * h, r[h]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (c + 16 * h < NT) tc::tmem_ld_wait_x16(r[h]);
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) part[(c + i) * L::kPitch + n] = nk > 0 ? __uint_as_float(r[i]) : 0.0f;
+      for (int i = 0; i < 32; ++i)
+        if (c + i < NT) part[(c + i) * L::kPitch + n] = nk > 0 ? __uint_as_float(r[i / 16][i % 16]) : 0.0f;
     }
   }
   tc::tc_fence_before();
@@ -216,44 +221,56 @@ __global__ void __launch_bounds__(kSplitThreads)
   // this CTA's share of the tokens: four columns a thread, the ranks' sums in order
   const int n_out = a.w.rows;
   const int per = (NT + ranks - 1) / ranks, c_lo = min(static_cast<int>(rank) * per, NT), c_hi = min(c_lo + per, NT);
-  for (int i = t; i < (c_hi - c_lo) * 32; i += kSplitThreads) {
-    const int c = c_lo + i / 32, n = 4 * (i % 32), m = m0 + c, gn = nt * kF4Rows + n;
-    if (m >= a.x.rows || gn >= n_out) continue;
-    float4 v[8], s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  const int items = (min(c_hi, a.x.rows - m0) - c_lo) * 32;
+  for (int i0 = t; i0 < items; i0 += 2 * kSplitThreads) {  // two at a time, all their loads in flight
+    float4 v[2][8], rn[2];
+    float rm[2];
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k)
-      if (k < ranks) v[k] = ld_cluster4(map_rank(tc::smem_addr(part + c * L::kPitch + n), k));
+    for (int h = 0; h < 2; ++h) {
+      const int i = i0 + h * kSplitThreads, c = c_lo + i / 32, n = 4 * (i % 32), gn = nt * kF4Rows + n;
+      if (i < items && gn < n_out) {
+        rm[h] = a.x.row_scales[m0 + c];
+        rn[h] = *reinterpret_cast<const float4 *>(a.w.row_scales + gn);  // (the plane holds whole tiles of rows)
 #pragma unroll
-    for (uint32_t k = 0; k < 8; ++k)
-      if (k < ranks) {
-        s.x += v[k].x;
-        s.y += v[k].y;
-        s.z += v[k].z;
-        s.w += v[k].w;
+        for (uint32_t k = 0; k < 8; ++k)
+          if (k < ranks) v[h][k] = ld_cluster4(map_rank(tc::smem_addr(part + c * L::kPitch + n), k));
       }
-    const float rm = a.x.row_scales[m];
-    const float4 rn = *reinterpret_cast<const float4 *>(a.w.row_scales + gn);  // (the plane holds whole tiles of rows)
-    s.x *= rm * rn.x;
-    s.y *= rm * rn.y;
-    s.z *= rm * rn.z;
-    s.w *= rm * rn.w;
-    const int64_t at = m * a.stride + gn;
-    if (gn + 4 <= n_out) {
-      if constexpr (kBf16) {
-        __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
-        *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) =
-            make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
-      } else {
-        *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = s;
-      }
-    } else {
-      const float v[4] = {s.x, s.y, s.z, s.w};
+    }
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (gn + j < n_out) {
-          if constexpr (kBf16) static_cast<__nv_bfloat16 *>(a.out)[at + j] = __float2bfloat16_rn(v[j]);
-          else static_cast<float *>(a.out)[at + j] = v[j];
+    for (int h = 0; h < 2; ++h) {
+      const int i = i0 + h * kSplitThreads, c = c_lo + i / 32, n = 4 * (i % 32), gn = nt * kF4Rows + n;
+      if (i >= items || gn >= n_out) continue;
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k)
+        if (k < ranks) {
+          s.x += v[h][k].x;
+          s.y += v[h][k].y;
+          s.z += v[h][k].z;
+          s.w += v[h][k].w;
         }
+      s.x *= rm[h] * rn[h].x;
+      s.y *= rm[h] * rn[h].y;
+      s.z *= rm[h] * rn[h].z;
+      s.w *= rm[h] * rn[h].w;
+      const int64_t at = (m0 + c) * a.stride + gn;
+      if (gn + 4 <= n_out) {
+        if constexpr (kBf16) {
+          __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
+          *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) =
+              make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
+        } else {
+          *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = s;
+        }
+      } else {
+        const float o[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (gn + j < n_out) {
+            if constexpr (kBf16) static_cast<__nv_bfloat16 *>(a.out)[at + j] = __float2bfloat16_rn(o[j]);
+            else static_cast<float *>(a.out)[at + j] = o[j];
+          }
+      }
     }
   }
   cluster_sync();  // no CTA leaves while another reads its sums
@@ -579,25 +596,28 @@ cudaError_t launch_split(const ProductArgs &a, int ranks, cudaStream_t s) {
   return launch_after(kern, grid, kSplitThreads, L::kBytes, ranks, s, a, mw, mx, ms);
 }
 // Which kernel, and how the split one cuts the work.  One GB300, us, NV to bf16, in a graph.
-//   Pairs once 64 CTAs have a tile and more than 64 tokens share it: 501 x 4096 x 8192
-//   (64 CTAs) 15.3 against 16.0 split, 256 x 12288 x 4096 (96) 11.2 against 17.8; below,
-//   256 x 4096 x 8192 (32) 15.1 against 11.6, 64 tokens x 12288 x 4096 10.7 against 8.9.
+//   Pairs once 64 CTAs have a tile (32 for up to 1,024 columns) and more than 64 tokens share
+//   it: 501 x 4096 x 8192 (64 CTAs) 14.3 against 15.6 split, 256 x 12288 x 4096 (96) 10.3
+//   against 18.1, 501 x 2048 x 1024 (32) 6.7 against 7.7; below, 256 x 4096 x 8192 (32) 14.1
+//   against 11.3, 64 tokens x 12288 x 4096 10.0 against 8.1.
 //   Split: the narrowest token tile that holds all tokens (a scale column is of 32 rows
 //   from the record's first on, so several tiles only of 128), then as many ranks as fit
-//   two CTAs per SM: 64 x 12288 x 4096 8.9 with 3 against 11.2 with 1, 1 x 4096 x 8192 5.8
-//   with 8 against 6.0 with 4.  128 tokens: 4 at most, their sums' way through shared
-//   memory costs more: 501 x 704 x 4104 7.7 with 4, 8.1 with 6, 9.5 with 8.
+//   two CTAs per SM: 64 x 12288 x 4096 8.1 with 3 against 12.1 with 1, 1 x 4096 x 8192 5.0
+//   with 8 against 5.9 with 4.  Of 128 tokens, whose sums' way through shared memory counts,
+//   as many as make 100 CTAs, or up to 4 if that is one: 128 x 704 x 4104 6.1 with 8 (48
+//   CTAs) against 6.8 with 4, 501 x 704 x 4104 8.0 with 4 (96) against 9.2 with 8, 256 x 4096
+//   x 8192 11.3 with 4 (256) against 14.5 with 2.
 template <bool kNv, bool kBf16>
 cudaError_t launch_product(const ProductArgs &a, cudaStream_t s) {
   const int m = a.x.rows;
-  const int64_t big = (f4_row_tiles(m) + 1) / 2 * ((a.w.rows + kPairN - 1) / kPairN);
-  if (m > 64 && 2 * big >= 64) return launch_pair<kNv, kBf16>(a, s);
+  const int64_t kt = f4_col_tiles(a.x.cols), big = (f4_row_tiles(m) + 1) / 2 * ((a.w.rows + kPairN - 1) / kPairN);
+  if (m > 64 && 2 * big >= (kt <= 8 ? 32 : 64)) return launch_pair<kNv, kBf16>(a, s);
   const int nt = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
   const int64_t tiles = f4_row_tiles(a.w.rows) * ((m + nt - 1) / nt), per = nt <= 32 ? 4 : 2;
-  const int64_t steps = (f4_col_tiles(a.x.cols) + per - 1) / per, most = 2 * device_sm_count();
+  const int64_t steps = (kt + per - 1) / per, most = 2 * device_sm_count();
   int ranks = 1;
   for (const int r : {2, 3, 4, 6, 8})
-    if (tiles * r <= most && r <= steps && (nt < 128 || r <= 4)) ranks = r;
+    if (r <= steps && tiles * r <= most && (nt < 128 || tiles * r <= 100 || (tiles > 33 && r <= 4))) ranks = r;
   switch (nt) {
     case 16: return launch_split<16, kNv, kBf16>(a, ranks, s);
     case 32: return launch_split<32, kNv, kBf16>(a, ranks, s);

@@ -105,7 +105,8 @@ def test_host_memory(calls, call):
     (_query, dict(pos=Fake(3, dtype=I32))), (_query, dict(rope_cs=Fake(9, 64, 2))), (_query, dict(rope_cs=Fake(9, 32, 2, dtype=BF16))), (_query, dict(out=Fake(3, 4, 512, dtype=BF16))),
     (_query, dict(out=Fake(3, 4, 576))), (_query, dict(out=Fake(3, 4, 576, dtype=BF16, stride=(4 * 600, 600, 1)))),
     (_value, dict(o=Fake(3, 4, 576))), (_value, dict(o=Fake(3, 4, 512, dtype=torch.float16))), (_value, dict(o=Fake(2, 4, 512))), (_value, dict(o=Fake(3, 4, 512, dev=1))),
-    (_value, dict(o=Fake(3, 4, 512, stride=(4 * 520, 520, 1)))), (_value, dict(out=Fake(3, 512))), (_value, dict(out=Fake(3, 500, dtype=BF16))), (_value, dict(w_uv=Fake(3, 128, 512, dtype=BF16))),
+    (_value, dict(o=Fake(3, 4, 512, stride=(4 * 520, 520, 1)))), (_value, dict(o=Fake(3, 4, 512, stride=(2000, 512, 1)))),
+    (_value, dict(o=Fake(3, 4, 512, stride=(4096, 1024, 2)))), (_value, dict(o=Fake(3, 512))), (_value, dict(out=Fake(3, 512))), (_value, dict(out=Fake(3, 500, dtype=BF16))), (_value, dict(w_uv=Fake(3, 128, 512, dtype=BF16))),
     (_quant, dict(x=Fake(3, 95))), (_quant, dict(x=Fake(2, 96))), (_quant, dict(x=Fake(3, 96, dtype=torch.float64))), (_quant, dict(x=Fake(3, 96, dev=1))),
     (_quant, dict(x=Fake(3, 96, stride=(1, 3)))), (_quant, dict(x=Fake(3, 96, stride=(40, 1)))), (_quant, dict(x=Fake(288))),
     (_product, dict(out=Fake(3, 6, dtype=BF16))), (_product, dict(out=Fake(3, 5, dtype=I32))), (_product, dict(w=_matrix(rows=5, dev=1))), (_product, dict(out=Fake(5, 3, dtype=BF16)))])

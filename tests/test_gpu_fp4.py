@@ -188,6 +188,14 @@ def test_product_of_small_integers_is_exact(fmt, M, N):
     assert torch.equal(out.double(), x.double() @ w.double().t())
 
 
+@pytest.mark.parametrize("M", [30, 700, 2100])
+def test_a_matrix_with_itself(M):
+    m = _packed(_rows(M, 264, torch.float32, 3).clamp(-1e3, 1e3), csa2.FP4_NV)
+    out = torch.empty(M, -(-M // 8) * 8, device=DEV)[:, :M]
+    csa2.fp4_product(m, m, out)
+    _within(out, m, m)
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 def test_product_of_nonfinite_rows(fmt):
     """A row with an infinity or NaN makes its row (column) NaN and nothing else; zero rows are zeros."""

@@ -107,7 +107,7 @@ VALUE = [(1, 64, 128), (2, 1, 16), (127, 16, 64), (128, 128, 128), (129, 5, 48),
 def test_value_project(T, H, D, dtype):
     g = torch.Generator(device=DEV).manual_seed(T)
     _, w = _weights(H, D, g)
-    o, err = torch.randn(T, H, 512, generator=g, device=DEV).to(dtype), _err()
+    o, err = torch.randn(T, H * 512 + 24, generator=g, device=DEV).to(dtype)[:, :H * 512].view(T, H, 512), _err()
     out = torch.full((T + 1, H * D + 8), 9.0, dtype=torch.bfloat16, device=DEV)
     csa2.value_project(o, w, out[:T, :H * D], err=err)
     assert int(err) == 0 and (out[T:] == 9).all() and (out[:, H * D:] == 9).all()
