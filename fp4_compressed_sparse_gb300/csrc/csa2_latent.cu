@@ -54,7 +54,7 @@ struct Sync {
   uint64_t pfull[2], pempty[2];  // fp32: the bf16 parts
   uint64_t tfull[2], tempty[2];
   uint32_t tmem;
-  uint32_t loaded;               // stages armed
+  uint32_t loaded, w_loaded;     // stages armed, and copies of W
   int dead;                      // a wait gave up
 };
 
@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
       tc::mbar_init(&sy.tfull[i], 1);
       tc::mbar_init(&sy.tempty[i], 4);
     }
-    sy.loaded = 0;
+    sy.loaded = sy.w_loaded = 0;
     sy.dead = 0;
     tc::fence_mbar_init();
   }
@@ -165,14 +165,15 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
     const int boxes = kQ ? (a.dim + 63) / 64 : kF ? 1 : 2, wide = kF ? 32 : 64;
     const int w_boxes = kQ ? a.np / 64 : kLat / 64, w_box = (kQ ? a.dim : a.np) * 128;
     int64_t held = -1;
-    uint32_t n = 0, st = 0, ph = 1, wn = 0;
+    uint32_t n = 0, st = 0, ph = 1, wn = 0;  // wn: copies of W so far
     bool ok = true;
     for (int64_t u = u0; u < u1 && ok; ++u) {
       const int64_t hp = u / a.tiles;
       const int tile = static_cast<int>(u - hp * a.tiles), h = static_cast<int>(hp / a.parts), part = static_cast<int>(hp % a.parts);
       if (hp != held) {
-        if (held >= 0) ok = wait_all(&sy.wdone, wn++ & 1);
+        if (wn > 0) ok = wait_all(&sy.wdone, (wn - 1) & 1);
         if (!ok) break;
+        ++wn;
         if (el) {
           tc::mbar_expect_tx(&sy.wfull, w_boxes * w_box);
           for (int i = 0; i < w_boxes; ++i)
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
     }
     if (lane == 0) {
       sy.loaded = n;
+      sy.w_loaded = wn;
       if (!ok) gave_up();
     }
   } else if (warp == 1) {
@@ -393,9 +395,11 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
   if (kQ && warp >= 4 && warp < 12 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
   tc::tc_fence_before();
   __syncthreads();
-  if (t == 0 && sy.dead)  // copies still in flight
+  if (t == 0 && sy.dead) {  // copies still in flight
     for (uint32_t i = sy.loaded > S::kStages ? sy.loaded - S::kStages : 0; i < sy.loaded; ++i)
       tc::mbar_wait_bounded(&sy.full[i % S::kStages], (i / S::kStages) & 1, kWaitIters);
+    if (sy.w_loaded > 0) tc::mbar_wait_bounded(&sy.wfull, (sy.w_loaded - 1) & 1, kWaitIters);
+  }
   __syncthreads();
   if (warp == 1) {
     tc::tc_fence_after();
