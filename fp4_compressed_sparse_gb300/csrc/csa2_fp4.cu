@@ -68,10 +68,11 @@ template <bool kBf16>
 __device__ __forceinline__ uint32_t nv8(const float *x, float s, float back, float fore) {
   if constexpr (kBf16) {
     float inv, q[8];
+    constexpr float kGrid = 1.5f * 2048.0f;  // what is added to it is rounded to a multiple of 2^-12
     asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(inv) : "f"(s));
     inv = __fmul_rn(inv, back);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = __fadd_rn(__fmaf_rn(x[i], inv, 3072.0f), -3072.0f);
+    for (int i = 0; i < 8; ++i) q[i] = __fadd_rn(__fmaf_rn(x[i], inv, kGrid), -kGrid);
     const uint32_t w = e2m1x8(q);
     return s != 0.0f ? w : 0u;
   } else {
@@ -296,7 +297,7 @@ __global__ void __launch_bounds__(kQThreads, kNv ? 4 : 3) k_fp4_quant_rows(F4Arg
     const int whole = cols * kElt & ~15;
 #pragma unroll 8
     for (int c = 16 * (lane + 32 * part); c < whole; c += 512 * kParts) {
-      const uint4 u = __ldg(reinterpret_cast<const uint4 *>(src + c));
+      const uint4 u = load_now(reinterpret_cast<const uint4 *>(src + c));
       if constexpr (kStaged) *reinterpret_cast<uint4 *>(stage + own * pitch + c) = u;
       if constexpr (kNv) m = word_top<kBf16>(word_top<kBf16>(word_top<kBf16>(word_top<kBf16>(m, u.x), u.y), u.z), u.w);
     }
@@ -401,7 +402,7 @@ __global__ void __launch_bounds__(256) k_fp4_read(csa2_fp4_matrix mx, void *out,
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int m = m0 + 4 * i;
-      w[i] = there[i] ? __ldg(reinterpret_cast<const uint2 *>(rec + (u >> 1) * 2048 + m * 16 + 8 * (u & 1))) : make_uint2(0, 0);
+      w[i] = there[i] ? load_now(reinterpret_cast<const uint2 *>(rec + (u >> 1) * 2048 + m * 16 + 8 * (u & 1))) : make_uint2(0, 0);
       c[i] = there[i] ? (kNv ? sc[512 * (u >> 2) + f4_scale_at(m) + (u & 3)] : sc[f4_scale_at(m) + (u >> 1)]) : 0u;
     }
     const int col = kF4Cols * k + 16 * u;

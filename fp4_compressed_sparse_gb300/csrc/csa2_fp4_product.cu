@@ -509,7 +509,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         float v[16];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const float4 s = __ldg(reinterpret_cast<const float4 *>(a.w.row_scales + c0 + min(c, (cols - 1) & ~15)) + u);
+          const float4 s = load_now(reinterpret_cast<const float4 *>(a.w.row_scales + c0 + min(c, (cols - 1) & ~15)) + u);
           v[4 * u] = __uint_as_float(r[c + 4 * u]) * (r_m * s.x);
           v[4 * u + 1] = __uint_as_float(r[c + 4 * u + 1]) * (r_m * s.y);
           v[4 * u + 2] = __uint_as_float(r[c + 4 * u + 2]) * (r_m * s.z);

@@ -48,6 +48,29 @@ __host__ __forceinline__ bool aligned16(const void *p) { return (reinterpret_cas
 // reads or writes anything in memory.
 __device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+// Loads of what a kernel before may have written, for kernels launched so: not through the
+// read-only path (the memory changes while such a kernel is resident), and volatile, which
+// keeps them behind wait_for_previous() and lets them pass the kernel's own stores.
+__device__ __forceinline__ uint4 load_now(const uint4 *p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(__cvta_generic_to_global(p)));
+  return v;
+}
+__device__ __forceinline__ float4 load_now(const float4 *p) {
+  float4 v;
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];\n" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(__cvta_generic_to_global(p)));
+  return v;
+}
+__device__ __forceinline__ uint2 load_now(const uint2 *p) {
+  uint2 v;
+  asm volatile("ld.global.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "l"(__cvta_generic_to_global(p)));
+  return v;
+}
+__device__ __forceinline__ uint32_t load_now(const uint32_t *p) {
+  uint32_t v;
+  asm volatile("ld.global.u32 %0, [%1];\n" : "=r"(v) : "l"(__cvta_generic_to_global(p)));
+  return v;
+}
 template <class... P, class... A>
 cudaError_t launch_after(void (*kern)(P...), dim3 grid, int block, size_t smem, int cluster, cudaStream_t s, A &&...args) {
   cudaLaunchConfig_t cfg = {};

@@ -57,7 +57,7 @@ struct Rope8 {
 };
 __device__ __forceinline__ Rope8 load_rope8(const LatentArgs &a, const uint16_t *src, int64_t p, int d8) {
   const float4 *cs = reinterpret_cast<const float4 *>(a.rope + p * kRope + 8 * d8);
-  return Rope8{__ldg(reinterpret_cast<const uint4 *>(src)), __ldg(cs), __ldg(cs + 1)};
+  return Rope8{load_now(reinterpret_cast<const uint4 *>(src)), load_now(cs), load_now(cs + 1)};
 }
 __device__ __forceinline__ void store_rope8(const Rope8 &r, uint16_t *dst) {
   const uint32_t in[4] = {r.v.x, r.v.y, r.v.z, r.v.w};

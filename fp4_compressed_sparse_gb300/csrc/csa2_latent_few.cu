@@ -60,14 +60,14 @@ __global__ void __launch_bounds__(kFewThreads) k_query_few(LatentArgs a) {
     const bool there = ks + 4 * i < steps;
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      r[i][j] = there ? __ldg(reinterpret_cast<const uint4 *>(w + static_cast<int64_t>(k + (j & 1) + 8 * (j >> 1)) * kLat))
+      r[i][j] = there ? load_now(reinterpret_cast<const uint4 *>(w + static_cast<int64_t>(k + (j & 1) + 8 * (j >> 1)) * kLat))
                       : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int m = 0; m < kTiles; ++m)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int64_t tok = tok0 + 16 * m + g + 8 * (j & 1);
-        f[i][m][j] = there && tok < a.total ? __ldg(reinterpret_cast<const uint32_t *>(xh + tok * a.x_stride + k + 8 * (j >> 1))) : 0u;
+        f[i][m][j] = there && tok < a.total ? load_now(reinterpret_cast<const uint32_t *>(xh + tok * a.x_stride + k + 8 * (j >> 1))) : 0u;
       }
   }
   float4 acc[kTiles][8] = {};
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kFewThreads) k_value_few(LatentArgs a) {
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const int j = j0 + 4 * g + v;
-      r[i][v] = j < a.dim ? __ldg(reinterpret_cast<const uint4 *>(w + static_cast<int64_t>(j) * kLat + 32 * i)) : make_uint4(0, 0, 0, 0);
+      r[i][v] = j < a.dim ? load_now(reinterpret_cast<const uint4 *>(w + static_cast<int64_t>(j) * kLat + 32 * i)) : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int m = 0; m < kTiles; ++m)
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kFewThreads) k_value_few(LatentArgs a) {
         if (tok < a.total) {
           if constexpr (kF32) {
             const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.x) + at);
-            const float4 u = __ldg(p), s = __ldg(p + 1);
+            const float4 u = load_now(p), s = load_now(p + 1);
             uint32_t hi[4], lo[4];
             split2(u.x, u.y, hi[0], lo[0]);
             split2(u.z, u.w, hi[1], lo[1]);
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kFewThreads) k_value_few(LatentArgs a) {
             x[i][m][half] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
             xl[i][m][half] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
           } else {
-            x[i][m][half] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + at));
+            x[i][m][half] = load_now(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + at));
           }
         }
       }

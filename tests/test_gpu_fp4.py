@@ -239,3 +239,46 @@ def test_streams_graphs_and_two_calls_at_once(M):
         csa2.fp4_product(n, w, p, stream=other)
         torch.cuda.synchronize()
         assert torch.equal(o, v) and torch.equal(p, want[1])
+
+
+@pytest.mark.parametrize("M,stride", [(20, (1 << 27) + 8), (2600, (1 << 20) + 8)])
+def test_rows_far_apart(M, stride):
+    """Row offsets that pass 32 bits: rows in, values out and sums out, against rows that lie together."""
+    N, K = 2600, 264
+    x = _rows(M, K, torch.bfloat16, 5).clamp(-1e3, 1e3)
+    w = _packed(_rows(N, K, torch.bfloat16, 6).clamp(-1e3, 1e3), csa2.FP4_NV)
+    wide = torch.empty((M - 1) * stride + N, dtype=torch.bfloat16, device=DEV)
+    far = wide.as_strided((M, K), (stride, 1))
+    far.copy_(x)
+    m, n = _packed(far, csa2.FP4_NV), _packed(x, csa2.FP4_NV)
+    v = torch.empty_like(x)
+    csa2.fp4_read(n, v)
+    far.zero_()
+    csa2.fp4_read(m, far)
+    assert torch.equal(far, v)
+    sums, far = torch.empty(M, N, dtype=torch.bfloat16, device=DEV), wide.as_strided((M, N), (stride, 1))
+    csa2.fp4_product(n, w, sums)
+    csa2.fp4_product(m, w, far)
+    assert torch.equal(far, sums)
+
+
+def test_calls_behind_one_another():
+    """Calls whose launches overlap: each reads what the one before has just written, over the same memory
+    again and again, as with the stream emptied in between."""
+    M, N = 40, 264
+    w = _packed(torch.randn(N, N, device=DEV) / 8, csa2.FP4_MX)
+    x0 = torch.randn(M, N, device=DEV)
+    ends = []
+    for wait in (True, False):
+        x, m = x0.clone(), csa2.Fp4Matrix(M, N, csa2.FP4_MX)
+        seen = []
+        for i in range(60):
+            for call in (lambda: csa2.fp4_quant(m, x), lambda: csa2.fp4_product(m, w, x), lambda: csa2.fp4_quant(m, x),
+                         lambda: csa2.fp4_read(m, x)):
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+            if i % 20 == 19:
+                seen.append(x.clone())
+        ends.append(seen)
+    assert all(torch.equal(a, b) for a, b in zip(*ends))

@@ -207,3 +207,47 @@ def test_streams_and_graphs(T):
         torch.cuda.synchronize()
         for r in (res, res2):
             assert torch.equal(r[0], w[0]) and torch.equal(r[1], w[1])
+
+
+@pytest.mark.parametrize("T,stride", [(20, (1 << 27) + 8), (1100, (1 << 21) + 8)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_far_apart(T, stride, dtype):
+    """Row offsets that pass 32 bits, in and out, against rows that lie together."""
+    H, D = 3, 48
+    g = torch.Generator(device=DEV).manual_seed(7)
+    wk, wv = _weights(H, D, g)
+    o = torch.randn(T, H, 512, generator=g, device=DEV).to(dtype)
+    wide = torch.empty((T - 1) * stride + H * 512, dtype=dtype, device=DEV)
+    far = wide.as_strided((T, H, 512), (stride, 512, 1))
+    far.copy_(o)
+    near = torch.empty(T, H * D, dtype=torch.bfloat16, device=DEV)
+    csa2.value_project(o, wv, near)
+    out = torch.empty(T, H * D, dtype=torch.bfloat16, device=DEV)
+    csa2.value_project(far, wv, out)
+    assert torch.equal(out, near)
+    if dtype == torch.float32:
+        return
+    q = torch.randn(T, H * (D + 64), generator=g, device=DEV).to(dtype)
+    far = wide.as_strided((T, H * D), (stride, 1))
+    csa2.value_project(o, wv, far)
+    assert torch.equal(far, near)
+    far = wide.as_strided(q.shape, (stride, 1))
+    far.copy_(q)
+    rope, pos = csa2.rope_table(THETA, 2000), torch.arange(T, device=DEV)
+    a, b = (torch.empty(T, H, 576, dtype=dtype, device=DEV) for _ in range(2))
+    csa2.query_latent(q, wk, pos, rope, a)
+    csa2.query_latent(far, wk, pos, rope, b)
+    assert torch.equal(a, b)
+
+
+def test_query_rows_behind_32_bits():
+    """More than 2^31 elements of queries: the last rows as in a call of their own."""
+    T, H, D = 30100, 128, 16
+    g = torch.Generator(device=DEV).manual_seed(8)
+    w, _ = _weights(H, D, g)
+    q = torch.randn(T, H * (D + 64), generator=g, device=DEV).to(torch.bfloat16)
+    rope, pos = csa2.rope_table(THETA, 40000), torch.arange(T, device=DEV)
+    out, few = (torch.zeros(n, H, 576, dtype=torch.bfloat16, device=DEV) for n in (T, 300))
+    csa2.query_latent(q, w, pos, rope, out)
+    csa2.query_latent(q[-300:], w, pos[-300:].clone(), rope, few)
+    assert torch.equal(out[-300:], few) and out[::1000].any(-1).all()
