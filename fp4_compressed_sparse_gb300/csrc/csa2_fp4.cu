@@ -21,11 +21,13 @@
 //   step of T: the rounded one lies on the same side.  The scale is divided.
 //
 // Bound: HBM for large matrices, a chain of loads, reductions and stores for a few rows.
-// Measured (in a graph): 12,288 x 4,096 bf16 to NV 24 us (5.4 TB/s; issue slots 50 %, DRAM
-// 54 % of peak), read back 24 us (5.4 TB/s); 8,192 x 4,096 bf16 14 us (6.3 TB/s), fp32 28 us
-// (5.5), read 12 us (7.1, L2 holds a part); 32 rows 1.7 us.  At 11.6 instructions per value
-// the same took 31 us, at 14 compares per fp32 value 42: the conversions above are what
-// brought it near the copy rate.
+// Measured (in a graph): 12,288 x 4,096 bf16 to NV 22.5 us (5.7 TB/s), read back 21.9 us (5.9
+// TB/s; a plain fill of its 100 MB takes 25.7); 8,192 x 4,096 bf16 13.4 us (6.4 TB/s), fp32 28
+// us (5.5), to MX 13.5 and 25.7, read 11.2 us (7.7, L2 holds a part); 32 rows 1.7 us.  At 11.6
+// instructions per value the first took 31 us, at 14 compares per fp32 value 42 of 8,192 x
+// 4,096: the conversions above are what brought them near the copy rate.
+#include <type_traits>
+
 #include "csa2_fp4.cuh"
 
 namespace csa2 {
@@ -275,7 +277,7 @@ __device__ __forceinline__ uint32_t word_top(uint32_t m, uint32_t w) {
   }
 }
 
-// Many rows: a block per kRows rows (8, whose 16 bytes of a piece are a whole 128 B line, 4
+// More rows: a block per kRows rows (8, whose 16 bytes of a piece are a whole 128 B line, 4
 // or 2).  kStaged: the rows are read once, coalesced, 8 / kRows warps per row, into shared
 // memory (row pitch an odd number of 16 bytes, so that 8 rows' loads meet no bank twice);
 // else, when they do not fit there, a second time through the caches.
@@ -378,6 +380,99 @@ __global__ void __launch_bounds__(kQThreads, kNv ? 4 : 3) k_fp4_quant_rows(F4Arg
   }
 }
 
+// Many rows to MX: persistent blocks, kRows rows at a time, which come by bulk copies into
+// one of two buffers while the other one's are quantised (for NV, whose codes wait for the
+// row's maximum, this gained nothing: 12,288 x 4,096 22.3 us against 22.5).
+struct RowsSync {
+  uint64_t full[2];
+  uint32_t bad[kQThreads / 32];
+};
+template <bool kBf16, int kRows>
+__global__ void __launch_bounds__(kQThreads, 3) k_fp4_quant_mx(F4Args a, int pitch) {
+  constexpr int kElt = kBf16 ? 2 : 4, kPolls = 200;  // suspended polls of <= 1 ms each
+  using Word = std::conditional_t<kBf16, uint16_t, uint32_t>;
+  extern __shared__ __align__(16) uint8_t stage[];
+  __shared__ __align__(8) RowsSync sy;
+  const int t = threadIdx.x, rows = a.m.rows, cols = a.m.cols, ct = static_cast<int>(f4_col_tiles(cols)), pieces = 4 * ct;
+  const int whole = cols * kElt & ~15, w0 = whole / kElt, tail = cols - w0;  // what the copies bring; the values behind it, < 8
+  const int items = (rows + kRows - 1) / kRows, per = static_cast<int>(gridDim.x), r8 = t % kRows;
+  const uint8_t *x = static_cast<const uint8_t *>(a.x);
+  if (t == 0) {
+    tc::mbar_init(&sy.full[0], 1);
+    tc::mbar_init(&sy.full[1], 1);
+    tc::fence_mbar_init();
+  }
+  for (int i = 0; i < 2 * kRows; ++i)  // zeros to the end of the last tile, once
+    for (int c = cols + t; c < 32 * pieces; c += kQThreads) reinterpret_cast<Word *>(stage + i * pitch)[c] = 0;
+  __syncthreads();
+  next_may_start();
+  wait_for_previous();
+  auto fetch = [&](int item, int b) {
+    const int n = min(kRows, rows - item * kRows);
+    tc::mbar_expect_tx(&sy.full[b], n * whole);
+    for (int i = 0; i < n && whole > 0; ++i)
+      tc::bulk_load(tc::smem_addr(stage + (b * kRows + i) * pitch), x + (item * kRows + i) * a.stride * kElt, whole, &sy.full[b]);
+  };
+  // the last values of a row, taken an item ahead: thread (row, value) of the first 8 kRows
+  const int tr = t / 8, tc8 = t % 8;
+  auto last = [&](int item) -> Word {
+    const int row = item * kRows + tr;
+    return tr < kRows && tc8 < tail && row < rows ? reinterpret_cast<const Word *>(x + row * a.stride * kElt)[w0 + tc8] : 0;
+  };
+  Word end = last(blockIdx.x);
+  if (t == 0)
+    for (int b = 0; b < 2; ++b)
+      if (static_cast<int>(blockIdx.x) + b * per < items) fetch(blockIdx.x + b * per, b);
+  int it = 0;
+  for (int item = blockIdx.x; item < items; item += per, ++it) {
+    const int row = item * kRows + r8, buf = it & 1, m = row % kF4Rows;
+    uint8_t *st = stage + buf * kRows * pitch;
+    if (tr < kRows && tc8 < tail) reinterpret_cast<Word *>(st + tr * pitch)[w0 + tc8] = end;
+    const bool ok = tc::mbar_wait_bounded(&sy.full[buf], (it >> 1) & 1, kPolls);
+    if (!__syncthreads_and(ok)) {  // (no copy may land later)
+      if (t == 0) {
+        raise_err(a.err, CSA2_DEVERR_TIMEOUT);
+        tc::mbar_wait_bounded(&sy.full[buf], (it >> 1) & 1, kPolls);
+        if (item + per < items) tc::mbar_wait_bounded(&sy.full[buf ^ 1], ((it + 1) >> 1) & 1, kPolls);
+      }
+      break;
+    }
+    end = last(item + per);
+    uint8_t *tiles = a.m.tiles + static_cast<int64_t>(row / kF4Rows) * ct * f4_tile_bytes(false);
+    const uint8_t *src = st + r8 * pitch;
+    uint32_t bad = 0;
+    // two pieces at a time, whose scales are half a word
+    for (int p = 2 * (t / kRows); p < pieces && row < rows; p += 2 * (kQThreads / kRows)) {
+      uint8_t *rec = tiles + static_cast<int64_t>(p >> 2) * f4_tile_bytes(false);
+      uint32_t code = 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t w[4];
+        float v[32];
+        load16<kBf16>(src, 32 * (p + i), 32 * pieces, v);
+        load16<kBf16>(src, 32 * (p + i) + 16, 32 * pieces, v + 16);
+        code |= mx32(v, bad, w) << (8 * i);
+        *reinterpret_cast<uint4 *>(rec + ((p + i) & 3) * 2048 + m * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      *reinterpret_cast<uint16_t *>(rec + kF4CodeBytes + f4_scale_at(m) + (p & 3)) = static_cast<uint16_t>(code);
+    }
+    // bad: of any thread of the row (threads of equal t % kRows), a bit each
+    uint32_t mask = bad ? 1u << r8 : 0u;
+    mask = __reduce_or_sync(0xffffffffu, mask);
+    if ((t & 31) == 0) sy.bad[t >> 5] = mask;
+    __syncthreads();  // the buffer has been read, too
+    if (t == 0 && item + 2 * per < items) fetch(item + 2 * per, buf);
+    if (t < kRows && row < rows) {
+      mask = 0;
+#pragma unroll
+      for (int i = 0; i < kQThreads / 32; ++i) mask |= sy.bad[i];
+      mask = mask >> r8 & 1u;
+      a.m.row_scales[row] = mask ? __uint_as_float(kNan) : 1.0f;
+      if (mask) raise_err(a.err, CSA2_DEVERR_NAN);
+    }
+  }
+}
+
 // A warp: 4 rows of a tile at a time, a lane 16 values (8 B of codes), so that a store of
 // the warp is 4 runs of 256 bytes (bf16); two groups of rows a time.
 template <bool kNv, bool kBf16>
@@ -467,23 +562,46 @@ static cudaError_t launch_rows(const F4Args &a, int pitch, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   return launch_after(kern, dim3((a.m.rows + kRows - 1) / kRows), kQThreads, kRows * pitch, 0, s, a, pitch);
 }
-// A block per row up to eight rows per SM (a block per 8 rows would leave SMs idle);
-// above, 8 rows a block, or 4 or 2 of longer rows, staged while two blocks fit an SM: 8,192
-// x 8,192 bf16 32 us with 4 against 57 read twice, fp32 with 2 against 111.
+template <bool kBf16, int kRows>
+static cudaError_t launch_mx(const F4Args &a, int pitch, cudaStream_t s) {
+  const auto kern = k_fp4_quant_mx<kBf16, kRows>;
+  const int bytes = 2 * kRows * pitch, items = (a.m.rows + kRows - 1) / kRows;
+  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), bytes);
+  if (e != cudaSuccess) return e;
+  const int fit = 227 * 1024 / (bytes + 2048), most = (fit < 3 ? fit : 3) * device_sm_count();
+  return launch_after(kern, dim3(items < most ? items : most), kQThreads, bytes, 0, s, a, pitch);
+}
+// Which kernel.  One GB300, us, in a graph.
+//   Up to eight rows per SM a block per row (a block per 8 rows would leave SMs idle).
+//   From 32 rows per SM on, 8 rows a block while four blocks fit an SM (MX: five, as its
+//   other kernel is the better one sooner): NV 8,192 x 3,000 bf16 11.6 against 14.0 with 4 rows,
+//   2,000 x 3,000 6.5 against 4.5; MX 8,192 x 2,048 7.8 against 9.5, x 3,000 13.4 against 12.0.
+//   NV else 4 rows staged, or 2, while two blocks fit an SM: 12,288 x 4,096 bf16 22.5 with 4
+//   against 24.0 with 8; 8,192 x 8,192 bf16 32 with 4 against 57 read twice, fp32 with 2
+//   62 against 111.
+//   MX else by k_fp4_quant_mx, 4 rows while three blocks fit an SM (8,192 x 8,192 bf16 34.7
+//   with 4 and one block, 29.5 with 2), else 2: 8,192 x 4,096 fp32 25.7 against 32.8 read as
+//   they come, x 12,288 74 against 92; bf16 with one block an SM only of few rows: 1,300 x
+//   20,000 16.7 against 28.8, 8,192 x 20,000 87 against 78.
 template <bool kNv, bool kBf16>
 static cudaError_t launch_quant(const F4Args &a, cudaStream_t s) {
-  if (a.m.rows < 8 * device_sm_count()) {
+  const int sms = device_sm_count();
+  if (a.m.rows < 8 * sms) {
     const int64_t iter = (f4_col_tiles(a.m.cols) * kF4Cols + 8 * kQThreads - 1) / (8 * kQThreads);
     const auto kern = iter <= 1 ? k_fp4_quant_row<kNv, kBf16, 1> : iter == 2 ? k_fp4_quant_row<kNv, kBf16, 2>
                     : iter == 3 ? k_fp4_quant_row<kNv, kBf16, 3> : k_fp4_quant_row<kNv, kBf16, 4>;
     return launch_after(kern, dim3(a.m.rows), kQThreads, 0, 0, s, a);
   }
+  constexpr int kK = 1024;
   const int pitch = static_cast<int>(f4_col_tiles(a.m.cols)) * kF4Cols * (kBf16 ? 2 : 4) + 16;
-  constexpr int kMost = 80 * 1024;
-  if (8 * pitch <= kMost) return launch_rows<kNv, kBf16, true, 8>(a, pitch, s);
-  if constexpr (kNv) {  // (MX reads its rows once anyway: 8,192 x 5,120 fp32 43 us against 48 with 4 rows staged)
-    if (4 * pitch <= kMost) return launch_rows<kNv, kBf16, true, 4>(a, pitch, s);
-    if (2 * pitch <= kMost) return launch_rows<kNv, kBf16, true, 2>(a, pitch, s);
+  const bool many = a.m.rows >= 32 * sms;
+  if (many && 8 * pitch <= (kNv ? 50 : 40) * kK) return launch_rows<kNv, kBf16, true, 8>(a, pitch, s);
+  if constexpr (kNv) {
+    if (4 * pitch <= 80 * kK) return launch_rows<kNv, kBf16, true, 4>(a, pitch, s);
+    if (2 * pitch <= 80 * kK) return launch_rows<kNv, kBf16, true, 2>(a, pitch, s);
+  } else {
+    if (4 * pitch <= 36 * kK) return launch_mx<kBf16, 4>(a, pitch, s);
+    if (2 * pitch <= (kBf16 && many ? 55 : 110) * kK) return launch_mx<kBf16, 2>(a, pitch, s);
   }
   return launch_rows<kNv, kBf16, false, 8>(a, 0, s);
 }
@@ -543,7 +661,8 @@ csa2_status csa2_fp4_read(const csa2_fp4_matrix *m, void *out, int64_t out_strid
   CSA2_REQUIRE_PTR(out);
   const int ct = static_cast<int>(csa2::f4_col_tiles(m->cols)), row_blocks = (m->rows + 7) / 8;
   int split = (4 * csa2::device_sm_count() + row_blocks - 1) / row_blocks;  // few rows: their tiles over more blocks
-  split = split < 1 ? 1 : split > (ct + 7) / 8 ? (ct + 7) / 8 : split;
+  split = split < 2 ? 2 : split;  // (12,288 x 4,096 21.9 us against 23.6 in one, 8,192 x 4,096 11.2 against 12.2)
+  split = split > (ct + 7) / 8 ? (ct + 7) / 8 : split;
   const int wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && out_stride % (out_dtype == CSA2_OUT_BF16 ? 16 : 8) == 0;
   const dim3 grid(row_blocks, split);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

@@ -582,7 +582,7 @@ size_t csa2_fp4_plane_bytes(int32_t rows, int32_t cols, int32_t format, int32_t 
  * x + t * x_stride elements (x_stride >= cols, a multiple of 8), into the matrix m.
  * csa2_fp4_read: the values m stands for, out_dtype (CSA2_OUT_*), rows out_stride
  * elements apart (>= cols, a multiple of 8); exact in fp32, and in bf16 too.
- * Device errors (quant): NAN.
+ * Device errors (quant): NAN, TIMEOUT.
  */
 csa2_status csa2_fp4_quant(const csa2_fp4_matrix *m, const void *x, int64_t x_stride, int32_t in_dtype, int32_t *err_word,
                            csa2_stream_t stream);

@@ -51,7 +51,8 @@ def _packed(x, fmt, err=None):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 128), (3, 136), (17, 31), (130, 520), (129, 4104), (2000, 264), (1300, 2056), (1217, 130), (1400, 6000), (1290, 17000),
                                        (7, 8192), (9, 8200), (2, 20000), (5, 2049), (3, 6144), (1221, 500),
-                                       (1220, 1000), (1300, 4096), (1219, 4100), (1225, 8192), (1218, 8200), (1219, 10400)])
+                                       (1220, 1000), (1300, 4096), (1219, 4100), (1225, 8192), (1218, 8200), (1219, 10400),
+                                       (1221, 5), (1250, 8), (1231, 20003), (1229, 2050), (4900, 136), (4871, 2050), (4866, 3001), (5003, 4099), (4865, 14200)])
 def test_quant_is_the_definition(fmt, dtype, rows, cols):
     """Codes and scales as values, equal; read back in both types; strided rows; columns behind the
     last one of the tile are zeros."""
@@ -95,7 +96,7 @@ def test_nv_codes_at_every_midpoint(dtype):
 @pytest.mark.parametrize("fmt", FMTS)
 def test_quant_extreme_rows(fmt):
     """The largest and least magnitudes, and rows of infinities and NaN: NaN wholly, the others untouched."""
-    x = torch.randn(1500, 96, device=DEV)
+    x = torch.randn(5001, 96, device=DEV)
     x[0] *= 2.0 ** 60
     x[1] *= 2.0 ** -100
     x[2] *= 2.0 ** -140
@@ -104,7 +105,7 @@ def test_quant_extreme_rows(fmt):
     x[7] = torch.nextafter(torch.tensor(2688.0 * 2.0 ** 62), torch.tensor(math.inf)).item()
     x[8] = torch.finfo(torch.float32).max
     x[9] = 2.0 ** -149
-    for rows in (12, 1500):
+    for rows in (12, 1500, 5001):
         err, y = _err(), x[:rows]
         m = _packed(y, fmt, err)
         want = fu.quantised(y, fmt)
