@@ -134,12 +134,12 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
   if (t == 0) {
     for (int i = 0; i < 4; ++i) {
       tc::mbar_init(&sy.full[i], 1);
-      tc::mbar_init(&sy.empty[i], kF ? 8 : 1);
+      tc::mbar_init(&sy.empty[i], kF ? 4 : 1);
     }
     tc::mbar_init(&sy.wfull, 1);
     tc::mbar_init(&sy.wdone, 1);
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sy.pfull[i], 8);
+      tc::mbar_init(&sy.pfull[i], 4);
       tc::mbar_init(&sy.pempty[i], 1);
       tc::mbar_init(&sy.tfull[i], 1);
       tc::mbar_init(&sy.tempty[i], 4);
@@ -362,23 +362,31 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
     }
   } else if (kF && warp >= 12) {
     // ------------------------------------------------------------ fp32 stages to bf16 parts
-    const int r8 = lane & 7, uo = lane >> 3, cw = warp - 12;
-    const uint32_t n_all = static_cast<uint32_t>(u1 - u0) * chunks;
+    // (two groups of four warps, each every second stage and one of the two buffers: while
+    // one waits the other splits)
+    const int r8 = lane & 7, uo = lane >> 3, cw = warp & 3;
+    const uint32_t n_all = static_cast<uint32_t>(u1 - u0) * chunks, pb = (warp - 12) >> 2;
     bool ok = true;
-    for (uint32_t n = 0; n < n_all; ++n) {
-      const uint32_t st = n % S::kStages, pb = n & 1;
+    for (uint32_t n = pb; n < n_all; n += 2) {
+      const uint32_t st = n % S::kStages;
       ok = wait_all(&sy.full[st], (n / S::kStages) & 1) && (n < 2 || wait_all(&sy.pempty[pb], ((n >> 1) - 1) & 1));
       if (!ok) break;
       const uint32_t src = s_x + st * S::kStage, dst = s_p + pb * 16384;
+      float4 v[4][2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 8 * (cw + 8 * i) + r8;
-        const float4 v0 = lds4(src + r * 128 + (((2 * uo) ^ r8) << 4)), v1 = lds4(src + r * 128 + (((2 * uo + 1) ^ r8) << 4));
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * (cw + 4 * i) + r8;
+        v[i][0] = lds4(src + r * 128 + (((2 * uo) ^ r8) << 4));
+        v[i][1] = lds4(src + r * 128 + (((2 * uo + 1) ^ r8) << 4));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 8 * (cw + 4 * i) + r8;
         uint32_t hi[4], lo[4];
-        split2(v0.x, v0.y, hi[0], lo[0]);
-        split2(v0.z, v0.w, hi[1], lo[1]);
-        split2(v1.x, v1.y, hi[2], lo[2]);
-        split2(v1.z, v1.w, hi[3], lo[3]);
+        split2(v[i][0].x, v[i][0].y, hi[0], lo[0]);
+        split2(v[i][0].z, v[i][0].w, hi[1], lo[1]);
+        split2(v[i][1].x, v[i][1].y, hi[2], lo[2]);
+        split2(v[i][1].z, v[i][1].w, hi[3], lo[3]);
         const uint32_t at = dst + uo * (kTok * 16) + r * 16;
         sts4(at, hi);
         sts4(at + 8192, lo);
