@@ -35,23 +35,26 @@ constexpr int kWBytes = 128 * kLat * 2;     // 128 KB: a head's W, or a part of 
 constexpr int kBox = kTok * 128;            // 128 rows of 128 bytes, 128-byte swizzle
 enum Mode { kQuery, kValue, kValueF32 };
 
-// Beside W: stages of the tokens' rows, for fp32 latents the bf16 parts that are made of
-// them, for queries what is on its way out.  A stage is what one wait and arming of the copying thread (0.2 us) is
+// Beside W: stages of the tokens' rows, and for queries what is on its way out.  A stage is what one wait and arming of the copying thread (0.2 us) is
 // worth: 32 KB, two boxes of 64 columns (query: all of a tile's; value: a quarter), fp32:
 // one of 32.
 template <Mode kM>
 struct Shape {
   static constexpr int kStage = kM == kValueF32 ? kBox : 2 * kBox;
-  static constexpr int kStages = kM == kValueF32 ? 4 : kM == kQuery ? 2 : 3;
-  static constexpr int kParts = kM == kValue ? 0 : 2;  // fp32: buffers of 16 KB, hi then lo; query: 4 KB per writing warp
-  static constexpr int kBytes = kWBytes + kStages * kStage + kParts * 16384 + 1024;
+  static constexpr int kStages = kM == kValueF32 ? 6 : kM == kQuery ? 2 : 3;
+  static constexpr int kOut = kM == kQuery ? 8 * 4096 : 0;  // 4 KB per writing warp
+  static constexpr int kBytes = kWBytes + kStages * kStage + kOut + 1024;
   static constexpr int kMoreWarps = kM == kValue ? 0 : 8;  // that rotate, or split
   static constexpr int kThreads = 32 * (12 + kMoreWarps);
 };
+// fp32 latents: their bf16 parts lie in tensor memory, as the MMA's rows, hi in 16 columns of
+// a buffer and lo in the next 16.  Four buffers fill the columns 128 to 255 that the first
+// accumulator leaves.
+constexpr int kPartBufs = 4, kPartCol = 128;
 struct Sync {
-  uint64_t full[4], empty[4];
+  uint64_t full[6], empty[6];
   uint64_t wfull, wdone;         // W has landed; the last MMAs that read it are done
-  uint64_t pfull[2], pempty[2];  // fp32: the bf16 parts
+  uint64_t pfull[kPartBufs], pempty[kPartBufs];  // fp32: the bf16 parts
   uint64_t tfull[2], tempty[2];
   uint32_t tmem;
   uint32_t loaded, w_loaded;     // stages armed, and copies of W
@@ -87,6 +90,20 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t a, uint64_t b, uin
       "l"(a), "l"(b), "r"(idesc), "r"(acc)
       : "memory");
 }
+// The same with its rows in tensor memory (a lane each, two values a column).
+__device__ __forceinline__ void mma_bf16_rows(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 // 128-byte swizzle.  K-major: sbo between 8-row groups.  MN-major (64 values of N per
 // row, a row per k): lbo between 64-value blocks along N, sbo between groups of 8 k.
 __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
@@ -111,8 +128,7 @@ __device__ __forceinline__ void sts4(uint32_t at, const uint32_t *v) {
 //   warps 4-11   read the sums out of tensor memory and write them: two groups of four,
 //                one per accumulator
 //   warps 12-    query: rotate the RoPE dims, from global memory to global memory;
-//                fp32 latents: split a stage into bf16 parts hi and lo (no swizzle: core
-//                matrices of 8 rows x 16 bytes)
+//                fp32 latents: split a stage into bf16 parts hi and lo in tensor memory
 template <Mode kM>
 __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
     k_latent(LatentArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
@@ -132,15 +148,17 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
     tc::tmem_relinquish();
   }
   if (t == 0) {
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < S::kStages; ++i) {
       tc::mbar_init(&sy.full[i], 1);
       tc::mbar_init(&sy.empty[i], kF ? 4 : 1);
+    }
+    for (int i = 0; i < kPartBufs; ++i) {
+      tc::mbar_init(&sy.pfull[i], 4);
+      tc::mbar_init(&sy.pempty[i], 1);
     }
     tc::mbar_init(&sy.wfull, 1);
     tc::mbar_init(&sy.wdone, 1);
     for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&sy.pfull[i], 4);
-      tc::mbar_init(&sy.pempty[i], 1);
       tc::mbar_init(&sy.tfull[i], 1);
       tc::mbar_init(&sy.tempty[i], 4);
     }
@@ -229,11 +247,11 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
                 mma_bf16(d, dx + (((s >> 2) * kBox + 32 * (s & 3)) >> 4), dw + (2048 * s >> 4), id, s > 0 ? 1u : 0u);
             } else if constexpr (kF) {
               const uint64_t dw = desc_sw128(s_w + (c >> 1) * a.np * 128, 16, 1024) + (64 * (c & 1) >> 4);
-              const uint64_t dx = tc::smem_desc_noswizzle(s_p + st * 16384, 2048, 128);
+              const uint32_t tx = tmem + kPartCol + 32 * st;
 #pragma unroll
               for (int s = 0; s < 2; ++s) {
-                mma_bf16(d, dx + (4096 * s >> 4), dw + (32 * s >> 4), id, c + s > 0 ? 1u : 0u);
-                mma_bf16(d, dx + ((8192 + 4096 * s) >> 4), dw + (32 * s >> 4), id, 1u);
+                mma_bf16_rows(d, tx + 8 * s, dw + (32 * s >> 4), id, c + s > 0 ? 1u : 0u);
+                mma_bf16_rows(d, tx + 16 + 8 * s, dw + (32 * s >> 4), id, 1u);
               }
             } else {
               const uint64_t dx = desc_sw128(s_x + st * S::kStage, 16, 1024);
@@ -249,7 +267,7 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
             }
           }
           __syncwarp();
-          if (b == jobs - 1 && ++st == (kF ? 2 : S::kStages)) {
+          if (b == jobs - 1 && ++st == (kF ? kPartBufs : S::kStages)) {
             st = 0;
             ph ^= 1;
           }
@@ -362,41 +380,32 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
     }
   } else if (kF && warp >= 12) {
     // ------------------------------------------------------------ fp32 stages to bf16 parts
-    // (two groups of four warps, each every second stage and one of the two buffers: while
-    // one waits the other splits)
-    const int r8 = lane & 7, uo = lane >> 3, cw = warp & 3;
-    const uint32_t n_all = static_cast<uint32_t>(u1 - u0) * chunks, pb = (warp - 12) >> 2;
+    // (two groups of four warps, each every second stage: while one waits the other splits; a
+    // lane takes a token's 32 values)
+    const int r8 = lane & 7;
+    const uint32_t n_all = static_cast<uint32_t>(u1 - u0) * chunks, quarter = 32 * (warp & 3);
     bool ok = true;
-    for (uint32_t n = pb; n < n_all; n += 2) {
-      const uint32_t st = n % S::kStages;
-      ok = wait_all(&sy.full[st], (n / S::kStages) & 1) && (n < 2 || wait_all(&sy.pempty[pb], ((n >> 1) - 1) & 1));
+    for (uint32_t n = (warp - 12) >> 2; n < n_all; n += 2) {
+      const uint32_t st = n % S::kStages, pb = n % kPartBufs, use = n / kPartBufs;
+      ok = wait_all(&sy.full[st], (n / S::kStages) & 1) && (use == 0 || wait_all(&sy.pempty[pb], (use - 1) & 1));
       if (!ok) break;
-      const uint32_t src = s_x + st * S::kStage, dst = s_p + pb * 16384;
-      float4 v[4][2];
+      tc::tc_fence_after();
+      const uint32_t src = s_x + st * S::kStage + (quarter + lane) * 128, dst = tmem + (quarter << 16) + kPartCol + 32 * pb;
+      uint32_t hi[16], lo[16];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * (cw + 4 * i) + r8;
-        v[i][0] = lds4(src + r * 128 + (((2 * uo) ^ r8) << 4));
-        v[i][1] = lds4(src + r * 128 + (((2 * uo + 1) ^ r8) << 4));
+      for (int i = 0; i < 8; ++i) {
+        const float4 v = lds4(src + ((i ^ r8) << 4));
+        split2(v.x, v.y, hi[2 * i], lo[2 * i]);
+        split2(v.z, v.w, hi[2 * i + 1], lo[2 * i + 1]);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * (cw + 4 * i) + r8;
-        uint32_t hi[4], lo[4];
-        split2(v[i][0].x, v[i][0].y, hi[0], lo[0]);
-        split2(v[i][0].z, v[i][0].w, hi[1], lo[1]);
-        split2(v[i][1].x, v[i][1].y, hi[2], lo[2]);
-        split2(v[i][1].z, v[i][1].w, hi[3], lo[3]);
-        const uint32_t at = dst + uo * (kTok * 16) + r * 16;
-        sts4(at, hi);
-        sts4(at + 8192, lo);
-      }
-      tc::fence_proxy_async_smem();  // read by the tensor cores
+      tmem_st_x16(dst, hi);
+      tmem_st_x16(dst + 16, lo);
       __syncwarp();
-      if (lane == 0) {
-        tc::mbar_arrive(&sy.pfull[pb]);
-        tc::mbar_arrive(&sy.empty[st]);
-      }
+      if (lane == 0) tc::mbar_arrive(&sy.empty[st]);
+      asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&sy.pfull[pb]);
     }
     if (!ok && lane == 0) gave_up();
   }
