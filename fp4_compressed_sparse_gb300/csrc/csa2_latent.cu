@@ -11,7 +11,7 @@
 // third of what the tensor cores need to be the bound.  HBM bounds long batches, the
 // chain of loads short ones.
 //
-// Two forms, by the number of tokens (both sides' times stand at kFewQuery): a block per
+// Two forms, by the number of tokens (both sides' times stand at few_queries): a block per
 // head and column part with everything in flight at once (csa2_latent_few.cu), and the
 // persistent kernel of this file.  fp32 latents are split into bf16 parts hi + lo, each
 // multiplied: what is lost is 2^-16 of a value, against 2^-8 that the bf16 result's
@@ -19,7 +19,7 @@
 //
 // Measured (in a graph, caches as the calls before leave them): 4,001 tokens of 64 heads of
 // 128: queries 74 us (403 MB, 5.4 TB/s, 80 % of the measured copy rate), values bf16 56 us
-// (336 MB, 6.0 TB/s, 88 %), fp32 117 us (599 MB, 5.1 TB/s); 128 tokens: 6.8, 5.5 and 11.5 us.
+// (336 MB, 6.0 TB/s, 88 %), fp32 99 us (599 MB, 6.1 TB/s); 128 tokens: 5.8, 4.6 and 7.2 us.
 // Tensor pipe 17 to 22 %.  Short of the copy rate: the reload of W when a CTA's run passes to
 // another head (nothing is computed meanwhile), rows of 1,152 B at 74 KB distance out.
 #include "csa2_latent.cuh"
@@ -490,7 +490,7 @@ csa2_status csa2_query_latent(const uint16_t *q, int64_t q_stride, int32_t total
   a.tiles = (total + csa2::kTok - 1) / csa2::kTok;
   a.wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
   a.err = err_word;
-  if (csa2::few_tokens(total, n_heads, csa2::kFewQuery))
+  if (csa2::few_queries(total, n_heads))
     return cuda_status(csa2::launch_query_few(a, reinterpret_cast<cudaStream_t>(stream)), "csa2_query_latent launch");
   // a CTA for every SM: columns in parts while heads and tiles are too few for that
   const int64_t units = static_cast<int64_t>(n_heads) * a.tiles, sms = csa2::device_sm_count();
@@ -530,7 +530,7 @@ csa2_status csa2_value_project(const void *o, int64_t o_stride, int32_t in_dtype
   a.wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && out_stride % 16 == 0;
   a.err = err_word;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (csa2::few_tokens(total, n_heads, csa2::kFewValue))
+  if (csa2::few_values(total, n_heads, dim))
     return cuda_status(csa2::launch_value_few(a, in_dtype == CSA2_IN_F32, s), "csa2_value_project launch");
   const int64_t units = static_cast<int64_t>(n_heads) * a.tiles, sms = csa2::device_sm_count();
   a.parts = 1;

@@ -23,14 +23,15 @@ struct LatentArgs {
   int32_t *err;
 };
 
-
-// Groups of 16 tokens times heads up to which the forms for few tokens are taken.  One
-// GB300, us, few / persistent: queries of 64 heads, 32 tokens 5.3 / 6.2, 33 tokens 7.9 /
-// 6.2; of 128 heads, 16 tokens 7.3 / 6.9, 17 tokens 9.3 / 7.0.  Values of 64 heads, bf16,
-// 32 tokens 3.4 / 5.2, 64 tokens 5.6 / 5.2; fp32 64 tokens 9.0 / 11.3; of 128 heads, 32
-// tokens bf16 5.7 / 6.1, fp32 9.0 / 12.0, 64 tokens 8.5 / 6.1 and 15.6 / 12.0.
-constexpr int kFewQuery = 128, kFewValue = 256;
-inline bool few_tokens(int total, int heads, int most) { return static_cast<int64_t>((total + 15) / 16) * heads <= most; }
+// Where the forms for few tokens are taken.  One GB300, us, few / persistent, dim 128:
+//   queries of 64 heads, 32 tokens 5.0 / 5.3, 33 tokens 7.5 / 5.3; of 32 heads, 17 tokens 4.1 /
+//   4.2, 32 tokens 4.7 / 4.1; of 128 heads, one token 5.6 / 6.3, 16 tokens 6.9 / 6.1;
+//   values of 64 heads, 32 tokens bf16 3.7 / 4.3, fp32 4.8 / 7.2, 33 tokens 4.8 / 4.3 and 6.9 /
+//   7.2, 64 tokens 5.2 / 4.3 and 8.5 / 7.1; of 128 heads, 16 tokens 3.7 / 5.3 and 5.4 / 8.1, 32
+//   tokens 5.1 / 5.2 and 8.5 / 7.9; of 64 heads of 64, 64 tokens 3.7 / 3.8 and 4.8 / 6.7.
+inline bool few_queries(int total, int heads) { return total <= (heads <= 64 ? 32 : 4); }
+// (a block takes 16 or 32 tokens, a head, 32 values)
+inline bool few_values(int total, int heads, int dim) { return static_cast<int64_t>((total + 15) / 16) * heads * ((dim + 31) / 32) <= 512; }
 cudaError_t launch_query_few(const LatentArgs &a, cudaStream_t s);
 cudaError_t launch_value_few(const LatentArgs &a, bool f32, cudaStream_t s);
 
