@@ -23,7 +23,7 @@
 // Bound: HBM for large matrices, a chain of loads, reductions and stores for a few rows.
 // Measured (in a graph): 12,288 x 4,096 bf16 to NV 22.5 us (5.7 TB/s), read back 21.9 us (5.9
 // TB/s; a plain fill of its 100 MB takes 25.7); 8,192 x 4,096 bf16 13.4 us (6.4 TB/s), fp32 28
-// us (5.5), to MX 13.5 and 25.7, read 11.2 us (7.7, L2 holds a part); 32 rows 1.7 us.  At 11.6
+// us (5.4), to MX 13.5 and 25.9, read 11.2 us (7.7, L2 holds a part); 32 rows 1.7 us.  At 11.6
 // instructions per value the first took 31 us, at 14 compares per fp32 value 42 of 8,192 x
 // 4,096: the conversions above are what brought them near the copy rate.
 #include <type_traits>
@@ -277,123 +277,119 @@ __device__ __forceinline__ uint32_t word_top(uint32_t m, uint32_t w) {
   }
 }
 
-// More rows: a block per kRows rows (8, whose 16 bytes of a piece are a whole 128 B line, 4
-// or 2).  kStaged: the rows are read once, coalesced, 8 / kRows warps per row, into shared
-// memory (row pitch an odd number of 16 bytes, so that 8 rows' loads meet no bank twice);
-// else, when they do not fit there, a second time through the caches.
-template <bool kNv, bool kBf16, bool kStaged, int kRows>
+// Two or one pieces of 32 values to their records: codes and scales of row m of a tile.
+template <bool kNv, bool kBf16, int kG>
+__device__ __forceinline__ void put_pieces(uint8_t *tiles, const uint8_t *src, int p, int have, int m, float back, float fore, uint32_t &bad) {
+  uint8_t *rec = tiles + static_cast<int64_t>(p >> 2) * f4_tile_bytes(kNv), *sc = rec + kF4CodeBytes + f4_scale_at(m);
+  uint32_t code = 0;
+#pragma unroll
+  for (int i = 0; i < kG; ++i) {
+    uint32_t w[4];
+    if constexpr (kNv) {
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        float v[16], s;
+        load16<kBf16>(src, 32 * (p + i) + 16 * g, have, v);
+        const uint32_t c = nv_scale<kBf16>(top_abs<16>(v), back, s);
+        w[2 * g] = nv8<kBf16>(v, s, back, fore);
+        w[2 * g + 1] = nv8<kBf16>(v + 8, s, back, fore);
+        code |= c << (16 * i + 8 * g);
+      }
+    } else {
+      float v[32];
+      load16<kBf16>(src, 32 * (p + i), have, v);
+      load16<kBf16>(src, 32 * (p + i) + 16, have, v + 16);
+      code |= mx32(v, bad, w) << (8 * i);
+    }
+    *reinterpret_cast<uint4 *>(rec + ((p + i) & 3) * 2048 + m * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  sc += kNv ? 512 * ((p >> 1) & 1) + 2 * (p & 1) : p & 3;
+  if constexpr (kNv && kG == 2) *reinterpret_cast<uint32_t *>(sc) = code;
+  else if constexpr (kNv || kG == 2) *reinterpret_cast<uint16_t *>(sc) = static_cast<uint16_t>(code);
+  else *sc = static_cast<uint8_t>(code);
+}
+
+// Many short rows to NV, and rows too long for shared memory: a block per 8 rows, whose
+// 16 bytes of a piece are a whole 128 B line.  kStaged: the rows are read once, coalesced,
+// a warp per row, into shared memory (row pitch an odd number of 16 bytes, so that 8 rows'
+// loads meet no bank twice); else a second time (NV) through the caches.
+template <bool kNv, bool kBf16, bool kStaged>
 __global__ void __launch_bounds__(kQThreads, kNv ? 4 : 3) k_fp4_quant_rows(F4Args a, int pitch) {
-  constexpr int kElt = kBf16 ? 2 : 4, kParts = 8 / kRows;
+  constexpr int kElt = kBf16 ? 2 : 4, kRows = 8;
   extern __shared__ __align__(16) uint8_t stage[];
-  __shared__ uint32_t top[8];
+  __shared__ uint32_t top[kRows];
   next_may_start();
   wait_for_previous();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, rows = a.m.rows, cols = a.m.cols;
   const int row0 = blockIdx.x * kRows, r8 = t % kRows, row = row0 + r8;  // row: this thread's, once it writes
   const uint8_t *x = static_cast<const uint8_t *>(a.x);
-  const int ct = static_cast<int>(f4_col_tiles(cols)), pieces = 4 * ct;
-  uint32_t bad = 0, m = 0;
-  const int own = warp % kRows, part = warp / kRows;  // the row this warp reads (a part of)
-  if ((kNv || kStaged) && row0 + own < rows) {
-    const uint8_t *src = x + (row0 + own) * a.stride * kElt;
-    const int whole = cols * kElt & ~15;
+  const int ct = static_cast<int>(f4_col_tiles(cols)), pieces = 4 * ct, m = row % kF4Rows;
+  uint32_t bad = 0;
+  float back = 1.0f, fore = 1.0f;  // 2^-e and 2^e, e the row's exponent
+  if constexpr (kNv) {
+    uint32_t big = 0;
+    if (row0 + warp < rows) {
+      const uint8_t *src = x + (row0 + warp) * a.stride * kElt;
+      const int whole = cols * kElt & ~15;
 #pragma unroll 8
-    for (int c = 16 * (lane + 32 * part); c < whole; c += 512 * kParts) {
-      const uint4 u = load_now(reinterpret_cast<const uint4 *>(src + c));
-      if constexpr (kStaged) *reinterpret_cast<uint4 *>(stage + own * pitch + c) = u;
-      if constexpr (kNv) m = word_top<kBf16>(word_top<kBf16>(word_top<kBf16>(word_top<kBf16>(m, u.x), u.y), u.z), u.w);
-    }
-    // the last values, and zeros to the end of the last tile
-    for (int c = whole / kElt + lane + 32 * part; c < 32 * pieces; c += 32 * kParts) {
-      const uint32_t u = c >= cols ? 0u : kBf16 ? reinterpret_cast<const uint16_t *>(src)[c] : reinterpret_cast<const uint32_t *>(src)[c];
-      if constexpr (kNv) m = word_top<kBf16>(m, u);
-      if constexpr (kStaged) {
-        if constexpr (kBf16) reinterpret_cast<uint16_t *>(stage + own * pitch)[c] = static_cast<uint16_t>(u);
-        else reinterpret_cast<uint32_t *>(stage + own * pitch)[c] = u;
+      for (int c = 16 * lane; c < whole; c += 512) {
+        const uint4 u = load_now(reinterpret_cast<const uint4 *>(src + c));
+        if constexpr (kStaged) *reinterpret_cast<uint4 *>(stage + warp * pitch + c) = u;
+        big = word_top<kBf16>(word_top<kBf16>(word_top<kBf16>(word_top<kBf16>(big, u.x), u.y), u.z), u.w);
+      }
+      // the last values, and zeros to the end of the last tile
+      for (int c = whole / kElt + lane; c < 32 * pieces; c += 32) {
+        const uint32_t u = c >= cols ? 0u : kBf16 ? reinterpret_cast<const uint16_t *>(src)[c] : reinterpret_cast<const uint32_t *>(src)[c];
+        big = word_top<kBf16>(big, u);
+        if constexpr (kStaged) {
+          if constexpr (kBf16) reinterpret_cast<uint16_t *>(stage + warp * pitch)[c] = static_cast<uint16_t>(u);
+          else reinterpret_cast<uint32_t *>(stage + warp * pitch)[c] = u;
+        }
       }
     }
+    if constexpr (kBf16) big = max(big << 16 & 0x7FFF0000u, big & 0x7FFF0000u);
+    big = __reduce_max_sync(0xffffffffu, big);
+    if (lane == 0) top[warp] = big;
+    __syncthreads();
+    const int e = row_exponent(top[r8], bad);
+    back = pow2f(bad ? 0 : -e), fore = pow2f(bad ? 0 : e);
   }
-  if constexpr (kNv) {
-    if constexpr (kBf16) m = max(m << 16 & 0x7FFF0000u, m & 0x7FFF0000u);
-    m = __reduce_max_sync(0xffffffffu, m);
-    if (lane == 0) top[warp] = m;
-  }
-  if constexpr (kNv || kStaged) __syncthreads();
-  const int mr = row % kF4Rows;
   uint8_t *tiles = a.m.tiles + static_cast<int64_t>(row / kF4Rows) * ct * f4_tile_bytes(kNv);
   const uint8_t *src = kStaged ? stage + r8 * pitch : x + row * a.stride * kElt;
-  const int have = kStaged ? 32 * pieces : cols;
-  if constexpr (kNv) {
-    m = top[r8];
-#pragma unroll
-    for (int i = 1; i < kParts; ++i) m = max(m, top[r8 + kRows * i]);
-    const int e = row_exponent(m, bad);
-    const float back = pow2f(bad ? 0 : -e), fore = pow2f(bad ? 0 : e);
-    if (row < rows && t < kRows) {
-      a.m.row_scales[row] = bad ? __uint_as_float(kNan) : fore;
-      if (bad) raise_err(a.err, CSA2_DEVERR_NAN);
-    }
-    // two pieces at a time, whose four scales are one word
-    for (int p = 2 * (t / kRows); p < pieces && row < rows; p += 2 * (kQThreads / kRows)) {
-      uint8_t *rec = tiles + static_cast<int64_t>(p >> 2) * f4_tile_bytes(true);
-      uint32_t code = 0;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t w[4];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float v[16], s;
-          load16<kBf16>(src, 32 * (p + i) + 16 * g, have, v);
-          const uint32_t sc = nv_scale<kBf16>(top_abs<16>(v), back, s);
-          w[2 * g] = nv8<kBf16>(v, s, back, fore);
-          w[2 * g + 1] = nv8<kBf16>(v + 8, s, back, fore);
-          code |= sc << (16 * i + 8 * g);
-        }
-        *reinterpret_cast<uint4 *>(rec + ((p + i) & 3) * 2048 + mr * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      *reinterpret_cast<uint32_t *>(rec + kF4CodeBytes + f4_scale_at(mr) + 512 * ((p >> 1) & 1)) = code;
-    }
-  } else {
-    for (int p = 2 * (t / kRows); p < pieces && row < rows; p += 2 * (kQThreads / kRows)) {
-      uint8_t *rec = tiles + static_cast<int64_t>(p >> 2) * f4_tile_bytes(false);
-      uint32_t code = 0;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t w[4];
-        float v[32];
-        load16<kBf16>(src, 32 * (p + i), have, v);
-        load16<kBf16>(src, 32 * (p + i) + 16, have, v + 16);
-        code |= mx32(v, bad, w) << (8 * i);
-        *reinterpret_cast<uint4 *>(rec + ((p + i) & 3) * 2048 + mr * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-      *reinterpret_cast<uint16_t *>(rec + kF4CodeBytes + f4_scale_at(mr) + (p & 3)) = static_cast<uint16_t>(code);
-    }
-    __syncthreads();
-    if (t < 8) top[t] = 0;
+  for (int p = 2 * (t / kRows); p < pieces && row < rows; p += 2 * (kQThreads / kRows))
+    put_pieces<kNv, kBf16, 2>(tiles, src, p, kStaged ? 32 * pieces : cols, m, back, fore, bad);
+  if constexpr (!kNv) {
+    if (t < kRows) top[t] = 0;
     __syncthreads();
     if (bad) atomicOr(&top[r8], 1u);
     __syncthreads();
-    if (row < rows && t < kRows) {
-      a.m.row_scales[row] = top[t] ? __uint_as_float(kNan) : 1.0f;
-      if (top[t]) raise_err(a.err, CSA2_DEVERR_NAN);
-    }
+    bad = top[r8];
+  }
+  if (row < rows && t < kRows) {
+    a.m.row_scales[row] = bad ? __uint_as_float(kNan) : fore;
+    if (bad) raise_err(a.err, CSA2_DEVERR_NAN);
   }
 }
 
-// Many rows to MX: persistent blocks, kRows rows at a time, which come by bulk copies into
-// one of two buffers while the other one's are quantised (for NV, whose codes wait for the
-// row's maximum, this gained nothing: 12,288 x 4,096 22.3 us against 22.5).
+// The others: persistent blocks, kRows rows at a time, which come by bulk copies into one of
+// two buffers while the other one's are quantised.  8,192 rows of 7,224 bf16 to NV 27.6 us (one
+// buffer filled by loads, a block per 4 rows 44), of 4,096 to MX 13.6 (14.4, 8 rows); fp32 of
+// 4,104 to NV 33.5 (45.6).  A thread takes one piece of 32 values a step (so that the last,
+// partial step is short), two of fp32 rows to MX, whose steps are short anyway (8,192 x 8,192
+// 53.6 us against 56.8).
 struct RowsSync {
   uint64_t full[2];
-  uint32_t bad[kQThreads / 32];
+  uint32_t part[kQThreads / 32];
 };
-template <bool kBf16, int kRows>
-__global__ void __launch_bounds__(kQThreads, 3) k_fp4_quant_mx(F4Args a, int pitch) {
+template <bool kNv, bool kBf16, int kRows>
+__global__ void __launch_bounds__(kQThreads, 3) k_fp4_quant_piped(F4Args a, int pitch) {
   constexpr int kElt = kBf16 ? 2 : 4, kPolls = 200;  // suspended polls of <= 1 ms each
+  constexpr int kG = kNv || kBf16 ? 1 : 2, kParts = 8 / kRows;
   using Word = std::conditional_t<kBf16, uint16_t, uint32_t>;
   extern __shared__ __align__(16) uint8_t stage[];
   __shared__ __align__(8) RowsSync sy;
-  const int t = threadIdx.x, rows = a.m.rows, cols = a.m.cols, ct = static_cast<int>(f4_col_tiles(cols)), pieces = 4 * ct;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+  const int rows = a.m.rows, cols = a.m.cols, ct = static_cast<int>(f4_col_tiles(cols)), pieces = 4 * ct;
   const int whole = cols * kElt & ~15, w0 = whole / kElt, tail = cols - w0;  // what the copies bring; the values behind it, < 8
   const int items = (rows + kRows - 1) / kRows, per = static_cast<int>(gridDim.x), r8 = t % kRows;
   const uint8_t *x = static_cast<const uint8_t *>(a.x);
@@ -438,37 +434,41 @@ __global__ void __launch_bounds__(kQThreads, 3) k_fp4_quant_mx(F4Args a, int pit
       break;
     }
     end = last(item + per);
-    uint8_t *tiles = a.m.tiles + static_cast<int64_t>(row / kF4Rows) * ct * f4_tile_bytes(false);
-    const uint8_t *src = st + r8 * pitch;
     uint32_t bad = 0;
-    // two pieces at a time, whose scales are half a word
-    for (int p = 2 * (t / kRows); p < pieces && row < rows; p += 2 * (kQThreads / kRows)) {
-      uint8_t *rec = tiles + static_cast<int64_t>(p >> 2) * f4_tile_bytes(false);
-      uint32_t code = 0;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t w[4];
-        float v[32];
-        load16<kBf16>(src, 32 * (p + i), 32 * pieces, v);
-        load16<kBf16>(src, 32 * (p + i) + 16, 32 * pieces, v + 16);
-        code |= mx32(v, bad, w) << (8 * i);
-        *reinterpret_cast<uint4 *>(rec + ((p + i) & 3) * 2048 + m * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+    float back = 1.0f, fore = 1.0f;
+    if constexpr (kNv) {  // a row's largest magnitude: kParts warps
+      const uint8_t *mine = st + (warp % kRows) * pitch;
+      uint32_t big = 0;
+#pragma unroll 4
+      for (int c = 16 * (lane + 32 * (warp / kRows)); c < 32 * pieces * kElt; c += 512 * kParts) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(mine + c);
+        big = word_top<kBf16>(word_top<kBf16>(word_top<kBf16>(word_top<kBf16>(big, u.x), u.y), u.z), u.w);
       }
-      *reinterpret_cast<uint16_t *>(rec + kF4CodeBytes + f4_scale_at(m) + (p & 3)) = static_cast<uint16_t>(code);
+      if constexpr (kBf16) big = max(big << 16 & 0x7FFF0000u, big & 0x7FFF0000u);
+      big = __reduce_max_sync(0xffffffffu, big);
+      if (lane == 0) sy.part[warp] = big;
+      __syncthreads();
+      big = sy.part[r8];
+#pragma unroll
+      for (int i = 1; i < kParts; ++i) big = max(big, sy.part[r8 + kRows * i]);
+      const int e = row_exponent(big, bad);
+      back = pow2f(bad ? 0 : -e), fore = pow2f(bad ? 0 : e);
     }
-    // bad: of any thread of the row (threads of equal t % kRows), a bit each
-    uint32_t mask = bad ? 1u << r8 : 0u;
-    mask = __reduce_or_sync(0xffffffffu, mask);
-    if ((t & 31) == 0) sy.bad[t >> 5] = mask;
-    __syncthreads();  // the buffer has been read, too
+    uint8_t *tiles = a.m.tiles + static_cast<int64_t>(row / kF4Rows) * ct * f4_tile_bytes(kNv);
+    for (int p = kG * (t / kRows); p < pieces && row < rows; p += kG * (kQThreads / kRows))
+      put_pieces<kNv, kBf16, kG>(tiles, st + r8 * pitch, p, 32 * pieces, m, back, fore, bad);
+    if constexpr (!kNv) {  // a bit for each row
+      const uint32_t mask = __reduce_or_sync(0xffffffffu, bad ? 1u << r8 : 0u);
+      if (lane == 0) sy.part[warp] = mask;
+    }
+    __syncthreads();  // the buffer has been read
     if (t == 0 && item + 2 * per < items) fetch(item + 2 * per, buf);
     if (t < kRows && row < rows) {
-      mask = 0;
-#pragma unroll
-      for (int i = 0; i < kQThreads / 32; ++i) mask |= sy.bad[i];
-      mask = mask >> r8 & 1u;
-      a.m.row_scales[row] = mask ? __uint_as_float(kNan) : 1.0f;
-      if (mask) raise_err(a.err, CSA2_DEVERR_NAN);
+      if constexpr (!kNv) {
+        for (int i = 0; i < kQThreads / 32; ++i) bad |= sy.part[i] >> r8 & 1u;
+      }
+      a.m.row_scales[row] = bad ? __uint_as_float(kNan) : fore;
+      if (bad) raise_err(a.err, CSA2_DEVERR_NAN);
     }
   }
 }
@@ -555,16 +555,16 @@ __global__ void __launch_bounds__(256) k_fp4_read(csa2_fp4_matrix mx, void *out,
 
 }  // namespace
 
-template <bool kNv, bool kBf16, bool kStaged, int kRows>
+template <bool kNv, bool kBf16, bool kStaged>
 static cudaError_t launch_rows(const F4Args &a, int pitch, cudaStream_t s) {
-  const auto kern = k_fp4_quant_rows<kNv, kBf16, kStaged, kRows>;
-  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), kRows * pitch);
+  const auto kern = k_fp4_quant_rows<kNv, kBf16, kStaged>;
+  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), 8 * pitch);
   if (e != cudaSuccess) return e;
-  return launch_after(kern, dim3((a.m.rows + kRows - 1) / kRows), kQThreads, kRows * pitch, 0, s, a, pitch);
+  return launch_after(kern, dim3((a.m.rows + 7) / 8), kQThreads, 8 * pitch, 0, s, a, pitch);
 }
-template <bool kBf16, int kRows>
-static cudaError_t launch_mx(const F4Args &a, int pitch, cudaStream_t s) {
-  const auto kern = k_fp4_quant_mx<kBf16, kRows>;
+template <bool kNv, bool kBf16, int kRows>
+static cudaError_t launch_piped(const F4Args &a, int pitch, cudaStream_t s) {
+  const auto kern = k_fp4_quant_piped<kNv, kBf16, kRows>;
   const int bytes = 2 * kRows * pitch, items = (a.m.rows + kRows - 1) / kRows;
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void *>(kern), bytes);
   if (e != cudaSuccess) return e;
@@ -573,37 +573,31 @@ static cudaError_t launch_mx(const F4Args &a, int pitch, cudaStream_t s) {
 }
 // Which kernel.  One GB300, us, in a graph.
 //   Up to eight rows per SM a block per row (a block per 8 rows would leave SMs idle).
-//   From 32 rows per SM on, 8 rows a block while four blocks fit an SM (MX: five, as its
-//   other kernel is the better one sooner): NV 8,192 x 3,000 bf16 11.6 against 14.0 with 4 rows,
-//   2,000 x 3,000 6.5 against 4.5; MX 8,192 x 2,048 7.8 against 9.5, x 3,000 13.4 against 12.0.
-//   NV else 4 rows staged, or 2, while two blocks fit an SM: 12,288 x 4,096 bf16 22.5 with 4
-//   against 24.0 with 8; 8,192 x 8,192 bf16 32 with 4 against 57 read twice, fp32 with 2
-//   62 against 111.
-//   MX else by k_fp4_quant_mx, 4 rows while three blocks fit an SM (8,192 x 8,192 bf16 34.7
-//   with 4 and one block, 29.5 with 2), else 2: 8,192 x 4,096 fp32 25.7 against 32.8 read as
-//   they come, x 12,288 74 against 92; bf16 with one block an SM only of few rows: 1,300 x
-//   20,000 16.7 against 28.8, 8,192 x 20,000 87 against 78.
+//   NV, 32 rows per SM and more, as long as four blocks of 8 rows fit an SM: 8,000 x 2,048 bf16
+//   7.5 against 8.5 piped, x 2,504 10.1 against 11.3; with fewer rows 2,500 x 512 bf16 3.5
+//   against 3.1 piped.
+//   Piped, 8 rows at a time while five buffers fit an SM (2,500 x 2,048 bf16 4.5 against 5.4 with
+//   4; 1,300 x 4,096 5.9 against 4.5), 4 while two blocks fit (8,000 x 5,120 bf16 20.4 against
+//   24.8 with 2, x 7,224 34.6 against 27.7), else 2, while that block fits: 8,000 x 12,288 fp32
+//   to NV 87 against 159 read through the caches, 8,000 x 20,000 bf16 to NV 78 against 130, to MX
+//   75 against 77.
 template <bool kNv, bool kBf16>
 static cudaError_t launch_quant(const F4Args &a, cudaStream_t s) {
-  const int sms = device_sm_count();
-  if (a.m.rows < 8 * sms) {
+  const int sms = device_sm_count(), rows = a.m.rows;
+  if (rows < 8 * sms) {
     const int64_t iter = (f4_col_tiles(a.m.cols) * kF4Cols + 8 * kQThreads - 1) / (8 * kQThreads);
     const auto kern = iter <= 1 ? k_fp4_quant_row<kNv, kBf16, 1> : iter == 2 ? k_fp4_quant_row<kNv, kBf16, 2>
                     : iter == 3 ? k_fp4_quant_row<kNv, kBf16, 3> : k_fp4_quant_row<kNv, kBf16, 4>;
-    return launch_after(kern, dim3(a.m.rows), kQThreads, 0, 0, s, a);
+    return launch_after(kern, dim3(rows), kQThreads, 0, 0, s, a);
   }
   constexpr int kK = 1024;
   const int pitch = static_cast<int>(f4_col_tiles(a.m.cols)) * kF4Cols * (kBf16 ? 2 : 4) + 16;
-  const bool many = a.m.rows >= 32 * sms;
-  if (many && 8 * pitch <= (kNv ? 50 : 40) * kK) return launch_rows<kNv, kBf16, true, 8>(a, pitch, s);
-  if constexpr (kNv) {
-    if (4 * pitch <= 80 * kK) return launch_rows<kNv, kBf16, true, 4>(a, pitch, s);
-    if (2 * pitch <= 80 * kK) return launch_rows<kNv, kBf16, true, 2>(a, pitch, s);
-  } else {
-    if (4 * pitch <= 36 * kK) return launch_mx<kBf16, 4>(a, pitch, s);
-    if (2 * pitch <= (kBf16 && many ? 55 : 110) * kK) return launch_mx<kBf16, 2>(a, pitch, s);
-  }
-  return launch_rows<kNv, kBf16, false, 8>(a, 0, s);
+  if constexpr (kNv)
+    if (rows >= 32 * sms && 8 * pitch <= 50 * kK) return launch_rows<true, kBf16, true>(a, pitch, s);
+  if (rows >= 16 * sms && 8 * pitch <= 40 * kK) return launch_piped<kNv, kBf16, 8>(a, pitch, s);
+  if (4 * pitch <= 44 * kK) return launch_piped<kNv, kBf16, 4>(a, pitch, s);
+  if (2 * pitch <= 110 * kK) return launch_piped<kNv, kBf16, 2>(a, pitch, s);
+  return launch_rows<kNv, kBf16, false>(a, 0, s);
 }
 
 csa2_status check_fp4(const csa2_fp4_matrix *m, const char *name) {

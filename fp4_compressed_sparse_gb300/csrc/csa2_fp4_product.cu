@@ -18,6 +18,8 @@
 // that csa2_mxf4_peak_launch reaches), MX 113; 8,192^3 151 us (7.3).  Without its copies it
 // takes 108 us, without its MMAs 105 (39 KB a stage and SM, 19 TB/s out of L2): two bounds
 // that meet.  Tensor memory that never had to be drained would save 4 us.
+#include <type_traits>
+
 #include "csa2_fp4.cuh"
 #include "csa2_tma.cuh"
 
@@ -95,6 +97,9 @@ struct Split {
   static constexpr int kBytes = (kStage * kStages > NT * kPitch * 4 ? kStage * kStages : NT * kPitch * 4) + 1024;
 };
 
+template <int n>
+using Int = std::integral_constant<int, n>;
+
 template <int NT, bool kNv, bool kBf16>
 __global__ void __launch_bounds__(kSplitThreads)
     k_fp4_split(ProductArgs a, const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
@@ -104,6 +109,8 @@ __global__ void __launch_bounds__(kSplitThreads)
   __shared__ __align__(8) uint64_t full[L::kStages], empty[L::kStages], done;
   __shared__ uint32_t tmem_at;
   __shared__ int loaded;  // stages whose copies were started
+  __shared__ float r_tok[NT];
+  __shared__ __align__(16) float r_col[kF4Rows];
   const uint32_t s0 = (tc::smem_addr(raw) + 1023) & ~1023u;
   uint8_t *smem = raw + (s0 - tc::smem_addr(raw));
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -134,6 +141,11 @@ __global__ void __launch_bounds__(kSplitThreads)
   wait_for_previous();
   const uint32_t tmem = tmem_at;
 
+  if (warp >= 2) {  // the rows' powers of two, for the join (a load each there takes longer than the sums' way)
+    const int i = t - 64;
+    if (i < NT) r_tok[i] = m0 + i < a.x.rows ? a.x.row_scales[m0 + i] : 0.0f;
+    r_col[i] = a.w.row_scales[nt * kF4Rows + i];  // (the plane holds whole tiles of rows)
+  }
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < nk; ++i) {
       const int st = i % L::kStages;
@@ -222,57 +234,62 @@ __global__ void __launch_bounds__(kSplitThreads)
   const int n_out = a.w.rows;
   const int per = (NT + ranks - 1) / ranks, c_lo = min(static_cast<int>(rank) * per, NT), c_hi = min(c_lo + per, NT);
   const int items = (min(c_hi, a.x.rows - m0) - c_lo) * 32;
-  for (int i0 = t; i0 < items; i0 += 2 * kSplitThreads) {  // two at a time, all their loads in flight
-    float4 v[2][8], rn[2];
-    float rm[2];
+  auto join = [&](auto held, auto most) {  // `held` at a time, all their loads in flight; up to `most` ranks
+    constexpr int kH = decltype(held)::value, kR = decltype(most)::value;
+    for (int i0 = t; i0 < items; i0 += kH * kSplitThreads) {
+      float4 v[kH][kR];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = i0 + h * kSplitThreads, c = c_lo + i / 32, n = 4 * (i % 32), gn = nt * kF4Rows + n;
-      if (i < items && gn < n_out) {
-        rm[h] = a.x.row_scales[m0 + c];
-        rn[h] = *reinterpret_cast<const float4 *>(a.w.row_scales + gn);  // (the plane holds whole tiles of rows)
+      for (int h = 0; h < kH; ++h) {
+        const int i = i0 + h * kSplitThreads, c = c_lo + i / 32, n = 4 * (i % 32);
+        if (i < items && nt * kF4Rows + n < n_out) {
 #pragma unroll
-        for (uint32_t k = 0; k < 8; ++k)
-          if (k < ranks) v[h][k] = ld_cluster4(map_rank(tc::smem_addr(part + c * L::kPitch + n), k));
+          for (uint32_t k = 0; k < kR; ++k)
+            if (k < ranks) v[h][k] = ld_cluster4(map_rank(tc::smem_addr(part + c * L::kPitch + n), k));
+        }
       }
-    }
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = i0 + h * kSplitThreads, c = c_lo + i / 32, n = 4 * (i % 32), gn = nt * kF4Rows + n;
-      if (i >= items || gn >= n_out) continue;
-      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int h = 0; h < kH; ++h) {
+        const int i = i0 + h * kSplitThreads, c = c_lo + i / 32, n = 4 * (i % 32), gn = nt * kF4Rows + n;
+        if (i >= items || gn >= n_out) continue;
+        float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-      for (uint32_t k = 0; k < 8; ++k)
-        if (k < ranks) {
-          s.x += v[h][k].x;
-          s.y += v[h][k].y;
-          s.z += v[h][k].z;
-          s.w += v[h][k].w;
-        }
-      s.x *= rm[h] * rn[h].x;
-      s.y *= rm[h] * rn[h].y;
-      s.z *= rm[h] * rn[h].z;
-      s.w *= rm[h] * rn[h].w;
-      const int64_t at = (m0 + c) * a.stride + gn;
-      if (gn + 4 <= n_out) {
-        if constexpr (kBf16) {
-          __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
-          *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) =
-              make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
-        } else {
-          *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = s;
-        }
-      } else {
-        const float o[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (gn + j < n_out) {
-            if constexpr (kBf16) static_cast<__nv_bfloat16 *>(a.out)[at + j] = __float2bfloat16_rn(o[j]);
-            else static_cast<float *>(a.out)[at + j] = o[j];
+        for (uint32_t k = 0; k < kR; ++k)
+          if (k < ranks) {
+            s.x += v[h][k].x;
+            s.y += v[h][k].y;
+            s.z += v[h][k].z;
+            s.w += v[h][k].w;
           }
+        const float rm = r_tok[c];
+        const float4 rn = *reinterpret_cast<const float4 *>(r_col + n);
+        s.x *= rm * rn.x;
+        s.y *= rm * rn.y;
+        s.z *= rm * rn.z;
+        s.w *= rm * rn.w;
+        const int64_t at = (m0 + c) * a.stride + gn;
+        if (gn + 4 <= n_out) {
+          if constexpr (kBf16) {
+            __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
+            *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.out) + at) =
+                make_uint2(*reinterpret_cast<uint32_t *>(&lo), *reinterpret_cast<uint32_t *>(&hi));
+          } else {
+            *reinterpret_cast<float4 *>(static_cast<float *>(a.out) + at) = s;
+          }
+        } else {
+          const float o[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (gn + j < n_out) {
+              if constexpr (kBf16) static_cast<__nv_bfloat16 *>(a.out)[at + j] = __float2bfloat16_rn(o[j]);
+              else static_cast<float *>(a.out)[at + j] = o[j];
+            }
+        }
       }
     }
-  }
+  };
+  if (ranks == 1) join(Int<8>{}, Int<1>{});
+  else if (ranks <= 4) join(Int<4>{}, Int<4>{});
+  else join(Int<2>{}, Int<8>{});
   cluster_sync();  // no CTA leaves while another reads its sums
   if (warp == 1) {
     tc::tc_fence_after();
