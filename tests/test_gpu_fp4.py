@@ -283,3 +283,18 @@ def test_calls_behind_one_another():
                 seen.append(x.clone())
         ends.append(seen)
     assert all(torch.equal(a, b) for a, b in zip(*ends))
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N", [(20, 300), (300, 264), (2600, 1496), (2600, 1501)])
+def test_product_rows_in_the_middle_of_a_sector(M, N, dtype):
+    """Output rows that begin 16 bytes behind a multiple of 32, all or every second one: the same bits, nothing beside them."""
+    x, w = (_packed(torch.randn(r, 392, device=DEV), csa2.FP4_NV) for r in (M, N))
+    wide = -(-N // 32) * 32
+    want = torch.empty(M, wide, dtype=dtype, device=DEV)[:, :N]
+    csa2.fp4_product(x, w, want)
+    for off, stride in ((0, wide + 8), (16 // want.element_size(), wide + 32), (16 // want.element_size(), wide + 40)):
+        out = torch.full((M, stride), 5.0, dtype=dtype, device=DEV)
+        csa2.fp4_product(x, w, out[:, off:off + N])
+        assert torch.equal(out[:, off:off + N], want)
+        assert (out[:, :off] == 5).all() and (out[:, off + N:] == 5).all()
