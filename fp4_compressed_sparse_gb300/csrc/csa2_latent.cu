@@ -18,8 +18,8 @@
 // rounding takes.
 //
 // Measured (in a graph, caches as the calls before leave them): 4,001 tokens of 64 heads of
-// 128: queries 74 us (403 MB, 5.4 TB/s, 80 % of the measured copy rate), values bf16 56 us
-// (336 MB, 6.0 TB/s, 88 %), fp32 99 us (599 MB, 6.1 TB/s); 128 tokens: 5.8, 4.6 and 7.2 us.
+// 128: queries 72 us (403 MB, 5.6 TB/s, 82 % of the measured copy rate), values bf16 55 us
+// (336 MB, 6.1 TB/s, 90 %), fp32 97 us (599 MB, 6.2 TB/s); 128 tokens: 5.7, 4.5 and 7.2 us.
 // Tensor pipe 17 to 22 %.  Short of the copy rate: the reload of W when a CTA's run passes to
 // another head (nothing is computed meanwhile), rows of 1,152 B at 74 KB distance out.
 #include "csa2_latent.cuh"
@@ -119,9 +119,10 @@ __device__ __forceinline__ void sts4(uint32_t at, const uint32_t *v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
 
-// One persistent CTA per SM.  A unit is (head, column part, tile of 128 tokens), units of
-// a head and part follow one another and a CTA takes a run of them, so that its part of
-// W stays in shared memory.  Tokens are the MMA's 128 rows (a lane holds one token and
+// One persistent CTA per SM.  A unit is (head, column part, tile of 128 tokens), done in one
+// job or, queries with all of their 512 columns, in two of 256; units of a head and part
+// follow one another and a CTA takes a run of jobs, so that its part of W stays in shared
+// memory.  Tokens are the MMA's 128 rows (a lane holds one token and
 // writes runs of its row), W's columns its N.
 //   warp 0       copies W (once per head and part) and the tokens' rows, by tensor maps
 //   warp 1       issues the MMAs
@@ -141,8 +142,11 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
   const uint32_t s_w = (tc::smem_addr(raw) + 1023) & ~1023u, s_x = s_w + kWBytes, s_p = s_x + S::kStages * S::kStage;
   const int jobs = kQ && a.np > 256 ? 2 : 1, cols = a.np / jobs;  // accumulators of a unit, their columns
   const int chunks = kQ ? 1 : kF ? kLat / 32 : kLat / 128;       // stages of a unit
-  const int64_t units = static_cast<int64_t>(a.heads) * a.parts * a.tiles;
-  const int64_t u0 = units * blockIdx.x / gridDim.x, u1 = units * (blockIdx.x + 1) / gridDim.x;
+  // this CTA's jobs: job v is of unit v >> shift (up to 2^27 jobs); whole units unless a.halves
+  const int shift = jobs - 1, keep = a.halves ? 0 : shift;
+  const int64_t shares = static_cast<int64_t>(a.heads) * a.parts * a.tiles << (shift - keep);
+  const int v0 = static_cast<int>(shares * blockIdx.x / gridDim.x) << keep;
+  const int v1 = static_cast<int>(shares * (blockIdx.x + 1) / gridDim.x) << keep;
   if (warp == 1) {
     tc::tmem_alloc(&sy.tmem, 512);
     tc::tmem_relinquish();
@@ -182,12 +186,11 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
     const uint32_t el = elect_one();
     const int boxes = kQ ? (a.dim + 63) / 64 : kF ? 1 : 2, wide = kF ? 32 : 64;
     const int w_boxes = kQ ? a.np / 64 : kLat / 64, w_box = (kQ ? a.dim : a.np) * 128;
-    int64_t held = -1;
+    int held = -1;
     uint32_t n = 0, st = 0, ph = 1, wn = 0;  // wn: copies of W so far
     bool ok = true;
-    for (int64_t u = u0; u < u1 && ok; ++u) {
-      const int64_t hp = u / a.tiles;
-      const int tile = static_cast<int>(u - hp * a.tiles), h = static_cast<int>(hp / a.parts), part = static_cast<int>(hp % a.parts);
+    for (int u = v0 >> shift; u << shift < v1 && ok; ++u) {
+      const int hp = u / a.tiles, tile = u - hp * a.tiles, h = hp / a.parts, part = hp - h * a.parts;
       if (hp != held) {
         if (wn > 0) ok = wait_all(&sy.wdone, (wn - 1) & 1);
         if (!ok) break;
@@ -223,20 +226,21 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMAs
     const uint32_t el = elect_one(), id = idesc_bf16(cols, kQ ? 1 : 0);
-    int64_t held = -1;
+    int held = -1;
     uint32_t st = 0, ph = 0, j = 0, wn = 0;
     bool ok = true;
-    for (int64_t u = u0; u < u1 && ok; ++u) {
-      const int64_t hp = u / a.tiles;
+    for (int v = v0; v < v1 && ok; ++v, ++j) {
+      const int hp = (v >> shift) / a.tiles, b = v & shift;
+      const bool first = b == 0 || v == v0, last = b == jobs - 1 || v == v1 - 1;  // of the unit's jobs here
       if (hp != held) {
         ok = wait_all(&sy.wfull, wn++ & 1);
         held = hp;
       }
-      for (int b = 0; b < jobs && ok; ++b, ++j) {
+      if (ok) {
         const uint32_t acc = j & 1, d = tmem + 256 * acc;
         if (j >= 2) ok = wait_all(&sy.tempty[acc], ((j >> 1) - 1) & 1);
         for (int c = 0; c < chunks && ok; ++c) {
-          if (b == 0) ok = kF ? wait_all(&sy.pfull[st], ph) : wait_all(&sy.full[st], ph);
+          if (first) ok = kF ? wait_all(&sy.pfull[st], ph) : wait_all(&sy.full[st], ph);
           if (!ok) break;
           tc::tc_fence_after();
           if (el) {
@@ -260,14 +264,14 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
                 mma_bf16(d, dx + (((s >> 2) * kBox + 32 * (s & 3)) >> 4),
                          desc_sw128(s_w + (2 * c + (s >> 2)) * a.np * 128, 16, 1024) + (32 * (s & 3) >> 4), id, c + s > 0 ? 1u : 0u);
             }
-            if (b == jobs - 1) tc::mma_commit(kF ? &sy.pempty[st] : &sy.empty[st]);
+            if (last) tc::mma_commit(kF ? &sy.pempty[st] : &sy.empty[st]);
             if (c == chunks - 1) {
               tc::mma_commit(&sy.tfull[acc]);
-              if (b == jobs - 1 && u + 1 < u1 && (u + 1) / a.tiles != hp) tc::mma_commit(&sy.wdone);
+              if (v + 1 < v1 && (v + 1 >> shift) / a.tiles != hp) tc::mma_commit(&sy.wdone);
             }
           }
           __syncwarp();
-          if (b == jobs - 1 && ++st == (kF ? kPartBufs : S::kStages)) {
+          if (last && ++st == (kF ? kPartBufs : S::kStages)) {
             st = 0;
             ph ^= 1;
           }
@@ -280,12 +284,10 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
     const int q = warp & 3, g = (warp - 4) >> 2;
     uint32_t j = 0;
     bool ok = true;
-    for (int64_t u = u0; u < u1 && ok; ++u) {
-      const int64_t hp = u / a.tiles;
-      const int tile = static_cast<int>(u - hp * a.tiles), h = static_cast<int>(hp / a.parts), part = static_cast<int>(hp % a.parts);
+    for (int v = v0; v < v1 && ok; ++v, ++j) {
+      const int u = v >> shift, b = v & shift, hp = u / a.tiles, tile = u - hp * a.tiles, h = hp / a.parts, part = hp - h * a.parts;
       const int64_t tok = static_cast<int64_t>(tile) * kTok + 32 * q + lane;
-      for (int b = 0; b < jobs && ok; ++b, ++j) {
-        if ((j & 1) != g) continue;
+      if ((j & 1) == g) {
         bool live = tok < a.total;
         int64_t p;
         if (kQ && live) live = row_position(a, tok, false, p);
@@ -351,9 +353,11 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
     // (all of a unit's loads at once, the positions a unit ahead: a chain of two loads
     // per unit took longer than its bytes)
     const int d8 = lane & 7, r0 = 4 * (warp - 12) + (lane >> 3);
+    const int u0 = (v0 + shift) >> shift, u1 = (v1 + shift) >> shift;  // units whose first job is here
     int64_t p[4];
-    auto positions = [&](int64_t u) {
-      const int64_t hp = u / a.tiles, t0 = (u - hp * a.tiles) * kTok;
+    auto positions = [&](int u) {
+      const int hp = u / a.tiles;
+      const int64_t t0 = static_cast<int64_t>(u - hp * a.tiles) * kTok;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int64_t tok = t0 + r0 + 32 * i;
@@ -361,8 +365,9 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
       }
     };
     positions(u0);
-    for (int64_t u = u0; u < u1; ++u) {
-      const int64_t hp = u / a.tiles, t0 = (u - hp * a.tiles) * kTok, h = hp / a.parts;
+    for (int u = u0; u < u1; ++u) {
+      const int hp = u / a.tiles, h = hp / a.parts;
+      const int64_t t0 = static_cast<int64_t>(u - hp * a.tiles) * kTok;
       const bool mine = hp % a.parts == 0;
       const uint16_t *src = static_cast<const uint16_t *>(a.x) + (t0 + r0) * a.x_stride + h * (a.dim + kRope) + a.dim + 8 * d8;
       Rope8 x[4];
@@ -383,7 +388,7 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
     // (two groups of four warps, each every second stage: while one waits the other splits; a
     // lane takes a token's 32 values)
     const int r8 = lane & 7;
-    const uint32_t n_all = static_cast<uint32_t>(u1 - u0) * chunks, quarter = 32 * (warp & 3);
+    const uint32_t n_all = static_cast<uint32_t>(v1 - v0) * chunks, quarter = 32 * (warp & 3);
     bool ok = true;
     for (uint32_t n = (warp - 12) >> 2; n < n_all; n += 2) {
       const uint32_t st = n % S::kStages, pb = n % kPartBufs, use = n / kPartBufs;
@@ -446,8 +451,8 @@ cudaError_t launch(const LatentArgs &a, cudaStream_t s) {
     const uint32_t o_box[2] = {64, 32};
     if (!tensor_map(&mo, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, a.out, o_dim, o_stride, o_box, true)) return cudaErrorNotSupported;
   }
-  const int64_t units = static_cast<int64_t>(a.heads) * a.parts * a.tiles, sms = device_sm_count();
-  return launch_after(kern, dim3(static_cast<unsigned>(units < sms ? units : sms)), Shape<kM>::kThreads, Shape<kM>::kBytes, 0, s, a, mx, mw, mo);
+  const int64_t shares = static_cast<int64_t>(a.heads) * a.parts * a.tiles << a.halves, sms = device_sm_count();
+  return launch_after(kern, dim3(static_cast<unsigned>(shares < sms ? shares : sms)), Shape<kM>::kThreads, Shape<kM>::kBytes, 0, s, a, mx, mw, mo);
 }
 
 }  // namespace
@@ -492,9 +497,14 @@ csa2_status csa2_query_latent(const uint16_t *q, int64_t q_stride, int32_t total
   a.err = err_word;
   if (csa2::few_queries(total, n_heads))
     return cuda_status(csa2::launch_query_few(a, reinterpret_cast<cudaStream_t>(stream)), "csa2_query_latent launch");
-  // a CTA for every SM: columns in parts while heads and tiles are too few for that
+  // A CTA for every SM: columns in parts while heads and tiles are too few for that.  Else runs
+  // of whole units, or, where that makes the longest run shorter, of halves: in two parts up to
+  // two units per CTA (384 tokens of 64 heads 9.6 us against 10.3 by halves and 11.2), by a run's
+  // ends above (1,000 tokens 20.7 against 22.5); where it does not, 250 tokens 8.2 against 7.0.
   const int64_t units = static_cast<int64_t>(n_heads) * a.tiles, sms = csa2::device_sm_count();
-  a.parts = 2 * units > sms ? 1 : 4 * units > sms ? 2 : 4;
+  const bool shorter = (2 * units + sms - 1) / sms < 2 * ((units + sms - 1) / sms);
+  a.parts = 4 * units <= sms ? 4 : 2 * units <= sms || (shorter && units <= 2 * sms) ? 2 : 1;
+  a.halves = a.parts == 1 && shorter;
   a.np = CSA2_D_LATENT / a.parts;
   return cuda_status(csa2::launch<csa2::kQuery>(a, reinterpret_cast<cudaStream_t>(stream)), "csa2_query_latent launch");
 }

@@ -18,6 +18,7 @@ struct LatentArgs {
   int64_t out_stride;   // elements per token
   int parts;            // column parts of a head
   int np;               // columns of a part
+  int halves;           // queries: a CTA's run may begin and end with half a unit
   int tiles;            // token tiles
   int wide;             // 32-byte stores are aligned
   int32_t *err;
