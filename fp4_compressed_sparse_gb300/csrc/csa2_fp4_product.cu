@@ -12,7 +12,7 @@
 // cluster, whose sums are added in rank order through distributed shared memory: no
 // workspace, equal calls give equal bits.  Bound: the weights' bytes.  One token by 12,288 x
 // 4,096 5.6 us with the weights in L2 (12.3 cold, 28 MB: a third of the copy rate; launch,
-// tensor memory, first box and the join are 4.5 us of either), 501 tokens x 704 x 4,104 7.7.
+// tensor memory, first box and the join are 4.5 us of either), 501 tokens x 704 x 4,104 7.2.
 //
 // k_fp4_pair, more: 8,192 x 12,288 x 4,096 NV 121 us (6.8 PFLOP/s, 71 % of the 9.5 PFLOP/s
 // that csa2_mxf4_peak_launch reaches), MX 113; 8,192^3 151 us (7.3).  Without its copies it
@@ -83,16 +83,17 @@ __device__ __forceinline__ uint32_t elect_one() {
 
 // Shared memory of a stage, kTiles K tiles: the weights' records (128 rows), the tokens'
 // codes and scales.  A copying thread takes about 0.2 us for a wait, an arming and a copy
-// of any size, so a stage is as large as two CTAs per SM allow.
+// of any size, so a stage is as large as two CTAs per SM allow; with 128 tokens there is
+// one per SM, and five stages (three: 501 x 704 x 4104 8.0 us against 7.2).
 template <int NT, bool kNv>
 struct Split {
-  static constexpr int kTiles = NT <= 32 ? 4 : 2, kStages = NT <= 32 ? 2 : 3;
+  static constexpr int kTiles = NT <= 32 ? 4 : 2, kStages = NT <= 32 ? 2 : NT <= 64 ? 3 : 5;
   static constexpr int kRec = f4_tile_bytes(kNv), kS = f4_scale_bytes(kNv);
   static constexpr int kA = kTiles * kRec, kB = kTiles * NT * 64;
   static constexpr int kStage = kA + kB + kTiles * kS;
   static constexpr int kAtoms = kNv ? 2 : 1;    // 512 B of scales per operand and K tile
   static constexpr int kSfCols = 8 * kAtoms;    // TMEM columns of a K tile's scales
-  static constexpr int kCols = NT + kSfCols * kTiles * kStages <= 128 ? 128 : 256;
+  static constexpr int kUsed = NT + kSfCols * kTiles * kStages, kCols = kUsed <= 128 ? 128 : kUsed <= 256 ? 256 : 512;
   static constexpr int kPitch = 128 + 4;        // floats per token of the partial sums
   static constexpr int kBytes = (kStage * kStages > NT * kPitch * 4 ? kStage * kStages : NT * kPitch * 4) + 1024;
 };
@@ -622,28 +623,30 @@ cudaError_t launch_split(const ProductArgs &a, int ranks, cudaStream_t s) {
   return launch_after(kern, grid, kSplitThreads, L::kBytes, ranks, s, a, mw, mx, ms);
 }
 // Which kernel, and how the split one cuts the work.  One GB300, us, NV to bf16, in a graph.
-//   Pairs once 64 CTAs have a tile (32 for up to 1,024 columns) and more than 64 tokens share
-//   it: 501 x 4096 x 8192 (64 CTAs) 14.3 against 15.6 split, 256 x 12288 x 4096 (96) 10.3
-//   against 18.1, 501 x 2048 x 1024 (32) 6.7 against 7.7; below, 256 x 4096 x 8192 (32) 14.1
-//   against 11.3, 64 tokens x 12288 x 4096 10.0 against 8.1.
+//   Pairs for more than 64 tokens with more tiles of 128 x 128 than SMs (250 x 12288 x 512 6.7
+//   against 11.4 split, x 4096 10.6 against 20.0), and from half as many on if both of a pair
+//   have tokens and there are more than 2,048 columns (250 x 9600 x 4096 10.2 against 10.8, 501
+//   x 4096 x 8192 14.3 against 15.1; 100 x 16384 x 1024 7.7 against 6.4, 250 x 4096 x 4096, of 64
+//   tiles, 10.4 against 8.8).
 //   Split: the narrowest token tile that holds all tokens (a scale column is of 32 rows
-//   from the record's first on, so several tiles only of 128), then as many ranks as fit
-//   two CTAs per SM: 64 x 12288 x 4096 8.1 with 3 against 12.1 with 1, 1 x 4096 x 8192 5.0
-//   with 8 against 5.9 with 4.  Of 128 tokens, whose sums' way through shared memory counts,
-//   as many as make 100 CTAs, or up to 4 if that is one: 128 x 704 x 4104 6.1 with 8 (48
-//   CTAs) against 6.8 with 4, 501 x 704 x 4104 8.0 with 4 (96) against 9.2 with 8, 256 x 4096
-//   x 8192 11.3 with 4 (256) against 14.5 with 2.
+//   from the record's first on, so several tiles only of 128), then as many ranks as are
+//   resident at once, of 128 tokens one CTA per SM, else two: 64 x 12288 x 4096 8.1 with 3
+//   against 12.1 with 1, 1 x 4096 x 8192 5.0 with 8 against 5.9 with 4, 501 x 704 x 4104 7.2 with
+//   4 against 10.2 with 1.  Clusters do not cover all SMs: a few that wait for a second turn
+//   cost as much as all (1 x 6144 x 4096 8.1 with 6, 4.9 with 4; 501 x 704 x 4104 10.8 with 6).
+// kRanks: ranks, the percentage of the SMs that clusters of so many cover with one CTA per
+// SM (of 152: 152, 138, 144, 138, 120), and with two (of 304: 304, 291, 296, 276, 288).
+constexpr int kRanks[5][3] = {{2, 100, 100}, {3, 90, 95}, {4, 94, 97}, {6, 90, 90}, {8, 78, 95}};
 template <bool kNv, bool kBf16>
 cudaError_t launch_product(const ProductArgs &a, cudaStream_t s) {
   const int m = a.x.rows;
-  const int64_t kt = f4_col_tiles(a.x.cols), big = (f4_row_tiles(m) + 1) / 2 * ((a.w.rows + kPairN - 1) / kPairN);
-  if (m > 64 && 2 * big >= (kt <= 8 ? 32 : 64)) return launch_pair<kNv, kBf16>(a, s);
+  const int64_t kt = f4_col_tiles(a.x.cols), sms = device_sm_count(), squares = f4_row_tiles(m) * f4_row_tiles(a.w.rows);
+  if (m > 64 && (squares > sms || (m > 128 && kt > 16 && 2 * squares > sms))) return launch_pair<kNv, kBf16>(a, s);
   const int nt = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
-  const int64_t tiles = f4_row_tiles(a.w.rows) * ((m + nt - 1) / nt), per = nt <= 32 ? 4 : 2;
-  const int64_t steps = (kt + per - 1) / per, most = 2 * device_sm_count();
+  const int64_t tiles = f4_row_tiles(a.w.rows) * ((m + nt - 1) / nt), per = nt <= 32 ? 4 : 2, steps = (kt + per - 1) / per;
   int ranks = 1;
-  for (const int r : {2, 3, 4, 6, 8})
-    if (r <= steps && tiles * r <= most && (nt < 128 || tiles * r <= 100 || (tiles > 33 && r <= 4))) ranks = r;
+  for (const auto &r : kRanks)
+    if (r[0] <= steps && tiles * r[0] <= (nt < 128 ? 2 * sms * r[2] : sms * r[1]) / 100) ranks = r[0];
   switch (nt) {
     case 16: return launch_split<16, kNv, kBf16>(a, ranks, s);
     case 32: return launch_split<32, kNv, kBf16>(a, ranks, s);
