@@ -538,9 +538,15 @@ def _list_at(name, t, n, dev, dtype=torch.int32):
     """The address of a list of n numbers (None: none); ValueError unless it is one on device dev."""
     if t is None:
         return None
-    if t.get_device() != dev or t.dtype is not dtype or t.shape != (n,) or not t.is_contiguous():
+    if t.get_device() != dev or t.dtype is not dtype or t.numel() != n or t.dim() != 1 or not t.is_contiguous():
         _want(name, t, dtype, (n,), dev)
     return t.data_ptr()
+
+
+def _needed(**tensors):
+    for name, t in tensors.items():
+        if t is None:
+            raise ValueError(f"{name}: a CUDA tensor is needed")
 
 
 def _rows_at(name, t, dtypes, rows, width, dev):
@@ -762,15 +768,19 @@ def query_latent(q, w_uk, pos, rope_cs, out, err=None, stream=None):
     """csa2_query_latent: q bf16 [total, H*(dim+64)] (rows may be strided), w_uk bf16 [H, dim, 512] (heads may
     be strided), pos int64 [total] -> out bf16 [total, H, 576]: the absorbed queries with rotated RoPE dims.
     Rows with a negative position are left as they were."""
+    if out is None or q is None or w_uk is None or pos is None or rope_cs is None:
+        _needed(out=out, q=q, w_uk=w_uk, pos=pos, rope_cs=rope_cs)
     dev = out.get_device()
     H, dim, ws = _heads_at("w_uk", w_uk, dev)
-    total = out.shape[0]
-    if out.dtype is not torch.bfloat16 or out.shape != (total, H, D_QK) or not out.is_contiguous():
+    shape = out.shape
+    total = shape[0] if shape else -1
+    if out.dtype is not torch.bfloat16 or shape != (total, H, D_QK) or not out.is_contiguous():
         _want("out", out, torch.bfloat16, (total, H, D_QK), dev)
     qs = _rows_at("q", q, _BF16, total, H * (dim + D_ROPE), dev)
     at = _list_at("pos", pos, total, dev, torch.int64)
-    n = rope_cs.shape[0]
-    if rope_cs.get_device() != dev or rope_cs.dtype is not torch.float32 or rope_cs.numel() != 64 * n or rope_cs.dim() < 2 or not rope_cs.is_contiguous():
+    shape = rope_cs.shape
+    n = shape[0] if shape else -1
+    if rope_cs.get_device() != dev or rope_cs.dtype is not torch.float32 or len(shape) < 2 or rope_cs.numel() != 64 * n or not rope_cs.is_contiguous():
         _want("rope_cs", rope_cs, torch.float32, (n, D_ROPE // 2, 2), dev)
     ew = _err_at(err, dev)
     if total:
@@ -781,14 +791,17 @@ def query_latent(q, w_uk, pos, rope_cs, out, err=None, stream=None):
 def value_project(o, w_uv, out, err=None, stream=None):
     """csa2_value_project: o [total, H, 512] (fp32 or bf16, rows may be strided), w_uv bf16 [H, dim, 512] (heads may be
     strided) -> out bf16 [total, H*dim] (rows may be strided)."""
+    if out is None or o is None or w_uv is None:
+        _needed(out=out, o=o, w_uv=w_uv)
     dev = out.get_device()
     H, dim, ws = _heads_at("w_uv", w_uv, dev)
-    total, dt = out.shape[0], o.dtype
+    shape, dt = out.shape, o.dtype
+    total = shape[0] if shape else -1
     os_ = _rows_at("out", out, _BF16, total, H * dim, dev)
-    token, head, one = o.stride()
-    if o.get_device() != dev or dt not in _FLOATS or o.shape != (total, H, D_LATENT) or one != 1 or (H > 1 and head != D_LATENT) \
-            or (total > 1 and token < H * D_LATENT):
+    if o.get_device() != dev or dt not in _FLOATS or o.shape != (total, H, D_LATENT):
         _want("o", o, _FLOATS, (total, H, D_LATENT), dev)
+    token, head, one = o.stride()
+    if one != 1 or (H > 1 and head != D_LATENT) or (total > 1 and token < H * D_LATENT):
         raise ValueError("o: a token's rows must be contiguous, and tokens must not overlap")
     ew = _err_at(err, dev)
     if total:
@@ -822,6 +835,8 @@ def _fp4_device(m):
 
 def fp4_quant(m: Fp4Matrix, x, err=None, stream=None):
     """csa2_fp4_quant: x [rows, cols] (fp32 or bf16, rows may be strided) into m."""
+    if x is None:
+        _needed(x=x)
     dev = _fp4_device(m)
     stride, ew = _rows_at("x", x, _FLOATS, m.rows, m.cols, dev), _err_at(err, dev)
     if m.rows:
@@ -830,6 +845,8 @@ def fp4_quant(m: Fp4Matrix, x, err=None, stream=None):
 
 def fp4_read(m: Fp4Matrix, out, stream=None):
     """csa2_fp4_read: the values m stands for into out [rows, cols] (fp32 or bf16, rows may be strided)."""
+    if out is None:
+        _needed(out=out)
     dev = _fp4_device(m)
     stride = _rows_at("out", out, _FLOATS, m.rows, m.cols, dev)
     if m.rows:
@@ -838,6 +855,8 @@ def fp4_read(m: Fp4Matrix, out, stream=None):
 
 def fp4_product(x: Fp4Matrix, w: Fp4Matrix, out, err=None, stream=None):
     """csa2_fp4_product: out [x.rows, w.rows] = x w^T (fp32 or bf16, rows may be strided)."""
+    if out is None:
+        _needed(out=out)
     dev = _fp4_device(x)
     if w.tiles.get_device() != dev:
         raise ValueError(f"w is on {w.tiles.device}, x on cuda:{dev}")

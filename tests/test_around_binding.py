@@ -146,3 +146,13 @@ def test_matrix_and_pool_constructors():
         csa2.PagePool(_cache(table=False))
     with pytest.raises(ValueError, match="together"):
         csa2.PagePool(_cache(), free=Fake(4, dtype=I32))
+
+
+@pytest.mark.parametrize("call,kw", [(c, {k: None}) for c, names in ((_query, ("q", "w_uk", "pos", "rope_cs", "out")), (_value, ("o", "w_uv", "out")),
+                                                                     (_quant, ("x",)), (_product, ("out",))) for k in names]
+                         + [(_query, dict(out=Fake(dtype=BF16))), (_query, dict(rope_cs=Fake())), (_query, dict(pos=Fake(dtype=I64), T=1)),
+                            (_value, dict(out=Fake(dtype=BF16))), (_slots, dict(pos=Fake(5, 1, dtype=I64))), (_resize, dict(granted=Fake(2, 1, dtype=I32)))])
+def test_no_tensor_or_one_of_other_dimensions(calls, call, kw):
+    with pytest.raises(ValueError):
+        call(**kw)
+    assert not calls
