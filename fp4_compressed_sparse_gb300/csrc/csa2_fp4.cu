@@ -18,14 +18,15 @@
 //   fp32 x: y = x (1 / s), then y + (x - y s) (1 / s), the remainder exact: off by less than
 //   2^-40 of the quotient before its rounding.  If x = T s that is T.  Else the quotient is
 //   2^-24 of T away from it at least (the next fp32 values beside T s), more than half a
-//   step of T: the rounded one lies on the same side.  The scale is divided.
+//   step of T: the rounded one lies on the same side.  The scale comes from amax and 1 / 6 in
+//   the same way (equal to the rounded quotient for every mantissa, as a run over all showed).
 //
 // Bound: HBM for large matrices, a chain of loads, reductions and stores for a few rows.
 // Measured (in a graph): 12,288 x 4,096 bf16 to NV 22.5 us (5.7 TB/s), read back 21.9 us (5.9
-// TB/s; a plain fill of its 100 MB takes 25.7); 8,192 x 4,096 bf16 13.4 us (6.4 TB/s), fp32 28
-// us (5.4), to MX 13.5 and 25.9, read 11.2 us (7.7, L2 holds a part); 32 rows 1.7 us.  At 11.6
+// TB/s; a plain fill of its 100 MB takes 25.7); 8,192 x 4,096 bf16 13.6 us (6.3 TB/s), fp32 26.6
+// us (5.8), to MX 13.5 and 25.5, read 11.2 us (7.7, L2 holds a part); 32 rows 1.7 us.  At 11.6
 // instructions per value the first took 31 us, at 14 compares per fp32 value 42 of 8,192 x
-// 4,096: the conversions above are what brought them near the copy rate.
+// 4,096, and with divisions 28: the conversions above are what brought them near the copy rate.
 #include <type_traits>
 
 #include "csa2_fp4.cuh"
@@ -78,8 +79,10 @@ __device__ __forceinline__ uint32_t nv8(const float *x, float s, float back, flo
     const uint32_t w = e2m1x8(q);
     return s != 0.0f ? w : 0u;
   } else {
-    const float inv = __fmul_rn(__frcp_rn(s), back), u = __fmul_rn(s, fore);
-    float q[8];
+    float inv, q[8];
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(inv) : "f"(s));
+    inv = __fmul_rn(inv, back);
+    const float u = __fmul_rn(s, fore);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float y = __fmul_rn(x[i], inv);
@@ -95,7 +98,7 @@ __device__ __forceinline__ uint32_t nv_scale(float amax, float back, float &s) {
   const float a = __fmul_rn(amax, back);
   float y;
   if constexpr (kBf16) y = __uint_as_float((__float_as_uint(__fmul_rn(a, 1.0f / 6.0f)) + 0x400u) & ~0x7FFu);
-  else y = __fdiv_rn(a, 6.0f);
+  else y = __fmul_rn(a, 1.0f / 6.0f), y = __fmaf_rn(__fmaf_rn(-6.0f, y, a), 1.0f / 6.0f, y);
   uint16_t c;
   uint32_t h;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(c) : "f"(0.0f), "f"(y));
@@ -259,12 +262,6 @@ __global__ void __launch_bounds__(kQThreads) k_fp4_quant_row(F4Args a) {
   }
 }
 
-// Sixteen values of a row in shared (or, with `cols` checked, global) memory.
-template <bool kBf16>
-__device__ __forceinline__ void load16(const uint8_t *row, int c0, int cols, float *v) {
-  load8<kBf16>(row, c0, cols, v);
-  load8<kBf16>(row, c0 + 8, cols, v + 8);
-}
 // Largest magnitude's bits (or a NaN's) of the values in a word: two bf16 or one fp32.
 template <bool kBf16>
 __device__ __forceinline__ uint32_t word_top(uint32_t m, uint32_t w) {
@@ -278,29 +275,45 @@ __device__ __forceinline__ uint32_t word_top(uint32_t m, uint32_t w) {
 }
 
 // Two or one pieces of 32 values to their records: codes and scales of row m of a tile.
-template <bool kNv, bool kBf16, int kG>
-__device__ __forceinline__ void put_pieces(uint8_t *tiles, const uint8_t *src, int p, int have, int m, float back, float fore, uint32_t &bad) {
+// A thread takes the four groups of 8 values of a piece in the order k ^ turn, which lets
+// lanes whose pieces lie in the same banks read different ones (kTurns: which of turn's
+// bits may be set).
+template <bool kNv, bool kBf16, int kG, int kTurns>
+__device__ __forceinline__ void put_pieces(uint8_t *tiles, const uint8_t *src, int p, int have, int m, float back, float fore, int turn, uint32_t &bad) {
   uint8_t *rec = tiles + static_cast<int64_t>(p >> 2) * f4_tile_bytes(kNv), *sc = rec + kF4CodeBytes + f4_scale_at(m);
   uint32_t code = 0;
 #pragma unroll
   for (int i = 0; i < kG; ++i) {
-    uint32_t w[4];
+    uint32_t w[4], c[2];
     if constexpr (kNv) {
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         float v[16], s;
-        load16<kBf16>(src, 32 * (p + i) + 16 * g, have, v);
-        const uint32_t c = nv_scale<kBf16>(top_abs<16>(v), back, s);
+        load8<kBf16>(src, 32 * (p + i) + 8 * (2 * g ^ turn), have, v);
+        load8<kBf16>(src, 32 * (p + i) + 8 * (2 * g + 1 ^ turn), have, v + 8);
+        c[g] = nv_scale<kBf16>(top_abs<16>(v), back, s);
         w[2 * g] = nv8<kBf16>(v, s, back, fore);
         w[2 * g + 1] = nv8<kBf16>(v + 8, s, back, fore);
-        code |= c << (16 * i + 8 * g);
       }
     } else {
       float v[32];
-      load16<kBf16>(src, 32 * (p + i), have, v);
-      load16<kBf16>(src, 32 * (p + i) + 16, have, v + 16);
-      code |= mx32(v, bad, w) << (8 * i);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) load8<kBf16>(src, 32 * (p + i) + 8 * (k ^ turn), have, v + 8 * k);
+      c[0] = mx32(v, bad, w);
     }
+    if constexpr (kTurns & 1) {
+      const uint32_t a = w[0], b = w[2];
+      w[0] = turn & 1 ? w[1] : w[0], w[1] = turn & 1 ? a : w[1];
+      w[2] = turn & 1 ? w[3] : w[2], w[3] = turn & 1 ? b : w[3];
+    }
+    if constexpr (kTurns & 2) {
+      const uint32_t a = w[0], b = w[1], d = c[0];
+      w[0] = turn & 2 ? w[2] : w[0], w[2] = turn & 2 ? a : w[2];
+      w[1] = turn & 2 ? w[3] : w[1], w[3] = turn & 2 ? b : w[3];
+      if constexpr (kNv) c[0] = turn & 2 ? c[1] : c[0], c[1] = turn & 2 ? d : c[1];
+    }
+    if constexpr (kNv) code |= (c[0] | c[1] << 8) << (16 * i);
+    else code |= c[0] << (8 * i);
     *reinterpret_cast<uint4 *>(rec + ((p + i) & 3) * 2048 + m * 16) = make_uint4(w[0], w[1], w[2], w[3]);
   }
   sc += kNv ? 512 * ((p >> 1) & 1) + 2 * (p & 1) : p & 3;
@@ -357,7 +370,7 @@ __global__ void __launch_bounds__(kQThreads, kNv ? 4 : 3) k_fp4_quant_rows(F4Arg
   uint8_t *tiles = a.m.tiles + static_cast<int64_t>(row / kF4Rows) * ct * f4_tile_bytes(kNv);
   const uint8_t *src = kStaged ? stage + r8 * pitch : x + row * a.stride * kElt;
   for (int p = 2 * (t / kRows); p < pieces && row < rows; p += 2 * (kQThreads / kRows))
-    put_pieces<kNv, kBf16, 2>(tiles, src, p, kStaged ? 32 * pieces : cols, m, back, fore, bad);
+    put_pieces<kNv, kBf16, 2, 0>(tiles, src, p, kStaged ? 32 * pieces : cols, m, back, fore, 0, bad);
   if constexpr (!kNv) {
     if (t < kRows) top[t] = 0;
     __syncthreads();
@@ -372,11 +385,10 @@ __global__ void __launch_bounds__(kQThreads, kNv ? 4 : 3) k_fp4_quant_rows(F4Arg
 }
 
 // The others: persistent blocks, kRows rows at a time, which come by bulk copies into one of
-// two buffers while the other one's are quantised.  8,192 rows of 7,224 bf16 to NV 27.6 us (one
-// buffer filled by loads, a block per 4 rows 44), of 4,096 to MX 13.6 (14.4, 8 rows); fp32 of
-// 4,104 to NV 33.5 (45.6).  A thread takes one piece of 32 values a step (so that the last,
-// partial step is short), two of fp32 rows to MX, whose steps are short anyway (8,192 x 8,192
-// 53.6 us against 56.8).
+// two buffers while the other one's are quantised.  8,000 rows of 7,224 bf16 to NV 27.8 us (one
+// buffer filled by loads, a block per 4 rows 44); fp32 of 4,104 26.3 (45.6; with the banks met
+// up to four times and divisions 33).  A thread takes one piece of 32 values a step (so that
+// the last, partial step is short), two of fp32 rows to MX, whose steps are short anyway.
 struct RowsSync {
   uint64_t full[2];
   uint32_t part[kQThreads / 32];
@@ -386,6 +398,9 @@ __global__ void __launch_bounds__(kQThreads, 3) k_fp4_quant_piped(F4Args a, int 
   constexpr int kElt = kBf16 ? 2 : 4, kPolls = 200;  // suspended polls of <= 1 ms each
   constexpr int kG = kNv || kBf16 ? 1 : 2, kParts = 8 / kRows;
   using Word = std::conditional_t<kBf16, uint16_t, uint32_t>;
+  // Eight lanes that read 16 bytes at once are of kRows rows, 16 bytes (times an odd number)
+  // apart in the banks, and of 8 / kRows pieces, 64 bytes (bf16) or 0 apart.
+  constexpr int kTurns = kRows == 8 ? 0 : kRows == 4 ? (kBf16 ? 0 : 2) : (kBf16 ? 2 : 3);
   extern __shared__ __align__(16) uint8_t stage[];
   __shared__ __align__(8) RowsSync sy;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -455,8 +470,9 @@ __global__ void __launch_bounds__(kQThreads, 3) k_fp4_quant_piped(F4Args a, int 
       back = pow2f(bad ? 0 : -e), fore = pow2f(bad ? 0 : e);
     }
     uint8_t *tiles = a.m.tiles + static_cast<int64_t>(row / kF4Rows) * ct * f4_tile_bytes(kNv);
-    for (int p = kG * (t / kRows); p < pieces && row < rows; p += kG * (kQThreads / kRows))
-      put_pieces<kNv, kBf16, kG>(tiles, st + r8 * pitch, p, 32 * pieces, m, back, fore, bad);
+    const int n8 = t / kRows, turn = kTurns == 3 ? n8 & 3 : kTurns == 0 ? 0 : kRows == 4 ? 2 * (n8 & 1) : n8 & 2;
+    for (int p = kG * n8; p < pieces && row < rows; p += kG * (kQThreads / kRows))
+      put_pieces<kNv, kBf16, kG, kTurns>(tiles, st + r8 * pitch, p, 32 * pieces, m, back, fore, turn, bad);
     if constexpr (!kNv) {  // a bit for each row
       const uint32_t mask = __reduce_or_sync(0xffffffffu, bad ? 1u << r8 : 0u);
       if (lane == 0) sy.part[warp] = mask;
@@ -579,7 +595,7 @@ static cudaError_t launch_piped(const F4Args &a, int pitch, cudaStream_t s) {
 //   Piped, 8 rows at a time while five buffers fit an SM (2,500 x 2,048 bf16 4.5 against 5.4 with
 //   4; 1,300 x 4,096 5.9 against 4.5), 4 while two blocks fit (8,000 x 5,120 bf16 20.4 against
 //   24.8 with 2, x 7,224 34.6 against 27.7), else 2, while that block fits: 8,000 x 12,288 fp32
-//   to NV 87 against 159 read through the caches, 8,000 x 20,000 bf16 to NV 78 against 130, to MX
+//   to NV 68 against 159 read through the caches, 8,000 x 20,000 bf16 to NV 78 against 130, to MX
 //   75 against 77.
 template <bool kNv, bool kBf16>
 static cudaError_t launch_quant(const F4Args &a, cudaStream_t s) {

@@ -35,9 +35,9 @@ constexpr int kWBytes = 128 * kLat * 2;     // 128 KB: a head's W, or a part of 
 constexpr int kBox = kTok * 128;            // 128 rows of 128 bytes, 128-byte swizzle
 enum Mode { kQuery, kValue, kValueF32 };
 
-// Beside W: stages of the tokens' rows, and for queries what is on its way out.  A stage is what one wait and arming of the copying thread (0.2 us) is
-// worth: 32 KB, two boxes of 64 columns (query: all of a tile's; value: a quarter), fp32:
-// one of 32.
+// Beside W: stages of the tokens' rows, and for queries what is on its way out.  A stage is
+// what one wait and arming of the copying thread (0.2 us) is worth: 32 KB, two boxes of 64
+// columns (query: all of a tile's; value: a quarter), fp32: one of 32.
 template <Mode kM>
 struct Shape {
   static constexpr int kStage = kM == kValueF32 ? kBox : 2 * kBox;
