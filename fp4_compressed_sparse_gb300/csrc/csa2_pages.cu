@@ -122,6 +122,8 @@ __global__ void __launch_bounds__(kPageThreads) k_pages_resize(PagesArgs a) {
   __shared__ int32_t l_held[kPageThreads], l_need[kPageThreads];
   const int t = threadIdx.x, nthr = blockDim.x, rank = blockIdx.x, ctas = gridDim.x;
   const int batch = a.c.batch, mp = a.c.max_pages;
+  next_may_start();
+  wait_for_previous();
   const int64_t n0 = *a.pool.n_free;
   int falls = 0;
   if (a.cu != nullptr)
@@ -235,6 +237,8 @@ __global__ void __launch_bounds__(kPageThreads) k_pages_resize(PagesArgs a) {
 // One thread per packed row: its sequence (a binary search in cu), position and entry.
 __global__ void __launch_bounds__(256) k_slot_map(csa2_cache c, const int32_t *cu, int total, int max_new, int64_t *slots,
                                                   int64_t *pos, int32_t *err) {
+  next_may_start();
+  wait_for_previous();
   const int r = blockIdx.x * 256 + threadIdx.x;
   if (r < c.batch) {  // every broken list shows in some sequence's bounds
     int first, n;
@@ -290,17 +294,9 @@ csa2_status csa2_pages_resize(const csa2_cache *cache, const csa2_page_pool *poo
   csa2::PagesArgs a{*cache, const_cast<int32_t *>(cache->block_table), *pool, target, cu_new, total, max_new, granted, err_word};
   const int threads = cache->batch >= csa2::kPageThreads ? csa2::kPageThreads : (cache->batch + 31) / 32 * 32;
   const int block = threads < 256 ? 256 : threads;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(csa2::kPageCtas);
-  cfg.blockDim = dim3(block);
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = csa2::kPageCtas;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cuda_status(cudaLaunchKernelEx(&cfg, csa2::k_pages_resize, a), "csa2_pages_resize launch");
+  return cuda_status(csa2::launch_after(csa2::k_pages_resize, dim3(csa2::kPageCtas), block, 0, csa2::kPageCtas,
+                                        reinterpret_cast<cudaStream_t>(stream), a),
+                     "csa2_pages_resize launch");
 }
 
 csa2_status csa2_slot_map(const csa2_cache *cache, const int32_t *cu_new, int32_t total, int32_t max_new, int64_t *slots,
@@ -315,9 +311,9 @@ csa2_status csa2_slot_map(const csa2_cache *cache, const int32_t *cu_new, int32_
   CSA2_REQUIRE_OPT_PTR(pos);
   if (total == 0) return CSA2_OK;
   const int n = total > cache->batch ? total : cache->batch;
-  csa2::k_slot_map<<<(n + 255) / 256, 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(*cache, cu_new, total, max_new, slots,
-                                                                                      pos, err_word);
-  return cuda_status(cudaGetLastError(), "csa2_slot_map launch");
+  return cuda_status(csa2::launch_after(csa2::k_slot_map, dim3((n + 255) / 256), 256, 0, 0, reinterpret_cast<cudaStream_t>(stream), *cache,
+                                        cu_new, total, max_new, slots, pos, err_word),
+                     "csa2_slot_map launch");
 }
 
 }  // extern "C"

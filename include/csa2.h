@@ -582,7 +582,7 @@ size_t csa2_fp4_plane_bytes(int32_t rows, int32_t cols, int32_t format, int32_t 
  * x + t * x_stride elements (x_stride >= cols, a multiple of 8), into the matrix m.
  * csa2_fp4_read: the values m stands for, out_dtype (CSA2_OUT_*), rows out_stride
  * elements apart (>= cols, a multiple of 8); exact in fp32, and in bf16 too.
- * Device errors (quant): NAN, TIMEOUT.
+ * x or out must not overlap m's planes.  Device errors (quant): NAN, TIMEOUT.
  */
 csa2_status csa2_fp4_quant(const csa2_fp4_matrix *m, const void *x, int64_t x_stride, int32_t in_dtype, int32_t *err_word,
                            csa2_stream_t stream);
@@ -631,7 +631,7 @@ csa2_status csa2_query_latent(const uint16_t *q, int64_t q_stride, int32_t total
  * (magnitudes from bf16's largest on as infinities).
  * n_heads 1..128, dim a multiple of 16, 16..128.  Device errors: TIMEOUT.
  * In both calls a row's last bits may change with the number of rows; equal calls
- * give equal bits.
+ * give equal bits; out must not overlap what is read.
  */
 csa2_status csa2_value_project(const void *o, int64_t o_stride, int32_t in_dtype, int32_t total, int32_t n_heads, int32_t dim,
                                const uint16_t *w_uv, int64_t w_stride, uint16_t *out, int64_t out_stride, int32_t *err_word,
