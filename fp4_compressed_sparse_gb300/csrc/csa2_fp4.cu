@@ -399,8 +399,9 @@ __global__ void __launch_bounds__(kQThreads, 3) k_fp4_quant_piped(F4Args a, int 
   constexpr int kG = kNv || kBf16 ? 1 : 2, kParts = 8 / kRows;
   using Word = std::conditional_t<kBf16, uint16_t, uint32_t>;
   // Eight lanes that read 16 bytes at once are of kRows rows, 16 bytes (times an odd number)
-  // apart in the banks, and of 8 / kRows pieces, 64 bytes (bf16) or 0 apart.
-  constexpr int kTurns = kRows == 8 ? 0 : kRows == 4 ? (kBf16 ? 0 : 2) : (kBf16 ? 2 : 3);
+  // apart in the banks, and of 8 / kRows pieces, 64 bytes (bf16) or 0 apart.  (8 pieces of an
+  // fp32 row still meet twice.)
+  constexpr int kTurns = kRows == 8 ? 0 : kRows == 4 ? (kBf16 ? 0 : 2) : kRows == 2 && kBf16 ? 2 : 3;
   extern __shared__ __align__(16) uint8_t stage[];
   __shared__ __align__(8) RowsSync sy;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(kQThreads, 3) k_fp4_quant_piped(F4Args a, int 
       back = pow2f(bad ? 0 : -e), fore = pow2f(bad ? 0 : e);
     }
     uint8_t *tiles = a.m.tiles + static_cast<int64_t>(row / kF4Rows) * ct * f4_tile_bytes(kNv);
-    const int n8 = t / kRows, turn = kTurns == 3 ? n8 & 3 : kTurns == 0 ? 0 : kRows == 4 ? 2 * (n8 & 1) : n8 & 2;
+    const int n8 = t / kRows, turn = kTurns == 3 ? (kBf16 ? n8 >> 1 : n8) & 3 : kTurns == 0 ? 0 : kRows == 4 ? 2 * (n8 & 1) : n8 & 2;
     for (int p = kG * n8; p < pieces && row < rows; p += kG * (kQThreads / kRows))
       put_pieces<kNv, kBf16, kG, kTurns>(tiles, st + r8 * pitch, p, 32 * pieces, m, back, fore, turn, bad);
     if constexpr (!kNv) {  // a bit for each row
@@ -594,9 +595,9 @@ static cudaError_t launch_piped(const F4Args &a, int pitch, cudaStream_t s) {
 //   against 3.1 piped.
 //   Piped, 8 rows at a time while five buffers fit an SM (2,500 x 2,048 bf16 4.5 against 5.4 with
 //   4; 1,300 x 4,096 5.9 against 4.5), 4 while two blocks fit (8,000 x 5,120 bf16 20.4 against
-//   24.8 with 2, x 7,224 34.6 against 27.7), else 2, while that block fits: 8,000 x 12,288 fp32
-//   to NV 68 against 159 read through the caches, 8,000 x 20,000 bf16 to NV 78 against 130, to MX
-//   75 against 77.
+//   24.8 with 2, x 7,224 34.6 against 27.7), else 2, or 1, while a block fits: 8,000 x 12,288 fp32 to
+//   NV 68 against 159 read through the caches, 5,000 x 20,000 fp32 to NV 79 against 182, to MX
+//   76 against 103.
 template <bool kNv, bool kBf16>
 static cudaError_t launch_quant(const F4Args &a, cudaStream_t s) {
   const int sms = device_sm_count(), rows = a.m.rows;
@@ -613,6 +614,7 @@ static cudaError_t launch_quant(const F4Args &a, cudaStream_t s) {
   if (rows >= 16 * sms && 8 * pitch <= 40 * kK) return launch_piped<kNv, kBf16, 8>(a, pitch, s);
   if (4 * pitch <= 44 * kK) return launch_piped<kNv, kBf16, 4>(a, pitch, s);
   if (2 * pitch <= 110 * kK) return launch_piped<kNv, kBf16, 2>(a, pitch, s);
+  if (pitch <= 110 * kK) return launch_piped<kNv, kBf16, 1>(a, pitch, s);
   return launch_rows<kNv, kBf16, false>(a, 0, s);
 }
 

@@ -52,7 +52,7 @@ def _packed(x, fmt, err=None):
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 128), (3, 136), (17, 31), (130, 520), (129, 4104), (2000, 264), (1300, 2056), (1217, 130), (1400, 6000), (1290, 17000),
                                        (7, 8192), (9, 8200), (2, 20000), (5, 2049), (3, 6144), (1221, 500),
                                        (1220, 1000), (1300, 4096), (1219, 4100), (1225, 8192), (1218, 8200), (1219, 10400),
-                                       (1221, 5), (1250, 8), (1231, 20003), (1229, 2050), (4900, 136), (4871, 2050), (4866, 3001), (5003, 4099), (4865, 14200)])
+                                       (1221, 5), (1250, 8), (1231, 20003), (1229, 2050), (4900, 136), (4871, 2050), (4866, 3001), (5003, 4099), (4865, 14200), (1221, 13990), (1219, 28605)])
 def test_quant_is_the_definition(fmt, dtype, rows, cols):
     """Codes and scales as values, equal; read back in both types; strided rows; columns behind the
     last one of the tile are zeros."""
