@@ -13,8 +13,8 @@
 //
 // Bound: latency.  A decode step of 32 sequences reads a few hundred bytes; what it
 // takes is the chain lengths -> prefix sum -> barrier -> free list -> table.  32 sequences
-// of 65,536 tokens 3.7 us, 512 with 51 that end and 51 prompts (4,011 pages moved) 4.9, a
-// launch alone 1.4; the slots of 32 and of 104,034 tokens 2.8 and 4.1.
+// of 65,536 tokens 3.2 us, 512 with 51 that end and 51 prompts (4,011 pages moved) 4.0, a
+// launch alone 1.4; the slots of 32 and of 104,034 tokens 2.3 and 4.2.
 #include "csa2_internal.cuh"
 
 namespace csa2 {
@@ -41,14 +41,18 @@ struct SeqPages {
   int held, need;
   bool ok;
 };
-__device__ __forceinline__ SeqPages seq_pages(const PagesArgs &a, int b, int falls, bool report) {
-  SeqPages s{a.pool.held[b], 0, false};
+struct SeqIn {
+  int held;
+  int64_t n;  // the target, or the tokens before the step
+};
+__device__ __forceinline__ SeqIn seq_in(const PagesArgs &a, int b) {
+  return SeqIn{a.pool.held[b], a.target != nullptr ? a.target[b] : a.c.n_tokens[b]};
+}
+__device__ __forceinline__ SeqPages seq_pages(const PagesArgs &a, int b, SeqIn in, int falls, bool report) {
+  SeqPages s{in.held, 0, false};
   bool good = s.held >= 0 && s.held <= a.c.max_pages;
-  int64_t n;
-  if (a.target != nullptr) {
-    n = a.target[b];
-  } else {
-    n = a.c.n_tokens[b];
+  int64_t n = in.n;
+  if (a.target == nullptr) {
     good = good && n >= 0;
     if (a.cu != nullptr) {
       int first, cnt;
@@ -125,24 +129,26 @@ __global__ void __launch_bounds__(kPageThreads) k_pages_resize(PagesArgs a) {
   next_may_start();
   wait_for_previous();
   const int64_t n0 = *a.pool.n_free;
+  const bool one = batch <= nthr;
+  SeqIn in{0, 0};
+  if (one && t < batch) in = seq_in(a, t);  // (on its way while the bounds are read)
   int falls = 0;
   if (a.cu != nullptr)
     for (int b = t; b < batch; b += nthr) falls |= a.cu[b + 1] < a.cu[b];
   falls = __syncthreads_or(falls);
 
   // pages that go back, altogether (one chunk: the scan below has them)
-  const bool one = batch <= nthr;
   SeqPages s{0, 0, false};
   int64_t R = 0;
   if (!one) {
     int64_t mine = 0;
     for (int b = t; b < batch; b += nthr) {
-      s = seq_pages(a, b, falls, rank == 0);
+      s = seq_pages(a, b, seq_in(a, b), falls, rank == 0);
       mine += max(s.held - s.need, 0);
     }
     R = block_scan2(mine, 0, sh).tx;
   } else if (t < batch) {
-    s = seq_pages(a, t, falls, rank == 0);
+    s = seq_pages(a, t, in, falls, rank == 0);
   }
   Scan2 c{};
   if (one) {
@@ -158,7 +164,7 @@ __global__ void __launch_bounds__(kPageThreads) k_pages_resize(PagesArgs a) {
   for (int b0 = 0; b0 < batch && sound && R > 0; b0 += nthr) {
     const int b = b0 + t;
     if (!one) {
-      s = b < batch ? seq_pages(a, b, falls, false) : SeqPages{0, 0, false};
+      s = b < batch ? seq_pages(a, b, seq_in(a, b), falls, false) : SeqPages{0, 0, false};
       c = block_scan2(max(s.held - s.need, 0), 0, sh);
     }
     l_back[t] = c.x;
@@ -185,7 +191,7 @@ __global__ void __launch_bounds__(kPageThreads) k_pages_resize(PagesArgs a) {
   for (int b0 = 0; b0 < batch && sound; b0 += nthr) {
     const int b = b0 + t;
     if (!one) {
-      s = b < batch ? seq_pages(a, b, falls, false) : SeqPages{0, 0, false};
+      s = b < batch ? seq_pages(a, b, seq_in(a, b), falls, false) : SeqPages{0, 0, false};
       c = block_scan2(0, max(s.need - s.held, 0), sh);
     }
     const int64_t fit = n1 - base;  // what the chunk may take
@@ -221,7 +227,7 @@ __global__ void __launch_bounds__(kPageThreads) k_pages_resize(PagesArgs a) {
   for (int b0 = 0; b0 < batch; b0 += nthr) {
     const int b = b0 + t;
     if (!one) {  // (held[b] is still the old one: this thread writes it next)
-      s = b < batch ? seq_pages(a, b, falls, false) : SeqPages{0, 0, false};
+      s = b < batch ? seq_pages(a, b, seq_in(a, b), falls, false) : SeqPages{0, 0, false};
       c = block_scan2(0, max(s.need - s.held, 0), sh);
     }
     if (b < batch) {
