@@ -135,3 +135,42 @@ def test_layer_as_a_graph():
         assert int(a.err) == 0 and int(b.err) == 0
         for p, q in ((a.c.block_table, b.c.block_table), (a.c.n_tokens, b.c.n_tokens), (a.lat[:n], b.lat[:n]), (a.att[:n], b.att[:n]), (a.out[:n], b.out[:n])):
             assert torch.equal(p, q)
+
+
+def test_calls_of_all_kinds_at_once():
+    """Queries, values, quantisations and products of several sizes on five streams at once: the bits of the
+    same calls one after the other."""
+    g = torch.Generator(device=DEV).manual_seed(11)
+    rand = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    H, D = 16, 64
+    w = (rand(H, 2 * D, 512) / 20).to(torch.bfloat16)
+    rope = csa2.rope_table(10000.0, 4000)
+    jobs = []
+    for T in (3, 300, 1500):
+        q, pos, out = rand(T, H * (D + 64)).to(torch.bfloat16), torch.arange(T, device=DEV), torch.zeros(T, H, 576, dtype=torch.bfloat16, device=DEV)
+        jobs.append((out, lambda s, q=q, pos=pos, out=out: csa2.query_latent(q, w[:, :D], pos, rope, out, stream=s)))
+    for T, dtype in ((3, torch.float32), (700, torch.float32), (1500, torch.bfloat16)):
+        o, out = rand(T, H, 512).to(dtype), torch.zeros(T, H * D, dtype=torch.bfloat16, device=DEV)
+        jobs.append((out, lambda s, o=o, out=out: csa2.value_project(o, w[:, D:], out, stream=s)))
+    for M, N, K, fmt in ((1, 2000, 1040, csa2.FP4_NV), (50, 1400, 520, csa2.FP4_MX), (400, 600, 2056, csa2.FP4_NV), (2500, 2600, 264, csa2.FP4_MX),
+                         (1500, 304, 4104, csa2.FP4_NV)):
+        x, b, m, out = rand(M, K), csa2.Fp4Matrix(N, K, fmt), csa2.Fp4Matrix(M, K, fmt), torch.zeros(M, N, device=DEV)
+        csa2.fp4_quant(b, rand(N, K))
+
+        def step(s, x=x, b=b, m=m, out=out):
+            csa2.fp4_quant(m, x, stream=s)
+            csa2.fp4_product(m, b, out, stream=s)
+        jobs.append((out, step))
+    want = []
+    for out, job in jobs:
+        job(None)
+        torch.cuda.synchronize()
+        want.append(out.clone())
+        out.zero_()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(5)]
+    for _ in range(30):
+        for i, (_, job) in enumerate(jobs):
+            job(streams[i % 5])
+    torch.cuda.synchronize()
+    assert all(torch.equal(out, v) for (out, _), v in zip(jobs, want))
