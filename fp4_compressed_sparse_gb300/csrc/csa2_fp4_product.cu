@@ -387,6 +387,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   using L = Pair<kNv>;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(128) PairSync sy;
+  __shared__ __align__(16) float r_col[2][kPairN];  // powers of two of a tile's columns, and of the next one's
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   uint32_t rank;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -507,15 +508,20 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     // ------------------------------------------------------------ results
     const int q = warp & 3, half = (warp - 4) >> 2;
     uint32_t j = 0;
-    bool ok = true;
-    for (int i = first; i < tiles && ok; i += pairs, ++j) {
+    bool gone = false;  // a wait gave up: the other warps still meet this one at the barrier
+    for (int i = first; i < tiles; i += pairs, ++j) {
       int m, n;
       tile_of(i, m, n);
       const int row = m * kF4Rows + 32 * q + lane, c0 = n * kPairN + 128 * half;
       const bool live = row < a.x.rows;
       const float r_m = live ? a.x.row_scales[row] : 0.0f;
-      ok = __all_sync(0xffffffffu, tc::mbar_wait_bounded(&sy.tfull, j & 1, kWaitIters));
-      if (!ok) break;
+      const int col = n * kPairN + t - 128;  // (the row scales' plane holds whole tiles of 128)
+      r_col[j & 1][t - 128] = col < static_cast<int>(f4_row_tiles(a.w.rows)) * kF4Rows ? a.w.row_scales[col] : 0.0f;
+      __syncwarp();
+      asm volatile("bar.sync 1, 256;\n" ::: "memory");  // warps 4-11
+      const float *r_n = r_col[j & 1] + 128 * half;
+      if (!gone) gone = !__all_sync(0xffffffffu, tc::mbar_wait_bounded(&sy.tfull, j & 1, kWaitIters));
+      if (gone) continue;
       tc::tc_fence_after();
       uint32_t r[128];
       const uint32_t at = tmem + 128 * half + (static_cast<uint32_t>(32 * q) << 16);
@@ -526,59 +532,60 @@ __global__ void __launch_bounds__(kPairThreads, 1)
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_at(&sy.tempty, 0);
-      const int cols = min(128, a.w.rows - c0);  // columns there are (the row scales' plane holds whole tiles)
-      if (!live || cols <= 0) continue;
-      // Whole sectors of 32 bytes a store (a lane's rows lie far apart: 16 bytes a store, fp32
-      // 8,192 x 12,288 x 4,096 224 us against 156), from the second 16 bytes on where the row
-      // begins in the middle of one.
-      constexpr int kElt = kBf16 ? 2 : 4, kWords = 128 * kElt / 4, kStep = 32 * kElt / 4;
-      uint8_t *p = static_cast<uint8_t *>(a.out) + (row * a.stride + c0) * kElt;
-      const bool odd = reinterpret_cast<uintptr_t>(p) & 16;
-      uint32_t w[kWords];
+      const int cols = min(128, a.w.rows - c0);  // columns there are
+      if (live && cols > 0) {
+        // Whole sectors of 32 bytes a store (a lane's rows lie far apart: 16 bytes a store, fp32
+        // 8,192 x 12,288 x 4,096 224 us against 156), from the second 16 bytes on where the row
+        // begins in the middle of one.
+        constexpr int kElt = kBf16 ? 2 : 4, kWords = 128 * kElt / 4, kStep = 32 * kElt / 4;
+        uint8_t *p = static_cast<uint8_t *>(a.out) + (row * a.stride + c0) * kElt;
+        const bool odd = reinterpret_cast<uintptr_t>(p) & 16;
+        uint32_t w[kWords];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < 4; ++k) {
 #pragma unroll
-        for (int c = 32 * k; c < 32 * k + 32; c += 4) {
-          const float4 s = load_now(reinterpret_cast<const float4 *>(a.w.row_scales + c0 + min(c, (cols - 1) & ~3)));
-          const float v[4] = {__uint_as_float(r[c]) * (r_m * s.x), __uint_as_float(r[c + 1]) * (r_m * s.y),
-                              __uint_as_float(r[c + 2]) * (r_m * s.z), __uint_as_float(r[c + 3]) * (r_m * s.w)};
+          for (int c = 32 * k; c < 32 * k + 32; c += 4) {
+            const float4 s = *reinterpret_cast<const float4 *>(r_n + c);
+            const float v[4] = {__uint_as_float(r[c]) * (r_m * s.x), __uint_as_float(r[c + 1]) * (r_m * s.y),
+                                __uint_as_float(r[c + 2]) * (r_m * s.z), __uint_as_float(r[c + 3]) * (r_m * s.w)};
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            if constexpr (!kBf16) w[c + u] = __float_as_uint(v[u]);
-            else if (u % 2 == 0) {
-              __nv_bfloat162 h = __floats2bfloat162_rn(v[u], v[u + 1]);
-              w[(c + u) / 2] = *reinterpret_cast<uint32_t *>(&h);
+            for (int u = 0; u < 4; ++u) {
+              if constexpr (!kBf16) w[c + u] = __float_as_uint(v[u]);
+              else if (u % 2 == 0) {
+                __nv_bfloat162 h = __floats2bfloat162_rn(v[u], v[u + 1]);
+                w[(c + u) / 2] = *reinterpret_cast<uint32_t *>(&h);
+              }
             }
           }
-        }
-        const int at = kStep * k;  // words
-        if (cols < 128) {          // the last columns: 16 bytes a store, then values
+          const int at = kStep * k;  // words
+          if (cols < 128) {          // the last columns: 16 bytes a store, then values
 #pragma unroll
-          for (int i = at; i < at + kStep; i += 4) {
-            const int left = cols - i * 4 / kElt;
-            if (left >= 16 / kElt) {
-              put4(p + 4 * i, w + i);
-            } else {
+            for (int i = at; i < at + kStep; i += 4) {
+              const int left = cols - i * 4 / kElt;
+              if (left >= 16 / kElt) {
+                put4(p + 4 * i, w + i);
+              } else {
 #pragma unroll
-              for (int u = 0; u < 16 / kElt; ++u)
-                if (u < left) {
-                  if constexpr (kBf16) reinterpret_cast<uint16_t *>(p + 4 * i)[u] = static_cast<uint16_t>(w[i + u / 2] >> (16 * (u & 1)));
-                  else reinterpret_cast<uint32_t *>(p + 4 * i)[u] = w[i + u];
-                }
+                for (int u = 0; u < 16 / kElt; ++u)
+                  if (u < left) {
+                    if constexpr (kBf16) reinterpret_cast<uint16_t *>(p + 4 * i)[u] = static_cast<uint16_t>(w[i + u / 2] >> (16 * (u & 1)));
+                    else reinterpret_cast<uint32_t *>(p + 4 * i)[u] = w[i + u];
+                  }
+              }
             }
+          } else if (odd) {
+            if (k == 0) put4(p, w);
+#pragma unroll
+            for (int i = k ? at - 4 : 4; i + 8 <= at + kStep; i += 8) put8(p + 4 * i, w + i);
+            if (k == 3) put4(p + 4 * (kWords - 4), w + kWords - 4);
+          } else {
+#pragma unroll
+            for (int i = at; i < at + kStep; i += 8) put8(p + 4 * i, w + i);
           }
-        } else if (odd) {
-          if (k == 0) put4(p, w);
-#pragma unroll
-          for (int i = k ? at - 4 : 4; i + 8 <= at + kStep; i += 8) put8(p + 4 * i, w + i);
-          if (k == 3) put4(p + 4 * (kWords - 4), w + kWords - 4);
-        } else {
-#pragma unroll
-          for (int i = at; i < at + kStep; i += 8) put8(p + 4 * i, w + i);
         }
       }
     }
-    if (!ok && lane == 0) gave_up();
+    if (gone && lane == 0) gave_up();
   }
   tc::tc_fence_before();
   __syncthreads();
