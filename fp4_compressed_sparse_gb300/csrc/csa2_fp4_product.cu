@@ -630,17 +630,19 @@ cudaError_t launch_split(const ProductArgs &a, int ranks, cudaStream_t s) {
   return launch_after(kern, grid, kSplitThreads, L::kBytes, ranks, s, a, mw, mx, ms);
 }
 // Which kernel, and how the split one cuts the work.  One GB300, us, NV to bf16, in a graph.
-//   Pairs for more than 64 tokens with more tiles of 128 x 128 than SMs (250 x 12288 x 512 6.7
-//   against 11.4 split, x 4096 10.6 against 20.0), and from half as many on if both of a pair
-//   have tokens and there are more than 2,048 columns (250 x 9600 x 4096 10.2 against 10.8, 501
-//   x 4096 x 8192 14.3 against 15.1; 100 x 16384 x 1024 7.7 against 6.4, 250 x 4096 x 4096, of 64
-//   tiles, 10.4 against 8.8).
+//   Pairs for more than 64 tokens with more tiles of 128 x 128 than SMs (250 x 12288 x 512 6.0
+//   against 11.3 split, x 4096 9.9 against 20.0), and with more than half as many if both CTAs of
+//   a pair have tokens (250 x 9600 x 512 5.6 against 6.2, x 4096 9.5 against 10.7) or from 2,048
+//   columns on (100 x 12288 x 4096 9.4 against 10.2, but x 1024 6.5 against 6.3), and of up to
+//   1,024 columns from 32 tiles on (501 x 1024 x 512 5.2 against 5.8, 8,000 x 50 x 512 4.8 against
+//   7.0); below, 250 x 4096 x 4096, of 64 tiles, 9.5 against 8.8.
 //   Split: the narrowest token tile that holds all tokens (a scale column is of 32 rows
 //   from the record's first on, so several tiles only of 128), then as many ranks as are
 //   resident at once, of 128 tokens one CTA per SM, else two: 64 x 12288 x 4096 8.1 with 3
 //   against 12.1 with 1, 1 x 4096 x 8192 5.0 with 8 against 5.9 with 4, 501 x 704 x 4104 7.2 with
 //   4 against 10.2 with 1.  Clusters do not cover all SMs: a few that wait for a second turn
 //   cost as much as all (1 x 6144 x 4096 8.1 with 6, 4.9 with 4; 501 x 704 x 4104 10.8 with 6).
+//   Of two stages none is dealt out (100 x 4096 x 512 6.2 with 2 ranks, 5.4 with 1).
 // kRanks: ranks, the percentage of the SMs that clusters of so many cover with one CTA per
 // SM (of 152: 152, 138, 144, 138, 120), and with two (of 304: 304, 291, 296, 276, 288).
 constexpr int kRanks[5][3] = {{2, 100, 100}, {3, 90, 95}, {4, 94, 97}, {6, 90, 90}, {8, 78, 95}};
@@ -648,12 +650,14 @@ template <bool kNv, bool kBf16>
 cudaError_t launch_product(const ProductArgs &a, cudaStream_t s) {
   const int m = a.x.rows;
   const int64_t kt = f4_col_tiles(a.x.cols), sms = device_sm_count(), squares = f4_row_tiles(m) * f4_row_tiles(a.w.rows);
-  if (m > 64 && (squares > sms || (m > 128 && kt > 16 && 2 * squares > sms))) return launch_pair<kNv, kBf16>(a, s);
+  const bool both = m > 128;
+  if (m > 64 && (squares > sms || (2 * squares > sms && (both || kt >= 16)) || (both && kt <= 8 && squares >= 32)))
+    return launch_pair<kNv, kBf16>(a, s);
   const int nt = m <= 16 ? 16 : m <= 32 ? 32 : m <= 64 ? 64 : 128;
   const int64_t tiles = f4_row_tiles(a.w.rows) * ((m + nt - 1) / nt), per = nt <= 32 ? 4 : 2, steps = (kt + per - 1) / per;
   int ranks = 1;
   for (const auto &r : kRanks)
-    if (r[0] <= steps && tiles * r[0] <= (nt < 128 ? 2 * sms * r[2] : sms * r[1]) / 100) ranks = r[0];
+    if (r[0] <= steps && steps > 2 && tiles * r[0] <= (nt < 128 ? 2 * sms * r[2] : sms * r[1]) / 100) ranks = r[0];
   switch (nt) {
     case 16: return launch_split<16, kNv, kBf16>(a, ranks, s);
     case 32: return launch_split<32, kNv, kBf16>(a, ranks, s);
