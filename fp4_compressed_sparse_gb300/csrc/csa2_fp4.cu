@@ -22,11 +22,12 @@
 //   the same way (equal to the rounded quotient for every mantissa, as a run over all showed).
 //
 // Bound: HBM for large matrices, a chain of loads, reductions and stores for a few rows.
-// Measured (in a graph): 12,288 x 4,096 bf16 to NV 22.5 us (5.7 TB/s), read back 21.9 us (5.9
-// TB/s; a plain fill of its 100 MB takes 25.7); 8,192 x 4,096 bf16 13.6 us (6.3 TB/s), fp32 26.6
-// us (5.8), to MX 13.5 and 25.5, read 11.2 us (7.7, L2 holds a part); 32 rows 1.7 us.  At 11.6
-// instructions per value the first took 31 us, at 14 compares per fp32 value 42 of 8,192 x
-// 4,096, and with divisions 28: the conversions above are what brought them near the copy rate.
+// Measured (in a graph): 12,288 x 4,096 bf16 to NV 22.5 us (5.7 TB/s), read back 21.6 us (6.0
+// TB/s; a plain fill of its 100 MB takes 25.7), 12,288 x 4,104 23.5; 8,192 x 4,096 bf16 13.6 us (6.3
+// TB/s), fp32 26.6 us (5.8), to MX 13.5 and 25.5, read 11.5 us (7.5, L2 holds a part); 32 rows
+// 1.7 us.  At 11.6 instructions per value the first took 31 us, at 14 compares per fp32 value 42
+// of 8,192 x 4,096, and with divisions 28: the conversions above are what brought them near the
+// copy rate.
 #include <type_traits>
 
 #include "csa2_fp4.cuh"
@@ -490,8 +491,10 @@ __global__ void __launch_bounds__(kQThreads, 3) k_fp4_quant_piped(F4Args a, int 
   }
 }
 
-// A warp: 4 rows of a tile at a time, a lane 16 values (8 B of codes), so that a store of
-// the warp is 4 runs of 256 bytes (bf16); two groups of rows a time.
+// A warp: 4 rows of a tile at a time, two groups of rows a time; a lane 16 values of a row in
+// chunks that eight lanes store as one run of 128 bytes (bf16: 8 values from 8 u and from 64 +
+// 8 u; 32 bytes a lane took 17.8 us for 8,192 x 4,104, whose rows begin in the middle of a
+// sector) or of 256 (fp32: 16 values from 16 u).
 template <bool kNv, bool kBf16>
 __global__ void __launch_bounds__(256) k_fp4_read(csa2_fp4_matrix mx, void *out, int64_t stride, int wide) {
   next_may_start();
@@ -509,62 +512,60 @@ __global__ void __launch_bounds__(256) k_fp4_read(csa2_fp4_matrix mx, void *out,
   }
   for (int k = blockIdx.y * 8 + warp; k < ct; k += 8 * gridDim.y) {
     const uint8_t *rec = tiles + static_cast<int64_t>(k) * f4_tile_bytes(kNv), *sc = rec + kF4CodeBytes;
-    uint2 w[2];
-    uint32_t c[2];
+    uint32_t w[2][2], c[2][2];  // per row and 8 values
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int m = m0 + 4 * i;
-      w[i] = there[i] ? load_now(reinterpret_cast<const uint2 *>(rec + (u >> 1) * 2048 + m * 16 + 8 * (u & 1))) : make_uint2(0, 0);
-      c[i] = there[i] ? (kNv ? sc[512 * (u >> 2) + f4_scale_at(m) + (u & 3)] : sc[f4_scale_at(m) + (u >> 1)]) : 0u;
-    }
-    const int col = kF4Cols * k + 16 * u;
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int z = 0; z < 2; ++z) {
+        const int m = m0 + 4 * i, n = kBf16 ? u + 8 * z : 2 * u + z;  // of the 16 eights of the tile's row
+        w[i][z] = there[i] ? load_now(reinterpret_cast<const uint32_t *>(rec + (n >> 2) * 2048 + m * 16 + 4 * (n & 3))) : 0u;
+        c[i][z] = there[i] ? (kNv ? sc[512 * (n >> 3) + f4_scale_at(m) + ((n >> 1) & 3)] : sc[f4_scale_at(m) + (n >> 2)]) : 0u;
+      }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       if (!there[i]) continue;
-      const float s = (kNv ? e4m3_value(c[i]) : e8m0_value(c[i])) * r[i];
-      uint32_t h[8];
-      e2m1x8_h2(w[i].x, h);
-      e2m1x8_h2(w[i].y, h + 4);
-      float v[16];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h[q]));
-        v[2 * q] = f.x * s;
-        v[2 * q + 1] = f.y * s;
-      }
-      const int64_t at = (row0 + 4 * i) * stride + col;
-      if (col + 16 <= mx.cols) {
-        uint32_t o[16];
-        if constexpr (kBf16) {
+      for (int z = 0; z < 2; ++z) {
+        const int col = kF4Cols * k + 8 * (kBf16 ? u + 8 * z : 2 * u + z);
+        const float s = (kNv ? e4m3_value(c[i][z]) : e8m0_value(c[i][z])) * r[i];
+        uint32_t h[4];
+        e2m1x8_h2(w[i][z], h);
+        float v[8];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
-            o[q] = *reinterpret_cast<uint32_t *>(&b);
+        for (int q = 0; q < 4; ++q) {
+          const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h[q]));
+          v[2 * q] = f.x * s;
+          v[2 * q + 1] = f.y * s;
+        }
+        const int64_t at = (row0 + 4 * i) * stride + col;
+        if (col + 8 <= mx.cols) {
+          if constexpr (kBf16) {
+            uint32_t o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * q], v[2 * q + 1]);
+              o[q] = *reinterpret_cast<uint32_t *>(&b);
+            }
+            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(out) + at) = make_uint4(o[0], o[1], o[2], o[3]);
+          } else {
+            float *dst = static_cast<float *>(out) + at;
+            if (wide) {
+              asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
+                           "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+                           : "memory");
+            } else {
+              reinterpret_cast<float4 *>(dst)[0] = make_float4(v[0], v[1], v[2], v[3]);
+              reinterpret_cast<float4 *>(dst)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            }
           }
         } else {
 #pragma unroll
-          for (int q = 0; q < 16; ++q) o[q] = __float_as_uint(v[q]);
+          for (int q = 0; q < 8; ++q)
+            if (col + q < mx.cols) {
+              if constexpr (kBf16) static_cast<__nv_bfloat16 *>(out)[at + q] = __float2bfloat16_rn(v[q]);
+              else static_cast<float *>(out)[at + q] = v[q];
+            }
         }
-        uint32_t *dst = kBf16 ? reinterpret_cast<uint32_t *>(static_cast<__nv_bfloat16 *>(out) + at)
-                              : reinterpret_cast<uint32_t *>(static_cast<float *>(out) + at);
-#pragma unroll
-        for (int q = 0; q < (kBf16 ? 8 : 16); q += 8) {
-          if (wide) {
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + q), "r"(o[q]), "r"(o[q + 1]),
-                         "r"(o[q + 2]), "r"(o[q + 3]), "r"(o[q + 4]), "r"(o[q + 5]), "r"(o[q + 6]), "r"(o[q + 7])
-                         : "memory");
-          } else {
-            reinterpret_cast<uint4 *>(dst + q)[0] = make_uint4(o[q], o[q + 1], o[q + 2], o[q + 3]);
-            reinterpret_cast<uint4 *>(dst + q)[1] = make_uint4(o[q + 4], o[q + 5], o[q + 6], o[q + 7]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < 16; ++q)
-          if (col + q < mx.cols) {
-            if constexpr (kBf16) static_cast<__nv_bfloat16 *>(out)[at + q] = __float2bfloat16_rn(v[q]);
-            else static_cast<float *>(out)[at + q] = v[q];
-          }
       }
     }
   }
@@ -672,10 +673,12 @@ csa2_status csa2_fp4_read(const csa2_fp4_matrix *m, void *out, int64_t out_strid
   if (m->rows == 0) return CSA2_OK;
   CSA2_REQUIRE_PTR(out);
   const int ct = static_cast<int>(csa2::f4_col_tiles(m->cols)), row_blocks = (m->rows + 7) / 8;
-  int split = (4 * csa2::device_sm_count() + row_blocks - 1) / row_blocks;  // few rows: their tiles over more blocks
-  split = split < 2 ? 2 : split;  // (12,288 x 4,096 21.9 us against 23.6 in one, 8,192 x 4,096 11.2 against 12.2)
+  // a row group's tiles over several blocks: eight per SM in all (2,048 x 4,096 fp32 5.9 us against
+  // 8.9 with four), two at least (12,288 x 4,096 21.6 against 23.6 with one)
+  int split = 8 * csa2::device_sm_count() / row_blocks;
+  split = split < 2 ? 2 : split;
   split = split > (ct + 7) / 8 ? (ct + 7) / 8 : split;
-  const int wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && out_stride % (out_dtype == CSA2_OUT_BF16 ? 16 : 8) == 0;
+  const int wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
   const dim3 grid(row_blocks, split);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const bool bf = out_dtype == CSA2_OUT_BF16;

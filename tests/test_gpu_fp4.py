@@ -298,3 +298,17 @@ def test_product_rows_in_the_middle_of_a_sector(M, N, dtype):
         csa2.fp4_product(x, w, out[:, off:off + N])
         assert torch.equal(out[:, off:off + N], want)
         assert (out[:, :off] == 5).all() and (out[:, off + N:] == 5).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,cols", [(3, 100), (37, 1000), (2500, 1288)])
+def test_read_rows_in_the_middle_of_a_sector(rows, cols, dtype):
+    """Output rows that begin 16 bytes behind a multiple of 32, all or every second one."""
+    m = _packed(_rows(rows, cols + cols % 8, torch.float32, 9)[:, :cols], csa2.FP4_MX)
+    wide = -(-cols // 32) * 32
+    want = fu.values(m)
+    for off, stride in ((0, wide), (0, wide + 8), (16 // dtype.itemsize, wide + 32), (16 // dtype.itemsize, wide + 40)):
+        out = torch.full((rows, stride), 5.0, dtype=dtype, device=DEV)
+        csa2.fp4_read(m, out[:, off:off + cols])
+        assert torch.equal(out[:, off:off + cols].double(), want)
+        assert (out[:, :off] == 5).all() and (out[:, off + cols:] == 5).all()
