@@ -251,3 +251,25 @@ def test_query_rows_behind_32_bits():
     csa2.query_latent(q, w, pos, rope, out)
     csa2.query_latent(q[-300:], w, pos[-300:].clone(), rope, few)
     assert torch.equal(out[-300:], few) and out[::1000].any(-1).all()
+
+
+@pytest.mark.parametrize("T,H", [(1, 4), (20, 4), (130, 64), (1000, 16)])
+def test_query_rows_left_alone(T, H):
+    """Every row idle: nothing is written and nothing reported; a row behind the RoPE table among others:
+    reported, left alone, the others as without it."""
+    rope, err = csa2.rope_table(THETA, 2000), _err()
+    g = torch.Generator(device=DEV).manual_seed(T)
+    w, _ = _weights(H, 48, g)
+    q = torch.randn(T, H * 112, generator=g, device=DEV).to(torch.bfloat16)
+    out = torch.full((T, H, 576), 9.0, dtype=torch.bfloat16, device=DEV)
+    csa2.query_latent(q, w, torch.full((T,), -5, device=DEV), rope, out, err=err)
+    assert (out == 9).all() and int(err) == 0
+    want = torch.empty_like(out)
+    pos = torch.arange(T, device=DEV)
+    csa2.query_latent(q, w, pos, rope, want, err=err)
+    assert int(err) == 0
+    pos[T // 2] = 2000
+    csa2.query_latent(q, w, pos, rope, out, err=err)
+    assert int(err) == csa2.DEVERR_ROPE and (out[T // 2] == 9).all()
+    out[T // 2] = want[T // 2]
+    assert torch.equal(out, want)
