@@ -19,7 +19,7 @@
 //
 // Measured (in a graph, caches as the calls before leave them): 4,001 tokens of 64 heads of
 // 128: queries 72 us (403 MB, 5.6 TB/s, 82 % of the measured copy rate), values bf16 55 us
-// (336 MB, 6.1 TB/s, 90 %), fp32 97 us (599 MB, 6.2 TB/s); 128 tokens: 5.7, 4.5 and 7.2 us.
+// (336 MB, 6.1 TB/s, 90 %), fp32 97 us (599 MB, 6.2 TB/s); 128 tokens: 5.7, 4.4 and 7.2 us.
 // Tensor pipe 17 to 22 %.  Short of the copy rate: the reload of W when a CTA's run passes to
 // another head (nothing is computed meanwhile), rows of 1,152 B at 74 KB distance out.
 #include "csa2_latent.cuh"
@@ -53,7 +53,7 @@ struct Shape {
 constexpr int kPartBufs = 4, kPartCol = 128;
 struct Sync {
   uint64_t full[6], empty[6];
-  uint64_t wfull, wdone;         // W has landed; the last MMAs that read it are done
+  uint64_t wfull[4], wdone;      // W, or a stage's columns of it, has landed; the last MMAs that read it are done
   uint64_t pfull[kPartBufs], pempty[kPartBufs];  // fp32: the bf16 parts
   uint64_t tfull[2], tempty[2];
   uint32_t tmem;
@@ -136,6 +136,10 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
              const __grid_constant__ CUtensorMap mo) {
   using S = Shape<kM>;
   constexpr bool kQ = kM == kQuery, kF = kM == kValueF32;
+  // bf16 values: W comes in four groups of 128 columns, each just before the stage that is multiplied
+  // by it (1,000 tokens of 64 heads 13.4 us against 14.7 with all of W first; for the others that
+  // gained nothing)
+  constexpr int kWGroups = kM == kValue ? 4 : 1;
   extern __shared__ uint8_t raw[];
   __shared__ __align__(128) Sync sy;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -160,7 +164,7 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
       tc::mbar_init(&sy.pfull[i], 4);
       tc::mbar_init(&sy.pempty[i], 1);
     }
-    tc::mbar_init(&sy.wfull, 1);
+    for (int i = 0; i < kWGroups; ++i) tc::mbar_init(&sy.wfull[i], 1);
     tc::mbar_init(&sy.wdone, 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sy.tfull[i], 1);
@@ -191,19 +195,24 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
     bool ok = true;
     for (int u = v0 >> shift; u << shift < v1 && ok; ++u) {
       const int hp = u / a.tiles, tile = u - hp * a.tiles, h = hp / a.parts, part = hp - h * a.parts;
+      auto w_group = [&](int g, int n_box) {
+        if (el) {
+          tc::mbar_expect_tx(&sy.wfull[g], n_box * w_box);
+          for (int i = g * n_box; i < (g + 1) * n_box; ++i)
+            load3(s_w + i * w_box, &mw, (kQ ? part * a.np : 0) + 64 * i, kQ ? 0 : part * a.np, h, &sy.wfull[g]);
+        }
+        __syncwarp();
+      };
       if (hp != held) {
         if (wn > 0) ok = wait_all(&sy.wdone, (wn - 1) & 1);
         if (!ok) break;
         ++wn;
-        if (el) {
-          tc::mbar_expect_tx(&sy.wfull, w_boxes * w_box);
-          for (int i = 0; i < w_boxes; ++i)
-            load3(s_w + i * w_box, &mw, (kQ ? part * a.np : 0) + 64 * i, kQ ? 0 : part * a.np, h, &sy.wfull);
-        }
-        __syncwarp();
-        held = hp;
+        if (kWGroups == 1) w_group(0, w_boxes);
       }
+      const bool fresh = hp != held;
+      held = hp;
       for (int c = 0; c < chunks; ++c, ++n) {
+        if (kWGroups > 1 && fresh) w_group(c, 2);
         if (n >= S::kStages) ok = wait_all(&sy.empty[st], ph);
         if (!ok) break;
         if (el) {
@@ -232,15 +241,18 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
     for (int v = v0; v < v1 && ok; ++v, ++j) {
       const int hp = (v >> shift) / a.tiles, b = v & shift;
       const bool first = b == 0 || v == v0, last = b == jobs - 1 || v == v1 - 1;  // of the unit's jobs here
-      if (hp != held) {
-        ok = wait_all(&sy.wfull, wn++ & 1);
+      const bool fresh = hp != held;
+      if (fresh) {
+        if (kWGroups == 1) ok = wait_all(&sy.wfull[0], wn & 1);
+        ++wn;
         held = hp;
       }
       if (ok) {
         const uint32_t acc = j & 1, d = tmem + 256 * acc;
         if (j >= 2) ok = wait_all(&sy.tempty[acc], ((j >> 1) - 1) & 1);
         for (int c = 0; c < chunks && ok; ++c) {
-          if (first) ok = kF ? wait_all(&sy.pfull[st], ph) : wait_all(&sy.full[st], ph);
+          if (kWGroups > 1 && fresh) ok = wait_all(&sy.wfull[c], (wn - 1) & 1);
+          if (first && ok) ok = kF ? wait_all(&sy.pfull[st], ph) : wait_all(&sy.full[st], ph);
           if (!ok) break;
           tc::tc_fence_after();
           if (el) {
@@ -420,7 +432,7 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
   if (t == 0 && sy.dead) {  // copies still in flight
     for (uint32_t i = sy.loaded > S::kStages ? sy.loaded - S::kStages : 0; i < sy.loaded; ++i)
       tc::mbar_wait_bounded(&sy.full[i % S::kStages], (i / S::kStages) & 1, kWaitIters);
-    if (sy.w_loaded > 0) tc::mbar_wait_bounded(&sy.wfull, (sy.w_loaded - 1) & 1, kWaitIters);
+    for (int i = 0; i < kWGroups && sy.w_loaded > 0; ++i) tc::mbar_wait_bounded(&sy.wfull[i], (sy.w_loaded - 1) & 1, kWaitIters);
   }
   __syncthreads();
   if (warp == 1) {
