@@ -13,9 +13,8 @@
 //
 // Two forms, by the number of tokens (both sides' times stand at few_queries): a block per
 // head and column part with everything in flight at once (csa2_latent_few.cu), and the
-// persistent kernel of this file.  fp32 latents are split into bf16 parts hi + lo, each
-// multiplied: what is lost is 2^-16 of a value, against 2^-8 that the bf16 result's
-// rounding takes.
+// persistent kernel of this file.  fp32 latents are cut into three bf16 parts that add up to
+// them, each multiplied: the sums are of the values as they were given.
 //
 // Measured (in a graph, caches as the calls before leave them): 4,001 tokens of 64 heads of
 // 128: queries 72 us (403 MB, 5.6 TB/s, 82 % of the measured copy rate), values bf16 55 us
@@ -47,10 +46,10 @@ struct Shape {
   static constexpr int kMoreWarps = kM == kValue ? 0 : 8;  // that rotate, or split
   static constexpr int kThreads = 32 * (12 + kMoreWarps);
 };
-// fp32 latents: their bf16 parts lie in tensor memory, as the MMA's rows, hi in 16 columns of
-// a buffer and lo in the next 16.  Four buffers fill the columns 128 to 255 that the first
-// accumulator leaves.
-constexpr int kPartBufs = 4, kPartCol = 128;
+// fp32 latents: their bf16 parts lie in tensor memory, as the MMA's rows, 16 columns of a
+// buffer each.  Two buffers lie behind each accumulator's 128 columns, 64 columns apart.
+constexpr int kPartBufs = 4;
+__device__ __forceinline__ uint32_t part_col(uint32_t buf) { return 128 + 64 * buf + 128 * (buf >> 1); }
 struct Sync {
   uint64_t full[6], empty[6];
   uint64_t wfull[4], wdone;      // W, or a stage's columns of it, has landed; the last MMAs that read it are done
@@ -129,7 +128,7 @@ __device__ __forceinline__ void sts4(uint32_t at, const uint32_t *v) {
 //   warps 4-11   read the sums out of tensor memory and write them: two groups of four,
 //                one per accumulator
 //   warps 12-    query: rotate the RoPE dims, from global memory to global memory;
-//                fp32 latents: split a stage into bf16 parts hi and lo in tensor memory
+//                fp32 latents: cut a stage into three bf16 parts in tensor memory
 template <Mode kM>
 __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
     k_latent(LatentArgs a, const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
@@ -263,12 +262,11 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
                 mma_bf16(d, dx + (((s >> 2) * kBox + 32 * (s & 3)) >> 4), dw + (2048 * s >> 4), id, s > 0 ? 1u : 0u);
             } else if constexpr (kF) {
               const uint64_t dw = desc_sw128(s_w + (c >> 1) * a.np * 128, 16, 1024) + (64 * (c & 1) >> 4);
-              const uint32_t tx = tmem + kPartCol + 32 * st;
+              const uint32_t tx = tmem + part_col(st);
 #pragma unroll
-              for (int s = 0; s < 2; ++s) {
-                mma_bf16_rows(d, tx + 8 * s, dw + (32 * s >> 4), id, c + s > 0 ? 1u : 0u);
-                mma_bf16_rows(d, tx + 16 + 8 * s, dw + (32 * s >> 4), id, 1u);
-              }
+              for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int z = 0; z < 3; ++z) mma_bf16_rows(d, tx + 16 * z + 8 * s, dw + (32 * s >> 4), id, c + s + z > 0 ? 1u : 0u);
             } else {
               const uint64_t dx = desc_sw128(s_x + st * S::kStage, 16, 1024);
 #pragma unroll
@@ -407,16 +405,19 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
       ok = wait_all(&sy.full[st], (n / S::kStages) & 1) && (use == 0 || wait_all(&sy.pempty[pb], (use - 1) & 1));
       if (!ok) break;
       tc::tc_fence_after();
-      const uint32_t src = s_x + st * S::kStage + (quarter + lane) * 128, dst = tmem + (quarter << 16) + kPartCol + 32 * pb;
-      uint32_t hi[16], lo[16];
+      const uint32_t src = s_x + st * S::kStage + (quarter + lane) * 128, dst = tmem + (quarter << 16) + part_col(pb);
+      uint32_t part[3][16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float4 v = lds4(src + ((i ^ r8) << 4));
-        split2(v.x, v.y, hi[2 * i], lo[2 * i]);
-        split2(v.z, v.w, hi[2 * i + 1], lo[2 * i + 1]);
+        uint32_t p[2][3];
+        split3(v.x, v.y, p[0]);
+        split3(v.z, v.w, p[1]);
+#pragma unroll
+        for (int z = 0; z < 3; ++z) part[z][2 * i] = p[0][z], part[z][2 * i + 1] = p[1][z];
       }
-      tmem_st_x16(dst, hi);
-      tmem_st_x16(dst + 16, lo);
+#pragma unroll
+      for (int z = 0; z < 3; ++z) tmem_st_x16(dst + 16 * z, part[z]);
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&sy.empty[st]);
       asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");

@@ -40,11 +40,19 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t *>(&v);
 }
-// x = hi + lo in bf16, to 2^-16 of x; infinities and NaN in hi alone
-__device__ __forceinline__ void split2(float a, float b, uint32_t &hi, uint32_t &lo) {
-  hi = pack_bf16(a, b);
-  const float ha = __uint_as_float(hi << 16), hb = __uint_as_float(hi & 0xFFFF0000u);
-  lo = pack_bf16(isfinite(ha) ? a - ha : 0.0f, isfinite(hb) ? b - hb : 0.0f);
+// Two fp32 values as three bf16 parts each (a's in the low half): 8 bits are cut off at a time,
+// so that nothing is rounded, a finite value never becomes infinite, and the parts add up to the
+// value but for its bits below bf16's least, 2^-133.  An infinity lies in the first part alone; a
+// NaN is at least one part's.
+__device__ __forceinline__ void split3(float a, float b, uint32_t *part) {
+  part[0] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  const float ha = __uint_as_float(part[0] << 16), hb = __uint_as_float(part[0] & 0xFFFF0000u);
+  a = a == ha ? 0.0f : a - ha;  // (an infinity less itself would be a NaN)
+  b = b == hb ? 0.0f : b - hb;
+  part[1] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+  a -= __uint_as_float(part[1] << 16);
+  b -= __uint_as_float(part[1] & 0xFFFF0000u);
+  part[2] = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
 // Whether a query row is written; one behind the RoPE table raises the bit.
 __device__ __forceinline__ bool row_position(const LatentArgs &a, int64_t tok, bool report, int64_t &p) {

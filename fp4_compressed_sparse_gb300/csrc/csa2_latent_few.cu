@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(kFewThreads) k_value_few(LatentArgs a) {
   const int h = blockIdx.x, j0 = blockIdx.y * 32, tok0 = blockIdx.z * 16 * kTiles;
   const int c0 = 64 * warp + 8 * t;
   const uint16_t *w = a.w + h * a.w_stride + c0;
-  uint4 r[2][4], x[2][kTiles][2], xl[2][kTiles][2];
+  constexpr int kWords = kF32 ? 2 : 1;  // of 16 bytes, for 8 values
+  uint4 r[2][4], x[2][kTiles][2][kWords];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
 #pragma unroll
@@ -149,40 +150,44 @@ __global__ void __launch_bounds__(kFewThreads) k_value_few(LatentArgs a) {
       for (int half = 0; half < 2; ++half) {
         const int64_t tok = tok0 + 16 * m + g + 8 * half;
         const int64_t at = tok * a.x_stride + static_cast<int64_t>(h) * kLat + c0 + 32 * i;
-        x[i][m][half] = xl[i][m][half] = make_uint4(0, 0, 0, 0);
-        if (tok < a.total) {
-          if constexpr (kF32) {
-            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.x) + at);
-            const float4 u = load_now(p), s = load_now(p + 1);
-            uint32_t hi[4], lo[4];
-            split2(u.x, u.y, hi[0], lo[0]);
-            split2(u.z, u.w, hi[1], lo[1]);
-            split2(s.x, s.y, hi[2], lo[2]);
-            split2(s.z, s.w, hi[3], lo[3]);
-            x[i][m][half] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            xl[i][m][half] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-          } else {
-            x[i][m][half] = load_now(reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + at));
-          }
-        }
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.x) + at * (kF32 ? 4 : 2));
+#pragma unroll
+        for (int z = 0; z < kWords; ++z) x[i][m][half][z] = tok < a.total ? load_now(p + z) : make_uint4(0, 0, 0, 0);
       }
   }
+  // values 4 s .. 4 s + 3 of two tokens: the MMA's rows, of fp32 latents in three parts (cut
+  // before the first product: 32 tokens of 64 heads 4.6 us, cut between products 4.9)
+  constexpr int kParts = kF32 ? 3 : 1;
+  uint32_t f[2][2][kTiles][kParts][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int m = 0; m < kTiles; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if constexpr (kF32) {
+            const uint4 &u = x[i][m][j & 1][s];
+            uint32_t p[3];
+            split3(__uint_as_float(j < 2 ? u.x : u.z), __uint_as_float(j < 2 ? u.y : u.w), p);
+#pragma unroll
+            for (int z = 0; z < 3; ++z) f[i][s][m][z][j] = p[z];
+          } else {
+            f[i][s][m][0][j] = word(x[i][m][j & 1][0], 2 * s + (j >> 1));
+          }
+        }
   float4 acc[kTiles][4] = {};
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int m = 0; m < kTiles; ++m) {
-        const uint32_t f[4] = {word(x[i][m][0], 2 * s), word(x[i][m][1], 2 * s), word(x[i][m][0], 2 * s + 1), word(x[i][m][1], 2 * s + 1)};
+      for (int m = 0; m < kTiles; ++m)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) mma16816(acc[m][v], f, word(r[i][v], 2 * s), word(r[i][v], 2 * s + 1));
-        if constexpr (kF32) {
-          const uint32_t l[4] = {word(xl[i][m][0], 2 * s), word(xl[i][m][1], 2 * s), word(xl[i][m][0], 2 * s + 1), word(xl[i][m][1], 2 * s + 1)};
+        for (int z = 0; z < kParts; ++z)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) mma16816(acc[m][v], l, word(r[i][v], 2 * s), word(r[i][v], 2 * s + 1));
-        }
-      }
+          for (int v = 0; v < 4; ++v) mma16816(acc[m][v], f[i][s][m][z], word(r[i][v], 2 * s), word(r[i][v], 2 * s + 1));
 #pragma unroll
   for (int m = 0; m < kTiles; ++m)
 #pragma unroll

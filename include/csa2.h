@@ -627,8 +627,8 @@ csa2_status csa2_query_latent(const uint16_t *q, int64_t q_stride, int32_t total
  *      heads 512 values each (o_stride >= n_heads x 512, a multiple of 8);
  *   w_uv: bf16, head h's dim rows of 512 at w_uv + h * w_stride, as w_uk;
  *   out: bf16, row t at out + t * out_stride (>= n_heads x dim, a multiple of 8).
- * Sums in fp32, rounded once; fp32 rows enter as two bf16 parts, to 2^-16 of a value
- * (magnitudes from bf16's largest on as infinities).
+ * Sums in fp32, rounded once; fp32 rows enter as three bf16 parts that add up to them
+ * (but for bits below 2^-126; an infinite weight may give NaN, 0 being among the parts).
  * n_heads 1..128, dim a multiple of 16, 16..128.  Device errors: TIMEOUT.
  * In both calls a row's last bits may change with the number of rows; equal calls
  * give equal bits; out must not overlap what is read.

@@ -273,3 +273,44 @@ def test_query_rows_left_alone(T, H):
     assert int(err) == csa2.DEVERR_ROPE and (out[T // 2] == 9).all()
     out[T // 2] = want[T // 2]
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("T", [5, 20, 1100])
+@pytest.mark.parametrize("scale", [0, 100, -100])
+def test_value_keeps_all_bits_of_fp32(T, scale):
+    """A value less its own first 16 bits, under a weight that is a power of two: what is left has 8 bits,
+    every sum on the way fits fp32, and so does the result bf16: equal."""
+    H, D = 4, 64
+    g = torch.Generator(device=DEV).manual_seed(9)
+    p = (1.0 + torch.randint(0, 1 << 23, (T, H), generator=g, device=DEV) * 2.0 ** -23) * 2.0 ** scale
+    p *= torch.randint(0, 2, (T, H), generator=g, device=DEV) * 2.0 - 1
+    first = (p.view(torch.int32) & -256).view(torch.float32)
+    o = torch.zeros(T, H, 512, device=DEV)
+    at = torch.randint(0, 256, (2, T, H, 1), generator=g, device=DEV)
+    o.scatter_(2, at[0], p[..., None])
+    o.scatter_(2, 256 + at[1], -first[..., None])
+    w = torch.exp2(torch.randint(-3, 4, (H, D, 1), generator=g, device=DEV).float()).expand(H, D, 512).to(torch.bfloat16).contiguous()
+    out = torch.empty(T, H * D, dtype=torch.bfloat16, device=DEV)
+    csa2.value_project(o, w, out)
+    want = (p.double() - first.double())[..., None] * w[None, :, :, 0].double()
+    assert (want != 0).any() and torch.equal(out.view(T, H, D).double(), want)
+
+
+@pytest.mark.parametrize("T", [5, 20, 1100])
+def test_value_of_the_largest_fp32(T):
+    """Finite latents above bf16's largest number stay finite; a NaN whose payload bf16 cuts off stays a NaN."""
+    H, D = 4, 64
+    o = torch.zeros(T, H, 512, device=DEV)
+    top = torch.finfo(torch.float32).max
+    o[..., 33], o[1::2, :, 33] = top, -top
+    o[2, 1, 33] = torch.nextafter(torch.tensor(top), torch.tensor(0.0)).item()
+    w = torch.full((H, D, 512), 0.125, dtype=torch.bfloat16, device=DEV)
+    out = torch.empty(T, H * D, dtype=torch.bfloat16, device=DEV)
+    csa2.value_project(o, w, out)
+    assert torch.equal(out.view(T, H, D), (o[..., 33:34] * 0.125).to(torch.bfloat16).expand(T, H, D)) and torch.isfinite(out).all()
+    nan = torch.tensor([0x7F800001, -8388607], dtype=torch.int32, device=DEV).view(torch.float32)
+    o[3, 0, 500], o[T - 1, 2, 7] = nan[0], nan[1]
+    csa2.value_project(o, w, out)
+    is_nan = torch.zeros(T, H, dtype=torch.bool, device=DEV)
+    is_nan[3, 0] = is_nan[T - 1, 2] = True
+    assert torch.equal(torch.isnan(out.view(T, H, D)), is_nan[..., None].expand(T, H, D))
