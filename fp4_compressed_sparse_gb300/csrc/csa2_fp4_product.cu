@@ -203,8 +203,10 @@ __global__ void __launch_bounds__(kSplitThreads)
     else if (lane == 0) raise_err(a.err, CSA2_DEVERR_TIMEOUT);
   }
   tc::tc_fence_after();
-  __syncthreads();  // (the stages are free: every copy has landed, every MMA is done)
-  if (!have) {      // ... or a wait gave up: no copy may land later
+  // The block's vote: a wait may give up in one warp and just not in another, and all of them go the
+  // same way here.  (After it the stages are free: every copy has landed, every MMA is done ...)
+  have = __syncthreads_and(have);
+  if (!have) {  // ... or a wait gave up: no copy may land later
     if (t == 0)
       for (int i = loaded > L::kStages ? loaded - L::kStages : 0; i < loaded; ++i)
         tc::mbar_wait_bounded(&full[i % L::kStages], (i / L::kStages) & 1, kWaitIters);
