@@ -4,13 +4,12 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
-#include <map>
 #include <mutex>
 #include <string>
-#include <utility>
 
 #include "csa2_encode.cuh"
 #include "csa2_internal.cuh"
+#include "csa2_smem_limit.cuh"
 
 namespace {
 
@@ -50,7 +49,7 @@ namespace {
 constexpr int kMaxDevices = 64;
 std::mutex g_dev_mu;
 int g_sm_count[kMaxDevices] = {};
-std::map<std::pair<int, const void *>, int> g_smem_limit;  // (device, kernel) -> bytes set
+SmemLimits g_smem_limits;
 }  // namespace
 
 int device_sm_count() {
@@ -76,18 +75,7 @@ cudaError_t ensure_smem_limit(const void *fn, int bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const auto key = std::make_pair(dev, fn);
-  {
-    std::lock_guard<std::mutex> lock(g_dev_mu);
-    auto it = g_smem_limit.find(key);
-    if (it != g_smem_limit.end() && it->second >= bytes) return cudaSuccess;
-  }
-  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lock(g_dev_mu);
-  int &have = g_smem_limit[key];
-  if (bytes > have) have = bytes;
-  return cudaSuccess;
+  return g_smem_limits.raise(dev, fn, bytes, [&] { return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
 }
 
 }  // namespace csa2

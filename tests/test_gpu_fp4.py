@@ -312,3 +312,30 @@ def test_read_rows_in_the_middle_of_a_sector(rows, cols, dtype):
         csa2.fp4_read(m, out[:, off:off + cols])
         assert torch.equal(out[:, off:off + cols].double(), want)
         assert (out[:, :off] == 5).all() and (out[:, off + cols:] == 5).all()
+
+
+def test_quant_from_two_host_threads():
+    """Narrow and wide matrices of one kernel, first used by two host threads at once, then the wide ones again."""
+    import threading
+    for dtype, narrow, wide in ((torch.bfloat16, 1100, 13990), (torch.float32, 600, 6400), (torch.float32, 14100, 28000)):
+        for fmt in FMTS:
+            xs = [torch.randn(1300, -(-c // 8) * 8, device=DEV).to(dtype)[:, :c] for c in (narrow, wide)]
+            ms = [csa2.Fp4Matrix(*x.shape, fmt) for x in xs]
+            torch.cuda.synchronize()
+            gate, failed = threading.Barrier(2), []
+
+            def run(x, m):
+                try:
+                    s = torch.cuda.Stream()
+                    gate.wait()
+                    csa2.fp4_quant(m, x, stream=s)
+                    s.synchronize()
+                except Exception as e:
+                    failed.append(e)
+            threads = [threading.Thread(target=run, args=a) for a in zip(xs, ms)]
+            [t.start() for t in threads]
+            [t.join() for t in threads]
+            assert not failed
+            csa2.fp4_quant(ms[1], xs[1])
+            for x, m in zip(xs, ms):
+                assert torch.equal(fu.values(m), fu.quantised(x, fmt))
