@@ -24,6 +24,7 @@ constexpr int kPageThreads = 1024;
 // one cluster: 32 sequences that take or give 499 pages each 8.5 us, with one CTA 42; a
 // decode step 3.7, with one CTA 3.8
 constexpr int kPageCtas = 8;
+constexpr int kMaskWords = 65536 / 32;  // a bit per sequence
 
 struct PagesArgs {
   csa2_cache c;
@@ -69,9 +70,9 @@ __device__ __forceinline__ SeqPages seq_pages(const PagesArgs &a, int b, SeqIn i
   return s;
 }
 
-// Inclusive sums of x and y over the block; the totals in tx, ty.
+// Inclusive sums of x and y over the block, and the totals.
 struct Scan2 {
-  int64_t x, y, tx, ty;
+  int64_t x, y, x_all, y_all;
 };
 __device__ __forceinline__ Scan2 block_scan2(int64_t x, int64_t y, int64_t (*sh)[2]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -95,14 +96,22 @@ __device__ __forceinline__ Scan2 block_scan2(int64_t x, int64_t y, int64_t (*sh)
       r.x += sh[w][0];
       r.y += sh[w][1];
     }
-    r.tx += sh[w][0];
-    r.ty += sh[w][1];
+    r.x_all += sh[w][0];
+    r.y_all += sh[w][1];
   }
   return r;
 }
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+
+// The 32 bits at the same place of CTA `rank`'s shared memory.
+__device__ __forceinline__ uint32_t peer_word(const void *p, int rank) {
+  uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(p)), v;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"(at), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];\n" : "=r"(v) : "r"(at) : "memory");
+  return v;
 }
 
 // First t in [0, n) with list[t] > v (list non-decreasing, list[n - 1] > v).
@@ -117,15 +126,20 @@ __device__ __forceinline__ int first_above(const int64_t *list, int n, int64_t v
 }
 
 // One cluster.  Every CTA computes all prefix sums (a chunk of blockDim sequences at a
-// time) and moves every gridDim-th page, so nothing but the barriers passes between
-// them.  free and table: written between the barriers; held, granted and n_free, which
-// every CTA reads, behind the last.
+// time) and moves every gridDim-th page, so what passes between them is the barriers and,
+// where pages come back, the sequences whose ids are no pages: those are looked for before
+// anything is written, since whoever grew would get such an id from the stack.  free and
+// table: written between the barriers; held, granted and n_free, which every CTA reads,
+// behind the last.
 __global__ void __launch_bounds__(kPageThreads) k_pages_resize(PagesArgs a) {
   __shared__ int64_t sh[32][2];
   __shared__ int64_t l_back[kPageThreads], l_grow[kPageThreads];
   __shared__ int32_t l_held[kPageThreads], l_need[kPageThreads];
+  __shared__ uint32_t found[kMaskWords], broken[kMaskWords];  // a bit per sequence: this CTA's finds, all CTAs'
+  __shared__ uint32_t any_found;
   const int t = threadIdx.x, nthr = blockDim.x, rank = blockIdx.x, ctas = gridDim.x;
   const int batch = a.c.batch, mp = a.c.max_pages;
+  for (int w = t; w < (batch + 31) / 32; w += nthr) found[w] = broken[w] = 0;
   next_may_start();
   wait_for_previous();
   const int64_t n0 = *a.pool.n_free;
@@ -137,61 +151,90 @@ __global__ void __launch_bounds__(kPageThreads) k_pages_resize(PagesArgs a) {
     for (int b = t; b < batch; b += nthr) falls |= a.cu[b + 1] < a.cu[b];
   falls = __syncthreads_or(falls);
 
-  // pages that go back, altogether (one chunk: the scan below has them)
   SeqPages s{0, 0, false};
-  int64_t R = 0;
-  if (!one) {
-    int64_t mine = 0;
-    for (int b = t; b < batch; b += nthr) {
-      s = seq_pages(a, b, seq_in(a, b), falls, rank == 0);
-      mine += max(s.held - s.need, 0);
-    }
-    R = block_scan2(mine, 0, sh).tx;
-  } else if (t < batch) {
-    s = seq_pages(a, t, in, falls, rank == 0);
-  }
   Scan2 c{};
-  if (one) {
-    c = block_scan2(max(s.held - s.need, 0), max(s.need - s.held, 0), sh);
-    R = c.tx;
+  int64_t R = 0;
+  auto seq = [&](int b, SeqIn in, bool report) {
+    SeqPages x = seq_pages(a, b, in, falls, report);
+    if (broken[b >> 5] >> (b & 31) & 1) x.need = x.held, x.ok = false;
+    return x;
+  };
+  // pages that go back, altogether (one chunk: s and c stay for what follows)
+  auto count = [&](bool report) {
+    if (one) {
+      if (t < batch) s = seq(t, in, report);
+      c = block_scan2(max(s.held - s.need, 0), max(s.need - s.held, 0), sh);
+      R = c.x_all;
+    } else {
+      int64_t mine = 0;
+      for (int b = t; b < batch; b += nthr) {
+        s = seq(b, seq_in(a, b), report);
+        mine += max(s.held - s.need, 0);
+      }
+      R = block_scan2(mine, 0, sh).x_all;
+    }
+  };
+  // each of them, dealt to the cluster's threads: its place in sequence and page order, its sequence, its entry
+  auto each_back = [&](auto use) {
+    int64_t base = 0;
+    for (int b0 = 0; b0 < batch; b0 += nthr) {
+      if (!one) {
+        s = b0 + t < batch ? seq(b0 + t, seq_in(a, b0 + t), false) : SeqPages{0, 0, false};
+        c = block_scan2(max(s.held - s.need, 0), 0, sh);
+      }
+      l_back[t] = c.x;
+      l_held[t] = s.held;
+      l_need[t] = s.need;
+      __syncthreads();
+      for (int64_t j = static_cast<int64_t>(rank) * nthr + t; j < c.x_all; j += static_cast<int64_t>(ctas) * nthr) {
+        const int q = first_above(l_back, nthr, j);
+        const int p = l_need[q] + static_cast<int>(j - (l_back[q] - (l_held[q] - l_need[q])));
+        use(base + j, b0 + q, a.table + static_cast<int64_t>(b0 + q) * mp + p);
+      }
+      base += c.x_all;
+      __syncthreads();
+    }
+  };
+  count(rank == 0);
+  if (R > 0) {  // (the same in every thread of the cluster)
+    int mine = 0;
+    each_back([&](int64_t, int b, const int32_t *e) {
+      if (*e >= 0 && *e < a.c.n_pages) return;
+      atomicOr(&found[b >> 5], 1u << (b & 31));
+      mine = 1;
+    });
+    if (mine) raise_err(a.err, CSA2_DEVERR_INDEX);
+    mine = __syncthreads_or(mine);
+    if (t == 0) any_found = mine;
+    cluster_sync();
+    if (__syncthreads_or(t < ctas ? peer_word(&any_found, t) : 0u)) {
+      for (int w = t; w < (batch + 31) / 32; w += nthr) {
+        uint32_t m = 0;
+        for (int r = 0; r < ctas; ++r) m |= peer_word(&found[w], r);
+        broken[w] = m;
+      }
+      __syncthreads();
+      count(false);
+    }
   }
   const int64_t n1 = n0 + R;
   const bool sound = n0 >= 0 && n1 <= a.c.n_pages;  // (the same in every thread of the cluster)
   if (!sound && rank == 0 && t == 0) raise_err(a.err, CSA2_DEVERR_INDEX);
 
   // ---- pages back to the stack
-  int64_t base = 0;
-  for (int b0 = 0; b0 < batch && sound && R > 0; b0 += nthr) {
-    const int b = b0 + t;
-    if (!one) {
-      s = b < batch ? seq_pages(a, b, seq_in(a, b), falls, false) : SeqPages{0, 0, false};
-      c = block_scan2(max(s.held - s.need, 0), 0, sh);
-    }
-    l_back[t] = c.x;
-    l_held[t] = s.held;
-    l_need[t] = s.need;
-    __syncthreads();
-    for (int64_t j = static_cast<int64_t>(rank) * nthr + t; j < c.tx; j += static_cast<int64_t>(ctas) * nthr) {
-      const int q = first_above(l_back, nthr, j);
-      const int p = l_need[q] + static_cast<int>(j - (l_back[q] - (l_held[q] - l_need[q])));
-      int32_t *e = a.table + static_cast<int64_t>(b0 + q) * mp + p;
-      const int32_t page = *e;
-      if (page < 0 || page >= a.c.n_pages) raise_err(a.err, CSA2_DEVERR_INDEX);
-      a.pool.free[n1 - 1 - (base + j)] = page;
+  if (sound && R > 0)
+    each_back([&](int64_t j, int, int32_t *e) {
+      a.pool.free[n1 - 1 - j] = *e;
       *e = -1;
-    }
-    base += c.tx;
-    __syncthreads();
-  }
+    });
   cluster_sync();
 
   // ---- pages from the stack, as long as a sequence's whole need fits
-  int64_t taken = 0;
-  base = 0;
+  int64_t taken = 0, base = 0;
   for (int b0 = 0; b0 < batch && sound; b0 += nthr) {
     const int b = b0 + t;
     if (!one) {
-      s = b < batch ? seq_pages(a, b, seq_in(a, b), falls, false) : SeqPages{0, 0, false};
+      s = b < batch ? seq(b, seq_in(a, b), false) : SeqPages{0, 0, false};
       c = block_scan2(0, max(s.need - s.held, 0), sh);
     }
     const int64_t fit = n1 - base;  // what the chunk may take
@@ -199,7 +242,7 @@ __global__ void __launch_bounds__(kPageThreads) k_pages_resize(PagesArgs a) {
     l_held[t] = s.held;
     l_need[t] = s.need;
     __syncthreads();
-    const int64_t last = min(c.ty, fit);
+    const int64_t last = min(c.y_all, fit);
     for (int64_t k = static_cast<int64_t>(rank) * nthr + t; k < last; k += static_cast<int64_t>(ctas) * nthr) {
       const int q = first_above(l_grow, nthr, k);
       if (l_grow[q] > fit) continue;  // the sequence's pages do not all fit: none
@@ -216,7 +259,7 @@ __global__ void __launch_bounds__(kPageThreads) k_pages_resize(PagesArgs a) {
     top = 0;
     for (int w = 0; w < (nthr >> 5); ++w) top = max(top, sh[w][0]);
     taken = top > 0 ? base + top : taken;
-    base += c.ty;
+    base += c.y_all;
     __syncthreads();
   }
   cluster_sync();
@@ -227,7 +270,7 @@ __global__ void __launch_bounds__(kPageThreads) k_pages_resize(PagesArgs a) {
   for (int b0 = 0; b0 < batch; b0 += nthr) {
     const int b = b0 + t;
     if (!one) {  // (held[b] is still the old one: this thread writes it next)
-      s = b < batch ? seq_pages(a, b, seq_in(a, b), falls, false) : SeqPages{0, 0, false};
+      s = b < batch ? seq(b, seq_in(a, b), false) : SeqPages{0, 0, false};
       c = block_scan2(0, max(s.need - s.held, 0), sh);
     }
     if (b < batch) {
@@ -235,7 +278,7 @@ __global__ void __launch_bounds__(kPageThreads) k_pages_resize(PagesArgs a) {
       if (has && s.need != s.held) a.pool.held[b] = s.need;
       if (a.granted != nullptr) a.granted[b] = has ? 1 : 0;
     }
-    base += c.ty;
+    base += c.y_all;
   }
   if (t == 0 && sound) *a.pool.n_free = static_cast<int32_t>(n1 - taken);
 }

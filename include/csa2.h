@@ -505,7 +505,7 @@ csa2_status csa2_chunk_attn(const csa2_cache *cache, const uint16_t *q, int32_t 
  * pool: held int32 [batch], the pages each sequence holds (entries 0..held-1 of its
  *   block_table row); free int32 [n_pages], a stack of free page ids, n_free int32
  *   [1] of them.  All device memory that the caller owns, as is block_table, which
- *   this call writes.
+ *   this call writes.  A page is in one place: on the stack or in one sequence's row.
  * Pages beyond need go back to the stack and their entries become -1 (a sequence
  *   that ended: length 0; drafted tokens that were refused: the shorter length).
  *   With R of them, the j-th in sequence and page order goes to
@@ -516,9 +516,9 @@ csa2_status csa2_chunk_attn(const csa2_cache *cache, const uint16_t *q, int32_t 
  * granted: int32 [batch] or NULL, 1 where a sequence holds what it needs, else 0.
  * Equal calls give equal tables; taking pages and giving them back restores both.
  * Device errors, the sequence left as it was: CAPACITY (need_b > max_pages), INDEX
- *   (cu_new, max_new, a negative length, held outside 0..max_pages).  INDEX with
- *   nothing done: n_free outside 0..n_pages, or more pages than the pool has.  INDEX
- *   also for a returned id outside the pool.  A pool that runs out is no error: see
+ *   (cu_new, max_new, a negative length, held outside 0..max_pages, an id outside the
+ *   pool among the pages that would go back).  INDEX with nothing done: n_free outside
+ *   0..n_pages, or more pages than the pool has.  A pool that runs out is no error: see
  *   granted.
  */
 typedef struct csa2_page_pool {

@@ -221,3 +221,43 @@ def test_a_captured_step():
         for k in (c, d):
             k.n_tokens += torch.tensor(counts, device=DEV)
             k.n_tokens[counts.index(max(counts))] = 0
+
+
+@pytest.mark.parametrize("batch,per,page", [(4, 5, 128), (300, 9, 128), (1500, 6, 256)])
+def test_ids_outside_the_pool_do_not_go_back(batch, per, page):
+    """A sequence that would give back an id that is no page stays as it was, and nobody gets the id; one that
+    keeps such an id gives back what lies behind it."""
+    n_pages = batch * per
+    c = _Bare(batch, per, n_pages, page)
+    pool, w = csa2.PagePool(c), Walk(batch, per, n_pages, page, 1)
+    granted, err = (torch.zeros(n, dtype=torch.int32, device=DEV) for n in (batch, 1))
+    lens = [page * (per - b % 2) for b in range(batch)]
+    w.resize(lens)
+    csa2.pages_resize(c, pool, target=torch.tensor(lens, device=DEV), granted=granted, err=err)
+    assert int(err) == 0
+    # (sequence, entry, id): behind the new length, the last entry of a chunk of sequences among them
+    bad = {0: (per - 1, -1), batch // 2: (1, n_pages), batch - 1: (per - 2, 2 ** 30), 2: (0, -5)}
+    for b, (p, v) in bad.items():
+        c.block_table[b, p] = v
+        w.table[b][p] = v
+    lens = [1 if b % 3 != 1 else page * per for b in range(batch)]  # a third grows by what the others give back
+    for b in bad:
+        lens[b] = 1
+    plain = [None if b in bad and b != 2 else n for b, n in enumerate(lens)]
+    for last in (False, True):  # (the same call again: the same answer)
+        ok = w.resize(plain)
+        err.zero_()
+        csa2.pages_resize(c, pool, target=torch.tensor(lens, device=DEV), granted=granted, err=err)
+        assert int(err) == csa2.DEVERR_INDEX and granted.tolist() == [int(o) for o in ok]
+        assert all(granted[b] == (b == 2) for b in bad)
+        _same(c, pool, w)
+    # mended, they go back
+    for b, (p, v) in bad.items():
+        if b != 2:
+            page_id = next(i for i in range(n_pages) if i not in set(w.free[:w.n]) | {x for row in w.table for x in row})
+            c.block_table[b, p] = page_id
+            w.table[b][p] = page_id
+    ok, _ = w.resize(lens), err.zero_()
+    csa2.pages_resize(c, pool, target=torch.tensor(lens, device=DEV), granted=granted, err=err)
+    assert int(err) == 0 and granted.tolist() == [int(o) for o in ok] == [1] * batch
+    _same(c, pool, w)
