@@ -551,7 +551,8 @@ csa2_status csa2_slot_map(const csa2_cache *cache, const int32_t *cu_new, int32_
  *   CSA2_FP4_NV: E2M1 codes, one E4M3 scale per 16 columns (as the main entry) and
  *     one power of two r per row.  r is the least one, 2^-62 at least, with
  *     largest magnitude of the row / r <= 2688 = 448 x 6; then per group
- *     s = E4M3(amax / (6 r)), codes E2M1(x / (r s)), zeros where s is 0.
+ *     s = E4M3(amax / (6 r)), codes E2M1(x / (r s)) (x's sign bit, of a zero too),
+ *     zeros where s is 0.
  *   CSA2_FP4_MX: E2M1 codes, one E8M0 scale per 32 columns (as the indexer key);
  *     r = 1.
  *   Value: code x scale x r.  A row that holds an infinity or NaN (NV: also one whose

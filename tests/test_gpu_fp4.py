@@ -339,3 +339,34 @@ def test_quant_from_two_host_threads():
             csa2.fp4_quant(ms[1], xs[1])
             for x, m in zip(xs, ms):
                 assert torch.equal(fu.values(m), fu.quantised(x, fmt))
+
+
+def _codes(m):
+    """The E2M1 codes of an Fp4Matrix, [rows, cols], from its records."""
+    rt, ct = -(-m.rows // 128), -(-m.cols // 128)
+    rec = m.tiles.view(rt, ct, -1)[..., :8192]
+    b = rec.reshape(rt, ct, 4, 128, 16).permute(0, 3, 1, 2, 4).reshape(rt * 128, ct * 64)
+    return torch.stack([b & 15, b >> 4], -1).flatten(1)[:m.rows, :m.cols]
+
+
+@pytest.mark.parametrize("rows,cols", [(5, 264), (1300, 520), (1300, 4104), (4900, 520), (1230, 20008)])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_codes_keep_the_sign(fmt, rows, cols):
+    """The sign bit of a code is the value's, also where it rounds to zero and of -0; bf16 rows and the same rows
+    in fp32 give the same bytes.  (A group of zeros is zeros: its scale, or its values, leave nothing to sign.)"""
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    x = torch.randn(rows, cols, generator=g, device=DEV)
+    x *= torch.exp2(torch.randint(-24, 1, x.shape, generator=g, device=DEV).float())  # down to 2^-13 of a code and below
+    x[:, ::16] = 6.0
+    x[:, 3::16] = -0.0
+    x[:, 5::16] = 0.0
+    x = x.to(torch.bfloat16)
+    m, n = _packed(x, fmt), _packed(x.float(), fmt)
+    sign = torch.signbit(x)
+    for k in (m, n):
+        assert torch.equal((_codes(k) & 8) != 0, sign)
+        assert torch.equal(fu.values(k), fu.quantised(x, fmt))
+    assert torch.equal(_codes(m), _codes(n)) and ((_codes(m) & 7) == 0).any()
+    out = torch.empty(rows, cols, device=DEV)
+    csa2.fp4_read(m, out)
+    assert torch.equal(torch.signbit(out), sign)
