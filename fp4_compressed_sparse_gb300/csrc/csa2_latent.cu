@@ -553,7 +553,7 @@ csa2_status csa2_value_project(const void *o, int64_t o_stride, int32_t in_dtype
   a.wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0 && out_stride % 16 == 0;
   a.err = err_word;
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  if (csa2::few_values(total, n_heads, dim))
+  if (csa2::few_values(total, n_heads, dim, in_dtype == CSA2_IN_F32))
     return cuda_status(csa2::launch_value_few(a, in_dtype == CSA2_IN_F32, s), "csa2_value_project launch");
   const int64_t units = static_cast<int64_t>(n_heads) * a.tiles, sms = csa2::device_sm_count();
   a.parts = 1;

@@ -24,15 +24,21 @@ struct LatentArgs {
   int32_t *err;
 };
 
-// Where the forms for few tokens are taken.  One GB300, us, few / persistent, dim 128:
-//   queries of 64 heads, 32 tokens 5.0 / 5.3, 33 tokens 7.5 / 5.3; of 32 heads, 17 tokens 4.1 /
-//   4.2, 32 tokens 4.7 / 4.1; of 128 heads, one token 5.6 / 6.3, 16 tokens 6.9 / 6.1;
-//   values of 64 heads, 32 tokens bf16 3.7 / 4.3, fp32 4.8 / 7.2, 33 tokens 4.8 / 4.3 and 6.9 /
-//   7.2, 64 tokens 5.2 / 4.3 and 8.5 / 7.1; of 128 heads, 16 tokens 3.7 / 5.3 and 5.4 / 8.1, 32
-//   tokens 5.1 / 5.2 and 8.5 / 7.9; of 64 heads of 64, 64 tokens 3.7 / 3.8 and 4.8 / 6.7.
+// Where the forms for few tokens are taken.  One GB300, us, few / persistent, dim 128 (queries
+// were swept at that width and at 64, which moves them little):
+//   queries of 64 heads, 32 tokens 5.0 / 5.0, 33 tokens 7.4 / 5.0; of 32 heads, 17 tokens 4.1 /
+//   3.8, 32 tokens 4.7 / 3.9; of 128 heads, one token 5.6 / 6.1, 5 tokens 5.8 / 5.9, 16 tokens
+//   6.8 / 6.0; of 64 heads of 64, 32 tokens 4.0 / 4.4, 33 tokens 6.2 / 4.4;
+//   values of 64 heads, 32 tokens bf16 3.7 / 4.1, fp32 4.6 / 8.1, 33 tokens 4.8 / 4.1 and 7.7 /
+//   8.1, 65 tokens 5.6 / 4.1 and 10.8 / 8.1; of 128 heads, 16 tokens 3.7 / 4.6 and 5.0 / 8.9, 32
+//   tokens 5.2 / 4.6 and 8.1 / 8.8, 33 tokens 7.1 / 4.7 and 12.6 / 9.0; of 16 heads, 129 tokens 3.8 /
+//   3.9 and 6.1 / 7.5, 256 tokens 5.1 / 4.0 and 8.2 / 7.6; of 64 heads of 64, 64 tokens 3.7 / 3.8
+//   and 4.6 / 7.6.
 inline bool few_queries(int total, int heads) { return total <= (heads <= 64 ? 32 : 4); }
 // (a block takes 16 or 32 tokens, a head, 32 values)
-inline bool few_values(int total, int heads, int dim) { return static_cast<int64_t>((total + 15) / 16) * heads * ((dim + 31) / 32) <= 512; }
+inline bool few_values(int total, int heads, int dim, bool f32) {
+  return static_cast<int64_t>((total + 15) / 16) * heads * ((dim + 31) / 32) <= (f32 ? 768 : 512);
+}
 cudaError_t launch_query_few(const LatentArgs &a, cudaStream_t s);
 cudaError_t launch_value_few(const LatentArgs &a, bool f32, cudaStream_t s);
 

@@ -24,8 +24,8 @@ def test_fp32_product_and_remainder_is_the_rounded_quotient():
 
 
 def test_the_rounded_quotient_gives_the_scale():
-    """E4M3 of the fp32 quotient is E4M3 of the quotient, over the scales' binades (2^-10 to 512)."""
-    for e in range(-10, 9):
+    """E4M3 of the fp32 quotient is E4M3 of the quotient, in the subnormal scales' binades and among the others."""
+    for e in (-10, -9, -8, -7, 0, 7):
         a = (np.arange(1 << 23, dtype=np.uint32) + ((127 + e + 2) << 23)).view(np.float32)
         q = a.astype(np.float64) / 6.0
         assert (_e4m3(q) == _e4m3(q.astype(np.float32).astype(np.float64))).all()
