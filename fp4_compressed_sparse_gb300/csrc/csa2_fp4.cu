@@ -22,12 +22,11 @@
 //   the same way (equal to the rounded quotient for every mantissa: tests/test_fp4_scale.py).
 //
 // Bound: HBM for large matrices, a chain of loads, reductions and stores for a few rows.
-// Measured (in a graph): 12,288 x 4,096 bf16 to NV 22.5 us (5.7 TB/s), read back 21.6 us (6.0
-// TB/s; a plain fill of its 100 MB takes 25.7), 12,288 x 4,104 23.5; 8,192 x 4,096 bf16 13.6 us (6.3
-// TB/s), fp32 26.6 us (5.8), to MX 13.5 and 25.5, read 11.5 us (7.5, L2 holds a part); 32 rows
-// 1.7 us.  At 11.6 instructions per value the first took 31 us, at 14 compares per fp32 value 42
+// Measured (in a graph): 12,288 x 4,096 bf16 to NV 23.2 us (5.6 TB/s), read back 22.2 us (5.8
+// TB/s); 8,192 x 4,096 bf16 14.2 us (6.1 TB/s), fp32 26.5 us (5.8), to MX 14.1 and 25.9, read 12.2
+// us (7.0, L2 holds a part); 32 rows 1.9 us.  At 11.6 instructions per value the first took 31 us, at 14 compares per fp32 value 42
 // of 8,192 x 4,096, and with divisions 28: the conversions above are what brought them near the
-// copy rate.
+// copy rate.  (Figures from one box to the next differ by 4 %.)
 #include <type_traits>
 
 #include "csa2_fp4.cuh"
@@ -401,7 +400,7 @@ __global__ void __launch_bounds__(kQThreads, kNv ? 4 : 3) k_fp4_quant_rows(F4Arg
 }
 
 // The others: persistent blocks, kRows rows at a time, which come by bulk copies into one of
-// two buffers while the other one's are quantised.  8,000 rows of 7,224 bf16 to NV 27.8 us (one
+// two buffers while the other one's are quantised.  8,000 rows of 7,224 bf16 to NV 28.9 us (one
 // buffer filled by loads, a block per 4 rows 44); fp32 of 4,104 26.3 (45.6; with the banks met
 // up to four times and divisions 33).  A thread takes one piece of 32 values a step (so that
 // the last, partial step is short), two of fp32 rows to MX, whose steps are short anyway.

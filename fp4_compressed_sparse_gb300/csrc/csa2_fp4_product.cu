@@ -11,8 +11,9 @@
 // (all of them, or 128 at a time).  The K tiles of an output tile are dealt to the CTAs of a
 // cluster, whose sums are added in rank order through distributed shared memory: no
 // workspace, equal calls give equal bits.  Bound: the weights' bytes.  One token by 12,288 x
-// 4,096 5.6 us with the weights in L2 (12.3 cold, 28 MB: a third of the copy rate; launch,
-// tensor memory, first box and the join are 4.5 us of either), 501 tokens x 704 x 4,104 7.2.
+// 4,096 5.8 us with the weights in L2, 8.0 with each call's in HBM (28 MB: 3.5 TB/s, half the copy
+// rate; no byte of them is requested before the kernel in front ends, and launch, tensor memory,
+// first box and the join are 4.5 us of either), 501 tokens x 704 x 4,104 7.3.
 //
 // k_fp4_pair, more: 8,192 x 12,288 x 4,096 NV 121 us (6.8 PFLOP/s, 71 % of the 9.5 PFLOP/s
 // that csa2_mxf4_peak_launch reaches), MX 113; 8,192^3 151 us (7.3).  Without its copies it
@@ -638,15 +639,18 @@ cudaError_t launch_split(const ProductArgs &a, int ranks, cudaStream_t s) {
 //   columns on (100 x 12288 x 4096 9.4 against 10.2, but x 1024 6.5 against 6.3), and of up to
 //   1,024 columns from 32 tiles on (501 x 1024 x 512 5.2 against 5.8, 8,000 x 50 x 512 4.8 against
 //   7.0); below, 250 x 4096 x 4096, of 64 tiles, 9.5 against 8.8.
-//   Split: the narrowest token tile that holds all tokens (a scale column is of 32 rows
-//   from the record's first on, so several tiles only of 128), then as many ranks as are
+//   Split: the narrowest token tile that holds all tokens, several tiles only of 128 (a tile of
+//   64 that begins in the middle of a record would need that half's codes and, of the scales'
+//   columns, those of rows 64 on, the last two of each four: not built), then as many ranks as are
 //   resident at once, of 128 tokens one CTA per SM, else two: 64 x 12288 x 4096 8.1 with 3
 //   against 12.1 with 1, 1 x 4096 x 8192 5.0 with 8 against 5.9 with 4, 501 x 704 x 4104 7.2 with
 //   4 against 10.2 with 1.  Clusters do not cover all SMs: a few that wait for a second turn
 //   cost as much as all (1 x 6144 x 4096 8.1 with 6, 4.9 with 4; 501 x 704 x 4104 10.8 with 6).
 //   Of two stages none is dealt out (100 x 4096 x 512 6.2 with 2 ranks, 5.4 with 1).
 // kRanks: ranks, the percentage of the SMs that clusters of so many cover with one CTA per
-// SM (of 152: 152, 138, 144, 138, 120), and with two (of 304: 304, 291, 296, 276, 288).
+// SM (of 152: 152, 138, 144, 138, 120), and with two (of 304: 304, 291, 296, 276, 288).  Read
+// from one GB300; where the SMs are spread otherwise over the GPU's clusters, a choice near
+// its border can cost a second turn, and gives the same bits.
 constexpr int kRanks[5][3] = {{2, 100, 100}, {3, 90, 95}, {4, 94, 97}, {6, 90, 90}, {8, 78, 95}};
 template <bool kNv, bool kBf16>
 cudaError_t launch_product(const ProductArgs &a, cudaStream_t s) {

@@ -17,9 +17,9 @@
 // them, each multiplied: the sums are of the values as they were given.
 //
 // Measured (in a graph, caches as the calls before leave them): 4,001 tokens of 64 heads of
-// 128: queries 72 us (403 MB, 5.6 TB/s, 82 % of the measured copy rate), values bf16 55 us
-// (336 MB, 6.1 TB/s, 90 %), fp32 97 us (599 MB, 6.2 TB/s); 128 tokens: 5.7, 4.4 and 7.2 us.
-// Tensor pipe 17 to 22 %.  Short of the copy rate: the reload of W when a CTA's run passes to
+// 128: queries 73 us (403 MB, 5.5 TB/s, 81 % of the measured copy rate), values bf16 56 us
+// (336 MB, 6.0 TB/s, 88 %), fp32 101 us (599 MB, 5.9 TB/s); 128 tokens: 5.8, 4.4 and 8.3 us (fp32:
+// a chain of 16 stages, each cut into its parts).  Tensor pipe 18 (queries), 22 and 39 %.  Short of the copy rate: the reload of W when a CTA's run passes to
 // another head (nothing is computed meanwhile), rows of 1,152 B at 74 KB distance out.
 #include "csa2_latent.cuh"
 #include "csa2_tc.cuh"

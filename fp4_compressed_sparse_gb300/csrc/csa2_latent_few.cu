@@ -1,16 +1,17 @@
 // csa2_latent_few.cu -- csa2_query_latent and csa2_value_project for few tokens.
 //
 // The weights' bytes bound these (8.4 MB for 64 heads of 128: 1.2 us), and before them the
-// chain launch -> loads -> products -> sums -> stores.  So every load of a block is issued
-// at once: a warp takes W from global memory straight into the fragments of
+// chain launch -> loads -> products -> sums -> stores.  So all loads of a block's operands
+// are issued at once (a query row's position, which decides whether it is stored, is read
+// behind the sums): a warp takes W from global memory straight into the fragments of
 // mma.sync m16n8k16 (tokens are its 16 rows), 16 bytes a lane, whose values are dealt to
 // fragment places by renaming columns (query) or summation indices (value).  The warps of
 // a block share out K and join their sums in shared memory, in order.
 //
-// Measured (in a graph, W in L2): queries of 64 heads of 128, one token 3.8 us, 32 tokens 5.3;
-// values, one token 2.7 (bf16) and 3.0 us (fp32), 32 tokens 3.4 and 4.8.  A launch alone takes
-// 1.4.  With cold caches 7.3 us (one token) and 10.8 us (32 fp32 tokens): four round trips to
-// HBM in a row (position or bounds, operands, sums, stores).
+// Measured (in a graph, W in L2): queries of 64 heads of 128, one token 3.9 us, 32 tokens 5.1;
+// values, one token 2.9 (bf16) and 3.4 us (fp32), 32 tokens 3.7 and 4.7.  A launch alone takes
+// 1.4.  With each call's W in HBM 4.5 and 5.6, 4.0 and 4.4, 4.5 and 5.6; with all else there
+// too 7.3 us (queries, one token) and 9.8 us (32 fp32 tokens).
 #include "csa2_latent.cuh"
 
 namespace csa2 {

@@ -13,16 +13,18 @@
 //
 // Bound: latency.  A decode step of 32 sequences reads a few hundred bytes; what it
 // takes is the chain lengths -> prefix sum -> barrier -> free list -> table.  32 sequences
-// of 65,536 tokens 3.2 us, 512 with 51 that end and 51 prompts (4,011 pages moved) 4.0, a
-// launch alone 1.4; the slots of 32 and of 104,034 tokens 2.3 and 4.2.
+// that keep their pages 2.9 us, a launch alone 1.4; that take a page each and give it back
+// 4.5 a call, 499 pages each 11.2; 512, of which 51 end and 51 bring prompts, and back 8.7 a
+// call (the look at what comes back: 1.5, 6 and 4 us of two such calls).  The slots of 32 and of
+// 104,034 tokens 2.6 and 4.2.
 #include "csa2_internal.cuh"
 
 namespace csa2 {
 namespace {
 
 constexpr int kPageThreads = 1024;
-// one cluster: 32 sequences that take or give 499 pages each 8.5 us, with one CTA 42; a
-// decode step 3.7, with one CTA 3.8
+// one cluster: 32 sequences that take or give 499 pages each 11.2 us, with one CTA 62; one
+// page each 4.5, with one CTA 4.3
 constexpr int kPageCtas = 8;
 constexpr int kMaskWords = 65536 / 32;  // a bit per sequence
 
