@@ -18,7 +18,7 @@
 //
 // Measured (in a graph, caches as the calls before leave them): 4,001 tokens of 64 heads of
 // 128: queries 73 us (403 MB, 5.5 TB/s, 81 % of the measured copy rate), values bf16 56 us
-// (336 MB, 6.0 TB/s, 88 %), fp32 101 us (599 MB, 5.9 TB/s); 128 tokens: 5.8, 4.4 and 8.3 us (fp32:
+// (336 MB, 6.0 TB/s, 88 %), fp32 104 us (599 MB, 5.8 TB/s); 128 tokens: 5.8, 4.4 and 8.4 us (fp32:
 // a chain of 16 stages, each cut into its parts).  Tensor pipe 18 (queries), 22 and 39 %.  Short of the copy rate: the reload of W when a CTA's run passes to
 // another head (nothing is computed meanwhile), rows of 1,152 B at 74 KB distance out.
 #include "csa2_latent.cuh"
@@ -47,9 +47,12 @@ struct Shape {
   static constexpr int kThreads = 32 * (12 + kMoreWarps);
 };
 // fp32 latents: their bf16 parts lie in tensor memory, as the MMA's rows, 16 columns of a
-// buffer each.  Two buffers lie behind each accumulator's 128 columns, 64 columns apart.
-constexpr int kPartBufs = 4;
-__device__ __forceinline__ uint32_t part_col(uint32_t buf) { return 128 + 64 * buf + 128 * (buf >> 1); }
+// buffer each, behind two accumulators of 128 columns: one for the first parts, one for the
+// others, 2^-8 as large.  An MMA's sums lose what lies below fp32's last bit, so in one accumulator
+// the two small parts' steps cost as much as the first's: of 8 million values 1.1 in 1,000 were
+// not the rounded 64-bit ones, so it is 0.27 (a plain fp32 product: 0.29).  The sums are read out
+// between two units, which takes 2.5 % (4,001 tokens 104.5 us against 102 with two of one each).
+constexpr int kPartBufs = 4, kRestCol = 128, kPartCol = 256, kPartCols = 64;
 struct Sync {
   uint64_t full[6], empty[6];
   uint64_t wfull[4], wdone;      // W, or a stage's columns of it, has landed; the last MMAs that read it are done
@@ -117,6 +120,17 @@ __device__ __forceinline__ float4 lds4(uint32_t at) {
 __device__ __forceinline__ void sts4(uint32_t at, const uint32_t *v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(at), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
 }
+// 16 bf16 values; wide: dst is on a boundary of 32 bytes.
+__device__ __forceinline__ void put16(uint16_t *dst, const uint32_t *o, bool wide) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]),
+                 "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4 *>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    reinterpret_cast<uint4 *>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
 
 // One persistent CTA per SM.  A unit is (head, column part, tile of 128 tokens), done in one
 // job or, queries with all of their 512 columns, in two of 256; units of a head and part
@@ -126,7 +140,7 @@ __device__ __forceinline__ void sts4(uint32_t at, const uint32_t *v) {
 //   warp 0       copies W (once per head and part) and the tokens' rows, by tensor maps
 //   warp 1       issues the MMAs
 //   warps 4-11   read the sums out of tensor memory and write them: two groups of four,
-//                one per accumulator
+//                one per accumulator (fp32 latents: both on every unit)
 //   warps 12-    query: rotate the RoPE dims, from global memory to global memory;
 //                fp32 latents: cut a stage into three bf16 parts in tensor memory
 template <Mode kM>
@@ -167,7 +181,7 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
     tc::mbar_init(&sy.wdone, 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&sy.tfull[i], 1);
-      tc::mbar_init(&sy.tempty[i], 4);
+      tc::mbar_init(&sy.tempty[i], kF ? 8 : 4);
     }
     sy.loaded = sy.w_loaded = 0;
     sy.dead = 0;
@@ -247,8 +261,9 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
         held = hp;
       }
       if (ok) {
-        const uint32_t acc = j & 1, d = tmem + 256 * acc;
-        if (j >= 2) ok = wait_all(&sy.tempty[acc], ((j >> 1) - 1) & 1);
+        const uint32_t acc = kF ? 0 : j & 1, d = tmem + 256 * acc;
+        if (kF && j >= 1) ok = wait_all(&sy.tempty[0], (j - 1) & 1);
+        if (!kF && j >= 2) ok = wait_all(&sy.tempty[acc], ((j >> 1) - 1) & 1);
         for (int c = 0; c < chunks && ok; ++c) {
           if (kWGroups > 1 && fresh) ok = wait_all(&sy.wfull[c], (wn - 1) & 1);
           if (first && ok) ok = kF ? wait_all(&sy.pfull[st], ph) : wait_all(&sy.full[st], ph);
@@ -262,11 +277,12 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
                 mma_bf16(d, dx + (((s >> 2) * kBox + 32 * (s & 3)) >> 4), dw + (2048 * s >> 4), id, s > 0 ? 1u : 0u);
             } else if constexpr (kF) {
               const uint64_t dw = desc_sw128(s_w + (c >> 1) * a.np * 128, 16, 1024) + (64 * (c & 1) >> 4);
-              const uint32_t tx = tmem + part_col(st);
+              const uint32_t tx = tmem + kPartCol + kPartCols * st;
 #pragma unroll
               for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int z = 0; z < 3; ++z) mma_bf16_rows(d, tx + 16 * z + 8 * s, dw + (32 * s >> 4), id, c + s + z > 0 ? 1u : 0u);
+                for (int z = 0; z < 3; ++z)
+                  mma_bf16_rows(z == 0 ? d : d + kRestCol, tx + 16 * z + 8 * s, dw + (32 * s >> 4), id, c + s > 0 || z == 2 ? 1u : 0u);
             } else {
               const uint64_t dx = desc_sw128(s_x + st * S::kStage, 16, 1024);
 #pragma unroll
@@ -297,7 +313,32 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
     for (int v = v0; v < v1 && ok; ++v, ++j) {
       const int u = v >> shift, b = v & shift, hp = u / a.tiles, tile = u - hp * a.tiles, h = hp / a.parts, part = hp - h * a.parts;
       const int64_t tok = static_cast<int64_t>(tile) * kTok + 32 * q + lane;
-      if ((j & 1) == g) {
+      if constexpr (kF) {  // both groups, every second 16 columns each; the sums are free before the stores
+        ok = wait_all(&sy.tfull[0], j & 1);
+        if (!ok) break;
+        tc::tc_fence_after();
+        const uint32_t at = tmem + (static_cast<uint32_t>(32 * q) << 16) + 16 * g;
+        uint32_t o[4][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (16 * g + 32 * i >= cols) break;
+          uint32_t r[16], rest[16];
+          tc::tmem_ld_32x32b_x16(at + 32 * i, r);
+          tc::tmem_ld_32x32b_x16(at + kRestCol + 32 * i, rest);
+          tc::tmem_ld_wait_x16(r);
+          tc::tmem_ld_wait_x16(rest);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            o[i][k] = pack_bf16(__uint_as_float(r[2 * k]) + __uint_as_float(rest[2 * k]), __uint_as_float(r[2 * k + 1]) + __uint_as_float(rest[2 * k + 1]));
+        }
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&sy.tempty[0]);
+        uint16_t *dst = a.out + tok * a.out_stride + static_cast<int64_t>(h) * a.dim + part * a.np + 16 * g;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (tok < a.total && 16 * g + 32 * i < cols) put16(dst + 32 * i, o[i], a.wide);
+      } else if ((j & 1) == g) {
         bool live = tok < a.total;
         int64_t p;
         if (kQ && live) live = row_position(a, tok, false, p);
@@ -340,16 +381,7 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
             tc::tmem_ld_wait_x16(r);
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = pack_bf16(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
-            if (live) {
-              if (a.wide) {
-                asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + c), "r"(o[0]), "r"(o[1]),
-                             "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-                             : "memory");
-              } else {
-                reinterpret_cast<uint4 *>(dst + c)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-                reinterpret_cast<uint4 *>(dst + c)[1] = make_uint4(o[4], o[5], o[6], o[7]);
-              }
-            }
+            if (live) put16(dst + c, o, a.wide);
           }
         }
         tc::tc_fence_before();
@@ -405,7 +437,7 @@ __global__ void __launch_bounds__(Shape<kM>::kThreads, 1)
       ok = wait_all(&sy.full[st], (n / S::kStages) & 1) && (use == 0 || wait_all(&sy.pempty[pb], (use - 1) & 1));
       if (!ok) break;
       tc::tc_fence_after();
-      const uint32_t src = s_x + st * S::kStage + (quarter + lane) * 128, dst = tmem + (quarter << 16) + part_col(pb);
+      const uint32_t src = s_x + st * S::kStage + (quarter + lane) * 128, dst = tmem + (quarter << 16) + kPartCol + kPartCols * pb;
       uint32_t part[3][16];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {

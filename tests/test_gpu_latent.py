@@ -314,3 +314,21 @@ def test_value_of_the_largest_fp32(T):
     is_nan = torch.zeros(T, H, dtype=torch.bool, device=DEV)
     is_nan[3, 0] = is_nan[T - 1, 2] = True
     assert torch.equal(torch.isnan(out.view(T, H, D)), is_nan[..., None].expand(T, H, D))
+
+
+@pytest.mark.parametrize("T", [32, 100, 1000])
+def test_value_sums_of_fp32_are_fp32_sums(T):
+    """The outputs that differ from the rounded 64-bit ones (sums close to a border of bf16, and off by more): not
+    more than twice as many as of torch's product in fp32.  An output changes sides where its sum is off by more than
+    its distance from the border, so their number is the sums' mean error, whatever its distribution."""
+    H, D = 64, 128
+    g = torch.Generator(device=DEV).manual_seed(T)
+    _, w = _weights(H, D, g)
+    o = torch.randn(T, H, 512, generator=g, device=DEV)
+    out = torch.empty(T, H * D, dtype=torch.bfloat16, device=DEV)
+    csa2.value_project(o, w, out)
+    want = torch.einsum("thc,hjc->thj", o.double(), w.double()).reshape(T, -1).float().to(torch.bfloat16)
+    assert not torch.backends.cuda.matmul.allow_tf32
+    plain = torch.matmul(o.transpose(0, 1), w.float().transpose(1, 2)).transpose(0, 1).reshape(T, -1).to(torch.bfloat16)
+    n = int((plain != want).sum())
+    assert n >= 20 and int((out != want).sum()) <= 2 * n
