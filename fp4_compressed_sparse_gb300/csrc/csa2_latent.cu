@@ -18,9 +18,10 @@
 //
 // Measured (in a graph, caches as the calls before leave them): 4,001 tokens of 64 heads of
 // 128: queries 73 us (403 MB, 5.5 TB/s, 81 % of the measured copy rate), values bf16 56 us
-// (336 MB, 6.0 TB/s, 88 %), fp32 104 us (599 MB, 5.8 TB/s); 128 tokens: 5.8, 4.4 and 8.4 us (fp32:
-// a chain of 16 stages, each cut into its parts).  Tensor pipe 18 (queries), 22 and 39 %.  Short of the copy rate: the reload of W when a CTA's run passes to
-// another head (nothing is computed meanwhile), rows of 1,152 B at 74 KB distance out.
+// (336 MB, 6.0 TB/s, 88 %), fp32 104 us (599 MB, 5.8 TB/s); 128 tokens: 5.8, 4.4 and 8.4 us
+// (fp32: a chain of 16 stages, each cut into its parts).  Tensor pipe 18, 22 and 39 %.  Short of
+// the copy rate: the reload of W when a CTA's run passes to another head (nothing is computed
+// meanwhile), rows of 1,152 B at 74 KB distance out.
 #include "csa2_latent.cuh"
 #include "csa2_tc.cuh"
 #include "csa2_tma.cuh"
@@ -51,7 +52,7 @@ struct Shape {
 // others, 2^-8 as large.  An MMA's sums lose what lies below fp32's last bit, so in one accumulator
 // the two small parts' steps cost as much as the first's: of 8 million values 1.1 in 1,000 were
 // not the rounded 64-bit ones, so it is 0.27 (a plain fp32 product: 0.29).  The sums are read out
-// between two units, which takes 2.5 % (4,001 tokens 104.5 us against 102 with two of one each).
+// between two units, which takes 2.5 % (4,001 tokens 104.5 us; 102 with one for all parts, double).
 constexpr int kPartBufs = 4, kRestCol = 128, kPartCol = 256, kPartCols = 64;
 struct Sync {
   uint64_t full[6], empty[6];
